@@ -306,3 +306,15 @@ class MoeLayer:
         return {"ids": ids.cpu().numpy(), "weights": wts.cpu().numpy(),
                 "offsets": offs.cpu().numpy(), "perm": perm.cpu().numpy(),
                 "inv": inv.cpu().numpy().reshape(T, k)}
+
+
+# The attention operators need torch; the expert layer's host functions do not.
+_ATTENTION = ("PagedAttention", "PagedKvCache", "moe_attn_rope", "moe_attn_rope_frequencies",
+              "EXPORTS_ATTN")
+
+
+def __getattr__(name):
+    if name in _ATTENTION:
+        from . import attention
+        return getattr(attention, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,317 @@
+// C ABI of the attention operators: argument validation, workspace, dispatch.
+#include <cmath>
+#include <cstdio>
+#include <new>
+
+#include "attn.h"
+
+using namespace moe;
+using namespace moe::attn;
+
+struct moe_attn_handle {
+  moe_attn_config cfg;
+  int device = 0;
+  int num_sms = 0;
+  void* ws = nullptr;
+  unsigned* err = nullptr;
+};
+
+namespace {
+
+int cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_ATTN_OK;
+  fprintf(stderr, "moe_attn: CUDA error %s\n", cudaGetErrorString(e));
+  return MOE_ATTN_ERR_CUDA;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int validate_config(const moe_attn_config* c) {
+  if (!c) return MOE_ATTN_ERR_INVALID_ARG;
+  if (c->flags != 0) return MOE_ATTN_ERR_INVALID_ARG;
+  if (c->dtype != MOE_ATTN_BF16 && c->dtype != MOE_ATTN_FP16) return MOE_ATTN_ERR_INVALID_ARG;
+  if (c->max_tokens < 1 || c->max_tokens > (1 << 20)) return MOE_ATTN_ERR_INVALID_ARG;
+  if (c->max_seqs < 1 || c->max_seqs > 65536) return MOE_ATTN_ERR_INVALID_ARG;
+  if (c->kv_heads < 1 || c->kv_heads > 1024 || c->q_heads < c->kv_heads ||
+      c->q_heads % c->kv_heads || c->q_heads / c->kv_heads > 64)
+    return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  if (c->head_dim < 8 || c->head_dim > 128 || c->head_dim % 8)
+    return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  return MOE_ATTN_OK;
+}
+
+int validate_rotation(const moe_attn_rotation* r, int head_dim) {
+  if (!r) return MOE_ATTN_ERR_INVALID_ARG;
+  if (r->layout != MOE_ATTN_ROPE_HALF && r->layout != MOE_ATTN_ROPE_INTERLEAVED)
+    return MOE_ATTN_ERR_INVALID_ARG;
+  if (r->inverse != 0 && r->inverse != 1) return MOE_ATTN_ERR_INVALID_ARG;
+  if (r->rot_dim < 0 || r->rot_dim > head_dim || r->rot_dim % 2)
+    return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  if (r->rot_dim > 0 && !r->freq) return MOE_ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(r->magnitude)) return MOE_ATTN_ERR_INVALID_ARG;
+  return MOE_ATTN_OK;
+}
+
+// 16-bit elements: data on 2 bytes at least, strides that do not go backwards
+int validate_rows(const moe_attn_rows* r) {
+  if (!r || !r->data) return MOE_ATTN_ERR_INVALID_ARG;
+  if (r->token_stride < 0 || r->head_stride < 0) return MOE_ATTN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(r->data) & 1u) return MOE_ATTN_ERR_MISALIGNED;
+  return MOE_ATTN_OK;
+}
+
+// first and last byte a [tokens, heads, head_dim] view touches overlap
+bool overlap(const moe_attn_rows* a, const moe_attn_rows* b, int tokens, int heads, int dim) {
+  const auto span = [&](const moe_attn_rows* r) {
+    return (uintptr_t)(((tokens - 1) * r->token_stride + (heads - 1) * r->head_stride + dim) * 2);
+  };
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a->data);
+  const uintptr_t pb = reinterpret_cast<uintptr_t>(b->data);
+  return pa < pb + span(b) && pb < pa + span(a);
+}
+
+bool same(const moe_attn_rows* a, const moe_attn_rows* b) {
+  return a->data == b->data && a->token_stride == b->token_stride &&
+         a->head_stride == b->head_stride;
+}
+
+int validate_cache(const moe_attn_cache* c) {
+  if (!c || !c->k || !c->v) return MOE_ATTN_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->num_pages > 0x7ffffffeLL) return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0)
+    return MOE_ATTN_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v) || c->page_stride % 8 || c->token_stride % 8 ||
+      c->head_stride % 8)
+    return MOE_ATTN_ERR_MISALIGNED;
+  return MOE_ATTN_OK;
+}
+
+Rows rows(const moe_attn_rows* r) {
+  return r ? Rows{static_cast<uint16_t*>(r->data), r->token_stride, r->head_stride}
+           : Rows{nullptr, 0, 0};
+}
+
+Rotation rotation(const moe_attn_rotation* r) {
+  return Rotation{reinterpret_cast<const long long*>(r->freq), r->rot_dim,
+                  r->layout == MOE_ATTN_ROPE_INTERLEAVED, r->magnitude,
+                  r->inverse ? -1.0f : 1.0f};
+}
+
+int log2i(int v) {
+  int n = 0;
+  while ((1 << n) < v) ++n;
+  return n;
+}
+
+size_t workspace(const moe_attn_config&) { return 256; }
+
+}  // namespace
+
+extern "C" {
+
+int moe_attn_rope_frequencies(int32_t rot_dim, double base, double factor, int32_t by_parts,
+                              double original_len, double beta_fast, double beta_slow,
+                              int64_t* freq, float* magnitude) {
+  if (!magnitude || (rot_dim > 0 && !freq)) return MOE_ATTN_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > 256 || rot_dim % 2) return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  if (!(base > 1.0) || !std::isfinite(base) || !(factor >= 1.0) || !std::isfinite(factor))
+    return MOE_ATTN_ERR_INVALID_ARG;
+  if (by_parts != 0 && by_parts != 1) return MOE_ATTN_ERR_INVALID_ARG;
+  if (by_parts && !(original_len > 0.0 && std::isfinite(original_len) && beta_slow >= 0.0 &&
+                    beta_fast > beta_slow && std::isfinite(beta_fast)))
+    return MOE_ATTN_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double theta = std::pow(base, -2.0 * i / rot_dim);
+    if (by_parts) {
+      double keep = (original_len * theta / two_pi - beta_slow) / (beta_fast - beta_slow);
+      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+      theta = theta * keep + theta / factor * (1.0 - keep);
+    } else {
+      theta /= factor;
+    }
+    // theta <= 1 radian: below 2^62, inside int64
+    freq[i] = (int64_t)std::ldexp(theta / two_pi, 64);
+  }
+  *magnitude = by_parts && factor > 1.0 ? (float)(1.0 + 0.1 * std::log(factor)) : 1.0f;
+  return MOE_ATTN_OK;
+}
+
+int moe_attn_rope(const moe_attn_rows* x, const moe_attn_rows* out, const int32_t* positions,
+                  int32_t T, int32_t heads, int32_t head_dim, int32_t dtype,
+                  const moe_attn_rotation* r, void* stream) {
+  if (T < 0 || heads < 0) return MOE_ATTN_ERR_INVALID_ARG;
+  if (head_dim < 1 || head_dim > 256) return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  if (dtype != MOE_ATTN_BF16 && dtype != MOE_ATTN_FP16) return MOE_ATTN_ERR_INVALID_ARG;
+  int st = validate_rotation(r, head_dim);
+  if (st != MOE_ATTN_OK) return st;
+  if (T == 0 || heads == 0) return MOE_ATTN_OK;
+  if ((st = validate_rows(x)) != MOE_ATTN_OK || (st = validate_rows(out)) != MOE_ATTN_OK) return st;
+  if (!positions) return MOE_ATTN_ERR_INVALID_ARG;
+  if (!same(x, out) && overlap(x, out, T, heads, head_dim)) return MOE_ATTN_ERR_INVALID_ARG;
+  RopeParams p{};
+  p.q = rows(x);
+  p.q_out = rows(out);
+  p.positions = positions;
+  p.r = rotation(r);
+  p.tokens = T;
+  p.hq = heads;
+  p.head_dim = head_dim;
+  return cuda_status(launch_rope(p, dtype, 0, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_attn_workspace_bytes(const moe_attn_config* cfg, size_t* bytes) {
+  if (!bytes) return MOE_ATTN_ERR_INVALID_ARG;
+  const int st = validate_config(cfg);
+  if (st != MOE_ATTN_OK) return st;
+  *bytes = workspace(*cfg);
+  return MOE_ATTN_OK;
+}
+
+int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn_handle** out) {
+  if (!out) return MOE_ATTN_ERR_INVALID_ARG;
+  *out = nullptr;
+  int st = validate_config(cfg);
+  if (st != MOE_ATTN_OK) return st;
+  int ndev = 0;
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev <= 0) {
+    cudaGetLastError();
+    return MOE_ATTN_ERR_NO_DEVICE;
+  }
+  if (device < 0 || device >= ndev) return MOE_ATTN_ERR_INVALID_ARG;
+  cudaDeviceProp prop;
+  if ((st = cuda_status(cudaGetDeviceProperties(&prop, device))) != MOE_ATTN_OK) return st;
+  if (prop.major != 10 || prop.minor != 3) return MOE_ATTN_ERR_NO_DEVICE;
+  if ((st = cuda_status(cudaSetDevice(device))) != MOE_ATTN_OK) return st;
+  moe_attn_handle* h = new (std::nothrow) moe_attn_handle();
+  if (!h) return MOE_ATTN_ERR_CUDA;
+  h->cfg = *cfg;
+  h->device = device;
+  h->num_sms = prop.multiProcessorCount;
+  const size_t bytes = workspace(*cfg);
+  if ((st = cuda_status(cudaMalloc(&h->ws, bytes))) != MOE_ATTN_OK ||
+      (st = cuda_status(cudaMemset(h->ws, 0, bytes))) != MOE_ATTN_OK) {
+    moe_attn_destroy(h);
+    return st;
+  }
+  h->err = static_cast<unsigned*>(h->ws);
+  *out = h;
+  return MOE_ATTN_OK;
+}
+
+int moe_attn_destroy(moe_attn_handle* h) {
+  if (!h) return MOE_ATTN_OK;
+  cudaSetDevice(h->device);
+  cudaDeviceSynchronize();
+  if (h->ws) cudaFree(h->ws);
+  delete h;
+  return MOE_ATTN_OK;
+}
+
+int moe_attn_append(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* q_out,
+                    const moe_attn_rows* k, const moe_attn_rows* v, const int32_t* positions,
+                    const int64_t* slots, int32_t T, const moe_attn_rotation* r,
+                    const moe_attn_cache* cache, void* stream) {
+  if (!h || T < 0) return MOE_ATTN_ERR_INVALID_ARG;
+  const moe_attn_config& c = h->cfg;
+  if (T > c.max_tokens) return MOE_ATTN_ERR_TOO_MANY_TOKENS;
+  int st = validate_rotation(r, c.head_dim);
+  if (st != MOE_ATTN_OK) return st;
+  if ((st = validate_cache(cache)) != MOE_ATTN_OK) return st;
+  if ((q == nullptr) != (q_out == nullptr)) return MOE_ATTN_ERR_INVALID_ARG;
+  if (T == 0) return MOE_ATTN_OK;
+  if (q && ((st = validate_rows(q)) != MOE_ATTN_OK || (st = validate_rows(q_out)) != MOE_ATTN_OK))
+    return st;
+  if ((st = validate_rows(k)) != MOE_ATTN_OK || (st = validate_rows(v)) != MOE_ATTN_OK) return st;
+  if (!positions || !slots) return MOE_ATTN_ERR_INVALID_ARG;
+  if (q && !same(q, q_out) && overlap(q, q_out, T, c.q_heads, c.head_dim))
+    return MOE_ATTN_ERR_INVALID_ARG;
+  int cur = -1;
+  if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) cudaSetDevice(h->device);
+  RopeParams p{};
+  p.q = rows(q);
+  p.q_out = rows(q_out);
+  p.k = rows(k);
+  p.v = rows(v);
+  p.k_pages = static_cast<uint16_t*>(cache->k);
+  p.v_pages = static_cast<uint16_t*>(cache->v);
+  p.page_shift = log2i(c.page_size);
+  p.num_slots = cache->num_pages << p.page_shift;
+  p.page_stride = cache->page_stride;
+  p.token_stride = cache->token_stride;
+  p.head_stride = cache->head_stride;
+  p.positions = positions;
+  p.slots = reinterpret_cast<const long long*>(slots);
+  p.r = rotation(r);
+  p.tokens = T;
+  p.hq = q ? c.q_heads : 0;
+  p.hk = p.hv = c.kv_heads;
+  p.head_dim = c.head_dim;
+  p.err = h->err;
+  return cuda_status(launch_rope(p, c.dtype, h->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out,
+                     float* lse, const moe_attn_cache* cache, const moe_attn_batch* b,
+                     const moe_attn_scores* sc, void* stream) {
+  if (!h || !b || !sc) return MOE_ATTN_ERR_INVALID_ARG;
+  const moe_attn_config& c = h->cfg;
+  if (b->num_tokens < 0 || b->num_seqs < 0 || b->max_q < 0) return MOE_ATTN_ERR_INVALID_ARG;
+  if (b->num_tokens > c.max_tokens || b->num_seqs > c.max_seqs)
+    return MOE_ATTN_ERR_TOO_MANY_TOKENS;
+  if (!std::isfinite(sc->scale) || !std::isfinite(sc->softcap) || sc->softcap < 0.0f ||
+      sc->window < 0)
+    return MOE_ATTN_ERR_INVALID_ARG;
+  int st = validate_cache(cache);
+  if (st != MOE_ATTN_OK) return st;
+  if (b->num_tokens == 0 || b->num_seqs == 0 || b->max_q == 0) return MOE_ATTN_OK;
+  if ((st = validate_rows(q)) != MOE_ATTN_OK || (st = validate_rows(out)) != MOE_ATTN_OK) return st;
+  if (!aligned16(q->data) || !aligned16(out->data) || q->token_stride % 8 || q->head_stride % 8 ||
+      out->token_stride % 8 || out->head_stride % 8)
+    return MOE_ATTN_ERR_MISALIGNED;
+  if (overlap(q, out, b->num_tokens, c.q_heads, c.head_dim)) return MOE_ATTN_ERR_INVALID_ARG;
+  if (!b->cu_q || !b->kv_len || !b->page_table || b->columns < 1 || b->table_stride < b->columns)
+    return MOE_ATTN_ERR_INVALID_ARG;
+  if ((long long)b->columns * c.page_size > 0x7fffffffLL - 1024)
+    return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;  // key indexes are int32
+  int cur = -1;
+  if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) cudaSetDevice(h->device);
+  AttnParams p{};
+  p.q = rows(q);
+  p.out = rows(out);
+  p.lse = lse;
+  p.k_pages = static_cast<const uint16_t*>(cache->k);
+  p.v_pages = static_cast<const uint16_t*>(cache->v);
+  p.num_pages = cache->num_pages;
+  p.page_stride = cache->page_stride;
+  p.token_stride = cache->token_stride;
+  p.head_stride = cache->head_stride;
+  p.b = Batch{b->cu_q, b->kv_len, b->page_table, b->table_stride, b->columns, b->num_seqs,
+              b->num_tokens, b->max_q};
+  p.sc = Scores{sc->scale, sc->softcap, sc->window, sc->slopes, sc->prefix};
+  p.hq = c.q_heads;
+  p.hk = c.kv_heads;
+  p.group = c.q_heads / c.kv_heads;
+  p.head_dim = c.head_dim;
+  p.page_shift = log2i(c.page_size);
+  p.err = h->err;
+  return cuda_status(launch_attn_rows(p, c.dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_attn_check_device_errors(moe_attn_handle* h, uint32_t* flags) {
+  if (!h || !flags) return MOE_ATTN_ERR_INVALID_ARG;
+  *flags = 0;
+  cudaSetDevice(h->device);
+  int st;
+  if ((st = cuda_status(cudaDeviceSynchronize())) != MOE_ATTN_OK) return st;
+  uint32_t v = 0;
+  if ((st = cuda_status(cudaMemcpy(&v, h->err, 4, cudaMemcpyDeviceToHost))) != MOE_ATTN_OK)
+    return st;
+  if (v && (st = cuda_status(cudaMemset(h->err, 0, 4))) != MOE_ATTN_OK) return st;
+  *flags = v;
+  return v ? MOE_ATTN_ERR_DEVICE : MOE_ATTN_OK;
+}
+
+}  // extern "C"
