@@ -4,6 +4,7 @@
 #include <new>
 
 #include "attn.h"
+#include "tensor_map.h"
 
 using namespace moe;
 using namespace moe::attn;
@@ -13,7 +14,9 @@ struct moe_attn_handle {
   int device = 0;
   int num_sms = 0;
   void* ws = nullptr;
+  int grid = 0;                 // CTAs of a split launch: one per SM
   unsigned* err = nullptr;
+  Partials decode{};
 };
 
 namespace {
@@ -80,8 +83,11 @@ bool same(const moe_attn_rows* a, const moe_attn_rows* b) {
 int validate_cache(const moe_attn_cache* c) {
   if (!c || !c->k || !c->v) return MOE_ATTN_ERR_INVALID_ARG;
   if (c->num_pages < 1 || c->num_pages > 0x7ffffffeLL) return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
-  if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0)
+  if (c->page_stride <= 0 || c->token_stride <= 0 || c->head_stride <= 0)
     return MOE_ATTN_ERR_INVALID_ARG;
+  if (c->page_stride >= (1LL << 39) || c->token_stride >= (1LL << 39) ||
+      c->head_stride >= (1LL << 39))
+    return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;  // 2^40 bytes: a tensor map's limit
   if (!aligned16(c->k) || !aligned16(c->v) || c->page_stride % 8 || c->token_stride % 8 ||
       c->head_stride % 8)
     return MOE_ATTN_ERR_MISALIGNED;
@@ -105,7 +111,53 @@ int log2i(int v) {
   return n;
 }
 
-size_t workspace(const moe_attn_config&) { return 256; }
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// Workspace carve-up; the order is the order of the fields filled in create().
+struct Layout {
+  size_t off[4];
+  size_t total;
+};
+Layout plan(const moe_attn_config& c) {
+  const size_t d = c.head_dim > 64 ? 128 : 64;
+  const size_t sizes[] = {
+      4,                                        // 0 err
+      kMaxGrid * 4,                             // 1 decode: pieces that arrived
+      kMaxGrid * 2 * kDecodeRows * 8,           // 2 decode: maximum, sum
+      kMaxGrid * 2 * kDecodeRows * d * 4,       // 3 decode: weighted sums
+  };
+  Layout L;
+  size_t o = 0;
+  for (size_t i = 0; i < sizeof(sizes) / sizeof(sizes[0]); ++i) {
+    L.off[i] = o;
+    o += align256(sizes[i]);
+  }
+  L.total = o;
+  return L;
+}
+
+// 4-D view {head_dim, page_size, kv_heads, pages} of K or V, boxes of `rows`
+// rows of one page and head, 64 values wide, 128-byte swizzle. A box that
+// reaches past head_dim, or a page past the cache, is filled with zeros.
+int encode_cache(CUtensorMap* m, const moe_attn_config& c, const moe_attn_cache* k,
+                 const void* base, int rows) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return MOE_ATTN_ERR_CUDA;
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
+                              (cuuint64_t)c.kv_heads, (cuuint64_t)k->num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)k->token_stride * 2, (cuuint64_t)k->head_stride * 2,
+                                 (cuuint64_t)k->page_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    fprintf(stderr, "moe_attn: cuTensorMapEncodeTiled failed (%d)\n", (int)r);
+    return MOE_ATTN_ERR_CUDA;
+  }
+  return MOE_ATTN_OK;
+}
 
 }  // namespace
 
@@ -166,7 +218,7 @@ int moe_attn_workspace_bytes(const moe_attn_config* cfg, size_t* bytes) {
   if (!bytes) return MOE_ATTN_ERR_INVALID_ARG;
   const int st = validate_config(cfg);
   if (st != MOE_ATTN_OK) return st;
-  *bytes = workspace(*cfg);
+  *bytes = plan(*cfg).total;
   return MOE_ATTN_OK;
 }
 
@@ -190,13 +242,19 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn_handle** ou
   h->cfg = *cfg;
   h->device = device;
   h->num_sms = prop.multiProcessorCount;
-  const size_t bytes = workspace(*cfg);
-  if ((st = cuda_status(cudaMalloc(&h->ws, bytes))) != MOE_ATTN_OK ||
-      (st = cuda_status(cudaMemset(h->ws, 0, bytes))) != MOE_ATTN_OK) {
+  h->grid = h->num_sms < kMaxGrid ? h->num_sms : kMaxGrid;
+  const Layout L = plan(*cfg);
+  if ((st = cuda_status(attn_decode_setup())) != MOE_ATTN_OK ||
+      (st = cuda_status(cudaMalloc(&h->ws, L.total))) != MOE_ATTN_OK ||
+      (st = cuda_status(cudaMemset(h->ws, 0, L.total))) != MOE_ATTN_OK) {
     moe_attn_destroy(h);
     return st;
   }
-  h->err = static_cast<unsigned*>(h->ws);
+  uint8_t* b = static_cast<uint8_t*>(h->ws);
+  h->err = reinterpret_cast<unsigned*>(b + L.off[0]);
+  h->decode.count = reinterpret_cast<unsigned*>(b + L.off[1]);
+  h->decode.ml = reinterpret_cast<float2*>(b + L.off[2]);
+  h->decode.o = reinterpret_cast<float*>(b + L.off[3]);
   *out = h;
   return MOE_ATTN_OK;
 }
@@ -297,7 +355,17 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
   p.head_dim = c.head_dim;
   p.page_shift = log2i(c.page_size);
   p.err = h->err;
-  return cuda_status(launch_attn_rows(p, c.dtype, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int box = c.page_size < kDecodeBlock ? c.page_size : kDecodeBlock;
+  CUtensorMap kmap, vmap;
+  if ((st = encode_cache(&kmap, c, cache, cache->k, box)) != MOE_ATTN_OK ||
+      (st = encode_cache(&vmap, c, cache, cache->v, box)) != MOE_ATTN_OK)
+    return st;
+  if ((st = cuda_status(launch_attn_decode(p, h->decode, kmap, vmap, c.dtype, h->grid, s))) !=
+      MOE_ATTN_OK)
+    return st;
+  if ((long long)b->max_q * p.group <= kDecodeRows) return MOE_ATTN_OK;
+  return cuda_status(launch_attn_rows(p, c.dtype, s));
 }
 
 int moe_attn_check_device_errors(moe_attn_handle* h, uint32_t* flags) {

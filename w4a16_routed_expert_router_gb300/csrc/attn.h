@@ -90,7 +90,90 @@ struct AttnParams {
   int hq, hk, group, head_dim, page_shift;
   unsigned* err;
 };
+
 cudaError_t launch_attn_rows(const AttnParams& p, int dtype, cudaStream_t s);
+
+// Split attention: a launch divides its key blocks evenly over the CTAs, in
+// the order of the work items, so a CTA holds the end of one item, whole
+// items, and the beginning of another; items that several CTAs hold are joined
+// by the last of them to finish, in the order of their pieces.
+constexpr int kMaxGrid = 160;         // CTAs of a split launch (152 SMs on GB300)
+constexpr int kDecodeRows = 16;       // query rows per kv head of the few-token kernel
+constexpr int kDecodeBlock = 64;      // keys per block of that kernel
+
+struct Partials {
+  float* o;           // [kMaxGrid][2][rows][head_dim rounded to 64] weighted sums, not normalised
+  float2* ml;         // [kMaxGrid][2][rows] maximum (log2 units) and sum
+  unsigned* count;    // [kMaxGrid] pieces that arrived, by the item's first CTA (self-resetting)
+};
+
+// Keys of one sequence that some query row sees, in blocks of `block` keys:
+// block n of `blocks` is key block n, or n + skip from n = near on (a prefix,
+// a gap, a window).
+struct Span {
+  int first, n, kv;       // q rows [first, first + n), keys
+  int near, skip, blocks;
+};
+
+// The sequence's rows and keys, or n = 0 with the error bit set where they
+// leave their ranges.
+__device__ __forceinline__ Span read_sequence(const Batch& b, int page_shift, int s,
+                                              unsigned* err) {
+  Span r{};
+  const int q0 = b.cu_q[s], q1 = b.cu_q[s + 1], kv = b.kv_len[s];
+  if (q0 < 0 || q1 < q0 || q1 > b.num_tokens || q1 - q0 > b.max_q || kv < 0 ||
+      kv > (b.columns << page_shift)) {
+    atomicOr(err, kErrRange);
+    return r;
+  }
+  r.first = q0;
+  r.n = q1 - q0;
+  r.kv = kv;
+  return r;
+}
+
+__device__ __forceinline__ int prefix_of(const Scores& sc, int s, int kv) {
+  return sc.prefix ? min(kv, max(0, sc.prefix[s])) : 0;
+}
+
+// Blocks seen by rows at positions [p0, p1] (p1 >= p0), at least one.
+__device__ __forceinline__ void span_blocks(Span& r, int p0, int p1, int window, int prefix,
+                                            int block) {
+  const int end = min(r.kv, max(p1 + 1, prefix));
+  const int from = window ? max(0, p0 - window + 1) : 0;
+  const int last = (max(end, 1) + block - 1) / block;      // blocks [.., last)
+  const int wb = min(from / block, last - 1);
+  const int pb = (prefix + block - 1) / block;
+  if (prefix == 0) {
+    r.near = 0;
+    r.skip = wb;
+  } else if (wb <= pb) {
+    r.near = 0;
+    r.skip = 0;
+  } else {
+    r.near = pb;
+    r.skip = wb - pb;
+  }
+  r.blocks = last - r.skip;
+}
+
+// CTA c of `grid` holds blocks [total c / grid, total (c + 1) / grid).
+__device__ __forceinline__ long long share_begin(long long total, int c, int grid) {
+  return total * c / grid;
+}
+// the CTA that holds block i (grid <= total)
+__device__ __forceinline__ int share_of(long long total, long long i, int grid) {
+  int c = (int)(i * grid / total);
+  while (c + 1 < grid && share_begin(total, c + 1, grid) <= i) ++c;
+  while (c > 0 && share_begin(total, c, grid) > i) --c;
+  return c;
+}
+
+// sequences with at most kDecodeRows query rows per kv head; the rest is left
+// to the tensor-core kernel
+cudaError_t attn_decode_setup();
+cudaError_t launch_attn_decode(const AttnParams& p, const Partials& w, const CUtensorMap& kmap,
+                               const CUtensorMap& vmap, int dtype, int grid, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace moe

@@ -1,0 +1,593 @@
+// Attention of a few new tokens per sequence over the paged cache (at most 16
+// query rows per kv head): decode steps and short drafts.
+//
+// Bound by the cache's bytes. The key blocks of all (sequence, kv head) items
+// are divided evenly over one persistent CTA per SM, so ragged lengths, one
+// long sequence and many short ones all keep every SM loading; an item that
+// several CTAs hold is joined by the last of them.
+//
+// Per CTA: warp 0 brings blocks of 64 keys (K and V, 128-byte-swizzled boxes
+// of a page) by TMA into a ring of stages. Warps 1-8 consume: two groups of
+// four take alternate blocks, and each warp 16 keys of its block, with a
+// running maximum, sum and weighted value sum of its own, so no warp waits for
+// another inside an item. The 16 query rows are the M side of mma.sync
+// m16n8k16; rows of other tokens and heads of the group fill it. (mma.sync is
+// enough: 64 keys take about 500 of its cycles an SM, their bytes 1400 at the
+// HBM rate.) At an item's end the eight states are joined by a tree in shared
+// memory.
+#include "attn.h"
+#include "tc_common.cuh"
+
+namespace moe {
+namespace attn {
+namespace {
+
+using namespace tc;
+
+constexpr int kConsumers = 8;
+constexpr int kThreads = (1 + kConsumers) * 32;
+constexpr int kBlk = kDecodeBlock;
+constexpr int kRows = kDecodeRows;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int ND>  // 64-value chunks of a head
+struct Smem {
+  static constexpr int kD = ND * 64;
+  static constexpr int kTile = ND * kBlk * 128;     // K or V of a block
+  static constexpr int kStages = ND == 2 ? 5 : 10;  // 160 KB in flight
+  static constexpr int kPad = kD + 8;               // row stride of a joined state
+  uint8_t ring[kStages][2 * kTile];
+  float o[kConsumers / 2][kRows][kPad];
+  float2 ml[kConsumers / 2][kRows];
+  uint64_t full[kStages], empty[kStages];
+  long long scan[kThreads / 32];
+  long long total, begin_at;
+  int begin_seq, last;
+};
+
+template <typename T>
+__device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16<Bf16>(float* d, const uint32_t* a, uint32_t b0,
+                                            uint32_t b1) {
+  mma_bf16_16816(d, a, b0, b1, d);
+}
+template <>
+__device__ __forceinline__ void mma16<Fp16>(float* d, const uint32_t* a, uint32_t b0,
+                                            uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
+}
+
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                         int c0, int row, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(row), "r"(head),
+      "r"(page)
+      : "memory");
+}
+
+__device__ __forceinline__ Span item_of(const AttnParams& p, int s) {
+  Span r = read_sequence(p.b, p.page_shift, s, p.err);
+  r.blocks = 0;
+  if (r.n > 0 && r.n * p.group <= kRows)
+    span_blocks(r, r.kv - r.n, r.kv - 1, p.sc.window, prefix_of(p.sc, s, r.kv), kBlk);
+  return r;
+}
+
+// log2-space score of a product
+template <bool GEN>
+__device__ __forceinline__ float score(const Scores& sc, float dot, float slope, int away) {
+  if (!GEN) return dot * (sc.scale * kLog2e);
+  float x = dot * sc.scale;
+  if (sc.softcap > 0.0f) {
+    // tanh(y) = 1 - 2 / (1 + e^2y): absolute error of a few 2^-24
+    const float e = ex2(x * (2.0f * kLog2e / sc.softcap));
+    x = sc.softcap * (1.0f - __fdividef(2.0f, 1.0f + e));
+  }
+  return (x - slope * (float)abs(away)) * kLog2e;
+}
+
+template <typename T, int ND, bool GEN>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_decode_kernel(const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, const AttnParams p,
+                       const Partials ws) {
+  typedef Smem<ND> S;
+  extern __shared__ uint8_t smem_raw[];
+  S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], kConsumers / 2);
+    }
+    fence_mbar_init();
+  }
+  // blocks of all sequences, and the sequence at which this CTA's share begins
+  const int per = (p.b.num_seqs + kThreads - 1) / kThreads;
+  const int s0 = min(p.b.num_seqs, (int)threadIdx.x * per);
+  const int s1 = min(p.b.num_seqs, s0 + per);
+  long long mine = 0;
+  for (int q = s0; q < s1; ++q) mine += (long long)item_of(p, q).blocks * p.hk;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s.scan[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += s.scan[i];
+    total += s.scan[i];
+  }
+  const int grid = (int)min((long long)gridDim.x, total);
+  if ((int)blockIdx.x >= grid) return;
+  const long long lo = share_begin(total, blockIdx.x, grid);
+  const long long hi = share_begin(total, blockIdx.x + 1, grid);
+  if (lo >= before && lo < before + mine) {
+    long long at = before;
+    for (int q = s0; q < s1; ++q) {
+      const long long c = (long long)item_of(p, q).blocks * p.hk;
+      if (lo < at + c) {
+        s.begin_seq = q;
+        s.begin_at = at;
+        break;
+      }
+      at += c;
+    }
+  }
+  __syncthreads();
+
+  // walk of the share: `at` is the first block of (seq, head 0)
+  int seq = s.begin_seq;
+  long long at = s.begin_at;
+  long long w = lo;
+  uint32_t stage = 0, ph = 0;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    if (lane == 0) {
+      prefetch_tmap(&kmap);
+      prefetch_tmap(&vmap);
+    }
+    const int ps = 1 << p.page_shift;
+    const int ppb = ps < kBlk ? kBlk / ps : 1;        // boxes of a block
+    const int box_rows = min(ps, kBlk);
+    const int per_batch = 32 / ppb;
+    uint32_t filled = 0, last_ph = 0;
+    bool ok = true;
+    while (w < hi && ok) {
+      const Span it = item_of(p, seq);
+      if (it.blocks == 0) {
+        ++seq;
+        continue;
+      }
+      const int head = (int)((w - at) / it.blocks);
+      int n = (int)((w - at) - (long long)head * it.blocks);
+      const int end = (int)min((long long)it.blocks, n + (hi - w));
+      const int* table = p.b.page_table + (long long)seq * p.b.table_stride;
+      const int bi = lane / ppb, pi = lane - bi * ppb;
+      // a lane holds the page of box pi of block (batch start + bi), one batch ahead
+      const auto fetch = [&](int n0) {
+        const int nn = n0 + bi;
+        const int kb = (nn < it.near ? nn : nn + it.skip) * kBlk;
+        const int key = kb + pi * box_rows;
+        int id = 0;
+        if (nn < end && key < it.kv) {
+          id = __ldg(table + (key >> p.page_shift));
+          if (id < 0 || id >= p.num_pages) {
+            atomicOr(p.err, kErrRange);
+            id = (int)p.num_pages;  // outside the tensor: the box is filled with zeros
+          }
+        }
+        return id;
+      };
+      int ids = fetch(n);
+      while (n < end && ok) {
+        const int batch = min(per_batch, end - n);
+        const int next = n + batch < end ? fetch(n + batch) : 0;
+        for (int i = 0; i < batch; ++i) {
+          const int nn = n + i;
+          const int kb = (nn < it.near ? nn : nn + it.skip) * kBlk;
+          const int boxes = min(ppb, max(0, it.kv - kb + box_rows - 1) / box_rows);
+          const int page = __shfl_sync(0xffffffffu, ids, i * ppb + min(lane, ppb - 1));
+          int go = 1;
+          if (lane == 0) {
+            go = bwait(&s.empty[stage], ph ^ 1u, p.err);
+            if (go) mbar_arrive_expect_tx(&s.full[stage], boxes * box_rows * 128 * ND * 2);
+          }
+          go = __shfl_sync(0xffffffffu, go, 0);
+          if (!go) {
+            ok = false;
+            break;
+          }
+          if (lane < boxes) {
+            const int row = (kb + lane * box_rows) & (ps - 1);
+            const uint32_t dst = smem_u32(s.ring[stage]) + lane * box_rows * 128;
+#pragma unroll
+            for (int c = 0; c < ND; ++c) {
+              tma_page(dst + c * kBlk * 128, &kmap, &s.full[stage], c * 64, row, head, page);
+              tma_page(dst + S::kTile + c * kBlk * 128, &vmap, &s.full[stage], c * 64, row, head,
+                       page);
+            }
+          }
+          filled |= 1u << stage;
+          last_ph = (last_ph & ~(1u << stage)) | (ph << stage);
+          if (++stage == S::kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+        n += batch;
+        ids = next;
+      }
+      w = at + (long long)head * it.blocks + end;
+      if (w == at + (long long)it.blocks * p.hk) {
+        at = w;
+        ++seq;
+      }
+    }
+    // wind down: no TMA copy may still be landing when the CTA exits
+    if (lane == 0)
+      for (int i = 0; i < S::kStages; ++i)
+        if (filled & (1u << i)) mbar_wait(&s.full[i], (last_ph >> i) & 1u, p.err);
+    return;
+  }
+
+  // ------------------------------------------------------------------ consumers
+  const int cw = warp - 1, grp = cw >> 2;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int krow = (cw & 3) * 16;                       // this warp's keys in a block
+  // ldmatrix lane addresses: K rows by key, V rows by key (transposed on load)
+  const int lk_row = krow + (lane & 7) + ((lane >> 4) << 3), lk_c = (lane >> 3) & 1;
+  const int lv_row = krow + (lane & 7) + (((lane >> 3) & 1) << 3), lv_c = lane >> 4;
+  int parity = 0;                                       // blocks this CTA took so far, mod 2
+  bool ok = true;
+  while (w < hi) {
+    const Span it = item_of(p, seq);
+    if (it.blocks == 0) {
+      ++seq;
+      continue;
+    }
+    const int head = (int)((w - at) / it.blocks);
+    const int n0 = (int)((w - at) - (long long)head * it.blocks);
+    const int end = (int)min((long long)it.blocks, n0 + (hi - w));
+    const int rows = it.n * p.group;
+    const int prefix = prefix_of(p.sc, seq, it.kv);
+    // Q fragments; rows gid and gid + 8 are (token r / group, head r % group)
+    uint32_t qf[ND * 4][4];
+    int pos[2];
+    float slope[2];
+    const uint16_t* qp[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = min(gid + 8 * i, rows - 1);
+      const int tok = r / p.group, h = head * p.group + (r - tok * p.group);
+      pos[i] = it.kv - it.n + tok;
+      slope[i] = GEN && p.sc.slopes ? p.sc.slopes[h] : 0.0f;
+      qp[i] = p.q.p + (long long)(it.first + tok) * p.q.token + (long long)h * p.q.head;
+    }
+#pragma unroll
+    for (int k = 0; k < ND * 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = k * 16 + (i >> 1) * 8 + 2 * tig;
+        qf[k][i] = c < p.head_dim && gid + 8 * (i & 1) < rows
+                       ? __ldg(reinterpret_cast<const uint32_t*>(qp[i & 1] + c))
+                       : 0u;
+      }
+    float o[ND * 8][4];
+#pragma unroll
+    for (int i = 0; i < ND * 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+    for (int n = n0; n < end; ++n) {
+      if (parity == grp) {
+        if (ok) ok = warp_wait(&s.full[stage], ph, p.err);
+        const int k0 = (n < it.near ? n : n + it.skip) * kBlk + krow;
+        if (ok && k0 < it.kv) {
+          const uint32_t kt = smem_u32(s.ring[stage]), vt = kt + S::kTile;
+          if (k0 + 16 > it.kv) {
+            // rows behind the last key may hold anything: V takes part in the
+            // product with weight zero, so it is cleared here
+            const int from = krow + it.kv - k0;
+            for (int i = lane; i < (krow + 16 - from) * ND * 8; i += 32) {
+              const int r = from + i / (ND * 8), c = i % (ND * 8);
+              sts128(vt + (c >> 3) * kBlk * 128 + r * 128 + (c & 7) * 16, 0, 0, 0, 0);
+            }
+            __syncwarp();
+          }
+          float sacc[2][4] = {};
+#pragma unroll
+          for (int k = 0; k < ND * 4; ++k) {
+            uint32_t b[4];
+            const int c = (k & 3) * 2 + lk_c;
+            ldsm4(kt + (k >> 2) * kBlk * 128 + lk_row * 128 + ((c ^ (lk_row & 7)) << 4), b);
+            mma16<T>(sacc[0], qf[k], b[0], b[1]);
+            mma16<T>(sacc[1], qf[k], b[2], b[3]);
+          }
+          float mx[2] = {m[0], m[1]};
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = k0 + t * 8 + 2 * tig + (i & 1), r = i >> 1;
+              const int away = pos[r] - key;
+              const bool seen = key < it.kv && (key < prefix || (away >= 0 && (p.sc.window == 0 ||
+                                                                            away < p.sc.window)));
+              sacc[t][i] =
+                  seen ? score<GEN>(p.sc, sacc[t][i], slope[r], away) : -INFINITY;
+              mx[r] = fmaxf(mx[r], sacc[t][i]);
+            }
+          float base[2], scale[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+            base[r] = mx[r] == -INFINITY ? 0.0f : mx[r];
+            scale[r] = ex2(m[r] - base[r]);
+            m[r] = mx[r];
+            l[r] *= scale[r];
+          }
+          uint32_t pf[4];
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float e0 = ex2(sacc[t][2 * r] - base[r]);
+              const float e1 = ex2(sacc[t][2 * r + 1] - base[r]);
+              l[r] += e0 + e1;
+              pf[2 * t + r] = T::pack(e0, e1);
+            }
+          if (__any_sync(0xffffffffu, scale[0] != 1.0f || scale[1] != 1.0f)) {
+#pragma unroll
+            for (int i = 0; i < ND * 8; ++i) {
+              o[i][0] *= scale[0];
+              o[i][1] *= scale[0];
+              o[i][2] *= scale[1];
+              o[i][3] *= scale[1];
+            }
+          }
+#pragma unroll
+          for (int d = 0; d < ND * 4; ++d) {
+            uint32_t b[4];
+            const int c = (d & 3) * 2 + lv_c;
+            ldsm4t(vt + (d >> 2) * kBlk * 128 + lv_row * 128 + ((c ^ (lv_row & 7)) << 4), b);
+            mma16<T>(o[2 * d], pf, b[0], b[1]);
+            mma16<T>(o[2 * d + 1], pf, b[2], b[3]);
+          }
+        }
+        // the generic reads (and the cleared rows) come before the next fill
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.empty[stage]);
+      }
+      parity ^= 1;
+      if (++stage == S::kStages) {
+        stage = 0;
+        ph ^= 1u;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+    // join the eight states: 4-7 into 0-3, 2-3 into 0-1, 1 into 0
+    for (int half = kConsumers / 2; half; half >>= 1) {
+      if (cw >= half && cw < 2 * half) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (gid + 8 * r >= rows) continue;
+          if (tig == 0) s.ml[cw - half][gid + 8 * r] = make_float2(m[r], l[r]);
+#pragma unroll
+          for (int i = 0; i < ND * 8; ++i)
+            *reinterpret_cast<float2*>(&s.o[cw - half][gid + 8 * r][i * 8 + 2 * tig]) =
+                make_float2(o[i][2 * r], o[i][2 * r + 1]);
+        }
+      }
+      consumers_sync();
+      if (cw < half) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (gid + 8 * r >= rows) continue;
+          const float2 x = s.ml[cw][gid + 8 * r];
+          const float mm = fmaxf(m[r], x.x), base = mm == -INFINITY ? 0.0f : mm;
+          const float a = ex2(m[r] - base), b = ex2(x.x - base);
+          m[r] = mm;
+          l[r] = l[r] * a + x.y * b;
+#pragma unroll
+          for (int i = 0; i < ND * 8; ++i) {
+            const float2 v = *reinterpret_cast<const float2*>(
+                &s.o[cw][gid + 8 * r][i * 8 + 2 * tig]);
+            o[i][2 * r] = o[i][2 * r] * a + v.x * b;
+            o[i][2 * r + 1] = o[i][2 * r + 1] * a + v.y * b;
+          }
+        }
+      }
+      consumers_sync();
+    }
+    const long long item0 = at + (long long)head * it.blocks;
+    if (end - n0 == it.blocks) {
+      if (cw == 0) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = gid + 8 * r;
+          if (row >= rows) continue;
+          const int tok = row / p.group, h = head * p.group + (row - tok * p.group);
+          const float inv = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
+          uint16_t* dst = p.out.p + (long long)(it.first + tok) * p.out.token +
+                          (long long)h * p.out.head;
+#pragma unroll
+          for (int i = 0; i < ND * 8; ++i)
+            if (i * 8 < p.head_dim)
+              *reinterpret_cast<uint32_t*>(dst + i * 8 + 2 * tig) =
+                  T::pack(o[i][2 * r] * inv, o[i][2 * r + 1] * inv);
+          if (p.lse && tig == 0)
+            p.lse[(long long)(it.first + tok) * p.hq + h] =
+                l[r] == 0.0f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+        }
+      }
+    } else {
+      // a piece: leave it in the workspace; the last CTA of the item joins them
+      const int c0 = share_of(total, item0, grid);
+      const int c1 = share_of(total, item0 + it.blocks - 1, grid);
+      if (cw == 0) {
+        const long long slot = 2LL * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = gid + 8 * r;
+          if (row >= rows) continue;
+          if (tig == 0) __stcg(ws.ml + slot * kRows + row, make_float2(m[r], l[r]));
+          float* dst = ws.o + (slot * kRows + row) * S::kD;
+#pragma unroll
+          for (int i = 0; i < ND * 8; ++i)
+            __stcg(reinterpret_cast<float2*>(dst + i * 8 + 2 * tig),
+                   make_float2(o[i][2 * r], o[i][2 * r + 1]));
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) {
+          const unsigned got = atomicAdd(ws.count + c0, 1u);
+          s.last = got == (unsigned)(c1 - c0);
+          if (s.last) ws.count[c0] = 0;
+          __threadfence();
+        }
+      }
+      consumers_sync();
+      if (s.last) {
+        const int pieces = c1 - c0 + 1;
+        float* wgt = &s.o[0][0][0];  // [rows][pieces], <= 16 * 160 floats
+        float* sums = reinterpret_cast<float*>(&s.ml[0][0]);
+        const auto slot_of = [&](int i) { return 2LL * (c0 + i) + (i == 0 ? 1 : 0); };
+        for (int row = cw; row < rows; row += kConsumers) {
+          float mm = -INFINITY, sum = 0.0f;
+          for (int i = lane; i < pieces; i += 32)
+            mm = fmaxf(mm, __ldcg(ws.ml + slot_of(i) * kRows + row).x);
+#pragma unroll
+          for (int q = 16; q; q >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, q));
+          const float base = mm == -INFINITY ? 0.0f : mm;
+          for (int i = lane; i < pieces; i += 32) {
+            const float2 x = __ldcg(ws.ml + slot_of(i) * kRows + row);
+            const float e = ex2(x.x - base);
+            wgt[row * pieces + i] = e;
+            sum += x.y * e;
+          }
+#pragma unroll
+          for (int q = 16; q; q >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
+          if (lane == 0) {
+            sums[row] = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int tok = row / p.group, h = head * p.group + (row - tok * p.group);
+            if (p.lse)
+              p.lse[(long long)(it.first + tok) * p.hq + h] =
+                  sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
+          }
+        }
+        consumers_sync();
+        const int half_d = p.head_dim >> 1;
+        for (int e = threadIdx.x - 32; e < rows * half_d; e += kConsumers * 32) {
+          const int row = e / half_d, c = 2 * (e - row * half_d);
+          float x = 0.0f, y = 0.0f;
+#pragma unroll 4
+          for (int i = 0; i < pieces; ++i) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(
+                ws.o + (slot_of(i) * kRows + row) * S::kD + c));
+            const float f = wgt[row * pieces + i];
+            x = fmaf(v.x, f, x);
+            y = fmaf(v.y, f, y);
+          }
+          const int tok = row / p.group, h = head * p.group + (row - tok * p.group);
+          *reinterpret_cast<uint32_t*>(p.out.p + (long long)(it.first + tok) * p.out.token +
+                                       (long long)h * p.out.head + c) =
+              T::pack(x * sums[row], y * sums[row]);
+        }
+      }
+      consumers_sync();  // s.last and the join's buffers are free again
+    }
+    w = item0 + end;
+    if (w == at + (long long)it.blocks * p.hk) {
+      at = w;
+      ++seq;
+    }
+  }
+}
+
+template <int ND>
+constexpr int smem_bytes() {
+  return (int)sizeof(Smem<ND>) + 1024;
+}
+
+template <typename T, int ND, bool GEN>
+cudaError_t setup_one() {
+  return cudaFuncSetAttribute(attn_decode_kernel<T, ND, GEN>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<ND>());
+}
+
+template <typename T, int ND>
+cudaError_t launch_one(const AttnParams& p, const Partials& w, const CUtensorMap& kmap,
+                       const CUtensorMap& vmap, int grid, cudaStream_t s) {
+  if (p.sc.softcap > 0.0f || p.sc.slopes)
+    attn_decode_kernel<T, ND, true><<<grid, kThreads, smem_bytes<ND>(), s>>>(kmap, vmap, p, w);
+  else
+    attn_decode_kernel<T, ND, false><<<grid, kThreads, smem_bytes<ND>(), s>>>(kmap, vmap, p, w);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attn_decode_setup() {
+  cudaError_t e;
+  if ((e = setup_one<Bf16, 1, false>()) != cudaSuccess) return e;
+  if ((e = setup_one<Bf16, 1, true>()) != cudaSuccess) return e;
+  if ((e = setup_one<Bf16, 2, false>()) != cudaSuccess) return e;
+  if ((e = setup_one<Bf16, 2, true>()) != cudaSuccess) return e;
+  if ((e = setup_one<Fp16, 1, false>()) != cudaSuccess) return e;
+  if ((e = setup_one<Fp16, 1, true>()) != cudaSuccess) return e;
+  if ((e = setup_one<Fp16, 2, false>()) != cudaSuccess) return e;
+  return setup_one<Fp16, 2, true>();
+}
+
+cudaError_t launch_attn_decode(const AttnParams& p, const Partials& w, const CUtensorMap& kmap,
+                               const CUtensorMap& vmap, int dtype, int grid, cudaStream_t s) {
+  const bool wide = p.head_dim > 64;
+  if (dtype == MOE_ATTN_BF16)
+    return wide ? launch_one<Bf16, 2>(p, w, kmap, vmap, grid, s)
+                : launch_one<Bf16, 1>(p, w, kmap, vmap, grid, s);
+  return wide ? launch_one<Fp16, 2>(p, w, kmap, vmap, grid, s)
+              : launch_one<Fp16, 1>(p, w, kmap, vmap, grid, s);
+}
+
+}  // namespace attn
+}  // namespace moe

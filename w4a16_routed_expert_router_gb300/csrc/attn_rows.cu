@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const AttnParams
     if (lane == 0) atomicOr(p.err, kErrRange);
     return;
   }
+  if (n * p.group <= kDecodeRows) return;
   const int pos = kv - n + (tok - first);
   const int prefix = p.sc.prefix ? min(kv, max(0, p.sc.prefix[lo])) : 0;
   const float slope = p.sc.slopes ? p.sc.slopes[h] : 0.0f;
