@@ -1,6 +1,7 @@
 // C ABI of the attention operators: argument validation, workspace, dispatch.
 #include <cmath>
 #include <cstdio>
+#include <initializer_list>
 #include <new>
 
 #include "attn.h"
@@ -17,6 +18,7 @@ struct moe_attn_handle {
   int grid = 0;                 // CTAs of a split launch: one per SM
   unsigned* err = nullptr;
   Partials decode{};
+  TcPlan tc{};
 };
 
 namespace {
@@ -115,9 +117,13 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Workspace carve-up; the order is the order of the fields filled in create().
 struct Layout {
-  size_t off[4];
+  size_t off[11];
   size_t total;
 };
+int entries(const moe_attn_config& c) {
+  return c.max_tokens / (2 * tile_tokens(c.q_heads / c.kv_heads)) + c.max_seqs;
+}
+
 Layout plan(const moe_attn_config& c) {
   const size_t d = c.head_dim > 64 ? 128 : 64;
   const size_t sizes[] = {
@@ -125,6 +131,13 @@ Layout plan(const moe_attn_config& c) {
       kMaxGrid * 4,                             // 1 decode: pieces that arrived
       kMaxGrid * 2 * kDecodeRows * 8,           // 2 decode: maximum, sum
       kMaxGrid * 2 * kDecodeRows * d * 4,       // 3 decode: weighted sums
+      entries(c) * sizeof(Entry),               // 4 entries
+      (c.max_seqs + (size_t)1) * 4,             // 5 entries before each sequence
+      kMaxGrid * 4,                             // 6 first entry of each share
+      8,                                        // 7 blocks of all items
+      kMaxGrid * sizeof(Split),                 // 8 split items
+      kMaxGrid * 4 * 128 * 8,                   // 9 maximum, sum
+      kMaxGrid * 4 * 128 * d * 4,               // 10 weighted sums
   };
   Layout L;
   size_t o = 0;
@@ -136,19 +149,12 @@ Layout plan(const moe_attn_config& c) {
   return L;
 }
 
-// 4-D view {head_dim, page_size, kv_heads, pages} of K or V, boxes of `rows`
-// rows of one page and head, 64 values wide, 128-byte swizzle. A box that
-// reaches past head_dim, or a page past the cache, is filled with zeros.
-int encode_cache(CUtensorMap* m, const moe_attn_config& c, const moe_attn_cache* k,
-                 const void* base, int rows) {
+int encode(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims,
+           const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return MOE_ATTN_ERR_CUDA;
-  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
-                              (cuuint64_t)c.kv_heads, (cuuint64_t)k->num_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)k->token_stride * 2, (cuuint64_t)k->head_stride * 2,
-                                 (cuuint64_t)k->page_stride * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, estr[4] = {1, 1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims,
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -157,6 +163,36 @@ int encode_cache(CUtensorMap* m, const moe_attn_config& c, const moe_attn_cache*
     return MOE_ATTN_ERR_CUDA;
   }
   return MOE_ATTN_OK;
+}
+
+// stride in bytes of a tensor map's dimension; one of a single element is free
+cuuint64_t bytes_of(long long stride, long long n, int head_dim) {
+  return (cuuint64_t)(n > 1 ? stride : (head_dim + 7) & ~7) * 2;
+}
+
+// 4-D view {head_dim, page_size, kv_heads, pages} of K or V, boxes of `rows`
+// rows of one page and head, 64 values wide, 128-byte swizzle. A box that
+// reaches past head_dim, or a page past the cache, is filled with zeros.
+int encode_cache(CUtensorMap* m, const moe_attn_config& c, const moe_attn_cache* k,
+                 const void* base, int rows) {
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
+                              (cuuint64_t)c.kv_heads, (cuuint64_t)k->num_pages};
+  const cuuint64_t strides[3] = {bytes_of(k->token_stride, c.page_size, c.head_dim),
+                                 bytes_of(k->head_stride, c.kv_heads, c.head_dim),
+                                 bytes_of(k->page_stride, k->num_pages, c.head_dim)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+  return encode(m, 4, base, dims, strides, box);
+}
+
+// 3-D view {head_dim, q_heads, tokens} of q, boxes of one tile: its tokens by
+// the heads of one group, 64 values wide.
+int encode_q(CUtensorMap* m, const moe_attn_config& c, const moe_attn_rows* q, int tokens) {
+  const int group = c.q_heads / c.kv_heads;
+  const cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.q_heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {bytes_of(q->head_stride, c.q_heads, c.head_dim),
+                                 bytes_of(q->token_stride, tokens, c.head_dim)};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tile_tokens(group)};
+  return encode(m, 3, q->data, dims, strides, box);
 }
 
 }  // namespace
@@ -244,7 +280,11 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn_handle** ou
   h->num_sms = prop.multiProcessorCount;
   h->grid = h->num_sms < kMaxGrid ? h->num_sms : kMaxGrid;
   const Layout L = plan(*cfg);
+  int per_sm = 0;
   if ((st = cuda_status(attn_decode_setup())) != MOE_ATTN_OK ||
+      (st = cuda_status(attn_tc_setup(&per_sm))) != MOE_ATTN_OK ||
+      // a CTA of the tensor-core kernel holds all of its SM's TMEM
+      (st = per_sm == 1 ? MOE_ATTN_OK : MOE_ATTN_ERR_CUDA) != MOE_ATTN_OK ||
       (st = cuda_status(cudaMalloc(&h->ws, L.total))) != MOE_ATTN_OK ||
       (st = cuda_status(cudaMemset(h->ws, 0, L.total))) != MOE_ATTN_OK) {
     moe_attn_destroy(h);
@@ -255,6 +295,14 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn_handle** ou
   h->decode.count = reinterpret_cast<unsigned*>(b + L.off[1]);
   h->decode.ml = reinterpret_cast<float2*>(b + L.off[2]);
   h->decode.o = reinterpret_cast<float*>(b + L.off[3]);
+  h->tc.entries = reinterpret_cast<Entry*>(b + L.off[4]);
+  h->tc.first_entry = reinterpret_cast<int*>(b + L.off[5]);
+  h->tc.begin = reinterpret_cast<int*>(b + L.off[6]);
+  h->tc.total = reinterpret_cast<long long*>(b + L.off[7]);
+  h->tc.split = reinterpret_cast<Split*>(b + L.off[8]);
+  h->tc.ml = reinterpret_cast<float2*>(b + L.off[9]);
+  h->tc.o = reinterpret_cast<float*>(b + L.off[10]);
+  h->tc.capacity = entries(*cfg);
   *out = h;
   return MOE_ATTN_OK;
 }
@@ -330,6 +378,12 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
       out->token_stride % 8 || out->head_stride % 8)
     return MOE_ATTN_ERR_MISALIGNED;
   if (overlap(q, out, b->num_tokens, c.q_heads, c.head_dim)) return MOE_ATTN_ERR_INVALID_ARG;
+  for (const moe_attn_rows* r : {q, out}) {  // broadcast rows are not taken here
+    if ((r->token_stride == 0 && b->num_tokens > 1) || (r->head_stride == 0 && c.q_heads > 1))
+      return MOE_ATTN_ERR_INVALID_ARG;
+    if (r->token_stride >= (1LL << 39) || r->head_stride >= (1LL << 39))
+      return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;  // 2^40 bytes: a tensor map's limit
+  }
   if (!b->cu_q || !b->kv_len || !b->page_table || b->columns < 1 || b->table_stride < b->columns)
     return MOE_ATTN_ERR_INVALID_ARG;
   if ((long long)b->columns * c.page_size > 0x7fffffffLL - 1024)
@@ -355,17 +409,33 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
   p.head_dim = c.head_dim;
   p.page_shift = log2i(c.page_size);
   p.err = h->err;
+  // Sequences of few query rows and of many may share a batch; each kernel takes
+  // its own. Where max_q says that there is one kind only, the other kernel is
+  // not launched, and the one that is takes what comes.
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int box = c.page_size < kDecodeBlock ? c.page_size : kDecodeBlock;
-  CUtensorMap kmap, vmap;
-  if ((st = encode_cache(&kmap, c, cache, cache->k, box)) != MOE_ATTN_OK ||
-      (st = encode_cache(&vmap, c, cache, cache->v, box)) != MOE_ATTN_OK)
-    return st;
-  if ((st = cuda_status(launch_attn_decode(p, h->decode, kmap, vmap, c.dtype, h->grid, s))) !=
-      MOE_ATTN_OK)
-    return st;
-  if ((long long)b->max_q * p.group <= kDecodeRows) return MOE_ATTN_OK;
-  return cuda_status(launch_attn_rows(p, c.dtype, s));
+  const bool many = (long long)b->max_q * p.group > kDecodeRows;
+  const bool few =
+      !many || (b->num_seqs > 1 && b->num_tokens < (long long)b->num_seqs * b->max_q);
+  p.few_rows = few ? kDecodeRows : 0;
+  CUtensorMap qmap, kmap, vmap;
+  if (few) {
+    const int box = c.page_size < kDecodeBlock ? c.page_size : kDecodeBlock;
+    if ((st = encode_cache(&kmap, c, cache, cache->k, box)) != MOE_ATTN_OK ||
+        (st = encode_cache(&vmap, c, cache, cache->v, box)) != MOE_ATTN_OK ||
+        (st = cuda_status(launch_attn_decode(p, h->decode, kmap, vmap, c.dtype, h->grid, s))) !=
+            MOE_ATTN_OK)
+      return st;
+  }
+  if (many) {
+    const int box = c.page_size < kTcBlock ? c.page_size : kTcBlock;
+    if ((st = encode_cache(&kmap, c, cache, cache->k, box)) != MOE_ATTN_OK ||
+        (st = encode_cache(&vmap, c, cache, cache->v, box)) != MOE_ATTN_OK ||
+        (st = encode_q(&qmap, c, q, b->num_tokens)) != MOE_ATTN_OK ||
+        (st = cuda_status(launch_attn_tc(p, h->tc, qmap, kmap, vmap, c.dtype, h->grid, s))) !=
+            MOE_ATTN_OK)
+      return st;
+  }
+  return MOE_ATTN_OK;
 }
 
 int moe_attn_check_device_errors(moe_attn_handle* h, uint32_t* flags) {

@@ -11,6 +11,7 @@ namespace attn {
 
 // one 16-bit element type per kernel instantiation
 struct Bf16 {
+  static constexpr bool kFp16 = false;
   static __device__ __forceinline__ float to_f32(uint16_t v) { return bf16_bits_to_f32(v); }
   static __device__ __forceinline__ uint16_t from_f32(float v) { return f32_to_bf16_bits(v); }
   // two floats -> one word, `lo` in the low half
@@ -20,6 +21,7 @@ struct Bf16 {
   }
 };
 struct Fp16 {
+  static constexpr bool kFp16 = true;
   static __device__ __forceinline__ float to_f32(uint16_t v) {
     return __half2float(__ushort_as_half(v));
   }
@@ -88,10 +90,9 @@ struct AttnParams {
   Batch b;
   Scores sc;
   int hq, hk, group, head_dim, page_shift;
+  int few_rows;  // sequences of at most this many rows per kv head go to the few-token kernel
   unsigned* err;
 };
-
-cudaError_t launch_attn_rows(const AttnParams& p, int dtype, cudaStream_t s);
 
 // Split attention: a launch divides its key blocks evenly over the CTAs, in
 // the order of the work items, so a CTA holds the end of one item, whole
@@ -174,6 +175,46 @@ __device__ __forceinline__ int share_of(long long total, long long i, int grid) 
 cudaError_t attn_decode_setup();
 cudaError_t launch_attn_decode(const AttnParams& p, const Partials& w, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, int dtype, int grid, cudaStream_t s);
+
+
+// ---------------------------------------------------------- tensor-core kernel
+// An entry is up to two tiles of query tokens of one sequence (all kv heads);
+// (entry, kv head) is a work item. A tile's 128 rows are tile_tokens tokens by
+// the heads of one group.
+constexpr int kTcBlock = 128;  // keys per block
+struct Entry {
+  int first, ntok;             // q row of the first token, tokens
+  int p0, kv;                  // position of the first token, keys of the sequence
+  int near, skip, blocks;      // see Span
+  int prefix;
+  long long at;                // blocks of all kv heads before this entry
+  int seq, pad;
+};
+static_assert(sizeof(Entry) == 48, "read as three 16-byte words");
+
+// An item whose first piece ended before it did.
+struct Split {
+  int entry, head, pieces, pad;
+};
+
+struct TcPlan {
+  Entry* entries;     // [capacity]
+  int* first_entry;   // [max_seqs + 1] entries before each sequence
+  int* begin;         // [kMaxGrid] entry at which a CTA's share begins
+  long long* total;   // blocks of all items
+  Split* split;       // [kMaxGrid] by the CTA of the first piece; pieces 0: none
+  float* o;           // [kMaxGrid][2 pieces][2 tiles][dim / 4][128 rows][4]
+  float2* ml;         // [kMaxGrid][2][2][128] maximum (log2 units), sum
+  int capacity;
+};
+
+__host__ __device__ inline int tile_tokens(int group) { return 128 / group; }
+
+// Three kernels: divide the work, attend, join the split items.
+cudaError_t attn_tc_setup(int* ctas_per_sm);
+cudaError_t launch_attn_tc(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
+                           const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, int grid,
+                           cudaStream_t s);
 
 }  // namespace attn
 }  // namespace moe

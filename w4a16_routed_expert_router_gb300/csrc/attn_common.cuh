@@ -1,0 +1,42 @@
+// Device helpers shared by the attention kernels.
+#pragma once
+
+#include "attn.h"
+#include "tc_common.cuh"
+
+namespace moe {
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// one box of a page: rows from `row`, values from `c0`, of a kv head
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                         int c0, int row, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(row), "r"(head),
+      "r"(page)
+      : "memory");
+}
+
+// log2-space score of a product
+template <bool GEN>
+__device__ __forceinline__ float score(const Scores& sc, float dot, float slope, int away) {
+  if (!GEN) return dot * (sc.scale * kLog2e);
+  float x = dot * sc.scale;
+  if (sc.softcap > 0.0f) {
+    // tanh(y) = 1 - 2 / (1 + e^2y): absolute error of a few 2^-24
+    const float e = ex2(x * (2.0f * kLog2e / sc.softcap));
+    x = sc.softcap * (1.0f - __fdividef(2.0f, 1.0f + e));
+  }
+  return (x - slope * (float)abs(away)) * kLog2e;
+}
+
+}  // namespace attn
+}  // namespace moe

@@ -15,8 +15,7 @@
 // enough: 64 keys take about 500 of its cycles an SM, their bytes 1400 at the
 // HBM rate.) At an item's end the eight states are joined by a tree in shared
 // memory.
-#include "attn.h"
-#include "tc_common.cuh"
+#include "attn_common.cuh"
 
 namespace moe {
 namespace attn {
@@ -28,7 +27,6 @@ constexpr int kConsumers = 8;
 constexpr int kThreads = (1 + kConsumers) * 32;
 constexpr int kBlk = kDecodeBlock;
 constexpr int kRows = kDecodeRows;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int ND>  // 64-value chunks of a head
 struct Smem {
@@ -74,23 +72,8 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
-}
-
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
-                                         int c0, int row, int head, int page) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(row), "r"(head),
-      "r"(page)
-      : "memory");
 }
 
 __device__ __forceinline__ Span item_of(const AttnParams& p, int s) {
@@ -99,19 +82,6 @@ __device__ __forceinline__ Span item_of(const AttnParams& p, int s) {
   if (r.n > 0 && r.n * p.group <= kRows)
     span_blocks(r, r.kv - r.n, r.kv - 1, p.sc.window, prefix_of(p.sc, s, r.kv), kBlk);
   return r;
-}
-
-// log2-space score of a product
-template <bool GEN>
-__device__ __forceinline__ float score(const Scores& sc, float dot, float slope, int away) {
-  if (!GEN) return dot * (sc.scale * kLog2e);
-  float x = dot * sc.scale;
-  if (sc.softcap > 0.0f) {
-    // tanh(y) = 1 - 2 / (1 + e^2y): absolute error of a few 2^-24
-    const float e = ex2(x * (2.0f * kLog2e / sc.softcap));
-    x = sc.softcap * (1.0f - __fdividef(2.0f, 1.0f + e));
-  }
-  return (x - slope * (float)abs(away)) * kLog2e;
 }
 
 template <typename T, int ND, bool GEN>

@@ -1,0 +1,813 @@
+// Attention of many new tokens per sequence over the paged cache: prompts and
+// chunks of prompts, on the 5th-generation tensor core.
+//
+// Three launches. attn_plan (one CTA) lists the entries (two tiles of query
+// tokens of one sequence) with their key blocks; attn_tc runs one persistent
+// CTA per SM over an equal share of all key blocks of all (entry, kv head)
+// items; attn_join adds the pieces of items that more than one CTA holds, in
+// their order. Equal shares keep every SM busy to the end under a causal mask,
+// ragged lengths or a single chunk over a long cache.
+//
+// attn_tc, one item: two tiles of 128 query rows (token, head of the group)
+// against blocks of 128 keys, S = Q K^T and O += P V with tcgen05.mma; S and O
+// of both tiles fill the 512 columns of TMEM, and P (16 bits) takes the place
+// of S, whose row a thread has in registers by then, as the A operand in TMEM.
+//   warps 0-3, 4-7  softmax of tile 0 / 1: one row per thread. The running
+//             maximum is only raised when a row exceeds it by 2^8, so that O is
+//             rescaled (by the same threads, in TMEM) in few blocks; numerators
+//             stay below 2^8 and the result is exact either way.
+//   warp 8    TMA producer: Q, and K and V blocks into one ring of slots.
+//   warp 9    MMA issuer. While one tile's softmax runs, the tensor core works
+//             on the other: PV0(j) QK0(j+1) PV1(j) QK1(j+1) ...
+// Every wait is bounded; a timeout sets the error bit and the kernel winds
+// down.
+#include "attn_common.cuh"
+
+namespace moe {
+namespace attn {
+namespace {
+
+using namespace tc;
+
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kBlk = kTcBlock;
+constexpr int kChunk = 128 * 128;   // 128 rows of 64 values
+constexpr float kRaise = 8.0f;      // log2 units
+
+template <int ND>
+struct Smem {
+  static constexpr int kSlots = ND == 2 ? 5 : 8;
+  uint8_t kv[kSlots][ND * kChunk];
+  uint8_t q[2][ND * kChunk];
+  uint64_t kv_full[kSlots], kv_empty[kSlots];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain;
+  uint32_t tmem_base;
+};
+
+// A operand (16-bit, K packed two per column) in TMEM
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory descriptor of an operand whose M/N index is contiguous, rows of
+// 64 values with the 128-byte swizzle: 8 K rows are 1024 B, the next 64 values
+// of M/N a chunk further.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr) {
+  uint64_t desc = 0;
+  desc |= (uint64_t)((addr >> 4) & 0x3FFF);
+  desc |= (uint64_t)((kChunk >> 4) & 0x3FFF) << 16;
+  desc |= (uint64_t)((1024 >> 4) & 0x3FFF) << 32;
+  desc |= (uint64_t)1 << 46;
+  desc |= (uint64_t)2 << 61;
+  return desc;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t idesc_of(int n, bool b_mn) {
+  uint32_t d = idesc_bf16(128, n);
+  if (T::kFp16) d &= ~((1u << 7) | (1u << 10));
+  return d | (b_mn ? 1u << 16 : 0u);
+}
+
+// 32 columns of this thread's TMEM lane, without the wait
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(
+          r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                      int head, int token) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(head), "r"(token)
+      : "memory");
+}
+
+__device__ __forceinline__ void wait_prior_launch() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ Entry load_entry(const Entry* e) {
+  union {
+    Entry v;
+    uint4 w[3];
+  } u;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) u.w[i] = __ldcg(reinterpret_cast<const uint4*>(e) + i);
+  return u.v;
+}
+
+// ------------------------------------------------------------------ the share of a CTA
+// One piece: blocks [n0, end) of an item.
+struct Piece {
+  Entry e;
+  int entry, head, n0, end;
+};
+struct Walk {
+  const TcPlan& w;
+  long long at, hi;
+  int entry;
+  __device__ __forceinline__ bool next(Piece& g, int hk) {
+    if (at >= hi) return false;
+    g.e = load_entry(w.entries + entry);
+    const long long rel = at - g.e.at;
+    g.entry = entry;
+    g.head = (int)(rel / g.e.blocks);
+    g.n0 = (int)(rel - (long long)g.head * g.e.blocks);
+    g.end = (int)min((long long)g.e.blocks, g.n0 + (hi - at));
+    at += g.end - g.n0;
+    if (at == g.e.at + (long long)g.e.blocks * hk) ++entry;
+    return true;
+  }
+};
+
+__device__ __forceinline__ int key_block(const Entry& e, int n) {
+  return n < e.near ? n : n + e.skip;
+}
+
+// listed blocks that rows of tile 0 see (tile 1 sees all, where it has tokens)
+__device__ __forceinline__ int blocks_of_tile0(const Entry& e, int tpt) {
+  const int p1 = e.p0 + min(e.ntok, tpt) - 1;
+  const int end = min(e.kv, max(p1 + 1, e.prefix));
+  const int kb = (max(end, 1) + kBlk - 1) / kBlk;
+  return min(e.blocks, kb <= e.near ? kb : max(max(e.near, 1), kb - e.skip));
+}
+
+// ------------------------------------------------------------------ plan
+__global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, const TcPlan w,
+                                                         int grid) {
+  __shared__ long long part[32];
+  __shared__ long long whole;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  let_next_launch();
+  const int span = 2 * tile_tokens(p.group);
+  // exclusive scan of one value per thread; the sum is left in `whole`
+  const auto scan = [&](long long mine) {
+    long long v = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+      long long x = part[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += u;
+      }
+      part[lane] = x;
+      if (lane == 31) whole = x;
+    }
+    __syncthreads();
+    return v - mine + (warp ? part[warp - 1] : 0);
+  };
+
+  for (int c = tid; c < grid; c += blockDim.x) w.split[c].pieces = 0;
+  // entries of each sequence
+  const int per = (p.b.num_seqs + 1023) / 1024;
+  const int s0 = min(p.b.num_seqs, tid * per), s1 = min(p.b.num_seqs, s0 + per);
+  const auto count = [&](int s) {
+    const Span r = read_sequence(p.b, p.page_shift, s, p.err);
+    return r.n * p.group > p.few_rows ? (r.n + span - 1) / span : 0;
+  };
+  long long mine = 0;
+  for (int s = s0; s < s1; ++s) mine += count(s);
+  long long at = scan(mine);
+  const long long n_all = whole;
+  if (n_all > w.capacity) {  // only where cu_q lists rows twice
+    if (tid == 0) {
+      atomicOr(p.err, kErrRange);
+      *w.total = 0;
+    }
+    return;
+  }
+  for (int s = s0; s < s1; ++s) {
+    w.first_entry[s] = (int)at;
+    at += count(s);
+  }
+  __syncthreads();  // first_entry is read below by other threads of this CTA
+  // the entries, a run of them per thread
+  const int n = (int)n_all;
+  const int run = (n + 1023) / 1024;
+  const int e0 = min(n, tid * run), e1 = min(n, e0 + run);
+  long long blocks = 0;
+  for (int i = e0; i < e1; ++i) {
+    int lo = 0, hi = p.b.num_seqs - 1;  // last sequence with first_entry <= i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (w.first_entry[mid] <= i)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    Span r = read_sequence(p.b, p.page_shift, lo, p.err);
+    const int t0 = (i - w.first_entry[lo]) * span;
+    Entry e;
+    e.first = r.first + t0;
+    e.ntok = min(span, r.n - t0);
+    e.p0 = r.kv - r.n + t0;
+    e.kv = r.kv;
+    e.prefix = prefix_of(p.sc, lo, r.kv);
+    span_blocks(r, e.p0, e.p0 + e.ntok - 1, p.sc.window, e.prefix, kBlk);
+    e.near = r.near;
+    e.skip = r.skip;
+    e.blocks = r.blocks;
+    e.at = blocks;
+    e.seq = lo;
+    e.pad = 0;
+    w.entries[i] = e;
+    blocks += (long long)r.blocks * p.hk;
+  }
+  const long long before = scan(blocks);
+  const long long total = whole;
+  if (tid == 0) *w.total = total;
+  if (total == 0) return;
+  const int g = (int)min((long long)grid, total);
+  for (int i = e0; i < e1; ++i) {
+    const long long a = before + w.entries[i].at;
+    const long long b = a + (long long)w.entries[i].blocks * p.hk;
+    w.entries[i].at = a;
+    for (int c = share_of(total, a, g); c < g; ++c) {  // shares that begin in [a, b)
+      const long long lo = share_begin(total, c, g);
+      if (lo >= b) break;
+      if (lo >= a) w.begin[c] = i;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ attention
+template <typename T, int ND, bool GEN>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap qmap,
+                   const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap, const AttnParams p, const TcPlan ws) {
+  typedef Smem<ND> S;
+  extern __shared__ uint8_t smem_raw[];
+  S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&s.kv_full[i], 1);
+      mbar_init(&s.kv_empty[i], 1);
+    }
+    mbar_init(&s.q_full, 1);
+    mbar_init(&s.q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s.s_full[t], 1);
+      mbar_init(&s.p_full[t], 4);
+      mbar_init(&s.o_full[t], 1);
+      mbar_init(&s.o_empty[t], 4);
+    }
+    mbar_init(&s.drain, 1);
+    fence_mbar_init();
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+  }
+  if (warp == kMmaWarp) tmem_alloc(&s.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  wait_prior_launch();
+
+  const long long total = __ldcg(ws.total);
+  const int grid = (int)min((long long)gridDim.x, total);
+  const int tpt = tile_tokens(p.group);
+  const bool busy = (int)blockIdx.x < grid;
+  Walk walk{ws, busy ? share_begin(total, blockIdx.x, grid) : 0,
+            busy ? share_begin(total, blockIdx.x + 1, grid) : 0,
+            busy ? __ldcg(ws.begin + blockIdx.x) : 0};
+  Piece g;
+
+  if (warp == kTmaWarp) {
+    // ---------------------------------------------------------------- producer
+    const int ps = 1 << p.page_shift;
+    const int ppb = ps < kBlk ? kBlk / ps : 1;
+    const int box_rows = min(ps, kBlk);
+    const int per_batch = 32 / ppb;
+    uint32_t slot = 0, ph = 0, filled = 0, last_ph = 0, qph = 0;
+    bool ok = true, q_used = false;
+    while (ok && walk.next(g, p.hk)) {
+      const int* table = p.b.page_table + (long long)g.e.seq * p.b.table_stride;
+      const int bi = lane / ppb, pi = lane - bi * ppb;
+      const auto fetch = [&](int n0) {
+        const int nn = n0 + bi;
+        const int key = key_block(g.e, nn) * kBlk + pi * box_rows;
+        int id = 0;
+        if (nn < g.end && key < g.e.kv) {
+          id = __ldg(table + (key >> p.page_shift));
+          if (id < 0 || id >= p.num_pages) {
+            atomicOr(p.err, kErrRange);
+            id = (int)p.num_pages;  // outside the tensor: the box is filled with zeros
+          }
+        }
+        return id;
+      };
+      int ids = fetch(g.n0);
+      // Q: tile t's tokens by the group's heads
+      if (lane == 0) {
+        ok = bwait(&s.q_empty, qph ^ 1u, p.err);
+        if (ok) {
+          const int tiles = g.e.ntok > tpt ? 2 : 1;
+          mbar_arrive_expect_tx(&s.q_full, tiles * ND * tpt * p.group * 128);
+          for (int t = 0; t < tiles; ++t)
+#pragma unroll
+            for (int c = 0; c < ND; ++c)
+              tma_q(smem_u32(s.q[t]) + c * kChunk, &qmap, &s.q_full, c * 64, g.head * p.group,
+                    g.e.first + t * tpt);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      q_used = true;
+      qph ^= 1u;
+      for (int n = g.n0; n < g.end && ok;) {
+        const int batch = min(per_batch, g.end - n);
+        const int next = n + batch < g.end ? fetch(n + batch) : 0;
+        for (int i = 0; i < batch && ok; ++i) {
+          const int kb = key_block(g.e, n + i) * kBlk;
+          const int boxes = min(ppb, max(0, g.e.kv - kb + box_rows - 1) / box_rows);
+          const int page = __shfl_sync(0xffffffffu, ids, i * ppb + min(lane, ppb - 1));
+          const int row = (kb + lane * box_rows) & (ps - 1);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            if (lane == 0) {
+              ok = bwait(&s.kv_empty[slot], ph ^ 1u, p.err);
+              if (ok) mbar_arrive_expect_tx(&s.kv_full[slot], boxes * box_rows * 128 * ND);
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            if (lane < boxes) {
+              const uint32_t dst = smem_u32(s.kv[slot]) + lane * box_rows * 128;
+#pragma unroll
+              for (int c = 0; c < ND; ++c)
+                tma_page(dst + c * kChunk, kv ? &vmap : &kmap, &s.kv_full[slot], c * 64, row,
+                         g.head, page);
+            }
+            filled |= 1u << slot;
+            last_ph = (last_ph & ~(1u << slot)) | (ph << slot);
+            if (++slot == S::kSlots) {
+              slot = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+        n += batch;
+        ids = next;
+      }
+    }
+    // wind down: no TMA copy may still be landing when the CTA exits
+    if (lane == 0) {
+      for (int i = 0; i < S::kSlots; ++i)
+        if (filled & (1u << i)) mbar_wait(&s.kv_full[i], (last_ph >> i) & 1u, p.err);
+      if (q_used) mbar_wait(&s.q_full, qph ^ 1u, p.err);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- MMA issuer
+    const int ksteps = (p.head_dim + 15) / 16;
+    const int dn = (p.head_dim + 15) & ~15;
+    const uint32_t id_qk = idesc_of<T>(kBlk, false), id_pv = idesc_of<T>(dn, true);
+    uint32_t slot = 0, ph = 0, qph = 0;
+    uint32_t pph[2] = {0, 0}, oph[2] = {0, 0};
+    bool ok = true;
+    const auto issue_qk = [&](int t, uint32_t kslot) {
+      const uint32_t a = smem_u32(s.q[t]), b = smem_u32(s.kv[kslot]);
+      for (int k = 0; k < ksteps; ++k) {
+        const uint32_t o = (k >> 2) * kChunk + (k & 3) * 32;
+        mma_bf16(tmem + t * 128, smem_desc_sw128(a + o), smem_desc_sw128(b + o), id_qk, k != 0);
+      }
+      mma_commit(&s.s_full[t]);
+    };
+    const auto advance = [&]() {
+      if (++slot == S::kSlots) {
+        slot = 0;
+        ph ^= 1u;
+      }
+    };
+    while (ok && walk.next(g, p.hk)) {
+      const int blocks = g.end - g.n0;
+      int cnt[2];
+      cnt[0] = min(g.end, blocks_of_tile0(g.e, tpt)) - g.n0;
+      cnt[1] = g.e.ntok > tpt ? blocks : 0;
+      if (!warp_wait(&s.q_full, qph, p.err) || !warp_wait(&s.kv_full[slot], ph, p.err)) break;
+      qph ^= 1u;
+      if (lane == 0) {
+        tc_fence_after();
+        if (cnt[0] > 0) issue_qk(0, slot);
+        if (cnt[1] > 0) issue_qk(1, slot);
+        mma_commit(&s.kv_empty[slot]);
+        if (blocks == 1) mma_commit(&s.q_empty);
+      }
+      __syncwarp();
+      advance();
+      for (int j = 0; j < blocks; ++j) {
+        const uint32_t vslot = slot;
+        if (!(ok = warp_wait(&s.kv_full[vslot], ph, p.err))) break;
+        advance();
+        const int left = g.e.kv - key_block(g.e, g.n0 + j) * kBlk;
+        if (left < kBlk) {
+          // rows behind the last key may hold anything, and V takes part in the
+          // product with weight zero: clear them
+          const uint32_t v = smem_u32(s.kv[vslot]);
+          const int from = max(left, 0);
+          for (int i = lane; i < (kBlk - from) * ND * 8; i += 32) {
+            const int r = from + i / (ND * 8), c = i % (ND * 8);
+            sts128(v + (c >> 3) * kChunk + r * 128 + (c & 7) * 16, 0, 0, 0, 0);
+          }
+          fence_async_shared();
+          __syncwarp();
+        }
+        const bool more = j + 1 < blocks;
+        const uint32_t kslot = slot;
+        if (more) {
+          if (!(ok = warp_wait(&s.kv_full[kslot], ph, p.err))) break;
+          advance();
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (j >= cnt[t]) continue;
+          if (j == 0) {  // the previous piece's O has been read
+            if (!(ok = warp_wait(&s.o_empty[t], oph[t] ^ 1u, p.err))) break;
+            oph[t] ^= 1u;
+          }
+          if (!(ok = warp_wait(&s.p_full[t], pph[t], p.err))) break;
+          pph[t] ^= 1u;
+          if (lane == 0) {
+            tc_fence_after();
+            const uint32_t v = smem_u32(s.kv[vslot]);
+            const uint32_t o = tmem + 256 + t * ND * 64;
+#pragma unroll
+            for (int k = 0; k < kBlk / 16; ++k)
+              mma_ts(o, tmem + t * 128 + k * 8, smem_desc_mn(v + k * 2048), id_pv, (j | k) != 0);
+            if (j + 1 == cnt[t]) mma_commit(&s.o_full[t]);
+            if (j + 1 < cnt[t]) issue_qk(t, kslot);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          mma_commit(&s.kv_empty[vslot]);
+          if (more) mma_commit(&s.kv_empty[kslot]);
+          if (j + 2 == blocks) mma_commit(&s.q_empty);
+        }
+        __syncwarp();
+      }
+    }
+    // wind down: every MMA issued here has completed before the exit
+    if (lane == 0) {
+      mma_commit(&s.drain);
+      mbar_wait(&s.drain, 0, p.err);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int t = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + t * 128;
+    const uint32_t o_tm = tmem + lane_base + 256 + t * ND * 64;
+    const int tok = row / p.group, hg = row - tok * p.group;  // token of the tile, head of the group
+    // scores are dot products until the exponent (plain), or log2 units (GEN)
+    const float c = GEN ? 1.0f : p.sc.scale * kLog2e;
+    const float raise = GEN ? kRaise : kRaise / c;
+    uint32_t sph = 0, oph = 0;
+    while (walk.next(g, p.hk)) {
+      const Entry& e = g.e;
+      const int ntok = min(tpt, e.ntok - t * tpt);        // tokens of this tile
+      if (ntok <= 0) continue;
+      const int last = t == 0 ? blocks_of_tile0(e, tpt) : e.blocks;
+      const int cnt = min(g.end, last) - g.n0;
+      const int p_first = e.p0 + t * tpt;
+      const int pos = p_first + tok;
+      const int lo = p.sc.window ? pos - p.sc.window : 0;
+      const int lo_last = p.sc.window ? p_first + ntok - 1 - p.sc.window : -1;
+      const bool mine = tok < ntok;                       // this row exists
+      const int h = g.head * p.group + hg;
+      const float slope = GEN && p.sc.slopes ? p.sc.slopes[min(h, p.hq - 1)] : 0.0f;
+      float m = -INFINITY, l = 0.0f;
+      bool ok = true;
+      for (int j = 0; j < cnt; ++j) {
+        if (!(ok = warp_wait(&s.s_full[t], sph, p.err))) break;
+        sph ^= 1u;
+        tc_fence_after();
+        const int kb = key_block(e, g.n0 + j) * kBlk;
+        float x[kBlk];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          tmem_ld32_nowait(s_tm + i * 32, reinterpret_cast<uint32_t*>(x) + i * 32);
+        tmem_ld_wait();
+        if (GEN) {
+#pragma unroll
+          for (int i = 0; i < kBlk; ++i) x[i] = score<true>(p.sc, x[i], slope, pos - kb - i);
+        }
+        // every row of the tile sees every key of the block, or not
+        const bool whole = (kb + kBlk - 1 <= p_first && kb > lo_last) || kb + kBlk <= e.prefix;
+        if (!whole) {
+          const int a = pos - kb, b = lo - kb, pre = e.prefix - kb;
+          const bool window = p.sc.window != 0;
+#pragma unroll
+          for (int i = 0; i < kBlk; ++i)
+            if (!((i <= a && (!window || i > b)) || i < pre)) x[i] = -INFINITY;
+        }
+        float mx = x[0];
+#pragma unroll
+        for (int i = 1; i < kBlk; ++i) mx = fmaxf(mx, x[i]);
+        if (__any_sync(0xffffffffu, mx > m + raise)) {
+          const float m2 = fmaxf(m, mx);
+          const float a = ex2((m - (m2 == -INFINITY ? 0.0f : m2)) * c);
+          l *= a;
+          m = m2;
+          if (j > 0) {
+#pragma unroll
+            for (int i = 0; i < ND * 2; ++i) {
+              uint32_t r[32];
+              tmem_ld32_nowait(o_tm + i * 32, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * a);
+              tmem_st32(o_tm + i * 32, r);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.0f : m * c;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t r[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float e0 = ex2(fmaf(x[half * 64 + 2 * i], c, -base));
+            const float e1 = ex2(fmaf(x[half * 64 + 2 * i + 1], c, -base));
+            sum[(2 * i) & 3] += e0;
+            sum[(2 * i + 1) & 3] += e1;
+            r[i] = T::pack(e0, e1);
+          }
+          tmem_st32(s_tm + half * 32, r);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.p_full[t]);
+      }
+      if (!ok) break;
+      const bool split = g.end - g.n0 < e.blocks;
+      if (cnt > 0) {
+        if (!warp_wait(&s.o_full[t], oph, p.err)) break;
+        oph ^= 1u;
+        tc_fence_after();
+      }
+      if (!split) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* dst = p.out.p + (long long)(e.first + t * tpt + tok) * p.out.token +
+                        (long long)h * p.out.head;
+#pragma unroll
+        for (int i = 0; i < ND * 2; ++i) {
+          uint32_t r[32];
+          tmem_ld32_nowait(o_tm + i * 32, r);
+          tmem_ld_wait();
+          if (mine) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (i * 32 + k * 8 < p.head_dim) {
+                uint4 v;
+                v.x = T::pack(__uint_as_float(r[8 * k]) * inv, __uint_as_float(r[8 * k + 1]) * inv);
+                v.y = T::pack(__uint_as_float(r[8 * k + 2]) * inv,
+                              __uint_as_float(r[8 * k + 3]) * inv);
+                v.z = T::pack(__uint_as_float(r[8 * k + 4]) * inv,
+                              __uint_as_float(r[8 * k + 5]) * inv);
+                v.w = T::pack(__uint_as_float(r[8 * k + 6]) * inv,
+                              __uint_as_float(r[8 * k + 7]) * inv);
+                *reinterpret_cast<uint4*>(dst + i * 32 + k * 8) = v;
+              }
+          }
+        }
+        if (mine && p.lse)
+          p.lse[(long long)(e.first + t * tpt + tok) * p.hq + h] =
+              l == 0.0f ? -INFINITY : (m * c + log2f(l)) * kLn2;
+      } else {
+        // a piece: slot 1 of the item's first CTA, slot 0 of the others
+        const bool begins = g.n0 == 0;
+        const long long sl = (2LL * blockIdx.x + (begins ? 1 : 0)) * 2 + t;
+        ws.ml[sl * 128 + row] = make_float2(m * c, l);
+        if (cnt > 0) {
+          float4* dst = reinterpret_cast<float4*>(ws.o) + sl * (ND * 16) * 128 + row;
+#pragma unroll
+          for (int i = 0; i < ND * 2; ++i) {
+            uint32_t r[32];
+            tmem_ld32_nowait(o_tm + i * 32, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              dst[(i * 8 + k) * 128] =
+                  make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
+                              __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
+          }
+        }
+        if (begins && t == 0 && row == 0) {
+          const long long item0 = e.at + (long long)g.head * e.blocks;
+          const int c1 = share_of(total, item0 + e.blocks - 1, grid);
+          Split sp;
+          sp.entry = g.entry;
+          sp.head = g.head;
+          sp.pieces = c1 - (int)blockIdx.x + 1;
+          sp.pad = 0;
+          ws.split[blockIdx.x] = sp;
+        }
+      }
+      if (cnt > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.o_empty[t]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  let_next_launch();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ join
+// 32 rows of a tile of one split item per CTA; a lane is a row.
+template <typename T, int ND>
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, const TcPlan w) {
+  wait_prior_launch();
+  const int c0 = blockIdx.x, t = blockIdx.y >> 2;
+  const Split sp = w.split[c0];
+  if (sp.pieces == 0) return;
+  const Entry e = load_entry(w.entries + sp.entry);
+  const int warp = threadIdx.x >> 5, row = (blockIdx.y & 3) * 32 + (threadIdx.x & 31);
+  const int tpt = tile_tokens(p.group);
+  const int tok = row / p.group, hg = row - tok * p.group;
+  if (tok >= min(tpt, e.ntok - t * tpt)) return;
+  const auto slot = [&](int i) { return (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * 2 + t; };
+  float m = -INFINITY;
+  for (int i = 0; i < sp.pieces; ++i) {
+    const float2 x = w.ml[slot(i) * 128 + row];
+    if (x.y != 0.0f) m = fmaxf(m, x.x);
+  }
+  const float base = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  float4 acc[ND * 4];
+#pragma unroll
+  for (int k = 0; k < ND * 4; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i = 0; i < sp.pieces; ++i) {
+    const float2 x = w.ml[slot(i) * 128 + row];
+    if (x.y == 0.0f) continue;  // saw no key: its sums may not have been written
+    const float f = ex2(x.x - base);
+    l += x.y * f;
+    const float4* src = reinterpret_cast<const float4*>(w.o) + slot(i) * (ND * 16) * 128 + row;
+#pragma unroll
+    for (int k = 0; k < ND * 4; ++k) {
+      const float4 v = src[(k * 4 + warp) * 128];
+      acc[k].x = fmaf(v.x, f, acc[k].x);
+      acc[k].y = fmaf(v.y, f, acc[k].y);
+      acc[k].z = fmaf(v.z, f, acc[k].z);
+      acc[k].w = fmaf(v.w, f, acc[k].w);
+    }
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const long long r = e.first + t * tpt + tok;
+  const int h = sp.head * p.group + hg;
+  uint16_t* dst = p.out.p + r * p.out.token + (long long)h * p.out.head;
+#pragma unroll
+  for (int k = 0; k < ND * 4; ++k) {
+    const int d = (k * 4 + warp) * 4;
+    if (d < p.head_dim)
+      *reinterpret_cast<uint2*>(dst + d) =
+          make_uint2(T::pack(acc[k].x * inv, acc[k].y * inv), T::pack(acc[k].z * inv, acc[k].w * inv));
+  }
+  if (p.lse && warp == 0)
+    p.lse[r * p.hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <int ND>
+constexpr int smem_bytes() {
+  return (int)sizeof(Smem<ND>) + 1024;
+}
+// A CTA holds all of TMEM, so there may be one per SM only.
+static_assert(2 * smem_bytes<1>() > 228 * 1024 && 2 * smem_bytes<2>() > 228 * 1024,
+              "attn_tc_kernel must stay at one CTA per SM");
+static_assert(smem_bytes<2>() <= 227 * 1024, "shared memory of a CTA");
+
+template <typename F>
+cudaError_t setup_one(F f, int bytes, int* per_sm) {
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  int n = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, kThreads, bytes);
+  if (n != 1) *per_sm = n;
+  return e;
+}
+
+template <typename T, int ND>
+cudaError_t setup_nd(int* per_sm) {
+  cudaError_t e = setup_one(attn_tc_kernel<T, ND, false>, smem_bytes<ND>(), per_sm);
+  return e != cudaSuccess ? e : setup_one(attn_tc_kernel<T, ND, true>, smem_bytes<ND>(), per_sm);
+}
+
+// a launch that may begin while the one before it ends (it waits for its data itself)
+template <typename... A, typename... B>
+cudaError_t launch_after(void (*f)(A...), dim3 grid, int threads, int smem, cudaStream_t s,
+                         B... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, args...);
+}
+
+template <typename T, int ND>
+cudaError_t launch_nd(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
+                      const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
+  // the plain form takes the maximum before it scales
+  const bool gen = p.sc.softcap > 0.0f || p.sc.slopes || !(p.sc.scale > 0.0f);
+  cudaError_t e = launch_after(gen ? attn_tc_kernel<T, ND, true> : attn_tc_kernel<T, ND, false>,
+                               dim3(grid), kThreads, smem_bytes<ND>(), s, qmap, kmap, vmap, p, w);
+  if (e != cudaSuccess) return e;
+  return launch_after(attn_join_kernel<T, ND>, dim3(grid, 8), 128, 0, s, p, w);
+}
+
+}  // namespace
+
+cudaError_t attn_tc_setup(int* ctas_per_sm) {
+  *ctas_per_sm = 1;
+  cudaError_t e;
+  if ((e = setup_nd<Bf16, 1>(ctas_per_sm)) != cudaSuccess) return e;
+  if ((e = setup_nd<Bf16, 2>(ctas_per_sm)) != cudaSuccess) return e;
+  if ((e = setup_nd<Fp16, 1>(ctas_per_sm)) != cudaSuccess) return e;
+  return setup_nd<Fp16, 2>(ctas_per_sm);
+}
+
+cudaError_t launch_attn_tc(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
+                           const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, int grid,
+                           cudaStream_t s) {
+  attn_plan_kernel<<<1, 1024, 0, s>>>(p, w, grid);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const bool wide = p.head_dim > 64;
+  if (dtype == MOE_ATTN_BF16)
+    return wide ? launch_nd<Bf16, 2>(p, w, qmap, kmap, vmap, grid, s)
+                : launch_nd<Bf16, 1>(p, w, qmap, kmap, vmap, grid, s);
+  return wide ? launch_nd<Fp16, 2>(p, w, qmap, kmap, vmap, grid, s)
+              : launch_nd<Fp16, 1>(p, w, qmap, kmap, vmap, grid, s);
+}
+
+}  // namespace attn
+}  // namespace moe
