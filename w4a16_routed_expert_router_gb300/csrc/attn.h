@@ -187,7 +187,7 @@ struct Entry {
   int p0, kv;                  // position of the first token, keys of the sequence
   int near, skip, blocks;      // see Span
   int prefix;
-  long long at;                // blocks of all kv heads before this entry
+  long long at;                // units of all kv heads before this entry
   int seq, pad;
 };
 static_assert(sizeof(Entry) == 48, "read as three 16-byte words");
@@ -201,7 +201,7 @@ struct TcPlan {
   Entry* entries;     // [capacity]
   int* first_entry;   // [max_seqs + 1] entries before each sequence
   int* begin;         // [kMaxGrid] entry at which a CTA's share begins
-  long long* total;   // blocks of all items
+  long long* total;   // units of all items
   Split* split;       // [kMaxGrid] by the CTA of the first piece; pieces 0: none
   float* o;           // [kMaxGrid][2 pieces][2 tiles][dim / 4][128 rows][4]
   float2* ml;         // [kMaxGrid][2][2][128] maximum (log2 units), sum

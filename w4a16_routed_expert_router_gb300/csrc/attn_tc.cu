@@ -30,10 +30,18 @@ namespace {
 using namespace tc;
 
 constexpr int kSoftmaxWarps = 8;
-constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+constexpr int kThreads = (kSoftmaxWarps + 4) * 32;  // whole warpgroups: setmaxnreg
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
+// Registers a thread: the launch gives every thread kLaunchRegs; the producer
+// warpgroup hands most of its share to the two softmax warpgroups, whose rows
+// of 128 scores do not fit otherwise.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "setmaxnreg draws on the launch");
 constexpr int kBlk = kTcBlock;
 constexpr int kChunk = 128 * 128;   // 128 rows of 64 values
+// An item's fixed cost, in blocks (prefill of 8192 tokens: 0 -> 902 us, 1 -> 717,
+// 2 -> 624, 4 -> 635, 7 -> 654; 16 prompts of 1024: 387, 328, 299, 312, 325).
+constexpr int kItemUnits = 2;
 constexpr float kRaise = 8.0f;      // log2 units
 
 template <int ND>
@@ -93,21 +101,65 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+// After the wait: values of a load before it, so that no use of them moves
+// above the wait.
+__device__ __forceinline__ void loaded16(uint32_t* r) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+// 16 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(
-          r[0]),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// two fp32 values in one 64-bit register
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 __device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0,
@@ -137,6 +189,10 @@ __device__ __forceinline__ Entry load_entry(const Entry* e) {
 }
 
 // ------------------------------------------------------------------ the share of a CTA
+// Shares are counted in units: kItemUnits for an item's fixed cost (Q, the
+// results), then one for each of its blocks.
+__device__ __forceinline__ int units_of(const Entry& e) { return e.blocks + kItemUnits; }
+
 // One piece: blocks [n0, end) of an item.
 struct Piece {
   Entry e;
@@ -146,17 +202,23 @@ struct Walk {
   const TcPlan& w;
   long long at, hi;
   int entry;
+  // the next piece with blocks
   __device__ __forceinline__ bool next(Piece& g, int hk) {
-    if (at >= hi) return false;
-    g.e = load_entry(w.entries + entry);
-    const long long rel = at - g.e.at;
-    g.entry = entry;
-    g.head = (int)(rel / g.e.blocks);
-    g.n0 = (int)(rel - (long long)g.head * g.e.blocks);
-    g.end = (int)min((long long)g.e.blocks, g.n0 + (hi - at));
-    at += g.end - g.n0;
-    if (at == g.e.at + (long long)g.e.blocks * hk) ++entry;
-    return true;
+    while (at < hi) {
+      g.e = load_entry(w.entries + entry);
+      const int units = units_of(g.e);
+      const long long rel = at - g.e.at;
+      g.entry = entry;
+      g.head = (int)(rel / units);
+      const int u0 = (int)(rel - (long long)g.head * units);
+      const int u1 = (int)min((long long)units, u0 + (hi - at));
+      at += u1 - u0;
+      if (at == g.e.at + (long long)units * hk) ++entry;
+      g.n0 = max(0, u0 - kItemUnits);
+      g.end = max(0, u1 - kItemUnits);
+      if (g.end > g.n0) return true;
+    }
+    return false;
   }
 };
 
@@ -259,7 +321,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, con
     e.seq = lo;
     e.pad = 0;
     w.entries[i] = e;
-    blocks += (long long)r.blocks * p.hk;
+    blocks += (long long)(r.blocks + kItemUnits) * p.hk;
   }
   const long long before = scan(blocks);
   const long long total = whole;
@@ -268,7 +330,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, con
   const int g = (int)min((long long)grid, total);
   for (int i = e0; i < e1; ++i) {
     const long long a = before + w.entries[i].at;
-    const long long b = a + (long long)w.entries[i].blocks * p.hk;
+    const long long b = a + (long long)units_of(w.entries[i]) * p.hk;
     w.entries[i].at = a;
     for (int c = share_of(total, a, g); c < g; ++c) {  // shares that begin in [a, b)
       const long long lo = share_begin(total, c, g);
@@ -323,188 +385,192 @@ __global__ void __launch_bounds__(kThreads, 1)
             busy ? __ldcg(ws.begin + blockIdx.x) : 0};
   Piece g;
 
-  if (warp == kTmaWarp) {
-    // ---------------------------------------------------------------- producer
-    const int ps = 1 << p.page_shift;
-    const int ppb = ps < kBlk ? kBlk / ps : 1;
-    const int box_rows = min(ps, kBlk);
-    const int per_batch = 32 / ppb;
-    uint32_t slot = 0, ph = 0, filled = 0, last_ph = 0, qph = 0;
-    bool ok = true, q_used = false;
-    while (ok && walk.next(g, p.hk)) {
-      const int* table = p.b.page_table + (long long)g.e.seq * p.b.table_stride;
-      const int bi = lane / ppb, pi = lane - bi * ppb;
-      const auto fetch = [&](int n0) {
-        const int nn = n0 + bi;
-        const int key = key_block(g.e, nn) * kBlk + pi * box_rows;
-        int id = 0;
-        if (nn < g.end && key < g.e.kv) {
-          id = __ldg(table + (key >> p.page_shift));
-          if (id < 0 || id >= p.num_pages) {
-            atomicOr(p.err, kErrRange);
-            id = (int)p.num_pages;  // outside the tensor: the box is filled with zeros
-          }
-        }
-        return id;
-      };
-      int ids = fetch(g.n0);
-      // Q: tile t's tokens by the group's heads
-      if (lane == 0) {
-        ok = bwait(&s.q_empty, qph ^ 1u, p.err);
-        if (ok) {
-          const int tiles = g.e.ntok > tpt ? 2 : 1;
-          mbar_arrive_expect_tx(&s.q_full, tiles * ND * tpt * p.group * 128);
-          for (int t = 0; t < tiles; ++t)
-#pragma unroll
-            for (int c = 0; c < ND; ++c)
-              tma_q(smem_u32(s.q[t]) + c * kChunk, &qmap, &s.q_full, c * 64, g.head * p.group,
-                    g.e.first + t * tpt);
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      q_used = true;
-      qph ^= 1u;
-      for (int n = g.n0; n < g.end && ok;) {
-        const int batch = min(per_batch, g.end - n);
-        const int next = n + batch < g.end ? fetch(n + batch) : 0;
-        for (int i = 0; i < batch && ok; ++i) {
-          const int kb = key_block(g.e, n + i) * kBlk;
-          const int boxes = min(ppb, max(0, g.e.kv - kb + box_rows - 1) / box_rows);
-          const int page = __shfl_sync(0xffffffffu, ids, i * ppb + min(lane, ppb - 1));
-          const int row = (kb + lane * box_rows) & (ps - 1);
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            if (lane == 0) {
-              ok = bwait(&s.kv_empty[slot], ph ^ 1u, p.err);
-              if (ok) mbar_arrive_expect_tx(&s.kv_full[slot], boxes * box_rows * 128 * ND);
-            }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-            if (lane < boxes) {
-              const uint32_t dst = smem_u32(s.kv[slot]) + lane * box_rows * 128;
-#pragma unroll
-              for (int c = 0; c < ND; ++c)
-                tma_page(dst + c * kChunk, kv ? &vmap : &kmap, &s.kv_full[slot], c * 64, row,
-                         g.head, page);
-            }
-            filled |= 1u << slot;
-            last_ph = (last_ph & ~(1u << slot)) | (ph << slot);
-            if (++slot == S::kSlots) {
-              slot = 0;
-              ph ^= 1u;
+  if (warp >= kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kTmaWarp) {
+      // ---------------------------------------------------------------- producer
+      const int ps = 1 << p.page_shift;
+      const int ppb = ps < kBlk ? kBlk / ps : 1;
+      const int box_rows = min(ps, kBlk);
+      const int per_batch = 32 / ppb;
+      uint32_t slot = 0, ph = 0, filled = 0, last_ph = 0, qph = 0;
+      bool ok = true, q_used = false;
+      while (ok && walk.next(g, p.hk)) {
+        const int* table = p.b.page_table + (long long)g.e.seq * p.b.table_stride;
+        const int bi = lane / ppb, pi = lane - bi * ppb;
+        const auto fetch = [&](int n0) {
+          const int nn = n0 + bi;
+          const int key = key_block(g.e, nn) * kBlk + pi * box_rows;
+          int id = 0;
+          if (nn < g.end && key < g.e.kv) {
+            id = __ldg(table + (key >> p.page_shift));
+            if (id < 0 || id >= p.num_pages) {
+              atomicOr(p.err, kErrRange);
+              id = (int)p.num_pages;  // outside the tensor: the box is filled with zeros
             }
           }
-        }
-        n += batch;
-        ids = next;
-      }
-    }
-    // wind down: no TMA copy may still be landing when the CTA exits
-    if (lane == 0) {
-      for (int i = 0; i < S::kSlots; ++i)
-        if (filled & (1u << i)) mbar_wait(&s.kv_full[i], (last_ph >> i) & 1u, p.err);
-      if (q_used) mbar_wait(&s.q_full, qph ^ 1u, p.err);
-    }
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- MMA issuer
-    const int ksteps = (p.head_dim + 15) / 16;
-    const int dn = (p.head_dim + 15) & ~15;
-    const uint32_t id_qk = idesc_of<T>(kBlk, false), id_pv = idesc_of<T>(dn, true);
-    uint32_t slot = 0, ph = 0, qph = 0;
-    uint32_t pph[2] = {0, 0}, oph[2] = {0, 0};
-    bool ok = true;
-    const auto issue_qk = [&](int t, uint32_t kslot) {
-      const uint32_t a = smem_u32(s.q[t]), b = smem_u32(s.kv[kslot]);
-      for (int k = 0; k < ksteps; ++k) {
-        const uint32_t o = (k >> 2) * kChunk + (k & 3) * 32;
-        mma_bf16(tmem + t * 128, smem_desc_sw128(a + o), smem_desc_sw128(b + o), id_qk, k != 0);
-      }
-      mma_commit(&s.s_full[t]);
-    };
-    const auto advance = [&]() {
-      if (++slot == S::kSlots) {
-        slot = 0;
-        ph ^= 1u;
-      }
-    };
-    while (ok && walk.next(g, p.hk)) {
-      const int blocks = g.end - g.n0;
-      int cnt[2];
-      cnt[0] = min(g.end, blocks_of_tile0(g.e, tpt)) - g.n0;
-      cnt[1] = g.e.ntok > tpt ? blocks : 0;
-      if (!warp_wait(&s.q_full, qph, p.err) || !warp_wait(&s.kv_full[slot], ph, p.err)) break;
-      qph ^= 1u;
-      if (lane == 0) {
-        tc_fence_after();
-        if (cnt[0] > 0) issue_qk(0, slot);
-        if (cnt[1] > 0) issue_qk(1, slot);
-        mma_commit(&s.kv_empty[slot]);
-        if (blocks == 1) mma_commit(&s.q_empty);
-      }
-      __syncwarp();
-      advance();
-      for (int j = 0; j < blocks; ++j) {
-        const uint32_t vslot = slot;
-        if (!(ok = warp_wait(&s.kv_full[vslot], ph, p.err))) break;
-        advance();
-        const int left = g.e.kv - key_block(g.e, g.n0 + j) * kBlk;
-        if (left < kBlk) {
-          // rows behind the last key may hold anything, and V takes part in the
-          // product with weight zero: clear them
-          const uint32_t v = smem_u32(s.kv[vslot]);
-          const int from = max(left, 0);
-          for (int i = lane; i < (kBlk - from) * ND * 8; i += 32) {
-            const int r = from + i / (ND * 8), c = i % (ND * 8);
-            sts128(v + (c >> 3) * kChunk + r * 128 + (c & 7) * 16, 0, 0, 0, 0);
-          }
-          fence_async_shared();
-          __syncwarp();
-        }
-        const bool more = j + 1 < blocks;
-        const uint32_t kslot = slot;
-        if (more) {
-          if (!(ok = warp_wait(&s.kv_full[kslot], ph, p.err))) break;
-          advance();
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (j >= cnt[t]) continue;
-          if (j == 0) {  // the previous piece's O has been read
-            if (!(ok = warp_wait(&s.o_empty[t], oph[t] ^ 1u, p.err))) break;
-            oph[t] ^= 1u;
-          }
-          if (!(ok = warp_wait(&s.p_full[t], pph[t], p.err))) break;
-          pph[t] ^= 1u;
-          if (lane == 0) {
-            tc_fence_after();
-            const uint32_t v = smem_u32(s.kv[vslot]);
-            const uint32_t o = tmem + 256 + t * ND * 64;
-#pragma unroll
-            for (int k = 0; k < kBlk / 16; ++k)
-              mma_ts(o, tmem + t * 128 + k * 8, smem_desc_mn(v + k * 2048), id_pv, (j | k) != 0);
-            if (j + 1 == cnt[t]) mma_commit(&s.o_full[t]);
-            if (j + 1 < cnt[t]) issue_qk(t, kslot);
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
+          return id;
+        };
+        int ids = fetch(g.n0);
+        // Q: tile t's tokens by the group's heads
         if (lane == 0) {
-          mma_commit(&s.kv_empty[vslot]);
-          if (more) mma_commit(&s.kv_empty[kslot]);
-          if (j + 2 == blocks) mma_commit(&s.q_empty);
+          ok = bwait(&s.q_empty, qph ^ 1u, p.err);
+          if (ok) {
+            const int tiles = g.e.ntok > tpt ? 2 : 1;
+            mbar_arrive_expect_tx(&s.q_full, tiles * ND * tpt * p.group * 128);
+            for (int t = 0; t < tiles; ++t)
+  #pragma unroll
+              for (int c = 0; c < ND; ++c)
+                tma_q(smem_u32(s.q[t]) + c * kChunk, &qmap, &s.q_full, c * 64, g.head * p.group,
+                      g.e.first + t * tpt);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        q_used = true;
+        qph ^= 1u;
+        for (int n = g.n0; n < g.end && ok;) {
+          const int batch = min(per_batch, g.end - n);
+          const int next = n + batch < g.end ? fetch(n + batch) : 0;
+          for (int i = 0; i < batch && ok; ++i) {
+            const int kb = key_block(g.e, n + i) * kBlk;
+            const int boxes = min(ppb, max(0, g.e.kv - kb + box_rows - 1) / box_rows);
+            const int page = __shfl_sync(0xffffffffu, ids, i * ppb + min(lane, ppb - 1));
+            const int row = (kb + lane * box_rows) & (ps - 1);
+  #pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              if (lane == 0) {
+                ok = bwait(&s.kv_empty[slot], ph ^ 1u, p.err);
+                if (ok) mbar_arrive_expect_tx(&s.kv_full[slot], boxes * box_rows * 128 * ND);
+              }
+              ok = __shfl_sync(0xffffffffu, ok, 0);
+              if (!ok) break;
+              if (lane < boxes) {
+                const uint32_t dst = smem_u32(s.kv[slot]) + lane * box_rows * 128;
+  #pragma unroll
+                for (int c = 0; c < ND; ++c)
+                  tma_page(dst + c * kChunk, kv ? &vmap : &kmap, &s.kv_full[slot], c * 64, row,
+                           g.head, page);
+              }
+              filled |= 1u << slot;
+              last_ph = (last_ph & ~(1u << slot)) | (ph << slot);
+              if (++slot == S::kSlots) {
+                slot = 0;
+                ph ^= 1u;
+              }
+            }
+          }
+          n += batch;
+          ids = next;
+        }
+      }
+      // wind down: no TMA copy may still be landing when the CTA exits
+      if (lane == 0) {
+        for (int i = 0; i < S::kSlots; ++i)
+          if (filled & (1u << i)) mbar_wait(&s.kv_full[i], (last_ph >> i) & 1u, p.err);
+        if (q_used) mbar_wait(&s.q_full, qph ^ 1u, p.err);
+      }
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------- MMA issuer
+      const int ksteps = (p.head_dim + 15) / 16;
+      const int dn = (p.head_dim + 15) & ~15;
+      const uint32_t id_qk = idesc_of<T>(kBlk, false), id_pv = idesc_of<T>(dn, true);
+      uint32_t slot = 0, ph = 0, qph = 0;
+      uint32_t pph[2] = {0, 0}, oph[2] = {0, 0};
+      bool ok = true;
+      const auto issue_qk = [&](int t, uint32_t kslot) {
+        const uint32_t a = smem_u32(s.q[t]), b = smem_u32(s.kv[kslot]);
+        for (int k = 0; k < ksteps; ++k) {
+          const uint32_t o = (k >> 2) * kChunk + (k & 3) * 32;
+          mma_bf16(tmem + t * 128, smem_desc_sw128(a + o), smem_desc_sw128(b + o), id_qk, k != 0);
+        }
+        mma_commit(&s.s_full[t]);
+      };
+      const auto advance = [&]() {
+        if (++slot == S::kSlots) {
+          slot = 0;
+          ph ^= 1u;
+        }
+      };
+      while (ok && walk.next(g, p.hk)) {
+        const int blocks = g.end - g.n0;
+        int cnt[2];
+        cnt[0] = min(g.end, blocks_of_tile0(g.e, tpt)) - g.n0;
+        cnt[1] = g.e.ntok > tpt ? blocks : 0;
+        if (!warp_wait(&s.q_full, qph, p.err) || !warp_wait(&s.kv_full[slot], ph, p.err)) break;
+        qph ^= 1u;
+        if (lane == 0) {
+          tc_fence_after();
+          if (cnt[0] > 0) issue_qk(0, slot);
+          if (cnt[1] > 0) issue_qk(1, slot);
+          mma_commit(&s.kv_empty[slot]);
+          if (blocks == 1) mma_commit(&s.q_empty);
         }
         __syncwarp();
+        advance();
+        for (int j = 0; j < blocks; ++j) {
+          const uint32_t vslot = slot;
+          if (!(ok = warp_wait(&s.kv_full[vslot], ph, p.err))) break;
+          advance();
+          const int left = g.e.kv - key_block(g.e, g.n0 + j) * kBlk;
+          if (left < kBlk) {
+            // rows behind the last key may hold anything, and V takes part in the
+            // product with weight zero: clear them
+            const uint32_t v = smem_u32(s.kv[vslot]);
+            const int from = max(left, 0);
+            for (int i = lane; i < (kBlk - from) * ND * 8; i += 32) {
+              const int r = from + i / (ND * 8), c = i % (ND * 8);
+              sts128(v + (c >> 3) * kChunk + r * 128 + (c & 7) * 16, 0, 0, 0, 0);
+            }
+            fence_async_shared();
+            __syncwarp();
+          }
+          const bool more = j + 1 < blocks;
+          const uint32_t kslot = slot;
+          if (more) {
+            if (!(ok = warp_wait(&s.kv_full[kslot], ph, p.err))) break;
+            advance();
+          }
+  #pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (j >= cnt[t]) continue;
+            if (j == 0) {  // the previous piece's O has been read
+              if (!(ok = warp_wait(&s.o_empty[t], oph[t] ^ 1u, p.err))) break;
+              oph[t] ^= 1u;
+            }
+            if (!(ok = warp_wait(&s.p_full[t], pph[t], p.err))) break;
+            pph[t] ^= 1u;
+            if (lane == 0) {
+              tc_fence_after();
+              const uint32_t v = smem_u32(s.kv[vslot]);
+              const uint32_t o = tmem + 256 + t * ND * 64;
+  #pragma unroll
+              for (int k = 0; k < kBlk / 16; ++k)
+                mma_ts(o, tmem + t * 128 + k * 8, smem_desc_mn(v + k * 2048), id_pv, (j | k) != 0);
+              if (j + 1 == cnt[t]) mma_commit(&s.o_full[t]);
+              if (j + 1 < cnt[t]) issue_qk(t, kslot);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            mma_commit(&s.kv_empty[vslot]);
+            if (more) mma_commit(&s.kv_empty[kslot]);
+            if (j + 2 == blocks) mma_commit(&s.q_empty);
+          }
+          __syncwarp();
+        }
       }
+      // wind down: every MMA issued here has completed before the exit
+      if (lane == 0) {
+        mma_commit(&s.drain);
+        mbar_wait(&s.drain, 0, p.err);
+      }
+      __syncwarp();
     }
-    // wind down: every MMA issued here has completed before the exit
-    if (lane == 0) {
-      mma_commit(&s.drain);
-      mbar_wait(&s.drain, 0, p.err);
-    }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int t = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -540,6 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i)
           tmem_ld32_nowait(s_tm + i * 32, reinterpret_cast<uint32_t*>(x) + i * 32);
         tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) loaded16(reinterpret_cast<uint32_t*>(x) + i * 16);
         if (GEN) {
 #pragma unroll
           for (int i = 0; i < kBlk; ++i) x[i] = score<true>(p.sc, x[i], slope, pos - kb - i);
@@ -553,42 +621,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kBlk; ++i)
             if (!((i <= a && (!window || i > b)) || i < pre)) x[i] = -INFINITY;
         }
-        float mx = x[0];
+        float mt[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int i = 1; i < kBlk; ++i) mx = fmaxf(mx, x[i]);
-        if (__any_sync(0xffffffffu, mx > m + raise)) {
-          const float m2 = fmaxf(m, mx);
-          const float a = ex2((m - (m2 == -INFINITY ? 0.0f : m2)) * c);
+        for (int i = 4; i < kBlk - 4; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mt[k] = max3(mt[k], x[i + 2 * k], x[i + 2 * k + 1]);
+        const float mx = fmaxf(max3(max3(mt[0], x[124], x[125]), mt[1], mt[2]),
+                               max3(mt[3], x[126], x[127]));
+        // each row by its own scores: what shares its warp does not change it
+        const bool up = mx > m + raise;
+        if (__any_sync(0xffffffffu, up)) {
+          const float a = up ? ex2((m - mx) * c) : 1.0f;
           l *= a;
-          m = m2;
+          m = up ? mx : m;
           if (j > 0) {
 #pragma unroll
-            for (int i = 0; i < ND * 2; ++i) {
-              uint32_t r[32];
-              tmem_ld32_nowait(o_tm + i * 32, r);
+            for (int i = 0; i < ND * 4; ++i) {
+              uint32_t r[16];
+              tmem_ld16_nowait(o_tm + i * 16, r);
               tmem_ld_wait();
+              loaded16(r);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * a);
-              tmem_st32(o_tm + i * 32, r);
+              for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * a);
+              tmem_st16(o_tm + i * 16, r);
             }
           }
         }
         const float base = m == -INFINITY ? 0.0f : m * c;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t c2 = pack2(c, c), base2 = pack2(-base, -base);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t r[32];
+        for (int part = 0; part < 4; ++part) {
+          uint32_t r[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float e0 = ex2(fmaf(x[half * 64 + 2 * i], c, -base));
-            const float e1 = ex2(fmaf(x[half * 64 + 2 * i + 1], c, -base));
-            sum[(2 * i) & 3] += e0;
-            sum[(2 * i + 1) & 3] += e1;
+          for (int i = 0; i < 16; ++i) {
+            float e0, e1;
+            unpack2(fma2(pack2(x[part * 32 + 2 * i], x[part * 32 + 2 * i + 1]), c2, base2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
             r[i] = T::pack(e0, e1);
           }
-          tmem_st32(s_tm + half * 32, r);
+          tmem_st16(s_tm + part * 16, r);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        {
+          float s0, s1;
+          unpack2(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -610,6 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t r[32];
           tmem_ld32_nowait(o_tm + i * 32, r);
           tmem_ld_wait();
+          loaded16(r);
+          loaded16(r + 16);
           if (mine) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -641,6 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t r[32];
             tmem_ld32_nowait(o_tm + i * 32, r);
             tmem_ld_wait();
+            loaded16(r);
+            loaded16(r + 16);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               dst[(i * 8 + k) * 128] =
@@ -649,8 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (begins && t == 0 && row == 0) {
-          const long long item0 = e.at + (long long)g.head * e.blocks;
-          const int c1 = share_of(total, item0 + e.blocks - 1, grid);
+          const long long item0 = e.at + (long long)g.head * units_of(e);
+          const int c1 = share_of(total, item0 + units_of(e) - 1, grid);
           Split sp;
           sp.entry = g.entry;
           sp.head = g.head;
@@ -744,6 +828,10 @@ template <typename F>
 cudaError_t setup_one(F f, int bytes, int* per_sm) {
   cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
+  cudaFuncAttributes attr;
+  if ((e = cudaFuncGetAttributes(&attr, f)) != cudaSuccess) return e;
+  // with fewer at launch the softmax warps would wait for registers for ever
+  if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
   int n = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, kThreads, bytes);
   if (n != 1) *per_sm = n;
