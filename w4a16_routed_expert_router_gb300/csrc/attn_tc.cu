@@ -171,6 +171,17 @@ __device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, uint
       : "memory");
 }
 
+// One thread of the converged warp, the same one every time. (Under elect.sync the
+// compiler knows that one thread issues the MMAs below; under `lane == 0` the
+// same 32 MMAs of a block took 3700 cycles to issue, more than they run.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void wait_prior_launch() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -479,10 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t pph[2] = {0, 0}, oph[2] = {0, 0};
       bool ok = true;
       const auto issue_qk = [&](int t, uint32_t kslot) {
-        const uint32_t a = smem_u32(s.q[t]), b = smem_u32(s.kv[kslot]);
-        for (int k = 0; k < ksteps; ++k) {
-          const uint32_t o = (k >> 2) * kChunk + (k & 3) * 32;
-          mma_bf16(tmem + t * 128, smem_desc_sw128(a + o), smem_desc_sw128(b + o), id_qk, k != 0);
+        const uint64_t a = smem_desc_sw128(smem_u32(s.q[t]));
+        const uint64_t b = smem_desc_sw128(smem_u32(s.kv[kslot]));
+#pragma unroll
+        for (int k = 0; k < ND * 4; ++k) {
+          const uint32_t o = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
+          if (k < ksteps) mma_bf16(tmem + t * 128, a + o, b + o, id_qk, k != 0);
         }
         mma_commit(&s.s_full[t]);
       };
@@ -499,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cnt[1] = g.e.ntok > tpt ? blocks : 0;
         if (!warp_wait(&s.q_full, qph, p.err) || !warp_wait(&s.kv_full[slot], ph, p.err)) break;
         qph ^= 1u;
-        if (lane == 0) {
+        if (elect_one()) {
           tc_fence_after();
           if (cnt[0] > 0) issue_qk(0, slot);
           if (cnt[1] > 0) issue_qk(1, slot);
@@ -540,20 +553,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!(ok = warp_wait(&s.p_full[t], pph[t], p.err))) break;
             pph[t] ^= 1u;
-            if (lane == 0) {
+            if (elect_one()) {
               tc_fence_after();
-              const uint32_t v = smem_u32(s.kv[vslot]);
+              const uint64_t v = smem_desc_mn(smem_u32(s.kv[vslot]));
               const uint32_t o = tmem + 256 + t * ND * 64;
-  #pragma unroll
+#pragma unroll
               for (int k = 0; k < kBlk / 16; ++k)
-                mma_ts(o, tmem + t * 128 + k * 8, smem_desc_mn(v + k * 2048), id_pv, (j | k) != 0);
+                mma_ts(o, tmem + t * 128 + k * 8, v + k * (2048 >> 4), id_pv, (j | k) != 0);
               if (j + 1 == cnt[t]) mma_commit(&s.o_full[t]);
               if (j + 1 < cnt[t]) issue_qk(t, kslot);
             }
             __syncwarp();
           }
           if (!ok) break;
-          if (lane == 0) {
+          if (elect_one()) {
             mma_commit(&s.kv_empty[vslot]);
             if (more) mma_commit(&s.kv_empty[kslot]);
             if (j + 2 == blocks) mma_commit(&s.q_empty);
@@ -562,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // wind down: every MMA issued here has completed before the exit
-      if (lane == 0) {
+      if (elect_one()) {
         mma_commit(&s.drain);
         mbar_wait(&s.drain, 0, p.err);
       }
