@@ -18,7 +18,10 @@
 //             stay below 2^8 and the result is exact either way.
 //   warp 8    TMA producer: Q, and K and V blocks into one ring of slots.
 //   warp 9    MMA issuer. While one tile's softmax runs, the tensor core works
-//             on the other: PV0(j) QK0(j+1) PV1(j) QK1(j+1) ...
+//             on the other: PV0(j) QK0(j+1) PV1(j) QK1(j+1) ... (A thread for
+//             each tile was slower, 836 to 804 us for 1000 tokens over 65536
+//             keys: the tiles' MMAs interleave and both results come late.)
+//   warp 10   clears V rows behind a sequence's last key.
 // Every wait is bounded; a timeout sets the error bit and the kernel winds
 // down.
 #include "attn_common.cuh"
@@ -31,7 +34,7 @@ using namespace tc;
 
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = (kSoftmaxWarps + 4) * 32;  // whole warpgroups: setmaxnreg
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kClearWarp = 10;
 // Registers a thread: the launch gives every thread kLaunchRegs; the producer
 // warpgroup hands most of its share to the two softmax warpgroups, whose rows
 // of 128 scores do not fit otherwise.
@@ -51,7 +54,7 @@ struct Smem {
   uint8_t q[2][ND * kChunk];
   uint64_t kv_full[kSlots], kv_empty[kSlots];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain;
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain, clear, cleared;
   uint32_t tmem_base;
 };
 
@@ -368,6 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&s.q_full, 1);
     mbar_init(&s.q_empty, 1);
+    mbar_init(&s.clear, 1);
+    mbar_init(&s.cleared, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s.s_full[t], 1);
       mbar_init(&s.p_full[t], 4);
@@ -483,103 +488,115 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- MMA issuer
+      // One thread; what it waits for is there already when the softmax keeps
+      // up, and a wait by a whole warp costs it about 150 cycles more.
       const int ksteps = (p.head_dim + 15) / 16;
       const int dn = (p.head_dim + 15) & ~15;
       const uint32_t id_qk = idesc_of<T>(kBlk, false), id_pv = idesc_of<T>(dn, true);
-      uint32_t slot = 0, ph = 0, qph = 0;
-      uint32_t pph[2] = {0, 0}, oph[2] = {0, 0};
-      bool ok = true;
-      const auto issue_qk = [&](int t, uint32_t kslot) {
-        const uint64_t a = smem_desc_sw128(smem_u32(s.q[t]));
-        const uint64_t b = smem_desc_sw128(smem_u32(s.kv[kslot]));
+      if (elect_one()) {
+        uint32_t slot = 0, ph = 0, qph = 0, cph = 0;
+        uint32_t pph[2] = {0, 0}, oph[2] = {0, 0};
+        bool ok = true;
+        const auto wait_slot = [&]() { return bwait(&s.kv_full[slot], ph, p.err); };
+        const auto advance = [&]() {
+          if (++slot == S::kSlots) {
+            slot = 0;
+            ph ^= 1u;
+          }
+        };
+        const auto issue_qk = [&](int t, uint32_t kslot) {
+          const uint64_t qd = smem_desc_sw128(smem_u32(s.q[t]));
+          const uint64_t kd = smem_desc_sw128(smem_u32(s.kv[kslot]));
 #pragma unroll
-        for (int k = 0; k < ND * 4; ++k) {
-          const uint32_t o = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
-          if (k < ksteps) mma_bf16(tmem + t * 128, a + o, b + o, id_qk, k != 0);
-        }
-        mma_commit(&s.s_full[t]);
-      };
-      const auto advance = [&]() {
-        if (++slot == S::kSlots) {
-          slot = 0;
-          ph ^= 1u;
-        }
-      };
-      while (ok && walk.next(g, p.hk)) {
-        const int blocks = g.end - g.n0;
-        int cnt[2];
-        cnt[0] = min(g.end, blocks_of_tile0(g.e, tpt)) - g.n0;
-        cnt[1] = g.e.ntok > tpt ? blocks : 0;
-        if (!warp_wait(&s.q_full, qph, p.err) || !warp_wait(&s.kv_full[slot], ph, p.err)) break;
-        qph ^= 1u;
-        if (elect_one()) {
+          for (int k = 0; k < ND * 4; ++k) {
+            const uint32_t o = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
+            if (k < ksteps) mma_bf16(tmem + t * 128, qd + o, kd + o, id_qk, k != 0);
+          }
+          mma_commit(&s.s_full[t]);
+        };
+        while (ok && walk.next(g, p.hk)) {
+          const int blocks = g.end - g.n0;
+          int cnt[2];
+          cnt[0] = min(g.end, blocks_of_tile0(g.e, tpt)) - g.n0;
+          cnt[1] = g.e.ntok > tpt ? blocks : 0;
+          if (!bwait(&s.q_full, qph, p.err) || !wait_slot()) break;
+          qph ^= 1u;
           tc_fence_after();
           if (cnt[0] > 0) issue_qk(0, slot);
           if (cnt[1] > 0) issue_qk(1, slot);
           mma_commit(&s.kv_empty[slot]);
           if (blocks == 1) mma_commit(&s.q_empty);
-        }
-        __syncwarp();
-        advance();
-        for (int j = 0; j < blocks; ++j) {
-          const uint32_t vslot = slot;
-          if (!(ok = warp_wait(&s.kv_full[vslot], ph, p.err))) break;
           advance();
-          const int left = g.e.kv - key_block(g.e, g.n0 + j) * kBlk;
-          if (left < kBlk) {
-            // rows behind the last key may hold anything, and V takes part in the
-            // product with weight zero: clear them
-            const uint32_t v = smem_u32(s.kv[vslot]);
-            const int from = max(left, 0);
-            for (int i = lane; i < (kBlk - from) * ND * 8; i += 32) {
-              const int r = from + i / (ND * 8), c = i % (ND * 8);
-              sts128(v + (c >> 3) * kChunk + r * 128 + (c & 7) * 16, 0, 0, 0, 0);
-            }
-            fence_async_shared();
-            __syncwarp();
-          }
-          const bool more = j + 1 < blocks;
-          const uint32_t kslot = slot;
-          if (more) {
-            if (!(ok = warp_wait(&s.kv_full[kslot], ph, p.err))) break;
+          for (int j = 0; j < blocks; ++j) {
+            const uint32_t vslot = slot;
+            if (!(ok = wait_slot())) break;
             advance();
-          }
-  #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (j >= cnt[t]) continue;
-            if (j == 0) {  // the previous piece's O has been read
-              if (!(ok = warp_wait(&s.o_empty[t], oph[t] ^ 1u, p.err))) break;
-              oph[t] ^= 1u;
+            if (g.e.kv - key_block(g.e, g.n0 + j) * kBlk < kBlk) {
+              mbar_arrive(&s.clear);
+              if (!(ok = bwait(&s.cleared, cph, p.err))) break;
+              cph ^= 1u;
             }
-            if (!(ok = warp_wait(&s.p_full[t], pph[t], p.err))) break;
-            pph[t] ^= 1u;
-            if (elect_one()) {
+            const bool more = j + 1 < blocks;
+            const uint32_t kslot = slot;
+            if (more) {
+              if (!(ok = wait_slot())) break;
+              advance();
+            }
+            const uint64_t vd = smem_desc_mn(smem_u32(s.kv[vslot]));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (j >= cnt[t]) continue;
+              if (j == 0) {  // the last piece's O has been read
+                if (!(ok = bwait(&s.o_empty[t], oph[t] ^ 1u, p.err))) break;
+                oph[t] ^= 1u;
+              }
+              if (!(ok = bwait(&s.p_full[t], pph[t], p.err))) break;
+              pph[t] ^= 1u;
               tc_fence_after();
-              const uint64_t v = smem_desc_mn(smem_u32(s.kv[vslot]));
-              const uint32_t o = tmem + 256 + t * ND * 64;
 #pragma unroll
               for (int k = 0; k < kBlk / 16; ++k)
-                mma_ts(o, tmem + t * 128 + k * 8, v + k * (2048 >> 4), id_pv, (j | k) != 0);
+                mma_ts(tmem + 256 + t * ND * 64, tmem + t * 128 + k * 8, vd + k * (2048 >> 4),
+                       id_pv, (j | k) != 0);
               if (j + 1 == cnt[t]) mma_commit(&s.o_full[t]);
               if (j + 1 < cnt[t]) issue_qk(t, kslot);
             }
-            __syncwarp();
-          }
-          if (!ok) break;
-          if (elect_one()) {
+            if (!ok) break;
             mma_commit(&s.kv_empty[vslot]);
             if (more) mma_commit(&s.kv_empty[kslot]);
             if (j + 2 == blocks) mma_commit(&s.q_empty);
           }
-          __syncwarp();
         }
-      }
-      // wind down: every MMA issued here has completed before the exit
-      if (elect_one()) {
+        // wind down: every MMA issued here has completed before the exit
         mma_commit(&s.drain);
         mbar_wait(&s.drain, 0, p.err);
       }
       __syncwarp();
+    } else if (warp == kClearWarp) {
+      // ---------------------------------------------------------------- cleared rows
+      // V rows behind the last key may hold anything, and take part in the
+      // product with weight zero: clear them in the block that has them, once
+      // the issuer has seen it arrive.
+      uint32_t slot = 0, cph = 0;
+      bool ok = true;
+      while (ok && walk.next(g, p.hk)) {
+        for (int n = g.n0; n < g.end; ++n) {
+          const uint32_t vslot = (slot + 1) % S::kSlots;
+          slot = (slot + 2) % S::kSlots;
+          const int left = g.e.kv - key_block(g.e, n) * kBlk;
+          if (left >= kBlk) continue;
+          if (!(ok = warp_wait(&s.clear, cph, p.err))) break;
+          cph ^= 1u;
+          const uint32_t v = smem_u32(s.kv[vslot]);
+          const int from = max(left, 0);
+          for (int i = lane; i < (kBlk - from) * ND * 8; i += 32) {
+            const int r = from + i / (ND * 8), c = i % (ND * 8);
+            sts128(v + (c >> 3) * kChunk + r * 128 + (c & 7) * 16, 0, 0, 0, 0);
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.cleared);
+        }
+      }
     }
   } else {
     // ---------------------------------------------------------------- softmax
