@@ -120,7 +120,8 @@ typedef struct moe_attn_batch {
   const int32_t* kv_len;     /* [num_seqs] keys of each sequence, new tokens included  */
   const int32_t* page_table; /* [num_seqs, columns], rows table_stride apart           */
   int64_t table_stride;      /* elements                                               */
-  int32_t columns;           /* pages listed per sequence: kv_len <= columns * page_size */
+  int32_t columns;           /* pages listed per sequence: kv_len <= columns * page_size,
+                                which is at most 2^29                                  */
   int32_t num_seqs;
   int32_t num_tokens;        /* rows of q                                              */
   int32_t max_q;             /* no sequence has more new tokens than this              */

@@ -386,8 +386,8 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
   }
   if (!b->cu_q || !b->kv_len || !b->page_table || b->columns < 1 || b->table_stride < b->columns)
     return MOE_ATTN_ERR_INVALID_ARG;
-  if ((long long)b->columns * c.page_size > 0x7fffffffLL - 1024)
-    return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;  // key indexes are int32
+  const long long max_kv = (long long)b->columns * c.page_size;
+  if (max_kv > (1LL << 29)) return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;  // int32 sums of positions
   int cur = -1;
   if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) cudaSetDevice(h->device);
   AttnParams p{};
@@ -402,7 +402,9 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
   p.head_stride = cache->head_stride;
   p.b = Batch{b->cu_q, b->kv_len, b->page_table, b->table_stride, b->columns, b->num_seqs,
               b->num_tokens, b->max_q};
-  p.sc = Scores{sc->scale, sc->softcap, sc->window, sc->slopes, sc->prefix};
+  // a window as long as the table hides nothing
+  p.sc = Scores{sc->scale, sc->softcap, sc->window >= max_kv ? 0 : sc->window, sc->slopes,
+                sc->prefix};
   p.hq = c.q_heads;
   p.hk = c.kv_heads;
   p.group = c.q_heads / c.kv_heads;

@@ -34,7 +34,8 @@ using namespace tc;
 
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = (kSoftmaxWarps + 4) * 32;  // whole warpgroups: setmaxnreg
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kClearWarp = 10;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kClearWarp = 10, kWalkWarp = 11;
+constexpr int kPieceReaders = kSoftmaxWarps + 3;
 // Registers a thread: the launch gives every thread kLaunchRegs; the producer
 // warpgroup hands most of its share to the two softmax warpgroups, whose rows
 // of 128 scores do not fit otherwise.
@@ -47,11 +48,15 @@ constexpr int kChunk = 128 * 128;   // 128 rows of 64 values
 constexpr int kItemUnits = 2;
 constexpr float kRaise = 8.0f;      // log2 units
 
+constexpr int kPieceBytes = 64, kPieces = 4;  // pieces handed out ahead
+
 template <int ND>
 struct Smem {
   static constexpr int kSlots = ND == 2 ? 5 : 8;
   uint8_t kv[kSlots][ND * kChunk];
   uint8_t q[2][ND * kChunk];
+  uint8_t piece[kPieces][kPieceBytes];
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t kv_full[kSlots], kv_empty[kSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain, clear, cleared;
@@ -140,6 +145,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// the n lowest bits, none below 0 and all from 32 on
+__device__ __forceinline__ uint32_t below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
 // two fp32 values in one 64-bit register
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t d;
@@ -207,36 +216,39 @@ __device__ __forceinline__ Entry load_entry(const Entry* e) {
 // results), then one for each of its blocks.
 __device__ __forceinline__ int units_of(const Entry& e) { return e.blocks + kItemUnits; }
 
-// One piece: blocks [n0, end) of an item.
-struct Piece {
-  Entry e;
-  int entry, head, n0, end;
+// One piece: blocks [n0, end) of an item, as one warp hands it to the others.
+struct alignas(16) Piece {
+  int first, ntok, p0, kv;          // see Entry
+  int near, skip, blocks, prefix;
+  int head, n0, end, seq;
+  int cnt[2];                       // blocks of the piece that tile 0 / 1 takes
+  int pad[2];
 };
-struct Walk {
-  const TcPlan& w;
-  long long at, hi;
-  int entry;
-  // the next piece with blocks
-  __device__ __forceinline__ bool next(Piece& g, int hk) {
-    while (at < hi) {
-      g.e = load_entry(w.entries + entry);
-      const int units = units_of(g.e);
-      const long long rel = at - g.e.at;
-      g.entry = entry;
-      g.head = (int)(rel / units);
-      const int u0 = (int)(rel - (long long)g.head * units);
-      const int u1 = (int)min((long long)units, u0 + (hi - at));
-      at += u1 - u0;
-      if (at == g.e.at + (long long)units * hk) ++entry;
-      g.n0 = max(0, u0 - kItemUnits);
-      g.end = max(0, u1 - kItemUnits);
-      if (g.end > g.n0) return true;
+static_assert(sizeof(Piece) == kPieceBytes, "shared memory of a piece");
+
+// One role's way through the pieces; `whole` warps or single threads.
+template <int ND, bool kWarp>
+struct Pieces {
+  Smem<ND>& s;
+  unsigned* err;
+  int i = 0;
+  uint32_t ph = 0;
+  // the next piece, or false at the end of the share or after a timeout
+  __device__ __forceinline__ bool next(Piece& g) {
+    if (!(kWarp ? warp_wait(&s.piece_full[i], ph, err) : bwait(&s.piece_full[i], ph, err)))
+      return false;
+    g = *reinterpret_cast<const Piece*>(s.piece[i]);
+    if (kWarp) __syncwarp();
+    if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&s.piece_empty[i]);
+    if (++i == kPieces) {
+      i = 0;
+      ph ^= 1u;
     }
-    return false;
+    return g.end > 0;
   }
 };
 
-__device__ __forceinline__ int key_block(const Entry& e, int n) {
+__device__ __forceinline__ int key_block(const Piece& e, int n) {
   return n < e.near ? n : n + e.skip;
 }
 
@@ -369,6 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.kv_full[i], 1);
       mbar_init(&s.kv_empty[i], 1);
     }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&s.piece_full[i], 1);
+      mbar_init(&s.piece_empty[i], kPieceReaders);
+    }
     mbar_init(&s.q_full, 1);
     mbar_init(&s.q_empty, 1);
     mbar_init(&s.clear, 1);
@@ -395,10 +411,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long total = __ldcg(ws.total);
   const int grid = (int)min((long long)gridDim.x, total);
   const int tpt = tile_tokens(p.group);
-  const bool busy = (int)blockIdx.x < grid;
-  Walk walk{ws, busy ? share_begin(total, blockIdx.x, grid) : 0,
-            busy ? share_begin(total, blockIdx.x + 1, grid) : 0,
-            busy ? __ldcg(ws.begin + blockIdx.x) : 0};
   Piece g;
 
   if (warp >= kSoftmaxWarps) {
@@ -411,14 +423,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int per_batch = 32 / ppb;
       uint32_t slot = 0, ph = 0, filled = 0, last_ph = 0, qph = 0;
       bool ok = true, q_used = false;
-      while (ok && walk.next(g, p.hk)) {
-        const int* table = p.b.page_table + (long long)g.e.seq * p.b.table_stride;
+      Pieces<ND, true> pieces{s, p.err};
+      while (ok && pieces.next(g)) {
+        const int* table = p.b.page_table + (long long)g.seq * p.b.table_stride;
         const int bi = lane / ppb, pi = lane - bi * ppb;
         const auto fetch = [&](int n0) {
           const int nn = n0 + bi;
-          const int key = key_block(g.e, nn) * kBlk + pi * box_rows;
+          const int key = key_block(g, nn) * kBlk + pi * box_rows;
           int id = 0;
-          if (nn < g.end && key < g.e.kv) {
+          if (nn < g.end && key < g.kv) {
             id = __ldg(table + (key >> p.page_shift));
             if (id < 0 || id >= p.num_pages) {
               atomicOr(p.err, kErrRange);
@@ -432,13 +445,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           ok = bwait(&s.q_empty, qph ^ 1u, p.err);
           if (ok) {
-            const int tiles = g.e.ntok > tpt ? 2 : 1;
+            const int tiles = g.ntok > tpt ? 2 : 1;
             mbar_arrive_expect_tx(&s.q_full, tiles * ND * tpt * p.group * 128);
             for (int t = 0; t < tiles; ++t)
   #pragma unroll
               for (int c = 0; c < ND; ++c)
                 tma_q(smem_u32(s.q[t]) + c * kChunk, &qmap, &s.q_full, c * 64, g.head * p.group,
-                      g.e.first + t * tpt);
+                      g.first + t * tpt);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -449,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int batch = min(per_batch, g.end - n);
           const int next = n + batch < g.end ? fetch(n + batch) : 0;
           for (int i = 0; i < batch && ok; ++i) {
-            const int kb = key_block(g.e, n + i) * kBlk;
-            const int boxes = min(ppb, max(0, g.e.kv - kb + box_rows - 1) / box_rows);
+            const int kb = key_block(g, n + i) * kBlk;
+            const int boxes = min(ppb, max(0, g.kv - kb + box_rows - 1) / box_rows);
             const int page = __shfl_sync(0xffffffffu, ids, i * ppb + min(lane, ppb - 1));
             const int row = (kb + lane * box_rows) & (ps - 1);
   #pragma unroll
@@ -497,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t slot = 0, ph = 0, qph = 0, cph = 0;
         uint32_t pph[2] = {0, 0}, oph[2] = {0, 0};
         bool ok = true;
+        Pieces<ND, false> pieces{s, p.err};
         const auto wait_slot = [&]() { return bwait(&s.kv_full[slot], ph, p.err); };
         const auto advance = [&]() {
           if (++slot == S::kSlots) {
@@ -514,11 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit(&s.s_full[t]);
         };
-        while (ok && walk.next(g, p.hk)) {
+        while (ok && pieces.next(g)) {
           const int blocks = g.end - g.n0;
-          int cnt[2];
-          cnt[0] = min(g.end, blocks_of_tile0(g.e, tpt)) - g.n0;
-          cnt[1] = g.e.ntok > tpt ? blocks : 0;
+          const int cnt[2] = {g.cnt[0], g.cnt[1]};
           if (!bwait(&s.q_full, qph, p.err) || !wait_slot()) break;
           qph ^= 1u;
           tc_fence_after();
@@ -531,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t vslot = slot;
             if (!(ok = wait_slot())) break;
             advance();
-            if (g.e.kv - key_block(g.e, g.n0 + j) * kBlk < kBlk) {
+            if (g.kv - key_block(g, g.n0 + j) * kBlk < kBlk) {
               mbar_arrive(&s.clear);
               if (!(ok = bwait(&s.cleared, cph, p.err))) break;
               cph ^= 1u;
@@ -578,11 +590,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the issuer has seen it arrive.
       uint32_t slot = 0, cph = 0;
       bool ok = true;
-      while (ok && walk.next(g, p.hk)) {
+      Pieces<ND, true> pieces{s, p.err};
+      while (ok && pieces.next(g)) {
         for (int n = g.n0; n < g.end; ++n) {
           const uint32_t vslot = (slot + 1) % S::kSlots;
           slot = (slot + 2) % S::kSlots;
-          const int left = g.e.kv - key_block(g.e, n) * kBlk;
+          const int left = g.kv - key_block(g, n) * kBlk;
           if (left >= kBlk) continue;
           if (!(ok = warp_wait(&s.clear, cph, p.err))) break;
           cph ^= 1u;
@@ -596,6 +609,64 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&s.cleared);
         }
+      }
+    } else if (lane == 0) {
+      // ---------------------------------------------------------------- the share, piece by piece
+      long long at = 0, hi = 0;
+      int entry = 0;
+      if ((int)blockIdx.x < grid) {
+        at = share_begin(total, blockIdx.x, grid);
+        hi = share_begin(total, blockIdx.x + 1, grid);
+        entry = __ldcg(ws.begin + blockIdx.x);
+      }
+      Entry e;
+      int head = -1, i = 0;   // head -1: the entry is to be read
+      uint32_t ph = 0;
+      bool ok = true;
+      while (ok) {
+        Piece o = {};
+        while (at < hi) {
+          if (head < 0) {
+            e = load_entry(ws.entries + entry);
+            head = (int)((at - e.at) / units_of(e));
+          }
+          const int units = units_of(e);
+          const long long item = e.at + (long long)head * units;
+          const int u0 = (int)(at - item), u1 = (int)min((long long)units, u0 + (hi - at));
+          at = item + u1;
+          o.head = head;
+          o.n0 = max(0, u0 - kItemUnits);
+          o.end = max(0, u1 - kItemUnits);
+          if (u1 == units && ++head == p.hk) {
+            head = -1;
+            ++entry;
+          }
+          if (o.end > o.n0) {
+            o.first = e.first, o.ntok = e.ntok, o.p0 = e.p0, o.kv = e.kv;
+            o.near = e.near, o.skip = e.skip, o.blocks = e.blocks, o.prefix = e.prefix;
+            o.seq = e.seq;
+            o.cnt[0] = min(o.end, blocks_of_tile0(e, tpt)) - o.n0;
+            o.cnt[1] = e.ntok > tpt ? o.end - o.n0 : 0;
+            if (o.n0 == 0 && o.end < e.blocks) {  // the first of several pieces
+              Split sp;
+              sp.entry = entry;
+              sp.head = o.head;
+              sp.pieces = share_of(total, item + units - 1, grid) - (int)blockIdx.x + 1;
+              sp.pad = 0;
+              ws.split[blockIdx.x] = sp;
+            }
+            break;
+          }
+        }
+        ok = bwait(&s.piece_empty[i], ph ^ 1u, p.err);
+        if (!ok) break;
+        *reinterpret_cast<Piece*>(s.piece[i]) = o;
+        mbar_arrive(&s.piece_full[i]);
+        if (++i == kPieces) {
+          i = 0;
+          ph ^= 1u;
+        }
+        if (o.end == 0) break;  // the end of the share, told to all
       }
     }
   } else {
@@ -611,26 +682,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = GEN ? 1.0f : p.sc.scale * kLog2e;
     const float raise = GEN ? kRaise : kRaise / c;
     uint32_t sph = 0, oph = 0;
-    while (walk.next(g, p.hk)) {
-      const Entry& e = g.e;
-      const int ntok = min(tpt, e.ntok - t * tpt);        // tokens of this tile
+    Pieces<ND, true> pieces{s, p.err};
+    while (pieces.next(g)) {
+      const int ntok = min(tpt, g.ntok - t * tpt);        // tokens of this tile
       if (ntok <= 0) continue;
-      const int last = t == 0 ? blocks_of_tile0(e, tpt) : e.blocks;
-      const int cnt = min(g.end, last) - g.n0;
-      const int p_first = e.p0 + t * tpt;
+      const int cnt = g.cnt[t];
+      const int p_first = g.p0 + t * tpt;
       const int pos = p_first + tok;
-      const int lo = p.sc.window ? pos - p.sc.window : 0;
       const int lo_last = p.sc.window ? p_first + ntok - 1 - p.sc.window : -1;
       const bool mine = tok < ntok;                       // this row exists
       const int h = g.head * p.group + hg;
-      const float slope = GEN && p.sc.slopes ? p.sc.slopes[min(h, p.hq - 1)] : 0.0f;
+      const float slope = GEN && p.sc.slopes ? p.sc.slopes[h] : 0.0f;
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
       for (int j = 0; j < cnt; ++j) {
         if (!(ok = warp_wait(&s.s_full[t], sph, p.err))) break;
         sph ^= 1u;
         tc_fence_after();
-        const int kb = key_block(e, g.n0 + j) * kBlk;
+        const int kb = key_block(g, g.n0 + j) * kBlk;
         float x[kBlk];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -643,13 +712,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kBlk; ++i) x[i] = score<true>(p.sc, x[i], slope, pos - kb - i);
         }
         // every row of the tile sees every key of the block, or not
-        const bool whole = (kb + kBlk - 1 <= p_first && kb > lo_last) || kb + kBlk <= e.prefix;
+        const bool whole = (kb + kBlk - 1 <= p_first && kb > lo_last) || kb + kBlk <= g.prefix;
         if (!whole) {
-          const int a = pos - kb, b = lo - kb, pre = e.prefix - kb;
-          const bool window = p.sc.window != 0;
+          // bit i of word w: this row sees key kb + 32 w + i
+          const int a = pos - kb + 1, b = p.sc.window ? pos - p.sc.window - kb + 1 : 0;
+          const int pre = g.prefix - kb;
 #pragma unroll
-          for (int i = 0; i < kBlk; ++i)
-            if (!((i <= a && (!window || i > b)) || i < pre)) x[i] = -INFINITY;
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t bits = (below(a - 32 * w) & ~below(b - 32 * w)) | below(pre - 32 * w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(bits & (1u << i))) x[32 * w + i] = -INFINITY;
+          }
         }
         float mt[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -705,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&s.p_full[t]);
       }
       if (!ok) break;
-      const bool split = g.end - g.n0 < e.blocks;
+      const bool split = g.end - g.n0 < g.blocks;
       if (cnt > 0) {
         if (!warp_wait(&s.o_full[t], oph, p.err)) break;
         oph ^= 1u;
@@ -713,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!split) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t* dst = p.out.p + (long long)(e.first + t * tpt + tok) * p.out.token +
+        uint16_t* dst = p.out.p + (long long)(g.first + t * tpt + tok) * p.out.token +
                         (long long)h * p.out.head;
 #pragma unroll
         for (int i = 0; i < ND * 2; ++i) {
@@ -739,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (mine && p.lse)
-          p.lse[(long long)(e.first + t * tpt + tok) * p.hq + h] =
+          p.lse[(long long)(g.first + t * tpt + tok) * p.hq + h] =
               l == 0.0f ? -INFINITY : (m * c + log2f(l)) * kLn2;
       } else {
         // a piece: slot 1 of the item's first CTA, slot 0 of the others
@@ -761,16 +835,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
                               __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
           }
-        }
-        if (begins && t == 0 && row == 0) {
-          const long long item0 = e.at + (long long)g.head * units_of(e);
-          const int c1 = share_of(total, item0 + units_of(e) - 1, grid);
-          Split sp;
-          sp.entry = g.entry;
-          sp.head = g.head;
-          sp.pieces = c1 - (int)blockIdx.x + 1;
-          sp.pad = 0;
-          ws.split[blockIdx.x] = sp;
         }
       }
       if (cnt > 0) {
