@@ -43,8 +43,9 @@ constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "setmaxnreg draws on the launch");
 constexpr int kBlk = kTcBlock;
 constexpr int kChunk = 128 * 128;   // 128 rows of 64 values
-// An item's fixed cost, in blocks (prefill of 8192 tokens: 0 -> 902 us, 1 -> 717,
-// 2 -> 624, 4 -> 635, 7 -> 654; 16 prompts of 1024: 387, 328, 299, 312, 325).
+// An item's fixed cost, in blocks (prefill of 8192 tokens: 2 -> 405 us, 4 -> 399,
+// 5 -> 402; 16 prompts of 1024: 196, 206, 203; without it 902 and 387 before the
+// cost itself was cut).
 constexpr int kItemUnits = 2;
 constexpr float kRaise = 8.0f;      // log2 units
 
@@ -787,30 +788,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!split) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t* dst = p.out.p + (long long)(g.first + t * tpt + tok) * p.out.token +
-                        (long long)h * p.out.head;
+        // A thread has a row; four neighbours exchange 16-byte units, so that
+        // they store 64 bytes of one row at a time (by rows alone, a warp's
+        // store touched 32 lines, 4500 cycles a tile).
+        long long own = -1, off[4];
+        if (mine)
+          own = (long long)(g.first + t * tpt + tok) * p.out.token + (long long)h * p.out.head;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) off[k] = __shfl_sync(0xffffffffu, own, (lane & ~3) + k);
+        const bool odd = lane & 1, upper = lane & 2;
 #pragma unroll
         for (int i = 0; i < ND * 2; ++i) {
-          uint32_t r[32];
+          uint32_t r[32], u[4][4];
           tmem_ld32_nowait(o_tm + i * 32, r);
           tmem_ld_wait();
           loaded16(r);
           loaded16(r + 16);
-          if (mine) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (i * 32 + k * 8 < p.head_dim) {
-                uint4 v;
-                v.x = T::pack(__uint_as_float(r[8 * k]) * inv, __uint_as_float(r[8 * k + 1]) * inv);
-                v.y = T::pack(__uint_as_float(r[8 * k + 2]) * inv,
-                              __uint_as_float(r[8 * k + 3]) * inv);
-                v.z = T::pack(__uint_as_float(r[8 * k + 4]) * inv,
-                              __uint_as_float(r[8 * k + 5]) * inv);
-                v.w = T::pack(__uint_as_float(r[8 * k + 6]) * inv,
-                              __uint_as_float(r[8 * k + 7]) * inv);
-                *reinterpret_cast<uint4*>(dst + i * 32 + k * 8) = v;
-              }
-          }
+          for (int k = 0; k < 16; ++k)
+            u[k >> 2][k & 3] = T::pack(__uint_as_float(r[2 * k]) * inv,
+                                       __uint_as_float(r[2 * k + 1]) * inv);
+#pragma unroll
+          for (int k = 0; k < 4; k += 2)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t v = __shfl_xor_sync(0xffffffffu, odd ? u[k][w] : u[k + 1][w], 1);
+              u[k][w] = odd ? v : u[k][w];
+              u[k + 1][w] = odd ? u[k + 1][w] : v;
+            }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t v = __shfl_xor_sync(0xffffffffu, upper ? u[k][w] : u[k + 2][w], 2);
+              u[k][w] = upper ? v : u[k][w];
+              u[k + 2][w] = upper ? u[k + 2][w] : v;
+            }
+          // u[k] is now this lane's unit of row k of the four
+          const int c0 = i * 32 + (lane & 3) * 8;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (off[k] >= 0 && c0 < p.head_dim)
+              *reinterpret_cast<uint4*>(p.out.p + off[k] + c0) =
+                  make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
         }
         if (mine && p.lse)
           p.lse[(long long)(g.first + t * tpt + tok) * p.hq + h] =
