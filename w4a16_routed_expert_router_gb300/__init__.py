@@ -316,5 +316,6 @@ _ATTENTION = ("PagedAttention", "PagedKvCache", "moe_attn_rope", "moe_attn_rope_
 def __getattr__(name):
     if name in _ATTENTION:
         from . import attention
-        return getattr(attention, name)
+        value = globals()[name] = getattr(attention, name)  # found directly from now on
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -113,8 +113,14 @@ def _check(status: int, what: str) -> None:
         raise MoeError(status, what)
 
 
+# the current stream's address without the Stream object around it (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(device.index)
         return torch.cuda.current_stream(device).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
@@ -159,11 +165,13 @@ def _empty(shape, dtype, device, stream):
 
 
 def _fill_rotation(s, freq, layout, magnitude, inverse, device):
-    if layout not in _LAYOUTS:
+    code = _LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
-    s.freq = _vector(freq, freq.shape[0] if freq.dim() else 0, torch.int64, device, "freq")
-    s.rot_dim = 2 * freq.shape[0]
-    s.layout = _LAYOUTS[layout]
+    n = freq.numel()
+    s.freq = _vector(freq, n, torch.int64, device, "freq")
+    s.rot_dim = 2 * n
+    s.layout = code
     s.magnitude = magnitude
     s.inverse = 1 if inverse else 0
 
@@ -202,10 +210,14 @@ def moe_attn_rope(x, positions, freq, out=None, layout="half", magnitude=1.0, in
         raise ValueError("x and out differ in tokens")
     _fill_rotation(rot, freq, layout, magnitude, inverse, device)
     pos = _vector(positions, tokens, torch.int32, device, "positions")
-    with torch.cuda.device(device):
-        st = _lib().moe_attn_rope(xs, os, pos, tokens, heads, dim, _DTYPES[dtype], rot,
-                                  _stream(stream, device))
-    _check(st, "moe_attn_rope")
+    args = (xs, os, pos, tokens, heads, dim, _DTYPES[dtype], rot, _stream(stream, device))
+    if torch.cuda.current_device() == device.index:
+        st = _lib().moe_attn_rope(*args)
+    else:
+        with torch.cuda.device(device):
+            st = _lib().moe_attn_rope(*args)
+    if st:
+        _check(st, "moe_attn_rope")
     return out
 
 

@@ -247,7 +247,7 @@ int moe_attn_rope(const moe_attn_rows* x, const moe_attn_rows* out, const int32_
   p.tokens = T;
   p.hq = heads;
   p.head_dim = head_dim;
-  return cuda_status(launch_rope(p, dtype, 0, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_rope(p, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_attn_workspace_bytes(const moe_attn_config* cfg, size_t* bytes) {
@@ -356,7 +356,7 @@ int moe_attn_append(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_r
   p.hk = p.hv = c.kv_heads;
   p.head_dim = c.head_dim;
   p.err = h->err;
-  return cuda_status(launch_rope(p, c.dtype, h->num_sms, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_rope(p, c.dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out,

@@ -63,7 +63,7 @@ struct RopeParams {
   int tokens, hq, hk, hv, head_dim;
   unsigned* err;
 };
-cudaError_t launch_rope(const RopeParams& p, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_rope(const RopeParams& p, int dtype, cudaStream_t s);
 
 struct Scores {
   float scale;
