@@ -260,6 +260,21 @@ def test_runs_are_identical_and_handles_are_reused():
         assert torch.equal(o2, out) and torch.equal(l2, lse)
 
 
+@pytest.mark.parametrize("d,page", [(128, 64), (64, 16)])
+def test_many_blocks_per_processor(d, page):
+    # some 60 blocks of keys for every SM: each ring of stages goes round many
+    # times, and a run repeats the one before bit by bit
+    shape = (8, 8, d, page, BF)
+    b = ac.Batch([(1, 18000), (1, 16384), (1, 17011), (1, 16001)], *shape)
+    layer = _layer(b, shape)
+    out, lse = b.run(layer)
+    b.check(out, lse)
+    for _ in range(20):
+        o2, l2 = b.run(layer)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+    assert layer.check_device_errors() == 0
+
+
 def test_graph_replays_with_new_lengths():
     shape = (8, 2, 128, 16, BF)
     lens = [[(1, 400), (120, 300), (1, 9)], [(1, 33), (120, 128), (1, 390)]]

@@ -14,6 +14,15 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Waits until the launch before this one is complete and its writes are visible.
+__device__ __forceinline__ void wait_prior_launch() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the next launch's CTAs start where there is room; they wait as above.
+__device__ __forceinline__ void let_next_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // one box of a page: rows from `row`, values from `c0`, of a kv head
 __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
                                          int c0, int row, int head, int page) {
@@ -36,6 +45,24 @@ __device__ __forceinline__ float score(const Scores& sc, float dot, float slope,
     x = sc.softcap * (1.0f - __fdividef(2.0f, 1.0f + e));
   }
   return (x - slope * (float)abs(away)) * kLog2e;
+}
+
+// A launch that may begin while the one before it ends: every kernel launched so
+// waits (wait_prior_launch) before it reads or writes memory.
+template <typename... A, typename... B>
+inline cudaError_t launch_after(void (*f)(A...), dim3 grid, dim3 block, int smem, cudaStream_t s,
+                         B... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, args...);
 }
 
 }  // namespace attn

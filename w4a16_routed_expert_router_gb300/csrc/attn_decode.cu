@@ -13,8 +13,7 @@
 // another inside an item. The 16 query rows are the M side of mma.sync
 // m16n8k16; rows of other tokens and heads of the group fill it. (mma.sync is
 // enough: 64 keys take about 500 of its cycles an SM, their bytes 1400 at the
-// HBM rate.) At an item's end the eight states are joined by a tree in shared
-// memory.
+// HBM rate.) At an item's end the eight states are joined in shared memory.
 #include "attn_common.cuh"
 
 namespace moe {
@@ -27,19 +26,24 @@ constexpr int kConsumers = 8;
 constexpr int kThreads = (1 + kConsumers) * 32;
 constexpr int kBlk = kDecodeBlock;
 constexpr int kRows = kDecodeRows;
+constexpr int kStateRows = 4 * kRows;
 
 template <int ND>  // 64-value chunks of a head
 struct Smem {
   static constexpr int kD = ND * 64;
   static constexpr int kTile = ND * kBlk * 128;     // K or V of a block
-  static constexpr int kStages = ND == 2 ? 5 : 10;  // 160 KB in flight
-  static constexpr int kPad = kD + 8;               // row stride of a joined state
+  static constexpr int kStages = ND == 2 ? 6 : 12;  // 192 KB in flight
+  // A group of warps takes every second block, so every second stage, always
+  // the same ones: a warp has to wait for every phase of a barrier it uses.
+  static_assert(kStages % 2 == 0, "stages belong to one consumer group each");
+  static constexpr int kPad = kD + 4;               // row stride of a state
   uint8_t ring[kStages][2 * kTile];
-  float o[kConsumers / 2][kRows][kPad];
-  float2 ml[kConsumers / 2][kRows];
+  // states to be joined: [state][row] with 8 states of 8 rows or 4 of 16
+  float o[kStateRows][kPad];
+  float2 ml[kStateRows];
   uint64_t full[kStages], empty[kStages];
   long long scan[kThreads / 32];
-  long long total, begin_at;
+  long long begin_at;
   int begin_seq, last;
 };
 
@@ -101,46 +105,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
-  // blocks of all sequences, and the sequence at which this CTA's share begins
-  const int per = (p.b.num_seqs + kThreads - 1) / kThreads;
-  const int s0 = min(p.b.num_seqs, (int)threadIdx.x * per);
-  const int s1 = min(p.b.num_seqs, s0 + per);
-  long long mine = 0;
-  for (int q = s0; q < s1; ++q) mine += (long long)item_of(p, q).blocks * p.hk;
-  long long incl = mine;
+  wait_prior_launch();
+  let_next_launch();
+  // blocks of all sequences, and the sequence at which this CTA's share begins:
+  // `at` is the first block of (seq, head 0), `w` walks the share [lo, hi)
+  long long total = 0, lo = 0, hi = 0, at = 0;
+  int grid = 0, seq = 0;
+  if (p.b.num_seqs <= 32) {  // each warp for itself
+    const long long mine = lane < p.b.num_seqs ? (long long)item_of(p, lane).blocks * p.hk : 0;
+    long long incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s.scan[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += s.scan[i];
-    total += s.scan[i];
-  }
-  const int grid = (int)min((long long)gridDim.x, total);
-  if ((int)blockIdx.x >= grid) return;
-  const long long lo = share_begin(total, blockIdx.x, grid);
-  const long long hi = share_begin(total, blockIdx.x + 1, grid);
-  if (lo >= before && lo < before + mine) {
-    long long at = before;
-    for (int q = s0; q < s1; ++q) {
-      const long long c = (long long)item_of(p, q).blocks * p.hk;
-      if (lo < at + c) {
-        s.begin_seq = q;
-        s.begin_at = at;
-        break;
-      }
-      at += c;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
     }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    grid = (int)min((long long)gridDim.x, total);
+    if ((int)blockIdx.x >= grid) return;
+    lo = share_begin(total, blockIdx.x, grid);
+    hi = share_begin(total, blockIdx.x + 1, grid);
+    seq = __ffs(__ballot_sync(0xffffffffu, lo < incl)) - 1;
+    at = __shfl_sync(0xffffffffu, incl - mine, seq);
+    __syncthreads();  // the barriers are set up
+  } else {
+    const int per = (p.b.num_seqs + kThreads - 1) / kThreads;
+    const int s0 = min(p.b.num_seqs, (int)threadIdx.x * per);
+    const int s1 = min(p.b.num_seqs, s0 + per);
+    long long mine = 0;
+    for (int q = s0; q < s1; ++q) mine += (long long)item_of(p, q).blocks * p.hk;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s.scan[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) before += s.scan[i];
+      total += s.scan[i];
+    }
+    grid = (int)min((long long)gridDim.x, total);
+    if ((int)blockIdx.x >= grid) return;
+    lo = share_begin(total, blockIdx.x, grid);
+    hi = share_begin(total, blockIdx.x + 1, grid);
+    if (lo >= before && lo < before + mine) {
+      long long first = before;
+      for (int q = s0; q < s1; ++q) {
+        const long long c = (long long)item_of(p, q).blocks * p.hk;
+        if (lo < first + c) {
+          s.begin_seq = q;
+          s.begin_at = first;
+          break;
+        }
+        first += c;
+      }
+    }
+    __syncthreads();
+    seq = s.begin_seq;
+    at = s.begin_at;
   }
-  __syncthreads();
-
-  // walk of the share: `at` is the first block of (seq, head 0)
-  int seq = s.begin_seq;
-  long long at = s.begin_at;
   long long w = lo;
   uint32_t stage = 0, ph = 0;
 
@@ -375,33 +400,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     }
-    // join the eight states: 4-7 into 0-3, 2-3 into 0-1, 1 into 0
-    for (int half = kConsumers / 2; half; half >>= 1) {
-      if (cw >= half && cw < 2 * half) {
+    // Join the warps' states: with more than 8 rows warps 4-7 first hand theirs
+    // to warps 0-3, then all states lie in shared memory and every thread adds up
+    // its values of them.
+    const auto put = [&](int state, int per_state) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (gid + 8 * r >= rows) continue;
-          if (tig == 0) s.ml[cw - half][gid + 8 * r] = make_float2(m[r], l[r]);
+      for (int r = 0; r < 2; ++r) {
+        const int row = gid + 8 * r;
+        if (row >= rows) continue;
+        const int at_row = state * per_state + row;
+        if (tig == 0) s.ml[at_row] = make_float2(m[r], l[r]);
 #pragma unroll
-          for (int i = 0; i < ND * 8; ++i)
-            *reinterpret_cast<float2*>(&s.o[cw - half][gid + 8 * r][i * 8 + 2 * tig]) =
-                make_float2(o[i][2 * r], o[i][2 * r + 1]);
-        }
+        for (int i = 0; i < ND * 8; ++i)
+          *reinterpret_cast<float2*>(&s.o[at_row][i * 8 + 2 * tig]) =
+              make_float2(o[i][2 * r], o[i][2 * r + 1]);
       }
+    };
+    const int states = rows > 8 ? 4 : 8, per_state = rows > 8 ? kRows : 8;
+    if (rows > 8) {
+      if (cw >= 4) put(cw - 4, kRows);
       consumers_sync();
-      if (cw < half) {
+      if (cw < 4) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          if (gid + 8 * r >= rows) continue;
-          const float2 x = s.ml[cw][gid + 8 * r];
+          const int row = gid + 8 * r;
+          if (row >= rows) continue;
+          const float2 x = s.ml[cw * kRows + row];
           const float mm = fmaxf(m[r], x.x), base = mm == -INFINITY ? 0.0f : mm;
           const float a = ex2(m[r] - base), b = ex2(x.x - base);
           m[r] = mm;
           l[r] = l[r] * a + x.y * b;
 #pragma unroll
           for (int i = 0; i < ND * 8; ++i) {
-            const float2 v = *reinterpret_cast<const float2*>(
-                &s.o[cw][gid + 8 * r][i * 8 + 2 * tig]);
+            const float2 v =
+                *reinterpret_cast<const float2*>(&s.o[cw * kRows + row][i * 8 + 2 * tig]);
             o[i][2 * r] = o[i][2 * r] * a + v.x * b;
             o[i][2 * r + 1] = o[i][2 * r + 1] * a + v.y * b;
           }
@@ -409,102 +441,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       consumers_sync();
     }
+    if (cw < states) put(cw, per_state);
+    consumers_sync();
+
     const long long item0 = at + (long long)head * it.blocks;
-    if (end - n0 == it.blocks) {
-      if (cw == 0) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = gid + 8 * r;
-          if (row >= rows) continue;
-          const int tok = row / p.group, h = head * p.group + (row - tok * p.group);
-          const float inv = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
-          uint16_t* dst = p.out.p + (long long)(it.first + tok) * p.out.token +
-                          (long long)h * p.out.head;
-#pragma unroll
-          for (int i = 0; i < ND * 8; ++i)
-            if (i * 8 < p.head_dim)
-              *reinterpret_cast<uint32_t*>(dst + i * 8 + 2 * tig) =
-                  T::pack(o[i][2 * r] * inv, o[i][2 * r + 1] * inv);
-          if (p.lse && tig == 0)
-            p.lse[(long long)(it.first + tok) * p.hq + h] =
-                l[r] == 0.0f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
-        }
+    const bool split = end - n0 < it.blocks;
+    const int c0 = split ? share_of(total, item0, grid) : 0;
+    const long long slot = 2LL * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0);
+    const int half_d = p.head_dim >> 1;
+    const auto write = [&](int row, int c, float x, float y, float mm, float sum) {
+      const int tok = row / p.group, h = head * p.group + (row - tok * p.group);
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      *reinterpret_cast<uint32_t*>(p.out.p + (long long)(it.first + tok) * p.out.token +
+                                   (long long)h * p.out.head + c) = T::pack(x * inv, y * inv);
+      if (p.lse && c == 0)
+        p.lse[(long long)(it.first + tok) * p.hq + h] =
+            sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
+    };
+    for (int e = threadIdx.x - 32; e < rows * half_d; e += kConsumers * 32) {
+      const int row = e / half_d, c = 2 * (e - row * half_d);
+      float mm = -INFINITY, sum = 0.0f, x = 0.0f, y = 0.0f;
+      for (int i = 0; i < states; ++i) mm = fmaxf(mm, s.ml[i * per_state + row].x);
+      const float base = mm == -INFINITY ? 0.0f : mm;
+      for (int i = 0; i < states; ++i) {
+        const float2 q = s.ml[i * per_state + row];
+        const float2 v = *reinterpret_cast<const float2*>(&s.o[i * per_state + row][c]);
+        const float f = ex2(q.x - base);
+        sum = fmaf(q.y, f, sum);
+        x = fmaf(v.x, f, x);
+        y = fmaf(v.y, f, y);
       }
-    } else {
-      // a piece: leave it in the workspace; the last CTA of the item joins them
-      const int c0 = share_of(total, item0, grid);
+      if (!split) {
+        write(row, c, x, y, mm, sum);
+      } else {
+        // a piece: left in the workspace
+        __stcg(reinterpret_cast<float2*>(ws.o + (slot * kRows + row) * S::kD + c),
+               make_float2(x, y));
+        if (c == 0) __stcg(ws.ml + slot * kRows + row, make_float2(mm, sum));
+      }
+    }
+    if (split) __threadfence();
+    consumers_sync();  // the states are read, and a piece is written
+    if (split) {
+      // the last CTA of the item joins the pieces, in their order
       const int c1 = share_of(total, item0 + it.blocks - 1, grid);
-      if (cw == 0) {
-        const long long slot = 2LL * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = gid + 8 * r;
-          if (row >= rows) continue;
-          if (tig == 0) __stcg(ws.ml + slot * kRows + row, make_float2(m[r], l[r]));
-          float* dst = ws.o + (slot * kRows + row) * S::kD;
-#pragma unroll
-          for (int i = 0; i < ND * 8; ++i)
-            __stcg(reinterpret_cast<float2*>(dst + i * 8 + 2 * tig),
-                   make_float2(o[i][2 * r], o[i][2 * r + 1]));
-        }
+      if (cw == 0 && lane == 0) {
+        const unsigned got = atomicAdd(ws.count + c0, 1u);
+        s.last = got == (unsigned)(c1 - c0);
+        if (s.last) ws.count[c0] = 0;
         __threadfence();
-        __syncwarp();
-        if (lane == 0) {
-          const unsigned got = atomicAdd(ws.count + c0, 1u);
-          s.last = got == (unsigned)(c1 - c0);
-          if (s.last) ws.count[c0] = 0;
-          __threadfence();
-        }
       }
       consumers_sync();
       if (s.last) {
         const int pieces = c1 - c0 + 1;
-        float* wgt = &s.o[0][0][0];  // [rows][pieces], <= 16 * 160 floats
-        float* sums = reinterpret_cast<float*>(&s.ml[0][0]);
-        const auto slot_of = [&](int i) { return 2LL * (c0 + i) + (i == 0 ? 1 : 0); };
-        for (int row = cw; row < rows; row += kConsumers) {
-          float mm = -INFINITY, sum = 0.0f;
-          for (int i = lane; i < pieces; i += 32)
-            mm = fmaxf(mm, __ldcg(ws.ml + slot_of(i) * kRows + row).x);
-#pragma unroll
-          for (int q = 16; q; q >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, q));
-          const float base = mm == -INFINITY ? 0.0f : mm;
-          for (int i = lane; i < pieces; i += 32) {
-            const float2 x = __ldcg(ws.ml + slot_of(i) * kRows + row);
-            const float e = ex2(x.x - base);
-            wgt[row * pieces + i] = e;
-            sum += x.y * e;
-          }
-#pragma unroll
-          for (int q = 16; q; q >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
-          if (lane == 0) {
-            sums[row] = sum == 0.0f ? 0.0f : 1.0f / sum;
-            const int tok = row / p.group, h = head * p.group + (row - tok * p.group);
-            if (p.lse)
-              p.lse[(long long)(it.first + tok) * p.hq + h] =
-                  sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
-          }
-        }
-        consumers_sync();
-        const int half_d = p.head_dim >> 1;
         for (int e = threadIdx.x - 32; e < rows * half_d; e += kConsumers * 32) {
           const int row = e / half_d, c = 2 * (e - row * half_d);
-          float x = 0.0f, y = 0.0f;
-#pragma unroll 4
-          for (int i = 0; i < pieces; ++i) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(
-                ws.o + (slot_of(i) * kRows + row) * S::kD + c));
-            const float f = wgt[row * pieces + i];
-            x = fmaf(v.x, f, x);
-            y = fmaf(v.y, f, y);
+          float mm = -INFINITY, sum = 0.0f, x = 0.0f, y = 0.0f;
+          for (int i0 = 0; i0 < pieces; i0 += 8) {  // eight pieces under way
+            float2 q[8], v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const long long at_row =
+                  (2LL * (c0 + i0 + i) + (i0 + i == 0 ? 1 : 0)) * kRows + row;
+              q[i] = make_float2(-INFINITY, 0.0f);
+              v[i] = make_float2(0.0f, 0.0f);
+              if (i0 + i < pieces) {
+                q[i] = __ldcg(ws.ml + at_row);
+                v[i] = __ldcg(reinterpret_cast<const float2*>(ws.o + at_row * S::kD + c));
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float m2 = fmaxf(mm, q[i].x), base = m2 == -INFINITY ? 0.0f : m2;
+              const float a = ex2(mm - base), b = ex2(q[i].x - base);
+              mm = m2;
+              sum = sum * a + q[i].y * b;
+              x = x * a + v[i].x * b;
+              y = y * a + v[i].y * b;
+            }
           }
-          const int tok = row / p.group, h = head * p.group + (row - tok * p.group);
-          *reinterpret_cast<uint32_t*>(p.out.p + (long long)(it.first + tok) * p.out.token +
-                                       (long long)h * p.out.head + c) =
-              T::pack(x * sums[row], y * sums[row]);
+          write(row, c, x, y, mm, sum);
         }
       }
-      consumers_sync();  // s.last and the join's buffers are free again
     }
     w = item0 + end;
     if (w == at + (long long)it.blocks * p.hk) {
@@ -518,6 +536,8 @@ template <int ND>
 constexpr int smem_bytes() {
   return (int)sizeof(Smem<ND>) + 1024;
 }
+static_assert(smem_bytes<1>() <= 227 * 1024 && smem_bytes<2>() <= 227 * 1024,
+              "shared memory of a CTA");
 
 template <typename T, int ND, bool GEN>
 cudaError_t setup_one() {
@@ -528,11 +548,9 @@ cudaError_t setup_one() {
 template <typename T, int ND>
 cudaError_t launch_one(const AttnParams& p, const Partials& w, const CUtensorMap& kmap,
                        const CUtensorMap& vmap, int grid, cudaStream_t s) {
-  if (p.sc.softcap > 0.0f || p.sc.slopes)
-    attn_decode_kernel<T, ND, true><<<grid, kThreads, smem_bytes<ND>(), s>>>(kmap, vmap, p, w);
-  else
-    attn_decode_kernel<T, ND, false><<<grid, kThreads, smem_bytes<ND>(), s>>>(kmap, vmap, p, w);
-  return cudaGetLastError();
+  const bool gen = p.sc.softcap > 0.0f || p.sc.slopes;
+  return launch_after(gen ? attn_decode_kernel<T, ND, true> : attn_decode_kernel<T, ND, false>,
+                      dim3(grid), dim3(kThreads), smem_bytes<ND>(), s, kmap, vmap, p, w);
 }
 
 }  // namespace

@@ -195,13 +195,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ void wait_prior_launch() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void let_next_launch() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __device__ __forceinline__ Entry load_entry(const Entry* e) {
   union {
     Entry v;
@@ -267,6 +260,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, con
   __shared__ long long part[32];
   __shared__ long long whole;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  wait_prior_launch();
   let_next_launch();
   const int span = 2 * tile_tokens(p.group);
   // exclusive scan of one value per thread; the sum is left in `whole`
@@ -958,32 +952,15 @@ cudaError_t setup_nd(int* per_sm) {
   return e != cudaSuccess ? e : setup_one(attn_tc_kernel<T, ND, true>, smem_bytes<ND>(), per_sm);
 }
 
-// a launch that may begin while the one before it ends (it waits for its data itself)
-template <typename... A, typename... B>
-cudaError_t launch_after(void (*f)(A...), dim3 grid, int threads, int smem, cudaStream_t s,
-                         B... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, f, args...);
-}
-
 template <typename T, int ND>
 cudaError_t launch_nd(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
                       const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
   // the plain form takes the maximum before it scales
   const bool gen = p.sc.softcap > 0.0f || p.sc.slopes || !(p.sc.scale > 0.0f);
   cudaError_t e = launch_after(gen ? attn_tc_kernel<T, ND, true> : attn_tc_kernel<T, ND, false>,
-                               dim3(grid), kThreads, smem_bytes<ND>(), s, qmap, kmap, vmap, p, w);
+                               dim3(grid), dim3(kThreads), smem_bytes<ND>(), s, qmap, kmap, vmap, p, w);
   if (e != cudaSuccess) return e;
-  return launch_after(attn_join_kernel<T, ND>, dim3(grid, 8), 128, 0, s, p, w);
+  return launch_after(attn_join_kernel<T, ND>, dim3(grid, 8), dim3(128), 0, s, p, w);
 }
 
 }  // namespace
@@ -1000,8 +977,7 @@ cudaError_t attn_tc_setup(int* ctas_per_sm) {
 cudaError_t launch_attn_tc(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
                            const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, int grid,
                            cudaStream_t s) {
-  attn_plan_kernel<<<1, 1024, 0, s>>>(p, w, grid);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_after(attn_plan_kernel, dim3(1), dim3(1024), 0, s, p, w, grid);
   if (e != cudaSuccess) return e;
   const bool wide = p.head_dim > 64;
   if (dtype == MOE_ATTN_BF16)

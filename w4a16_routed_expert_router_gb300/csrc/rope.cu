@@ -13,7 +13,7 @@
 // all heads. Bound by memory: q, k and v of 8192
 // tokens (32, 8 and 8 heads of 128) take 35.4 us, 5.7 TB/s, 0.84 of the measured
 // copy rate; by flat chunk numbers, divided out per chunk, they took 60 us.
-#include "attn.h"
+#include "attn_common.cuh"
 
 namespace moe {
 namespace attn {
@@ -80,6 +80,8 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
   const int nt = min(tokens_per_thread, cta_tokens - first);
   float* sines = cosines + tokens_per_cta * pairs;
 
+  wait_prior_launch();
+  let_next_launch();
   const int u = threadIdx.x, hd = blockIdx.y * blockDim.y + threadIdx.y;
   const bool active = hd < p.hq + p.hk + p.hv;
   const bool key = hd >= p.hq && hd < p.hq + p.hk, value = hd >= p.hq + p.hk;
@@ -183,9 +185,8 @@ cudaError_t launch_il(const RopeParams& p, cudaStream_t s) {
          2 * tokens * block.z * p.r.rot <= 4096)
     tokens *= 2;
   const int cta = tokens * block.z;
-  rope_kernel<T, V, IL><<<dim3((p.tokens + cta - 1) / cta, groups), block,
-                          cta * p.r.rot * sizeof(float), s>>>(p, tokens, units, turn_units);
-  return cudaGetLastError();
+  return launch_after(rope_kernel<T, V, IL>, dim3((p.tokens + cta - 1) / cta, groups), block,
+                      cta * p.r.rot * (int)sizeof(float), s, p, tokens, units, turn_units);
 }
 
 template <typename T, int V>
