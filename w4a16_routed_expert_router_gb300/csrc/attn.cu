@@ -153,7 +153,7 @@ int encode(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims,
            const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return MOE_ATTN_ERR_CUDA;
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -182,6 +182,22 @@ int encode_cache(CUtensorMap* m, const moe_attn_config& c, const moe_attn_cache*
                                  bytes_of(k->page_stride, k->num_pages, c.head_dim)};
   const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
   return encode(m, 4, base, dims, strides, box);
+}
+
+// The same with the chunks of 64 values as a dimension behind the rows: where
+// head_dim is 128, one box brings both, [chunk][row][64 values]. Otherwise that
+// dimension has one element and a box one chunk, as above.
+int encode_cache_chunks(CUtensorMap* m, const moe_attn_config& c, const moe_attn_cache* k,
+                        const void* base, int rows) {
+  const bool both = c.head_dim == 128;
+  const cuuint64_t dims[5] = {(cuuint64_t)(both ? 64 : c.head_dim), (cuuint64_t)c.page_size,
+                              (cuuint64_t)(both ? 2 : 1), (cuuint64_t)c.kv_heads,
+                              (cuuint64_t)k->num_pages};
+  const cuuint64_t strides[4] = {bytes_of(k->token_stride, c.page_size, c.head_dim), 128,
+                                 bytes_of(k->head_stride, c.kv_heads, c.head_dim),
+                                 bytes_of(k->page_stride, k->num_pages, c.head_dim)};
+  const cuuint32_t box[5] = {64, (cuuint32_t)rows, (cuuint32_t)(both ? 2 : 1), 1, 1};
+  return encode(m, 5, base, dims, strides, box);
 }
 
 // 3-D view {head_dim, q_heads, tokens} of q, boxes of one tile: its tokens by
@@ -421,9 +437,10 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
   p.few_rows = few ? kDecodeRows : 0;
   CUtensorMap qmap, kmap, vmap;
   if (few) {
-    const int box = c.page_size < kDecodeBlock ? c.page_size : kDecodeBlock;
-    if ((st = encode_cache(&kmap, c, cache, cache->k, box)) != MOE_ATTN_OK ||
-        (st = encode_cache(&vmap, c, cache, cache->v, box)) != MOE_ATTN_OK ||
+    const int block = decode_block(c.head_dim > 64 ? 2 : 1);
+    const int box = c.page_size < block ? c.page_size : block;
+    if ((st = encode_cache_chunks(&kmap, c, cache, cache->k, box)) != MOE_ATTN_OK ||
+        (st = encode_cache_chunks(&vmap, c, cache, cache->v, box)) != MOE_ATTN_OK ||
         (st = cuda_status(launch_attn_decode(p, h->decode, kmap, vmap, c.dtype, h->grid, s))) !=
             MOE_ATTN_OK)
       return st;

@@ -100,7 +100,8 @@ struct AttnParams {
 // by the last of them to finish, in the order of their pieces.
 constexpr int kMaxGrid = 160;         // CTAs of a split launch (152 SMs on GB300)
 constexpr int kDecodeRows = 16;       // query rows per kv head of the few-token kernel
-constexpr int kDecodeBlock = 64;      // keys per block of that kernel
+// keys per block of that kernel, by 64-value chunks of a head: 32 KB of K and V
+__host__ __device__ constexpr int decode_block(int chunks) { return 128 / chunks; }
 
 struct Partials {
   float* o;           // [kMaxGrid][2][rows][head_dim rounded to 64] weighted sums, not normalised

@@ -6,10 +6,10 @@
 // long sequence and many short ones all keep every SM loading; an item that
 // several CTAs hold is joined by the last of them.
 //
-// Per CTA: warp 0 brings blocks of 64 keys (K and V, 128-byte-swizzled boxes
-// of a page) by TMA into a ring of stages. Warps 1-8 consume: two groups of
-// four take alternate blocks, and each warp 16 keys of its block, with a
-// running maximum, sum and weighted value sum of its own, so no warp waits for
+// Per CTA: warp 0 brings blocks of 64 keys (128 at head sizes up to 64; K and V,
+// 128-byte-swizzled boxes of a page) by TMA into a ring of stages. Warps 1-8
+// consume: two groups of four take alternate blocks, and each warp a quarter of
+// its block's keys, with a running maximum, sum and weighted value sum of its own, so no warp waits for
 // another inside an item. The 16 query rows are the M side of mma.sync
 // m16n8k16; rows of other tokens and heads of the group fill it. (mma.sync is
 // enough: 64 keys take about 500 of its cycles an SM, their bytes 1400 at the
@@ -24,15 +24,15 @@ using namespace tc;
 
 constexpr int kConsumers = 8;
 constexpr int kThreads = (1 + kConsumers) * 32;
-constexpr int kBlk = kDecodeBlock;
 constexpr int kRows = kDecodeRows;
 constexpr int kStateRows = 4 * kRows;
 
 template <int ND>  // 64-value chunks of a head
 struct Smem {
   static constexpr int kD = ND * 64;
-  static constexpr int kTile = ND * kBlk * 128;     // K or V of a block
-  static constexpr int kStages = ND == 2 ? 6 : 12;  // 192 KB in flight
+  static constexpr int kSub = decode_block(ND) / 64;  // 16-key tiles of a warp in a block
+  static constexpr int kTile = 16 * 1024;             // K or V of a block
+  static constexpr int kStages = 6;                   // 192 KB in flight
   // A group of warps takes every second block, so every second stage, always
   // the same ones: a warp has to wait for every phase of a barrier it uses.
   static_assert(kStages % 2 == 0, "stages belong to one consumer group each");
@@ -80,12 +80,26 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
 
+template <int ND>
 __device__ __forceinline__ Span item_of(const AttnParams& p, int s) {
   Span r = read_sequence(p.b, p.page_shift, s, p.err);
   r.blocks = 0;
   if (r.n > 0 && r.n * p.group <= kRows)
-    span_blocks(r, r.kv - r.n, r.kv - 1, p.sc.window, prefix_of(p.sc, s, r.kv), kBlk);
+    span_blocks(r, r.kv - r.n, r.kv - 1, p.sc.window, prefix_of(p.sc, s, r.kv), decode_block(ND));
   return r;
+}
+
+// The boxes of a page: 64 values of both chunks of a head at once where the
+// head has 128 (half as many copies: 16-token pages went from 5.7 to MEAS TB/s),
+// one chunk otherwise.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                        int c0, int row, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(row), "r"(0),
+      "r"(head), "r"(page)
+      : "memory");
 }
 
 template <typename T, int ND, bool GEN>
@@ -94,6 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap vmap, const AttnParams p,
                        const Partials ws) {
   typedef Smem<ND> S;
+  constexpr int kBlk = decode_block(ND), kSub = S::kSub;
   extern __shared__ uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -112,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long total = 0, lo = 0, hi = 0, at = 0;
   int grid = 0, seq = 0;
   if (p.b.num_seqs <= 32) {  // each warp for itself
-    const long long mine = lane < p.b.num_seqs ? (long long)item_of(p, lane).blocks * p.hk : 0;
+    const long long mine = lane < p.b.num_seqs ? (long long)item_of<ND>(p, lane).blocks * p.hk : 0;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -132,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s0 = min(p.b.num_seqs, (int)threadIdx.x * per);
     const int s1 = min(p.b.num_seqs, s0 + per);
     long long mine = 0;
-    for (int q = s0; q < s1; ++q) mine += (long long)item_of(p, q).blocks * p.hk;
+    for (int q = s0; q < s1; ++q) mine += (long long)item_of<ND>(p, q).blocks * p.hk;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -153,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lo >= before && lo < before + mine) {
       long long first = before;
       for (int q = s0; q < s1; ++q) {
-        const long long c = (long long)item_of(p, q).blocks * p.hk;
+        const long long c = (long long)item_of<ND>(p, q).blocks * p.hk;
         if (lo < first + c) {
           s.begin_seq = q;
           s.begin_at = first;
@@ -168,6 +183,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   long long w = lo;
   uint32_t stage = 0, ph = 0;
+  // a stage holds its boxes one after the other, each [chunk][box_rows][64 values]
+  const int ps = 1 << p.page_shift;
+  const int box_rows = min(ps, kBlk);
+  const int box_bytes = ND * box_rows * 128;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
@@ -175,14 +194,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tmap(&kmap);
       prefetch_tmap(&vmap);
     }
-    const int ps = 1 << p.page_shift;
-    const int ppb = ps < kBlk ? kBlk / ps : 1;        // boxes of a block
-    const int box_rows = min(ps, kBlk);
+    const int ppb = kBlk / box_rows;                  // boxes of a block
+    const bool both = p.head_dim == ND * 64;          // all chunks of a head in one box
     const int per_batch = 32 / ppb;
     uint32_t filled = 0, last_ph = 0;
     bool ok = true;
     while (w < hi && ok) {
-      const Span it = item_of(p, seq);
+      const Span it = item_of<ND>(p, seq);
       if (it.blocks == 0) {
         ++seq;
         continue;
@@ -219,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int go = 1;
           if (lane == 0) {
             go = bwait(&s.empty[stage], ph ^ 1u, p.err);
-            if (go) mbar_arrive_expect_tx(&s.full[stage], boxes * box_rows * 128 * ND * 2);
+            if (go) mbar_arrive_expect_tx(&s.full[stage], 2 * boxes * box_bytes);
           }
           go = __shfl_sync(0xffffffffu, go, 0);
           if (!go) {
@@ -228,12 +246,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane < boxes) {
             const int row = (kb + lane * box_rows) & (ps - 1);
-            const uint32_t dst = smem_u32(s.ring[stage]) + lane * box_rows * 128;
-#pragma unroll
-            for (int c = 0; c < ND; ++c) {
-              tma_page(dst + c * kBlk * 128, &kmap, &s.full[stage], c * 64, row, head, page);
-              tma_page(dst + S::kTile + c * kBlk * 128, &vmap, &s.full[stage], c * 64, row, head,
-                       page);
+            const uint32_t dst = smem_u32(s.ring[stage]) + lane * box_bytes;
+            for (int c = 0; c < (both ? 1 : ND); ++c) {
+              const uint32_t to = dst + c * box_rows * 128;
+              tma_box(to, &kmap, &s.full[stage], c * 64, row, head, page);
+              tma_box(to + S::kTile, &vmap, &s.full[stage], c * 64, row, head, page);
             }
           }
           filled |= 1u << stage;
@@ -262,14 +279,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ------------------------------------------------------------------ consumers
   const int cw = warp - 1, grp = cw >> 2;
   const int gid = lane >> 2, tig = lane & 3;
-  const int krow = (cw & 3) * 16;                       // this warp's keys in a block
-  // ldmatrix lane addresses: K rows by key, V rows by key (transposed on load)
-  const int lk_row = krow + (lane & 7) + ((lane >> 4) << 3), lk_c = (lane >> 3) & 1;
-  const int lv_row = krow + (lane & 7) + (((lane >> 3) & 1) << 3), lv_c = lane >> 4;
+  const int krow = (cw & 3) * 16 * kSub;                // this warp's keys in a block
+  // where its 16-key tiles lie in a stage, and the ldmatrix lane addresses in a
+  // tile: K rows by key, V rows by key (transposed on load)
+  uint32_t tile_at[kSub];
+#pragma unroll
+  for (int i = 0; i < kSub; ++i) {
+    const int r = krow + 16 * i;
+    tile_at[i] = (r / box_rows) * box_bytes + (r % box_rows) * 128;
+  }
+  const uint32_t chunk = box_rows * 128;
+  const int lk_row = (lane & 7) + ((lane >> 4) << 3), lk_c = (lane >> 3) & 1;
+  const int lv_row = (lane & 7) + (((lane >> 3) & 1) << 3), lv_c = lane >> 4;
   int parity = 0;                                       // blocks this CTA took so far, mod 2
   bool ok = true;
   while (w < hi) {
-    const Span it = item_of(p, seq);
+    const Span it = item_of<ND>(p, seq);
     if (it.blocks == 0) {
       ++seq;
       continue;
@@ -314,38 +339,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int k0 = (n < it.near ? n : n + it.skip) * kBlk + krow;
         if (ok && k0 < it.kv) {
           const uint32_t kt = smem_u32(s.ring[stage]), vt = kt + S::kTile;
-          if (k0 + 16 > it.kv) {
+          if (k0 + 16 * kSub > it.kv) {
             // rows behind the last key may hold anything: V takes part in the
             // product with weight zero, so it is cleared here
-            const int from = krow + it.kv - k0;
-            for (int i = lane; i < (krow + 16 - from) * ND * 8; i += 32) {
-              const int r = from + i / (ND * 8), c = i % (ND * 8);
-              sts128(vt + (c >> 3) * kBlk * 128 + r * 128 + (c & 7) * 16, 0, 0, 0, 0);
+            const int from = it.kv - k0;
+            for (int i = lane; i < (16 * kSub - from) * ND * 8; i += 32) {
+              const int r = krow + from + i / (ND * 8), c = i % (ND * 8);
+              sts128(vt + (r / box_rows) * box_bytes + (c >> 3) * chunk + (r % box_rows) * 128 +
+                         (c & 7) * 16,
+                     0, 0, 0, 0);
             }
             __syncwarp();
           }
-          float sacc[2][4] = {};
+          float sacc[2 * kSub][4] = {};
 #pragma unroll
           for (int k = 0; k < ND * 4; ++k) {
-            uint32_t b[4];
             const int c = (k & 3) * 2 + lk_c;
-            ldsm4(kt + (k >> 2) * kBlk * 128 + lk_row * 128 + ((c ^ (lk_row & 7)) << 4), b);
-            mma16<T>(sacc[0], qf[k], b[0], b[1]);
-            mma16<T>(sacc[1], qf[k], b[2], b[3]);
+#pragma unroll
+            for (int i = 0; i < kSub; ++i) {
+              uint32_t b[4];
+              ldsm4(kt + tile_at[i] + (k >> 2) * chunk + lk_row * 128 + ((c ^ (lk_row & 7)) << 4),
+                    b);
+              mma16<T>(sacc[2 * i], qf[k], b[0], b[1]);
+              mma16<T>(sacc[2 * i + 1], qf[k], b[2], b[3]);
+            }
+          }
+          if (GEN || !(k0 + 16 * kSub <= it.kv - it.n + 1 && p.sc.window == 0)) {
+#pragma unroll
+            for (int t = 0; t < 2 * kSub; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = k0 + t * 8 + 2 * tig + (i & 1), r = i >> 1;
+                const int away = pos[r] - key;
+                const bool seen =
+                    key < it.kv && (key < prefix || (away >= 0 && (p.sc.window == 0 ||
+                                                                  away < p.sc.window)));
+                sacc[t][i] = seen ? score<GEN>(p.sc, sacc[t][i], slope[r], away) : -INFINITY;
+              }
+          } else {  // every row sees every key
+#pragma unroll
+            for (int t = 0; t < 2 * kSub; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sacc[t][i] = score<false>(p.sc, sacc[t][i], 0.0f, 0);
           }
           float mx[2] = {m[0], m[1]};
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2 * kSub; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = k0 + t * 8 + 2 * tig + (i & 1), r = i >> 1;
-              const int away = pos[r] - key;
-              const bool seen = key < it.kv && (key < prefix || (away >= 0 && (p.sc.window == 0 ||
-                                                                            away < p.sc.window)));
-              sacc[t][i] =
-                  seen ? score<GEN>(p.sc, sacc[t][i], slope[r], away) : -INFINITY;
-              mx[r] = fmaxf(mx[r], sacc[t][i]);
-            }
+            for (int i = 0; i < 4; ++i) mx[i >> 1] = fmaxf(mx[i >> 1], sacc[t][i]);
           float base[2], scale[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
@@ -356,15 +397,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             m[r] = mx[r];
             l[r] *= scale[r];
           }
-          uint32_t pf[4];
+          uint32_t pf[kSub][4];
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2 * kSub; ++t)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const float e0 = ex2(sacc[t][2 * r] - base[r]);
               const float e1 = ex2(sacc[t][2 * r + 1] - base[r]);
               l[r] += e0 + e1;
-              pf[2 * t + r] = T::pack(e0, e1);
+              pf[t >> 1][2 * (t & 1) + r] = T::pack(e0, e1);
             }
           if (__any_sync(0xffffffffu, scale[0] != 1.0f || scale[1] != 1.0f)) {
 #pragma unroll
@@ -377,11 +418,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int d = 0; d < ND * 4; ++d) {
-            uint32_t b[4];
             const int c = (d & 3) * 2 + lv_c;
-            ldsm4t(vt + (d >> 2) * kBlk * 128 + lv_row * 128 + ((c ^ (lv_row & 7)) << 4), b);
-            mma16<T>(o[2 * d], pf, b[0], b[1]);
-            mma16<T>(o[2 * d + 1], pf, b[2], b[3]);
+#pragma unroll
+            for (int i = 0; i < kSub; ++i) {
+              uint32_t b[4];
+              ldsm4t(vt + tile_at[i] + (d >> 2) * chunk + lv_row * 128 + ((c ^ (lv_row & 7)) << 4),
+                     b);
+              mma16<T>(o[2 * d], pf[i], b[0], b[1]);
+              mma16<T>(o[2 * d + 1], pf[i], b[2], b[3]);
+            }
           }
         }
         // the generic reads (and the cleared rows) come before the next fill
