@@ -26,6 +26,7 @@ constexpr int kConsumers = 8;
 constexpr int kThreads = (1 + kConsumers) * 32;
 constexpr int kRows = kDecodeRows;
 constexpr int kStateRows = 4 * kRows;
+constexpr int kAhead = 12;  // pieces whose loads are under way together in a join
 
 template <int ND>  // 64-value chunks of a head
 struct Smem {
@@ -90,7 +91,7 @@ __device__ __forceinline__ Span item_of(const AttnParams& p, int s) {
 }
 
 // The boxes of a page: 64 values of both chunks of a head at once where the
-// head has 128 (half as many copies: 16-token pages went from 5.7 to MEAS TB/s),
+// head has 128 (half as many copies: 16-token pages went from 5.7 to 6.9 TB/s),
 // one chunk otherwise.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
                                         int c0, int row, int head, int page) {
@@ -124,8 +125,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   let_next_launch();
   // blocks of all sequences, and the sequence at which this CTA's share begins:
   // `at` is the first block of (seq, head 0), `w` walks the share [lo, hi)
-  long long total = 0, lo = 0, hi = 0, at = 0;
-  int grid = 0, seq = 0;
+  long long total = 0, lo = 0, at = 0;
+  int seq = 0;
   if (p.b.num_seqs <= 32) {  // each warp for itself
     const long long mine = lane < p.b.num_seqs ? (long long)item_of<ND>(p, lane).blocks * p.hk : 0;
     long long incl = mine;
@@ -135,10 +136,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane >= o) incl += v;
     }
     total = __shfl_sync(0xffffffffu, incl, 31);
-    grid = (int)min((long long)gridDim.x, total);
-    if ((int)blockIdx.x >= grid) return;
-    lo = share_begin(total, blockIdx.x, grid);
-    hi = share_begin(total, blockIdx.x + 1, grid);
+    const Shares sh(total, gridDim.x);
+    if ((int)blockIdx.x >= sh.grid) return;
+    lo = sh.begin(blockIdx.x);
     seq = __ffs(__ballot_sync(0xffffffffu, lo < incl)) - 1;
     at = __shfl_sync(0xffffffffu, incl - mine, seq);
     __syncthreads();  // the barriers are set up
@@ -161,10 +161,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i < warp) before += s.scan[i];
       total += s.scan[i];
     }
-    grid = (int)min((long long)gridDim.x, total);
-    if ((int)blockIdx.x >= grid) return;
-    lo = share_begin(total, blockIdx.x, grid);
-    hi = share_begin(total, blockIdx.x + 1, grid);
+    const Shares sh(total, gridDim.x);
+    if ((int)blockIdx.x >= sh.grid) return;
+    lo = sh.begin(blockIdx.x);
     if (lo >= before && lo < before + mine) {
       long long first = before;
       for (int q = s0; q < s1; ++q) {
@@ -181,7 +180,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     seq = s.begin_seq;
     at = s.begin_at;
   }
+  const Shares sh(total, gridDim.x);
+  const long long hi = sh.begin(blockIdx.x + 1);
   long long w = lo;
+  int head = -1;   // -1: to be worked out, in the first item
   uint32_t stage = 0, ph = 0;
   // a stage holds its boxes one after the other, each [chunk][box_rows][64 values]
   const int ps = 1 << p.page_shift;
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++seq;
         continue;
       }
-      const int head = (int)((w - at) / it.blocks);
+      if (head < 0) head = (int)quotient(w - at, it.blocks);
       int n = (int)((w - at) - (long long)head * it.blocks);
       const int end = (int)min((long long)it.blocks, n + (hi - w));
       const int* table = p.b.page_table + (long long)seq * p.b.table_stride;
@@ -264,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ids = next;
       }
       w = at + (long long)head * it.blocks + end;
-      if (w == at + (long long)it.blocks * p.hk) {
+      if (++head == p.hk) {  // (a share's last item may end early; nothing follows it)
+        head = 0;
         at = w;
         ++seq;
       }
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++seq;
       continue;
     }
-    const int head = (int)((w - at) / it.blocks);
+    if (head < 0) head = (int)quotient(w - at, it.blocks);
     const int n0 = (int)((w - at) - (long long)head * it.blocks);
     const int end = (int)min((long long)it.blocks, n0 + (hi - w));
     const int rows = it.n * p.group;
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const long long item0 = at + (long long)head * it.blocks;
     const bool split = end - n0 < it.blocks;
-    const int c0 = split ? share_of(total, item0, grid) : 0;
+    const int c0 = split ? sh.of(item0) : 0;
     const long long slot = 2LL * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0);
     const int half_d = p.head_dim >> 1;
     const auto write = [&](int row, int c, float x, float y, float mm, float sum) {
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     consumers_sync();  // the states are read, and a piece is written
     if (split) {
       // the last CTA of the item joins the pieces, in their order
-      const int c1 = share_of(total, item0 + it.blocks - 1, grid);
+      const int c1 = sh.of(item0 + it.blocks - 1);
       if (cw == 0 && lane == 0) {
         const unsigned got = atomicAdd(ws.count + c0, 1u);
         s.last = got == (unsigned)(c1 - c0);
@@ -542,10 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = threadIdx.x - 32; e < rows * half_d; e += kConsumers * 32) {
           const int row = e / half_d, c = 2 * (e - row * half_d);
           float mm = -INFINITY, sum = 0.0f, x = 0.0f, y = 0.0f;
-          for (int i0 = 0; i0 < pieces; i0 += 8) {  // eight pieces under way
-            float2 q[8], v[8];
+          for (int i0 = 0; i0 < pieces; i0 += kAhead) {
+            float2 q[kAhead], v[kAhead];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kAhead; ++i) {
               const long long at_row =
                   (2LL * (c0 + i0 + i) + (i0 + i == 0 ? 1 : 0)) * kRows + row;
               q[i] = make_float2(-INFINITY, 0.0f);
@@ -556,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kAhead; ++i) {
               const float m2 = fmaxf(mm, q[i].x), base = m2 == -INFINITY ? 0.0f : m2;
               const float a = ex2(mm - base), b = ex2(q[i].x - base);
               mm = m2;
@@ -570,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     w = item0 + end;
-    if (w == at + (long long)it.blocks * p.hk) {
+    if (++head == p.hk) {
+      head = 0;
       at = w;
       ++seq;
     }

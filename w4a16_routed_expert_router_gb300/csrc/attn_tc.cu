@@ -348,13 +348,13 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, con
   const long long total = whole;
   if (tid == 0) *w.total = total;
   if (total == 0) return;
-  const int g = (int)min((long long)grid, total);
+  const Shares sh(total, grid);
   for (int i = e0; i < e1; ++i) {
     const long long a = before + w.entries[i].at;
     const long long b = a + (long long)units_of(w.entries[i]) * p.hk;
     w.entries[i].at = a;
-    for (int c = share_of(total, a, g); c < g; ++c) {  // shares that begin in [a, b)
-      const long long lo = share_begin(total, c, g);
+    for (int c = sh.of(a); c < sh.grid; ++c) {  // shares that begin in [a, b)
+      const long long lo = sh.begin(c);
       if (lo >= b) break;
       if (lo >= a) w.begin[c] = i;
     }
@@ -403,8 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s.tmem_base;
   wait_prior_launch();
 
-  const long long total = __ldcg(ws.total);
-  const int grid = (int)min((long long)gridDim.x, total);
+  const Shares sh(__ldcg(ws.total), gridDim.x);
   const int tpt = tile_tokens(p.group);
   Piece g;
 
@@ -609,9 +608,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- the share, piece by piece
       long long at = 0, hi = 0;
       int entry = 0;
-      if ((int)blockIdx.x < grid) {
-        at = share_begin(total, blockIdx.x, grid);
-        hi = share_begin(total, blockIdx.x + 1, grid);
+      if ((int)blockIdx.x < sh.grid) {
+        at = sh.begin(blockIdx.x);
+        hi = sh.begin(blockIdx.x + 1);
         entry = __ldcg(ws.begin + blockIdx.x);
       }
       Entry e;
@@ -623,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (at < hi) {
           if (head < 0) {
             e = load_entry(ws.entries + entry);
-            head = (int)((at - e.at) / units_of(e));
+            head = (int)quotient(at - e.at, units_of(e));
           }
           const int units = units_of(e);
           const long long item = e.at + (long long)head * units;
@@ -646,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               Split sp;
               sp.entry = entry;
               sp.head = o.head;
-              sp.pieces = share_of(total, item + units - 1, grid) - (int)blockIdx.x + 1;
+              sp.pieces = sh.of(item + units - 1) - (int)blockIdx.x + 1;
               sp.pad = 0;
               ws.split[blockIdx.x] = sp;
             }
