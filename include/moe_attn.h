@@ -99,7 +99,7 @@ typedef struct moe_attn_config {
   int32_t head_dim;     /* multiple of 8, 8..128                                      */
   int32_t page_size;    /* 16, 32, 64, 128 or 256                                     */
   int32_t max_tokens;   /* new tokens of one call, 1..2^20                            */
-  int32_t max_seqs;     /* sequences of one call, 1..65536                            */
+  int32_t max_seqs;     /* sequences of one call, 1..16384                            */
   int32_t dtype;        /* moe_attn_dtype                                             */
   uint32_t flags;       /* must be 0                                                  */
 } moe_attn_config;

@@ -36,7 +36,7 @@ int validate_config(const moe_attn_config* c) {
   if (c->flags != 0) return MOE_ATTN_ERR_INVALID_ARG;
   if (c->dtype != MOE_ATTN_BF16 && c->dtype != MOE_ATTN_FP16) return MOE_ATTN_ERR_INVALID_ARG;
   if (c->max_tokens < 1 || c->max_tokens > (1 << 20)) return MOE_ATTN_ERR_INVALID_ARG;
-  if (c->max_seqs < 1 || c->max_seqs > 65536) return MOE_ATTN_ERR_INVALID_ARG;
+  if (c->max_seqs < 1 || c->max_seqs > kMaxSeqs) return MOE_ATTN_ERR_INVALID_ARG;
   if (c->kv_heads < 1 || c->kv_heads > 1024 || c->q_heads < c->kv_heads ||
       c->q_heads % c->kv_heads || c->q_heads / c->kv_heads > 64)
     return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
@@ -117,13 +117,9 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Workspace carve-up; the order is the order of the fields filled in create().
 struct Layout {
-  size_t off[11];
+  size_t off[7];
   size_t total;
 };
-int entries(const moe_attn_config& c) {
-  return c.max_tokens / (2 * tile_tokens(c.q_heads / c.kv_heads)) + c.max_seqs;
-}
-
 Layout plan(const moe_attn_config& c) {
   const size_t d = c.head_dim > 64 ? 128 : 64;
   const size_t sizes[] = {
@@ -131,13 +127,9 @@ Layout plan(const moe_attn_config& c) {
       kMaxGrid * 4,                             // 1 decode: pieces that arrived
       kMaxGrid * 2 * kDecodeRows * 8,           // 2 decode: maximum, sum
       kMaxGrid * 2 * kDecodeRows * d * 4,       // 3 decode: weighted sums
-      entries(c) * sizeof(Entry),               // 4 entries
-      (c.max_seqs + (size_t)1) * 4,             // 5 entries before each sequence
-      kMaxGrid * 4,                             // 6 first entry of each share
-      8,                                        // 7 blocks of all items
-      kMaxGrid * sizeof(Split),                 // 8 split items
-      kMaxGrid * 4 * 128 * 8,                   // 9 maximum, sum
-      kMaxGrid * 4 * 128 * d * 4,               // 10 weighted sums
+      kMaxGrid * sizeof(Split),                 // 4 split items
+      kMaxGrid * 4 * 128 * 8,                   // 5 maximum, sum
+      kMaxGrid * 4 * 128 * d * 4,               // 6 weighted sums
   };
   Layout L;
   size_t o = 0;
@@ -311,14 +303,9 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn_handle** ou
   h->decode.count = reinterpret_cast<unsigned*>(b + L.off[1]);
   h->decode.ml = reinterpret_cast<float2*>(b + L.off[2]);
   h->decode.o = reinterpret_cast<float*>(b + L.off[3]);
-  h->tc.entries = reinterpret_cast<Entry*>(b + L.off[4]);
-  h->tc.first_entry = reinterpret_cast<int*>(b + L.off[5]);
-  h->tc.begin = reinterpret_cast<int*>(b + L.off[6]);
-  h->tc.total = reinterpret_cast<long long*>(b + L.off[7]);
-  h->tc.split = reinterpret_cast<Split*>(b + L.off[8]);
-  h->tc.ml = reinterpret_cast<float2*>(b + L.off[9]);
-  h->tc.o = reinterpret_cast<float*>(b + L.off[10]);
-  h->tc.capacity = entries(*cfg);
+  h->tc.split = reinterpret_cast<Split*>(b + L.off[4]);
+  h->tc.ml = reinterpret_cast<float2*>(b + L.off[5]);
+  h->tc.o = reinterpret_cast<float*>(b + L.off[6]);
   *out = h;
   return MOE_ATTN_OK;
 }

@@ -98,6 +98,7 @@ struct AttnParams {
 // the order of the work items, so a CTA holds the end of one item, whole
 // items, and the beginning of another; items that several CTAs hold are joined
 // by the last of them to finish, in the order of their pieces.
+constexpr int kMaxSeqs = 16384;       // a number for each fits the ring of the tensor-core kernel
 constexpr int kMaxGrid = 160;         // CTAs of a split launch (152 SMs on GB300)
 constexpr int kDecodeRows = 16;       // query rows per kv head of the few-token kernel
 // keys per block of that kernel, by 64-value chunks of a head: 32 KB of K and V
@@ -195,31 +196,25 @@ struct Entry {
   int first, ntok;             // q row of the first token, tokens
   int p0, kv;                  // position of the first token, keys of the sequence
   int near, skip, blocks;      // see Span
-  int prefix;
-  long long at;                // units of all kv heads before this entry
-  int seq, pad;
+  int prefix, seq;
 };
-static_assert(sizeof(Entry) == 48, "read as three 16-byte words");
 
 // An item whose first piece ended before it did.
 struct Split {
-  int entry, head, pieces, pad;
+  int pieces;       // 0: there is none
+  int first, ntok;  // see Entry
+  int head;
 };
 
 struct TcPlan {
-  Entry* entries;     // [capacity]
-  int* first_entry;   // [max_seqs + 1] entries before each sequence
-  int* begin;         // [kMaxGrid] entry at which a CTA's share begins
-  long long* total;   // units of all items
-  Split* split;       // [kMaxGrid] by the CTA of the first piece; pieces 0: none
-  float* o;           // [kMaxGrid][2 pieces][2 tiles][dim / 4][128 rows][4]
-  float2* ml;         // [kMaxGrid][2][2][128] maximum (log2 units), sum
-  int capacity;
+  Split* split;     // [kMaxGrid] by the CTA of the first piece
+  float* o;         // [kMaxGrid][2 pieces][2 tiles][dim / 4][128 rows][4]
+  float2* ml;       // [kMaxGrid][2][2][128] maximum (log2 units), sum
 };
 
 __host__ __device__ inline int tile_tokens(int group) { return 128 / group; }
 
-// Three kernels: divide the work, attend, join the split items.
+// Two kernels: attend, and join the split items.
 cudaError_t attn_tc_setup(int* ctas_per_sm);
 cudaError_t launch_attn_tc(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
                            const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, int grid,

@@ -14,6 +14,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Waits until the launch before this one is complete and its writes are visible.
 __device__ __forceinline__ void wait_prior_launch() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

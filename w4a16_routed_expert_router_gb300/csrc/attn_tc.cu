@@ -1,12 +1,12 @@
 // Attention of many new tokens per sequence over the paged cache: prompts and
 // chunks of prompts, on the 5th-generation tensor core.
 //
-// Three launches. attn_plan (one CTA) lists the entries (two tiles of query
-// tokens of one sequence) with their key blocks; attn_tc runs one persistent
-// CTA per SM over an equal share of all key blocks of all (entry, kv head)
-// items; attn_join adds the pieces of items that more than one CTA holds, in
-// their order. Equal shares keep every SM busy to the end under a causal mask,
-// ragged lengths or a single chunk over a long cache.
+// Two launches. attn_tc runs one persistent CTA per SM over an equal share of
+// all key blocks of all items, an item being up to two tiles of query tokens of
+// one sequence (an entry) and a kv head; attn_join adds the pieces of items that
+// more than one CTA holds, in their order. Equal shares keep every SM busy to
+// the end under a causal mask, ragged lengths or a single chunk over a long
+// cache.
 //
 // attn_tc, one item: two tiles of 128 query rows (token, head of the group)
 // against blocks of 128 keys, S = Q K^T and O += P V with tcgen05.mma; S and O
@@ -22,6 +22,7 @@
 //             each tile was slower, 836 to 804 us for 1000 tokens over 65536
 //             keys: the tiles' MMAs interleave and both results come late.)
 //   warp 10   clears V rows behind a sequence's last key.
+//   warp 11   walks the share and hands its pieces to the others.
 // Every wait is bounded; a timeout sets the error bit and the kernel winds
 // down.
 #include "attn_common.cuh"
@@ -47,7 +48,30 @@ constexpr int kChunk = 128 * 128;   // 128 rows of 64 values
 // 5 -> 402; 16 prompts of 1024: 196, 206, 203; without it 902 and 387 before the
 // cost itself was cut).
 constexpr int kItemUnits = 2;
+// tanh(y) = y P(y^2) for |y| < 0.75: a least-maximum fit of tanh(y) / y in y^2,
+// below 2e-8 off, 1.1e-7 with fp32 arithmetic.
+constexpr float kTanhMax = 0.75f;
+__device__ constexpr float kTanh[6] = {0.9999999719f, -0.33332966662f, 0.13325515284f,
+                                      -0.05334982016f, 0.01959378583f, -0.00472395227f};
 constexpr float kRaise = 8.0f;      // log2 units
+
+// one value per warp of a scan over the CTA
+struct Scan {
+  long long part[kThreads / 32];
+};
+// What an entry needs of its sequence: n = 0 where its rows are few or its
+// lengths leave their ranges.
+struct alignas(16) Seq {
+  int first, n, kv, prefix;
+};
+
+// Where a CTA's share begins: entry `index` of sequence `seq`, whose first unit
+// is number `at` of all.
+struct Begin {
+  long long at;
+  Seq s;
+  int seq, index;
+};
 
 constexpr int kPieceBytes = 64, kPieces = 4;  // pieces handed out ahead
 
@@ -58,6 +82,8 @@ struct Smem {
   uint8_t q[2][ND * kChunk];
   uint8_t piece[kPieces][kPieceBytes];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
+  Scan scan;
+  Begin begin;
   uint64_t kv_full[kSlots], kv_empty[kSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain, clear, cleared;
@@ -195,16 +221,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ Entry load_entry(const Entry* e) {
-  union {
-    Entry v;
-    uint4 w[3];
-  } u;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) u.w[i] = __ldcg(reinterpret_cast<const uint4*>(e) + i);
-  return u.v;
-}
-
 // ------------------------------------------------------------------ the share of a CTA
 // Shares are counted in units: kItemUnits for an item's fixed cost (Q, the
 // results), then one for each of its blocks.
@@ -254,111 +270,122 @@ __device__ __forceinline__ int blocks_of_tile0(const Entry& e, int tpt) {
   return min(e.blocks, kb <= e.near ? kb : max(max(e.near, 1), kb - e.skip));
 }
 
-// ------------------------------------------------------------------ plan
-__global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, const TcPlan w,
-                                                         int grid) {
-  __shared__ long long part[32];
-  __shared__ long long whole;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  wait_prior_launch();
-  let_next_launch();
-  const int span = 2 * tile_tokens(p.group);
-  // exclusive scan of one value per thread; the sum is left in `whole`
-  const auto scan = [&](long long mine) {
-    long long v = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    __syncthreads();
-    if (lane == 31) part[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-      long long x = part[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += u;
-      }
-      part[lane] = x;
-      if (lane == 31) whole = x;
-    }
-    __syncthreads();
-    return v - mine + (warp ? part[warp - 1] : 0);
-  };
+// ------------------------------------------------------------------ dividing the work
+__device__ __forceinline__ Seq sequence_of(const AttnParams& p, int q) {
+  const Span r = read_sequence(p.b, p.page_shift, q, p.err);
+  return Seq{r.first, r.n * p.group > p.few_rows ? r.n : 0, r.kv, prefix_of(p.sc, q, r.kv)};
+}
+__device__ __forceinline__ int entries_of(const Seq& r, int tpt) {
+  return (int)((unsigned)(r.n + 2 * tpt - 1) / (unsigned)(2 * tpt));
+}
 
-  for (int c = tid; c < grid; c += blockDim.x) w.split[c].pieces = 0;
-  // entries of each sequence
-  const int per = (p.b.num_seqs + 1023) / 1024;
-  const int s0 = min(p.b.num_seqs, tid * per), s1 = min(p.b.num_seqs, s0 + per);
-  const auto count = [&](int s) {
-    const Span r = read_sequence(p.b, p.page_shift, s, p.err);
-    return r.n * p.group > p.few_rows ? (r.n + span - 1) / span : 0;
-  };
-  long long mine = 0;
-  for (int s = s0; s < s1; ++s) mine += count(s);
-  long long at = scan(mine);
-  const long long n_all = whole;
-  if (n_all > w.capacity) {  // only where cu_q lists rows twice
-    if (tid == 0) {
-      atomicOr(p.err, kErrRange);
-      *w.total = 0;
-    }
-    return;
+// entry i of a sequence
+__device__ __forceinline__ Entry entry_of(const AttnParams& p, const Seq& q, int seq, int i,
+                                          int tpt) {
+  const int t0 = i * 2 * tpt;
+  Entry e;
+  e.seq = seq;
+  e.first = q.first + t0;
+  e.ntok = min(2 * tpt, q.n - t0);
+  e.p0 = q.kv - q.n + t0;
+  e.kv = q.kv;
+  e.prefix = q.prefix;
+  Span r;
+  r.kv = q.kv;
+  span_blocks(r, e.p0, e.p0 + e.ntok - 1, p.sc.window, e.prefix, kBlk);
+  e.near = r.near;
+  e.skip = r.skip;
+  e.blocks = r.blocks;
+  return e;
+}
+
+// Exclusive scan of a value per thread over the CTA; the sum in `whole`.
+__device__ __forceinline__ long long cta_scan(Scan& sc, long long mine, long long& whole) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long v = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
   }
-  for (int s = s0; s < s1; ++s) {
-    w.first_entry[s] = (int)at;
-    at += count(s);
+  __syncthreads();
+  if (lane == 31) sc.part[warp] = v;
+  __syncthreads();
+  long long before = v - mine;
+  whole = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += sc.part[i];
+    whole += sc.part[i];
   }
-  __syncthreads();  // first_entry is read below by other threads of this CTA
-  // the entries, a run of them per thread
-  const int n = (int)n_all;
-  const int run = (n + 1023) / 1024;
-  const int e0 = min(n, tid * run), e1 = min(n, e0 + run);
-  long long blocks = 0;
-  for (int i = e0; i < e1; ++i) {
-    int lo = 0, hi = p.b.num_seqs - 1;  // last sequence with first_entry <= i
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (w.first_entry[mid] <= i)
-        lo = mid;
+  return before;
+}
+
+// Every CTA divides the work for itself (a launch that did it once took longer):
+// the entries of all sequences, a run of sequences a thread, then their units, a
+// run of entries a thread. `room` is shared memory for a number per sequence and
+// one more, and for the sequences themselves while they are few. Returns all
+// units.
+constexpr int kSeqsKept = 4096;
+__device__ __forceinline__ long long divide(const AttnParams& p, Scan& sc, uint8_t* room,
+                                            Begin& begin, int tpt) {
+  const int tid = threadIdx.x, seqs = p.b.num_seqs;
+  Seq* kept = reinterpret_cast<Seq*>(room);
+  int* first = reinterpret_cast<int*>(room + (seqs <= kSeqsKept ? seqs * sizeof(Seq) : 0));
+  const int per = (seqs + kThreads - 1) / kThreads;
+  const int s0 = min(seqs, tid * per), s1 = min(seqs, s0 + per);
+  const auto get = [&](int q) { return seqs <= kSeqsKept ? kept[q] : sequence_of(p, q); };
+  long long mine = 0, n = 0;
+  for (int q = s0; q < s1; ++q) {
+    const Seq r = sequence_of(p, q);
+    if (seqs <= kSeqsKept) kept[q] = r;
+    mine += entries_of(r, tpt);
+  }
+  long long at = cta_scan(sc, mine, n);
+  for (int q = s0; q < s1; ++q) {
+    first[q] = (int)at;
+    at += s1 - s0 == 1 ? mine : entries_of(get(q), tpt);
+  }
+  if (tid == 0) first[seqs] = (int)n;
+  __syncthreads();
+  const int run = ((int)n + kThreads - 1) / kThreads;
+  const int e0 = min((int)n, tid * run), e1 = min((int)n, e0 + run);
+  int seq = 0;
+  if (e0 < e1) {  // last sequence with first <= e0
+    int hi = seqs - 1;
+    while (seq < hi) {
+      const int mid = (seq + hi + 1) >> 1;
+      if (first[mid] <= e0)
+        seq = mid;
       else
         hi = mid - 1;
     }
-    Span r = read_sequence(p.b, p.page_shift, lo, p.err);
-    const int t0 = (i - w.first_entry[lo]) * span;
-    Entry e;
-    e.first = r.first + t0;
-    e.ntok = min(span, r.n - t0);
-    e.p0 = r.kv - r.n + t0;
-    e.kv = r.kv;
-    e.prefix = prefix_of(p.sc, lo, r.kv);
-    span_blocks(r, e.p0, e.p0 + e.ntok - 1, p.sc.window, e.prefix, kBlk);
-    e.near = r.near;
-    e.skip = r.skip;
-    e.blocks = r.blocks;
-    e.at = blocks;
-    e.seq = lo;
-    e.pad = 0;
-    w.entries[i] = e;
-    blocks += (long long)(r.blocks + kItemUnits) * p.hk;
   }
-  const long long before = scan(blocks);
-  const long long total = whole;
-  if (tid == 0) *w.total = total;
-  if (total == 0) return;
-  const Shares sh(total, grid);
-  for (int i = e0; i < e1; ++i) {
-    const long long a = before + w.entries[i].at;
-    const long long b = a + (long long)units_of(w.entries[i]) * p.hk;
-    w.entries[i].at = a;
-    for (int c = sh.of(a); c < sh.grid; ++c) {  // shares that begin in [a, b)
-      const long long lo = sh.begin(c);
-      if (lo >= b) break;
-      if (lo >= a) w.begin[c] = i;
+  const auto units = [&](int q, int e) {
+    return (long long)units_of(entry_of(p, get(q), q, e - first[q], tpt)) * p.hk;
+  };
+  long long sum = 0, total;
+  int q = seq;
+  for (int e = e0; e < e1; ++e) {
+    while (first[q + 1] <= e) ++q;
+    sum += units(q, e);
+  }
+  at = cta_scan(sc, sum, total);
+  const Shares sh(total, gridDim.x);
+  const long long lo = sh.begin(blockIdx.x);
+  if (lo >= at && lo < at + sum) {
+    q = seq;
+    for (int e = e0; e < e1; ++e) {
+      while (first[q + 1] <= e) ++q;
+      const long long u = e1 - e0 == 1 ? sum : units(q, e);
+      if (lo < at + u) {
+        begin = Begin{at, get(q), q, e - first[q]};
+        break;
+      }
+      at += u;
     }
   }
+  return total;
 }
 
 // ------------------------------------------------------------------ attention
@@ -403,9 +430,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s.tmem_base;
   wait_prior_launch();
 
-  const Shares sh(__ldcg(ws.total), gridDim.x);
   const int tpt = tile_tokens(p.group);
+  const Shares sh(divide(p, s.scan, &s.kv[0][0], s.begin, tpt), gridDim.x);
   Piece g;
+  fence_async_shared();  // the ring's first use was that one
+  __syncthreads();
 
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -606,26 +635,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (lane == 0) {
       // ---------------------------------------------------------------- the share, piece by piece
-      long long at = 0, hi = 0;
-      int entry = 0;
+      long long at = 0, hi = 0, entry_at = 0;
+      int seq = 0, index = 0;
       if ((int)blockIdx.x < sh.grid) {
         at = sh.begin(blockIdx.x);
         hi = sh.begin(blockIdx.x + 1);
-        entry = __ldcg(ws.begin + blockIdx.x);
+        entry_at = s.begin.at;
+        seq = s.begin.seq;
+        index = s.begin.index;
       }
+      Split split = {};
       Entry e;
-      int head = -1, i = 0;   // head -1: the entry is to be read
+      Seq r = s.begin.s;
+      int head = -1, i = 0;   // head -2: the sequence is to be read, -1: the entry made
       uint32_t ph = 0;
       bool ok = true;
       while (ok) {
         Piece o = {};
         while (at < hi) {
           if (head < 0) {
-            e = load_entry(ws.entries + entry);
-            head = (int)quotient(at - e.at, units_of(e));
+            if (head == -2) r = sequence_of(p, seq);
+            if (index == entries_of(r, tpt)) {
+              ++seq;
+              index = 0;
+              head = -2;
+              continue;
+            }
+            e = entry_of(p, r, seq, index, tpt);
+            head = (int)quotient(at - entry_at, units_of(e));
           }
           const int units = units_of(e);
-          const long long item = e.at + (long long)head * units;
+          const long long item = entry_at + (long long)head * units;
           const int u0 = (int)(at - item), u1 = (int)min((long long)units, u0 + (hi - at));
           at = item + u1;
           o.head = head;
@@ -633,7 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           o.end = max(0, u1 - kItemUnits);
           if (u1 == units && ++head == p.hk) {
             head = -1;
-            ++entry;
+            ++index;
+            entry_at = at;
           }
           if (o.end > o.n0) {
             o.first = e.first, o.ntok = e.ntok, o.p0 = e.p0, o.kv = e.kv;
@@ -641,14 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             o.seq = e.seq;
             o.cnt[0] = min(o.end, blocks_of_tile0(e, tpt)) - o.n0;
             o.cnt[1] = e.ntok > tpt ? o.end - o.n0 : 0;
-            if (o.n0 == 0 && o.end < e.blocks) {  // the first of several pieces
-              Split sp;
-              sp.entry = entry;
-              sp.head = o.head;
-              sp.pieces = sh.of(item + units - 1) - (int)blockIdx.x + 1;
-              sp.pad = 0;
-              ws.split[blockIdx.x] = sp;
-            }
+            if (o.n0 == 0 && o.end < e.blocks)  // the first of several pieces
+              split = Split{sh.of(item + units - 1) - (int)blockIdx.x + 1, e.first, e.ntok, o.head};
             break;
           }
         }
@@ -662,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (o.end == 0) break;  // the end of the share, told to all
       }
+      ws.split[blockIdx.x] = split;  // pieces 0: none
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -675,6 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // scores are dot products until the exponent (plain), or log2 units (GEN)
     const float c = GEN ? 1.0f : p.sc.scale * kLog2e;
     const float raise = GEN ? kRaise : kRaise / c;
+    const float scale2 = p.sc.scale * kLog2e;
+    const float cap_in = p.sc.softcap > 0.0f ? p.sc.scale / p.sc.softcap : 0.0f;
+    const float cap_out = p.sc.softcap * kLog2e;
     uint32_t sph = 0, oph = 0;
     Pieces<ND, true> pieces{s, p.err};
     while (pieces.next(g)) {
@@ -686,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lo_last = p.sc.window ? p_first + ntok - 1 - p.sc.window : -1;
       const bool mine = tok < ntok;                       // this row exists
       const int h = g.head * p.group + hg;
-      const float slope = GEN && p.sc.slopes ? p.sc.slopes[h] : 0.0f;
+      const float slope = GEN && p.sc.slopes ? p.sc.slopes[h] * kLog2e : 0.0f;
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
       for (int j = 0; j < cnt; ++j) {
@@ -702,8 +741,56 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) loaded16(reinterpret_cast<uint32_t*>(x) + i * 16);
         if (GEN) {
+          if (p.sc.softcap > 0.0f) {
+            // cap tanh(x scale / cap) in log2 units. While every |x| scale / cap of
+            // the warp's rows is below kTanhMax, tanh is an odd polynomial, two to
+            // an instruction; else 1 - 2 / (1 + e^2y).
+            float top = fabsf(x[0]);
 #pragma unroll
-          for (int i = 0; i < kBlk; ++i) x[i] = score<true>(p.sc, x[i], slope, pos - kb - i);
+            for (int i = 1; i < kBlk - 1; i += 2) top = max3(top, fabsf(x[i]), fabsf(x[i + 1]));
+            top = fmaxf(top, fabsf(x[kBlk - 1]));
+            if (__all_sync(0xffffffffu, top * fabsf(cap_in) < kTanhMax)) {
+#pragma unroll
+              for (int i = 0; i < kBlk / 2; ++i) {
+                const uint64_t y = mul2(pack2(x[2 * i], x[2 * i + 1]), pack2(cap_in, cap_in));
+                const uint64_t t = mul2(y, y);
+                uint64_t r = pack2(kTanh[5], kTanh[5]);
+#pragma unroll
+                for (int k = 4; k >= 0; --k) r = fma2(r, t, pack2(kTanh[k], kTanh[k]));
+                r = mul2(mul2(r, y), pack2(cap_out, cap_out));
+                unpack2(r, x[2 * i], x[2 * i + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kBlk; ++i) {
+                const float e = ex2(x[i] * (2.0f * kLog2e * cap_in));
+                x[i] = fmaf(-2.0f * cap_out, rcp(1.0f + e), cap_out);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kBlk / 2; ++i) {
+              const uint64_t r = mul2(pack2(x[2 * i], x[2 * i + 1]), pack2(scale2, scale2));
+              unpack2(r, x[2 * i], x[2 * i + 1]);
+            }
+          }
+          if (p.sc.slopes) {
+            // distances are whole numbers: exact steps of -1 from key to key
+            const float far = (float)(pos - kb);
+            if (kb + kBlk - 1 <= p_first) {  // no key lies ahead of its query
+              uint64_t away = pack2(far, far - 1.0f);
+#pragma unroll
+              for (int i = 0; i < kBlk / 2; ++i) {
+                const uint64_t r =
+                    fma2(away, pack2(-slope, -slope), pack2(x[2 * i], x[2 * i + 1]));
+                unpack2(r, x[2 * i], x[2 * i + 1]);
+                away = add2(away, pack2(-2.0f, -2.0f));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kBlk; ++i) x[i] = fmaf(-slope, fabsf(far - (float)i), x[i]);
+            }
+          }
         }
         // every row of the tile sees every key of the block, or not
         const bool whole = (kb + kBlk - 1 <= p_first && kb > lo_last) || kb + kBlk <= g.prefix;
@@ -869,46 +956,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ join
-// 32 rows of a tile of one split item per CTA; a lane is a row.
+// 32 rows of a tile of one split item per CTA; a lane is a row, a warp a quarter
+// of its values.
 template <typename T, int ND>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, const TcPlan w) {
   wait_prior_launch();
+  let_next_launch();
   const int c0 = blockIdx.x, t = blockIdx.y >> 2;
   const Split sp = w.split[c0];
-  if (sp.pieces == 0) return;
-  const Entry e = load_entry(w.entries + sp.entry);
   const int warp = threadIdx.x >> 5, row = (blockIdx.y & 3) * 32 + (threadIdx.x & 31);
   const int tpt = tile_tokens(p.group);
   const int tok = row / p.group, hg = row - tok * p.group;
-  if (tok >= min(tpt, e.ntok - t * tpt)) return;
-  const auto slot = [&](int i) { return (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * 2 + t; };
-  float m = -INFINITY;
-  for (int i = 0; i < sp.pieces; ++i) {
-    const float2 x = w.ml[slot(i) * 128 + row];
-    if (x.y != 0.0f) m = fmaxf(m, x.x);
-  }
-  const float base = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f;
+  if (sp.pieces == 0 || tok >= min(tpt, sp.ntok - t * tpt)) return;
+  float m = -INFINITY, l = 0.0f;
   float4 acc[ND * 4];
 #pragma unroll
   for (int k = 0; k < ND * 4; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
   for (int i = 0; i < sp.pieces; ++i) {
-    const float2 x = w.ml[slot(i) * 128 + row];
+    const long long slot = (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * 2 + t;
+    const float2 x = w.ml[slot * 128 + row];
+    const float4* src = reinterpret_cast<const float4*>(w.o) + slot * (ND * 16) * 128 + row;
+    float4 v[ND * 4];
+#pragma unroll
+    for (int k = 0; k < ND * 4; ++k) v[k] = src[(k * 4 + warp) * 128];
     if (x.y == 0.0f) continue;  // saw no key: its sums may not have been written
-    const float f = ex2(x.x - base);
-    l += x.y * f;
-    const float4* src = reinterpret_cast<const float4*>(w.o) + slot(i) * (ND * 16) * 128 + row;
+    const float m2 = fmaxf(m, x.x);
+    const float a = ex2(m - m2), f = ex2(x.x - m2);
+    m = m2;
+    l = l * a + x.y * f;
 #pragma unroll
     for (int k = 0; k < ND * 4; ++k) {
-      const float4 v = src[(k * 4 + warp) * 128];
-      acc[k].x = fmaf(v.x, f, acc[k].x);
-      acc[k].y = fmaf(v.y, f, acc[k].y);
-      acc[k].z = fmaf(v.z, f, acc[k].z);
-      acc[k].w = fmaf(v.w, f, acc[k].w);
+      acc[k].x = acc[k].x * a + v[k].x * f;
+      acc[k].y = acc[k].y * a + v[k].y * f;
+      acc[k].z = acc[k].z * a + v[k].z * f;
+      acc[k].w = acc[k].w * a + v[k].w * f;
     }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const long long r = e.first + t * tpt + tok;
+  const long long r = sp.first + t * tpt + tok;
   const int h = sp.head * p.group + hg;
   uint16_t* dst = p.out.p + r * p.out.token + (long long)h * p.out.head;
 #pragma unroll
@@ -976,8 +1062,6 @@ cudaError_t attn_tc_setup(int* ctas_per_sm) {
 cudaError_t launch_attn_tc(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
                            const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, int grid,
                            cudaStream_t s) {
-  cudaError_t e = launch_after(attn_plan_kernel, dim3(1), dim3(1024), 0, s, p, w, grid);
-  if (e != cudaSuccess) return e;
   const bool wide = p.head_dim > 64;
   if (dtype == MOE_ATTN_BF16)
     return wide ? launch_nd<Bf16, 2>(p, w, qmap, kmap, vmap, grid, s)
