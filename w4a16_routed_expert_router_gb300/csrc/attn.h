@@ -90,7 +90,6 @@ struct AttnParams {
   Batch b;
   Scores sc;
   int hq, hk, group, head_dim, page_shift;
-  int few_rows;  // sequences of at most this many rows per kv head go to the few-token kernel
   unsigned* err;
 };
 
@@ -180,8 +179,7 @@ struct Shares {
   __device__ __forceinline__ int of(long long i) const { return (int)quotient(i, per); }
 };
 
-// sequences with at most kDecodeRows query rows per kv head; the rest is left
-// to the tensor-core kernel
+// batches with at most kDecodeRows query rows per sequence and kv head
 cudaError_t attn_decode_setup();
 cudaError_t launch_attn_decode(const AttnParams& p, const Partials& w, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, int dtype, int grid, cudaStream_t s);

@@ -85,7 +85,7 @@ template <int ND>
 __device__ __forceinline__ Span item_of(const AttnParams& p, int s) {
   Span r = read_sequence(p.b, p.page_shift, s, p.err);
   r.blocks = 0;
-  if (r.n > 0 && r.n * p.group <= kRows)
+  if (r.n > 0)  // and at most max_q, which is kRows / group or less
     span_blocks(r, r.kv - r.n, r.kv - 1, p.sc.window, prefix_of(p.sc, s, r.kv), decode_block(ND));
   return r;
 }

@@ -59,8 +59,7 @@ constexpr float kRaise = 8.0f;      // log2 units
 struct Scan {
   long long part[kThreads / 32];
 };
-// What an entry needs of its sequence: n = 0 where its rows are few or its
-// lengths leave their ranges.
+// What an entry needs of its sequence: n = 0 where its lengths leave their ranges.
 struct alignas(16) Seq {
   int first, n, kv, prefix;
 };
@@ -273,7 +272,7 @@ __device__ __forceinline__ int blocks_of_tile0(const Entry& e, int tpt) {
 // ------------------------------------------------------------------ dividing the work
 __device__ __forceinline__ Seq sequence_of(const AttnParams& p, int q) {
   const Span r = read_sequence(p.b, p.page_shift, q, p.err);
-  return Seq{r.first, r.n * p.group > p.few_rows ? r.n : 0, r.kv, prefix_of(p.sc, q, r.kv)};
+  return Seq{r.first, r.n, r.kv, prefix_of(p.sc, q, r.kv)};
 }
 __device__ __forceinline__ int entries_of(const Seq& r, int tpt) {
   return (int)((unsigned)(r.n + 2 * tpt - 1) / (unsigned)(2 * tpt));
