@@ -248,6 +248,28 @@ def test_strides_and_cache_orders(lens):
     assert torch.equal(o2, out)
 
 
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("order", ["heads", "tokens", "padded", "one page"])
+def test_cache_orders_of_wide_heads(page, order):
+    # heads of 128 values come in other boxes where the cache is regular
+    lens, hk = [(150, 16)] if order == "one page" else MIXED + [(150, 513)], 2
+    shape = (8, hk, 128, page, BF)
+    b = ac.Batch(lens, *shape, heads_inner=order != "tokens")
+    if order == "one page":   # a cache of a single page
+        first = b.table[0, 0].item()
+        b.k_pages, b.v_pages = b.k_pages[first:first + 1], b.v_pages[first:first + 1]
+        b.table = torch.zeros_like(b.table)
+    if order == "padded":
+        for name in ("k_pages", "v_pages"):
+            t = getattr(b, name)
+            wide = torch.full((t.shape[0], hk + 1, page, 128), math.nan, dtype=BF, device=DEV)
+            wide[:, :hk] = t
+            setattr(b, name, wide[:, :hk])
+    layer = _layer(b, shape)
+    b.check(*b.run(layer))
+    assert layer.check_device_errors() == 0
+
+
 def test_runs_are_identical_and_handles_are_reused():
     shape = (32, 8, 128, 16, BF)
     b = ac.Batch(MIXED, *shape)

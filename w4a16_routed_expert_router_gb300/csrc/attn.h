@@ -81,6 +81,14 @@ struct Batch {
   int columns, num_seqs, num_tokens, max_q;
 };
 
+// How the tensor-core kernel's boxes of K and V are addressed: where `both`,
+// one box brings 8-row groups with both 64-value chunks of a head; its group
+// coordinate is page * page_groups + group in the page, its head coordinate
+// page * page_heads + head.
+struct Boxes {
+  int both, page_groups, page_heads;
+};
+
 struct AttnParams {
   Rows q, out;
   float* lse;
@@ -90,6 +98,7 @@ struct AttnParams {
   Batch b;
   Scores sc;
   int hq, hk, group, head_dim, page_shift;
+  Boxes boxes;
   unsigned* err;
 };
 

@@ -39,8 +39,9 @@ constexpr int kTmaWarp = 8, kMmaWarp = 9, kClearWarp = 10, kWalkWarp = 11;
 constexpr int kPieceReaders = kSoftmaxWarps + 3;
 // Registers a thread: the launch gives every thread kLaunchRegs; the producer
 // warpgroup hands most of its share to the two softmax warpgroups, whose rows
-// of 128 scores do not fit otherwise.
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+// of 128 scores do not fit otherwise. (216 and 72 spill in the issuing thread:
+// prefill of 8192 tokens 407 us, 390 us with these.)
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "setmaxnreg draws on the launch");
 constexpr int kBlk = kTcBlock;
 constexpr int kChunk = 128 * 128;   // 128 rows of 64 values
@@ -99,18 +100,24 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       : "memory");
 }
 
-// Shared-memory descriptor of an operand whose M/N index is contiguous, rows of
-// 64 values with the 128-byte swizzle: 8 K rows are 1024 B, the next 64 values
-// of M/N a chunk further.
-__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr) {
-  uint64_t desc = 0;
-  desc |= (uint64_t)((addr >> 4) & 0x3FFF);
-  desc |= (uint64_t)((kChunk >> 4) & 0x3FFF) << 16;
-  desc |= (uint64_t)((1024 >> 4) & 0x3FFF) << 32;
-  desc |= (uint64_t)1 << 46;
-  desc |= (uint64_t)2 << 61;
-  return desc;
-}
+// How a block of keys lies in its slot: atoms of 8 rows of 64 values (1024 B,
+// 128-byte swizzle), kGroup bytes from 8 rows to the next, kNext bytes from 64
+// values to the next. BOTH: one box brings both chunks of a head, 8 rows by 8
+// rows; else a box a chunk. (As numbers known at run time they cost the issuing
+// thread 5 % of a prefill.)
+template <bool BOTH>
+struct BlockLayout {
+  static constexpr uint32_t kGroup = BOTH ? 2048 : 1024, kNext = BOTH ? 1024 : kChunk;
+  // shared-memory descriptors: K, values along the sum
+  static __device__ __forceinline__ uint64_t k(uint32_t addr) {
+    return (smem_desc_sw128(addr) & ~((uint64_t)0x3FFF << 32)) | (uint64_t)(kGroup >> 4) << 32;
+  }
+  // V, keys along the sum and values contiguous: the leading offset goes from 64
+  // values to the next, the stride offset from 8 keys to the next
+  static __device__ __forceinline__ uint64_t v(uint32_t addr) {
+    return (k(addr) & ~((uint64_t)0x3FFF << 16)) | (uint64_t)(kNext >> 4) << 16;
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ uint32_t idesc_of(int n, bool b_mn) {
@@ -198,6 +205,16 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// groups of 8 rows, both chunks of a head
+__device__ __forceinline__ void tma_groups(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                           int group, int head) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(group), "r"(head)
+      : "memory");
 }
 
 __device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0,
@@ -388,12 +405,13 @@ __device__ __forceinline__ long long divide(const AttnParams& p, Scan& sc, uint8
 }
 
 // ------------------------------------------------------------------ attention
-template <typename T, int ND, bool GEN>
+template <typename T, int ND, bool GEN, bool BOTH>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const AttnParams p, const TcPlan ws) {
   typedef Smem<ND> S;
+  typedef BlockLayout<BOTH> L;
   extern __shared__ uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -497,11 +515,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = __shfl_sync(0xffffffffu, ok, 0);
               if (!ok) break;
               if (lane < boxes) {
-                const uint32_t dst = smem_u32(s.kv[slot]) + lane * box_rows * 128;
-  #pragma unroll
-                for (int c = 0; c < ND; ++c)
-                  tma_page(dst + c * kChunk, kv ? &vmap : &kmap, &s.kv_full[slot], c * 64, row,
-                           g.head, page);
+                const uint32_t dst = smem_u32(s.kv[slot]) + lane * (box_rows >> 3) * L::kGroup;
+                const CUtensorMap* map = kv ? &vmap : &kmap;
+                if (BOTH) {
+                  tma_groups(dst, map, &s.kv_full[slot],
+                             page * p.boxes.page_groups + (row >> 3),
+                             page * p.boxes.page_heads + g.head);
+                } else {
+#pragma unroll
+                  for (int c = 0; c < ND; ++c)
+                    tma_page(dst + c * kChunk, map, &s.kv_full[slot], c * 64, row, g.head, page);
+                }
               }
               filled |= 1u << slot;
               last_ph = (last_ph & ~(1u << slot)) | (ph << slot);
@@ -542,12 +566,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const auto issue_qk = [&](int t, uint32_t kslot) {
           const uint64_t qd = smem_desc_sw128(smem_u32(s.q[t]));
-          const uint64_t kd = smem_desc_sw128(smem_u32(s.kv[kslot]));
+          const uint64_t kd = L::k(smem_u32(s.kv[kslot]));
 #pragma unroll
-          for (int k = 0; k < ND * 4; ++k) {
-            const uint32_t o = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
-            if (k < ksteps) mma_bf16(tmem + t * 128, qd + o, kd + o, id_qk, k != 0);
-          }
+          for (int k = 0; k < ND * 4; ++k)
+            if (k < ksteps)
+              mma_bf16(tmem + t * 128, qd + (((k >> 2) * kChunk + (k & 3) * 32) >> 4),
+                       kd + (((k >> 2) * L::kNext + (k & 3) * 32) >> 4), id_qk, k != 0);
           mma_commit(&s.s_full[t]);
         };
         while (ok && pieces.next(g)) {
@@ -576,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = wait_slot())) break;
               advance();
             }
-            const uint64_t vd = smem_desc_mn(smem_u32(s.kv[vslot]));
+            const uint64_t vd = L::v(smem_u32(s.kv[vslot]));
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (j >= cnt[t]) continue;
@@ -589,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
 #pragma unroll
               for (int k = 0; k < kBlk / 16; ++k)
-                mma_ts(tmem + 256 + t * ND * 64, tmem + t * 128 + k * 8, vd + k * (2048 >> 4),
+                mma_ts(tmem + 256 + t * ND * 64, tmem + t * 128 + k * 8, vd + k * (L::kGroup >> 3),
                        id_pv, (j | k) != 0);
               if (j + 1 == cnt[t]) mma_commit(&s.o_full[t]);
               if (j + 1 < cnt[t]) issue_qk(t, kslot);
@@ -625,7 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int from = max(left, 0);
           for (int i = lane; i < (kBlk - from) * ND * 8; i += 32) {
             const int r = from + i / (ND * 8), c = i % (ND * 8);
-            sts128(v + (c >> 3) * kChunk + r * 128 + (c & 7) * 16, 0, 0, 0, 0);
+            sts128(v + (c >> 3) * L::kNext + (r >> 3) * L::kGroup + (r & 7) * 128 + (c & 7) * 16, 0,
+                   0, 0, 0);
           }
           fence_async_shared();
           __syncwarp();
@@ -1030,21 +1055,31 @@ cudaError_t setup_one(F f, int bytes, int* per_sm) {
   return e;
 }
 
-template <typename T, int ND>
+template <typename T, int ND, bool BOTH>
 cudaError_t setup_nd(int* per_sm) {
-  cudaError_t e = setup_one(attn_tc_kernel<T, ND, false>, smem_bytes<ND>(), per_sm);
-  return e != cudaSuccess ? e : setup_one(attn_tc_kernel<T, ND, true>, smem_bytes<ND>(), per_sm);
+  cudaError_t e = setup_one(attn_tc_kernel<T, ND, false, BOTH>, smem_bytes<ND>(), per_sm);
+  return e != cudaSuccess ? e
+                          : setup_one(attn_tc_kernel<T, ND, true, BOTH>, smem_bytes<ND>(), per_sm);
 }
 
-template <typename T, int ND>
+template <typename T, int ND, bool BOTH>
 cudaError_t launch_nd(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
                       const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
   // the plain form takes the maximum before it scales
   const bool gen = p.sc.softcap > 0.0f || p.sc.slopes || !(p.sc.scale > 0.0f);
-  cudaError_t e = launch_after(gen ? attn_tc_kernel<T, ND, true> : attn_tc_kernel<T, ND, false>,
-                               dim3(grid), dim3(kThreads), smem_bytes<ND>(), s, qmap, kmap, vmap, p, w);
+  cudaError_t e = launch_after(
+      gen ? attn_tc_kernel<T, ND, true, BOTH> : attn_tc_kernel<T, ND, false, BOTH>, dim3(grid),
+      dim3(kThreads), smem_bytes<ND>(), s, qmap, kmap, vmap, p, w);
   if (e != cudaSuccess) return e;
   return launch_after(attn_join_kernel<T, ND>, dim3(grid, 8), dim3(128), 0, s, p, w);
+}
+
+template <typename T>
+cudaError_t launch_t(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
+                     const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
+  if (p.head_dim <= 64) return launch_nd<T, 1, false>(p, w, qmap, kmap, vmap, grid, s);
+  return p.boxes.both ? launch_nd<T, 2, true>(p, w, qmap, kmap, vmap, grid, s)
+                      : launch_nd<T, 2, false>(p, w, qmap, kmap, vmap, grid, s);
 }
 
 }  // namespace
@@ -1052,21 +1087,19 @@ cudaError_t launch_nd(const AttnParams& p, const TcPlan& w, const CUtensorMap& q
 cudaError_t attn_tc_setup(int* ctas_per_sm) {
   *ctas_per_sm = 1;
   cudaError_t e;
-  if ((e = setup_nd<Bf16, 1>(ctas_per_sm)) != cudaSuccess) return e;
-  if ((e = setup_nd<Bf16, 2>(ctas_per_sm)) != cudaSuccess) return e;
-  if ((e = setup_nd<Fp16, 1>(ctas_per_sm)) != cudaSuccess) return e;
-  return setup_nd<Fp16, 2>(ctas_per_sm);
+  if ((e = setup_nd<Bf16, 1, false>(ctas_per_sm)) != cudaSuccess) return e;
+  if ((e = setup_nd<Bf16, 2, false>(ctas_per_sm)) != cudaSuccess) return e;
+  if ((e = setup_nd<Bf16, 2, true>(ctas_per_sm)) != cudaSuccess) return e;
+  if ((e = setup_nd<Fp16, 1, false>(ctas_per_sm)) != cudaSuccess) return e;
+  if ((e = setup_nd<Fp16, 2, false>(ctas_per_sm)) != cudaSuccess) return e;
+  return setup_nd<Fp16, 2, true>(ctas_per_sm);
 }
 
 cudaError_t launch_attn_tc(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
                            const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, int grid,
                            cudaStream_t s) {
-  const bool wide = p.head_dim > 64;
-  if (dtype == MOE_ATTN_BF16)
-    return wide ? launch_nd<Bf16, 2>(p, w, qmap, kmap, vmap, grid, s)
-                : launch_nd<Bf16, 1>(p, w, qmap, kmap, vmap, grid, s);
-  return wide ? launch_nd<Fp16, 2>(p, w, qmap, kmap, vmap, grid, s)
-              : launch_nd<Fp16, 1>(p, w, qmap, kmap, vmap, grid, s);
+  return dtype == MOE_ATTN_BF16 ? launch_t<Bf16>(p, w, qmap, kmap, vmap, grid, s)
+                                : launch_t<Fp16>(p, w, qmap, kmap, vmap, grid, s);
 }
 
 }  // namespace attn
