@@ -94,6 +94,15 @@ def register(L: ctypes.CDLL) -> None:
         fn.restype = ctypes.c_int
 
 
+def _by_address(L: ctypes.CDLL, name: str):
+    """The function with its structures passed as plain addresses (half the cost
+    of the pointers that ctypes makes of them)."""
+    fn = L[name]  # a function object of its own
+    fn.argtypes = [_vp if issubclass(a, ctypes._Pointer) else a for a in _signatures()[name]]
+    fn.restype = ctypes.c_int
+    return fn
+
+
 _library = None
 
 
@@ -125,32 +134,39 @@ def _stream(stream, device) -> int:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _fill_rows(s, t, heads, dim, dtype, device, what):
-    """Describe t [tokens, heads, dim] in s; returns the number of tokens."""
+def _fill_rows(s, t, heads, dim, dtype, index, what):
+    """Describe t [tokens, heads, dim] on device `index` in s; returns its tokens."""
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{what} must be [tokens, {heads}, {dim}], got {list(shape)}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{what} must be {dtype} on cuda:{index}, got {t.dtype} on {t.device}")
     token, head, last = t.stride()
     if last != 1 and dim > 1:
         raise ValueError(f"{what} must be contiguous along head_dim")
     s.data = t.data_ptr()
     # the stride of a dimension of one element says nothing
     s.head_stride = head if heads > 1 else dim
-    s.token_stride = token if shape[0] > 1 else heads * s.head_stride
-    return shape[0]
+    tokens = shape[0]
+    s.token_stride = token if tokens > 1 else heads * s.head_stride
+    return tokens
 
 
-def _vector(t, n, dtype, device, what):
-    """Address of t, a contiguous vector of n elements."""
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n}, got "
-                         f"{t.dtype} {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, got {t.device}")
+def _new_rows(s, tokens, heads, dim, dtype, device, stream):
+    """A new tensor [tokens, heads, dim], described in s."""
+    t = _empty((tokens, heads, dim), dtype, device, stream)
+    s.data = t.data_ptr()
+    s.head_stride = dim
+    s.token_stride = heads * dim
+    return t
+
+
+def _vector(t, n, dtype, index, what):
+    """Address of t, a contiguous vector of n elements on device `index`."""
+    if (t.dtype is not dtype or t.get_device() != index or t.dim() != 1 or t.numel() != n or
+            not t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} on cuda:{index}, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
@@ -164,12 +180,12 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _fill_rotation(s, freq, layout, magnitude, inverse, device):
+def _fill_rotation(s, freq, layout, magnitude, inverse, index):
     code = _LAYOUTS.get(layout)
     if code is None:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
     n = freq.numel()
-    s.freq = _vector(freq, n, torch.int64, device, "freq")
+    s.freq = _vector(freq, n, torch.int64, index, "freq")
     s.rot_dim = 2 * n
     s.layout = code
     s.magnitude = magnitude
@@ -198,20 +214,22 @@ def moe_attn_rope(x, positions, freq, out=None, layout="half", magnitude=1.0, in
     """Rotary positions of x [tokens, heads, head_dim] (bf16 or fp16, any token
     and head strides) at positions int32 [tokens]; out may be x. ``inverse``
     turns the other way: the gradient of x from the gradient of the result."""
-    if x.dim() != 3 or x.dtype not in _DTYPES or not x.is_cuda:
+    dtype, device = x.dtype, x.device
+    code = _DTYPES.get(dtype)
+    if code is None or device.type != "cuda" or x.dim() != 3:
         raise ValueError("x must be a bf16 or fp16 CUDA tensor [tokens, heads, head_dim]")
-    device, dtype = x.device, x.dtype
+    index = device.index
     tokens, heads, dim = x.shape
-    if out is None:
-        out = _empty((tokens, heads, dim), dtype, device, stream)
     xs, os, rot = moe_attn_rows(), moe_attn_rows(), moe_attn_rotation()
-    _fill_rows(xs, x, heads, dim, dtype, device, "x")
-    if _fill_rows(os, out, heads, dim, dtype, device, "out") != tokens:
+    _fill_rows(xs, x, heads, dim, dtype, index, "x")
+    if out is None:
+        out = _new_rows(os, tokens, heads, dim, dtype, device, stream)
+    elif _fill_rows(os, out, heads, dim, dtype, index, "out") != tokens:
         raise ValueError("x and out differ in tokens")
-    _fill_rotation(rot, freq, layout, magnitude, inverse, device)
-    pos = _vector(positions, tokens, torch.int32, device, "positions")
-    args = (xs, os, pos, tokens, heads, dim, _DTYPES[dtype], rot, _stream(stream, device))
-    if torch.cuda.current_device() == device.index:
+    _fill_rotation(rot, freq, layout, magnitude, inverse, index)
+    args = (xs, os, _vector(positions, tokens, torch.int32, index, "positions"), tokens, heads,
+            dim, code, rot, _stream(stream, device))
+    if torch.cuda.current_device() == index:
         st = _lib().moe_attn_rope(*args)
     else:
         with torch.cuda.device(device):
@@ -246,11 +264,18 @@ class PagedAttention:
         _check(self._library.moe_attn_create(ctypes.byref(self.cfg), index, ctypes.byref(handle)),
                "moe_attn_create")
         self.handle = handle
-        # filled anew by every call
+        # filled anew by every call, and passed by their addresses
         self._q, self._o = moe_attn_rows(), moe_attn_rows()
         self._k, self._v = moe_attn_rows(), moe_attn_rows()
         self._rot, self._cache = moe_attn_rotation(), moe_attn_cache()
         self._batch, self._scores = moe_attn_batch(), moe_attn_scores()
+        at = ctypes.addressof
+        self._at_q, self._at_o, self._at_k, self._at_v = (at(self._q), at(self._o), at(self._k),
+                                                          at(self._v))
+        self._at_rot, self._at_cache = at(self._rot), at(self._cache)
+        self._at_batch, self._at_scores = at(self._batch), at(self._scores)
+        self._append = _by_address(self._library, "moe_attn_append")
+        self._forward = _by_address(self._library, "moe_attn_forward")
 
     def close(self):
         if self.handle is not None and self.handle.value:
@@ -278,7 +303,7 @@ class PagedAttention:
         return flags.value
 
     def _fill_cache(self, k_pages, v_pages):
-        c = self._cache
+        c, index = self._cache, self.device.index
         shape, strides = k_pages.shape, k_pages.stride()
         if (len(shape) != 4 or shape[1] != self.kv_heads or shape[2] != self.page_size or
                 shape[3] != self.head_dim):
@@ -287,17 +312,17 @@ class PagedAttention:
         if v_pages.shape != shape or v_pages.stride() != strides or strides[3] != 1:
             raise ValueError("k_pages and v_pages must have one shape and strides, head_dim "
                              "contiguous")
-        if k_pages.dtype is not self.dtype or v_pages.dtype is not self.dtype:
-            raise ValueError(f"the cache must be {self.dtype}")
-        if k_pages.device != self.device or v_pages.device != self.device:
-            raise ValueError(f"the cache must be on {self.device}")
+        dtype = self.dtype
+        if (k_pages.dtype is not dtype or v_pages.dtype is not dtype or
+                k_pages.get_device() != index or v_pages.get_device() != index):
+            raise ValueError(f"the cache must be {dtype} on {self.device}")
         c.k, c.v = k_pages.data_ptr(), v_pages.data_ptr()
-        c.num_pages, c.page_stride, c.token_stride = shape[0], strides[0], strides[2]
+        c.num_pages = pages = shape[0]
+        c.token_stride = strides[2]
         # the stride of a dimension of one element says nothing
-        c.head_stride = strides[1] if shape[1] > 1 else self.head_dim
-        if shape[0] == 1:
-            c.page_stride = self.page_size * self.kv_heads * self.head_dim
-        return c
+        c.head_stride = strides[1] if self.kv_heads > 1 else self.head_dim
+        c.page_stride = (strides[0] if pages > 1 else
+                         self.page_size * self.kv_heads * self.head_dim)
 
     def append(self, q, k, v, positions, slots, k_pages, v_pages, freq, layout="half",
                magnitude=1.0, q_out=None, stream=None):
@@ -305,27 +330,28 @@ class PagedAttention:
         write k and v to their slots (int64; page * page_size + offset, negative:
         not written) of the cache. Returns q_out (new unless given, may be q);
         q None: keys and values only."""
-        T = _fill_rows(self._k, k, self.kv_heads, self.head_dim, self.dtype, self.device, "k")
-        if _fill_rows(self._v, v, self.kv_heads, self.head_dim, self.dtype, self.device,
-                      "v") != T:
+        device, dtype, dim = self.device, self.dtype, self.head_dim
+        index = device.index
+        T = _fill_rows(self._k, k, self.kv_heads, dim, dtype, index, "k")
+        if _fill_rows(self._v, v, self.kv_heads, dim, dtype, index, "v") != T:
             raise ValueError("k and v differ in tokens")
-        qs = os = None
+        at_q = at_o = None
         if q is not None:
+            at_q, at_o = self._at_q, self._at_o
+            if _fill_rows(self._q, q, self.q_heads, dim, dtype, index, "q") != T:
+                raise ValueError("q and k differ in tokens")
             if q_out is None:
-                q_out = _empty((T, self.q_heads, self.head_dim), self.dtype, self.device, stream)
-            qs, os = self._q, self._o
-            if (_fill_rows(qs, q, self.q_heads, self.head_dim, self.dtype, self.device, "q") != T or
-                    _fill_rows(os, q_out, self.q_heads, self.head_dim, self.dtype, self.device,
-                               "q_out") != T):
-                raise ValueError("q, q_out and k differ in tokens")
+                q_out = _new_rows(self._o, T, self.q_heads, dim, dtype, device, stream)
+            elif _fill_rows(self._o, q_out, self.q_heads, dim, dtype, index, "q_out") != T:
+                raise ValueError("q_out and q differ in tokens")
         elif q_out is not None:
             raise ValueError("q_out without q")
-        _fill_rotation(self._rot, freq, layout, magnitude, False, self.device)
-        st = self._library.moe_attn_append(
-            self.handle, qs, os, self._k, self._v,
-            _vector(positions, T, torch.int32, self.device, "positions"),
-            _vector(slots, T, torch.int64, self.device, "slots"), T, self._rot,
-            self._fill_cache(k_pages, v_pages), _stream(stream, self.device))
+        _fill_rotation(self._rot, freq, layout, magnitude, False, index)
+        self._fill_cache(k_pages, v_pages)
+        st = self._append(self.handle, at_q, at_o, self._at_k, self._at_v,
+                          _vector(positions, T, torch.int32, index, "positions"),
+                          _vector(slots, T, torch.int64, index, "slots"), T, self._at_rot,
+                          self._at_cache, _stream(stream, device))
         if st:
             _check(st, "moe_attn_append")
         return q_out
@@ -341,39 +367,45 @@ class PagedAttention:
         no sequence has more new tokens. scale defaults to 1 / sqrt(head_dim).
         Returns out, or (out, lse) with lse fp32 [tokens, q_heads].
         """
-        device = self.device
+        device, dim = self.device, self.head_dim
+        index = device.index
+        T = _fill_rows(self._q, q, self.q_heads, dim, self.dtype, index, "q")
         if out is None:
-            out = _empty(q.shape, self.dtype, device, stream)
-        T = _fill_rows(self._q, q, self.q_heads, self.head_dim, self.dtype, device, "q")
-        if _fill_rows(self._o, out, self.q_heads, self.head_dim, self.dtype, device, "out") != T:
+            out = _new_rows(self._o, T, self.q_heads, dim, self.dtype, device, stream)
+        elif _fill_rows(self._o, out, self.q_heads, dim, self.dtype, index, "out") != T:
             raise ValueError("q and out differ in tokens")
-        n = kv_len.shape[0] if kv_len.dim() == 1 else -1
         b, s = self._batch, self._scores
-        if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or
-                page_table.shape[0] != n or page_table.device != device or
-                (page_table.stride(1) != 1 and page_table.shape[1] > 1)):
+        table = page_table.shape
+        n = kv_len.numel()
+        if (len(table) != 2 or table[0] != n or page_table.dtype is not torch.int32 or
+                page_table.get_device() != index or
+                (page_table.stride(1) != 1 and table[1] > 1)):
             raise ValueError(f"page_table must be int32 [{n}, columns] on {device}, contiguous "
                              "along the columns")
-        b.cu_q = _vector(cu_q, n + 1, torch.int32, device, "cu_q")
-        b.kv_len = _vector(kv_len, n, torch.int32, device, "kv_len")
+        b.cu_q = _vector(cu_q, n + 1, torch.int32, index, "cu_q")
+        b.kv_len = _vector(kv_len, n, torch.int32, index, "kv_len")
         b.page_table = page_table.data_ptr()
-        b.columns = page_table.shape[1]
-        b.table_stride = page_table.stride(0) if n > 1 else b.columns
+        b.columns = columns = table[1]
+        b.table_stride = page_table.stride(0) if n > 1 else columns
         b.num_seqs, b.num_tokens, b.max_q = n, T, max_q
-        s.scale = self.head_dim ** -0.5 if scale is None else scale
+        s.scale = dim ** -0.5 if scale is None else scale
         s.softcap, s.window = softcap, window
-        s.slopes = None if slopes is None else _vector(slopes, self.q_heads, torch.float32, device,
+        s.slopes = None if slopes is None else _vector(slopes, self.q_heads, torch.float32, index,
                                                        "slopes")
-        s.prefix = None if prefix is None else _vector(prefix, n, torch.int32, device, "prefix")
-        if lse is None:
-            if return_lse:
-                lse = _empty((T, self.q_heads), torch.float32, device, stream)
-        elif (lse.dtype is not torch.float32 or tuple(lse.shape) != (T, self.q_heads) or
-              not lse.is_contiguous() or lse.device != device):
-            raise ValueError(f"lse must be contiguous float32 [{T}, {self.q_heads}] on {device}")
-        st = self._library.moe_attn_forward(
-            self.handle, self._q, self._o, None if lse is None else lse.data_ptr(),
-            self._fill_cache(k_pages, v_pages), b, s, _stream(stream, device))
+        s.prefix = None if prefix is None else _vector(prefix, n, torch.int32, index, "prefix")
+        at_lse = None
+        if lse is not None:
+            if (lse.dtype is not torch.float32 or tuple(lse.shape) != (T, self.q_heads) or
+                    not lse.is_contiguous() or lse.get_device() != index):
+                raise ValueError(f"lse must be contiguous float32 [{T}, {self.q_heads}] on "
+                                 f"{device}")
+            at_lse = lse.data_ptr()
+        elif return_lse:
+            lse = _empty((T, self.q_heads), torch.float32, device, stream)
+            at_lse = lse.data_ptr()
+        self._fill_cache(k_pages, v_pages)
+        st = self._forward(self.handle, self._at_q, self._at_o, at_lse, self._at_cache,
+                           self._at_batch, self._at_scores, _stream(stream, device))
         if st:
             _check(st, "moe_attn_forward")
         return (out, lse) if return_lse else out
