@@ -767,22 +767,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (GEN) {
           if (p.sc.softcap > 0.0f) {
             // cap tanh(x scale / cap) in log2 units. While every |x| scale / cap of
-            // the warp's rows is below kTanhMax, tanh is an odd polynomial, two to
-            // an instruction; else 1 - 2 / (1 + e^2y).
+            // the warp's rows is below kTanhMax, it is x times a polynomial in x^2
+            // (the factors go into its coefficients; up to 1000, so that their
+            // powers stay finite), two keys to an instruction; else 1 - 2 / (1 +
+            // e^2y).
             float top = fabsf(x[0]);
 #pragma unroll
             for (int i = 1; i < kBlk - 1; i += 2) top = max3(top, fabsf(x[i]), fabsf(x[i + 1]));
             top = fmaxf(top, fabsf(x[kBlk - 1]));
-            if (__all_sync(0xffffffffu, top * fabsf(cap_in) < kTanhMax)) {
+            if (__all_sync(0xffffffffu, top * fabsf(cap_in) < kTanhMax) && fabsf(cap_in) < 1e3f) {
+              float f[6], power = cap_in * cap_out;
+#pragma unroll
+              for (int k = 0; k < 6; ++k) {
+                f[k] = kTanh[k] * power;
+                power *= cap_in * cap_in;
+              }
 #pragma unroll
               for (int i = 0; i < kBlk / 2; ++i) {
-                const uint64_t y = mul2(pack2(x[2 * i], x[2 * i + 1]), pack2(cap_in, cap_in));
+                const uint64_t y = pack2(x[2 * i], x[2 * i + 1]);
                 const uint64_t t = mul2(y, y);
-                uint64_t r = pack2(kTanh[5], kTanh[5]);
+                uint64_t r = pack2(f[5], f[5]);
 #pragma unroll
-                for (int k = 4; k >= 0; --k) r = fma2(r, t, pack2(kTanh[k], kTanh[k]));
-                r = mul2(mul2(r, y), pack2(cap_out, cap_out));
-                unpack2(r, x[2 * i], x[2 * i + 1]);
+                for (int k = 4; k >= 0; --k) r = fma2(r, t, pack2(f[k], f[k]));
+                unpack2(mul2(r, y), x[2 * i], x[2 * i + 1]);
               }
             } else {
 #pragma unroll
