@@ -18,7 +18,7 @@ struct moe_attn_handle {
   int grid = 0;                 // CTAs of a split launch: one per SM
   unsigned* err = nullptr;
   Partials decode{};
-  TcPlan tc{};
+  TcPieces tc{};
 };
 
 namespace {
@@ -127,7 +127,7 @@ Layout plan(const moe_attn_config& c) {
       kMaxGrid * 4,                             // 1 decode: pieces that arrived
       kMaxGrid * 2 * kDecodeRows * 8,           // 2 decode: maximum, sum
       kMaxGrid * 2 * kDecodeRows * d * 4,       // 3 decode: weighted sums
-      kMaxGrid * sizeof(Split),                 // 4 split items
+      kMaxGrid * 2 * 4,                         // 4 tensor cores: halves that arrived
       kMaxGrid * 4 * 128 * 8,                   // 5 maximum, sum
       kMaxGrid * 4 * 128 * d * 4,               // 6 weighted sums
   };
@@ -339,7 +339,7 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn_handle** ou
   h->decode.count = reinterpret_cast<unsigned*>(b + L.off[1]);
   h->decode.ml = reinterpret_cast<float2*>(b + L.off[2]);
   h->decode.o = reinterpret_cast<float*>(b + L.off[3]);
-  h->tc.split = reinterpret_cast<Split*>(b + L.off[4]);
+  h->tc.count = reinterpret_cast<unsigned*>(b + L.off[4]);
   h->tc.ml = reinterpret_cast<float2*>(b + L.off[5]);
   h->tc.o = reinterpret_cast<float*>(b + L.off[6]);
   *out = h;

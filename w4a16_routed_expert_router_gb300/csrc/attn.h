@@ -206,24 +206,17 @@ struct Entry {
   int prefix, seq;
 };
 
-// An item whose first piece ended before it did.
-struct Split {
-  int pieces;       // 0: there is none
-  int first, ntok;  // see Entry
-  int head;
-};
-
-struct TcPlan {
-  Split* split;     // [kMaxGrid] by the CTA of the first piece
+// What pieces of items leave for each other.
+struct TcPieces {
+  unsigned* count;  // [kMaxGrid][2 tiles] halves of a pair that arrived (self-resetting)
   float* o;         // [kMaxGrid][2 pieces][2 tiles][dim / 4][128 rows][4]
   float2* ml;       // [kMaxGrid][2][2][128] maximum (log2 units), sum
 };
 
 __host__ __device__ inline int tile_tokens(int group) { return 128 / group; }
 
-// Two kernels: attend, and join the split items.
 cudaError_t attn_tc_setup(int* ctas_per_sm);
-cudaError_t launch_attn_tc(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
+cudaError_t launch_attn_tc(const AttnParams& p, const TcPieces& w, const CUtensorMap& qmap,
                            const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, int grid,
                            cudaStream_t s);
 

@@ -1,14 +1,15 @@
 // Attention of many new tokens per sequence over the paged cache: prompts and
 // chunks of prompts, on the 5th-generation tensor core.
 //
-// Two launches. attn_tc runs one persistent CTA per SM over an equal share of
-// all key blocks of all items, an item being up to two tiles of query tokens of
-// one sequence (an entry) and a kv head; attn_join adds the pieces of items that
-// more than one CTA holds, in their order. Equal shares keep every SM busy to
-// the end under a causal mask, ragged lengths or a single chunk over a long
-// cache.
+// One persistent CTA per SM over an equal share of all key blocks of all items,
+// an item being up to two tiles of query tokens of one sequence (an entry) and a
+// kv head. Equal shares keep every SM busy to the end under a causal mask, ragged
+// lengths or a single chunk over a long cache. The pieces of an item that more
+// than one CTA holds are joined by pairs, by whichever of the two comes second
+// (which has its own piece in TMEM still), in an order that does not depend on
+// who that is. (A launch of its own that added them took 8 to 15 us.)
 //
-// attn_tc, one item: two tiles of 128 query rows (token, head of the group)
+// One item: two tiles of 128 query rows (token, head of the group)
 // against blocks of 128 keys, S = Q K^T and O += P V with tcgen05.mma; S and O
 // of both tiles fill the 512 columns of TMEM, and P (16 bits) takes the place
 // of S, whose row a thread has in registers by then, as the A operand in TMEM.
@@ -84,6 +85,7 @@ struct Smem {
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   Scan scan;
   Begin begin;
+  unsigned there[2];
   uint64_t kv_full[kSlots], kv_empty[kSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drain, clear, cleared;
@@ -248,7 +250,7 @@ struct alignas(16) Piece {
   int near, skip, blocks, prefix;
   int head, n0, end, seq;
   int cnt[2];                       // blocks of the piece that tile 0 / 1 takes
-  int pad[2];
+  int cta0, pieces;                 // of a split item: CTA of its first piece, pieces; or 0, 0
 };
 static_assert(sizeof(Piece) == kPieceBytes, "shared memory of a piece");
 
@@ -259,18 +261,29 @@ struct Pieces {
   unsigned* err;
   int i = 0;
   uint32_t ph = 0;
-  // the next piece, or false at the end of the share or after a timeout
-  __device__ __forceinline__ bool next(Piece& g) {
+  // the next piece, or null at the end of the share or after a timeout
+  __device__ __forceinline__ const Piece* hold() {
     if (!(kWarp ? warp_wait(&s.piece_full[i], ph, err) : bwait(&s.piece_full[i], ph, err)))
-      return false;
-    g = *reinterpret_cast<const Piece*>(s.piece[i]);
+      return nullptr;
+    const Piece* g = reinterpret_cast<const Piece*>(s.piece[i]);
+    return g->end > 0 ? g : nullptr;
+  }
+  // done with it
+  __device__ __forceinline__ void release() {
     if (kWarp) __syncwarp();
     if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&s.piece_empty[i]);
     if (++i == kPieces) {
       i = 0;
       ph ^= 1u;
     }
-    return g.end > 0;
+  }
+  // a copy of the next piece
+  __device__ __forceinline__ bool next(Piece& g) {
+    const Piece* held = hold();
+    if (!held) return false;
+    g = *held;
+    release();
+    return true;
   }
 };
 
@@ -404,12 +417,175 @@ __device__ __forceinline__ long long divide(const AttnParams& p, Scan& sc, uint8
   return total;
 }
 
+// What a softmax group does with the rows of a piece when its blocks are done: m
+// in log2 units and l of this thread's row, O in TMEM (cnt > 0). Its loops are
+// not unrolled: the code runs once a piece, and what it takes is mostly the
+// fetching of its instructions (unrolled, a whole item's results took 6500
+// cycles to store, 3300 so).
+template <typename T, int ND>
+__device__ __forceinline__ void finish_piece(const AttnParams& p, const TcPieces& ws, Smem<ND>& s,
+                                          const Piece* piece, int t, uint32_t o_tm, int cnt,
+                                          float m, float l) {
+  const Piece& g = *piece;
+  const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const int tpt = tile_tokens(p.group);
+  const int tok = row / p.group, h = g.head * p.group + (row - tok * p.group);
+  const bool mine = tok < min(tpt, g.ntok - t * tpt);  // this row exists
+  bool holds = true;  // this group has what is known of the item's rows
+  if (g.pieces) {
+    bool have = cnt > 0;  // O lies in TMEM
+    int a = (int)blockIdx.x - g.cta0;  // first piece of what it has
+    const auto place = [&](int i) {    // of a piece: the item begins in slot 1 of its CTA
+      return (2LL * (g.cta0 + i) + (i == 0 ? 1 : 0)) * 2 + t;
+    };
+    const auto group_sync = [&]() {
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+    };
+    const bool first_thread = (threadIdx.x & 127) == 0;
+    for (int size = 1; size < g.pieces && holds; size <<= 1) {
+      // pieces [a, a + size) are here; the other half of their pair
+      const bool left = (a & size) == 0;
+      const int other = left ? a + size : a - size;
+      if (other >= g.pieces) continue;
+      unsigned* node = ws.count + 2 * (g.cta0 + max(a, other)) + t;
+      if (first_thread) {
+        unsigned v;
+        asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(v) : "l"(node) : "memory");
+        s.there[t] = v;
+      }
+      group_sync();
+      bool there = s.there[t] != 0;
+      if (!there) {
+        // leave it in the workspace, unless the other half came meanwhile
+        const long long at = place(a);
+        __stcg(ws.ml + at * 128 + row, make_float2(m, l));
+        if (have) {
+          float4* dst = reinterpret_cast<float4*>(ws.o) + at * (ND * 16) * 128 + row;
+#pragma unroll 1
+          for (int i = 0; i < ND * 2; ++i) {
+            uint32_t r[32];
+            tmem_ld32_nowait(o_tm + i * 32, r);
+            tmem_ld_wait();
+            loaded16(r);
+            loaded16(r + 16);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              __stcg(dst + (i * 8 + k) * 128,
+                     make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
+                                 __uint_as_float(r[4 * k + 2]),
+                                 __uint_as_float(r[4 * k + 3])));
+          }
+        }
+        __threadfence();
+        group_sync();
+        if (first_thread) {
+          s.there[t] = atomicAdd(node, 1u);
+          __threadfence();
+        }
+        group_sync();
+        there = s.there[t] != 0;
+      }
+      if (!there) {
+        holds = false;
+      } else {
+        const long long at = place(other);
+        const float2 x = __ldcg(ws.ml + at * 128 + row);
+        const float4* src = reinterpret_cast<const float4*>(ws.o) + at * (ND * 16) * 128 + row;
+        const float m2 = fmaxf(m, x.x), base = m2 == -INFINITY ? 0.0f : m2;
+        const float f = ex2(m - base), fx = ex2(x.x - base);
+        m = m2;
+        l = left ? fmaf(x.y, fx, l * f) : fmaf(l, f, x.y * fx);
+        const bool nothing = x.y == 0.0f;  // saw no key: its sums may not have been written
+#pragma unroll 1
+        for (int i = 0; i < ND; ++i) {     // 64 values: 16 loads under way
+          float4 v[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = __ldcg(src + (i * 16 + k) * 128);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[16];
+            if (have) {
+              tmem_ld16_nowait(o_tm + i * 64 + c * 16, r);
+              tmem_ld_wait();
+              loaded16(r);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float* q = reinterpret_cast<const float*>(&v[c * 4 + (k >> 2)]);
+              const float y = nothing ? 0.0f : q[k & 3];
+              const float o = have ? __uint_as_float(r[k]) : 0.0f;
+              r[k] = __float_as_uint(left ? fmaf(y, fx, o * f) : fmaf(o, f, y * fx));
+            }
+            tmem_st16(o_tm + i * 64 + c * 16, r);
+          }
+        }
+        tmem_st_wait();
+        if (first_thread) *node = 0;  // for the next launch
+        have = true;
+        a = min(a, other);
+      }
+      group_sync();  // s.there is free again
+    }
+  }
+  if (holds) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    // A thread has a row; four neighbours exchange 16-byte units, so that
+    // they store 64 bytes of one row at a time (by rows alone, a warp's
+    // store touched 32 lines, 4500 cycles a tile).
+    long long own = -1, off[4];
+    if (mine)
+      own = (long long)(g.first + t * tpt + tok) * p.out.token + (long long)h * p.out.head;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) off[k] = __shfl_sync(0xffffffffu, own, (lane & ~3) + k);
+    const bool odd = lane & 1, upper = lane & 2;
+#pragma unroll 1
+    for (int i = 0; i < ND * 2; ++i) {
+      uint32_t r[32], u[4][4];
+      tmem_ld32_nowait(o_tm + i * 32, r);
+      tmem_ld_wait();
+      loaded16(r);
+      loaded16(r + 16);
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        u[k >> 2][k & 3] = T::pack(__uint_as_float(r[2 * k]) * inv,
+                                   __uint_as_float(r[2 * k + 1]) * inv);
+#pragma unroll
+      for (int k = 0; k < 4; k += 2)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t v = __shfl_xor_sync(0xffffffffu, odd ? u[k][w] : u[k + 1][w], 1);
+          u[k][w] = odd ? v : u[k][w];
+          u[k + 1][w] = odd ? u[k + 1][w] : v;
+        }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t v = __shfl_xor_sync(0xffffffffu, upper ? u[k][w] : u[k + 2][w], 2);
+          u[k][w] = upper ? v : u[k][w];
+          u[k + 2][w] = upper ? u[k + 2][w] : v;
+        }
+      // u[k] is now this lane's unit of row k of the four
+      const int c0 = i * 32 + (lane & 3) * 8;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (off[k] >= 0 && c0 < p.head_dim)
+          *reinterpret_cast<uint4*>(p.out.p + off[k] + c0) =
+              make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
+    }
+    if (mine && p.lse)
+      p.lse[(long long)(g.first + t * tpt + tok) * p.hq + h] =
+          l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+
 // ------------------------------------------------------------------ attention
 template <typename T, int ND, bool GEN, bool BOTH>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap, const AttnParams p, const TcPlan ws) {
+                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ AttnParams p,
+                   const __grid_constant__ TcPieces ws) {
   typedef Smem<ND> S;
   typedef BlockLayout<BOTH> L;
   extern __shared__ uint8_t smem_raw[];
@@ -668,7 +844,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         seq = s.begin.seq;
         index = s.begin.index;
       }
-      Split split = {};
       Entry e;
       Seq r = s.begin.s;
       int head = -1, i = 0;   // head -2: the sequence is to be read, -1: the entry made
@@ -706,8 +881,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             o.seq = e.seq;
             o.cnt[0] = min(o.end, blocks_of_tile0(e, tpt)) - o.n0;
             o.cnt[1] = e.ntok > tpt ? o.end - o.n0 : 0;
-            if (o.n0 == 0 && o.end < e.blocks)  // the first of several pieces
-              split = Split{sh.of(item + units - 1) - (int)blockIdx.x + 1, e.first, e.ntok, o.head};
+            if (o.end - o.n0 < e.blocks) {
+              o.cta0 = sh.of(item + kItemUnits);
+              o.pieces = sh.of(item + units - 1) - o.cta0 + 1;
+            }
             break;
           }
         }
@@ -721,7 +898,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (o.end == 0) break;  // the end of the share, told to all
       }
-      ws.split[blockIdx.x] = split;  // pieces 0: none
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -740,23 +916,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float cap_out = p.sc.softcap * kLog2e;
     uint32_t sph = 0, oph = 0;
     Pieces<ND, true> pieces{s, p.err};
-    while (pieces.next(g)) {
-      const int ntok = min(tpt, g.ntok - t * tpt);        // tokens of this tile
-      if (ntok <= 0) continue;
-      const int cnt = g.cnt[t];
-      const int p_first = g.p0 + t * tpt;
+    while (const Piece* held = pieces.hold()) {
+      const int ntok = min(tpt, held->ntok - t * tpt);    // tokens of this tile
+      if (ntok <= 0) {
+        pieces.release();
+        continue;
+      }
+      const int cnt = held->cnt[t];
+      const int n0 = held->n0, near = held->near, skip = held->skip, prefix = held->prefix;
+      const int p_first = held->p0 + t * tpt;
       const int pos = p_first + tok;
       const int lo_last = p.sc.window ? p_first + ntok - 1 - p.sc.window : -1;
-      const bool mine = tok < ntok;                       // this row exists
-      const int h = g.head * p.group + hg;
-      const float slope = GEN && p.sc.slopes ? p.sc.slopes[h] * kLog2e : 0.0f;
+      const float slope =
+          GEN && p.sc.slopes ? p.sc.slopes[held->head * p.group + hg] * kLog2e : 0.0f;
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
       for (int j = 0; j < cnt; ++j) {
         if (!(ok = warp_wait(&s.s_full[t], sph, p.err))) break;
         sph ^= 1u;
         tc_fence_after();
-        const int kb = key_block(g, g.n0 + j) * kBlk;
+        const int n = n0 + j, kb = (n < near ? n : n + skip) * kBlk;
         float x[kBlk];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -824,11 +1003,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // every row of the tile sees every key of the block, or not
-        const bool whole = (kb + kBlk - 1 <= p_first && kb > lo_last) || kb + kBlk <= g.prefix;
+        const bool whole = (kb + kBlk - 1 <= p_first && kb > lo_last) || kb + kBlk <= prefix;
         if (!whole) {
           // bit i of word w: this row sees key kb + 32 w + i
           const int a = pos - kb + 1, b = p.sc.window ? pos - p.sc.window - kb + 1 : 0;
-          const int pre = g.prefix - kb;
+          const int pre = prefix - kb;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const uint32_t bits = (below(a - 32 * w) & ~below(b - 32 * w)) | below(pre - 32 * w);
@@ -891,88 +1070,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&s.p_full[t]);
       }
       if (!ok) break;
-      const bool split = g.end - g.n0 < g.blocks;
       if (cnt > 0) {
         if (!warp_wait(&s.o_full[t], oph, p.err)) break;
         oph ^= 1u;
         tc_fence_after();
       }
-      if (!split) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        // A thread has a row; four neighbours exchange 16-byte units, so that
-        // they store 64 bytes of one row at a time (by rows alone, a warp's
-        // store touched 32 lines, 4500 cycles a tile).
-        long long own = -1, off[4];
-        if (mine)
-          own = (long long)(g.first + t * tpt + tok) * p.out.token + (long long)h * p.out.head;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) off[k] = __shfl_sync(0xffffffffu, own, (lane & ~3) + k);
-        const bool odd = lane & 1, upper = lane & 2;
-#pragma unroll
-        for (int i = 0; i < ND * 2; ++i) {
-          uint32_t r[32], u[4][4];
-          tmem_ld32_nowait(o_tm + i * 32, r);
-          tmem_ld_wait();
-          loaded16(r);
-          loaded16(r + 16);
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            u[k >> 2][k & 3] = T::pack(__uint_as_float(r[2 * k]) * inv,
-                                       __uint_as_float(r[2 * k + 1]) * inv);
-#pragma unroll
-          for (int k = 0; k < 4; k += 2)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t v = __shfl_xor_sync(0xffffffffu, odd ? u[k][w] : u[k + 1][w], 1);
-              u[k][w] = odd ? v : u[k][w];
-              u[k + 1][w] = odd ? u[k + 1][w] : v;
-            }
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t v = __shfl_xor_sync(0xffffffffu, upper ? u[k][w] : u[k + 2][w], 2);
-              u[k][w] = upper ? v : u[k][w];
-              u[k + 2][w] = upper ? u[k + 2][w] : v;
-            }
-          // u[k] is now this lane's unit of row k of the four
-          const int c0 = i * 32 + (lane & 3) * 8;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (off[k] >= 0 && c0 < p.head_dim)
-              *reinterpret_cast<uint4*>(p.out.p + off[k] + c0) =
-                  make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
-        }
-        if (mine && p.lse)
-          p.lse[(long long)(g.first + t * tpt + tok) * p.hq + h] =
-              l == 0.0f ? -INFINITY : (m * c + log2f(l)) * kLn2;
-      } else {
-        // a piece: slot 1 of the item's first CTA, slot 0 of the others
-        const bool begins = g.n0 == 0;
-        const long long sl = (2LL * blockIdx.x + (begins ? 1 : 0)) * 2 + t;
-        ws.ml[sl * 128 + row] = make_float2(m * c, l);
-        if (cnt > 0) {
-          float4* dst = reinterpret_cast<float4*>(ws.o) + sl * (ND * 16) * 128 + row;
-#pragma unroll
-          for (int i = 0; i < ND * 2; ++i) {
-            uint32_t r[32];
-            tmem_ld32_nowait(o_tm + i * 32, r);
-            tmem_ld_wait();
-            loaded16(r);
-            loaded16(r + 16);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              dst[(i * 8 + k) * 128] =
-                  make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
-                              __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
-          }
-        }
-      }
+      finish_piece<T, ND>(p, ws, s, held, t, o_tm, cnt, m * c, l);
       if (cnt > 0) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.o_empty[t]);
       }
+      pieces.release();
     }
   }
 
@@ -984,59 +1093,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_free(tmem, 512);
   }
-}
-
-// ------------------------------------------------------------------ join
-// 32 rows of a tile of one split item per CTA; a lane is a row, a warp a quarter
-// of its values.
-template <typename T, int ND>
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, const TcPlan w) {
-  wait_prior_launch();
-  let_next_launch();
-  const int c0 = blockIdx.x, t = blockIdx.y >> 2;
-  const Split sp = w.split[c0];
-  const int warp = threadIdx.x >> 5, row = (blockIdx.y & 3) * 32 + (threadIdx.x & 31);
-  const int tpt = tile_tokens(p.group);
-  const int tok = row / p.group, hg = row - tok * p.group;
-  if (sp.pieces == 0 || tok >= min(tpt, sp.ntok - t * tpt)) return;
-  float m = -INFINITY, l = 0.0f;
-  float4 acc[ND * 4];
-#pragma unroll
-  for (int k = 0; k < ND * 4; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-  for (int i = 0; i < sp.pieces; ++i) {
-    const long long slot = (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * 2 + t;
-    const float2 x = w.ml[slot * 128 + row];
-    const float4* src = reinterpret_cast<const float4*>(w.o) + slot * (ND * 16) * 128 + row;
-    float4 v[ND * 4];
-#pragma unroll
-    for (int k = 0; k < ND * 4; ++k) v[k] = src[(k * 4 + warp) * 128];
-    if (x.y == 0.0f) continue;  // saw no key: its sums may not have been written
-    const float m2 = fmaxf(m, x.x);
-    const float a = ex2(m - m2), f = ex2(x.x - m2);
-    m = m2;
-    l = l * a + x.y * f;
-#pragma unroll
-    for (int k = 0; k < ND * 4; ++k) {
-      acc[k].x = acc[k].x * a + v[k].x * f;
-      acc[k].y = acc[k].y * a + v[k].y * f;
-      acc[k].z = acc[k].z * a + v[k].z * f;
-      acc[k].w = acc[k].w * a + v[k].w * f;
-    }
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const long long r = sp.first + t * tpt + tok;
-  const int h = sp.head * p.group + hg;
-  uint16_t* dst = p.out.p + r * p.out.token + (long long)h * p.out.head;
-#pragma unroll
-  for (int k = 0; k < ND * 4; ++k) {
-    const int d = (k * 4 + warp) * 4;
-    if (d < p.head_dim)
-      *reinterpret_cast<uint2*>(dst + d) =
-          make_uint2(T::pack(acc[k].x * inv, acc[k].y * inv), T::pack(acc[k].z * inv, acc[k].w * inv));
-  }
-  if (p.lse && warp == 0)
-    p.lse[r * p.hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <int ND>
@@ -1070,19 +1126,17 @@ cudaError_t setup_nd(int* per_sm) {
 }
 
 template <typename T, int ND, bool BOTH>
-cudaError_t launch_nd(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
+cudaError_t launch_nd(const AttnParams& p, const TcPieces& w, const CUtensorMap& qmap,
                       const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
   // the plain form takes the maximum before it scales
   const bool gen = p.sc.softcap > 0.0f || p.sc.slopes || !(p.sc.scale > 0.0f);
-  cudaError_t e = launch_after(
+  return launch_after(
       gen ? attn_tc_kernel<T, ND, true, BOTH> : attn_tc_kernel<T, ND, false, BOTH>, dim3(grid),
       dim3(kThreads), smem_bytes<ND>(), s, qmap, kmap, vmap, p, w);
-  if (e != cudaSuccess) return e;
-  return launch_after(attn_join_kernel<T, ND>, dim3(grid, 8), dim3(128), 0, s, p, w);
 }
 
 template <typename T>
-cudaError_t launch_t(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
+cudaError_t launch_t(const AttnParams& p, const TcPieces& w, const CUtensorMap& qmap,
                      const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
   if (p.head_dim <= 64) return launch_nd<T, 1, false>(p, w, qmap, kmap, vmap, grid, s);
   return p.boxes.both ? launch_nd<T, 2, true>(p, w, qmap, kmap, vmap, grid, s)
@@ -1102,7 +1156,7 @@ cudaError_t attn_tc_setup(int* ctas_per_sm) {
   return setup_nd<Fp16, 2, true>(ctas_per_sm);
 }
 
-cudaError_t launch_attn_tc(const AttnParams& p, const TcPlan& w, const CUtensorMap& qmap,
+cudaError_t launch_attn_tc(const AttnParams& p, const TcPieces& w, const CUtensorMap& qmap,
                            const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, int grid,
                            cudaStream_t s) {
   return dtype == MOE_ATTN_BF16 ? launch_t<Bf16>(p, w, qmap, kmap, vmap, grid, s)
