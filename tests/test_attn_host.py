@@ -139,6 +139,19 @@ def test_frequencies():
         assert e.value.status == -1
 
 
+def test_tensors_of_the_host_are_refused(L):
+    import torch
+    freq = moe.moe_attn_rope_frequencies(8, device="cpu")[0]
+    x, pos = torch.zeros(2, 3, 8, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    for args in [(x, pos, freq), (x.float(), pos, freq), (x[0], pos, freq)]:
+        with pytest.raises(ValueError):
+            moe.moe_attn_rope(*args)
+    with pytest.raises(ValueError):
+        moe.moe_attn_rope(x, pos, freq, layout="other")
+    with pytest.raises(AttributeError):
+        moe.moe_attn_rope(None, pos, freq)
+
+
 def test_cache_bookkeeping():
     c = moe.PagedKvCache(5, 2, 16, 64, device="cpu")
     assert c.k_pages.shape == c.v_pages.shape == (5, 2, 16, 64)

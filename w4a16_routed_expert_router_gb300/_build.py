@@ -1,8 +1,9 @@
-"""Build the sm_103a shared library ``libmoe_w4a16.so`` in-tree with nvcc.
+"""Build the sm_103a shared library ``libmoe_w4a16.so`` in-tree with nvcc, and
+the attention operators' Python binding ``_attn_binding.so``.
 
 Each ``csrc/*.cu`` is compiled to an object in parallel, then linked into one
-shared library next to this file. Rebuilds only when a source is newer than
-the library.
+shared library next to this file; ``csrc/binding.c`` is host code. Rebuilds only
+when a source is newer than the libraries.
 
     python -m w4a16_routed_expert_router_gb300._build [--force] [--verbose]
 """
@@ -14,12 +15,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_w4a16.so")
+BINDING_SRC = os.path.join(CSRC, "binding.c")
+BINDING = os.path.join(PKG, "_attn_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -38,10 +42,10 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    deps = [BINDING_SRC] + sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     deps += glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -63,8 +67,20 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{res.stderr}")
         return obj, res.stderr
 
+    def compile_binding():
+        tmp = BINDING + ".tmp"
+        cmd = [cc, "-O2", "-cudart", "none", "-shared", "-Xcompiler", "-fPIC",
+               "-I" + sysconfig.get_paths()["include"], BINDING_SRC, "-o", tmp]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"building {BINDING_SRC} failed (it needs the Python headers):\n"
+                               f"{res.stderr}")
+        os.replace(tmp, BINDING)
+
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(compile_binding)
         results = list(ex.map(compile_one, sources()))
+        binding.result()
     for _, log in results:
         if verbose and log:
             sys.stderr.write(log)

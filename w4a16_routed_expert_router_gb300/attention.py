@@ -94,25 +94,26 @@ def register(L: ctypes.CDLL) -> None:
         fn.restype = ctypes.c_int
 
 
-def _by_address(L: ctypes.CDLL, name: str):
-    """The function with its structures passed as plain addresses (half the cost
-    of the pointers that ctypes makes of them)."""
-    fn = L[name]  # a function object of its own
-    fn.argtypes = [_vp if issubclass(a, ctypes._Pointer) else a for a in _signatures()[name]]
-    fn.restype = ctypes.c_int
-    return fn
-
-
 _library = None
+_native = None  # csrc/binding.c: checks tensors, calls the library
 
 
 def _lib() -> ctypes.CDLL:
-    global _library
+    global _library, _native
     if _library is None:
         from . import lib
         L = lib()
         register(L)
-        _library = L
+        from . import _attn_binding
+
+        def address(name):
+            return ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+
+        _attn_binding.setup(address("moe_attn_rope"), address("moe_attn_append"),
+                            address("moe_attn_forward"), _check, torch.empty, _raw_stream,
+                            _current_device, torch.bfloat16, torch.float16,
+                            torch.float32, torch.int32, torch.int64)
+        _native, _library = _attn_binding, L
     return _library
 
 
@@ -122,74 +123,33 @@ def _check(status: int, what: str) -> None:
         raise MoeError(status, what)
 
 
-# the current stream's address without the Stream object around it (2 us a call)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+def _stream_address(index) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
 
 
-def _stream(stream, device) -> int:
-    if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(device.index)
-        return torch.cuda.current_stream(device).cuda_stream
-    return stream if isinstance(stream, int) else stream.cuda_stream
+# the current stream's address and the current device without the objects and
+# checks around them (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_address)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _fill_rows(s, t, heads, dim, dtype, index, what):
-    """Describe t [tokens, heads, dim] on device `index` in s; returns its tokens."""
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-        raise ValueError(f"{what} must be [tokens, {heads}, {dim}], got {list(shape)}")
-    if t.dtype is not dtype or t.get_device() != index:
-        raise ValueError(f"{what} must be {dtype} on cuda:{index}, got {t.dtype} on {t.device}")
-    token, head, last = t.stride()
-    if last != 1 and dim > 1:
-        raise ValueError(f"{what} must be contiguous along head_dim")
-    s.data = t.data_ptr()
-    # the stride of a dimension of one element says nothing
-    s.head_stride = head if heads > 1 else dim
-    tokens = shape[0]
-    s.token_stride = token if tokens > 1 else heads * s.head_stride
-    return tokens
-
-
-def _new_rows(s, tokens, heads, dim, dtype, device, stream):
-    """A new tensor [tokens, heads, dim], described in s."""
-    t = _empty((tokens, heads, dim), dtype, device, stream)
-    s.data = t.data_ptr()
-    s.head_stride = dim
-    s.token_stride = heads * dim
-    return t
-
-
-def _vector(t, n, dtype, index, what):
-    """Address of t, a contiguous vector of n elements on device `index`."""
-    if (t.dtype is not dtype or t.get_device() != index or t.dim() != 1 or t.numel() != n or
-            not t.is_contiguous()):
-        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} on cuda:{index}, got "
-                         f"{t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _empty(shape, dtype, device, stream):
-    """New tensor for a call on `stream`: owned by that stream, where one is given."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if isinstance(stream, int):
-        raise ValueError("an output is needed where the stream is a raw address")
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _fill_rotation(s, freq, layout, magnitude, inverse, index):
+def _layout(layout) -> int:
     code = _LAYOUTS.get(layout)
     if code is None:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
-    n = freq.numel()
-    s.freq = _vector(freq, n, torch.int64, index, "freq")
-    s.rot_dim = 2 * n
-    s.layout = code
-    s.magnitude = magnitude
-    s.inverse = 1 if inverse else 0
+    return code
+
+
+def _on_stream(stream, out, shape, dtype, device):
+    """(address of a given stream, output for a call on it: new ones belong to it)."""
+    if isinstance(stream, int):
+        if out is None:
+            raise ValueError("an output is needed where the stream is a raw address")
+        return stream, out
+    if out is None:
+        with torch.cuda.stream(stream):
+            out = torch.empty(shape, dtype=dtype, device=device)
+    return stream.cuda_stream, out
 
 
 def moe_attn_rope_frequencies(rot_dim, base=10000.0, factor=1.0, by_parts=False,
@@ -214,29 +174,16 @@ def moe_attn_rope(x, positions, freq, out=None, layout="half", magnitude=1.0, in
     """Rotary positions of x [tokens, heads, head_dim] (bf16 or fp16, any token
     and head strides) at positions int32 [tokens]; out may be x. ``inverse``
     turns the other way: the gradient of x from the gradient of the result."""
-    dtype, device = x.dtype, x.device
-    code = _DTYPES.get(dtype)
-    if code is None or device.type != "cuda" or x.dim() != 3:
-        raise ValueError("x must be a bf16 or fp16 CUDA tensor [tokens, heads, head_dim]")
-    index = device.index
-    tokens, heads, dim = x.shape
-    xs, os, rot = moe_attn_rows(), moe_attn_rows(), moe_attn_rotation()
-    _fill_rows(xs, x, heads, dim, dtype, index, "x")
-    if out is None:
-        out = _new_rows(os, tokens, heads, dim, dtype, device, stream)
-    elif _fill_rows(os, out, heads, dim, dtype, index, "out") != tokens:
-        raise ValueError("x and out differ in tokens")
-    _fill_rotation(rot, freq, layout, magnitude, inverse, index)
-    args = (xs, os, _vector(positions, tokens, torch.int32, index, "positions"), tokens, heads,
-            dim, code, rot, _stream(stream, device))
-    if torch.cuda.current_device() == index:
-        st = _lib().moe_attn_rope(*args)
-    else:
-        with torch.cuda.device(device):
-            st = _lib().moe_attn_rope(*args)
-    if st:
-        _check(st, "moe_attn_rope")
-    return out
+    if _native is None:
+        _lib()
+    if stream is not None:
+        stream, out = _on_stream(stream, out, x.shape, x.dtype, x.device)
+    args = (x, positions, freq, out, _layout(layout), magnitude, inverse, stream)
+    done = _native.rope(*args)
+    if done is NotImplemented:  # another device is current
+        with torch.cuda.device(x.device):
+            done = _native.rope(*args)
+    return done
 
 
 class PagedAttention:
@@ -264,23 +211,18 @@ class PagedAttention:
         _check(self._library.moe_attn_create(ctypes.byref(self.cfg), index, ctypes.byref(handle)),
                "moe_attn_create")
         self.handle = handle
-        # filled anew by every call, and passed by their addresses
-        self._q, self._o = moe_attn_rows(), moe_attn_rows()
-        self._k, self._v = moe_attn_rows(), moe_attn_rows()
-        self._rot, self._cache = moe_attn_rotation(), moe_attn_cache()
-        self._batch, self._scores = moe_attn_batch(), moe_attn_scores()
-        at = ctypes.addressof
-        self._at_q, self._at_o, self._at_k, self._at_v = (at(self._q), at(self._o), at(self._k),
-                                                          at(self._v))
-        self._at_rot, self._at_cache = at(self._rot), at(self._cache)
-        self._at_batch, self._at_scores = at(self._batch), at(self._scores)
-        self._append = _by_address(self._library, "moe_attn_append")
-        self._forward = _by_address(self._library, "moe_attn_forward")
+        self._layer = _native.layer(handle.value, q_heads, kv_heads, head_dim, page_size, index,
+                                    dtype, self.device)
 
     def close(self):
         if self.handle is not None and self.handle.value:
             _check(self._library.moe_attn_destroy(self.handle), "moe_attn_destroy")
         self.handle = None
+
+    def _open(self):
+        if self.handle is None:
+            raise RuntimeError("this layer has been closed")
+        return self._layer
 
     def __del__(self):
         try:
@@ -302,59 +244,19 @@ class PagedAttention:
             _check(st, "moe_attn_check_device_errors")
         return flags.value
 
-    def _fill_cache(self, k_pages, v_pages):
-        c, index = self._cache, self.device.index
-        shape, strides = k_pages.shape, k_pages.stride()
-        if (len(shape) != 4 or shape[1] != self.kv_heads or shape[2] != self.page_size or
-                shape[3] != self.head_dim):
-            raise ValueError(f"k_pages must be [pages, {self.kv_heads}, {self.page_size}, "
-                             f"{self.head_dim}], got {list(shape)}")
-        if v_pages.shape != shape or v_pages.stride() != strides or strides[3] != 1:
-            raise ValueError("k_pages and v_pages must have one shape and strides, head_dim "
-                             "contiguous")
-        dtype = self.dtype
-        if (k_pages.dtype is not dtype or v_pages.dtype is not dtype or
-                k_pages.get_device() != index or v_pages.get_device() != index):
-            raise ValueError(f"the cache must be {dtype} on {self.device}")
-        c.k, c.v = k_pages.data_ptr(), v_pages.data_ptr()
-        c.num_pages = pages = shape[0]
-        c.token_stride = strides[2]
-        # the stride of a dimension of one element says nothing
-        c.head_stride = strides[1] if self.kv_heads > 1 else self.head_dim
-        c.page_stride = (strides[0] if pages > 1 else
-                         self.page_size * self.kv_heads * self.head_dim)
-
     def append(self, q, k, v, positions, slots, k_pages, v_pages, freq, layout="half",
                magnitude=1.0, q_out=None, stream=None):
         """Turn q and k [tokens, heads, head_dim] to their positions (int32) and
         write k and v to their slots (int64; page * page_size + offset, negative:
         not written) of the cache. Returns q_out (new unless given, may be q);
         q None: keys and values only."""
-        device, dtype, dim = self.device, self.dtype, self.head_dim
-        index = device.index
-        T = _fill_rows(self._k, k, self.kv_heads, dim, dtype, index, "k")
-        if _fill_rows(self._v, v, self.kv_heads, dim, dtype, index, "v") != T:
-            raise ValueError("k and v differ in tokens")
-        at_q = at_o = None
-        if q is not None:
-            at_q, at_o = self._at_q, self._at_o
-            if _fill_rows(self._q, q, self.q_heads, dim, dtype, index, "q") != T:
-                raise ValueError("q and k differ in tokens")
-            if q_out is None:
-                q_out = _new_rows(self._o, T, self.q_heads, dim, dtype, device, stream)
-            elif _fill_rows(self._o, q_out, self.q_heads, dim, dtype, index, "q_out") != T:
-                raise ValueError("q_out and q differ in tokens")
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        _fill_rotation(self._rot, freq, layout, magnitude, False, index)
-        self._fill_cache(k_pages, v_pages)
-        st = self._append(self.handle, at_q, at_o, self._at_k, self._at_v,
-                          _vector(positions, T, torch.int32, index, "positions"),
-                          _vector(slots, T, torch.int64, index, "slots"), T, self._at_rot,
-                          self._at_cache, _stream(stream, device))
-        if st:
-            _check(st, "moe_attn_append")
-        return q_out
+        if stream is not None:
+            if q is not None:
+                stream, q_out = _on_stream(stream, q_out, q.shape, self.dtype, self.device)
+            elif not isinstance(stream, int):
+                stream = stream.cuda_stream
+        return _native.append(self._open(), q, k, v, positions, slots, k_pages, v_pages, freq,
+                              _layout(layout), magnitude, q_out, stream)
 
     def forward(self, q, k_pages, v_pages, page_table, cu_q, kv_len, max_q, scale=None,
                 softcap=0.0, window=0, slopes=None, prefix=None, out=None, lse=None,
@@ -367,48 +269,13 @@ class PagedAttention:
         no sequence has more new tokens. scale defaults to 1 / sqrt(head_dim).
         Returns out, or (out, lse) with lse fp32 [tokens, q_heads].
         """
-        device, dim = self.device, self.head_dim
-        index = device.index
-        T = _fill_rows(self._q, q, self.q_heads, dim, self.dtype, index, "q")
-        if out is None:
-            out = _new_rows(self._o, T, self.q_heads, dim, self.dtype, device, stream)
-        elif _fill_rows(self._o, out, self.q_heads, dim, self.dtype, index, "out") != T:
-            raise ValueError("q and out differ in tokens")
-        b, s = self._batch, self._scores
-        table = page_table.shape
-        n = kv_len.numel()
-        if (len(table) != 2 or table[0] != n or page_table.dtype is not torch.int32 or
-                page_table.get_device() != index or
-                (page_table.stride(1) != 1 and table[1] > 1)):
-            raise ValueError(f"page_table must be int32 [{n}, columns] on {device}, contiguous "
-                             "along the columns")
-        b.cu_q = _vector(cu_q, n + 1, torch.int32, index, "cu_q")
-        b.kv_len = _vector(kv_len, n, torch.int32, index, "kv_len")
-        b.page_table = page_table.data_ptr()
-        b.columns = columns = table[1]
-        b.table_stride = page_table.stride(0) if n > 1 else columns
-        b.num_seqs, b.num_tokens, b.max_q = n, T, max_q
-        s.scale = dim ** -0.5 if scale is None else scale
-        s.softcap, s.window = softcap, window
-        s.slopes = None if slopes is None else _vector(slopes, self.q_heads, torch.float32, index,
-                                                       "slopes")
-        s.prefix = None if prefix is None else _vector(prefix, n, torch.int32, index, "prefix")
-        at_lse = None
-        if lse is not None:
-            if (lse.dtype is not torch.float32 or tuple(lse.shape) != (T, self.q_heads) or
-                    not lse.is_contiguous() or lse.get_device() != index):
-                raise ValueError(f"lse must be contiguous float32 [{T}, {self.q_heads}] on "
-                                 f"{device}")
-            at_lse = lse.data_ptr()
-        elif return_lse:
-            lse = _empty((T, self.q_heads), torch.float32, device, stream)
-            at_lse = lse.data_ptr()
-        self._fill_cache(k_pages, v_pages)
-        st = self._forward(self.handle, self._at_q, self._at_o, at_lse, self._at_cache,
-                           self._at_batch, self._at_scores, _stream(stream, device))
-        if st:
-            _check(st, "moe_attn_forward")
-        return (out, lse) if return_lse else out
+        if stream is not None:
+            if return_lse and lse is None:
+                _, lse = _on_stream(stream, None, q.shape[:2], torch.float32, self.device)
+            stream, out = _on_stream(stream, out, q.shape, self.dtype, self.device)
+        return _native.forward(self._open(), q, k_pages, v_pages, page_table, cu_q, kv_len, max_q,
+                               scale, softcap, window, slopes, prefix, out, lse, return_lse,
+                               stream)
 
 
 class PagedKvCache:
