@@ -282,6 +282,25 @@ def test_runs_are_identical_and_handles_are_reused():
         assert torch.equal(o2, out) and torch.equal(l2, lse)
 
 
+@pytest.mark.parametrize("kw", [dict(softcap=30.0), dict(softcap=3.0, window=40), dict(slopes=True),
+                                dict(prefix=[70] * 40)])
+def test_what_does_not_exist_changes_nothing(kw):
+    # rows behind a tile's tokens and keys behind a sequence's end hold what was
+    # there before: runs after other work repeat bit by bit
+    shape = (15, 5, 40, 64, BF)
+    lens = [(1 + 7 * i % 90, 1 + 37 * i % 200) for i in range(40)]
+    b = ac.Batch(lens, *shape, **kw)
+    layer = _layer(b, shape, tokens=4000)
+    out, lse = b.run(layer)
+    b.check(out, lse)
+    others = [ac.Batch([(300, 700), (90, 90), (200, 10)], *shape, seed=i) for i in (1, 2)]
+    for i in range(6):
+        others[i % 2].q.mul_(1 + i)
+        others[i % 2].run(layer)
+        o2, l2 = b.run(layer)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+
 @pytest.mark.parametrize("d,page", [(128, 64), (64, 16)])
 def test_many_blocks_per_processor(d, page):
     # some 60 blocks of keys for every SM: each ring of stages goes round many

@@ -937,11 +937,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int cnt = held->cnt[t];
       const int n0 = held->n0, near = held->near, skip = held->skip, prefix = held->prefix;
+      const int kv = held->kv;
       const int p_first = held->p0 + t * tpt;
       const int pos = p_first + tok;
       const int lo_last = p.sc.window ? p_first + ntok - 1 - p.sc.window : -1;
       const float slope =
           GEN && p.sc.slopes ? p.sc.slopes[held->head * p.group + hg] * kLog2e : 0.0f;
+      const bool mine = tok < ntok;                       // this row exists
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
       for (int j = 0; j < cnt; ++j) {
@@ -956,18 +958,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; ++i) loaded16(reinterpret_cast<uint32_t*>(x) + i * 16);
+        // every row of the tile sees every key of the block, or not
+        const bool whole = (kb + kBlk - 1 <= p_first && kb > lo_last) || kb + kBlk <= prefix;
         if (GEN) {
           if (p.sc.softcap > 0.0f) {
             // cap tanh(x scale / cap) in log2 units. While every |x| scale / cap of
             // the warp's rows is below kTanhMax, it is x times a polynomial in x^2
             // (the factors go into its coefficients; up to 1000, so that their
             // powers stay finite), two keys to an instruction; else 1 - 2 / (1 +
-            // e^2y).
+            // e^2y). Rows and keys that do not exist have no part in the choice: the
+            // block with the last key takes the second form.
             float top = fabsf(x[0]);
 #pragma unroll
             for (int i = 1; i < kBlk - 1; i += 2) top = max3(top, fabsf(x[i]), fabsf(x[i + 1]));
             top = fmaxf(top, fabsf(x[kBlk - 1]));
-            if (__all_sync(0xffffffffu, top * fabsf(cap_in) < kTanhMax) && fabsf(cap_in) < 1e3f) {
+            if (kb + kBlk <= kv && fabsf(cap_in) < 1e3f &&
+                __all_sync(0xffffffffu, !mine || top * fabsf(cap_in) < kTanhMax)) {
               float f[6], power = cap_in * cap_out;
 #pragma unroll
               for (int k = 0; k < 6; ++k) {
@@ -1015,8 +1021,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // every row of the tile sees every key of the block, or not
-        const bool whole = (kb + kBlk - 1 <= p_first && kb > lo_last) || kb + kBlk <= prefix;
         if (!whole) {
           // bit i of word w: this row sees key kb + 32 w + i
           const int a = pos - kb + 1, b = p.sc.window ? pos - p.sc.window - kb + 1 : 0;
