@@ -95,6 +95,7 @@ def test_rope_refusals(L):
     assert call(T=0) == 0 and call(heads=0) == 0
     assert call(T=-1) == -1 and call(heads=-1) == -1 and call(dtype=2) == -1
     assert call(dim=0) == -2 and call(dim=257) == -2 and call(dim=62) == -2
+    assert call(heads=65537) == -2
     assert call(rot=None) == -1 and call(x=None) == -1 and call(pos=None) == -1
     assert call(x=odd) == -4
     for bad in (at.moe_attn_rotation(8, 63, 0, 1.0, 0), at.moe_attn_rotation(8, -2, 0, 1.0, 0)):

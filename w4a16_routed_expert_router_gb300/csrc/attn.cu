@@ -275,7 +275,7 @@ int moe_attn_rope(const moe_attn_rows* x, const moe_attn_rows* out, const int32_
                   int32_t T, int32_t heads, int32_t head_dim, int32_t dtype,
                   const moe_attn_rotation* r, void* stream) {
   if (T < 0 || heads < 0) return MOE_ATTN_ERR_INVALID_ARG;
-  if (head_dim < 1 || head_dim > 256) return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  if (head_dim < 1 || head_dim > 256 || heads > 65536) return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
   if (dtype != MOE_ATTN_BF16 && dtype != MOE_ATTN_FP16) return MOE_ATTN_ERR_INVALID_ARG;
   int st = validate_rotation(r, head_dim);
   if (st != MOE_ATTN_OK) return st;

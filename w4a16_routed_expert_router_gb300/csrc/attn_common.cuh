@@ -19,6 +19,24 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// tc::bwait for what another role of the CTA does only once a piece of its work,
+// which may take seconds over hundreds of millions of keys; the waits inside a
+// piece keep the short limit.
+__device__ __forceinline__ bool bwait_piece(uint64_t* bar, uint32_t parity, unsigned* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if ((i & 15u) == 0) {
+      if (tc::aborted(err)) return false;
+      if (global_ns() - t0 > 30 * kWaitLimitNs) {
+        atomicOr(err, kErrTimeout);
+        return false;
+      }
+    }
+  }
+}
+
 // Waits until the launch before this one is complete and its writes are visible.
 __device__ __forceinline__ void wait_prior_launch() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

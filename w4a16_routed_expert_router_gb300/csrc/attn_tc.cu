@@ -263,8 +263,8 @@ struct Pieces {
   uint32_t ph = 0;
   // the next piece, or null at the end of the share or after a timeout
   __device__ __forceinline__ const Piece* hold() {
-    if (!(kWarp ? warp_wait(&s.piece_full[i], ph, err) : bwait(&s.piece_full[i], ph, err)))
-      return nullptr;
+    const bool there = bwait_piece(&s.piece_full[i], ph, err);
+    if (!(kWarp ? __all_sync(0xffffffffu, there) : there)) return nullptr;
     const Piece* g = reinterpret_cast<const Piece*>(s.piece[i]);
     return g->end > 0 ? g : nullptr;
   }
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ids = fetch(g.n0);
         // Q: tile t's tokens by the group's heads
         if (lane == 0) {
-          ok = bwait(&s.q_empty, qph ^ 1u, p.err);
+          ok = bwait_piece(&s.q_empty, qph ^ 1u, p.err);
           if (ok) {
             const int tiles = g.ntok > tpt ? 2 : 1;
             mbar_arrive_expect_tx(&s.q_full, tiles * ND * tpt * p.group * 128);
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           slot = (slot + 2) % S::kSlots;
           const int left = g.kv - key_block(g, n) * kBlk;
           if (left >= kBlk) continue;
-          if (!(ok = warp_wait(&s.clear, cph, p.err))) break;
+          if (!(ok = __all_sync(0xffffffffu, bwait_piece(&s.clear, cph, p.err)))) break;
           cph ^= 1u;
           const uint32_t v = smem_u32(s.kv[vslot]);
           const int from = max(left, 0);
@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
         }
-        ok = bwait(&s.piece_empty[i], ph ^ 1u, p.err);
+        ok = bwait_piece(&s.piece_empty[i], ph ^ 1u, p.err);
         if (!ok) break;
         *reinterpret_cast<Piece*>(s.piece[i]) = o;
         mbar_arrive(&s.piece_full[i]);
