@@ -316,6 +316,54 @@ def test_many_blocks_per_processor(d, page):
     assert layer.check_device_errors() == 0
 
 
+@pytest.mark.parametrize("hq,hk,d,page,lens,kw", [
+    (8, 8, 64, 64, [(1500, 30000)], dict()),
+    (32, 8, 128, 16, [(300, 65536), (1, 40000)], dict()),
+    (16, 4, 96, 32, [(200, 50000), (64, 33333), (130, 60001)], dict(softcap=20.0)),
+    (8, 8, 64, 128, [(700, 40000), (700, 40000)], dict(window=20000)),
+    (4, 1, 128, 64, [(40, 300000), (200, 200000)], dict()),
+])
+def test_long_caches_against_single_tokens(hq, hk, d, page, lens, kw):
+    # few items over many keys: their cuts and joins, against every query as a
+    # sequence of its own (the few-token kernel), both within the bound of
+    # attn_cases.py of the definition, with A from a run on |V|
+    g = torch.Generator(device=DEV).manual_seed(7)
+    used = [-(-kv // page) for _, kv in lens]
+    shape = (sum(used), hk, page, d)
+    kp = torch.randn(shape, generator=g, device=DEV).to(BF)
+    vp = torch.randn(shape, generator=g, device=DEV).to(BF)
+    n, kv = [a for a, _ in lens], [b for _, b in lens]
+    T = sum(n)
+    q = torch.randn(T, hq, d, generator=g, device=DEV).to(BF)
+    order = torch.randperm(sum(used), generator=g, device=DEV).to(torch.int32)
+    table = torch.zeros(len(lens), max(used), dtype=torch.int32, device=DEV)
+    for s, (u, part) in enumerate(zip(used, order.split(used))):
+        table[s, :u] = part
+    i32 = dict(dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0] + n).cumsum(0).to(**i32)
+    layer = moe.PagedAttention(hq, hk, d, page, T, max(T, 1))
+    out, lse = layer.forward(q, kp, vp, table, cu, torch.tensor(kv, **i32), max(n),
+                             return_lse=True, **kw)
+    rows = torch.cat([torch.full((a,), s) for s, a in enumerate(n)]).to(DEV)
+    ends = torch.cat([torch.arange(b - a + 1, b + 1) for a, b in lens]).to(**i32)
+    each = dict(page_table=table[rows], cu_q=torch.arange(T + 1, **i32), kv_len=ends, max_q=1)
+    one, lse1 = layer.forward(q, kp, vp, return_lse=True, **each, **kw)
+    a = layer.forward(q, kp, vp.abs(), **each, **kw).double()
+    u = ac.ROUND[BF]
+    bound = 2 * (u * one.double().abs() + (u + 1e-4) * a * (1 + 2 * u)) + 2.0 ** -23
+    diff = out.double() - one.double()
+    assert bool((diff.abs() <= bound).all())
+    # of independent values, with numerators and outputs rounded once in either
+    # run, the whole differs by at most sqrt(4 u^2 / 3) of its norm, here 2 u
+    assert float(diff.norm() / one.double().norm()) <= 2 * u
+    assert bool(((lse - lse1).abs() <= 2e-4 + 2.0 ** -21 * lse1.abs()).all())
+    for _ in range(3):
+        o2, l2 = layer.forward(q, kp, vp, table, cu, torch.tensor(kv, **i32), max(n),
+                               return_lse=True, **kw)
+        assert torch.equal(o2, out) and torch.equal(l2, lse)
+    assert layer.check_device_errors() == 0
+
+
 def test_graph_replays_with_new_lengths():
     shape = (8, 2, 128, 16, BF)
     lens = [[(1, 400), (120, 300), (1, 9)], [(1, 33), (120, 128), (1, 390)]]
