@@ -127,7 +127,7 @@ Layout plan(const moe_attn_config& c) {
       kMaxGrid * 4,                             // 1 decode: pieces that arrived
       kMaxGrid * 2 * kDecodeRows * 8,           // 2 decode: maximum, sum
       kMaxGrid * 2 * kDecodeRows * d * 4,       // 3 decode: weighted sums
-      kMaxGrid * 2 * 4,                         // 4 tensor cores: halves that arrived
+      kMaxGrid * 4 * 4,                         // 4 tensor cores: halves that arrived
       kMaxGrid * 4 * 128 * 8,                   // 5 maximum, sum
       kMaxGrid * 4 * 128 * d * 4,               // 6 weighted sums
   };

@@ -208,7 +208,7 @@ struct Entry {
 
 // What pieces of items leave for each other.
 struct TcPieces {
-  unsigned* count;  // [kMaxGrid][2 tiles] halves of a pair that arrived (self-resetting)
+  unsigned* count;  // [kMaxGrid][2][2 tiles] halves of a pair that arrived (self-resetting)
   float* o;         // [kMaxGrid][2 pieces][2 tiles][dim / 4][128 rows][4]
   float2* ml;       // [kMaxGrid][2][2][128] maximum (log2 units), sum
 };

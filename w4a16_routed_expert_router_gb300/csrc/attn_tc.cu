@@ -4,10 +4,11 @@
 // One persistent CTA per SM over an equal share of all key blocks of all items,
 // an item being up to two tiles of query tokens of one sequence (an entry) and a
 // kv head. Equal shares keep every SM busy to the end under a causal mask, ragged
-// lengths or a single chunk over a long cache. The pieces of an item that more
-// than one CTA holds are joined by pairs, by whichever of the two comes second
-// (which has its own piece in TMEM still), in an order that does not depend on
-// who that is. (A launch of its own that added them took 8 to 15 us.)
+// lengths or a single chunk over a long cache; few items over many keys are cut in
+// step (kCutShare). The pieces of an item that more than one CTA holds are joined
+// by pairs, by whichever of the two comes second (which has its own piece in TMEM
+// still), in an order that does not depend on who that is. (A launch of its own
+// that added them took 8 to 15 us.)
 //
 // One item: two tiles of 128 query rows (token, head of the group)
 // against blocks of 128 keys, S = Q K^T and O += P V with tcgen05.mma; S and O
@@ -46,6 +47,17 @@ constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "setmaxnreg draws on the launch");
 constexpr int kBlk = kTcBlock;
 constexpr int kChunk = 128 * 128;   // 128 rows of 64 values
+// Where items are no more than CTAs and shares no smaller than kCutShare units,
+// items are cut from their first key on, a share a CTA: the CTAs of a kv head then
+// read the same keys at the same time, and its cache comes from DRAM about once
+// and not for each of them. 1000 tokens over 65536 keys: 2.69 -> 0.38 GB read, and
+// with the power that saves 786 -> 695 us back to back; 700 over 32768: 262 -> 249;
+// over 16384 keys, which L2 holds, no change; 1000 over 8192 cut as well (12 units):
+// 96.6 -> 98.2. Bounded by their softmax, capped scores lost (1178 -> 1199 us), as
+// did biased ones (980 -> 1043) and head sizes up to 64 (511 -> 514): not cut.
+// What is left of the items makes the remaining shares; kRestUnits is its
+// fixed cost there.
+constexpr int kCutShare = 64, kRestUnits = 5;
 // An item's fixed cost, in blocks (prefill of 8192 tokens: 2 -> 405 us, 4 -> 399,
 // 5 -> 402; 16 prompts of 1024: 196, 206, 203; without it 902 and 387 before the
 // cost itself was cut).
@@ -66,15 +78,19 @@ struct alignas(16) Seq {
   int first, n, kv, prefix;
 };
 
-// Where a CTA's share begins: entry `index` of sequence `seq`, whose first unit
-// is number `at` of all.
-struct Begin {
-  long long at;
+// A CTA's share: units [at, hi) of the list of items, from entry `index` of
+// sequence `seq` on, whose first unit is number `entry_at`. With `cut`, items are
+// first cut into chunks of `per` units, the first `cuts` CTAs have one chunk each,
+// and the list is of what is left of the items; `cut_at` is the number of the
+// entry's first chunk.
+struct Share {
+  long long per, at, hi, entry_at;
   Seq s;
   int seq, index;
+  int cut, cuts, cut_at;
 };
 
-constexpr int kPieceBytes = 64, kPieces = 4;  // pieces handed out ahead
+constexpr int kPieceBytes = 80, kPieces = 4;  // pieces handed out ahead
 
 template <int ND>
 struct Smem {
@@ -84,7 +100,7 @@ struct Smem {
   uint8_t piece[kPieces][kPieceBytes];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   Scan scan;
-  Begin begin;
+  Share share;
   unsigned there[2];
   uint64_t kv_full[kSlots], kv_empty[kSlots];
   uint64_t q_full, q_empty;
@@ -250,7 +266,11 @@ struct alignas(16) Piece {
   int near, skip, blocks, prefix;
   int head, n0, end, seq;
   int cnt[2];                       // blocks of the piece that tile 0 / 1 takes
-  int cta0, pieces;                 // of a split item: CTA of its first piece, pieces; or 0, 0
+  // of a split item: pieces (0: it is whole), number of this one; the first
+  // `chunks` of them on CTAs from `chunk0` on, the others on those from cta0 on
+  // (both from cta0 where there are no chunks)
+  int pieces, number, chunks, chunk0, cta0;
+  int pad;
 };
 static_assert(sizeof(Piece) == kPieceBytes, "shared memory of a piece");
 
@@ -350,14 +370,17 @@ __device__ __forceinline__ long long cta_scan(Scan& sc, long long mine, long lon
   return before;
 }
 
+// units on the list of what cutting leaves of an item
+__device__ __forceinline__ int rest_of(int units) { return units ? units + kRestUnits : 0; }
+
 // Every CTA divides the work for itself (a launch that did it once took longer):
 // the entries of all sequences, a run of sequences a thread, then their units, a
 // run of entries a thread. `room` is shared memory for a number per sequence and
-// one more, and for the sequences themselves while they are few. Returns all
-// units.
+// one more, and for the sequences themselves while they are few.
 constexpr int kSeqsKept = 4096;
-__device__ __forceinline__ long long divide(const AttnParams& p, Scan& sc, uint8_t* room,
-                                            Begin& begin, int tpt) {
+template <bool CUT>
+__device__ __forceinline__ void divide(const AttnParams& p, Scan& sc, uint8_t* room, Share& share,
+                                       int tpt) {
   const int tid = threadIdx.x, seqs = p.b.num_seqs;
   Seq* kept = reinterpret_cast<Seq*>(room);
   int* first = reinterpret_cast<int*>(room + (seqs <= kSeqsKept ? seqs * sizeof(Seq) : 0));
@@ -399,22 +422,40 @@ __device__ __forceinline__ long long divide(const AttnParams& p, Scan& sc, uint8
     while (first[q + 1] <= e) ++q;
     sum += units(q, e);
   }
+  if (tid == 0) share.at = share.hi = 0;  // nothing, unless a thread below finds more
   at = cta_scan(sc, sum, total);
   const Shares sh(total, gridDim.x);
-  const long long lo = sh.begin(blockIdx.x);
+  const int cta = blockIdx.x;
+  if (CUT && n * p.hk <= gridDim.x && sh.per >= kCutShare) {  // at most one entry a thread
+    const Shares cut(total + n * p.hk * kRestUnits, gridDim.x);
+    const int per = (int)cut.per;  // at least one item's units in all: int
+    const int u = e0 < e1 ? (int)quotient(sum, p.hk) : 0;
+    const int chunks = u / per, rest = u - chunks * per;
+    const long long mine2 = (long long)rest_of(rest) * p.hk;
+    long long both;  // chunks in the low bits, no more than CTAs
+    const long long at2 = cta_scan(sc, mine2 << 8 | chunks * p.hk, both);
+    const int cut_at = (int)(at2 & 255), cuts = (int)(both & 255);
+    const long long lo = cta < cuts ? 0 : (long long)(cta - cuts) * per;
+    const bool here = cta < cuts ? cut_at <= cta && cta < cut_at + chunks * p.hk
+                                 : at2 >> 8 <= lo && lo < (at2 >> 8) + mine2;
+    if (here)
+      share = Share{per, lo, cta < cuts ? 1 : min(both >> 8, lo + per), at2 >> 8, get(q), q,
+                    e0 - first[q], 1, cuts, cut_at};
+    return;
+  }
+  const long long lo = sh.begin(cta);
   if (lo >= at && lo < at + sum) {
     q = seq;
     for (int e = e0; e < e1; ++e) {
       while (first[q + 1] <= e) ++q;
       const long long u = e1 - e0 == 1 ? sum : units(q, e);
       if (lo < at + u) {
-        begin = Begin{at, get(q), q, e - first[q]};
+        share = Share{sh.per, lo, sh.begin(cta + 1), at, get(q), q, e - first[q], 0, 0, 0};
         break;
       }
       at += u;
     }
   }
-  return total;
 }
 
 // What a softmax group does with the rows of a piece when its blocks are done: m
@@ -422,7 +463,7 @@ __device__ __forceinline__ long long divide(const AttnParams& p, Scan& sc, uint8
 // not unrolled: the code runs once a piece, and what it takes is mostly the
 // fetching of its instructions (unrolled, a whole item's results took 6500
 // cycles to store, 3300 so).
-template <typename T, int ND>
+template <typename T, int ND, bool CUT>
 __device__ __forceinline__ void finish_piece(const AttnParams& p, const TcPieces& ws, Smem<ND>& s,
                                           const Piece* piece, int t, uint32_t o_tm, int cnt,
                                           float m, float l) {
@@ -434,9 +475,16 @@ __device__ __forceinline__ void finish_piece(const AttnParams& p, const TcPieces
   bool holds = true;  // this group has what is known of the item's rows
   if (g.pieces) {
     bool have = cnt > 0;  // O lies in TMEM
-    int a = (int)blockIdx.x - g.cta0;  // first piece of what it has
-    const auto place = [&](int i) {    // of a piece: the item begins in slot 1 of its CTA
-      return (2LL * (g.cta0 + i) + (i == 0 ? 1 : 0)) * 2 + t;
+    int a = g.number;  // first piece of what it has
+    // Where piece i is left, and where the second half of a pair is counted that
+    // begins with it: slot 0 of its CTA, or slot 1 of the item's first CTA for the
+    // first piece behind its chunks, as its own CTA may end one item there and
+    // begin the next.
+    const auto slot = [&](int i) {
+      const int chunks = CUT ? g.chunks : 0;
+      const int n = i == chunks ? 2 * g.chunk0 + 1
+                                  : 2 * (i < chunks ? g.chunk0 + i : g.cta0 + (i - chunks));
+      return n * 2 + t;
     };
     const auto group_sync = [&]() {
       asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
@@ -447,7 +495,7 @@ __device__ __forceinline__ void finish_piece(const AttnParams& p, const TcPieces
       const bool left = (a & size) == 0;
       const int other = left ? a + size : a - size;
       if (other >= g.pieces) continue;
-      unsigned* node = ws.count + 2 * (g.cta0 + max(a, other)) + t;
+      unsigned* node = ws.count + slot(max(a, other));
       if (first_thread) {
         unsigned v;
         asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(v) : "l"(node) : "memory");
@@ -457,7 +505,7 @@ __device__ __forceinline__ void finish_piece(const AttnParams& p, const TcPieces
       bool there = s.there[t] != 0;
       if (!there) {
         // leave it in the workspace, unless the other half came meanwhile
-        const long long at = place(a);
+        const long long at = slot(a);
         __stcg(ws.ml + at * 128 + row, make_float2(m, l));
         if (have) {
           float4* dst = reinterpret_cast<float4*>(ws.o) + at * (ND * 16) * 128 + row;
@@ -488,7 +536,7 @@ __device__ __forceinline__ void finish_piece(const AttnParams& p, const TcPieces
       if (!there) {
         holds = false;
       } else {
-        const long long at = place(other);
+        const long long at = slot(other);
         const float2 x = __ldcg(ws.ml + at * 128 + row);
         const float4* src = reinterpret_cast<const float4*>(ws.o) + at * (ND * 16) * 128 + row;
         const float m2 = fmaxf(m, x.x), base = m2 == -INFINITY ? 0.0f : m2;
@@ -592,6 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // softmax is the longer way (16384 tokens 1107 -> 1057 us); above, the tensor
   // core is (8192 tokens 376 -> 391 us with it).
   constexpr bool kHalves = ND == 1;
+  constexpr bool kCut = ND == 2 && !GEN;  // what the softmax does not bound, see kCutShare
   extern __shared__ uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -629,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait_prior_launch();
 
   const int tpt = tile_tokens(p.group);
-  const Shares sh(divide(p, s.scan, &s.kv[0][0], s.begin, tpt), gridDim.x);
+  divide<kCut>(p, s.scan, &s.kv[0][0], s.share, tpt);
   Piece g;
   fence_async_shared();  // the ring's first use was that one
   __syncthreads();
@@ -848,17 +897,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (lane == 0) {
       // ---------------------------------------------------------------- the share, piece by piece
-      long long at = 0, hi = 0, entry_at = 0;
-      int seq = 0, index = 0;
-      if ((int)blockIdx.x < sh.grid) {
-        at = sh.begin(blockIdx.x);
-        hi = sh.begin(blockIdx.x + 1);
-        entry_at = s.begin.at;
-        seq = s.begin.seq;
-        index = s.begin.index;
-      }
+      const Share& sh = s.share;
+      const int cta = blockIdx.x;
+      const bool chunk = kCut && cta < sh.cuts;  // a chunk of an item, and nothing else
+      long long at = sh.at, entry_at = sh.entry_at;
+      const long long hi = sh.hi;
+      int seq = sh.seq, index = sh.index, cut_at = sh.cut_at;
       Entry e;
-      Seq r = s.begin.s;
+      Seq r = sh.s;
+      // an item of the entry: its chunks; the units it has on the list, the first
+      // of which read nothing, and the block that the others begin with
+      int chunks = 0, listed = 0, fixed = 0, behind = 0;
       int head = -1, i = 0;   // head -2: the sequence is to be read, -1: the entry made
       uint32_t ph = 0;
       bool ok = true;
@@ -874,32 +923,53 @@ __global__ void __launch_bounds__(kThreads, 1)
               continue;
             }
             e = entry_of(p, r, seq, index, tpt);
-            head = (int)quotient(at - entry_at, units_of(e));
+            listed = units_of(e);
+            if (kCut && sh.cut) {
+              chunks = listed / (int)sh.per;
+              listed = rest_of(listed - chunks * (int)sh.per);
+              behind = max(0, chunks * (int)sh.per - kItemUnits);
+            }
+            fixed = listed - (e.blocks - behind);
+            head = chunk ? (cta - cut_at) / chunks
+                         : listed ? (int)quotient(at - entry_at, listed) : p.hk;
           }
-          const int units = units_of(e);
-          const long long item = entry_at + (long long)head * units;
-          const int u0 = (int)(at - item), u1 = (int)min((long long)units, u0 + (hi - at));
-          at = item + u1;
-          o.head = head;
-          o.n0 = max(0, u0 - kItemUnits);
-          o.end = max(0, u1 - kItemUnits);
-          if (u1 == units && ++head == p.hk) {
-            head = -1;
-            ++index;
-            entry_at = at;
+          const long long item = entry_at + (long long)head * listed;
+          if (chunk) {
+            o.number = cta - cut_at - head * chunks;
+            o.n0 = max(0, o.number * (int)sh.per - kItemUnits);
+            o.end = (o.number + 1) * (int)sh.per - kItemUnits;
+            at = hi;
+          } else if (listed) {
+            const int u0 = (int)(at - item), u1 = (int)min((long long)listed, u0 + (hi - at));
+            at = item + u1;
+            o.n0 = behind + max(0, u0 - fixed);
+            o.end = behind + max(0, u1 - fixed);
           }
-          if (o.end > o.n0) {
+          if (o.end <= o.n0) o.end = 0;  // nothing to read: no piece
+          if (o.end) {
+            o.head = head;
             o.first = e.first, o.ntok = e.ntok, o.p0 = e.p0, o.kv = e.kv;
             o.near = e.near, o.skip = e.skip, o.blocks = e.blocks, o.prefix = e.prefix;
             o.seq = e.seq;
             o.cnt[0] = min(o.end, blocks_of_tile0(e, tpt)) - o.n0;
             o.cnt[1] = e.ntok > tpt ? o.end - o.n0 : 0;
             if (o.end - o.n0 < e.blocks) {
-              o.cta0 = sh.of(item + kItemUnits);
-              o.pieces = sh.of(item + units - 1) - o.cta0 + 1;
+              o.cta0 = sh.cuts + (int)quotient(item + fixed, sh.per);
+              const int last = sh.cuts + (int)quotient(item + listed - 1, sh.per);
+              o.pieces = chunks + (listed ? last - o.cta0 + 1 : 0);
+              o.chunks = chunks;
+              o.chunk0 = chunks ? cut_at + head * chunks : o.cta0;
+              if (!chunk) o.number = chunks + cta - o.cta0;
             }
-            break;
           }
+          if (listed == 0 || at == item + listed) ++head;
+          if (head >= p.hk) {
+            head = -1;
+            ++index;
+            entry_at += (long long)listed * p.hk;
+            cut_at += chunks * p.hk;
+          }
+          if (o.end) break;
         }
         ok = bwait_piece(&s.piece_empty[i], ph ^ 1u, p.err);
         if (!ok) break;
@@ -1098,7 +1168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         oph ^= 1u;
         tc_fence_after();
       }
-      finish_piece<T, ND>(p, ws, s, held, t, o_tm, cnt, m * c, l);
+      finish_piece<T, ND, kCut>(p, ws, s, held, t, o_tm, cnt, m * c, l);
       if (cnt > 0) {
         tc_fence_before();
         __syncwarp();
