@@ -47,21 +47,25 @@ constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "setmaxnreg draws on the launch");
 constexpr int kBlk = kTcBlock;
 constexpr int kChunk = 128 * 128;   // 128 rows of 64 values
-// Where items are no more than CTAs and shares no smaller than kCutShare units,
-// items are cut from their first key on, a share a CTA: the CTAs of a kv head then
-// read the same keys at the same time, and its cache comes from DRAM about once
-// and not for each of them. 1000 tokens over 65536 keys: 2.69 -> 0.38 GB read, and
-// with the power that saves 786 -> 695 us back to back; 700 over 32768: 262 -> 249;
-// over 16384 keys, which L2 holds, no change; 1000 over 8192 cut as well (12 units):
-// 96.6 -> 98.2. Bounded by their softmax, capped scores lost (1178 -> 1199 us), as
-// did biased ones (980 -> 1043) and head sizes up to 64 (511 -> 514): not cut.
-// What is left of the items makes the remaining shares; kRestUnits is its
-// fixed cost there.
-constexpr int kCutShare = 64, kRestUnits = 5;
+// Where items are no more than CTAs, sequences have two entries or more and items
+// kCutItem units (means), items are cut from their first key on, a share a CTA: the
+// CTAs of a kv head then read the same keys at the same time, and its cache comes
+// from DRAM about once and not for each of them. 1000 tokens over 65536 keys: 2.69
+// -> 0.38 GB read, and with the power that saves 786 -> 695 us back to back; 700
+// over 32768 262 -> 249, 100 over 65536 122 -> 114, 100 over 32768 76.8 -> 74.8.
+// Shorter items lost (100 over 16384 keys, 131 units: 54.7 -> 55.4; 500 over 8192:
+// 61.9 -> 62.9) or stayed (1000 over 16384), and so did single entries, which share
+// no keys (64 over 131072: 126.2 -> 128.7). Bounded by their softmax, capped scores
+// lost (1178 -> 1199), as did biased ones (980 -> 1043) and head sizes up to 64
+// (511 -> 514): not cut. What is left of the items makes the remaining shares;
+// kRestUnits is its fixed cost there. A share has kCutShare units at least: a chunk
+// must hold more than an item's fixed cost.
+constexpr int kCutItem = 192, kCutShare = 8, kRestUnits = 5;
 // An item's fixed cost, in blocks (prefill of 8192 tokens: 2 -> 405 us, 4 -> 399,
 // 5 -> 402; 16 prompts of 1024: 196, 206, 203; without it 902 and 387 before the
 // cost itself was cut).
 constexpr int kItemUnits = 2;
+static_assert(kCutShare > kItemUnits, "every chunk reads something");
 // tanh(y) = y P(y^2) for |y| < 0.75: a least-maximum fit of tanh(y) / y in y^2,
 // below 2e-8 off, 1.1e-7 with fp32 arithmetic.
 constexpr float kTanhMax = 0.75f;
@@ -426,7 +430,8 @@ __device__ __forceinline__ void divide(const AttnParams& p, Scan& sc, uint8_t* r
   at = cta_scan(sc, sum, total);
   const Shares sh(total, gridDim.x);
   const int cta = blockIdx.x;
-  if (CUT && n * p.hk <= gridDim.x && sh.per >= kCutShare) {  // at most one entry a thread
+  if (CUT && n * p.hk <= gridDim.x && n >= 2 * seqs && sh.per >= kCutShare &&
+      total >= n * p.hk * kCutItem) {  // at most one entry a thread
     const Shares cut(total + n * p.hk * kRestUnits, gridDim.x);
     const int per = (int)cut.per;  // at least one item's units in all: int
     const int u = e0 < e1 ? (int)quotient(sum, p.hk) : 0;
