@@ -1,5 +1,6 @@
 // C ABI of the attention operators: argument validation, workspace, dispatch.
 #include <cmath>
+#include <cstddef>
 #include <cstdio>
 #include <initializer_list>
 #include <new>
@@ -20,6 +21,8 @@ struct moe_attn_handle {
   Partials decode{};
   TcPieces tc{};
 };
+// The error word is the workspace's first; tests set its bits through here.
+static_assert(offsetof(moe_attn_handle, ws) == sizeof(moe_attn_config) + 8, "place of ws");
 
 namespace {
 

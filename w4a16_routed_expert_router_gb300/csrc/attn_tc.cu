@@ -25,8 +25,10 @@
 //             keys: the tiles' MMAs interleave and both results come late.)
 //   warp 10   clears V rows behind a sequence's last key.
 //   warp 11   walks the share and hands its pieces to the others.
-// Every wait is bounded; a timeout sets the error bit and the kernel winds
-// down.
+// Every wait on an mbarrier is bounded; a timeout sets the error bit and the kernel
+// winds down. The four warps of a softmax group meet at named barriers, which have
+// no limit, so they go on or leave as one (group_all): a warp whose wait gave up
+// takes part in the next vote before it leaves.
 #include "attn_common.cuh"
 
 namespace moe {
@@ -193,6 +195,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Whether `ok` holds in all four warps of softmax group t. Every warp of the group
+// takes part in every vote, whatever became of its own waits.
+__device__ __forceinline__ bool group_all(int t, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n"
+      " barrier.cta.red.and.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(1 + t)
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -1004,7 +1019,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float cap_out = p.sc.softcap * kLog2e;
     uint32_t sph = 0, oph = 0;
     Pieces<ND, true> pieces{s, p.err};
-    while (const Piece* held = pieces.hold()) {
+    for (;;) {
+      const Piece* held = pieces.hold();
+      if (!group_all(t, held != nullptr)) break;  // the end of the share, or a timeout
       const int ntok = min(tpt, held->ntok - t * tpt);    // tokens of this tile
       if (ntok <= 0) {
         pieces.release();
@@ -1167,12 +1184,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.p_full[t]);
       }
-      if (!ok) break;
-      if (cnt > 0) {
-        if (!warp_wait(&s.o_full[t], oph, p.err)) break;
+      if (ok && cnt > 0) {
+        ok = warp_wait(&s.o_full[t], oph, p.err);
         oph ^= 1u;
         tc_fence_after();
       }
+      // A piece of a split item meets barriers in there: a vote first. A whole item
+      // has none, and a warp that gave up takes part in the group's next vote, the
+      // one above, from here.
+      if ((!ok || held->pieces) && !group_all(t, ok)) break;
       finish_piece<T, ND, kCut>(p, ws, s, held, t, o_tm, cnt, m * c, l);
       if (cnt > 0) {
         tc_fence_before();
