@@ -182,7 +182,9 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
                      const moe_attn_scores* scores, void* stream);
 
 /* Synchronises the device, returns the error flag bits in *flags and clears
- * them; MOE_ATTN_ERR_DEVICE when any was set. */
+ * them; MOE_ATTN_ERR_DEVICE when any was set. Once a wait has given up, the
+ * results of all launches until this call are worthless; after it the handle is
+ * as good as new. */
 int moe_attn_check_device_errors(moe_attn_handle* h, uint32_t* flags);
 
 #ifdef __cplusplus

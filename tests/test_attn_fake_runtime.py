@@ -1,0 +1,115 @@
+"""The host side of the attention operators' C ABI (csrc/attn.cu) against a
+stand-in for the CUDA runtime (fake_cudart.cpp): what it asks of the runtime, in
+which order, on which device, and what it makes of errors. No GPU takes part."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+from w4a16_routed_expert_router_gb300 import _build, attention as at
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+TIMEOUT, RANGE = at.MOE_ATTN_DEVERR_TIMEOUT, at.MOE_ATTN_DEVERR_RANGE
+
+
+@pytest.fixture(scope="module")
+def F(tmp_path_factory):
+    out = tmp_path_factory.mktemp("fake")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_build.nvcc())))
+    runtime = os.path.join(HERE, "fake_cudart.cpp")
+    jobs = [["g++", "-std=c++17", "-O1", "-fPIC", "-I" + os.path.join(cuda, "include"), "-c",
+             runtime]]
+    for src in (os.path.join(_build.CSRC, "attn.cu"), os.path.join(HERE, "fake_launches.cu")):
+        jobs.append([_build.nvcc(), *_build.ARCH, *_build.FLAGS, "-I" + _build.CSRC, "-c", src])
+    objects = [str(out / f"{i}.o") for i in range(len(jobs))]
+    for job, obj in zip(jobs, objects):
+        subprocess.run([*job, "-o", obj], check=True)
+    lib = str(out / "fake.so")
+    # its own calls go to its own functions, whatever else the process has loaded
+    subprocess.run(["g++", "-shared", "-Wl,-Bsymbolic", *objects, "-o", lib], check=True)
+    L = ctypes.CDLL(lib)
+    at.register(L)
+    L.fake_calls.restype = ctypes.c_char_p
+    L.fake_counters.restype = ctypes.c_void_p
+    L.fake_fail.argtypes = [ctypes.c_char_p]
+    return L
+
+
+class Handle:
+    """A handle on device 1 while device 0 is current; calls by ctypes."""
+
+    def __init__(self, F, device=1):
+        self.F = F
+        F.fake_reset()
+        F.fake_use(0)
+        self.cfg = at.moe_attn_config(8, 2, 64, 16, 64, 8, 0, 0)
+        self.h = ctypes.c_void_p()
+        assert F.moe_attn_create(self.cfg, device, self.h) == 0
+        ws = ctypes.c_void_p.from_address(self.h.value + ctypes.sizeof(self.cfg) + 8).value
+        n = ctypes.c_size_t()
+        assert F.moe_attn_workspace_bytes(self.cfg, n) == 0
+        self.words = (ctypes.c_uint32 * (n.value // 4)).from_address(ws)
+        self.created = self.calls()
+
+    def calls(self):
+        got = self.F.fake_calls().decode().split(";")[:-1]
+        self.F.fake_reset()
+        return got
+
+    def forward(self, max_q):
+        rows = lambda a: at.moe_attn_rows(a, 8 * 64, 64)  # noqa: E731
+        cache = at.moe_attn_cache(1 << 20, 1 << 21, 9, 2 * 16 * 64, 64, 16 * 64)
+        batch = at.moe_attn_batch(64, 64, 64, 4, 4, 1, max_q, max_q)
+        return self.F.moe_attn_forward(self.h, rows(1 << 22), rows(1 << 23), None, cache, batch,
+                                       at.moe_attn_scores(0.125, 0.0, 0, None, None), None)
+
+    def append(self):
+        rows = lambda a: at.moe_attn_rows(a, 2 * 64, 64)  # noqa: E731
+        cache = at.moe_attn_cache(1 << 20, 1 << 21, 9, 2 * 16 * 64, 64, 16 * 64)
+        return self.F.moe_attn_append(self.h, None, None, rows(1 << 22), rows(1 << 23), 64, 64, 1,
+                                      at.moe_attn_rotation(64, 64, 0, 1.0, 0), cache, None)
+
+    def check(self):
+        flags = ctypes.c_uint32()
+        return self.F.moe_attn_check_device_errors(self.h, flags), flags.value
+
+    def counters(self, kernel):
+        return (ctypes.c_uint32 * self.F.fake_counter_words(kernel)).from_address(
+            self.F.fake_counters(kernel))
+
+
+def test_a_new_handle_counts_from_zero(F):
+    h = Handle(F)
+    assert not any(h.words[:4096])
+    assert h.forward(1) == 0 and h.forward(40) == 0
+    for kernel in (0, 1):
+        assert not any(h.counters(kernel))
+    assert F.moe_attn_destroy(h.h) == 0
+
+
+@pytest.mark.parametrize("bits", [TIMEOUT, TIMEOUT | RANGE])
+def test_after_a_timeout_joins_count_from_zero(F, bits):
+    # a launch that winds down leaves counters raised that only the second half of
+    # a pair resets
+    h = Handle(F)
+    assert h.forward(1) == 0 and h.forward(40) == 0
+    for kernel in (0, 1):
+        c = h.counters(kernel)
+        for i in range(len(c)):
+            c[i] = 1 + i % 2
+    h.words[0] = bits
+    assert h.check() == (-6, bits)
+    for kernel in (0, 1):
+        assert not any(h.counters(kernel))
+    assert h.check() == (0, 0)
+    assert F.moe_attn_destroy(h.h) == 0
+
+
+def test_without_a_timeout_counters_are_left_alone(F):
+    h = Handle(F)
+    assert h.forward(40) == 0
+    h.counters(1)[3] = 1  # a launch that is under way elsewhere would own it
+    h.words[0] = RANGE
+    assert h.check() == (-6, RANGE) and h.counters(1)[3] == 1
+    assert F.moe_attn_destroy(h.h) == 0

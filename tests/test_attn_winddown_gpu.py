@@ -52,3 +52,19 @@ def test_launches_end_and_the_timeout_is_reported(hq, hk, d, page, dtype, lens, 
         b.run(layer)
     assert layer.check_device_errors() == at.MOE_ATTN_DEVERR_TIMEOUT
     assert layer.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("hq,hk,d,page,dtype,lens,kw", CASES)
+def test_results_after_a_timeout_are_right_again(hq, hk, d, page, dtype, lens, kw):
+    b = ac.Batch(lens, hq, hk, d, page, dtype, **kw)
+    layer = moe.PagedAttention(hq, hk, d, page, b.tokens, len(lens), dtype=dtype)
+    out, lse = b.run(layer)
+    word = _error_word(layer)
+    for _ in range(3):
+        word.fill_(at.MOE_ATTN_DEVERR_TIMEOUT)
+        b.run(layer)
+        assert layer.check_device_errors() == at.MOE_ATTN_DEVERR_TIMEOUT
+        for _ in range(3):
+            o2, l2 = b.run(layer)
+            assert torch.equal(o2, out) and torch.equal(l2, lse)
+        assert layer.check_device_errors() == 0

@@ -120,7 +120,7 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Workspace carve-up; the order is the order of the fields filled in create().
 struct Layout {
-  size_t off[7];
+  size_t off[7], sizes[7];
   size_t total;
 };
 Layout plan(const moe_attn_config& c) {
@@ -138,6 +138,7 @@ Layout plan(const moe_attn_config& c) {
   size_t o = 0;
   for (size_t i = 0; i < sizeof(sizes) / sizeof(sizes[0]); ++i) {
     L.off[i] = o;
+    L.sizes[i] = sizes[i];
     o += align256(sizes[i]);
   }
   L.total = o;
@@ -483,6 +484,14 @@ int moe_attn_check_device_errors(moe_attn_handle* h, uint32_t* flags) {
   uint32_t v = 0;
   if ((st = cuda_status(cudaMemcpy(&v, h->err, 4, cudaMemcpyDeviceToHost))) != MOE_ATTN_OK)
     return st;
+  // A launch that gave up leaves counters of joins raised, which only the second
+  // half of a pair resets; the next launch would take old sums for that half.
+  if (v & kErrTimeout) {
+    const Layout L = plan(h->cfg);
+    uint8_t* b = static_cast<uint8_t*>(h->ws);
+    for (int i : {1, 4})
+      if ((st = cuda_status(cudaMemset(b + L.off[i], 0, L.sizes[i]))) != MOE_ATTN_OK) return st;
+  }
   if (v && (st = cuda_status(cudaMemset(h->err, 0, 4))) != MOE_ATTN_OK) return st;
   *flags = v;
   return v ? MOE_ATTN_ERR_DEVICE : MOE_ATTN_OK;
