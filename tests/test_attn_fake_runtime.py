@@ -113,3 +113,28 @@ def test_without_a_timeout_counters_are_left_alone(F):
     h.words[0] = RANGE
     assert h.check() == (-6, RANGE) and h.counters(1)[3] == 1
     assert F.moe_attn_destroy(h.h) == 0
+
+
+def test_cleared_memory_is_waited_for(F):
+    # a memset returns before it has run, and streams other than the legacy one do
+    # not wait for it: create and check return behind a synchronisation
+    h = Handle(F)
+    assert h.created[-2:] == ["memset", "sync"]
+    for bits in (RANGE, TIMEOUT):
+        h.words[0] = bits
+        assert h.check()[1] == bits
+        calls = h.calls()
+        assert calls[0] == "sync" and calls[-2:] == ["memset", "sync"]
+    h.check()
+    assert h.calls() == ["sync", "memcpy"]
+    assert F.moe_attn_destroy(h.h) == 0
+
+
+@pytest.mark.parametrize("what", ["decode setup", "tc setup", "malloc", "memset", "sync"])
+def test_create_reports_a_failing_call(F, what):
+    F.fake_reset()
+    F.fake_fail(what.encode())
+    h = ctypes.c_void_p()
+    assert F.moe_attn_create(at.moe_attn_config(8, 2, 64, 16, 64, 8, 0, 0), 0, h) == -5
+    assert not h.value
+    F.fake_reset()

@@ -1,0 +1,29 @@
+"""GPU tests of the attention operators' handles: what a new one may be used for at
+once, and what making and dropping one leaves undisturbed."""
+import pytest
+import torch
+
+import w4a16_routed_expert_router_gb300 as moe
+from tests import attn_cases as ac
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF = torch.bfloat16
+
+
+def test_a_new_handle_is_ready_for_any_stream():
+    # its memory is cleared behind what the default stream still has to do, which
+    # another stream does not wait for: create returns when that is over
+    moe.PagedAttention(8, 2, 128, 16, 64, 4).close()      # loads the kernels
+    b = ac.Batch([(40, 3000), (1, 700)], 8, 2, 128, 16, BF)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)                        # some 0.2 s
+    behind = torch.cuda.Event()
+    behind.record()
+    layer = moe.PagedAttention(8, 2, 128, 16, b.tokens, 2)
+    assert behind.query()
+    s = torch.cuda.Stream()
+    out, lse = b.run(layer, stream=s)
+    s.synchronize()
+    b.check(out, lse)
+    assert layer.check_device_errors() == 0

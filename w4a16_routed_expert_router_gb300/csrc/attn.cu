@@ -334,7 +334,9 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn_handle** ou
       // a CTA of the tensor-core kernel holds all of its SM's TMEM
       (st = per_sm == 1 ? MOE_ATTN_OK : MOE_ATTN_ERR_CUDA) != MOE_ATTN_OK ||
       (st = cuda_status(cudaMalloc(&h->ws, L.total))) != MOE_ATTN_OK ||
-      (st = cuda_status(cudaMemset(h->ws, 0, L.total))) != MOE_ATTN_OK) {
+      (st = cuda_status(cudaMemset(h->ws, 0, L.total))) != MOE_ATTN_OK ||
+      // cudaMemset does not wait, and other streams do not wait for it
+      (st = cuda_status(cudaDeviceSynchronize())) != MOE_ATTN_OK) {
     moe_attn_destroy(h);
     return st;
   }
@@ -492,7 +494,10 @@ int moe_attn_check_device_errors(moe_attn_handle* h, uint32_t* flags) {
     for (int i : {1, 4})
       if ((st = cuda_status(cudaMemset(b + L.off[i], 0, L.sizes[i]))) != MOE_ATTN_OK) return st;
   }
-  if (v && (st = cuda_status(cudaMemset(h->err, 0, 4))) != MOE_ATTN_OK) return st;
+  // and a bit that the next launch sets must not be cleared by a late memset
+  if (v && ((st = cuda_status(cudaMemset(h->err, 0, 4))) != MOE_ATTN_OK ||
+            (st = cuda_status(cudaDeviceSynchronize())) != MOE_ATTN_OK))
+    return st;
   *flags = v;
   return v ? MOE_ATTN_ERR_DEVICE : MOE_ATTN_OK;
 }
