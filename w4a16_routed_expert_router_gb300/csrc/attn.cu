@@ -1,4 +1,5 @@
 // C ABI of the attention operators: argument validation, workspace, dispatch.
+#include <cfloat>
 #include <cmath>
 #include <cstddef>
 #include <cstdio>
@@ -99,6 +100,14 @@ int validate_cache(const moe_attn_cache* c) {
   return MOE_ATTN_OK;
 }
 
+// The cap, small enough that it is finite in log2 units, and what brings a product
+// to a part of it: at most the largest number, which takes every product but zero
+// to +-1, as infinity would.
+float cap_of(const moe_attn_scores* s) { return fminf(s->softcap, 2.3e38f); }
+float cap_in_of(const moe_attn_scores* s) {
+  if (!(s->softcap > 0.0f)) return 0.0f;
+  return fmaxf(fminf(s->scale / cap_of(s), FLT_MAX), -FLT_MAX);
+}
 Rows rows(const moe_attn_rows* r) {
   return r ? Rows{static_cast<uint16_t*>(r->data), r->token_stride, r->head_stride}
            : Rows{nullptr, 0, 0};
@@ -448,7 +457,7 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
   p.b = Batch{b->cu_q, b->kv_len, b->page_table, b->table_stride, b->columns, b->num_seqs,
               b->num_tokens, b->max_q};
   // a window as long as the table hides nothing
-  p.sc = Scores{sc->scale, sc->softcap, sc->window >= max_kv ? 0 : sc->window, sc->slopes,
+  p.sc = Scores{sc->scale, cap_of(sc), cap_in_of(sc), sc->window >= max_kv ? 0 : sc->window, sc->slopes,
                 sc->prefix};
   p.hq = c.q_heads;
   p.hk = c.kv_heads;

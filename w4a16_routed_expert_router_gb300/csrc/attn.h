@@ -68,6 +68,7 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, cudaStream_t s);
 struct Scores {
   float scale;
   float softcap;
+  float cap_in;  // scale / softcap, finite; 0 without a cap
   int window;
   const float* slopes;
   const int* prefix;

@@ -68,11 +68,13 @@ constexpr int kCutItem = 192, kCutShare = 8, kRestUnits = 5;
 // cost itself was cut).
 constexpr int kItemUnits = 2;
 static_assert(kCutShare > kItemUnits, "every chunk reads something");
-// tanh(y) = y P(y^2) for |y| < 0.75: a least-maximum fit of tanh(y) / y in y^2,
-// below 2e-8 off, 1.1e-7 with fp32 arithmetic.
-constexpr float kTanhMax = 0.75f;
-__device__ constexpr float kTanh[6] = {0.9999999719f, -0.33332966662f, 0.13325515284f,
-                                      -0.05334982016f, 0.01959378583f, -0.00472395227f};
+// tanh(y) = y P(y^2) for |y| < 0.6: the fit of tanh(y) / y in y^2 with the least
+// relative error, 7.4e-8, and 1.8e-7 with fp32 arithmetic. (Up to 0.75 it takes a
+// coefficient more.)
+constexpr float kTanhMax = 0.6f;
+constexpr int kTanhTerms = 5;
+__device__ constexpr float kTanh[kTanhTerms] = {0.99999992687f, -0.3333230997f, 0.13310173604f,
+                                                -0.052101477875f, 0.01547542443f};
 constexpr float kRaise = 8.0f;      // log2 units
 
 // one value per warp of a scan over the CTA
@@ -1015,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = GEN ? 1.0f : p.sc.scale * kLog2e;
     const float raise = GEN ? kRaise : kRaise / c;
     const float scale2 = p.sc.scale * kLog2e;
-    const float cap_in = p.sc.softcap > 0.0f ? p.sc.scale / p.sc.softcap : 0.0f;
+    const float cap_in = p.sc.cap_in;
     const float cap_out = p.sc.softcap * kLog2e;
     uint32_t sph = 0, oph = 0;
     Pieces<ND, true> pieces{s, p.err};
@@ -1054,31 +1056,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = (kb + kBlk - 1 <= p_first && kb > lo_last) || kb + kBlk <= prefix;
         if (GEN) {
           if (p.sc.softcap > 0.0f) {
-            // cap tanh(x scale / cap) in log2 units. While every |x| scale / cap of
-            // the warp's rows is below kTanhMax, it is x times a polynomial in x^2
-            // (the factors go into its coefficients; up to 1000, so that their
-            // powers stay finite), two keys to an instruction; else 1 - 2 / (1 +
-            // e^2y). Rows and keys that do not exist have no part in the choice: the
-            // block with the last key takes the second form.
+            // cap tanh(y) in log2 units, y = x scale / cap. While every |y| of the
+            // warp's rows is below kTanhMax, it is y times a polynomial in y^2, two
+            // keys to an instruction; else 1 - 2 / (1 + e^2y). Rows and keys that do
+            // not exist have no part in the choice: the block with the last key takes
+            // the second form. (The powers of scale / cap do not go into the
+            // coefficients, which saves a product but lets the highest ones vanish
+            // where scale / cap is small: scores were 0.3 off at a cap of 2000.)
             float top = fabsf(x[0]);
 #pragma unroll
             for (int i = 1; i < kBlk - 1; i += 2) top = max3(top, fabsf(x[i]), fabsf(x[i + 1]));
             top = fmaxf(top, fabsf(x[kBlk - 1]));
-            if (kb + kBlk <= kv && fabsf(cap_in) < 1e3f &&
+            if (kb + kBlk <= kv &&
                 __all_sync(0xffffffffu, !mine || top * fabsf(cap_in) < kTanhMax)) {
-              float f[6], power = cap_in * cap_out;
+              const uint64_t in2 = pack2(cap_in, cap_in);
+              float f[kTanhTerms];
 #pragma unroll
-              for (int k = 0; k < 6; ++k) {
-                f[k] = kTanh[k] * power;
-                power *= cap_in * cap_in;
-              }
+              for (int k = 0; k < kTanhTerms; ++k) f[k] = kTanh[k] * cap_out;
 #pragma unroll
               for (int i = 0; i < kBlk / 2; ++i) {
-                const uint64_t y = pack2(x[2 * i], x[2 * i + 1]);
+                const uint64_t y = mul2(pack2(x[2 * i], x[2 * i + 1]), in2);
                 const uint64_t t = mul2(y, y);
-                uint64_t r = pack2(f[5], f[5]);
+                uint64_t r = pack2(f[kTanhTerms - 1], f[kTanhTerms - 1]);
 #pragma unroll
-                for (int k = 4; k >= 0; --k) r = fma2(r, t, pack2(f[k], f[k]));
+                for (int k = kTanhTerms - 2; k >= 0; --k) r = fma2(r, t, pack2(f[k], f[k]));
                 unpack2(mul2(r, y), x[2 * i], x[2 * i + 1]);
               }
             } else {
