@@ -1,5 +1,4 @@
 // C ABI of the attention operators: argument validation, workspace, dispatch.
-#include <cfloat>
 #include <cmath>
 #include <cstddef>
 #include <cstdio>
@@ -101,13 +100,14 @@ int validate_cache(const moe_attn_cache* c) {
 }
 
 // The cap, small enough that it is finite in log2 units, and what brings a product
-// to a part of it: at most the largest number, which takes every product but zero
-// to +-1, as infinity would.
+// to a part of it: at most 1e38, which takes every product but zero to +-1, as
+// infinity would.
 float cap_of(const moe_attn_scores* s) { return fminf(s->softcap, 2.3e38f); }
 float cap_in_of(const moe_attn_scores* s) {
   if (!(s->softcap > 0.0f)) return 0.0f;
-  return fmaxf(fminf(s->scale / cap_of(s), FLT_MAX), -FLT_MAX);
+  return fmaxf(fminf(s->scale / cap_of(s), 1e38f), -1e38f);
 }
+
 Rows rows(const moe_attn_rows* r) {
   return r ? Rows{static_cast<uint16_t*>(r->data), r->token_stride, r->head_stride}
            : Rows{nullptr, 0, 0};

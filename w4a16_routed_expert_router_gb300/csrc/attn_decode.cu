@@ -149,7 +149,7 @@ __device__ __forceinline__ bool next_piece(const AttnParams& p, Walk& k, Piece& 
   return false;
 }
 
-template <typename T, int ND, bool GEN>
+template <typename T, int ND, int FORM>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const AttnParams p,
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = min(gid + 8 * i, rows - 1);
       const int tok = r / p.group, h = head * p.group + (r - tok * p.group);
       pos[i] = it.kv - it.n + tok;
-      slope[i] = GEN && p.sc.slopes ? p.sc.slopes[h] : 0.0f;
+      slope[i] = FORM != kPlain && p.sc.slopes ? p.sc.slopes[h] : 0.0f;
       qp[i] = p.q.p + (long long)(it.first + tok) * p.q.token + (long long)h * p.q.head;
     }
 #pragma unroll
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma16<T>(sacc[2 * i + 1], qf[k], b[2], b[3]);
             }
           }
-          if (GEN || !(k0 + 16 * kSub <= it.kv - it.n + 1 && p.sc.window == 0)) {
+          if (FORM != kPlain || !(k0 + 16 * kSub <= it.kv - it.n + 1 && p.sc.window == 0)) {
 #pragma unroll
             for (int t = 0; t < 2 * kSub; ++t)
 #pragma unroll
@@ -404,13 +404,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool seen =
                     key < it.kv && (key < prefix || (away >= 0 && (p.sc.window == 0 ||
                                                                   away < p.sc.window)));
-                sacc[t][i] = seen ? score<GEN>(p.sc, sacc[t][i], slope[r], away) : -INFINITY;
+                sacc[t][i] = seen ? score<FORM>(p.sc, sacc[t][i], slope[r], away) : -INFINITY;
               }
           } else {  // every row sees every key
 #pragma unroll
             for (int t = 0; t < 2 * kSub; ++t)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) sacc[t][i] = score<false>(p.sc, sacc[t][i], 0.0f, 0);
+              for (int i = 0; i < 4; ++i) sacc[t][i] = score<kPlain>(p.sc, sacc[t][i], 0.0f, 0);
           }
           float mx[2] = {m[0], m[1]};
 #pragma unroll
@@ -617,17 +617,26 @@ constexpr int smem_bytes() {
 static_assert(smem_bytes<1>() <= 227 * 1024 && smem_bytes<2>() <= 227 * 1024,
               "shared memory of a CTA");
 
-template <typename T, int ND, bool GEN>
-cudaError_t setup_one() {
-  return cudaFuncSetAttribute(attn_decode_kernel<T, ND, GEN>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<ND>());
+template <typename F>
+cudaError_t setup_one(F f, int bytes) {
+  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+template <typename T, int ND>
+cudaError_t setup_nd() {
+  cudaError_t e;
+  if ((e = setup_one(attn_decode_kernel<T, ND, kPlain>, smem_bytes<ND>())) != cudaSuccess) return e;
+  if ((e = setup_one(attn_decode_kernel<T, ND, kGeneral>, smem_bytes<ND>())) != cudaSuccess)
+    return e;
+  return setup_one(attn_decode_kernel<T, ND, kWide>, smem_bytes<ND>());
 }
 
 template <typename T, int ND>
 cudaError_t launch_one(const AttnParams& p, const Partials& w, const CUtensorMap& kmap,
                        const CUtensorMap& vmap, int grid, cudaStream_t s) {
-  const bool gen = p.sc.softcap > 0.0f || p.sc.slopes;
-  return launch_after(gen ? attn_decode_kernel<T, ND, true> : attn_decode_kernel<T, ND, false>,
+  const Form form = form_of(p.sc);
+  return launch_after(form == kPlain     ? attn_decode_kernel<T, ND, kPlain>
+                      : form == kGeneral ? attn_decode_kernel<T, ND, kGeneral>
+                                         : attn_decode_kernel<T, ND, kWide>,
                       dim3(grid), dim3(kThreads), smem_bytes<ND>(), s, kmap, vmap, p, w);
 }
 
@@ -635,14 +644,10 @@ cudaError_t launch_one(const AttnParams& p, const Partials& w, const CUtensorMap
 
 cudaError_t attn_decode_setup() {
   cudaError_t e;
-  if ((e = setup_one<Bf16, 1, false>()) != cudaSuccess) return e;
-  if ((e = setup_one<Bf16, 1, true>()) != cudaSuccess) return e;
-  if ((e = setup_one<Bf16, 2, false>()) != cudaSuccess) return e;
-  if ((e = setup_one<Bf16, 2, true>()) != cudaSuccess) return e;
-  if ((e = setup_one<Fp16, 1, false>()) != cudaSuccess) return e;
-  if ((e = setup_one<Fp16, 1, true>()) != cudaSuccess) return e;
-  if ((e = setup_one<Fp16, 2, false>()) != cudaSuccess) return e;
-  return setup_one<Fp16, 2, true>();
+  if ((e = setup_nd<Bf16, 1>()) != cudaSuccess) return e;
+  if ((e = setup_nd<Bf16, 2>()) != cudaSuccess) return e;
+  if ((e = setup_nd<Fp16, 1>()) != cudaSuccess) return e;
+  return setup_nd<Fp16, 2>();
 }
 
 cudaError_t launch_attn_decode(const AttnParams& p, const Partials& w, const CUtensorMap& kmap,

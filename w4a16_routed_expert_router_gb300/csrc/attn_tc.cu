@@ -650,7 +650,7 @@ __device__ __forceinline__ void finish_piece(const AttnParams& p, const TcPieces
 }
 
 // ------------------------------------------------------------------ attention
-template <typename T, int ND, bool GEN, bool BOTH>
+template <typename T, int ND, int FORM, bool BOTH>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
@@ -662,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // softmax is the longer way (16384 tokens 1107 -> 1057 us); above, the tensor
   // core is (8192 tokens 376 -> 391 us with it).
   constexpr bool kHalves = ND == 1;
+  constexpr bool GEN = FORM != kPlain;
   constexpr bool kCut = ND == 2 && !GEN;  // what the softmax does not bound, see kCutShare
   extern __shared__ uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -1058,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.sc.softcap > 0.0f) {
             // cap tanh(y) in log2 units, y = x scale / cap. While every |y| of the
             // warp's rows is below kTanhMax, it is y times a polynomial in y^2, two
-            // keys to an instruction; else 1 - 2 / (1 + e^2y). Rows and keys that do
+            // keys to an instruction; else as FORM has it. Rows and keys that do
             // not exist have no part in the choice: the block with the last key takes
             // the second form. (The powers of scale / cap do not go into the
             // coefficients, which saves a product but lets the highest ones vanish
@@ -1081,6 +1082,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = kTanhTerms - 2; k >= 0; --k) r = fma2(r, t, pack2(f[k], f[k]));
                 unpack2(mul2(r, y), x[2 * i], x[2 * i + 1]);
+              }
+            } else if (FORM == kWide) {
+#pragma unroll
+              for (int i = 0; i < kBlk / 2; ++i) {
+                const uint64_t y = pack2(tanh_range(x[2 * i] * cap_in),
+                                         tanh_range(x[2 * i + 1] * cap_in));
+                const uint64_t t = mul2(y, y);
+                uint64_t a = pack2(kTanhP[4], kTanhP[4]), b = pack2(kTanhQ[4], kTanhQ[4]);
+#pragma unroll
+                for (int k = 3; k >= 0; --k) {
+                  a = fma2(a, t, pack2(kTanhP[k], kTanhP[k]));
+                  b = fma2(b, t, pack2(kTanhQ[k], kTanhQ[k]));
+                }
+                float b0, b1;
+                unpack2(b, b0, b1);
+                a = mul2(mul2(a, y), pack2(rcp(b0), rcp(b1)));
+                unpack2(mul2(a, pack2(cap_out, cap_out)), x[2 * i], x[2 * i + 1]);
               }
             } else {
 #pragma unroll
@@ -1239,19 +1257,22 @@ cudaError_t setup_one(F f, int bytes, int* per_sm) {
 
 template <typename T, int ND, bool BOTH>
 cudaError_t setup_nd(int* per_sm) {
-  cudaError_t e = setup_one(attn_tc_kernel<T, ND, false, BOTH>, smem_bytes<ND>(), per_sm);
-  return e != cudaSuccess ? e
-                          : setup_one(attn_tc_kernel<T, ND, true, BOTH>, smem_bytes<ND>(), per_sm);
+  const int bytes = smem_bytes<ND>();
+  cudaError_t e = setup_one(attn_tc_kernel<T, ND, kPlain, BOTH>, bytes, per_sm);
+  if (e == cudaSuccess) e = setup_one(attn_tc_kernel<T, ND, kGeneral, BOTH>, bytes, per_sm);
+  return e != cudaSuccess ? e : setup_one(attn_tc_kernel<T, ND, kWide, BOTH>, bytes, per_sm);
 }
 
 template <typename T, int ND, bool BOTH>
 cudaError_t launch_nd(const AttnParams& p, const TcPieces& w, const CUtensorMap& qmap,
                       const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
+  Form form = form_of(p.sc);
   // the plain form takes the maximum before it scales
-  const bool gen = p.sc.softcap > 0.0f || p.sc.slopes || !(p.sc.scale > 0.0f);
-  return launch_after(
-      gen ? attn_tc_kernel<T, ND, true, BOTH> : attn_tc_kernel<T, ND, false, BOTH>, dim3(grid),
-      dim3(kThreads), smem_bytes<ND>(), s, qmap, kmap, vmap, p, w);
+  if (form == kPlain && !(p.sc.scale > 0.0f)) form = kGeneral;
+  return launch_after(form == kPlain     ? attn_tc_kernel<T, ND, kPlain, BOTH>
+                      : form == kGeneral ? attn_tc_kernel<T, ND, kGeneral, BOTH>
+                                         : attn_tc_kernel<T, ND, kWide, BOTH>,
+                      dim3(grid), dim3(kThreads), smem_bytes<ND>(), s, qmap, kmap, vmap, p, w);
 }
 
 template <typename T>
