@@ -39,7 +39,8 @@
  * Types: bf16 or fp16, one type for q, k, v, the cache and the outputs; lse
  * and slopes fp32. All pointers are device pointers owned by the caller. A
  * handle owns its workspace, is bound to one device, and serves one stream at
- * a time. Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy
+ * a time; its calls run on that device and leave the caller's current device as
+ * it is. Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy
  * default stream), allocate nothing and can be captured into a CUDA graph;
  * lengths, positions, slots and page tables are read on the device, so a graph
  * replays with new ones.

@@ -138,3 +138,22 @@ def test_create_reports_a_failing_call(F, what):
     assert F.moe_attn_create(at.moe_attn_config(8, 2, 64, 16, 64, 8, 0, 0), 0, h) == -5
     assert not h.value
     F.fake_reset()
+
+
+def test_calls_run_on_the_handles_device_and_leave_the_callers(F):
+    h = Handle(F, device=1)                 # device 0 is current throughout
+    assert F.fake_device() == 0
+    for call, launch in ((lambda: h.forward(1), "decode on 1"), (lambda: h.forward(40), "tc on 1"),
+                         (h.append, "rope on 1")):
+        assert call() == 0 and h.calls() == [launch]
+        assert F.fake_device() == 0
+        F.fake_fail(launch.split()[0].encode())  # a launch that fails
+        assert call() == -5
+        assert F.fake_device() == 0
+        F.fake_reset()
+    assert h.check() == (0, 0) and F.fake_device() == 0
+    assert F.moe_attn_destroy(h.h) == 0 and F.fake_device() == 0
+    F.fake_fail(b"malloc")
+    out = ctypes.c_void_p()
+    assert F.moe_attn_create(h.cfg, 1, out) == -5 and F.fake_device() == 0
+    F.fake_reset()

@@ -32,6 +32,29 @@ int cuda_status(cudaError_t e) {
   return MOE_ATTN_ERR_CUDA;
 }
 
+// A handle's device is current within, the caller's again behind.
+class OnDevice {
+ public:
+  explicit OnDevice(int device) {
+    error_ = cudaGetDevice(&before_);
+    if (error_ == cudaSuccess && before_ != device) {
+      error_ = cudaSetDevice(device);
+      changed_ = error_ == cudaSuccess;
+    }
+  }
+  ~OnDevice() {
+    if (changed_) cudaSetDevice(before_);
+  }
+  OnDevice(const OnDevice&) = delete;
+  OnDevice& operator=(const OnDevice&) = delete;
+  int status() const { return cuda_status(error_); }
+
+ private:
+  int before_ = -1;
+  bool changed_ = false;
+  cudaError_t error_;
+};
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int validate_config(const moe_attn_config* c) {
@@ -329,7 +352,8 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn_handle** ou
   cudaDeviceProp prop;
   if ((st = cuda_status(cudaGetDeviceProperties(&prop, device))) != MOE_ATTN_OK) return st;
   if (prop.major != 10 || prop.minor != 3) return MOE_ATTN_ERR_NO_DEVICE;
-  if ((st = cuda_status(cudaSetDevice(device))) != MOE_ATTN_OK) return st;
+  const OnDevice on(device);
+  if ((st = on.status()) != MOE_ATTN_OK) return st;
   moe_attn_handle* h = new (std::nothrow) moe_attn_handle();
   if (!h) return MOE_ATTN_ERR_CUDA;
   h->cfg = *cfg;
@@ -363,7 +387,7 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn_handle** ou
 
 int moe_attn_destroy(moe_attn_handle* h) {
   if (!h) return MOE_ATTN_OK;
-  cudaSetDevice(h->device);
+  const OnDevice on(h->device);
   cudaDeviceSynchronize();
   if (h->ws) cudaFree(h->ws);
   delete h;
@@ -388,8 +412,8 @@ int moe_attn_append(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_r
   if (!positions || !slots) return MOE_ATTN_ERR_INVALID_ARG;
   if (q && !same(q, q_out) && overlap(q, q_out, T, c.q_heads, c.head_dim))
     return MOE_ATTN_ERR_INVALID_ARG;
-  int cur = -1;
-  if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) cudaSetDevice(h->device);
+  const OnDevice on(h->device);
+  if ((st = on.status()) != MOE_ATTN_OK) return st;
   RopeParams p{};
   p.q = rows(q);
   p.q_out = rows(q_out);
@@ -442,8 +466,8 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
     return MOE_ATTN_ERR_INVALID_ARG;
   const long long max_kv = (long long)b->columns * c.page_size;
   if (max_kv > (1LL << 29)) return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;  // int32 sums of positions
-  int cur = -1;
-  if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) cudaSetDevice(h->device);
+  const OnDevice on(h->device);
+  if ((st = on.status()) != MOE_ATTN_OK) return st;
   AttnParams p{};
   p.q = rows(q);
   p.out = rows(out);
@@ -489,8 +513,9 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
 int moe_attn_check_device_errors(moe_attn_handle* h, uint32_t* flags) {
   if (!h || !flags) return MOE_ATTN_ERR_INVALID_ARG;
   *flags = 0;
-  cudaSetDevice(h->device);
-  int st;
+  const OnDevice on(h->device);
+  int st = on.status();
+  if (st != MOE_ATTN_OK) return st;
   if ((st = cuda_status(cudaDeviceSynchronize())) != MOE_ATTN_OK) return st;
   uint32_t v = 0;
   if ((st = cuda_status(cudaMemcpy(&v, h->err, 4, cudaMemcpyDeviceToHost))) != MOE_ATTN_OK)
