@@ -177,3 +177,24 @@ def test_cache_bookkeeping():
     c.release("a")
     assert c.length("a") == 0 and len(c.extend("b", 64)[1]) == 64
     assert c.tables([])[0].shape[0] == 0
+
+
+@pytest.mark.parametrize("device,index", [(None, 3), ("cuda", 3), ("cuda:0", 0), ("cuda:2", 2)])
+def test_a_layer_without_a_device_number_is_on_the_current_one(L, monkeypatch, device, index):
+    # as the cache's pages and the frequencies are
+    import torch
+    asked = []
+
+    class Library:
+        @staticmethod
+        def moe_attn_create(cfg, device, out):
+            asked.append(device)
+            return at.MOE_ATTN_ERR_DEVICE
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(at, "_lib", lambda: Library)
+    with pytest.raises(moe.MoeError):
+        moe.PagedAttention(8, 2, 64, 16, 4, 4, device=device)
+    assert asked == [index]
+    with pytest.raises(ValueError):
+        moe.PagedAttention(8, 2, 64, 16, 4, 4, device="cpu")

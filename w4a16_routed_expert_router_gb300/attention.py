@@ -205,7 +205,10 @@ class PagedAttention:
         self.cfg = moe_attn_config(q_heads, kv_heads, head_dim, page_size, max_tokens, max_seqs,
                                    _DTYPES[dtype], 0)
         self._library = _lib()
-        index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+        device = torch.device("cuda" if device is None else device)
+        if device.type != "cuda":
+            raise ValueError(f"device must be a CUDA device, got {device}")
+        index = torch.cuda.current_device() if device.index is None else device.index
         self.device = torch.device("cuda", index)
         handle = _vp()
         _check(self._library.moe_attn_create(ctypes.byref(self.cfg), index, ctypes.byref(handle)),
