@@ -27,3 +27,22 @@ def test_a_new_handle_is_ready_for_any_stream():
     s.synchronize()
     b.check(out, lse)
     assert layer.check_device_errors() == 0
+
+
+def test_a_layer_dropped_in_a_capture_does_not_end_it():
+    import gc
+    b = ac.Batch([(40, 300), (1, 70)], 8, 2, 64, 16, BF)
+    layer = moe.PagedAttention(8, 2, 64, 16, b.tokens, 2)
+    other = moe.PagedAttention(8, 2, 64, 16, 64, 4)
+    out, lse = torch.empty_like(b.q), torch.empty(b.tokens, 8, device=DEV)
+    b.run(layer, out=out, lse=lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        del other
+        gc.collect()
+        b.run(layer, out=out, lse=lse)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    b.check(out, lse)
+    assert layer.check_device_errors() == 0

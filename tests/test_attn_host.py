@@ -198,3 +198,35 @@ def test_a_layer_without_a_device_number_is_on_the_current_one(L, monkeypatch, d
     assert asked == [index]
     with pytest.raises(ValueError):
         moe.PagedAttention(8, 2, 64, 16, 4, 4, device="cpu")
+
+
+def test_layers_dropped_in_a_capture_are_destroyed_behind_it(L, monkeypatch):
+    import gc
+    import torch
+    capturing, destroyed = [True], []
+
+    class Library:
+        @staticmethod
+        def moe_attn_destroy(handle):
+            assert not capturing[0]
+            destroyed.append(handle.value)
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+
+    def layer(address):
+        a = object.__new__(moe.PagedAttention)
+        a._library, a.handle = Library, ctypes.c_void_p(address)
+        return a
+
+    first, second = layer(8), layer(16)
+    del first
+    gc.collect()
+    second.close()
+    assert second.handle is None and destroyed == []
+    second.close()
+    capturing[0] = False
+    layer(24).close()
+    assert sorted(destroyed) == [8, 16, 24]
+    second.close()
+    assert len(destroyed) == 3

@@ -186,6 +186,20 @@ def moe_attn_rope(x, positions, freq, out=None, layout="half", magnitude=1.0, in
     return done
 
 
+# Handles to be destroyed. That waits for the device, which would end a capture of
+# this thread's stream (a collection of garbage comes at any time): they stay here
+# until a layer is made or closed outside of one.
+_dropped = []
+
+
+def _destroy_dropped():
+    if not _dropped or torch.cuda.is_current_stream_capturing():
+        return
+    while _dropped:
+        library, handle = _dropped.pop()
+        _check(library.moe_attn_destroy(handle), "moe_attn_destroy")
+
+
 class PagedAttention:
     """Append and attention for layers of one shape: a handle with its
     workspace, usable by every layer of a model on one stream at a time.
@@ -210,6 +224,7 @@ class PagedAttention:
             raise ValueError(f"device must be a CUDA device, got {device}")
         index = torch.cuda.current_device() if device.index is None else device.index
         self.device = torch.device("cuda", index)
+        _destroy_dropped()
         handle = _vp()
         _check(self._library.moe_attn_create(ctypes.byref(self.cfg), index, ctypes.byref(handle)),
                "moe_attn_create")
@@ -219,7 +234,9 @@ class PagedAttention:
 
     def close(self):
         if self.handle is not None and self.handle.value:
-            _check(self._library.moe_attn_destroy(self.handle), "moe_attn_destroy")
+            _dropped.append((self._library, self.handle))
+            self.handle = None
+            _destroy_dropped()
         self.handle = None
 
     def _open(self):
