@@ -2,9 +2,9 @@
 positions, appending keys and values to a paged cache, and attention over it.
 
 Argument marshalling and checks only; the operators are the CUDA kernels of
-``libmoe_w4a16.so``. Tensors of the wrong type, device or form raise
-``ValueError`` before anything is launched; a status of the library raises
-``MoeError``.
+``libmoe_w4a16.so``. Tensors of the wrong type, device or form, and tensors that
+autograd would follow, raise ``ValueError`` before anything is launched; a status
+of the library raises ``MoeError``.
 """
 from __future__ import annotations
 
@@ -111,8 +111,9 @@ def _lib() -> ctypes.CDLL:
 
         _attn_binding.setup(address("moe_attn_rope"), address("moe_attn_append"),
                             address("moe_attn_forward"), _check, torch.empty, _raw_stream,
-                            _current_device, torch.bfloat16, torch.float16,
-                            torch.float32, torch.int32, torch.int64)
+                            _current_device, torch.is_grad_enabled,
+                            torch.is_inference_mode_enabled, _increment_version, torch.bfloat16,
+                            torch.float16, torch.float32, torch.int32, torch.int64)
         _native, _library = _attn_binding, L
     return _library
 
@@ -131,6 +132,15 @@ def _stream_address(index) -> int:
 # checks around them (2 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_address)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _increment_versions(tensors):
+    for t in tensors:
+        torch.autograd.graph.increment_version(t)
+
+
+# of a list of tensors that were written to
+_increment_version = getattr(torch._C, "_increment_version", _increment_versions)
 
 
 def _layout(layout) -> int:
@@ -173,7 +183,8 @@ def moe_attn_rope(x, positions, freq, out=None, layout="half", magnitude=1.0, in
                   stream=None):
     """Rotary positions of x [tokens, heads, head_dim] (bf16 or fp16, any token
     and head strides) at positions int32 [tokens]; out may be x. ``inverse``
-    turns the other way: the gradient of x from the gradient of the result."""
+    turns the other way: the gradient of x from the gradient of the result (autograd
+    does not follow this call, and tensors that require a gradient are refused)."""
     if _native is None:
         _lib()
     if stream is not None:

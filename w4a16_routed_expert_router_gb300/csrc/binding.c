@@ -26,8 +26,11 @@ static struct {
   forward_fn forward;
   PyObject *check;                       /* (status, what): raises */
   PyObject *empty, *raw_stream, *current_device;
+  PyObject *grad_enabled, *inference_enabled; /* of the thread */
+  PyObject *increment_version;           /* (tensors): they were written to */
   PyObject *bf16, *fp16, *f32, *i32, *i64;
-  PyObject *shape, *stride, *dtype, *device, *get_device, *data_ptr, *is_contiguous;
+  PyObject *shape, *stride, *dtype, *device, *get_device, *data_ptr, *is_contiguous,
+      *requires_grad;
   PyObject *empty_names;                 /* ("dtype", "device") */
 } G;
 
@@ -260,6 +263,62 @@ static int checked(int status, const char* what) {
   return -1;
 }
 
+/* 1, 0, or -1 with an error */
+static int asked(PyObject* what) {
+  PyObject* v = PyObject_CallNoArgs(what);
+  if (!v) return -1;
+  Py_DECREF(v);
+  return v == Py_True;
+}
+
+/* No gradient runs through these calls: refuses tensors that ask for one. */
+static int no_gradient(PyObject* const* t, int n, const char* what) {
+  const int on = asked(G.grad_enabled);
+  for (int i = 0; i < n && on == 1; ++i) {
+    if (t[i] == Py_None) continue;
+    PyObject* v = PyObject_GetAttr(t[i], G.requires_grad);
+    if (!v) return -1;
+    Py_DECREF(v);
+    if (v == Py_True) {
+      PyErr_Format(PyExc_ValueError,
+                   "%s has no autograd formula: call it under torch.no_grad(), or on detached "
+                   "tensors (the gradient of rotary positions is moe_attn_rope with inverse=True)",
+                   what);
+      return -1;
+    }
+  }
+  return on < 0 ? -1 : 0;
+}
+
+/* Tells autograd which of the outputs that the caller gave were written to, so that
+ * a backward pass that kept one raises. Inference tensors keep no count. (Not the
+ * cache's pages: 1.2 us more for each append, for tensors that are only ever read by
+ * the calls here.) */
+static int wrote(PyObject* const* t, int n) {
+  PyObject* list = NULL;
+  for (int i = 0; i < n; ++i) {
+    if (t[i] == Py_None) continue;
+    if (!list) {
+      const int inference = asked(G.inference_enabled);
+      if (inference) return inference < 0 ? -1 : 0;
+      if (!(list = PyList_New(0))) return -1;
+    }
+    if (PyList_Append(list, t[i])) {
+      Py_DECREF(list);
+      return -1;
+    }
+  }
+  if (!list) return 0;
+  PyObject* r = PyObject_CallOneArg(G.increment_version, list);
+  Py_DECREF(list);
+  if (!r) {
+    if (!PyErr_ExceptionMatches(PyExc_RuntimeError)) return -1;
+    PyErr_Clear(); /* an inference tensor outside of inference mode */
+  }
+  Py_XDECREF(r);
+  return 0;
+}
+
 static int arity(Py_ssize_t n, Py_ssize_t want, const char* what) {
   if (n == want) return 0;
   PyErr_Format(PyExc_TypeError, "%s takes %zd arguments, got %zd", what, want, n);
@@ -307,6 +366,8 @@ static PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       vector_of(a[1], tokens, G.i32, index, &pos, "positions") < 0 ||
       stream_of(a[7], index, &stream))
     return NULL;
+  PyObject* const tracked[2] = {x, a[3]};
+  if (no_gradient(tracked, 2, "moe_attn_rope")) return NULL;
   PyObject* device = PyObject_GetAttr(x, G.device);
   if (!device) return NULL;
   PyObject* out = output(a[3], tokens, d[1], d[2], dtype, device, index, &outr, "out");
@@ -316,7 +377,7 @@ static PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Py_BEGIN_ALLOW_THREADS;
   st = G.rope(&xr, &outr, pos, (int32_t)tokens, (int32_t)d[1], (int32_t)d[2], code, &r, stream);
   Py_END_ALLOW_THREADS;
-  if (checked(st, "moe_attn_rope")) Py_CLEAR(out);
+  if (checked(st, "moe_attn_rope") || wrote(a + 3, 1)) Py_CLEAR(out);
   return out;
 }
 
@@ -380,6 +441,8 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       vector_of(a[5], T, G.i64, l->index, &slots, "slots") < 0 || cache_of(l, a[6], a[7], &c) ||
       stream_of(a[12], l->index, &stream))
     return NULL;
+  PyObject* const tracked[6] = {a[1], a[2], a[3], a[6], a[7], a[11]};
+  if (no_gradient(tracked, 6, "PagedAttention.append")) return NULL;
   PyObject* out = with_q ? output(a[11], T, l->q_heads, l->dim, l->dtype, l->device, l->index, &qo,
                                   "q_out")
                          : Py_NewRef(Py_None);
@@ -389,7 +452,7 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   st = G.append(l->handle, with_q ? &q : NULL, with_q ? &qo : NULL, &k, &v, pos, slots, (int32_t)T,
                 &r, &c, stream);
   Py_END_ALLOW_THREADS;
-  if (checked(st, "moe_attn_append")) Py_CLEAR(out);
+  if (checked(st, "moe_attn_append") || wrote(a + 11, 1)) Py_CLEAR(out);
   return out;
 }
 
@@ -451,6 +514,8 @@ static PyObject* forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   }
   const int with_lse = PyObject_IsTrue(a[15]);
   if (with_lse < 0 || stream_of(a[16], l->index, &stream)) return NULL;
+  PyObject* const tracked[6] = {a[1], a[2], a[3], a[11], a[13], a[14]};
+  if (no_gradient(tracked, 6, "PagedAttention.forward")) return NULL;
   PyObject* lse;
   if (a[14] != Py_None) {
     const int ld = shape_of(a[14], d);
@@ -487,26 +552,28 @@ static PyObject* forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   status = G.forward(l->handle, &q, &o, lse_at, &c, &b, &s, stream);
   Py_END_ALLOW_THREADS;
   PyObject* result = NULL;
-  if (!checked(status, "moe_attn_forward"))
+  if (!checked(status, "moe_attn_forward") && !wrote(tracked + 4, 2))
     result = with_lse ? PyTuple_Pack(2, out, lse) : Py_NewRef(out);
   Py_DECREF(out);
   Py_DECREF(lse);
   return result;
 }
 
-/* setup(rope, append, forward, check, empty, raw_stream, current_device, bf16,
- * fp16, f32, i32, i64): addresses of the library's functions, what raises for a
+/* setup(rope, append, forward, check, empty, raw_stream, current_device,
+ * grad_enabled, inference_enabled, increment_version, bf16, fp16, f32, i32, i64): addresses of the library's functions, what raises for a
  * status, and of torch what is needed here. Once, before any other call. */
 static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (arity(n, 12, "setup")) return NULL;
+  if (arity(n, 15, "setup")) return NULL;
   G.rope = (rope_fn)PyLong_AsVoidPtr(a[0]);
   G.append = (append_fn)PyLong_AsVoidPtr(a[1]);
   G.forward = (forward_fn)PyLong_AsVoidPtr(a[2]);
   if (PyErr_Occurred()) return NULL;
-  PyObject** to[] = {&G.check, &G.empty, &G.raw_stream, &G.current_device, &G.bf16,
-                     &G.fp16,  &G.f32,   &G.i32,        &G.i64};
-  for (int i = 0; i < 9; ++i) Py_XSETREF(*to[i], Py_NewRef(a[3 + i]));
+  PyObject** to[] = {&G.check,        &G.empty,             &G.raw_stream,
+                     &G.current_device, &G.grad_enabled,    &G.inference_enabled,
+                     &G.increment_version, &G.bf16,         &G.fp16,
+                     &G.f32,          &G.i32,               &G.i64};
+  for (int i = 0; i < 12; ++i) Py_XSETREF(*to[i], Py_NewRef(a[3 + i]));
   Py_RETURN_NONE;
 }
 
@@ -529,9 +596,10 @@ PyMODINIT_FUNC PyInit__attn_binding(void) {
   G.get_device = PyUnicode_InternFromString("get_device");
   G.data_ptr = PyUnicode_InternFromString("data_ptr");
   G.is_contiguous = PyUnicode_InternFromString("is_contiguous");
+  G.requires_grad = PyUnicode_InternFromString("requires_grad");
   G.empty_names = Py_BuildValue("(ss)", "dtype", "device");
   if (!G.shape || !G.stride || !G.dtype || !G.device || !G.get_device || !G.data_ptr ||
-      !G.is_contiguous || !G.empty_names)
+      !G.is_contiguous || !G.requires_grad || !G.empty_names)
     return NULL;
   return PyModule_Create(&module);
 }
