@@ -104,7 +104,13 @@ def _lib() -> ctypes.CDLL:
         from . import lib
         L = lib()
         register(L)
-        from . import _attn_binding
+        try:
+            from . import _attn_binding
+        except ImportError as e:
+            raise RuntimeError(
+                "the attention operators' Python binding is missing for this interpreter: build it "
+                "with `python -m w4a16_routed_expert_router_gb300._build` (it needs the Python "
+                "headers)") from e
 
         def address(name):
             return ctypes.cast(getattr(L, name), ctypes.c_void_p).value
