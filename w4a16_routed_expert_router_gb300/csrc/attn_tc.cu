@@ -1115,9 +1115,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (p.sc.slopes) {
-            // distances are whole numbers: exact steps of -1 from key to key
+            // distances are whole numbers: exact steps of -1 from key to key, where
+            // fp32 holds them all and no key lies ahead of its query
             const float far = (float)(pos - kb);
-            if (kb + kBlk - 1 <= p_first) {  // no key lies ahead of its query
+            if (kb + kBlk - 1 <= p_first && p_first - kb < (1 << 24) - 128) {
               uint64_t away = pack2(far, far - 1.0f);
 #pragma unroll
               for (int i = 0; i < kBlk / 2; ++i) {
