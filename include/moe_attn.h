@@ -152,7 +152,8 @@ int moe_attn_rope_frequencies(int32_t rot_dim, double base, double factor, int32
 
 /* out = rotary positions of x, [num_tokens, heads, head_dim] each; positions
  * [num_tokens]. head_dim 1..256, heads 0..65536. Any element strides (16-byte multiples are
- * fastest); out == x with equal strides is allowed, other overlaps are not. */
+ * fastest); out == x with equal strides is allowed, other overlaps are not, nor is
+ * an output whose rows lie on each other (broadcast). */
 int moe_attn_rope(const moe_attn_rows* x, const moe_attn_rows* out, const int32_t* positions,
                   int32_t num_tokens, int32_t heads, int32_t head_dim, int32_t dtype,
                   const moe_attn_rotation* rotation, void* stream);

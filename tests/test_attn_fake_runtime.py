@@ -157,3 +157,39 @@ def test_calls_run_on_the_handles_device_and_leave_the_callers(F):
     out = ctypes.c_void_p()
     assert F.moe_attn_create(h.cfg, 1, out) == -5 and F.fake_device() == 0
     F.fake_reset()
+
+
+@pytest.mark.parametrize("token,head,status", [
+    (512, 64, 0), (64, 128, 0), (1000, 72, 0), (64, 512, 0), (100, 200, 0), (0, 64, -1),
+    (128, 0, -1), (32, 256, -1), (256, 56, -1), (128, 64, -1), (450, 72, -1), (250, 72, -1),
+    (504, 72, -1), (570, 72, 0)])
+def test_outputs_whose_rows_lie_on_each_other_are_refused(F, token, head, status):
+    at_rows = [set(range(t * token + h * head, t * token + h * head + 64))
+               for t in range(2) for h in range(8)]
+    assert (status == 0) == (len(set.union(*at_rows)) == 2 * 8 * 64)
+    # q and out apart, 8 heads of 64; a turn in place of such rows as well
+    h = Handle(F)
+    x, out = at.moe_attn_rows(1 << 22, 512, 64), at.moe_attn_rows(1 << 23, token, head)
+    r = at.moe_attn_rotation(64, 64, 0, 1.0, 0)
+    assert F.moe_attn_rope(x, out, 64, 2, 8, 64, 0, r, None) == status
+    assert F.moe_attn_rope(out, out, 64, 2, 8, 64, 0, r, None) == status
+    # one row of each is no matter
+    assert F.moe_attn_rope(x, at.moe_attn_rows(1 << 23, 0, 0), 64, 1, 1, 64, 0, r, None) == 0
+    kv = at.moe_attn_rows(1 << 24, 128, 64)
+    cache = at.moe_attn_cache(1 << 20, 1 << 21, 9, 2 * 16 * 64, 64, 16 * 64)
+    assert F.moe_attn_append(h.h, x, out, kv, kv, 64, 64, 2, r, cache, None) == status
+    batch = at.moe_attn_batch(64, 64, 64, 4, 4, 1, 2, 2)
+    if token % 8 == 0 and head % 8 == 0:
+        assert F.moe_attn_forward(h.h, x, out, None, cache, batch,
+                                  at.moe_attn_scores(0.125, 0.0, 0, None, None), None) == status
+    assert F.moe_attn_destroy(h.h) == 0
+
+
+def test_long_outputs_are_checked_in_no_time(F):
+    # a million tokens in between the heads, and heads in between the tokens
+    r = at.moe_attn_rotation(64, 64, 0, 1.0, 0)
+    for token, head, n, heads in ((64, 64 << 20, 1 << 20, 8), (64 * 8, 64, 1 << 20, 8),
+                                  (64, 0, 1 << 20, 1), (0, 64, 1, 65536)):
+        x, out = at.moe_attn_rows(0, token, head), at.moe_attn_rows(1 << 40, token, head)
+        x.data = 1 << 22
+        assert F.moe_attn_rope(x, out, 64, n, heads, 64, 0, r, None) == 0

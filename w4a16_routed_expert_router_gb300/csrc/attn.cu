@@ -4,6 +4,7 @@
 #include <cstdio>
 #include <initializer_list>
 #include <new>
+#include <utility>
 
 #include "attn.h"
 #include "tensor_map.h"
@@ -101,6 +102,24 @@ bool overlap(const moe_attn_rows* a, const moe_attn_rows* b, int tokens, int hea
   const uintptr_t pa = reinterpret_cast<uintptr_t>(a->data);
   const uintptr_t pb = reinterpret_cast<uintptr_t>(b->data);
   return pa < pb + span(b) && pb < pa + span(a);
+}
+
+// rows to be written: no row lies on another (of a broadcast output, whichever row
+// came last would stay)
+bool apart(const moe_attn_rows* r, int tokens, int heads, int dim) {
+  long long near = r->head_stride, far = r->token_stride;
+  long long n_near = heads, n_far = tokens;
+  if (n_far > 1 && (n_near <= 1 || far < near)) {
+    std::swap(near, far);
+    std::swap(n_near, n_far);
+  }
+  if (n_near > 1 && near < dim) return false;
+  for (long long j = 1; j < n_far && j * far < (n_near - 1) * near + dim; ++j) {
+    if (n_near <= 1) return false;
+    const long long i = j * far / near, rest = j * far % near;  // between rows i and i + 1
+    if ((i < n_near && rest < dim) || (i + 1 < n_near && near - rest < dim)) return false;
+  }
+  return true;
 }
 
 bool same(const moe_attn_rows* a, const moe_attn_rows* b) {
@@ -318,7 +337,9 @@ int moe_attn_rope(const moe_attn_rows* x, const moe_attn_rows* out, const int32_
   if (T == 0 || heads == 0) return MOE_ATTN_OK;
   if ((st = validate_rows(x)) != MOE_ATTN_OK || (st = validate_rows(out)) != MOE_ATTN_OK) return st;
   if (!positions) return MOE_ATTN_ERR_INVALID_ARG;
-  if (!same(x, out) && overlap(x, out, T, heads, head_dim)) return MOE_ATTN_ERR_INVALID_ARG;
+  if (!apart(out, T, heads, head_dim) ||
+      (!same(x, out) && overlap(x, out, T, heads, head_dim)))
+    return MOE_ATTN_ERR_INVALID_ARG;
   RopeParams p{};
   p.q = rows(x);
   p.q_out = rows(out);
@@ -410,7 +431,8 @@ int moe_attn_append(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_r
     return st;
   if ((st = validate_rows(k)) != MOE_ATTN_OK || (st = validate_rows(v)) != MOE_ATTN_OK) return st;
   if (!positions || !slots) return MOE_ATTN_ERR_INVALID_ARG;
-  if (q && !same(q, q_out) && overlap(q, q_out, T, c.q_heads, c.head_dim))
+  if (q && (!apart(q_out, T, c.q_heads, c.head_dim) ||
+            (!same(q, q_out) && overlap(q, q_out, T, c.q_heads, c.head_dim))))
     return MOE_ATTN_ERR_INVALID_ARG;
   const OnDevice on(h->device);
   if ((st = on.status()) != MOE_ATTN_OK) return st;
@@ -455,7 +477,9 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
   if (!aligned16(q->data) || !aligned16(out->data) || q->token_stride % 8 || q->head_stride % 8 ||
       out->token_stride % 8 || out->head_stride % 8)
     return MOE_ATTN_ERR_MISALIGNED;
-  if (overlap(q, out, b->num_tokens, c.q_heads, c.head_dim)) return MOE_ATTN_ERR_INVALID_ARG;
+  if (!apart(out, b->num_tokens, c.q_heads, c.head_dim) ||
+      overlap(q, out, b->num_tokens, c.q_heads, c.head_dim))
+    return MOE_ATTN_ERR_INVALID_ARG;
   for (const moe_attn_rows* r : {q, out}) {  // broadcast rows are not taken here
     if ((r->token_stride == 0 && b->num_tokens > 1) || (r->head_stride == 0 && c.q_heads > 1))
       return MOE_ATTN_ERR_INVALID_ARG;
