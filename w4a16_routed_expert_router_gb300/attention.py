@@ -39,6 +39,7 @@ _LAYOUTS = {"half": MOE_ATTN_ROPE_HALF, "interleaved": MOE_ATTN_ROPE_INTERLEAVED
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 
+# The C ABI's structures, for calls by ctypes; the calls below go through csrc/binding.c.
 class moe_attn_rows(ctypes.Structure):
     _fields_ = [("data", _vp), ("token_stride", _i64), ("head_stride", _i64)]
 

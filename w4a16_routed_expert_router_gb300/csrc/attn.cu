@@ -496,12 +496,7 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
   p.q = rows(q);
   p.out = rows(out);
   p.lse = lse;
-  p.k_pages = static_cast<const uint16_t*>(cache->k);
-  p.v_pages = static_cast<const uint16_t*>(cache->v);
   p.num_pages = cache->num_pages;
-  p.page_stride = cache->page_stride;
-  p.token_stride = cache->token_stride;
-  p.head_stride = cache->head_stride;
   p.b = Batch{b->cu_q, b->kv_len, b->page_table, b->table_stride, b->columns, b->num_seqs,
               b->num_tokens, b->max_q};
   // a window as long as the table hides nothing

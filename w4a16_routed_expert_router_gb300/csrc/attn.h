@@ -93,9 +93,7 @@ struct Boxes {
 struct AttnParams {
   Rows q, out;
   float* lse;
-  const uint16_t* k_pages;
-  const uint16_t* v_pages;
-  long long num_pages, page_stride, token_stride, head_stride;
+  long long num_pages;
   Batch b;
   Scores sc;
   int hq, hk, group, head_dim, page_shift;

@@ -39,7 +39,7 @@ using namespace tc;
 
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = (kSoftmaxWarps + 4) * 32;  // whole warpgroups: setmaxnreg
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kClearWarp = 10, kWalkWarp = 11;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kClearWarp = 10;  // and 11, which walks the share
 constexpr int kPieceReaders = kSoftmaxWarps + 3;
 // Registers a thread: the launch gives every thread kLaunchRegs; the producer
 // warpgroup hands most of its share to the two softmax warpgroups, whose rows
