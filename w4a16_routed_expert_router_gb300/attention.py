@@ -169,6 +169,16 @@ def _on_stream(stream, out, shape, dtype, device):
     return stream.cuda_stream, out
 
 
+def _in_use(stream, *tensors):
+    """Memory of tensors that a call on a given stream works on is not handed out
+    again before it is done, though they belong to another."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def moe_attn_rope_frequencies(rot_dim, base=10000.0, factor=1.0, by_parts=False,
                               original_len=4096.0, beta_fast=32.0, beta_slow=1.0, device="cuda"):
     """(freq, magnitude) of rotary positions over rot_dim values of a head.
@@ -194,6 +204,7 @@ def moe_attn_rope(x, positions, freq, out=None, layout="half", magnitude=1.0, in
     does not follow this call, and tensors that require a gradient are refused)."""
     if _native is None:
         _lib()
+    given = stream
     if stream is not None:
         stream, out = _on_stream(stream, out, x.shape, x.dtype, x.device)
     args = (x, positions, freq, out, _layout(layout), magnitude, inverse, stream)
@@ -201,6 +212,8 @@ def moe_attn_rope(x, positions, freq, out=None, layout="half", magnitude=1.0, in
     if done is NotImplemented:  # another device is current
         with torch.cuda.device(x.device):
             done = _native.rope(*args)
+    if given is not None:
+        _in_use(given, x, positions, freq, out)
     return done
 
 
@@ -288,13 +301,17 @@ class PagedAttention:
         write k and v to their slots (int64; page * page_size + offset, negative:
         not written) of the cache. Returns q_out (new unless given, may be q);
         q None: keys and values only."""
+        given = stream
         if stream is not None:
             if q is not None:
                 stream, q_out = _on_stream(stream, q_out, q.shape, self.dtype, self.device)
             elif not isinstance(stream, int):
                 stream = stream.cuda_stream
-        return _native.append(self._open(), q, k, v, positions, slots, k_pages, v_pages, freq,
+        done = _native.append(self._open(), q, k, v, positions, slots, k_pages, v_pages, freq,
                               _layout(layout), magnitude, q_out, stream)
+        if given is not None:
+            _in_use(given, q, k, v, positions, slots, k_pages, v_pages, freq, q_out)
+        return done
 
     def forward(self, q, k_pages, v_pages, page_table, cu_q, kv_len, max_q, scale=None,
                 softcap=0.0, window=0, slopes=None, prefix=None, out=None, lse=None,
@@ -307,13 +324,17 @@ class PagedAttention:
         no sequence has more new tokens. scale defaults to 1 / sqrt(head_dim).
         Returns out, or (out, lse) with lse fp32 [tokens, q_heads].
         """
+        given = stream
         if stream is not None:
             if return_lse and lse is None:
                 _, lse = _on_stream(stream, None, q.shape[:2], torch.float32, self.device)
             stream, out = _on_stream(stream, out, q.shape, self.dtype, self.device)
-        return _native.forward(self._open(), q, k_pages, v_pages, page_table, cu_q, kv_len, max_q,
+        done = _native.forward(self._open(), q, k_pages, v_pages, page_table, cu_q, kv_len, max_q,
                                scale, softcap, window, slopes, prefix, out, lse, return_lse,
                                stream)
+        if given is not None:
+            _in_use(given, q, k_pages, v_pages, page_table, cu_q, kv_len, slopes, prefix, out, lse)
+        return done
 
 
 class PagedKvCache:
