@@ -13,8 +13,8 @@ namespace moe {
 namespace attn {
 cudaError_t launch_rope(const RopeParams&, int, cudaStream_t) { return fake_call("rope", true); }
 cudaError_t attn_decode_setup() { return fake_call("decode setup", false); }
-cudaError_t attn_tc_setup(int* n) {
-  *n = 1;
+cudaError_t attn_tc_setup(bool* usable) {
+  *usable = fake_call("tc usable", false) == cudaSuccess;
   return fake_call("tc setup", false);
 }
 cudaError_t launch_attn_decode(const AttnParams&, const Partials& w, const CUtensorMap&,

@@ -193,3 +193,19 @@ def test_long_outputs_are_checked_in_no_time(F):
         x, out = at.moe_attn_rows(0, token, head), at.moe_attn_rows(1 << 40, token, head)
         x.data = 1 << 22
         assert F.moe_attn_rope(x, out, 64, n, heads, 64, 0, r, None) == 0
+
+
+def test_single_tokens_run_where_the_tensor_core_kernel_does_not(F):
+    # built with other registers than its warps hand each other, it would wait for
+    # ever: it is refused, and only it
+    F.fake_reset()
+    F.fake_fail(b"tc usable")
+    h = ctypes.c_void_p()
+    assert F.moe_attn_create(at.moe_attn_config(8, 2, 64, 16, 64, 8, 0, 0), 0, h) == 0
+    F.fake_reset()
+    handle = object.__new__(Handle)
+    handle.F, handle.h = F, h
+    assert handle.forward(1) == 0 and handle.calls() == ["decode on 0"]
+    assert handle.append() == 0 and handle.calls() == ["rope on 0"]
+    assert handle.forward(40) == -5 and handle.calls() == []
+    assert F.moe_attn_destroy(h) == 0

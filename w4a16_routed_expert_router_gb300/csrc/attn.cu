@@ -21,6 +21,7 @@ struct moe_attn_handle {
   unsigned* err = nullptr;
   Partials decode{};
   TcPieces tc{};
+  bool tc_usable = false;
 };
 // The error word is the workspace's first; tests set its bits through here.
 static_assert(offsetof(moe_attn_handle, ws) == sizeof(moe_attn_config) + 8, "place of ws");
@@ -382,11 +383,8 @@ int moe_attn_create(const moe_attn_config* cfg, int device, moe_attn_handle** ou
   h->num_sms = prop.multiProcessorCount;
   h->grid = h->num_sms < kMaxGrid ? h->num_sms : kMaxGrid;
   const Layout L = plan(*cfg);
-  int per_sm = 0;
   if ((st = cuda_status(attn_decode_setup())) != MOE_ATTN_OK ||
-      (st = cuda_status(attn_tc_setup(&per_sm))) != MOE_ATTN_OK ||
-      // a CTA of the tensor-core kernel holds all of its SM's TMEM
-      (st = per_sm == 1 ? MOE_ATTN_OK : MOE_ATTN_ERR_CUDA) != MOE_ATTN_OK ||
+      (st = cuda_status(attn_tc_setup(&h->tc_usable))) != MOE_ATTN_OK ||
       (st = cuda_status(cudaMalloc(&h->ws, L.total))) != MOE_ATTN_OK ||
       (st = cuda_status(cudaMemset(h->ws, 0, L.total))) != MOE_ATTN_OK ||
       // cudaMemset does not wait, and other streams do not wait for it
@@ -520,6 +518,10 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
         (st = encode_cache_chunks(&vmap, c, cache, cache->v, box)) != MOE_ATTN_OK)
       return st;
     return cuda_status(launch_attn_decode(p, h->decode, kmap, vmap, c.dtype, h->grid, s));
+  }
+  if (!h->tc_usable) {  // another compiler: few-token batches go on
+    fprintf(stderr, "moe_attn: the tensor-core kernel was built with other registers than it needs\n");
+    return MOE_ATTN_ERR_CUDA;
   }
   p.boxes = tc_boxes(c, cache);
   if ((st = encode_tc_cache(&kmap, c, cache, cache->k, p.boxes)) != MOE_ATTN_OK ||

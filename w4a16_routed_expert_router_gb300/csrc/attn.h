@@ -214,7 +214,8 @@ struct TcPieces {
 
 __host__ __device__ inline int tile_tokens(int group) { return 128 / group; }
 
-cudaError_t attn_tc_setup(int* ctas_per_sm);
+// *usable: the kernels came out of the compiler with what they rely on
+cudaError_t attn_tc_setup(bool* usable);
 cudaError_t launch_attn_tc(const AttnParams& p, const TcPieces& w, const CUtensorMap& qmap,
                            const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, int grid,
                            cudaStream_t s);

@@ -1243,25 +1243,26 @@ static_assert(2 * smem_bytes<1>() > 228 * 1024 && 2 * smem_bytes<2>() > 228 * 10
 static_assert(smem_bytes<2>() <= 227 * 1024, "shared memory of a CTA");
 
 template <typename F>
-cudaError_t setup_one(F f, int bytes, int* per_sm) {
+cudaError_t setup_one(F f, int bytes, bool* usable) {
   cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   cudaFuncAttributes attr;
   if ((e = cudaFuncGetAttributes(&attr, f)) != cudaSuccess) return e;
-  // with fewer at launch the softmax warps would wait for registers for ever
-  if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
   int n = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, kThreads, bytes);
-  if (n != 1) *per_sm = n;
-  return e;
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, kThreads, bytes)) != cudaSuccess)
+    return e;
+  // With fewer registers at launch the softmax warps would wait for more for ever,
+  // and a CTA holds all of its SM's TMEM.
+  if (attr.numRegs != kLaunchRegs || n != 1) *usable = false;
+  return cudaSuccess;
 }
 
 template <typename T, int ND, bool BOTH>
-cudaError_t setup_nd(int* per_sm) {
+cudaError_t setup_nd(bool* usable) {
   const int bytes = smem_bytes<ND>();
-  cudaError_t e = setup_one(attn_tc_kernel<T, ND, kPlain, BOTH>, bytes, per_sm);
-  if (e == cudaSuccess) e = setup_one(attn_tc_kernel<T, ND, kGeneral, BOTH>, bytes, per_sm);
-  return e != cudaSuccess ? e : setup_one(attn_tc_kernel<T, ND, kWide, BOTH>, bytes, per_sm);
+  cudaError_t e = setup_one(attn_tc_kernel<T, ND, kPlain, BOTH>, bytes, usable);
+  if (e == cudaSuccess) e = setup_one(attn_tc_kernel<T, ND, kGeneral, BOTH>, bytes, usable);
+  return e != cudaSuccess ? e : setup_one(attn_tc_kernel<T, ND, kWide, BOTH>, bytes, usable);
 }
 
 template <typename T, int ND, bool BOTH>
@@ -1286,15 +1287,15 @@ cudaError_t launch_t(const AttnParams& p, const TcPieces& w, const CUtensorMap& 
 
 }  // namespace
 
-cudaError_t attn_tc_setup(int* ctas_per_sm) {
-  *ctas_per_sm = 1;
+cudaError_t attn_tc_setup(bool* usable) {
+  *usable = true;
   cudaError_t e;
-  if ((e = setup_nd<Bf16, 1, false>(ctas_per_sm)) != cudaSuccess) return e;
-  if ((e = setup_nd<Bf16, 2, false>(ctas_per_sm)) != cudaSuccess) return e;
-  if ((e = setup_nd<Bf16, 2, true>(ctas_per_sm)) != cudaSuccess) return e;
-  if ((e = setup_nd<Fp16, 1, false>(ctas_per_sm)) != cudaSuccess) return e;
-  if ((e = setup_nd<Fp16, 2, false>(ctas_per_sm)) != cudaSuccess) return e;
-  return setup_nd<Fp16, 2, true>(ctas_per_sm);
+  if ((e = setup_nd<Bf16, 1, false>(usable)) != cudaSuccess) return e;
+  if ((e = setup_nd<Bf16, 2, false>(usable)) != cudaSuccess) return e;
+  if ((e = setup_nd<Bf16, 2, true>(usable)) != cudaSuccess) return e;
+  if ((e = setup_nd<Fp16, 1, false>(usable)) != cudaSuccess) return e;
+  if ((e = setup_nd<Fp16, 2, false>(usable)) != cudaSuccess) return e;
+  return setup_nd<Fp16, 2, true>(usable);
 }
 
 cudaError_t launch_attn_tc(const AttnParams& p, const TcPieces& w, const CUtensorMap& qmap,
