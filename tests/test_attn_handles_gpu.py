@@ -46,3 +46,18 @@ def test_a_layer_dropped_in_a_capture_does_not_end_it():
     torch.cuda.synchronize()
     b.check(out, lse)
     assert layer.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_strides_of_single_elements_say_nothing(n):
+    # a cache of one page and one kv head, K and V cut from differently wide buffers
+    b = ac.Batch([(n, 16)], 20, 1, 64, 16, BF)
+    layer = moe.PagedAttention(20, 1, 64, 16, n, 1)
+    page = int(b.table[0, 0])
+    b.k_pages = b.k_pages[page:page + 1].as_strided((1, 1, 16, 64), (7, 3, 64, 1))
+    v = torch.zeros(1, 5, 16, 64, dtype=BF, device=DEV)
+    v[:, 2] = b.v_pages[page]
+    b.v_pages = v[:, 2:3]
+    b.table = torch.zeros_like(b.table)
+    b.check(*b.run(layer))
+    assert layer.check_device_errors() == 0

@@ -238,7 +238,7 @@ static int cache_of(const layer_t* l, PyObject* k, PyObject* v, moe_attn_cache* 
   }
   if (strides_of(k, s) < 0 || strides_of(v, s2) < 0) return -1;
   int same = n2 == 4 && s[3] == 1;
-  for (int i = 0; same && i < 4; ++i) same = d[i] == d2[i] && s[i] == s2[i];
+  for (int i = 0; same && i < 4; ++i) same = d[i] == d2[i] && (s[i] == s2[i] || d[i] == 1);
   if (!same) {
     PyErr_SetString(PyExc_ValueError,
                     "k_pages and v_pages must have one shape and strides, head_dim contiguous");
