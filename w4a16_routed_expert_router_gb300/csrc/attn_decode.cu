@@ -156,6 +156,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const Partials ws) {
   typedef Smem<ND> S;
   constexpr int kBlk = decode_block(ND), kSub = S::kSub;
+  // Weights are in units of 2^m, m the running maximum less kUp: fp16 keeps all bits
+  // of those down to 2^-29 of the largest then, and not 2^-14 (below 2^-25 they would
+  // vanish).
+  constexpr float kUp = T::kFp16 ? 15.0f : 0.0f;
   extern __shared__ uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) sacc[t][i] = score<kPlain>(p.sc, sacc[t][i], 0.0f, 0);
           }
-          float mx[2] = {m[0], m[1]};
+          float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int t = 0; t < 2 * kSub; ++t)
 #pragma unroll
@@ -422,6 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int r = 0; r < 2; ++r) {
             mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
             mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+            // up: no numerator above 2^kUp
+            mx[r] = fmaxf(m[r], __fadd_ru(mx[r], -kUp));
             base[r] = mx[r] == -INFINITY ? 0.0f : mx[r];
             scale[r] = ex2(m[r] - base[r]);
             m[r] = mx[r];

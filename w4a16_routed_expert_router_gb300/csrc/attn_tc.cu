@@ -15,9 +15,9 @@
 // of both tiles fill the 512 columns of TMEM, and P (16 bits) takes the place
 // of S, whose row a thread has in registers by then, as the A operand in TMEM.
 //   warps 0-3, 4-7  softmax of tile 0 / 1: one row per thread. The running
-//             maximum is only raised when a row exceeds it by 2^8, so that O is
-//             rescaled (by the same threads, in TMEM) in few blocks; numerators
-//             stay below 2^8 and the result is exact either way.
+//             maximum is only raised when a row exceeds it by 2^8 (2^3 in fp16), so
+//             that O is rescaled (by the same threads, in TMEM) in few blocks;
+//             numerators stay below that and the result is exact either way.
 //   warp 8    TMA producer: Q, and K and V blocks into one ring of slots.
 //   warp 9    MMA issuer. While one tile's softmax runs, the tensor core works
 //             on the other: PV0(j) QK0(j+1) PV1(j) QK1(j+1) ... (A thread for
@@ -75,7 +75,15 @@ constexpr float kTanhMax = 0.6f;
 constexpr int kTanhTerms = 5;
 __device__ constexpr float kTanh[kTanhTerms] = {0.99999992687f, -0.3333230997f, 0.13310173604f,
                                                 -0.052101477875f, 0.01547542443f};
-constexpr float kRaise = 8.0f;      // log2 units
+// A row's maximum is raised when scores exceed it by kRaise (log2 units). Numerators,
+// and so their sums, are 2^kUp times what they would be by the maximum: fp16 holds
+// up to 2^15 and, with all its bits, down to 2^-14, so weights of 2^-26 of the
+// largest and above keep theirs (without it they lose them below 2^-14, and vanish
+// below 2^-25: a hundred thousand keys each 2^-25 of one were not there).
+template <typename T>
+constexpr float kRaise = T::kFp16 ? 3.0f : 8.0f;
+template <typename T>
+constexpr float kUp = T::kFp16 ? 12.0f : 0.0f;
 
 // one value per warp of a scan over the CTA
 struct Scan {
@@ -480,11 +488,11 @@ __device__ __forceinline__ void divide(const AttnParams& p, Scan& sc, uint8_t* r
   }
 }
 
-// What a softmax group does with the rows of a piece when its blocks are done: m
-// in log2 units and l of this thread's row, O in TMEM (cnt > 0). Its loops are
-// not unrolled: the code runs once a piece, and what it takes is mostly the
-// fetching of its instructions (unrolled, a whole item's results took 6500
-// cycles to store, 3300 so).
+// What a softmax group does with the rows of a piece when its blocks are done: of
+// this thread's row, m, the logarithm of its sums' unit, and l, its sum of weights;
+// O in TMEM (cnt > 0). Its loops are not unrolled: the code runs once a piece, and
+// what it takes is mostly the fetching of its instructions (unrolled, a whole
+// item's results took 6500 cycles to store, 3300 so).
 template <typename T, int ND, bool CUT>
 __device__ __forceinline__ void finish_piece(const AttnParams& p, const TcPieces& ws, Smem<ND>& s,
                                           const Piece* piece, int t, uint32_t o_tm, int cnt,
@@ -1014,10 +1022,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_tm = tmem + lane_base + t * 128;
     const uint32_t o_tm = tmem + lane_base + 256 + t * ND * 64;
     const int tok = row / p.group, hg = row - tok * p.group;  // token of the tile, head of the group
-    // scores are dot products until the exponent (plain), or log2 units (GEN)
-    const float c = GEN ? 1.0f : p.sc.scale * kLog2e;
-    const float raise = GEN ? kRaise : kRaise / c;
     const float scale2 = p.sc.scale * kLog2e;
+    // scores are dot products until the exponent (plain), or log2 units (GEN)
+    const float c = GEN ? 1.0f : scale2, raise = GEN ? kRaise<T> : kRaise<T> / c;
     const float cap_in = p.sc.cap_in;
     const float cap_out = p.sc.softcap * kLog2e;
     uint32_t sph = 0, oph = 0;
@@ -1039,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float slope =
           GEN && p.sc.slopes ? p.sc.slopes[held->head * p.group + hg] * kLog2e : 0.0f;
       const bool mine = tok < ntok;                       // this row exists
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, ref = -INFINITY, l = 0.0f;  // ref: 2^ref is the sums' unit
       bool ok = true;
       for (int j = 0; j < cnt; ++j) {
         if (!(ok = warp_wait(&s.s_full[t], sph, p.err))) break;
@@ -1152,12 +1159,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k) mt[k] = max3(mt[k], x[i + 2 * k], x[i + 2 * k + 1]);
         const float mx = fmaxf(max3(max3(mt[0], x[124], x[125]), mt[1], mt[2]),
                                max3(mt[3], x[126], x[127]));
-        // each row by its own scores: what shares its warp does not change it
-        const bool up = mx > m + raise;
+        // each row by its own scores: what shares its warp does not change it (rounded
+        // so that no numerator passes its limit, however large the scores)
+        const bool up = mx > __fadd_rd(m, raise);
         if (__any_sync(0xffffffffu, up)) {
-          const float a = up ? ex2((m - mx) * c) : 1.0f;
+          const float to = __fmaf_ru(mx, c, -kUp<T>);
+          const float a = up ? ex2(ref - to) : 1.0f;
           l *= a;
           m = up ? mx : m;
+          ref = up ? to : ref;
           if (j > 0) {
 #pragma unroll
             for (int i = 0; i < ND * 4; ++i) {
@@ -1171,7 +1181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float base = m == -INFINITY ? 0.0f : m * c;
+        const float base = ref == -INFINITY ? 0.0f : ref;
         const uint64_t c2 = pack2(c, c), base2 = pack2(-base, -base);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -1213,7 +1223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // has none, and a warp that gave up takes part in the group's next vote, the
       // one above, from here.
       if ((!ok || held->pieces) && !group_all(t, ok)) break;
-      finish_piece<T, ND, kCut>(p, ws, s, held, t, o_tm, cnt, m * c, l);
+      finish_piece<T, ND, kCut>(p, ws, s, held, t, o_tm, cnt, ref, l);
       if (cnt > 0) {
         tc_fence_before();
         __syncwarp();
@@ -1269,8 +1279,9 @@ template <typename T, int ND, bool BOTH>
 cudaError_t launch_nd(const AttnParams& p, const TcPieces& w, const CUtensorMap& qmap,
                       const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
   Form form = form_of(p.sc);
-  // the plain form takes the maximum before it scales
-  if (form == kPlain && !(p.sc.scale > 0.0f)) form = kGeneral;
+  // The plain form takes the maximum before it scales, and tells a score's distance
+  // from it by one fused multiply-add, whose parts should stay below 2^26.
+  if (form == kPlain && !(p.sc.scale > 0.0f && p.sc.scale <= 16.0f)) form = kGeneral;
   return launch_after(form == kPlain     ? attn_tc_kernel<T, ND, kPlain, BOTH>
                       : form == kGeneral ? attn_tc_kernel<T, ND, kGeneral, BOTH>
                                          : attn_tc_kernel<T, ND, kWide, BOTH>,
