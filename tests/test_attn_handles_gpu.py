@@ -61,3 +61,20 @@ def test_strides_of_single_elements_say_nothing(n):
     b.table = torch.zeros_like(b.table)
     b.check(*b.run(layer))
     assert layer.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("group", [1, 4, 20])
+def test_new_tokens_that_max_q_does_not_allow_are_reported(group):
+    b = ac.Batch([(3, 40), (0, 9), (2, 20)], group, 1, 64, 16, BF)
+    layer = moe.PagedAttention(group, 1, 64, 16, b.tokens, 3)
+    for max_q, flags in ((3, 0), (2, 0x2), (1, 0x2), (0, 0x2)):
+        b.max_q = max_q
+        out, lse = torch.full_like(b.q, 7.0), torch.full((b.tokens, group), 7.0, device=DEV)
+        b.run(layer, out=out, lse=lse)
+        assert layer.check_device_errors() == flags
+        kept = [n > max_q for n, _ in b.lens]
+        assert bool((out[:3] == 7.0).all()) == kept[0] and bool((out[3:] == 7.0).all()) == kept[2]
+    # none at all: nothing to report
+    b.cu_q, b.max_q = torch.zeros_like(b.cu_q), 0
+    b.run(layer)
+    assert layer.check_device_errors() == 0

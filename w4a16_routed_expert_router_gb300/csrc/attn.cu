@@ -470,7 +470,8 @@ int moe_attn_forward(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
     return MOE_ATTN_ERR_INVALID_ARG;
   int st = validate_cache(cache);
   if (st != MOE_ATTN_OK) return st;
-  if (b->num_tokens == 0 || b->num_seqs == 0 || b->max_q == 0) return MOE_ATTN_OK;
+  // (with a max_q of 0 the device finds out whether the sequences are empty)
+  if (b->num_tokens == 0 || b->num_seqs == 0) return MOE_ATTN_OK;
   if ((st = validate_rows(q)) != MOE_ATTN_OK || (st = validate_rows(out)) != MOE_ATTN_OK) return st;
   if (!aligned16(q->data) || !aligned16(out->data) || q->token_stride % 8 || q->head_stride % 8 ||
       out->token_stride % 8 || out->head_stride % 8)
