@@ -209,3 +209,36 @@ def test_single_tokens_run_where_the_tensor_core_kernel_does_not(F):
     assert handle.append() == 0 and handle.calls() == ["rope on 0"]
     assert handle.forward(40) == -5 and handle.calls() == []
     assert F.moe_attn_destroy(h) == 0
+
+
+def test_parts_of_one_buffer_do_not_overlap(F):
+    # inputs and outputs with the same strides: against the elements themselves
+    import random
+    rng = random.Random(4)
+    r = at.moe_attn_rotation(16, 16, 0, 1.0, 0)
+    seen = set()
+    for _ in range(3000):
+        T, H = rng.choice([1, 2, 3, 5]), rng.choice([1, 2, 4])
+        a, b = 16 + rng.choice([0, 0, 8, 16, 100]), rng.choice([1, 2, 3]) * 24
+        token, head = (H * a + b, a) if rng.random() < 0.6 else (a, T * a + b)
+        off = rng.choice([rng.randint(-200, 200), 16 * rng.randint(-12, 12), b, a, token, head])
+        x, out = at.moe_attn_rows(1 << 20, token, head), at.moe_attn_rows((1 << 20) + 2 * off,
+                                                                          token, head)
+        rows = [t * token + h * head for t in range(T) for h in range(H)]
+        if off == 0:
+            want = 0                      # in place
+        else:
+            want = -1 if any(abs(off + p - q) < 16 for p in rows for q in rows) else 0
+        assert F.moe_attn_rope(x, out, 64, T, H, 16, 0, r, None) == want, (T, H, token, head, off)
+        seen.add((want, off == 0))
+    assert len(seen) == 3
+    # the queries and the results of one buffer, a slice each
+    h = Handle(F)
+    cache = at.moe_attn_cache(1 << 20, 1 << 21, 9, 2 * 16 * 64, 64, 16 * 64)
+    batch = at.moe_attn_batch(64, 64, 64, 4, 4, 1, 40, 40)
+    q, o = at.moe_attn_rows(1 << 22, 20 * 64, 64), at.moe_attn_rows((1 << 22) + 8 * 128, 20 * 64, 64)
+    scores = at.moe_attn_scores(0.125, 0.0, 0, None, None)
+    assert F.moe_attn_forward(h.h, q, o, None, cache, batch, scores, None) == 0
+    o.data -= 128
+    assert F.moe_attn_forward(h.h, q, o, None, cache, batch, scores, None) == -1
+    assert F.moe_attn_destroy(h.h) == 0

@@ -1,7 +1,9 @@
 // C ABI of the attention operators: argument validation, workspace, dispatch.
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
 #include <cstdio>
+#include <cstdlib>
 #include <initializer_list>
 #include <new>
 #include <utility>
@@ -95,14 +97,35 @@ int validate_rows(const moe_attn_rows* r) {
   return MOE_ATTN_OK;
 }
 
-// first and last byte a [tokens, heads, head_dim] view touches overlap
+// Whether [tokens, heads, dim] views share an element: exact where their strides are
+// the same (parts of one buffer), else by the first and last byte that each touches.
 bool overlap(const moe_attn_rows* a, const moe_attn_rows* b, int tokens, int heads, int dim) {
   const auto span = [&](const moe_attn_rows* r) {
     return (uintptr_t)(((tokens - 1) * r->token_stride + (heads - 1) * r->head_stride + dim) * 2);
   };
   const uintptr_t pa = reinterpret_cast<uintptr_t>(a->data);
   const uintptr_t pb = reinterpret_cast<uintptr_t>(b->data);
-  return pa < pb + span(b) && pb < pa + span(a);
+  if (!(pa < pb + span(b) && pb < pa + span(a))) return false;
+  if ((tokens > 1 && a->token_stride != b->token_stride) ||
+      (heads > 1 && a->head_stride != b->head_stride))
+    return true;
+  long long near = heads > 1 ? a->head_stride : dim, far = tokens > 1 ? a->token_stride : near;
+  long long n_near = heads, n_far = tokens;
+  if (n_far > 1 && far < near) {
+    std::swap(near, far);
+    std::swap(n_near, n_far);
+  }
+  if (near <= 0 || far <= 0) return true;
+  // rows i of a and j of b are d + (their distance in rows) apart
+  const long long d = (long long)(pb - pa) / 2, reach = (n_near - 1) * near + dim;
+  const long long f0 = std::max(1 - n_far, (-reach - d) / far - 1);
+  const long long f1 = std::min(n_far - 1, (reach - d) / far + 1);
+  for (long long f = f0; f <= f1; ++f) {
+    const long long r = d + f * far, n = std::min(std::max(-r / near, 1 - n_near), n_near - 1);
+    for (long long k = n - 1; k <= n + 1; ++k)
+      if (k > -n_near && k < n_near && std::llabs(r + k * near) < dim) return true;
+  }
+  return false;
 }
 
 // rows to be written: no row lies on another (of a broadcast output, whichever row
