@@ -230,3 +230,18 @@ def test_layers_dropped_in_a_capture_are_destroyed_behind_it(L, monkeypatch):
     assert sorted(destroyed) == [8, 16, 24]
     second.close()
     assert len(destroyed) == 3
+
+
+def test_a_stream_by_address_is_of_the_tensors_device(monkeypatch):
+    import torch
+    made, used = [], []
+
+    class Tensor:
+        def record_stream(self, stream):
+            used.append(stream)
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream",
+                        lambda address, device=None: made.append((address, device)) or "stream")
+    device = torch.device("cuda", 1)
+    at._in_use(4096, device, Tensor(), None, Tensor())
+    assert made == [(4096, device)] and used == ["stream", "stream"]
