@@ -29,9 +29,11 @@
  *   x = scale * q.k;  x = softcap * tanh(x / softcap) if softcap > 0;
  *   x = x - slopes[h] * |p - j| if slopes
  * the output is sum_j softmax(x)_j v_j, and lse = log sum_j exp(x_j). A row
- * that sees no key gives zeros and lse = -inf. Sums and softmax statistics are
- * fp32; the softmax's numerators are rounded to the cache's type before they
- * are multiplied with V. Keys at and after kv_len, and pages behind them, are
+ * that sees no key gives zeros and lse = -inf. Scores, sums and softmax statistics
+ * are fp32 (under a cap of 64 or less, to 2^-22 of the cap; under larger ones, to
+ * 2^-21 of the score); the softmax's numerators are rounded to the cache's type
+ * before they are multiplied with V, in fp16 from units in which weights down to
+ * 2^-26 of a row's largest keep all their bits. Keys at and after kv_len, and pages behind them, are
  * never used, whatever they hold; a NaN or an infinity in a V row before
  * kv_len may reach other rows of its sequence that do not see that key (a
  * masked weight is an exact zero, and zero times infinity is NaN).
@@ -43,7 +45,8 @@
  * it is. Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy
  * default stream), allocate nothing and can be captured into a CUDA graph;
  * lengths, positions, slots and page tables are read on the device, so a graph
- * replays with new ones.
+ * replays with new ones. They must not change while a call runs: its parts read
+ * them at different times.
  *
  * Errors: MOE_ATTN_OK or a negative status (the values and meanings of
  * moe_w4a16_status); invalid arguments are rejected on the host and nothing is
@@ -143,8 +146,10 @@ typedef struct moe_attn_handle moe_attn_handle;
  * contexts longer than original_len:
  *   by_parts == 0: every theta_i / factor (positions interpolated);
  *   by_parts == 1: pairs with fewer than beta_slow turns in original_len are
- *     divided by factor, pairs with more than beta_fast are kept, linearly
- *     between, and the magnitude is 1 + 0.1 log(factor).
+ *     divided by factor, pairs with more than beta_fast are kept, and between them
+ *     the part kept is linear in the number of turns (not in the pair's index, as
+ *     some programs have it); the magnitude is 1 + 0.1 log(factor). A model made
+ *     with another ramp brings its own frequencies: freq is any table.
  * freq: [rot_dim / 2]; magnitude: one float. */
 int moe_attn_rope_frequencies(int32_t rot_dim, double base, double factor, int32_t by_parts,
                               double original_len, double beta_fast, double beta_slow,
@@ -169,7 +174,7 @@ int moe_attn_destroy(moe_attn_handle* h);
  * of the cache. positions [num_tokens]; slots int64 [num_tokens], a negative
  * slot leaves the cache alone (padding), one past the cache sets
  * MOE_ATTN_DEVERR_RANGE. q and q_out may both be NULL (keys and values only);
- * q_out == q is allowed. Two tokens with one slot leave either's row. */
+ * q_out == q is allowed. Two tokens with one slot leave a row with parts of both. */
 int moe_attn_append(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* q_out,
                     const moe_attn_rows* k, const moe_attn_rows* v, const int32_t* positions,
                     const int64_t* slots, int32_t num_tokens, const moe_attn_rotation* rotation,

@@ -10,9 +10,9 @@
 // and takes it for a few tokens: addresses and the kind of head are
 // worked out once, and all its loads are under way while the CTA puts the
 // cosines and sines of its tokens' pairs into shared memory, one evaluation for
-// all heads. Bound by memory: q, k and v of 8192
-// tokens (32, 8 and 8 heads of 128) take 35.4 us, 5.7 TB/s, 0.84 of the measured
-// copy rate; by flat chunk numbers, divided out per chunk, they took 60 us.
+// all heads. Bound by memory: q, k and v of 8192 tokens (32, 8 and 8 heads of 128),
+// not in the caches, take 32.8 us, 6.1 TB/s, 0.90 of the measured copy rate (replayed
+// on the same inputs 35.6 us); by flat chunk numbers, divided out per chunk, 60 us.
 #include "attn_common.cuh"
 
 namespace moe {
