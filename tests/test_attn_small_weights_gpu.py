@@ -83,3 +83,13 @@ def test_large_scores_give_the_largest_ones_value(dtype, scale, n, hq, softcap, 
             return
     ac.check_attention(out, lse, want, a, want_lse, dtype)
     assert layer.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("scale", [0.0, 1e-45, 1e-38, 1e-37, 1e-31, 1e-29, -1e-38, -0.2])
+@pytest.mark.parametrize("lens", [[(40, 3000), (150, 150)], [(1, 3000), (2, 77)]])
+def test_small_and_negative_scales(dtype, scale, lens):
+    b = ac.Batch(lens, 8, 2, 64, 32, dtype, scale=scale)
+    layer = moe.PagedAttention(8, 2, 64, 32, b.tokens, 2, dtype=dtype)
+    b.check(*b.run(layer))
+    assert layer.check_device_errors() == 0

@@ -1279,9 +1279,10 @@ template <typename T, int ND, bool BOTH>
 cudaError_t launch_nd(const AttnParams& p, const TcPieces& w, const CUtensorMap& qmap,
                       const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
   Form form = form_of(p.sc);
-  // The plain form takes the maximum before it scales, and tells a score's distance
-  // from it by one fused multiply-add, whose parts should stay below 2^26.
-  if (form == kPlain && !(p.sc.scale > 0.0f && p.sc.scale <= 16.0f)) form = kGeneral;
+  // The plain form takes the maximum before it scales (kRaise over the scale has to be
+  // a number), and tells a score's distance from it by one fused multiply-add, whose
+  // parts should stay below 2^26.
+  if (form == kPlain && !(p.sc.scale > 1e-30f && p.sc.scale <= 16.0f)) form = kGeneral;
   return launch_after(form == kPlain     ? attn_tc_kernel<T, ND, kPlain, BOTH>
                       : form == kGeneral ? attn_tc_kernel<T, ND, kGeneral, BOTH>
                                          : attn_tc_kernel<T, ND, kWide, BOTH>,
