@@ -309,8 +309,9 @@ class MoeLayer:
 
 
 # The attention operators need torch; the expert layer's host functions do not.
-_ATTENTION = ("PagedAttention", "PagedKvCache", "moe_attn_rope", "moe_attn_rope_frequencies",
-              "EXPORTS_ATTN")
+_ATTENTION = ("PagedAttention", "PagedKvCache", "HeadNorm", "moe_attn_rope",
+              "moe_attn_rope_frequencies", "moe_attn_norm_rope", "moe_attn_norm_rope_backward",
+              "EXPORTS_ATTN", "EXPORTS_ATTN8")
 
 
 def __getattr__(name):

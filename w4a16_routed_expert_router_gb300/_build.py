@@ -65,7 +65,8 @@ def build_binding(force: bool = False) -> bool:
     headers = python_headers()
     if headers is None:
         return False
-    deps = [BINDING_SRC, os.path.join(INCLUDE, "moe_attn.h"), os.path.abspath(__file__)]
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "moe_attn.h"), os.path.join(INCLUDE, "moe_attn8.h"),
+            os.path.abspath(__file__)]
     if not force and not _older(BINDING, deps):
         return True
     tmp = BINDING + ".tmp"

@@ -1,5 +1,7 @@
-"""Python binding of the attention operators (``include/moe_attn.h``): rotary
-positions, appending keys and values to a paged cache, and attention over it.
+"""Python binding of the attention operators (``include/moe_attn.h``,
+``include/moe_attn8.h``): rotary positions, alone or behind norms of the heads, with
+their gradients, appending keys and values to a paged cache of 16-bit values or of
+8-bit codes with scales, reading that one back, and attention over either.
 
 Argument marshalling and checks only; the operators are the CUDA kernels of
 ``libmoe_w4a16.so``. Tensors of the wrong type, device or form, and tensors that
@@ -9,6 +11,7 @@ of the library raises ``MoeError``.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -32,6 +35,21 @@ EXPORTS_ATTN = (
     "moe_attn_forward",
     "moe_attn_check_device_errors",
 )
+
+# every symbol include/moe_attn8.h declares
+EXPORTS_ATTN8 = (
+    "moe_attn_norm_rope",
+    "moe_attn_norm_rope_backward_bytes",
+    "moe_attn_norm_rope_backward",
+    "moe_attn_append_norm",
+    "moe_attn_append8",
+    "moe_attn_read8",
+    "moe_attn_forward8",
+    "moe_attn_forward_sinks",
+)
+MOE_ATTN8_BLOCK = 16
+MOE_ATTN_WEIGHT_SAME = 0
+MOE_ATTN_WEIGHT_F32 = 1
 
 _DTYPES = {torch.bfloat16: MOE_ATTN_BF16, torch.float16: MOE_ATTN_FP16}
 _LAYOUTS = {"half": MOE_ATTN_ROPE_HALF, "interleaved": MOE_ATTN_ROPE_INTERLEAVED}
@@ -70,6 +88,33 @@ class moe_attn_scores(ctypes.Structure):
                 ("prefix", _vp)]
 
 
+class moe_attn_norm(ctypes.Structure):
+    _fields_ = [("q_weight", _vp), ("k_weight", _vp), ("q_head_stride", _i64),
+                ("k_head_stride", _i64), ("eps", _f32), ("offset", _f32), ("weight_type", _i32)]
+
+
+class moe_attn_cache8(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scales", _vp), ("v_scales", _vp), ("num_pages", _i64),
+                ("page_stride", _i64), ("token_stride", _i64), ("head_stride", _i64),
+                ("scale_page_stride", _i64), ("scale_head_stride", _i64),
+                ("scale_block_stride", _i64)]
+
+
+class moe_attn_extent(ctypes.Structure):
+    _fields_ = [("cu_rows", _vp), ("first", _vp), ("page_table", _vp), ("table_stride", _i64),
+                ("columns", _i32), ("num_seqs", _i32), ("num_rows", _i32)]
+
+
+class HeadNorm(NamedTuple):
+    """Norms of queries and keys for each head: x / sqrt(mean(x^2) + eps) * (weight +
+    offset). Weights are [head_dim] for all heads or [heads, head_dim], of x's type or
+    fp32 (both alike)."""
+    q_weight: torch.Tensor
+    k_weight: torch.Tensor
+    eps: float = 1e-6
+    offset: float = 0.0
+
+
 def _signatures():
     p = ctypes.POINTER
     rows, rot, cache = p(moe_attn_rows), p(moe_attn_rotation), p(moe_attn_cache)
@@ -85,6 +130,36 @@ def _signatures():
                              _vp],
         "moe_attn_check_device_errors": [_vp, p(ctypes.c_uint32)],
     }
+
+
+def _signatures8():
+    p = ctypes.POINTER
+    rows, rot, norm, cache = (p(c) for c in (moe_attn_rows, moe_attn_rotation, moe_attn_norm,
+                                             moe_attn_cache8))
+    batch, scores = p(moe_attn_batch), p(moe_attn_scores)
+    appended = [_vp, rows, rows, rows, rows, _vp, _vp, _i32, norm, rot]
+    return {
+        "moe_attn_norm_rope": [rows, rows, rows, rows, _vp, _i32, _i32, _i32, _i32, _i32, norm,
+                               rot, _vp],
+        "moe_attn_norm_rope_backward_bytes": [_i32, _i32, _i32, _i32, p(ctypes.c_size_t)],
+        "moe_attn_norm_rope_backward": [rows, rows, rows, _vp, rows, rows, rows, _vp, _vp, _i32,
+                                        _i32, _i32, _i32, _i32, norm, rot, _vp, ctypes.c_size_t,
+                                        _vp],
+        "moe_attn_append_norm": [*appended, p(moe_attn_cache), _vp],
+        "moe_attn_append8": [*appended, cache, _vp],
+        "moe_attn_read8": [_vp, cache, p(moe_attn_extent), rows, rows, _vp],
+        "moe_attn_forward8": [_vp, rows, rows, _vp, cache, batch, scores, _i32, _vp],
+        "moe_attn_forward_sinks": [_vp, rows, rows, _vp, p(moe_attn_cache), batch, scores, _i32,
+                                   _vp],
+    }
+
+
+def register8(L: ctypes.CDLL) -> None:
+    """Give the library's functions of moe_attn8.h their argument types."""
+    for name, args in _signatures8().items():
+        fn = getattr(L, name)
+        fn.argtypes = args
+        fn.restype = ctypes.c_int
 
 
 def register(L: ctypes.CDLL) -> None:
@@ -105,6 +180,7 @@ def _lib() -> ctypes.CDLL:
         from . import lib
         L = lib()
         register(L)
+        register8(L)
         try:
             from . import _attn_binding
         except ImportError as e:
@@ -116,11 +192,13 @@ def _lib() -> ctypes.CDLL:
         def address(name):
             return ctypes.cast(getattr(L, name), ctypes.c_void_p).value
 
-        _attn_binding.setup(address("moe_attn_rope"), address("moe_attn_append"),
-                            address("moe_attn_forward"), _check, torch.empty, _raw_stream,
-                            _current_device, torch.is_grad_enabled,
-                            torch.is_inference_mode_enabled, _increment_version, torch.bfloat16,
-                            torch.float16, torch.float32, torch.int32, torch.int64)
+        functions = tuple(address(f"moe_attn_{name}") for name in (
+            "rope", "append", "forward", "norm_rope", "norm_rope_backward_bytes",
+            "norm_rope_backward", "append_norm", "append8", "read8", "forward8", "forward_sinks"))
+        _attn_binding.setup(functions, _check, torch.empty, _raw_stream, _current_device,
+                            torch.is_grad_enabled, torch.is_inference_mode_enabled,
+                            _increment_version, torch.bfloat16, torch.float16, torch.float32,
+                            torch.int32, torch.int64, torch.float8_e4m3fn)
         _native, _library = _attn_binding, L
     return _library
 
@@ -217,6 +295,64 @@ def moe_attn_rope(x, positions, freq, out=None, layout="half", magnitude=1.0, in
     return done
 
 
+def _norm(norm) -> "HeadNorm":
+    if not isinstance(norm, HeadNorm):
+        raise ValueError(f"norm must be a HeadNorm, got {type(norm).__name__}")
+    return norm
+
+
+def moe_attn_norm_rope(q, k, positions, freq, norm, layout="half", magnitude=1.0, q_out=None,
+                       k_out=None, stream=None):
+    """Norms of q and k [tokens, heads, head_dim] (bf16 or fp16, any token and head
+    strides) for each head, then rotary positions at int32 [tokens], in one pass:
+    (q_out, k_out). Outputs may be their inputs; q or k may be None. Autograd does not
+    follow this call; moe_attn_norm_rope_backward is its gradient."""
+    if _native is None:
+        _lib()
+    given = stream
+    x = k if q is None else q
+    if stream is not None:
+        for t, o in ((q, q_out), (k, k_out)):
+            if t is not None and o is None and isinstance(stream, int):
+                raise ValueError("outputs are needed where the stream is a raw address")
+        if q is not None:
+            stream, q_out = _on_stream(given, q_out, q.shape, q.dtype, q.device)
+        if k is not None:
+            stream, k_out = _on_stream(given, k_out, k.shape, k.dtype, k.device)
+    args = (q, k, positions, freq, _norm(norm), _layout(layout), magnitude, q_out, k_out, stream)
+    done = _native.norm_rope(*args)
+    if done is NotImplemented:  # another device is current
+        with torch.cuda.device(x.device):
+            done = _native.norm_rope(*args)
+    if given is not None:
+        _in_use(given, x.device, q, k, positions, freq, norm.q_weight, norm.k_weight, q_out, k_out)
+    return done
+
+
+def moe_attn_norm_rope_backward(dq, dk, q, k, positions, freq, norm, layout="half",
+                                magnitude=1.0, stream=None):
+    """The gradients of moe_attn_norm_rope's inputs and weights, (q, k, q_weight,
+    k_weight), from those of its results, dq and dk; q and k are what it was called
+    with. The weights' are fp32, of the weights' shapes. q and dq, or k and dk, may be
+    None. Runs on `stream`, a torch stream (default: the current one)."""
+    if _native is None:
+        _lib()
+    x = k if q is None else q
+    args = (dq, dk, q, k, positions, freq, _norm(norm), _layout(layout), magnitude)
+    if stream is not None:
+        if isinstance(stream, int):
+            raise ValueError("a torch stream is needed: the results belong to it")
+        with torch.cuda.stream(stream):
+            done = moe_attn_norm_rope_backward(*args[:7], layout=layout, magnitude=magnitude)
+        _in_use(stream, x.device, dq, dk, q, k, positions, freq, norm.q_weight, norm.k_weight)
+        return done
+    done = _native.norm_back(*args)
+    if done is NotImplemented:  # another device is current
+        with torch.cuda.device(x.device):
+            done = _native.norm_back(*args)
+    return done
+
+
 # Handles to be destroyed. That waits for the device, which would end a capture of
 # this thread's stream (a collection of garbage comes at any time): they stay here
 # until a layer is made or closed outside of one.
@@ -236,7 +372,10 @@ class PagedAttention:
     workspace, usable by every layer of a model on one stream at a time.
 
     k_pages and v_pages are [pages, kv_heads, page_size, head_dim] (any strides
-    with head_dim contiguous, the same for both; 16-byte multiples).
+    with head_dim contiguous, the same for both; 16-byte multiples), of the layer's
+    type, or, with k_scales and v_scales, torch.float8_e4m3fn codes: a value is its code
+    times the scale of its 16 tokens, float32 [pages, kv_heads, page_size // 16]
+    (head_dim a multiple of 16).
     """
 
     def __init__(self, q_heads, kv_heads, head_dim, page_size, max_tokens, max_seqs,
@@ -296,32 +435,60 @@ class PagedAttention:
         return flags.value
 
     def append(self, q, k, v, positions, slots, k_pages, v_pages, freq, layout="half",
-               magnitude=1.0, q_out=None, stream=None):
+               magnitude=1.0, q_out=None, stream=None, norm=None, k_scales=None, v_scales=None):
         """Turn q and k [tokens, heads, head_dim] to their positions (int32) and
         write k and v to their slots (int64; page * page_size + offset, negative:
         not written) of the cache. Returns q_out (new unless given, may be q);
-        q None: keys and values only."""
+        q None: keys and values only. norm: a HeadNorm applied to q and k before.
+
+        Into an 8-bit cache k and v are quantised: a block's scale grows with its
+        largest value, as a power of two, and the codes it held go by the new one; the
+        token in a block's first row begins the block. New tokens of one block follow
+        each other, in the order of their slots.
+        """
         given = stream
         if stream is not None:
             if q is not None:
                 stream, q_out = _on_stream(stream, q_out, q.shape, self.dtype, self.device)
             elif not isinstance(stream, int):
                 stream = stream.cuda_stream
+        if norm is not None:
+            _norm(norm)
         done = _native.append(self._open(), q, k, v, positions, slots, k_pages, v_pages, freq,
-                              _layout(layout), magnitude, q_out, stream)
+                              _layout(layout), magnitude, q_out, norm, k_scales, v_scales, stream)
         if given is not None:
-            _in_use(given, self.device, q, k, v, positions, slots, k_pages, v_pages, freq, q_out)
+            _in_use(given, self.device, q, k, v, positions, slots, k_pages, v_pages, freq, q_out,
+                    k_scales, v_scales, *((norm.q_weight, norm.k_weight) if norm else ()))
+        return done
+
+    def read(self, k_pages, v_pages, page_table, cu_rows, first, rows, k_scales=None,
+             v_scales=None, k_out=None, v_out=None, stream=None):
+        """Keys and values of an 8-bit cache in the layer's type, (k, v) of `rows` rows
+        [rows, kv_heads, head_dim]: those of sequence s, its tokens from first[s] on, are
+        rows cu_rows[s] .. cu_rows[s + 1] (int32 [seqs + 1] and [seqs]; page_table int32
+        [seqs, columns]). Rows of no sequence are not written."""
+        given = stream
+        if stream is not None:
+            shape = (rows, self.kv_heads, self.head_dim)
+            stream, k_out = _on_stream(given, k_out, shape, self.dtype, self.device)
+            stream, v_out = _on_stream(given, v_out, shape, self.dtype, self.device)
+        done = _native.read(self._open(), k_pages, v_pages, page_table, cu_rows, first, rows,
+                            k_scales, v_scales, k_out, v_out, stream)
+        if given is not None:
+            _in_use(given, self.device, k_pages, v_pages, page_table, cu_rows, first, k_scales,
+                    v_scales, k_out, v_out)
         return done
 
     def forward(self, q, k_pages, v_pages, page_table, cu_q, kv_len, max_q, scale=None,
                 softcap=0.0, window=0, slopes=None, prefix=None, out=None, lse=None,
-                return_lse=False, stream=None):
+                return_lse=False, stream=None, sinks=0, k_scales=None, v_scales=None):
         """Attention of q [tokens, q_heads, head_dim], the last tokens of each
         sequence, over the sequences' keys in the cache.
 
         cu_q int32 [seqs + 1]: first row of each sequence; kv_len int32 [seqs]:
         its keys, the new ones included; page_table int32 [seqs, columns]; max_q:
         no sequence has more new tokens. scale defaults to 1 / sqrt(head_dim).
+        sinks: first tokens of a sequence that a window does not hide.
         Returns out, or (out, lse) with lse fp32 [tokens, q_heads].
         """
         given = stream
@@ -331,16 +498,18 @@ class PagedAttention:
             stream, out = _on_stream(stream, out, q.shape, self.dtype, self.device)
         done = _native.forward(self._open(), q, k_pages, v_pages, page_table, cu_q, kv_len, max_q,
                                scale, softcap, window, slopes, prefix, out, lse, return_lse,
-                               stream)
+                               sinks, k_scales, v_scales, stream)
         if given is not None:
             _in_use(given, self.device, q, k_pages, v_pages, page_table, cu_q, kv_len, slopes,
-                    prefix, out, lse)
+                    prefix, out, lse, k_scales, v_scales)
         return done
 
 
 class PagedKvCache:
     """Pages of one layer's keys and values and the bookkeeping of which
-    sequence holds which: slots for new tokens, page tables for attention.
+    sequence holds which: slots for new tokens, page tables for attention. With dtype
+    torch.float8_e4m3fn an 8-bit cache: `scales` is then {"k_scales", "v_scales"} for the
+    layer's calls, otherwise it is empty.
 
     The bookkeeping is plain Python, for examples and small batches: `tables` makes
     every row anew (3 ms for 64 sequences of 1000 pages). A server keeps its tables
@@ -352,6 +521,11 @@ class PagedKvCache:
         self.k_pages = torch.empty((num_pages, kv_heads, page_size, head_dim), dtype=dtype,
                                    device=device)
         self.v_pages = torch.empty_like(self.k_pages)
+        self.scales = {}
+        if dtype == torch.float8_e4m3fn:
+            blocks = page_size // MOE_ATTN8_BLOCK
+            self.scales = {name: torch.zeros((num_pages, kv_heads, blocks), device=device)
+                           for name in ("k_scales", "v_scales")}
         self.page_size = page_size
         self._free = list(range(num_pages - 1, -1, -1))
         self._pages, self._length = {}, {}

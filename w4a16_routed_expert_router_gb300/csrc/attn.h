@@ -3,7 +3,7 @@
 
 #include <cuda_fp16.h>
 
-#include "../../include/moe_attn.h"
+#include "../../include/moe_attn8.h"
 #include "common.cuh"
 
 namespace moe {
@@ -65,6 +65,67 @@ struct RopeParams {
 };
 cudaError_t launch_rope(const RopeParams& p, int dtype, cudaStream_t s);
 
+// Norms of heads before their rotation.
+struct Norm {
+  const void *q_weight, *k_weight;
+  long long q_head, k_head;   // elements from head to head, 0: one weight for all
+  float eps, offset;
+  int wide;                   // the weights are fp32
+  int on;                     // 0: no norm at all
+};
+
+// q to q_out, k to k_out, both normed and turned; where `slots` is set k goes to
+// 16-bit pages instead, and v with it.
+struct NormParams {
+  RopeParams r;
+  Rows k_out;
+  Norm n;
+};
+cudaError_t launch_norm_rope(const NormParams& p, int dtype, cudaStream_t s);
+
+// Gradients: p.r.q and p.r.k are the inputs, p.r.q_out and p.k_out get the gradients.
+struct NormGradParams {
+  NormParams p;
+  Rows dq, dk;
+  float *dw_q, *dw_k;
+  float* parts;               // sums of weight gradients, see norm_grad_plan
+};
+// CTAs along the tokens and groups of heads of either kernel of the gradient
+struct NormGradPlan {
+  int rows, z, groups, parts;  // heads of a CTA, tokens side by side
+};
+NormGradPlan norm_grad_plan(int tokens, int heads, int lanes);
+size_t norm_grad_bytes(int tokens, int heads, int head_dim);
+cudaError_t launch_norm_rope_grad(const NormGradParams& p, int dtype, cudaStream_t s);
+
+// ------------------------------------------------------------------ 8-bit cache
+constexpr int kScaleBlock = MOE_ATTN8_BLOCK;
+constexpr float kCodeTop = 448.0f;     // the largest e4m3 value
+constexpr int kScaleExp = 64;          // scales are 2^-64 .. 2^64
+
+struct Cache8 {
+  uint8_t *k, *v;
+  float *k_scales, *v_scales;
+  long long num_pages, page, token, head;           // strides of the codes
+  long long scale_page, scale_head, scale_block;
+};
+
+struct Append8Params {
+  NormParams p;       // k and v have no 16-bit pages here; n.on says whether there is a norm
+  Cache8 c;
+};
+cudaError_t launch_append8(const Append8Params& p, int dtype, cudaStream_t s);
+
+struct Read8Params {
+  Cache8 c;
+  const int *cu, *first, *page_table;
+  long long table_stride;
+  int columns, num_seqs, rows, hk, head_dim, page_shift;
+  Rows k_out, v_out;
+  unsigned* err;
+};
+cudaError_t launch_read8(const Read8Params& p, int dtype, cudaStream_t s);
+
 struct Scores {
   float scale;
   float softcap;
@@ -72,6 +133,7 @@ struct Scores {
   int window;
   const float* slopes;
   const int* prefix;
+  int sinks;     // first keys that a window does not hide; 0 without a window
 };
 
 struct Batch {
@@ -146,15 +208,21 @@ __device__ __forceinline__ int prefix_of(const Scores& sc, int s, int kv) {
   return sc.prefix ? min(kv, max(0, sc.prefix[s])) : 0;
 }
 
+// First keys that a row at position p sees apart from its window.
+__device__ __forceinline__ int kept_of(const Scores& sc, int prefix, int p) {
+  return max(prefix, min(sc.sinks, p + 1));
+}
+
 // Blocks seen by rows at positions [p0, p1] (p1 >= p0), at least one.
-__device__ __forceinline__ void span_blocks(Span& r, int p0, int p1, int window, int prefix,
+__device__ __forceinline__ void span_blocks(Span& r, int p0, int p1, const Scores& sc, int prefix,
                                             int block) {
   const int end = min(r.kv, max(p1 + 1, prefix));
-  const int from = window ? max(0, p0 - window + 1) : 0;
+  const int from = sc.window ? max(0, p0 - sc.window + 1) : 0;
   const int last = (max(end, 1) + block - 1) / block;      // blocks [.., last)
   const int wb = min(from / block, last - 1);
-  const int pb = (prefix + block - 1) / block;
-  if (prefix == 0) {
+  const int kept = kept_of(sc, prefix, p1);
+  const int pb = (kept + block - 1) / block;
+  if (kept == 0) {
     r.near = 0;
     r.skip = wb;
   } else if (wb <= pb) {
@@ -219,6 +287,14 @@ cudaError_t attn_tc_setup(bool* usable);
 cudaError_t launch_attn_tc(const AttnParams& p, const TcPieces& w, const CUtensorMap& qmap,
                            const CUtensorMap& kmap, const CUtensorMap& vmap, int dtype, int grid,
                            cudaStream_t s);
+
+// ------------------------------------------------------------------ 8-bit attention
+struct Attn8Params {
+  AttnParams a;
+  Cache8 c;
+  int dtype;
+};
+cudaError_t launch_attn8_rows(const Attn8Params& p, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace moe

@@ -1,0 +1,351 @@
+// C ABI of include/moe_attn8.h: argument validation and dispatch.
+#include "attn_host.h"
+
+namespace {
+
+int validate_norm(const moe_attn_norm* n, int head_dim, int q_heads, int k_heads) {
+  if (!n) return MOE_ATTN_ERR_INVALID_ARG;
+  if (n->weight_type != MOE_ATTN_WEIGHT_SAME && n->weight_type != MOE_ATTN_WEIGHT_F32)
+    return MOE_ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(n->eps) || n->eps < 0.0f || !std::isfinite(n->offset))
+    return MOE_ATTN_ERR_INVALID_ARG;
+  const uintptr_t odd = n->weight_type == MOE_ATTN_WEIGHT_F32 ? 3u : 1u;
+  const struct {
+    const void* w;
+    int64_t stride;
+    int heads;
+  } both[2] = {{n->q_weight, n->q_head_stride, q_heads}, {n->k_weight, n->k_head_stride, k_heads}};
+  for (const auto& b : both) {
+    if (b.heads == 0) continue;
+    if (!b.w || b.stride < 0 || (b.stride > 0 && b.stride < head_dim))
+      return MOE_ATTN_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(b.w) & odd) return MOE_ATTN_ERR_MISALIGNED;
+  }
+  return MOE_ATTN_OK;
+}
+
+Norm norm_of(const moe_attn_norm* n) {
+  if (!n) return Norm{nullptr, nullptr, 0, 0, 0.0f, 0.0f, 0, 0};
+  return Norm{n->q_weight, n->k_weight, n->q_head_stride, n->k_head_stride, n->eps, n->offset,
+              n->weight_type == MOE_ATTN_WEIGHT_F32, 1};
+}
+
+// an input and what becomes of it
+int validate_pair(const moe_attn_rows* x, const moe_attn_rows* out, int tokens, int heads,
+                  int dim) {
+  int st;
+  if ((st = validate_rows(x)) != MOE_ATTN_OK || (st = validate_rows(out)) != MOE_ATTN_OK) return st;
+  if (!apart(out, tokens, heads, dim) || (!same(x, out) && overlap(x, out, tokens, heads, dim)))
+    return MOE_ATTN_ERR_INVALID_ARG;
+  return MOE_ATTN_OK;
+}
+
+// rows of two kinds of heads: whether they share a byte (by their first and last ones;
+// parts of one buffer, heads behind heads, are told apart)
+bool share(const moe_attn_rows* a, int heads_a, const moe_attn_rows* b, int heads_b, int tokens,
+           int dim) {
+  const auto span = [&](const moe_attn_rows* r, int heads) {
+    return (uintptr_t)(((tokens - 1) * r->token_stride + (heads - 1) * r->head_stride + dim) * 2);
+  };
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a->data);
+  const uintptr_t pb = reinterpret_cast<uintptr_t>(b->data);
+  if (!(pa < pb + span(b, heads_b) && pb < pa + span(a, heads_a))) return false;
+  if (tokens > 1 && a->token_stride != b->token_stride) return true;
+  // a token's rows of either kind, and where the others begin among them
+  const long long wa = (heads_a - 1) * a->head_stride + dim, wb = (heads_b - 1) * b->head_stride + dim;
+  const long long step = a->token_stride, d = (long long)(pb - pa) / 2;
+  if (tokens == 1) return d < wa && -d < wb;
+  if (step <= 0) return true;
+  const long long in = ((d % step) + step) % step;
+  return in < wa || in + wb > step;
+}
+
+int validate_heads(int32_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                   int32_t dtype) {
+  if (tokens < 0 || q_heads < 0 || kv_heads < 0) return MOE_ATTN_ERR_INVALID_ARG;
+  if (tokens > (1 << 30)) return MOE_ATTN_ERR_TOO_MANY_TOKENS;
+  if (head_dim < 1 || head_dim > 256 || q_heads > 65536 || kv_heads > 65536)
+    return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  if (dtype != MOE_ATTN_BF16 && dtype != MOE_ATTN_FP16) return MOE_ATTN_ERR_INVALID_ARG;
+  return MOE_ATTN_OK;
+}
+
+int validate_cache8(const moe_attn_config& cfg, const moe_attn_cache8* c) {
+  if (!c || !c->k || !c->v || !c->k_scales || !c->v_scales) return MOE_ATTN_ERR_INVALID_ARG;
+  if (cfg.head_dim % 16) return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  if (c->num_pages < 1 || c->num_pages > 0x7ffffffeLL) return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  if (c->page_stride <= 0 || c->token_stride <= 0 || c->head_stride <= 0 ||
+      c->scale_page_stride < 0 || c->scale_head_stride < 0 || c->scale_block_stride < 0)
+    return MOE_ATTN_ERR_INVALID_ARG;
+  if (c->page_stride >= (1LL << 40) || c->token_stride >= (1LL << 40) ||
+      c->head_stride >= (1LL << 40))
+    return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;  // a tensor map's limit
+  if (!aligned16(c->k) || !aligned16(c->v) || c->page_stride % 16 || c->token_stride % 16 ||
+      c->head_stride % 16 || ((reinterpret_cast<uintptr_t>(c->k_scales) |
+                               reinterpret_cast<uintptr_t>(c->v_scales)) & 3u))
+    return MOE_ATTN_ERR_MISALIGNED;
+  return MOE_ATTN_OK;
+}
+
+Cache8 cache_of(const moe_attn_cache8* c) {
+  return Cache8{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_scales, c->v_scales,
+                c->num_pages, c->page_stride, c->token_stride, c->head_stride,
+                c->scale_page_stride, c->scale_head_stride, c->scale_block_stride};
+}
+
+// What moe_attn_append_norm and moe_attn_append8 have in common.
+int check_append(const moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* q_out,
+                 int32_t T, const moe_attn_rotation* r, const moe_attn_norm* norm) {
+  if (!h || T < 0) return MOE_ATTN_ERR_INVALID_ARG;
+  const moe_attn_config& c = h->cfg;
+  if (T > c.max_tokens) return MOE_ATTN_ERR_TOO_MANY_TOKENS;
+  int st = validate_rotation(r, c.head_dim);
+  if (st != MOE_ATTN_OK) return st;
+  if ((q == nullptr) != (q_out == nullptr)) return MOE_ATTN_ERR_INVALID_ARG;
+  return norm ? validate_norm(norm, c.head_dim, q ? c.q_heads : 0, c.kv_heads) : MOE_ATTN_OK;
+}
+int check_append_rows(const moe_attn_config& c, const moe_attn_rows* q, const moe_attn_rows* q_out,
+                      const moe_attn_rows* k, const moe_attn_rows* v, const int32_t* positions,
+                      const int64_t* slots, int32_t T) {
+  int st;
+  if (q && (st = validate_pair(q, q_out, T, c.q_heads, c.head_dim)) != MOE_ATTN_OK) return st;
+  if ((st = validate_rows(k)) != MOE_ATTN_OK || (st = validate_rows(v)) != MOE_ATTN_OK) return st;
+  if (q && (share(q_out, c.q_heads, k, c.kv_heads, T, c.head_dim) ||
+            share(q_out, c.q_heads, v, c.kv_heads, T, c.head_dim)))
+    return MOE_ATTN_ERR_INVALID_ARG;
+  return positions && slots ? MOE_ATTN_OK : MOE_ATTN_ERR_INVALID_ARG;
+}
+NormParams append_params(const moe_attn_handle* h, const moe_attn_rows* q,
+                         const moe_attn_rows* q_out, const moe_attn_rows* k,
+                         const moe_attn_rows* v, const int32_t* positions, const int64_t* slots,
+                         int32_t T, const moe_attn_norm* norm, const moe_attn_rotation* r,
+                         long long num_pages) {
+  const moe_attn_config& c = h->cfg;
+  NormParams p{};
+  p.r.q = rows(q);
+  p.r.q_out = rows(q_out);
+  p.r.k = rows(k);
+  p.r.v = rows(v);
+  p.r.page_shift = log2i(c.page_size);
+  p.r.num_slots = num_pages << p.r.page_shift;
+  p.r.positions = positions;
+  p.r.slots = reinterpret_cast<const long long*>(slots);
+  p.r.r = rotation(r);
+  p.r.tokens = T;
+  p.r.hq = q ? c.q_heads : 0;
+  p.r.hk = p.r.hv = c.kv_heads;
+  p.r.head_dim = c.head_dim;
+  p.r.err = h->err;
+  p.n = norm_of(norm);
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_attn_norm_rope(const moe_attn_rows* q, const moe_attn_rows* q_out, const moe_attn_rows* k,
+                       const moe_attn_rows* k_out, const int32_t* positions, int32_t T,
+                       int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t dtype,
+                       const moe_attn_norm* norm, const moe_attn_rotation* r, void* stream) {
+  int st = validate_heads(T, q_heads, kv_heads, head_dim, dtype);
+  if (st != MOE_ATTN_OK) return st;
+  if ((st = validate_rotation(r, head_dim)) != MOE_ATTN_OK) return st;
+  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr))
+    return MOE_ATTN_ERR_INVALID_ARG;
+  const int hq = q ? q_heads : 0, hk = k ? kv_heads : 0;
+  if ((st = validate_norm(norm, head_dim, hq, hk)) != MOE_ATTN_OK) return st;
+  if (T == 0 || hq + hk == 0) return MOE_ATTN_OK;
+  if (hq && (st = validate_pair(q, q_out, T, hq, head_dim)) != MOE_ATTN_OK) return st;
+  if (hk && (st = validate_pair(k, k_out, T, hk, head_dim)) != MOE_ATTN_OK) return st;
+  if (!positions) return MOE_ATTN_ERR_INVALID_ARG;
+  // an output is written while the other's input is read
+  if (hq && hk &&
+      (share(q_out, hq, k, hk, T, head_dim) || share(k_out, hk, q, hq, T, head_dim) ||
+       share(q_out, hq, k_out, hk, T, head_dim)))
+    return MOE_ATTN_ERR_INVALID_ARG;
+  NormParams p{};
+  p.r.q = rows(hq ? q : nullptr);
+  p.r.q_out = rows(hq ? q_out : nullptr);
+  p.r.k = rows(hk ? k : nullptr);
+  p.k_out = rows(hk ? k_out : nullptr);
+  p.r.positions = positions;
+  p.r.r = rotation(r);
+  p.r.tokens = T;
+  p.r.hq = hq;
+  p.r.hk = hk;
+  p.r.head_dim = head_dim;
+  p.n = norm_of(norm);
+  return cuda_status(launch_norm_rope(p, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_attn_norm_rope_backward_bytes(int32_t T, int32_t q_heads, int32_t kv_heads,
+                                      int32_t head_dim, size_t* bytes) {
+  if (!bytes) return MOE_ATTN_ERR_INVALID_ARG;
+  const int st = validate_heads(T, q_heads, kv_heads, head_dim, MOE_ATTN_BF16);
+  if (st != MOE_ATTN_OK) return st;
+  *bytes = T && q_heads + kv_heads ? norm_grad_bytes(T, q_heads + kv_heads, head_dim) : 0;
+  return MOE_ATTN_OK;
+}
+
+int moe_attn_norm_rope_backward(const moe_attn_rows* dq, const moe_attn_rows* q,
+                                const moe_attn_rows* dx_q, float* dw_q, const moe_attn_rows* dk,
+                                const moe_attn_rows* k, const moe_attn_rows* dx_k, float* dw_k,
+                                const int32_t* positions, int32_t T, int32_t q_heads,
+                                int32_t kv_heads, int32_t head_dim, int32_t dtype,
+                                const moe_attn_norm* norm, const moe_attn_rotation* r,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  int st = validate_heads(T, q_heads, kv_heads, head_dim, dtype);
+  if (st != MOE_ATTN_OK) return st;
+  if ((st = validate_rotation(r, head_dim)) != MOE_ATTN_OK) return st;
+  const bool with_q = q || dq || dx_q || dw_q, with_k = k || dk || dx_k || dw_k;
+  const int hq = with_q ? q_heads : 0, hk = with_k ? kv_heads : 0;
+  if ((st = validate_norm(norm, head_dim, hq, hk)) != MOE_ATTN_OK) return st;
+  if (hq + hk == 0) return MOE_ATTN_OK;
+  if ((hq && !dw_q) || (hk && !dw_k)) return MOE_ATTN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(dw_q) | reinterpret_cast<uintptr_t>(dw_k)) & 3u)
+    return MOE_ATTN_ERR_MISALIGNED;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {  // no token: no gradient of the weights
+    const size_t row = (size_t)head_dim * sizeof(float);
+    if (hq && (st = cuda_status(cudaMemsetAsync(dw_q, 0, row * (norm->q_head_stride ? hq : 1), s))))
+      return st;
+    return hk ? cuda_status(cudaMemsetAsync(dw_k, 0, row * (norm->k_head_stride ? hk : 1), s))
+              : MOE_ATTN_OK;
+  }
+  const struct {
+    const moe_attn_rows *dy, *x, *dx;
+    int heads;
+  } both[2] = {{dq, q, dx_q, hq}, {dk, k, dx_k, hk}};
+  for (const auto& b : both) {
+    if (!b.heads) continue;
+    if ((st = validate_pair(b.dy, b.dx, T, b.heads, head_dim)) != MOE_ATTN_OK ||
+        (st = validate_pair(b.x, b.dx, T, b.heads, head_dim)) != MOE_ATTN_OK)
+      return st;
+  }
+  if (hq && hk &&
+      (share(dx_q, hq, k, hk, T, head_dim) || share(dx_q, hq, dk, hk, T, head_dim) ||
+       share(dx_k, hk, q, hq, T, head_dim) || share(dx_k, hk, dq, hq, T, head_dim) ||
+       share(dx_q, hq, dx_k, hk, T, head_dim)))
+    return MOE_ATTN_ERR_INVALID_ARG;
+  if (!positions || !workspace || workspace_bytes < norm_grad_bytes(T, hq + hk, head_dim))
+    return MOE_ATTN_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return MOE_ATTN_ERR_MISALIGNED;
+  NormGradParams g{};
+  g.p.r.q = rows(hq ? q : nullptr);
+  g.p.r.q_out = rows(hq ? dx_q : nullptr);
+  g.p.r.k = rows(hk ? k : nullptr);
+  g.p.k_out = rows(hk ? dx_k : nullptr);
+  g.dq = rows(hq ? dq : nullptr);
+  g.dk = rows(hk ? dk : nullptr);
+  g.p.r.positions = positions;
+  g.p.r.r = rotation(r);
+  g.p.r.r.sign = -g.p.r.r.sign;  // the opposite rotation
+  g.p.r.tokens = T;
+  g.p.r.hq = hq;
+  g.p.r.hk = hk;
+  g.p.r.head_dim = head_dim;
+  g.p.n = norm_of(norm);
+  g.dw_q = dw_q;
+  g.dw_k = dw_k;
+  g.parts = static_cast<float*>(workspace);
+  return cuda_status(launch_norm_rope_grad(g, dtype, s));
+}
+
+int moe_attn_append_norm(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* q_out,
+                         const moe_attn_rows* k, const moe_attn_rows* v, const int32_t* positions,
+                         const int64_t* slots, int32_t T, const moe_attn_norm* norm,
+                         const moe_attn_rotation* r, const moe_attn_cache* cache, void* stream) {
+  if (!norm) return MOE_ATTN_ERR_INVALID_ARG;
+  int st = check_append(h, q, q_out, T, r, norm);
+  if (st != MOE_ATTN_OK || (st = validate_cache(cache)) != MOE_ATTN_OK || T == 0) return st;
+  if ((st = check_append_rows(h->cfg, q, q_out, k, v, positions, slots, T)) != MOE_ATTN_OK)
+    return st;
+  const OnDevice on(h->device);
+  if ((st = on.status()) != MOE_ATTN_OK) return st;
+  NormParams p = append_params(h, q, q_out, k, v, positions, slots, T, norm, r, cache->num_pages);
+  p.r.k_pages = static_cast<uint16_t*>(cache->k);
+  p.r.v_pages = static_cast<uint16_t*>(cache->v);
+  p.r.page_stride = cache->page_stride;
+  p.r.token_stride = cache->token_stride;
+  p.r.head_stride = cache->head_stride;
+  return cuda_status(launch_norm_rope(p, h->cfg.dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_attn_append8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* q_out,
+                     const moe_attn_rows* k, const moe_attn_rows* v, const int32_t* positions,
+                     const int64_t* slots, int32_t T, const moe_attn_norm* norm,
+                     const moe_attn_rotation* r, const moe_attn_cache8* cache, void* stream) {
+  int st = check_append(h, q, q_out, T, r, norm);
+  if (st != MOE_ATTN_OK || (st = validate_cache8(h->cfg, cache)) != MOE_ATTN_OK || T == 0) return st;
+  if ((st = check_append_rows(h->cfg, q, q_out, k, v, positions, slots, T)) != MOE_ATTN_OK)
+    return st;
+  const OnDevice on(h->device);
+  if ((st = on.status()) != MOE_ATTN_OK) return st;
+  Append8Params g{};
+  g.p = append_params(h, q, q_out, k, v, positions, slots, T, norm, r, cache->num_pages);
+  g.c = cache_of(cache);
+  return cuda_status(launch_append8(g, h->cfg.dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_attn_read8(moe_attn_handle* h, const moe_attn_cache8* cache, const moe_attn_extent* e,
+                   const moe_attn_rows* k_out, const moe_attn_rows* v_out, void* stream) {
+  if (!h || !e || e->num_seqs < 0 || e->num_rows < 0) return MOE_ATTN_ERR_INVALID_ARG;
+  const moe_attn_config& c = h->cfg;
+  if (e->num_seqs > c.max_seqs) return MOE_ATTN_ERR_TOO_MANY_TOKENS;
+  int st = validate_cache8(c, cache);
+  if (st != MOE_ATTN_OK || e->num_seqs == 0 || e->num_rows == 0) return st;
+  if ((st = validate_rows(k_out)) != MOE_ATTN_OK || (st = validate_rows(v_out)) != MOE_ATTN_OK)
+    return st;
+  if (!apart(k_out, e->num_rows, c.kv_heads, c.head_dim) ||
+      !apart(v_out, e->num_rows, c.kv_heads, c.head_dim) ||
+      share(k_out, c.kv_heads, v_out, c.kv_heads, e->num_rows, c.head_dim))
+    return MOE_ATTN_ERR_INVALID_ARG;
+  if (!e->cu_rows || !e->first || !e->page_table || e->columns < 1 || e->table_stride < e->columns)
+    return MOE_ATTN_ERR_INVALID_ARG;
+  if ((long long)e->columns * c.page_size > (1LL << 29)) return MOE_ATTN_ERR_UNSUPPORTED_SHAPE;
+  const OnDevice on(h->device);
+  if ((st = on.status()) != MOE_ATTN_OK) return st;
+  Read8Params p{};
+  p.c = cache_of(cache);
+  p.cu = e->cu_rows;
+  p.first = e->first;
+  p.page_table = e->page_table;
+  p.table_stride = e->table_stride;
+  p.columns = e->columns;
+  p.num_seqs = e->num_seqs;
+  p.rows = e->num_rows;
+  p.hk = c.kv_heads;
+  p.head_dim = c.head_dim;
+  p.page_shift = log2i(c.page_size);
+  p.k_out = rows(k_out);
+  p.v_out = rows(v_out);
+  p.err = h->err;
+  return cuda_status(launch_read8(p, c.dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_attn_forward8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out,
+                      float* lse, const moe_attn_cache8* cache, const moe_attn_batch* b,
+                      const moe_attn_scores* sc, int32_t sinks, void* stream) {
+  int st = check_call(h, b, sc, sinks);
+  if (st != MOE_ATTN_OK) return st;
+  const moe_attn_config& c = h->cfg;
+  if ((st = validate_cache8(c, cache)) != MOE_ATTN_OK) return st;
+  if (b->num_tokens == 0 || b->num_seqs == 0) return MOE_ATTN_OK;
+  if ((st = check_batch(c, q, out, b)) != MOE_ATTN_OK) return st;
+  const OnDevice on(h->device);
+  if ((st = on.status()) != MOE_ATTN_OK) return st;
+  Attn8Params p{};
+  p.a = params_of(h, q, out, lse, cache->num_pages, b, sc, sinks);
+  p.c = cache_of(cache);
+  p.dtype = c.dtype;
+  return cuda_status(launch_attn8_rows(p, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_attn_forward_sinks(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out,
+                           float* lse, const moe_attn_cache* cache, const moe_attn_batch* b,
+                           const moe_attn_scores* sc, int32_t sinks, void* stream) {
+  return forward_sinks(h, q, out, lse, cache, b, sc, sinks, stream);
+}
+
+}  // extern "C"

@@ -93,7 +93,7 @@ __device__ __forceinline__ Span item_of(const AttnParams& p, int s) {
   Span r = read_sequence(p.b, p.page_shift, s, p.err);
   r.blocks = 0;
   if (r.n > 0)  // and at most max_q, which is kRows / group or less
-    span_blocks(r, r.kv - r.n, r.kv - 1, p.sc.window, prefix_of(p.sc, s, r.kv), decode_block(ND));
+    span_blocks(r, r.kv - r.n, r.kv - 1, p.sc, prefix_of(p.sc, s, r.kv), decode_block(ND));
   return r;
 }
 
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int prefix = prefix_of(p.sc, g.seq, it.kv);
     // Q fragments; rows gid and gid + 8 are (token r / group, head r % group)
     uint32_t qf[ND * 4][4];
-    int pos[2];
+    int pos[2], kept[2];
     float slope[2];
     const uint16_t* qp[2];
 #pragma unroll
@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = min(gid + 8 * i, rows - 1);
       const int tok = r / p.group, h = head * p.group + (r - tok * p.group);
       pos[i] = it.kv - it.n + tok;
+      kept[i] = kept_of(p.sc, prefix, pos[i]);
       slope[i] = FORM != kPlain && p.sc.slopes ? p.sc.slopes[h] : 0.0f;
       qp[i] = p.q.p + (long long)(it.first + tok) * p.q.token + (long long)h * p.q.head;
     }
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key = k0 + t * 8 + 2 * tig + (i & 1), r = i >> 1;
                 const int away = pos[r] - key;
                 const bool seen =
-                    key < it.kv && (key < prefix || (away >= 0 && (p.sc.window == 0 ||
+                    key < it.kv && (key < kept[r] || (away >= 0 && (p.sc.window == 0 ||
                                                                   away < p.sc.window)));
                 sacc[t][i] = seen ? score<FORM>(p.sc, sacc[t][i], slope[r], away) : -INFINITY;
               }

@@ -370,7 +370,7 @@ __device__ __forceinline__ Entry entry_of(const AttnParams& p, const Seq& q, int
   e.prefix = q.prefix;
   Span r;
   r.kv = q.kv;
-  span_blocks(r, e.p0, e.p0 + e.ntok - 1, p.sc.window, e.prefix, kBlk);
+  span_blocks(r, e.p0, e.p0 + e.ntok - 1, p.sc, e.prefix, kBlk);
   e.near = r.near;
   e.skip = r.skip;
   e.blocks = r.blocks;
@@ -1143,7 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!whole) {
           // bit i of word w: this row sees key kb + 32 w + i
           const int a = pos - kb + 1, b = p.sc.window ? pos - p.sc.window - kb + 1 : 0;
-          const int pre = prefix - kb;
+          const int pre = kept_of(p.sc, prefix, pos) - kb;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const uint32_t bits = (below(a - 32 * w) & ~below(b - 32 * w)) | below(pre - 32 * w);

@@ -1,5 +1,5 @@
 /* Argument marshalling of the attention operators' Python calls: checks the
- * tensors, describes them to the C ABI (include/moe_attn.h) and calls it. Small
+ * tensors, describes them to the C ABI (include/moe_attn.h, moe_attn8.h) and calls it. Small
  * calls are bound by this work (an append of 64 tokens took 13 us of host time
  * through ctypes, 4 us of GPU time), so it is done here. Tensors are read
  * through their Python attributes; nothing of torch's own ABI is used. */
@@ -8,7 +8,7 @@
 #include <limits.h>
 #include <math.h>
 
-#include "../../include/moe_attn.h"
+#include "../../include/moe_attn8.h"
 
 typedef int (*rope_fn)(const moe_attn_rows*, const moe_attn_rows*, const int32_t*, int32_t, int32_t,
                        int32_t, int32_t, const moe_attn_rotation*, void*);
@@ -19,16 +19,50 @@ typedef int (*append_fn)(moe_attn_handle*, const moe_attn_rows*, const moe_attn_
 typedef int (*forward_fn)(moe_attn_handle*, const moe_attn_rows*, const moe_attn_rows*, float*,
                           const moe_attn_cache*, const moe_attn_batch*, const moe_attn_scores*,
                           void*);
+typedef int (*norm_rope_fn)(const moe_attn_rows*, const moe_attn_rows*, const moe_attn_rows*,
+                            const moe_attn_rows*, const int32_t*, int32_t, int32_t, int32_t,
+                            int32_t, int32_t, const moe_attn_norm*, const moe_attn_rotation*,
+                            void*);
+typedef int (*norm_bytes_fn)(int32_t, int32_t, int32_t, int32_t, size_t*);
+typedef int (*norm_back_fn)(const moe_attn_rows*, const moe_attn_rows*, const moe_attn_rows*,
+                            float*, const moe_attn_rows*, const moe_attn_rows*,
+                            const moe_attn_rows*, float*, const int32_t*, int32_t, int32_t,
+                            int32_t, int32_t, int32_t, const moe_attn_norm*,
+                            const moe_attn_rotation*, void*, size_t, void*);
+typedef int (*append_norm_fn)(moe_attn_handle*, const moe_attn_rows*, const moe_attn_rows*,
+                              const moe_attn_rows*, const moe_attn_rows*, const int32_t*,
+                              const int64_t*, int32_t, const moe_attn_norm*,
+                              const moe_attn_rotation*, const moe_attn_cache*, void*);
+typedef int (*append8_fn)(moe_attn_handle*, const moe_attn_rows*, const moe_attn_rows*,
+                          const moe_attn_rows*, const moe_attn_rows*, const int32_t*,
+                          const int64_t*, int32_t, const moe_attn_norm*, const moe_attn_rotation*,
+                          const moe_attn_cache8*, void*);
+typedef int (*read8_fn)(moe_attn_handle*, const moe_attn_cache8*, const moe_attn_extent*,
+                        const moe_attn_rows*, const moe_attn_rows*, void*);
+typedef int (*forward8_fn)(moe_attn_handle*, const moe_attn_rows*, const moe_attn_rows*, float*,
+                           const moe_attn_cache8*, const moe_attn_batch*, const moe_attn_scores*,
+                           int32_t, void*);
+typedef int (*forward_sinks_fn)(moe_attn_handle*, const moe_attn_rows*, const moe_attn_rows*,
+                                float*, const moe_attn_cache*, const moe_attn_batch*,
+                                const moe_attn_scores*, int32_t, void*);
 
 static struct {
   rope_fn rope;
   append_fn append;
   forward_fn forward;
+  norm_rope_fn norm_rope;
+  norm_bytes_fn norm_bytes;
+  norm_back_fn norm_back;
+  append_norm_fn append_norm;
+  append8_fn append8;
+  read8_fn read8;
+  forward8_fn forward8;
+  forward_sinks_fn forward_sinks;
   PyObject *check;                       /* (status, what): raises */
   PyObject *empty, *raw_stream, *current_device;
   PyObject *grad_enabled, *inference_enabled; /* of the thread */
   PyObject *increment_version;           /* (tensors): they were written to */
-  PyObject *bf16, *fp16, *f32, *i32, *i64;
+  PyObject *bf16, *fp16, *f32, *i32, *i64, *f8;
   PyObject *shape, *stride, *dtype, *device, *get_device, *data_ptr, *is_contiguous,
       *requires_grad;
   PyObject *empty_names;                 /* ("dtype", "device") */
@@ -254,6 +288,100 @@ static int cache_of(const layer_t* l, PyObject* k, PyObject* v, moe_attn_cache* 
   return pointer_of(k, &c->k) || pointer_of(v, &c->v) ? -1 : 0;
 }
 
+/* The 8-bit cache: e4m3 codes in the form of k_pages and v_pages, fp32 scales
+ * [pages, kv_heads, page / 16]. */
+static int cache8_of(const layer_t* l, PyObject* k, PyObject* v, PyObject* ks, PyObject* vs,
+                     moe_attn_cache8* c) {
+  if (ks == Py_None || vs == Py_None) {
+    PyErr_SetString(PyExc_ValueError, "k_scales and v_scales come together");
+    return -1;
+  }
+  layer_t codes = *l;
+  codes.dtype = G.f8;
+  moe_attn_cache p;
+  if (cache_of(&codes, k, v, &p)) return -1;
+  c->k = p.k, c->v = p.v, c->num_pages = p.num_pages;
+  c->page_stride = p.page_stride, c->token_stride = p.token_stride, c->head_stride = p.head_stride;
+  long long d[MAX_DIMS], s[MAX_DIMS], d2[MAX_DIMS], s2[MAX_DIMS];
+  const int n = shape_of(ks, d), n2 = shape_of(vs, d2);
+  if (n < 0 || n2 < 0) return -1;
+  const long long blocks = l->page / MOE_ATTN8_BLOCK;
+  if (n != 3 || d[0] != c->num_pages || d[1] != l->kv_heads || d[2] != blocks) {
+    PyErr_Format(PyExc_ValueError, "k_scales must be [%lld, %lld, %lld]", (long long)c->num_pages,
+                 l->kv_heads, blocks);
+    return -1;
+  }
+  if (strides_of(ks, s) < 0 || strides_of(vs, s2) < 0) return -1;
+  int same = n2 == 3;
+  for (int i = 0; same && i < 3; ++i) same = d[i] == d2[i] && (s[i] == s2[i] || d[i] == 1);
+  /* scales that lie on each other would be raised by one another's blocks */
+  for (int i = 0; same && i < 3; ++i) same = d[i] == 1 || s[i] > 0;
+  if (!same) {
+    PyErr_SetString(PyExc_ValueError, "k_scales and v_scales must have one shape and strides");
+    return -1;
+  }
+  if (placed(ks, G.f32, l->index) != 1) return refuse_place(ks, "k_scales", G.f32, l->index);
+  if (placed(vs, G.f32, l->index) != 1) return refuse_place(vs, "v_scales", G.f32, l->index);
+  c->scale_page_stride = d[0] > 1 ? s[0] : 0;
+  c->scale_head_stride = d[1] > 1 ? s[1] : 0;
+  c->scale_block_stride = d[2] > 1 ? s[2] : 0;
+  void *kp, *vp;
+  if (pointer_of(ks, &kp) || pointer_of(vs, &vp)) return -1;
+  c->k_scales = kp, c->v_scales = vp;
+  return 0;
+}
+
+/* a weight of heads [dim] or [heads, dim] */
+static int weight_of(PyObject* t, long long heads, long long dim, PyObject* dtype, long index,
+                     const void** w, int64_t* stride, int32_t* type, const char* what) {
+  long long d[MAX_DIMS], s[MAX_DIMS];
+  const int n = shape_of(t, d);
+  if (n < 0 || strides_of(t, s) < 0) return -1;
+  const int each = n == 2 && d[0] == heads;
+  if (!(n == 1 || each) || d[n - 1] != dim || (s[n - 1] != 1 && dim > 1)) {
+    PyErr_Format(PyExc_ValueError, "%s must be [%lld] or [%lld, %lld], contiguous along head_dim",
+                 what, dim, heads, dim);
+    return -1;
+  }
+  PyObject* own = PyObject_GetAttr(t, G.dtype);
+  if (!own) return -1;
+  Py_DECREF(own);
+  const int32_t wide = own == G.f32 ? MOE_ATTN_WEIGHT_F32 : MOE_ATTN_WEIGHT_SAME;
+  if (placed(t, wide ? G.f32 : dtype, index) != 1) return refuse_place(t, what, dtype, index);
+  if (*type >= 0 && *type != wide) {
+    PyErr_SetString(PyExc_ValueError, "the weights of q and k must have one type");
+    return -1;
+  }
+  *type = wide;
+  *stride = each && heads > 1 ? s[0] : each ? dim : 0;
+  void* p;
+  if (pointer_of(t, &p)) return -1;
+  *w = p;
+  return 0;
+}
+
+/* t: (q_weight, k_weight, eps, offset); heads of 0: not looked at */
+static int norm_of(PyObject* t, long long hq, long long hk, long long dim, PyObject* dtype,
+                   long index, moe_attn_norm* n) {
+  if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 4) {
+    PyErr_SetString(PyExc_ValueError, "norm must be a HeadNorm");
+    return -1;
+  }
+  int32_t type = -1;
+  n->q_weight = n->k_weight = NULL;
+  n->q_head_stride = n->k_head_stride = 0;
+  if (hq && weight_of(PyTuple_GET_ITEM(t, 0), hq, dim, dtype, index, &n->q_weight,
+                      &n->q_head_stride, &type, "q_weight"))
+    return -1;
+  if (hk && weight_of(PyTuple_GET_ITEM(t, 1), hk, dim, dtype, index, &n->k_weight,
+                      &n->k_head_stride, &type, "k_weight"))
+    return -1;
+  n->weight_type = type > 0 ? MOE_ATTN_WEIGHT_F32 : MOE_ATTN_WEIGHT_SAME;
+  return float_of(PyTuple_GET_ITEM(t, 2), &n->eps) || float_of(PyTuple_GET_ITEM(t, 3), &n->offset)
+             ? -1
+             : 0;
+}
+
 /* raises for a status other than 0 */
 static int checked(int status, const char* what) {
   if (!status) return 0;
@@ -272,7 +400,7 @@ static int asked(PyObject* what) {
 }
 
 /* No gradient runs through these calls: refuses tensors that ask for one. */
-static int no_gradient(PyObject* const* t, int n, const char* what) {
+static int no_gradient_but(PyObject* const* t, int n, const char* what, const char* but) {
   const int on = asked(G.grad_enabled);
   for (int i = 0; i < n && on == 1; ++i) {
     if (t[i] == Py_None) continue;
@@ -282,12 +410,16 @@ static int no_gradient(PyObject* const* t, int n, const char* what) {
     if (v == Py_True) {
       PyErr_Format(PyExc_ValueError,
                    "%s has no autograd formula: call it under torch.no_grad(), or on detached "
-                   "tensors (the gradient of rotary positions is moe_attn_rope with inverse=True)",
-                   what);
+                   "tensors (the gradient of %s)",
+                   what, but);
       return -1;
     }
   }
   return on < 0 ? -1 : 0;
+}
+
+static int no_gradient(PyObject* const* t, int n, const char* what) {
+  return no_gradient_but(t, n, what, "rotary positions is moe_attn_rope with inverse=True");
 }
 
 /* Tells autograd which of the outputs that the caller gave were written to, so that
@@ -412,15 +544,17 @@ static PyObject* layer(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 /* append(layer, q, k, v, positions, slots, k_pages, v_pages, freq, layout,
- * magnitude, q_out, stream): q_out, or None without q */
+ * magnitude, q_out, norm, k_scales, v_scales, stream): q_out, or None without q */
 static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (arity(n, 13, "append")) return NULL;
+  if (arity(n, 16, "append")) return NULL;
   const layer_t* l = PyCapsule_GetPointer(a[0], "moe_attn_layer");
   if (!l) return NULL;
   moe_attn_rows q, qo, k, v;
   moe_attn_rotation r;
   moe_attn_cache c;
+  moe_attn_cache8 c8;
+  moe_attn_norm norm;
   const void *pos, *slots;
   void* stream;
   const long long T = rows_of(a[2], l->kv_heads, l->dim, l->dtype, l->index, &k, "k");
@@ -436,38 +570,71 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
                                                          : "q_out without q");
     return NULL;
   }
+  const int bits8 = a[13] != Py_None || a[14] != Py_None, with_norm = a[12] != Py_None;
   if (rotation_of(a[8], a[9], a[10], 0, l->index, &r) ||
       vector_of(a[4], T, G.i32, l->index, &pos, "positions") < 0 ||
-      vector_of(a[5], T, G.i64, l->index, &slots, "slots") < 0 || cache_of(l, a[6], a[7], &c) ||
-      stream_of(a[12], l->index, &stream))
+      vector_of(a[5], T, G.i64, l->index, &slots, "slots") < 0 ||
+      (bits8 ? cache8_of(l, a[6], a[7], a[13], a[14], &c8) : cache_of(l, a[6], a[7], &c)) ||
+      (with_norm &&
+       norm_of(a[12], with_q ? l->q_heads : 0, l->kv_heads, l->dim, l->dtype, l->index, &norm)) ||
+      stream_of(a[15], l->index, &stream))
     return NULL;
-  PyObject* const tracked[6] = {a[1], a[2], a[3], a[6], a[7], a[11]};
-  if (no_gradient(tracked, 6, "PagedAttention.append")) return NULL;
+  PyObject* const tracked[10] = {
+      a[1],  a[2],  a[3],  a[6],  a[7],
+      a[11], a[13], a[14], with_norm && with_q ? PyTuple_GET_ITEM(a[12], 0) : Py_None,
+      with_norm ? PyTuple_GET_ITEM(a[12], 1) : Py_None};
+  if (no_gradient(tracked, 10, "PagedAttention.append")) return NULL;
   PyObject* out = with_q ? output(a[11], T, l->q_heads, l->dim, l->dtype, l->device, l->index, &qo,
                                   "q_out")
                          : Py_NewRef(Py_None);
   if (!out) return NULL;
   int st;
   Py_BEGIN_ALLOW_THREADS;
-  st = G.append(l->handle, with_q ? &q : NULL, with_q ? &qo : NULL, &k, &v, pos, slots, (int32_t)T,
-                &r, &c, stream);
+  if (bits8)
+    st = G.append8(l->handle, with_q ? &q : NULL, with_q ? &qo : NULL, &k, &v, pos, slots,
+                   (int32_t)T, with_norm ? &norm : NULL, &r, &c8, stream);
+  else if (with_norm)
+    st = G.append_norm(l->handle, with_q ? &q : NULL, with_q ? &qo : NULL, &k, &v, pos, slots,
+                       (int32_t)T, &norm, &r, &c, stream);
+  else
+    st = G.append(l->handle, with_q ? &q : NULL, with_q ? &qo : NULL, &k, &v, pos, slots,
+                  (int32_t)T, &r, &c, stream);
   Py_END_ALLOW_THREADS;
-  if (checked(st, "moe_attn_append") || wrote(a + 11, 1)) Py_CLEAR(out);
+  if (checked(st, bits8 ? "moe_attn_append8" : "moe_attn_append") || wrote(a + 11, 1)) Py_CLEAR(out);
   return out;
 }
 
+/* a page table, int32 [seqs, columns] */
+static int table_of(PyObject* t, long long seqs, long index, void** p, long long* columns,
+                    long long* stride) {
+  long long d[MAX_DIMS], st[MAX_DIMS];
+  const int dims = shape_of(t, d);
+  if (dims < 0 || strides_of(t, st) < 0) return -1;
+  if (placed(t, G.i32, index) != 1) return refuse_place(t, "page_table", G.i32, index);
+  if (dims != 2 || d[0] != seqs || (st[1] != 1 && d[1] > 1) || d[1] > INT_MAX) {
+    PyErr_Format(PyExc_ValueError,
+                 "page_table must be [%lld, columns], contiguous along the columns", seqs);
+    return -1;
+  }
+  *columns = d[1];
+  *stride = seqs > 1 ? st[0] : d[1];
+  return pointer_of(t, p);
+}
+
 /* forward(layer, q, k_pages, v_pages, page_table, cu_q, kv_len, max_q, scale,
- * softcap, window, slopes, prefix, out, lse, return_lse, stream): out, or (out, lse) */
+ * softcap, window, slopes, prefix, out, lse, return_lse, sinks, k_scales, v_scales,
+ * stream): out, or (out, lse) */
 static PyObject* forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (arity(n, 17, "forward")) return NULL;
+  if (arity(n, 20, "forward")) return NULL;
   const layer_t* l = PyCapsule_GetPointer(a[0], "moe_attn_layer");
   if (!l) return NULL;
   moe_attn_rows q, o;
   moe_attn_cache c;
+  moe_attn_cache8 c8;
   moe_attn_batch b;
   moe_attn_scores s = {0};
-  long long d[MAX_DIMS], st[MAX_DIMS];
+  long long d[MAX_DIMS];
   const void* p;
   void *stream, *lse_at = NULL, *table;
   const long long T = rows_of(a[1], l->q_heads, l->dim, l->dtype, l->index, &q, "q");
@@ -481,24 +648,18 @@ static PyObject* forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   b.kv_len = p;
   if (vector_of(a[5], seqs + 1, G.i32, l->index, &p, "cu_q") < 0) return NULL;
   b.cu_q = p;
-  const int dims = shape_of(a[4], d);
-  if (dims < 0 || strides_of(a[4], st) < 0) return NULL;
-  if (placed(a[4], G.i32, l->index) != 1) {
-    refuse_place(a[4], "page_table", G.i32, l->index);
-    return NULL;
-  }
-  if (dims != 2 || d[0] != seqs || (st[1] != 1 && d[1] > 1) || d[1] > INT_MAX) {
-    PyErr_Format(PyExc_ValueError,
-                 "page_table must be [%lld, columns], contiguous along the columns", seqs);
-    return NULL;
-  }
-  if (pointer_of(a[4], &table)) return NULL;
+  long long columns, table_stride;
+  if (table_of(a[4], seqs, l->index, &table, &columns, &table_stride)) return NULL;
   b.page_table = table;
-  b.columns = (int32_t)d[1];
-  b.table_stride = seqs > 1 ? st[0] : d[1];
+  b.columns = (int32_t)columns;
+  b.table_stride = table_stride;
   b.num_seqs = (int32_t)seqs;
   b.num_tokens = (int32_t)T;
-  if (int32_of(a[7], &b.max_q, "max_q") || cache_of(l, a[2], a[3], &c)) return NULL;
+  const int bits8 = a[17] != Py_None || a[18] != Py_None;
+  int32_t sinks;
+  if (int32_of(a[7], &b.max_q, "max_q") || int32_of(a[16], &sinks, "sinks") ||
+      (bits8 ? cache8_of(l, a[2], a[3], a[17], a[18], &c8) : cache_of(l, a[2], a[3], &c)))
+    return NULL;
   if (a[8] == Py_None)
     s.scale = (float)(1.0 / sqrt((double)l->dim));
   else if (float_of(a[8], &s.scale))
@@ -513,9 +674,9 @@ static PyObject* forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     s.prefix = p;
   }
   const int with_lse = PyObject_IsTrue(a[15]);
-  if (with_lse < 0 || stream_of(a[16], l->index, &stream)) return NULL;
-  PyObject* const tracked[6] = {a[1], a[2], a[3], a[11], a[13], a[14]};
-  if (no_gradient(tracked, 6, "PagedAttention.forward")) return NULL;
+  if (with_lse < 0 || stream_of(a[19], l->index, &stream)) return NULL;
+  PyObject* const tracked[8] = {a[1], a[2], a[3], a[11], a[13], a[14], a[17], a[18]};
+  if (no_gradient(tracked, 8, "PagedAttention.forward")) return NULL;
   PyObject* lse;
   if (a[14] != Py_None) {
     const int ld = shape_of(a[14], d);
@@ -549,31 +710,267 @@ static PyObject* forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   }
   int status;
   Py_BEGIN_ALLOW_THREADS;
-  status = G.forward(l->handle, &q, &o, lse_at, &c, &b, &s, stream);
+  if (bits8)
+    status = G.forward8(l->handle, &q, &o, lse_at, &c8, &b, &s, sinks, stream);
+  else if (sinks)
+    status = G.forward_sinks(l->handle, &q, &o, lse_at, &c, &b, &s, sinks, stream);
+  else
+    status = G.forward(l->handle, &q, &o, lse_at, &c, &b, &s, stream);
   Py_END_ALLOW_THREADS;
   PyObject* result = NULL;
-  if (!checked(status, "moe_attn_forward") && !wrote(tracked + 4, 2))
+  if (!checked(status, bits8 ? "moe_attn_forward8" : "moe_attn_forward") && !wrote(tracked + 4, 2))
     result = with_lse ? PyTuple_Pack(2, out, lse) : Py_NewRef(out);
   Py_DECREF(out);
   Py_DECREF(lse);
   return result;
 }
 
-/* setup(rope, append, forward, check, empty, raw_stream, current_device,
- * grad_enabled, inference_enabled, increment_version, bf16, fp16, f32, i32, i64): addresses of the library's functions, what raises for a
- * status, and of torch what is needed here. Once, before any other call. */
+/* read(layer, k_pages, v_pages, page_table, cu_rows, first, rows, k_scales, v_scales,
+ * k_out, v_out, stream): (k, v) */
+static PyObject* read_back(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (arity(n, 12, "read")) return NULL;
+  const layer_t* l = PyCapsule_GetPointer(a[0], "moe_attn_layer");
+  if (!l) return NULL;
+  moe_attn_cache8 c;
+  moe_attn_extent e;
+  moe_attn_rows ko, vo;
+  const void* p;
+  void *stream, *table;
+  long long columns, stride;
+  const long long seqs = vector_of(a[5], -1, G.i32, l->index, &p, "first");
+  if (seqs < 0) return NULL;
+  if (seqs >= INT_MAX) {
+    PyErr_SetString(PyExc_ValueError, "too many sequences");
+    return NULL;
+  }
+  e.first = p;
+  if (vector_of(a[4], seqs + 1, G.i32, l->index, &p, "cu_rows") < 0) return NULL;
+  e.cu_rows = p;
+  if (table_of(a[3], seqs, l->index, &table, &columns, &stride) ||
+      int32_of(a[6], &e.num_rows, "rows") || cache8_of(l, a[1], a[2], a[7], a[8], &c) ||
+      stream_of(a[11], l->index, &stream))
+    return NULL;
+  if (e.num_rows < 0) {
+    PyErr_SetString(PyExc_ValueError, "rows must not be negative");
+    return NULL;
+  }
+  e.page_table = table;
+  e.columns = (int32_t)columns;
+  e.table_stride = stride;
+  e.num_seqs = (int32_t)seqs;
+  PyObject* const tracked[6] = {a[1], a[2], a[7], a[8], a[9], a[10]};
+  if (no_gradient(tracked, 6, "PagedAttention.read")) return NULL;
+  PyObject* k = output(a[9], e.num_rows, l->kv_heads, l->dim, l->dtype, l->device, l->index, &ko,
+                       "k_out");
+  if (!k) return NULL;
+  PyObject* v = output(a[10], e.num_rows, l->kv_heads, l->dim, l->dtype, l->device, l->index, &vo,
+                       "v_out");
+  if (!v) {
+    Py_DECREF(k);
+    return NULL;
+  }
+  int status;
+  Py_BEGIN_ALLOW_THREADS;
+  status = G.read8(l->handle, &c, &e, &ko, &vo, stream);
+  Py_END_ALLOW_THREADS;
+  PyObject* result = NULL;
+  if (!checked(status, "moe_attn_read8") && !wrote(a + 9, 2)) result = PyTuple_Pack(2, k, v);
+  Py_DECREF(k);
+  Py_DECREF(v);
+  return result;
+}
+
+/* What norm_rope and its gradient are called with: q or k may be None. */
+typedef struct {
+  PyObject *dtype, *device;   /* device: a new reference */
+  long index;
+  int32_t code;
+  long long tokens, hq, hk, dim;
+  moe_attn_rows q, k;
+  moe_attn_rotation r;
+  moe_attn_norm norm;
+  const void* pos;
+  void* stream;
+} heads_t;
+
+/* 0, 1 where another device than the tensors' is current, -1 with an error */
+static int heads_of(PyObject* q, PyObject* k, PyObject* positions, PyObject* freq, PyObject* norm,
+                    PyObject* layout, PyObject* magnitude, PyObject* stream, heads_t* t) {
+  PyObject* x = q != Py_None ? q : k;
+  t->device = NULL;
+  t->dtype = PyObject_GetAttr(x, G.dtype);
+  if (!t->dtype) return -1;
+  Py_DECREF(t->dtype); /* torch keeps its types for good */
+  t->code = t->dtype == G.bf16 ? MOE_ATTN_BF16 : t->dtype == G.fp16 ? MOE_ATTN_FP16 : -1;
+  PyObject* on = method(x, G.get_device);
+  if (!on) return -1;
+  t->index = PyLong_AsLong(on);
+  Py_DECREF(on);
+  if (PyErr_Occurred()) return -1;
+  long long dq[MAX_DIMS] = {0}, dk[MAX_DIMS] = {0};
+  const int nq = q == Py_None ? 3 : shape_of(q, dq), nk = k == Py_None ? 3 : shape_of(k, dk);
+  if (nq < 0 || nk < 0) return -1;
+  if (t->code < 0 || t->index < 0 || nq != 3 || nk != 3 || dq[1] > INT_MAX || dk[1] > INT_MAX ||
+      dq[2] > INT_MAX || dk[2] > INT_MAX) {
+    PyErr_SetString(PyExc_ValueError,
+                    "q and k must be bf16 or fp16 CUDA tensors [tokens, heads, head_dim]");
+    return -1;
+  }
+  PyObject* current = PyObject_CallNoArgs(G.current_device);
+  if (!current) return -1;
+  const long now = PyLong_AsLong(current);
+  Py_DECREF(current);
+  if (now != t->index) return PyErr_Occurred() ? -1 : 1;
+  t->hq = dq[1], t->hk = dk[1];
+  t->dim = q != Py_None ? dq[2] : dk[2];
+  t->tokens = q != Py_None ? dq[0] : dk[0];
+  if (q != Py_None && rows_of(q, t->hq, t->dim, t->dtype, t->index, &t->q, "q") < 0) return -1;
+  if (k != Py_None && rows_of(k, t->hk, t->dim, t->dtype, t->index, &t->k, "k") < 0) return -1;
+  if (q != Py_None && k != Py_None && dq[0] != dk[0]) {
+    PyErr_SetString(PyExc_ValueError, "q and k differ in tokens");
+    return -1;
+  }
+  if (rotation_of(freq, layout, magnitude, 0, t->index, &t->r) ||
+      vector_of(positions, t->tokens, G.i32, t->index, &t->pos, "positions") < 0 ||
+      norm_of(norm, t->hq, t->hk, t->dim, t->dtype, t->index, &t->norm) ||
+      stream_of(stream, t->index, &t->stream))
+    return -1;
+  PyObject* const tracked[4] = {q, k, t->hq ? PyTuple_GET_ITEM(norm, 0) : Py_None,
+                                t->hk ? PyTuple_GET_ITEM(norm, 1) : Py_None};
+  if (no_gradient_but(tracked, 4, "moe_attn_norm_rope", "it is moe_attn_norm_rope_backward"))
+    return -1;
+  t->device = PyObject_GetAttr(x, G.device);
+  return t->device ? 0 : -1;
+}
+
+/* norm_rope(q, k, positions, freq, norm, layout, magnitude, q_out, k_out, stream):
+ * (q_out, k_out), or NotImplemented where another device is current */
+static PyObject* norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (arity(n, 10, "norm_rope")) return NULL;
+  heads_t t;
+  const int st = heads_of(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[9], &t);
+  if (st) return st < 0 ? NULL : Py_NewRef(Py_NotImplemented);
+  moe_attn_rows qo, ko;
+  PyObject* out[2] = {NULL, NULL};
+  PyObject* result = NULL;
+  if (no_gradient(a + 7, 2, "moe_attn_norm_rope")) goto done;
+  for (int i = 0; i < 2; ++i) {
+    if (a[i] == Py_None) {
+      if (a[7 + i] != Py_None) {
+        PyErr_SetString(PyExc_ValueError, "an output without its input");
+        goto done;
+      }
+      out[i] = Py_NewRef(Py_None);
+    } else {
+      out[i] = output(a[7 + i], t.tokens, i ? t.hk : t.hq, t.dim, t.dtype, t.device, t.index,
+                      i ? &ko : &qo, i ? "k_out" : "q_out");
+    }
+    if (!out[i]) goto done;
+  }
+  const int with_q = a[0] != Py_None, with_k = a[1] != Py_None;
+  int status;
+  Py_BEGIN_ALLOW_THREADS;
+  status = G.norm_rope(with_q ? &t.q : NULL, with_q ? &qo : NULL, with_k ? &t.k : NULL,
+                       with_k ? &ko : NULL, t.pos, (int32_t)t.tokens, (int32_t)t.hq, (int32_t)t.hk,
+                       (int32_t)t.dim, t.code, &t.norm, &t.r, t.stream);
+  Py_END_ALLOW_THREADS;
+  if (!checked(status, "moe_attn_norm_rope") && !wrote(a + 7, 2))
+    result = PyTuple_Pack(2, out[0], out[1]);
+done:
+  Py_XDECREF(out[0]);
+  Py_XDECREF(out[1]);
+  Py_DECREF(t.device);
+  return result;
+}
+
+/* norm_back(dq, dk, q, k, positions, freq, norm, layout, magnitude): the gradients of
+ * (q, k, q_weight, k_weight), on the current stream; NotImplemented as above */
+static PyObject* norm_back(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (arity(n, 9, "norm_back")) return NULL;
+  if ((a[0] == Py_None) != (a[2] == Py_None) || (a[1] == Py_None) != (a[3] == Py_None)) {
+    PyErr_SetString(PyExc_ValueError, "dq belongs to q, and dk to k");
+    return NULL;
+  }
+  heads_t t;
+  const int st = heads_of(a[2], a[3], a[4], a[5], a[6], a[7], a[8], Py_None, &t);
+  if (st) return st < 0 ? NULL : Py_NewRef(Py_NotImplemented);
+  moe_attn_rows dy[2], dx[2];
+  PyObject *out[4] = {NULL, NULL, NULL, NULL}, *work = NULL, *result = NULL;
+  void *dw[2] = {NULL, NULL}, *at = NULL;
+  size_t bytes = 0;
+  if (no_gradient(a, 2, "moe_attn_norm_rope_backward")) goto done;
+  for (int i = 0; i < 2; ++i) {
+    if (a[i] == Py_None) {
+      out[i] = Py_NewRef(Py_None);
+      out[2 + i] = Py_NewRef(Py_None);
+      continue;
+    }
+    const long long heads = i ? t.hk : t.hq;
+    const long long rows = rows_of(a[i], heads, t.dim, t.dtype, t.index, &dy[i], i ? "dk" : "dq");
+    if (rows < 0) goto done;
+    if (rows != t.tokens) {
+      PyErr_SetString(PyExc_ValueError, "the gradients differ in tokens from q and k");
+      goto done;
+    }
+    out[i] = output(Py_None, t.tokens, heads, t.dim, t.dtype, t.device, t.index, &dx[i], "");
+    const int each = (i ? t.norm.k_head_stride : t.norm.q_head_stride) != 0;
+    out[2 + i] = new_tensor(each ? Py_BuildValue("(LL)", heads, t.dim) : Py_BuildValue("(L)", t.dim),
+                            G.f32, t.device);
+    if (!out[i] || !out[2 + i] || pointer_of(out[2 + i], &dw[i])) goto done;
+  }
+  if (checked(G.norm_bytes((int32_t)t.tokens, (int32_t)t.hq, (int32_t)t.hk, (int32_t)t.dim, &bytes),
+              "moe_attn_norm_rope_backward_bytes"))
+    goto done;
+  work = new_tensor(Py_BuildValue("(L)", (long long)(bytes / 4)), G.f32, t.device);
+  if (!work || pointer_of(work, &at)) goto done;
+  const int with_q = a[0] != Py_None, with_k = a[1] != Py_None;
+  int status;
+  Py_BEGIN_ALLOW_THREADS;
+  status = G.norm_back(with_q ? &dy[0] : NULL, with_q ? &t.q : NULL, with_q ? &dx[0] : NULL, dw[0],
+                       with_k ? &dy[1] : NULL, with_k ? &t.k : NULL, with_k ? &dx[1] : NULL, dw[1],
+                       t.pos, (int32_t)t.tokens, (int32_t)t.hq, (int32_t)t.hk, (int32_t)t.dim,
+                       t.code, &t.norm, &t.r, at, bytes, t.stream);
+  Py_END_ALLOW_THREADS;
+  if (!checked(status, "moe_attn_norm_rope_backward"))
+    result = PyTuple_Pack(4, out[0], out[1], out[2], out[3]);
+done:
+  for (int i = 0; i < 4; ++i) Py_XDECREF(out[i]);
+  Py_XDECREF(work);
+  Py_DECREF(t.device);
+  return result;
+}
+
+/* setup(addresses, check, empty, raw_stream, current_device, grad_enabled,
+ * inference_enabled, increment_version, bf16, fp16, f32, i32, i64, f8): addresses of the
+ * library's functions (a tuple, in the order below), what raises for a status, and of
+ * torch what is needed here. Once, before any other call. */
 static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (arity(n, 15, "setup")) return NULL;
-  G.rope = (rope_fn)PyLong_AsVoidPtr(a[0]);
-  G.append = (append_fn)PyLong_AsVoidPtr(a[1]);
-  G.forward = (forward_fn)PyLong_AsVoidPtr(a[2]);
+  if (arity(n, 14, "setup")) return NULL;
+  void* f[11];
+  if (!PyTuple_Check(a[0]) || arity(PyTuple_GET_SIZE(a[0]), 11, "addresses")) return NULL;
+  for (int i = 0; i < 11; ++i) f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[0], i));
   if (PyErr_Occurred()) return NULL;
+  G.rope = (rope_fn)f[0];
+  G.append = (append_fn)f[1];
+  G.forward = (forward_fn)f[2];
+  G.norm_rope = (norm_rope_fn)f[3];
+  G.norm_bytes = (norm_bytes_fn)f[4];
+  G.norm_back = (norm_back_fn)f[5];
+  G.append_norm = (append_norm_fn)f[6];
+  G.append8 = (append8_fn)f[7];
+  G.read8 = (read8_fn)f[8];
+  G.forward8 = (forward8_fn)f[9];
+  G.forward_sinks = (forward_sinks_fn)f[10];
   PyObject** to[] = {&G.check,        &G.empty,             &G.raw_stream,
                      &G.current_device, &G.grad_enabled,    &G.inference_enabled,
                      &G.increment_version, &G.bf16,         &G.fp16,
-                     &G.f32,          &G.i32,               &G.i64};
-  for (int i = 0; i < 12; ++i) Py_XSETREF(*to[i], Py_NewRef(a[3 + i]));
+                     &G.f32,          &G.i32,               &G.i64,
+                     &G.f8};
+  for (int i = 0; i < 13; ++i) Py_XSETREF(*to[i], Py_NewRef(a[1 + i]));
   Py_RETURN_NONE;
 }
 
@@ -583,6 +980,9 @@ static PyMethodDef methods[] = {
     {"rope", (PyCFunction)(void (*)(void))rope, METH_FASTCALL, NULL},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, NULL},
     {"forward", (PyCFunction)(void (*)(void))forward, METH_FASTCALL, NULL},
+    {"read", (PyCFunction)(void (*)(void))read_back, METH_FASTCALL, NULL},
+    {"norm_rope", (PyCFunction)(void (*)(void))norm_rope, METH_FASTCALL, NULL},
+    {"norm_back", (PyCFunction)(void (*)(void))norm_back, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_binding", NULL, -1, methods,

@@ -1,0 +1,657 @@
+// Writing keys and values to the 8-bit cache, and reading them back.
+//
+// Append. Tokens of one block (16 rows of a page) follow each other in a call, so a
+// block's new tokens are a run of at most 16 consecutive tokens. A warp has one run
+// and one kv head, of K or of V: it reads the run's rows, raises the block's scale to
+// the power of two that their largest value needs, writes their codes, and where the
+// scale has grown re-expresses the codes of the block's other rows. A CTA looks at a
+// window of 16 tokens for the runs that begin there (one, in a prompt; up to 16, in a
+// decode step, which `split` CTAs share), so nothing is planned on the host. Keys are
+// normed and turned on the way, twice (for the largest value and for the codes)
+// rather than kept. Queries are normed and turned by CTAs of the same launch.
+// Bound by memory.
+#include "norm_parts.cuh"
+
+namespace moe {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kSms = 152;
+constexpr int kRun = kScaleBlock;
+
+// ------------------------------------------------------------------ codes
+// two values as e4m3 codes, `lo` in the low byte; what is above 448 becomes 448
+__device__ __forceinline__ uint16_t to_codes(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes_to_f16(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+__device__ __forceinline__ float2 codes_to_f32(uint16_t c) {
+  const uint32_t h = codes_to_f16(c);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// The least power of two s in 2^-64 .. 2^64 with top <= 448 s: 448 is 1.75 2^8.
+__device__ __forceinline__ float scale_for(float top) {
+  const int bits = __float_as_int(top);
+  const int e = (bits >> 23) - 127 - 8 + ((bits & 0x7fffff) > 0x600000);
+  return __int_as_float((min(max(e, -kScaleExp), kScaleExp) + 127) << 23);
+}
+// |x|, or 0 where that is no number
+__device__ __forceinline__ float size_of(float x) {
+  const float a = fabsf(x);
+  return a < INFINITY ? a : 0.0f;
+}
+__device__ __forceinline__ bool power_of_two(float s) {
+  return (__float_as_int(s) & 0x807fffff) == 0;
+}
+// what x / scale is: exactly the product where the scale is a power of two
+struct Divide {
+  float scale, inverse;
+  bool exact;
+  __device__ __forceinline__ explicit Divide(float s)
+      : scale(s), inverse(1.0f / s), exact(power_of_two(s)) {}
+  __device__ __forceinline__ float operator()(float x) const {
+    return exact ? x * inverse : __fdiv_rn(x, scale);
+  }
+};
+
+// ------------------------------------------------------------------ append
+struct Dims {  // of a launch
+  int q_ctas, token_groups;           // CTAs of the queries; along the tokens
+  int q_heads, q_z, q_tokens;         // heads of one, tokens side by side, tokens of a thread
+  int q_rows;                         // groups of heads
+  int split, combos;                  // CTAs that share a window's runs; of 8 (half, head)s
+  int units, turned, lanes;
+};
+
+// A row's values in a lane, in either form: `a` and `b` chunks, or up to 4 single
+// values (head sizes up to 128).
+// (STEPS: how often a warp goes on until it has 16 rows; 0: a row at a time, any form.)
+template <typename T, bool IL, int STEPS>
+struct RowOf {
+  static constexpr int kSteps = STEPS;
+  Lane<IL> lane;
+  int lanes, group, rows;
+  bool active;
+  struct Raw {
+    Chunk8 a, b;
+  };
+  __device__ __forceinline__ RowOf(const Dims& d, int rot)
+      : lane((threadIdx.x & (d.lanes - 1)) < d.units ? threadIdx.x & (d.lanes - 1) : 0, d.turned,
+             rot),
+        lanes(d.lanes),
+        group((threadIdx.x & 31) / d.lanes),
+        rows(32 / d.lanes),
+        active((int)(threadIdx.x & (d.lanes - 1)) < d.units) {}
+  __device__ __forceinline__ int steps() const { return (kRun + rows - 1) / rows; }
+  __device__ __forceinline__ void load(const uint16_t* row, bool on, Raw& raw) const {
+    raw.a.v = raw.b.v = make_uint4(0, 0, 0, 0);
+    if (on && active) {
+      raw.a.v = *reinterpret_cast<const uint4*>(row + lane.at);
+      if (lane.two) raw.b.v = *reinterpret_cast<const uint4*>(row + lane.at + lane.gap);
+    }
+  }
+  struct Weights {
+    float a[8], b[8];
+  };
+  __device__ __forceinline__ void weights(const Norm& n, int h, Weights& w) const {
+    lane.template weights<T>(n.k_weight, h * n.k_head, n.wide, n.offset, w.a, w.b);
+  }
+  __device__ __forceinline__ float squares(const Raw& raw) const {
+    float fa[8], fb[8], s = 0.0f;
+    unpack8<T>(raw.a, fa);
+    unpack8<T>(raw.b, fb);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = fmaf(fa[k], fa[k], fmaf(fb[k], fb[k], s));
+    return s;
+  }
+  // f: the norm's factor; weights null: neither norm nor weight
+  template <bool KEY>
+  __device__ __forceinline__ void values(const Raw& raw, float f, const Weights* w,
+                                         const float* cosines, const float* sines, float* fa,
+                                         float* fb) const {
+    unpack8<T>(raw.a, fa);
+    unpack8<T>(raw.b, fb);
+    if (!KEY) return;
+    if (w) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        fa[k] = fa[k] * f * w->a[k];
+        if (lane.two) fb[k] = fb[k] * f * w->b[k];
+      }
+    }
+    if (lane.turns) lane.turn(fa, fb, cosines, sines);
+  }
+  template <bool KEY>
+  __device__ __forceinline__ float top(const Raw& raw, float f, const Weights* w,
+                                       const float* cosines, const float* sines) const {
+    float fa[8], fb[8], m = 0.0f;
+    values<KEY>(raw, f, w, cosines, sines, fa, fb);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, size_of(fa[k]));
+    if (lane.two) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = fmaxf(m, size_of(fb[k]));
+    }
+    return active ? m : 0.0f;
+  }
+  static __device__ __forceinline__ uint2 codes(const float* f, const Divide& by) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w[i] = to_codes(by(f[4 * i]), by(f[4 * i + 1])) |
+             (uint32_t)to_codes(by(f[4 * i + 2]), by(f[4 * i + 3])) << 16;
+    return make_uint2(w[0], w[1]);
+  }
+  template <bool KEY>
+  __device__ __forceinline__ void store(const Raw& raw, float f, const Weights* w,
+                                        const float* cosines, const float* sines, const Divide& by,
+                                        uint8_t* row) const {
+    float fa[8], fb[8];
+    values<KEY>(raw, f, w, cosines, sines, fa, fb);
+    if (!active) return;
+    *reinterpret_cast<uint2*>(row + lane.at) = codes(fa, by);
+    if (lane.two) *reinterpret_cast<uint2*>(row + lane.at + lane.gap) = codes(fb, by);
+  }
+};
+
+template <typename T>
+struct RowOf<T, false, 0> {
+  static constexpr int kSteps = kRun, kLane = 4;
+  const Append8Params& g;
+  float* row_smem;
+  int lanes = 32, group = 0, rows = 1;
+  bool active = true;
+  int dim;
+  struct Raw {
+    uint16_t x[kLane];
+  };
+  struct Weights {
+    float w[kLane];
+  };
+  __device__ __forceinline__ RowOf(const Append8Params& p, float* smem)
+      : g(p), row_smem(smem + (threadIdx.x >> 5) * 128), dim(p.p.r.head_dim) {}
+  __device__ __forceinline__ int steps() const { return kRun; }
+  __device__ __forceinline__ void load(const uint16_t* row, bool on, Raw& raw) const {
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+      const int i = (threadIdx.x & 31) + 32 * k;
+      raw.x[k] = on && i < dim ? row[i] : (uint16_t)0;
+    }
+  }
+  __device__ __forceinline__ void weights(const Norm& n, int h, Weights& w) const {
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+      const int i = (threadIdx.x & 31) + 32 * k;
+      w.w[k] = i < dim ? weight_any<T>(n.k_weight, h * n.k_head + i, n.wide, n.offset) : 0.0f;
+    }
+  }
+  __device__ __forceinline__ float squares(const Raw& raw) const {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) s = fmaf(T::to_f32(raw.x[k]), T::to_f32(raw.x[k]), s);
+    return s;
+  }
+  template <bool KEY>
+  __device__ __forceinline__ void values(const Raw& raw, float f, const Weights* w, int position,
+                                         float* v) const {
+    if (KEY) __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+      const int i = (threadIdx.x & 31) + 32 * k;
+      v[k] = T::to_f32(raw.x[k]);
+      if (KEY && w) v[k] = v[k] * f * w->w[k];
+      if (KEY) row_smem[i] = v[k];
+    }
+    if (!KEY) return;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+      const int i = (threadIdx.x & 31) + 32 * k;
+      v[k] = i < dim ? turned_any(g.p.r.r, position, row_smem, i) : 0.0f;
+    }
+  }
+  template <bool KEY>
+  __device__ __forceinline__ float top(const Raw& raw, float f, const Weights* w,
+                                       int position) const {
+    float v[kLane], m = 0.0f;
+    values<KEY>(raw, f, w, position, v);
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) m = fmaxf(m, size_of(v[k]));
+    return m;
+  }
+  template <bool KEY>
+  __device__ __forceinline__ void store(const Raw& raw, float f, const Weights* w, int position,
+                                        const Divide& by, uint8_t* row) const {
+    float v[kLane];
+    values<KEY>(raw, f, w, position, v);
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+      const int i = (threadIdx.x & 31) + 32 * k;
+      if (i < dim) row[i] = (uint8_t)to_codes(by(v[k]), 0.0f);
+    }
+  }
+};
+
+// Codes of a block's rows that are not in `written` (a bit a row), by a new scale.
+__device__ __forceinline__ void reexpress(uint8_t* block, long long token, int dim,
+                                          unsigned written, float ratio) {
+  const int lane = threadIdx.x & 31, chunks = dim >> 4;
+  for (int i = lane; i < kScaleBlock * chunks; i += 32) {
+    const int r = i / chunks, c = i - r * chunks;
+    if (written >> r & 1) continue;
+    uint4* at = reinterpret_cast<uint4*>(block + r * token + c * 16);
+    uint4 w = *at;
+    uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 lo = codes_to_f32((uint16_t)x[k]), hi = codes_to_f32((uint16_t)(x[k] >> 16));
+      x[k] = to_codes(lo.x * ratio, lo.y * ratio) |
+             (uint32_t)to_codes(hi.x * ratio, hi.y * ratio) << 16;
+    }
+    *at = w;
+  }
+}
+
+// One warp: the run [t0, t0 + n) into its block, of K (KEY) or V, kv head h.
+template <typename T, bool IL, int STEPS, bool KEY>
+__device__ __forceinline__ void append_run(const Append8Params& g, const RowOf<T, IL, STEPS>& of,
+                                           int t0, int n, int h, const float* cosines,
+                                           const float* sines) {
+  typedef RowOf<T, IL, STEPS> R;
+  const RopeParams& r = g.p.r;
+  const Rows& in = KEY ? r.k : r.v;
+  const long long slot = r.slots[t0], page = slot >> r.page_shift;
+  const int in_page = (int)(slot - (page << r.page_shift));
+  const int first = in_page & (kScaleBlock - 1), block = in_page / kScaleBlock;
+  uint8_t* codes = (KEY ? g.c.k : g.c.v) + page * g.c.page + (long long)h * g.c.head +
+                   (long long)(in_page - first) * g.c.token;
+  float* scale_at = (KEY ? g.c.k_scales : g.c.v_scales) + page * g.c.scale_page +
+                    h * g.c.scale_head + block * g.c.scale_block;
+  const float before = first ? *scale_at : 0.0f;
+  typename R::Raw raw[R::kSteps];
+  const int steps = min(of.steps(), (n + of.rows - 1) / of.rows);
+#pragma unroll
+  for (int i = 0; i < R::kSteps; ++i)
+    if (i < steps) {
+      const int k = i * of.rows + of.group;
+      of.load(in.p + (long long)(t0 + min(k, n - 1)) * in.token + (long long)h * in.head, k < n,
+              raw[i]);
+    }
+  typename R::Weights w;
+  const typename R::Weights* wp = nullptr;
+  float f[R::kSteps], top = 0.0f;
+  if (KEY && g.p.n.on) {
+    of.weights(g.p.n, h, w);
+    wp = &w;
+  }
+  const int pairs = r.r.rot >> 1;
+#pragma unroll
+  for (int i = 0; i < R::kSteps; ++i)
+    if (i < steps) {
+      const int k = min(i * of.rows + of.group, n - 1);
+      f[i] = 1.0f;
+      if (wp)
+        f[i] = rsqrtf(fmaf(group_sum(of.squares(raw[i]), of.lanes), 1.0f / (float)r.head_dim,
+                           g.p.n.eps));
+      float m;
+      if constexpr (STEPS > 0)
+        m = of.template top<KEY>(raw[i], f[i], wp, cosines + k * pairs, sines + k * pairs);
+      else
+        m = of.template top<KEY>(raw[i], f[i], wp, KEY ? r.positions[t0 + k] : 0);
+      top = fmaxf(top, m);
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float scale = scale_for(top);
+  unsigned written = 0;  // rows of the block that the run has
+  for (int k = 0; k < n; ++k) written |= 1u << ((int)(r.slots[t0 + k] - slot) + first);
+  if (first && before > 0.0f && before < INFINITY) {
+    if (before >= scale)
+      scale = before;
+    else
+      reexpress(codes, g.c.token, r.head_dim, written, before / scale);
+  }
+  if ((threadIdx.x & 31) == 0) *scale_at = scale;
+  const Divide by(scale);
+#pragma unroll
+  for (int i = 0; i < R::kSteps; ++i)
+    if (i < steps) {
+      const int k = i * of.rows + of.group, kk = min(k, n - 1);
+      uint8_t* row = codes + (first + (r.slots[t0 + kk] - slot)) * g.c.token;
+      if constexpr (STEPS > 0) {
+        if (k < n)
+          of.template store<KEY>(raw[i], f[i], wp, cosines + kk * pairs, sines + kk * pairs, by,
+                                 row);
+      } else {
+        of.template store<KEY>(raw[i], f[i], wp, KEY ? r.positions[t0 + kk] : 0, by, row);
+      }
+    }
+}
+
+// Queries: norm and rotation, a lane group a head, as in norm_rope.cu.
+template <typename T, bool IL>
+__device__ __forceinline__ void queries(const Append8Params& g, const Dims& d, float* table) {
+  const RopeParams& r = g.p.r;
+  const int pairs = r.r.rot >> 1;
+  const int tg = blockIdx.x % d.token_groups, hg = blockIdx.x / d.token_groups;
+  const int u = threadIdx.x & (d.lanes - 1), y = threadIdx.x / d.lanes;
+  const int z = y / d.q_heads, hd = hg * d.q_heads + (y - z * d.q_heads);
+  const int per_cta = d.q_tokens * d.q_z, cta0 = tg * per_cta;
+  const int cta_tokens = min(per_cta, r.tokens - cta0);
+  const int first = z * d.q_tokens;
+  const bool active = z < d.q_z && hd < r.hq && u < d.units;
+  const Lane<IL> lane(u < d.units ? u : 0, d.turned, r.r.rot);
+  float* cosines = table;
+  float* sines = table + per_cta * pairs;
+  constexpr int kTokens = IL ? 4 : 2;
+  Chunk8 a[kTokens], b[kTokens];
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t) {
+    a[t].v = b[t].v = make_uint4(0, 0, 0, 0);
+    if (active && t < d.q_tokens && first + t < cta_tokens) {
+      const uint16_t* src = r.q.p + (long long)(cta0 + first + t) * r.q.token +
+                            (long long)hd * r.q.head + lane.at;
+      a[t].v = *reinterpret_cast<const uint4*>(src);
+      if (lane.two) b[t].v = *reinterpret_cast<const uint4*>(src + lane.gap);
+    }
+  }
+  float wa[8], wb[8];
+  if (active && g.p.n.on)
+    lane.template weights<T>(g.p.n.q_weight, hd * g.p.n.q_head, g.p.n.wide, g.p.n.offset, wa, wb);
+  fill_table(r.r, r.positions + cta0, cta_tokens, cosines, sines, threadIdx.x, kThreads);
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t) {
+    float fa[8], fb[8], sum = 0.0f;
+    unpack8<T>(a[t], fa);
+    unpack8<T>(b[t], fb);
+    if (g.p.n.on) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum = fmaf(fa[k], fa[k], fmaf(fb[k], fb[k], sum));
+      sum = group_sum(sum, d.lanes);
+    }
+    if (!active || t >= d.q_tokens || first + t >= cta_tokens) continue;
+    if (g.p.n.on) {
+      const float f = rsqrtf(fmaf(sum, 1.0f / (float)r.head_dim, g.p.n.eps));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        fa[k] = fa[k] * f * wa[k];
+        if (lane.two) fb[k] = fb[k] * f * wb[k];
+      }
+    }
+    if (lane.turns)
+      lane.turn(fa, fb, cosines + (first + t) * pairs, sines + (first + t) * pairs);
+    uint16_t* dst = r.q_out.p + (long long)(cta0 + first + t) * r.q_out.token +
+                    (long long)hd * r.q_out.head + lane.at;
+    *reinterpret_cast<uint4*>(dst) = pack8<T>(fa);
+    if (lane.two) *reinterpret_cast<uint4*>(dst + lane.gap) = pack8<T>(fb);
+  }
+}
+
+// Queries in the form for any rows: a warp a head.
+template <typename T>
+__device__ __forceinline__ void queries_any(const Append8Params& g, const Dims& d, float* smem) {
+  const RopeParams& r = g.p.r;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x % d.token_groups;
+  const int hd = blockIdx.x / d.token_groups * kWarps + warp;
+  if (hd >= r.hq) return;
+  float* row = smem + warp * 128;
+  const uint16_t* src = r.q.p + (long long)t * r.q.token + (long long)hd * r.q.head;
+  float v[4], sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = lane + 32 * k;
+    v[k] = i < r.head_dim ? T::to_f32(src[i]) : 0.0f;
+    sum = fmaf(v[k], v[k], sum);
+  }
+  if (g.p.n.on) {
+    const float f = rsqrtf(fmaf(group_sum(sum, 32), 1.0f / (float)r.head_dim, g.p.n.eps));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = lane + 32 * k;
+      if (i < r.head_dim)
+        v[k] *= f * weight_any<T>(g.p.n.q_weight, hd * g.p.n.q_head + i, g.p.n.wide,
+                                  g.p.n.offset);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) row[lane + 32 * k] = v[k];
+  __syncwarp();
+  uint16_t* dst = r.q_out.p + (long long)t * r.q_out.token + (long long)hd * r.q_out.head;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = lane + 32 * k;
+    if (i < r.head_dim) dst[i] = T::from_f32(turned_any(r.r, r.positions[t], row, i));
+  }
+}
+
+template <typename T, bool IL, int STEPS>
+__global__ void __launch_bounds__(kThreads, 2)
+    append8_kernel(const __grid_constant__ Append8Params g, const Dims d) {
+  extern __shared__ float4 smem4[];
+  float* smem = reinterpret_cast<float*>(smem4);
+  const RopeParams& r = g.p.r;
+  wait_prior_launch();
+  let_next_launch();
+  if ((int)blockIdx.x < d.q_ctas) {
+    if constexpr (STEPS > 0)
+      queries<T, IL>(g, d, smem);
+    else
+      queries_any<T>(g, d, smem);
+    return;
+  }
+  int cta = blockIdx.x - d.q_ctas;
+  const int combo = cta % d.combos * kWarps + (threadIdx.x >> 5);  // K heads, then V heads
+  cta /= d.combos;
+  const int part = cta % d.split, w0 = cta / d.split * kRun;
+  // lane l has token w0 - 1 + l: the one before the window, the window, and what runs
+  // that begin there may go on with
+  const int lane = threadIdx.x & 31, t = w0 - 1 + lane;
+  long long slot = -1;
+  if (t >= 0 && t < r.tokens) {
+    slot = r.slots[t];
+    if (slot >= r.num_slots) {
+      if (lane > 0 && lane <= kRun) atomicOr(r.err, kErrRange);
+      slot = -1;
+    }
+  }
+  const long long prev = __shfl_up_sync(0xffffffffu, slot, 1);
+  const bool follows = lane > 0 && slot >= 0 && prev >= 0 && prev < slot &&
+                       prev / kScaleBlock == slot / kScaleBlock;
+  const unsigned go_on = __ballot_sync(0xffffffffu, follows);
+  unsigned begin = __ballot_sync(0xffffffffu, slot >= 0 && !follows && lane > 0 && lane <= kRun);
+  const bool key = combo < r.hk, on = combo < 2 * r.hk;
+  const bool any_keys = combo - (int)(threadIdx.x >> 5) < r.hk;  // in the CTA
+  const int h = key ? combo : combo - r.hk;
+  const int pairs = r.r.rot >> 1;
+  float *cosines = smem, *sines = smem + kRun * pairs;
+  for (int i = 0; begin; ++i) {
+    const int at = __ffs(begin) - 1;
+    begin &= begin - 1;
+    if (i % d.split != part) continue;
+    // the run goes on while the bits behind its first token are set
+    const int n = at == 31 ? 1 : __ffs(~(go_on >> (at + 1)));
+    const int t0 = w0 - 1 + at;
+    if constexpr (STEPS > 0) {
+      const RowOf<T, IL, STEPS> of(d, r.r.rot);
+      if (any_keys) {
+        __syncthreads();
+        fill_table(r.r, r.positions + t0, n, cosines, sines, threadIdx.x, kThreads);
+        __syncthreads();
+      }
+      if (!on) continue;
+      if (key)
+        append_run<T, IL, STEPS, true>(g, of, t0, n, h, cosines, sines);
+      else
+        append_run<T, IL, STEPS, false>(g, of, t0, n, h, cosines, sines);
+    } else {
+      const RowOf<T, false, 0> of(g, smem);
+      if (!on) continue;
+      if (key)
+        append_run<T, false, 0, true>(g, of, t0, n, h, nullptr, nullptr);
+      else
+        append_run<T, false, 0, false>(g, of, t0, n, h, nullptr, nullptr);
+    }
+  }
+}
+
+template <typename T, bool IL, int STEPS>
+cudaError_t launch_append(const Append8Params& g, cudaStream_t s) {
+  const RopeParams& r = g.p.r;
+  Dims d{};
+  int smem;
+  if (STEPS > 0) {
+    const Units u = units_of_head<IL>(r.head_dim, r.r.rot);
+    d.units = u.count;
+    d.turned = u.turned;
+    d.lanes = u.lanes;
+    const int most = kThreads / u.lanes;
+    d.q_rows = (r.hq + most - 1) / most;
+    d.q_heads = d.q_rows ? (r.hq + d.q_rows - 1) / d.q_rows : 1;
+    d.q_z = most / d.q_heads;
+    const long long all = (long long)r.tokens * d.q_rows;
+    while (d.q_z > 1 && (all < 4LL * kSms * d.q_z || d.q_z * r.r.rot > 4096)) d.q_z /= 2;
+    d.q_tokens = 1;
+    while (d.q_tokens < (IL ? 4 : 2) && all >= 8LL * kSms * d.q_z * d.q_tokens &&
+           2 * d.q_tokens * d.q_z * r.r.rot <= 4096)
+      d.q_tokens *= 2;
+    const int table = d.q_tokens * d.q_z > kRun ? d.q_tokens * d.q_z : kRun;
+    smem = table * r.r.rot * (int)sizeof(float);
+    d.token_groups = (r.tokens + d.q_tokens * d.q_z - 1) / (d.q_tokens * d.q_z);
+  } else {
+    d.q_rows = (r.hq + kWarps - 1) / kWarps;
+    d.token_groups = r.tokens;
+    smem = kWarps * 128 * (int)sizeof(float);
+  }
+  d.q_ctas = d.token_groups * d.q_rows;
+  d.combos = (2 * r.hk + kWarps - 1) / kWarps;
+  const int windows = (r.tokens + kRun - 1) / kRun;
+  // a window's runs to as many CTAs as the GPU takes at once: decode steps have a run
+  // for each token, prompts one for each window
+  d.split = kRun;
+  while (d.split > 1 && (long long)windows * d.combos * d.split > 4 * kSms) d.split /= 2;
+  const long long ctas = d.q_ctas + (long long)windows * d.combos * d.split;
+  return launch_after(append8_kernel<T, IL, STEPS>, dim3((unsigned)ctas), dim3(kThreads), smem, s, g,
+                      d);
+}
+
+// four rows at a time, or two
+template <typename T>
+cudaError_t launch_units(const Append8Params& g, cudaStream_t s) {
+  const RopeParams& r = g.p.r;
+  if (r.r.interleaved)
+    return units_of_head<true>(r.head_dim, r.r.rot).lanes <= 8 ? launch_append<T, true, 4>(g, s)
+                                                               : launch_append<T, true, 8>(g, s);
+  return units_of_head<false>(r.head_dim, r.r.rot).lanes <= 8 ? launch_append<T, false, 4>(g, s)
+                                                              : launch_append<T, false, 8>(g, s);
+}
+
+// ------------------------------------------------------------------ read back
+// A CTA has 32 rows of the outputs, all heads: it finds their sequence (every thread
+// counts some of the sequences that begin at or before its first row), 32 lanes look
+// up their pages, then all threads bring 16 codes at a time to 32 bytes of the
+// outputs. Bound by memory.
+constexpr int kReadRows = 32;
+
+template <typename T>
+__device__ __forceinline__ void read16(const uint8_t* codes, float scale, uint16_t* to, bool wide) {
+  const uint4 w = __ldg(reinterpret_cast<const uint4*>(codes));
+  const uint32_t* x = reinterpret_cast<const uint32_t*>(&w);
+  uint32_t y[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 lo = codes_to_f32((uint16_t)x[k]), hi = codes_to_f32((uint16_t)(x[k] >> 16));
+    y[2 * k] = T::pack(lo.x * scale, lo.y * scale);
+    y[2 * k + 1] = T::pack(hi.x * scale, hi.y * scale);
+  }
+  if (wide) {
+    reinterpret_cast<uint4*>(to)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+    reinterpret_cast<uint4*>(to)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) to[k] = (uint16_t)(y[k >> 1] >> (16 * (k & 1)));
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) read8_kernel(const Read8Params p, int wide) {
+  __shared__ long long code_at[kReadRows], scale_at[kReadRows];
+  __shared__ int counts[kWarps];
+  const int row0 = blockIdx.x * kReadRows;
+  wait_prior_launch();
+  let_next_launch();
+  int mine = 0;
+  for (int s = 1 + threadIdx.x; s <= p.num_seqs; s += kThreads) mine += p.cu[s] <= row0;
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = mine;
+  __syncthreads();
+  if (threadIdx.x < kReadRows) {
+    int s = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) s += counts[i];
+    const int row = row0 + threadIdx.x;
+    while (s < p.num_seqs && p.cu[s + 1] <= row) ++s;
+    long long at = -1, sc = 0;
+    if (row < p.rows && s < p.num_seqs && p.cu[s] >= 0 && row >= p.cu[s]) {
+      const long long pos = (long long)p.first[s] + (row - p.cu[s]);
+      const long long limit = (long long)p.columns << p.page_shift;
+      int page = -1;
+      if (p.first[s] >= 0 && pos < limit)
+        page = p.page_table[s * p.table_stride + (pos >> p.page_shift)];
+      if (page < 0 || page >= p.c.num_pages) {
+        atomicOr(p.err, kErrRange);
+      } else {
+        const int in_page = (int)(pos & ((1 << p.page_shift) - 1));
+        at = page * p.c.page + in_page * p.c.token;
+        sc = page * p.c.scale_page + in_page / kScaleBlock * p.c.scale_block;
+      }
+    }
+    code_at[threadIdx.x] = at;
+    scale_at[threadIdx.x] = sc;
+  }
+  __syncthreads();
+  const int chunks = p.head_dim >> 4, heads = p.hk, items = kReadRows * heads * chunks;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < items; i += kThreads) {
+    const int rest = i / chunks, c = i - rest * chunks;
+    const int r = rest & (kReadRows - 1), h = rest / kReadRows;
+    if (code_at[r] < 0) continue;
+    const long long at = code_at[r] + h * p.c.head + c * 16, sc = scale_at[r] + h * p.c.scale_head;
+    const float ks = __ldg(p.c.k_scales + sc), vs = __ldg(p.c.v_scales + sc);
+    read16<T>(p.c.k + at, ks,
+              p.k_out.p + (long long)(row0 + r) * p.k_out.token + h * p.k_out.head + c * 16, wide);
+    read16<T>(p.c.v + at, vs,
+              p.v_out.p + (long long)(row0 + r) * p.v_out.token + h * p.v_out.head + c * 16, wide);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append8(const Append8Params& g, int dtype, cudaStream_t s) {
+  const RopeParams& r = g.p.r;
+  const bool fast = units_fit(r.r, r.head_dim) && weights_aligned(g.p.n) && rows_aligned(r.q) &&
+                    rows_aligned(r.q_out) && rows_aligned(r.k) && rows_aligned(r.v);
+  if (!fast)
+    return dtype == MOE_ATTN_BF16 ? launch_append<Bf16, false, 0>(g, s)
+                                  : launch_append<Fp16, false, 0>(g, s);
+  return dtype == MOE_ATTN_BF16 ? launch_units<Bf16>(g, s) : launch_units<Fp16>(g, s);
+}
+
+cudaError_t launch_read8(const Read8Params& p, int dtype, cudaStream_t s) {
+  const dim3 grid((p.rows + kReadRows - 1) / kReadRows), block(kThreads);
+  const int wide = rows_aligned(p.k_out) && rows_aligned(p.v_out);
+  return dtype == MOE_ATTN_BF16 ? launch_after(read8_kernel<Bf16>, grid, block, 0, s, p, wide)
+                                : launch_after(read8_kernel<Fp16>, grid, block, 0, s, p, wide);
+}
+
+}  // namespace attn
+}  // namespace moe

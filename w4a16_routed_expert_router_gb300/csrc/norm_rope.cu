@@ -1,0 +1,534 @@
+// Norms of queries and keys for each head with the rotary positions in the same
+// pass, and their gradient.
+//
+// Forward: y = R_p(x rsqrt(mean x^2 + eps) (w + offset)), read once, written once. A
+// group of lanes has a head (norm_parts.cuh) for a few tokens; all its loads are
+// under way while the CTA makes the table of cosines and sines of its tokens, one
+// evaluation for all heads. Bound by memory.
+//
+// Gradient: with u = R_p^T dy, n = x r and h = u (w + offset),
+//   dx = r (h - n mean(h n)),  dw = sum u n.
+// mean(h n) = r mean(h x), so both sums over a head, of x^2 and of h x, are taken
+// together. Each thread keeps one unit of one head for many tokens and adds up that
+// unit's dw; a CTA adds its rows in order, and a second launch the CTAs.
+#include "norm_parts.cuh"
+
+namespace moe {
+namespace attn {
+namespace {
+
+constexpr int kMaxThreads = 512;
+constexpr int kSms = 152;
+constexpr int tokens_of(bool two_chunks) { return two_chunks ? 2 : 4; }
+
+// where a key or value of token t goes in the pages, or null
+__device__ __forceinline__ uint16_t* page_row(const RopeParams& r, bool key, int t, int h) {
+  const long long slot = r.slots[t];
+  if (slot < 0) return nullptr;
+  if (slot >= r.num_slots) {
+    atomicOr(r.err, kErrRange);
+    return nullptr;
+  }
+  const long long page = slot >> r.page_shift;
+  return (key ? r.k_pages : r.v_pages) + page * r.page_stride +
+         (slot - (page << r.page_shift)) * r.token_stride + (long long)h * r.head_stride;
+}
+
+// What row (token, head) is: queries, then keys, then values.
+struct Head {
+  int h;
+  bool key, value;
+  __device__ __forceinline__ Head(const RopeParams& r, int hd) {
+    key = hd >= r.hq && hd < r.hq + r.hk;
+    value = hd >= r.hq + r.hk;
+    h = hd - (value ? r.hq + r.hk : key ? r.hq : 0);
+  }
+  __device__ __forceinline__ const Rows& in(const RopeParams& r) const {
+    return value ? r.v : key ? r.k : r.q;
+  }
+  __device__ __forceinline__ uint16_t* out(const NormParams& p, int t) const {
+    if ((key || value) && p.r.slots) return page_row(p.r, key, t, h);
+    const Rows& o = key ? p.k_out : p.r.q_out;
+    return o.p + (long long)t * o.token + (long long)h * o.head;
+  }
+};
+
+template <typename T, bool IL>
+__global__ void __launch_bounds__(kMaxThreads, 2)
+    norm_rope_kernel(const NormParams p, int tokens_per_thread, int units, int turned) {
+  extern __shared__ float4 table4[];  // cosines, then sines: [tokens of the CTA][rot / 2]
+  float* cosines = reinterpret_cast<float*>(table4);
+  constexpr int kTokens = tokens_of(!IL);
+  const RopeParams& r = p.r;
+  const int pairs = r.r.rot >> 1;
+  const int tokens_per_cta = tokens_per_thread * blockDim.z;
+  const int cta0 = blockIdx.x * tokens_per_cta;
+  const int cta_tokens = min(tokens_per_cta, r.tokens - cta0);
+  const int first = threadIdx.z * tokens_per_thread, t0 = cta0 + first;
+  const int nt = min(tokens_per_thread, cta_tokens - first);
+  float* sines = cosines + tokens_per_cta * pairs;
+
+  wait_prior_launch();
+  let_next_launch();
+  const int u = threadIdx.x, hd = blockIdx.y * blockDim.y + threadIdx.y;
+  const bool active = hd < r.hq + r.hk + r.hv && u < units;
+  const Head hh(r, active ? hd : 0);
+  const Lane<IL> lane(active ? u : 0, turned, r.r.rot);
+  const Rows& in = hh.in(r);
+  const uint16_t* src = in.p + (long long)t0 * in.token + (long long)hh.h * in.head + lane.at;
+  Chunk8 a[kTokens], b[kTokens];
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t) {
+    a[t].v = b[t].v = make_uint4(0, 0, 0, 0);
+    if (active && t < nt) {
+      a[t].v = *reinterpret_cast<const uint4*>(src + t * in.token);
+      if (lane.two) b[t].v = *reinterpret_cast<const uint4*>(src + t * in.token + lane.gap);
+    }
+  }
+  float wa[8], wb[8];
+  if (active && !hh.value)
+    lane.template weights<T>(hh.key ? p.n.k_weight : p.n.q_weight,
+                             hh.h * (hh.key ? p.n.k_head : p.n.q_head), p.n.wide, p.n.offset, wa,
+                             wb);
+  const int tid = (threadIdx.z * blockDim.y + threadIdx.y) * blockDim.x + threadIdx.x;
+  fill_table(r.r, r.positions + cta0, cta_tokens, cosines, sines, tid,
+             blockDim.x * blockDim.y * blockDim.z);
+  __syncthreads();
+  const float mean = 1.0f / (float)r.head_dim;
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t) {
+    float fa[8], fb[8], sum = 0.0f;
+    unpack8<T>(a[t], fa);
+    unpack8<T>(b[t], fb);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      sum = fmaf(fa[k], fa[k], sum);
+      sum = fmaf(fb[k], fb[k], sum);
+    }
+    sum = group_sum(sum, blockDim.x);
+    if (!active || t >= nt) continue;
+    uint16_t* dst = hh.out(p, t0 + t);
+    if (!dst) continue;
+    dst += lane.at;
+    if (!hh.value) {
+      const float f = rsqrtf(fmaf(sum, mean, p.n.eps));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        fa[k] = fa[k] * f * wa[k];
+        if (lane.two) fb[k] = fb[k] * f * wb[k];
+      }
+      if (lane.turns)
+        lane.turn(fa, fb, cosines + (first + t) * pairs, sines + (first + t) * pairs);
+      a[t].v = pack8<T>(fa);
+      b[t].v = pack8<T>(fb);
+    }
+    *reinterpret_cast<uint4*>(dst) = a[t].v;
+    if (lane.two) *reinterpret_cast<uint4*>(dst + lane.gap) = b[t].v;
+  }
+}
+
+constexpr int kAnyWarps = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(kAnyWarps * 32)
+    norm_rope_any_kernel(const NormParams p, int tokens_per_warp) {
+  __shared__ float row[kAnyWarps][32 * kAnyValues];
+  const RopeParams& r = p.r;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hd = blockIdx.y * kAnyWarps + warp;
+  wait_prior_launch();
+  let_next_launch();
+  if (hd >= r.hq + r.hk + r.hv) return;
+  const Head hh(r, hd);
+  const Rows& in = hh.in(r);
+  const void* w = hh.key ? p.n.k_weight : p.n.q_weight;
+  const long long wh = hh.h * (hh.key ? p.n.k_head : p.n.q_head);
+  const int t1 = min(r.tokens, (int)(blockIdx.x + 1) * tokens_per_warp);
+  for (int t = blockIdx.x * tokens_per_warp; t < t1; ++t) {
+    const uint16_t* src = in.p + (long long)t * in.token + (long long)hh.h * in.head;
+    uint16_t x[kAnyValues];
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kAnyValues; ++k) {
+      const int i = lane + 32 * k;
+      x[k] = i < r.head_dim ? src[i] : (uint16_t)0;
+      sum = fmaf(T::to_f32(x[k]), T::to_f32(x[k]), sum);
+    }
+    sum = group_sum(sum, 32);
+    const float f = rsqrtf(fmaf(sum, 1.0f / (float)r.head_dim, p.n.eps));
+    uint16_t* dst = hh.out(p, t);
+    if (!hh.value) {
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kAnyValues; ++k) {
+        const int i = lane + 32 * k;
+        if (i < r.head_dim)
+          row[warp][i] = T::to_f32(x[k]) * f * weight_any<T>(w, wh + i, p.n.wide, p.n.offset);
+      }
+      __syncwarp();
+    }
+    if (!dst) continue;
+#pragma unroll
+    for (int k = 0; k < kAnyValues; ++k) {
+      const int i = lane + 32 * k;
+      if (i < r.head_dim)
+        dst[i] = hh.value ? x[k] : T::from_f32(turned_any(r.r, r.positions[t], row[warp], i));
+    }
+  }
+}
+
+template <typename T, bool IL>
+cudaError_t launch_fast(const NormParams& p, cudaStream_t s) {
+  const RopeParams& r = p.r;
+  const Units u = units_of_head<IL>(r.head_dim, r.r.rot);
+  const int heads = r.hq + r.hk + r.hv;
+  // as in launch_il of the rotation alone: groups of heads of at most kMaxThreads
+  // threads, tokens side by side where heads are few, several tokens to a thread
+  // where every SM has enough
+  const int most = kMaxThreads / u.lanes;
+  const int groups = (heads + most - 1) / most;
+  dim3 block(u.lanes, (heads + groups - 1) / groups, 1);
+  const long long all = (long long)r.tokens * groups;
+  while (block.x * block.y * block.z <= 128 && block.z < 64 && all >= 4LL * kSms * block.z &&
+         2 * block.z * r.r.rot <= 4096)
+    block.z *= 2;
+  int tokens = 1;
+  while (tokens < tokens_of(!IL) && all >= 8LL * kSms * block.z * tokens &&
+         2 * tokens * block.z * r.r.rot <= 4096)
+    tokens *= 2;
+  const int cta = tokens * block.z;
+  return launch_after(norm_rope_kernel<T, IL>, dim3((r.tokens + cta - 1) / cta, groups), block,
+                      cta * r.r.rot * (int)sizeof(float), s, p, tokens, u.count, u.turned);
+}
+
+bool fits(const NormParams& p) {
+  const RopeParams& r = p.r;
+  if (!units_fit(r.r, r.head_dim) || !weights_aligned(p.n)) return false;
+  if (r.slots && (r.page_stride % 8 || r.token_stride % 8 || r.head_stride % 8)) return false;
+  return rows_aligned(r.q) && rows_aligned(r.q_out) && rows_aligned(r.k) && rows_aligned(p.k_out) &&
+         rows_aligned(r.v);
+}
+
+template <typename T>
+cudaError_t launch_t(const NormParams& p, cudaStream_t s) {
+  if (fits(p)) return p.r.r.interleaved ? launch_fast<T, true>(p, s) : launch_fast<T, false>(p, s);
+  const int heads = p.r.hq + p.r.hk + p.r.hv, groups = (heads + kAnyWarps - 1) / kAnyWarps;
+  const int tokens = p.r.tokens >= 16 * kSms ? 4 : 1;
+  return launch_after(norm_rope_any_kernel<T>, dim3((p.r.tokens + tokens - 1) / tokens, groups),
+                      dim3(kAnyWarps * 32), 0, s, p, tokens);
+}
+
+// ------------------------------------------------------------------ gradient
+
+constexpr int kGradThreads = 256;  // and registers for three CTAs an SM
+
+template <typename T, bool IL>
+__global__ void __launch_bounds__(kGradThreads, 3)
+    norm_grad_kernel(const NormGradParams g, int units, int turned, int shared) {
+  extern __shared__ float4 smem4[];
+  float* smem = reinterpret_cast<float*>(smem4);
+  const NormParams& p = g.p;
+  const RopeParams& r = p.r;
+  const int pairs = r.r.rot >> 1, z = blockDim.z, heads = r.hq + r.hk;
+  // two tables of cosines and sines, [z tokens][pairs] each, in turn
+  wait_prior_launch();
+  let_next_launch();
+  const int u = threadIdx.x, hd = blockIdx.y * blockDim.y + threadIdx.y;
+  const bool active = hd < heads && u < units;
+  const Head hh(r, active ? hd : 0);
+  const Lane<IL> lane(active ? u : 0, turned, r.r.rot);
+  const Rows &in = hh.in(r), &dy = hh.key ? g.dk : g.dq, &dx = hh.key ? p.k_out : r.q_out;
+  const long long hi = hh.h * in.head + lane.at, hy = hh.h * dy.head + lane.at,
+                  ho = hh.h * dx.head + lane.at;
+  float wa[8], wb[8], da[8], db[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) da[k] = db[k] = wa[k] = wb[k] = 0.0f;
+  if (active)
+    lane.template weights<T>(hh.key ? p.n.k_weight : p.n.q_weight,
+                             hh.h * (hh.key ? p.n.k_head : p.n.q_head), p.n.wide, p.n.offset, wa,
+                             wb);
+  const int tid = (threadIdx.z * blockDim.y + threadIdx.y) * blockDim.x + threadIdx.x;
+  const int threads = blockDim.x * blockDim.y * blockDim.z;
+  const float mean = 1.0f / (float)r.head_dim;
+  int turn = 0;
+  for (int c0 = blockIdx.x * z; c0 < r.tokens; c0 += gridDim.x * z, turn ^= 1) {
+    const int t = c0 + threadIdx.z;
+    const bool on = active && t < r.tokens;
+    Chunk8 xa, xb, ya, yb;
+    xa.v = xb.v = ya.v = yb.v = make_uint4(0, 0, 0, 0);
+    if (on) {
+      const uint16_t* x = in.p + (long long)t * in.token + hi;
+      const uint16_t* y = dy.p + (long long)t * dy.token + hy;
+      xa.v = *reinterpret_cast<const uint4*>(x);
+      ya.v = *reinterpret_cast<const uint4*>(y);
+      if (lane.two) {
+        xb.v = *reinterpret_cast<const uint4*>(x + lane.gap);
+        yb.v = *reinterpret_cast<const uint4*>(y + lane.gap);
+      }
+    }
+    float* cosines = smem + turn * 2 * z * pairs;
+    float* sines = cosines + z * pairs;
+    fill_table(r.r, r.positions + c0, min(z, r.tokens - c0), cosines, sines, tid, threads);
+    __syncthreads();
+    float fx[8], gx[8], ua[8], ub[8];
+    unpack8<T>(xa, fx);
+    unpack8<T>(xb, gx);
+    unpack8<T>(ya, ua);
+    unpack8<T>(yb, ub);
+    if (on && lane.turns)
+      lane.turn(ua, ub, cosines + threadIdx.z * pairs, sines + threadIdx.z * pairs);
+    float sq = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      sq = fmaf(fx[k], fx[k], sq);
+      sq = fmaf(gx[k], gx[k], sq);
+      dot = fmaf(ua[k] * wa[k], fx[k], dot);
+      dot = fmaf(ub[k] * wb[k], gx[k], dot);
+    }
+    sq = group_sum(sq, blockDim.x);
+    dot = group_sum(dot, blockDim.x);
+    if (!on) continue;
+    const float f = rsqrtf(fmaf(sq, mean, p.n.eps));
+    const float c = dot * mean * f * f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      da[k] = fmaf(ua[k], fx[k] * f, da[k]);
+      ua[k] = f * fmaf(-c, fx[k], ua[k] * wa[k]);
+      if (lane.two) {
+        db[k] = fmaf(ub[k], gx[k] * f, db[k]);
+        ub[k] = f * fmaf(-c, gx[k], ub[k] * wb[k]);
+      }
+    }
+    uint16_t* out = dx.p + (long long)t * dx.token + ho;
+    *reinterpret_cast<uint4*>(out) = pack8<T>(ua);
+    if (lane.two) *reinterpret_cast<uint4*>(out + lane.gap) = pack8<T>(ub);
+  }
+  // the CTA's rows in order: tokens side by side, then the heads that share a weight
+  __syncthreads();
+  const int d = r.head_dim, ny = blockDim.y;
+  if (active) {
+    float* to = smem + (threadIdx.z * ny + threadIdx.y) * d + lane.at;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) to[k] = da[k];
+    if (lane.two) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) to[lane.gap + k] = db[k];
+    }
+  }
+  __syncthreads();
+  const int h0 = blockIdx.y * ny, h1 = min(heads, h0 + ny);
+  const long long cta = (long long)blockIdx.x * gridDim.y + blockIdx.y;
+  const int rows = shared ? 2 : ny;
+  for (int i = tid; i < rows * d; i += threads) {
+    const int w = i / d, v = i - w * d;
+    int y0 = w, y1 = w + 1;
+    if (shared) {  // queries, or keys, of this CTA
+      y0 = w == 0 ? 0 : max(0, r.hq - h0);
+      y1 = w == 0 ? min(h1, r.hq) - h0 : h1 - h0;
+    } else if (h0 + w >= h1) {
+      y1 = y0;
+    }
+    float sum = 0.0f;
+    for (int y = y0; y < y1; ++y)
+      for (int k = 0; k < z; ++k) sum += smem[(k * ny + y) * d + v];
+    g.parts[(cta * rows + w) * d + v] = sum;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAnyWarps * 32) norm_grad_any_kernel(const NormGradParams g) {
+  __shared__ float row[kAnyWarps][32 * kAnyValues];
+  const NormParams& p = g.p;
+  const RopeParams& r = p.r;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = r.hq + r.hk;
+  const int hd = blockIdx.y * kAnyWarps + warp;
+  wait_prior_launch();
+  let_next_launch();
+  if (hd >= heads) return;
+  const Head hh(r, hd);
+  const Rows &in = hh.in(r), &dy = hh.key ? g.dk : g.dq, &dx = hh.key ? p.k_out : r.q_out;
+  const void* w = hh.key ? p.n.k_weight : p.n.q_weight;
+  const long long wh = hh.h * (hh.key ? p.n.k_head : p.n.q_head);
+  const float mean = 1.0f / (float)r.head_dim;
+  float dw[kAnyValues] = {};
+  for (int t = blockIdx.x; t < r.tokens; t += gridDim.x) {
+    const uint16_t* x = in.p + (long long)t * in.token + hh.h * in.head;
+    const uint16_t* y = dy.p + (long long)t * dy.token + hh.h * dy.head;
+    float f[kAnyValues], sq = 0.0f, dot = 0.0f;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kAnyValues; ++k) {
+      const int i = lane + 32 * k;
+      f[k] = i < r.head_dim ? T::to_f32(x[i]) : 0.0f;
+      if (i < r.head_dim) row[warp][i] = T::to_f32(y[i]);
+      sq = fmaf(f[k], f[k], sq);
+    }
+    __syncwarp();
+    float u[kAnyValues], h[kAnyValues];
+#pragma unroll
+    for (int k = 0; k < kAnyValues; ++k) {
+      const int i = lane + 32 * k;
+      u[k] = h[k] = 0.0f;
+      if (i < r.head_dim) {
+        u[k] = turned_any(r.r, r.positions[t], row[warp], i);
+        h[k] = u[k] * weight_any<T>(w, wh + i, p.n.wide, p.n.offset);
+      }
+      dot = fmaf(h[k], f[k], dot);
+    }
+    sq = group_sum(sq, 32);
+    dot = group_sum(dot, 32);
+    const float n = rsqrtf(fmaf(sq, mean, p.n.eps)), c = dot * mean * n * n;
+    uint16_t* out = dx.p + (long long)t * dx.token + hh.h * dx.head;
+#pragma unroll
+    for (int k = 0; k < kAnyValues; ++k) {
+      const int i = lane + 32 * k;
+      dw[k] = fmaf(u[k], f[k] * n, dw[k]);
+      if (i < r.head_dim) out[i] = T::from_f32(n * fmaf(-c, f[k], h[k]));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kAnyValues; ++k)
+    if (lane + 32 * k < r.head_dim)
+      g.parts[((long long)blockIdx.x * heads + hd) * r.head_dim + lane + 32 * k] = dw[k];
+}
+
+constexpr int kAddRows = 16;
+
+// dw of the queries' and the keys' weights: outputs [0, n_q) and [n_q, n_q + n_k); the
+// sums of `outer` CTAs, `rows` rows each; a weight's are rows [row0, row0 + inner).
+struct AddParams {
+  const float* parts;
+  float *dw_q, *dw_k;
+  int d, outer, rows;
+  int weights_q, weights_k, inner_q, inner_k;
+  // rows of the CTAs' heads where each has its own: head = group * per + row
+  int per, groups, heads_q;
+};
+__global__ void __launch_bounds__(32 * kAddRows) norm_grad_add_kernel(const AddParams a) {
+  __shared__ float part[kAddRows][32];
+  wait_prior_launch();
+  let_next_launch();
+  const int n_q = a.weights_q * a.d, i = blockIdx.x * 32 + threadIdx.x;
+  const bool on = i < n_q + a.weights_k * a.d, key = i >= n_q;
+  float sum = 0.0f;
+  if (on) {
+    const int j = key ? i - n_q : i, w = j / a.d, v = j - w * a.d;
+    // first of the weight's rows among all rows of one CTA along the tokens
+    const long long row0 = a.per ? (key ? a.heads_q : 0) + w : (key ? 1 : 0);
+    const int inner = key ? a.inner_k : a.inner_q;
+    // (CTA, row) pairs in order, dealt out over threadIdx.y
+    const long long n = (long long)a.outer * inner;
+    for (long long k = threadIdx.y; k < n; k += kAddRows) {
+      const long long o = k / inner, h = row0 + (k - o * inner);
+      const long long at = a.per ? (o * a.groups + h / a.per) * a.rows + h % a.per
+                                 : o * a.rows + h;
+      sum += a.parts[at * a.d + v];
+    }
+  }
+  part[threadIdx.y][threadIdx.x] = sum;
+  __syncthreads();
+  if (threadIdx.y == 0 && on) {
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kAddRows; ++k) sum += part[k][threadIdx.x];
+    (key ? a.dw_k : a.dw_q)[key ? i - n_q : i] = sum;
+  }
+}
+
+template <typename T, bool IL>
+cudaError_t launch_grad_fast(const NormGradParams& g, const NormGradPlan& n, cudaStream_t s) {
+  const RopeParams& r = g.p.r;
+  const Units u = units_of_head<IL>(r.head_dim, r.r.rot);
+  const int shared = (!r.hq || g.p.n.q_head == 0) && (!r.hk || g.p.n.k_head == 0);
+  const int table = 4 * n.z * (r.r.rot / 2), sums = n.rows * n.z * r.head_dim;
+  cudaError_t e = launch_after(norm_grad_kernel<T, IL>, dim3(n.parts, n.groups),
+                               dim3(u.lanes, n.rows, n.z),
+                               (table > sums ? table : sums) * (int)sizeof(float), s, g, u.count,
+                               u.turned, shared);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const NormParams& p, int dtype, cudaStream_t s) {
+  return dtype == MOE_ATTN_BF16 ? launch_t<Bf16>(p, s) : launch_t<Fp16>(p, s);
+}
+
+// Heads of a CTA and tokens side by side, up to kGradThreads; CTAs along the tokens
+// until every SM has three.
+NormGradPlan norm_grad_plan(int tokens, int heads, int lanes) {
+  NormGradPlan n;
+  const int most = kGradThreads / lanes;
+  n.groups = (heads + most - 1) / most;
+  n.rows = (heads + n.groups - 1) / n.groups;
+  n.groups = (heads + n.rows - 1) / n.rows;
+  n.z = 1;
+  while (lanes < 32 * kAnyWarps && 2 * n.z * n.rows * lanes <= kGradThreads && n.z < 8) n.z *= 2;
+  const int want = (3 * kSms + n.groups - 1) / n.groups, all = (tokens + n.z - 1) / n.z;
+  n.parts = want < all ? want : all;
+  return n;
+}
+
+size_t norm_grad_bytes(int tokens, int heads, int head_dim) {
+  size_t most = 0;
+  for (int lanes = 1; lanes <= 32; lanes *= 2) {
+    const NormGradPlan n = norm_grad_plan(tokens, heads, lanes);
+    const size_t rows = (size_t)n.parts * n.groups * (n.rows > 2 ? n.rows : 2);
+    most = rows > most ? rows : most;
+  }
+  return most * head_dim * sizeof(float);
+}
+
+cudaError_t launch_norm_rope_grad(const NormGradParams& g, int dtype, cudaStream_t s) {
+  const NormParams& p = g.p;
+  const RopeParams& r = p.r;
+  const int heads = r.hq + r.hk;
+  const bool fast = fits(p) && rows_aligned(g.dq) && rows_aligned(g.dk);
+  const bool each_q = r.hq && p.n.q_head, each_k = r.hk && p.n.k_head;
+  const bool shared = !each_q && !each_k;
+  AddParams a{};
+  a.parts = g.parts;
+  a.dw_q = g.dw_q;
+  a.dw_k = g.dw_k;
+  a.d = r.head_dim;
+  a.weights_q = r.hq ? (each_q ? r.hq : 1) : 0;
+  a.weights_k = r.hk ? (each_k ? r.hk : 1) : 0;
+  a.inner_q = each_q ? 1 : r.hq;
+  a.inner_k = each_k ? 1 : r.hk;
+  a.heads_q = r.hq;
+  cudaError_t e;
+  if (fast) {
+    const int lanes = r.r.interleaved ? units_of_head<true>(r.head_dim, r.r.rot).lanes
+                                      : units_of_head<false>(r.head_dim, r.r.rot).lanes;
+    const NormGradPlan n = norm_grad_plan(r.tokens, heads, lanes);
+    if (shared) {  // two rows a CTA, of the queries and of the keys
+      a.outer = n.parts * n.groups;
+      a.rows = 2;
+      a.inner_q = a.inner_k = 1;
+    } else {
+      a.outer = n.parts;
+      a.rows = a.per = n.rows;
+      a.groups = n.groups;
+    }
+    if (dtype == MOE_ATTN_BF16)
+      e = r.r.interleaved ? launch_grad_fast<Bf16, true>(g, n, s)
+                          : launch_grad_fast<Bf16, false>(g, n, s);
+    else
+      e = r.r.interleaved ? launch_grad_fast<Fp16, true>(g, n, s)
+                          : launch_grad_fast<Fp16, false>(g, n, s);
+  } else {
+    const NormGradPlan n = norm_grad_plan(r.tokens, heads, 32);
+    a.outer = n.parts;
+    a.rows = a.per = heads;
+    a.groups = 1;
+    const dim3 grid(n.parts, (heads + kAnyWarps - 1) / kAnyWarps), block(kAnyWarps * 32);
+    e = dtype == MOE_ATTN_BF16 ? launch_after(norm_grad_any_kernel<Bf16>, grid, block, 0, s, g)
+                               : launch_after(norm_grad_any_kernel<Fp16>, grid, block, 0, s, g);
+  }
+  if (e != cudaSuccess) return e;
+  const int outputs = (a.weights_q + a.weights_k) * a.d;
+  return launch_after(norm_grad_add_kernel, dim3((outputs + 31) / 32), dim3(32, kAddRows), 0, s, a);
+}
+
+}  // namespace attn
+}  // namespace moe
