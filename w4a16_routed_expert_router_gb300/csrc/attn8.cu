@@ -93,6 +93,32 @@ Cache8 cache_of(const moe_attn_cache8* c) {
                 c->scale_page_stride, c->scale_head_stride, c->scale_block_stride};
 }
 
+// 4-D view {head_dim, page_size, kv_heads, pages} of codes, boxes of `rows` rows of one
+// page and head, `width` bytes wide (128 or 64: one swizzled row). What a box reaches
+// past head_dim, or a page past the cache, is filled with zeros.
+int encode_codes(CUtensorMap* m, const moe_attn_config& c, const moe_attn_cache8* k,
+                 const void* base, int rows, int width) {
+  const auto stride = [&](long long s, long long n) {
+    return (cuuint64_t)(n > 1 ? s : c.head_dim);  // of a single element: free
+  };
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
+                              (cuuint64_t)c.kv_heads, (cuuint64_t)k->num_pages};
+  const cuuint64_t strides[3] = {stride(k->token_stride, c.page_size),
+                                 stride(k->head_stride, c.kv_heads),
+                                 stride(k->page_stride, k->num_pages)};
+  const cuuint32_t box[4] = {(cuuint32_t)width, (cuuint32_t)rows, 1, 1};
+  return encode(m, 4, base, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// The kernels' attributes are set before a handle's first call over an 8-bit cache.
+int make_ready(moe_attn_handle* h) {
+  if (h->ready8) return MOE_ATTN_OK;
+  const int st = cuda_status(attn8_decode_setup());
+  h->ready8 = st == MOE_ATTN_OK;
+  return st;
+}
+
 // What moe_attn_append_norm and moe_attn_append8 have in common.
 int check_append(const moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* q_out,
                  int32_t T, const moe_attn_rotation* r, const moe_attn_norm* norm) {
@@ -339,7 +365,18 @@ int moe_attn_forward8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn
   p.a = params_of(h, q, out, lse, cache->num_pages, b, sc, sinks);
   p.c = cache_of(cache);
   p.dtype = c.dtype;
-  return cuda_status(launch_attn8_rows(p, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CUtensorMap kmap, vmap;
+  if ((long long)b->max_q * p.a.group <= kDecodeRows) {
+    if ((st = make_ready(h)) != MOE_ATTN_OK) return st;
+    const int chunks = c.head_dim > 64 ? 2 : 1, block = decode8_block(chunks);
+    const int box = c.page_size < block ? c.page_size : block;
+    if ((st = encode_codes(&kmap, c, cache, cache->k, box, 64 * chunks)) != MOE_ATTN_OK ||
+        (st = encode_codes(&vmap, c, cache, cache->v, box, 64 * chunks)) != MOE_ATTN_OK)
+      return st;
+    return cuda_status(launch_attn8_decode(p, h->decode, kmap, vmap, h->grid, s));
+  }
+  return cuda_status(launch_attn8_rows(p, s));
 }
 
 int moe_attn_forward_sinks(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out,

@@ -26,6 +26,8 @@ struct moe_attn_handle {
   Partials decode{};
   TcPieces tc{};
   bool tc_usable = false;
+  bool ready8 = false;          // the kernels over an 8-bit cache are set up
+  bool tc8_usable = false;
 };
 // The error word is the workspace's first; tests set its bits through here.
 static_assert(offsetof(moe_attn_handle, ws) == sizeof(moe_attn_config) + 8, "place of ws");
@@ -195,13 +197,15 @@ inline int log2i(int v) {
 }
 
 inline int encode(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims,
-           const cuuint64_t* strides, const cuuint32_t* box) {
+           const cuuint64_t* strides, const cuuint32_t* box,
+           CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT16,
+           CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return MOE_ATTN_ERR_CUDA;
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(base), dims,
+  const CUresult r = fn(m, type, rank, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     fprintf(stderr, "moe_attn: cuTensorMapEncodeTiled failed (%d)\n", (int)r);
