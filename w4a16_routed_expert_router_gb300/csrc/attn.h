@@ -296,9 +296,8 @@ struct Attn8Params {
 };
 cudaError_t launch_attn8_rows(const Attn8Params& p, cudaStream_t s);
 
-// keys per block of the few-token kernel, by 64-value chunks of a head: 16 KB of codes
-__host__ __device__ constexpr int decode8_block(int chunks) { return 128 / chunks; }
-// rows of a box of the cache there: the box brings whole heads
+// keys per block of the few-token kernel, by 64-value chunks of a head: 32 KB of codes
+__host__ __device__ constexpr int decode8_block(int chunks) { return 256 / chunks; }
 cudaError_t attn8_decode_setup();
 cudaError_t launch_attn8_decode(const Attn8Params& p, const Partials& w, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, int grid, cudaStream_t s);

@@ -2,16 +2,22 @@
 // the 8-bit cache: decode steps and short drafts.
 //
 // Bound by the cache's bytes; the division of the work, the roles and the joins are
-// those of attn_decode.cu, on blocks of 64 keys (128 at head sizes up to 64), 16 KB of
-// codes, in a ring of 10 stages. A key's codes are 128 (64) bytes: one swizzled row, and
+// those of attn_decode.cu, on blocks of 128 keys (256 at head sizes up to 64), 32 KB of
+// codes, in a ring of 6 stages. A key's codes are 128 (64) bytes: one swizzled row, and
 // one box brings a page's rows whole. The scales, one for 16 keys, come with the block
 // by asynchronous copies of 4 bytes.
+//
+// The keys are the M side of mma.sync m16n8k16 and the query rows the N side, 8 or 16
+// of them (S^T = K Q^T, O^T = V^T P^T): codes are converted once for all rows, and up
+// to 8 rows take half of the products, sums and registers of 16, so that more
+// warps fit. (With the rows as the M side, 8 warps took 373 us for 64 sequences of up to
+// 16384 keys, at a third of the issue slots and 16 % of the matrix unit: latency.)
 //
 // Codes go to fp16 in registers, two an instruction. ldmatrix deals in units of 16
 // bits, so a thread gets 4 values of a key in a row, (4 tig .. 4 tig + 3) of a 16-value
 // step: the sum over a head does not mind the order, and Q is laid out alike. Of V it
-// gets 2 values of 2 keys; their middle bytes change places, and the columns of two
-// neighbouring tiles of the result are the even and the odd values of 16.
+// gets 2 values of 2 keys; their middle bytes change places, and rows gid and gid + 8 of
+// the product are values 2 gid and 2 gid + 1 of 16.
 //
 // Scales. S = (q.k) (scale sk) with the key's scale sk. With v = code * sv, weights
 // enter the product as p sv: the exponent takes log2 sv, the running maximum is of
@@ -25,16 +31,35 @@ namespace moe {
 namespace attn {
 namespace {
 
-template <int ND>  // 64-value chunks of a head
+// Row tiles of 8: warps that consume, in groups of four that take blocks in turn.
+template <int NT>
+constexpr int kConsumers = NT == 1 ? 12 : 8;
+// Before them four that produce: K, V, scales; the last of them fills the warpgroup. (One
+// warp for all issued a box in 75 cycles and took 1000 for a block with its scales: 363
+// us for 64 sequences in 16-token pages, 216 without any arithmetic in 64-token pages.)
+constexpr int kProducers = 4;
+template <int NT>
+constexpr int kThreads = (kProducers + kConsumers<NT>) * 32;
+
+template <int ND>
+struct Split {
+  static constexpr int kBlk = decode8_block(ND);
+  static constexpr int kItem = 3;  // as much as in attn_decode.cu
+};
+
+template <int ND, int NT>  // 64-value chunks of a head, row tiles
 struct Smem {
   static constexpr int kD = ND * 64;
   static constexpr int kRow = ND * 64;                // bytes of a key's codes
   static constexpr int kBlk = decode8_block(ND);
   static constexpr int kSub = kBlk / 64;              // 16-key tiles of a warp in a block
-  static constexpr int kTile = 8 * 1024;              // K or V of a block
-  static constexpr int kStages = 10;                  // 160 KB in flight
+  static constexpr int kTile = 16 * 1024;             // K or V of a block
+  static constexpr int kGroupsOfWarps = kConsumers<NT> / 4;
+  static constexpr int kStages = NT == 1 ? 6 : 4;     // 192 or 128 KB in flight
+  static constexpr int kStateRows = NT == 1 ? kConsumers<1> / 2 * 8 : 4 * kRows;
   static_assert(kTile == kBlk * kRow, "a block's codes");
-  static_assert(kStages % 2 == 0, "stages belong to one consumer group each");
+  // a warp has to wait for every phase of a barrier it uses
+  static_assert(kStages % kGroupsOfWarps == 0, "stages belong to one consumer group each");
   static constexpr int kPad = kD + 4;                 // row stride of a state
   uint8_t ring[kStages][2 * kTile];
   float scales[kStages][2][kBlk / kScaleBlock];       // K's, V's
@@ -42,48 +67,61 @@ struct Smem {
   float o[kStateRows][kPad];
   float2 ml[kStateRows];
   uint64_t full[kStages], empty[kStages];
-  long long scan[kThreads / 32];
+  long long scan[kThreads<NT> / 32];
   long long begin_at;
   int begin_seq, last;
 };
 
-// A state's values in a warp: of 16 values, a thread has 4 in a row.
-template <int ND>
+// A state in a warp: rows 2 tig and 2 tig + 1 of each tile, of 16 values 2 gid and the
+// next.
+template <int ND, int NT>
 struct State8 {
-  typedef float Values[ND * 8][4];
-  static __device__ __forceinline__ void put(float* row, const Values& o, int r, int tig) {
+  typedef float Values[NT][ND * 4][4];
+  static constexpr int kRows = 2 * NT, kLanes = 4;  // lanes 4, 8, 16 apart: other keys of a row
+  static __device__ __forceinline__ int row(int r, int lane) {
+    return 8 * (r >> 1) + 2 * (lane & 3) + (r & 1);
+  }
+  static __device__ __forceinline__ bool first(int lane) { return lane < 4; }
+  static __device__ __forceinline__ void put(float* row, const Values& o, int r, int lane) {
 #pragma unroll
     for (int i = 0; i < ND * 4; ++i)
-      *reinterpret_cast<float4*>(row + i * 16 + 4 * tig) =
-          make_float4(o[2 * i][2 * r], o[2 * i + 1][2 * r], o[2 * i][2 * r + 1],
-                      o[2 * i + 1][2 * r + 1]);
+      *reinterpret_cast<float2*>(row + i * 16 + 2 * (lane >> 2)) =
+          make_float2(o[r >> 1][i][r & 1], o[r >> 1][i][2 + (r & 1)]);
   }
   // o = o a + row b
-  static __device__ __forceinline__ void add(const float* row, Values& o, int r, int tig, float a,
+  static __device__ __forceinline__ void add(const float* row, Values& o, int r, int lane, float a,
                                              float b) {
 #pragma unroll
     for (int i = 0; i < ND * 4; ++i) {
-      const float4 v = *reinterpret_cast<const float4*>(row + i * 16 + 4 * tig);
-      o[2 * i][2 * r] = o[2 * i][2 * r] * a + v.x * b;
-      o[2 * i + 1][2 * r] = o[2 * i + 1][2 * r] * a + v.y * b;
-      o[2 * i][2 * r + 1] = o[2 * i][2 * r + 1] * a + v.z * b;
-      o[2 * i + 1][2 * r + 1] = o[2 * i + 1][2 * r + 1] * a + v.w * b;
+      const float2 v = *reinterpret_cast<const float2*>(row + i * 16 + 2 * (lane >> 2));
+      float(&to)[4] = o[r >> 1][i];
+      to[r & 1] = to[r & 1] * a + v.x * b;
+      to[2 + (r & 1)] = to[2 + (r & 1)] * a + v.y * b;
     }
   }
 };
+
+// an 8 x 8 tile of 16-bit values, rows by columns, turned over its diagonal
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 
 template <int ND>
 __device__ __forceinline__ uint32_t swizzled(int row, int unit) {
   return (unit ^ (ND == 2 ? row & 7 : (row >> 1) & 3)) << 4;
 }
 
-template <int ND, int FORM>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int ND, int NT, int FORM>
+__global__ void __launch_bounds__(kThreads<NT>, 1)
     attn8_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap,
                         const __grid_constant__ Attn8Params g8,
                         const __grid_constant__ Partials ws) {
-  typedef Smem<ND> S;
+  typedef Smem<ND, NT> S;
+  typedef State8<ND, NT> State;
+  constexpr int R = State::kRows;
   const AttnParams& p = g8.a;
   constexpr int kBlk = S::kBlk, kSub = S::kSub, kUnits = ND * 4;
   constexpr float kUp = 15.0f;  // see attn_decode.cu
@@ -93,8 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&s.full[i], 1 + 32);  // the codes, and each lane's scales
-      mbar_init(&s.empty[i], kConsumers / 2);
+      mbar_init(&s.full[i], 2 + 32);  // K, V, and each lane's scales
+      mbar_init(&s.empty[i], 4);
     }
     fence_mbar_init();
   }
@@ -102,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   let_next_launch();
   long long total;
   Walk walk;
-  if (!begin_share<kBlk>(p, s, total, walk)) return;
+  if (!begin_share<Split<ND>, kThreads<NT>>(p, s, total, walk)) return;
   const Shares sh(total, gridDim.x);
   Piece g;
   uint32_t stage = 0, ph = 0;
@@ -111,22 +149,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int box_rows = min(ps, kBlk);
   const int box_bytes = box_rows * S::kRow;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- producer
-    if (lane == 0) {
-      prefetch_tmap(&kmap);
-      prefetch_tmap(&vmap);
-    }
+  if (warp < kProducers) {
+    // ---------------------------------------------------------------- producers
+    if (warp == kProducers - 1) return;
+    const bool scaler = warp == 2;
+    const CUtensorMap* map = warp == 0 ? &kmap : &vmap;
+    if (lane == 0 && !scaler) prefetch_tmap(map);
     const int ppb = kBlk / box_rows;                  // boxes of a block
     const int per_batch = 32 / ppb;
-    // lanes 0 .. 2 kGroups - 1 bring the scales of 16 keys each, K's then V's
+    // scales: lanes 0 .. 2 kGroups - 1 bring those of 16 keys each, K's then V's
     constexpr int kGroups = kBlk / kScaleBlock;
     const int grp = lane & (kGroups - 1);
-    const bool scaler = lane < 2 * kGroups;
     const float* scale_base = lane < kGroups ? g8.c.k_scales : g8.c.v_scales;
+    const int grp_box = min(grp * kScaleBlock / box_rows, ppb - 1);  // the box of its scale
     uint32_t filled = 0, last_ph = 0;
     bool ok = true;
-    while (ok && next_piece<kBlk>(p, walk, g)) {
+    while (ok && next_piece<Split<ND>>(p, walk, g)) {
       const Span& it = g.it;
       const int head = g.head, end = g.end;
       int n = g.n0;
@@ -155,34 +193,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int nn = n + i;
           const int kb = (nn < it.near ? nn : nn + it.skip) * kBlk;
           const int boxes = min(ppb, max(0, it.kv - kb + box_rows - 1) / box_rows);
-          const int page = __shfl_sync(0xffffffffu, ids, i * ppb + min(lane, ppb - 1));
-          const int scale_page =
-              __shfl_sync(0xffffffffu, ids, i * ppb + min(grp * kScaleBlock / box_rows, ppb - 1));
-          int go = 1;
-          if (lane == 0) {
-            go = bwait(&s.empty[stage], ph ^ 1u, p.err);
-            if (go) mbar_arrive_expect_tx(&s.full[stage], 2 * boxes * box_bytes);
-          }
-          go = __shfl_sync(0xffffffffu, go, 0);
-          if (!go) {
-            ok = false;
-            break;
-          }
-          __syncwarp();
+          if (!(ok = warp_wait(&s.empty[stage], ph ^ 1u, p.err))) break;
           if (scaler) {
-            const int key = kb + grp * kScaleBlock;
-            const bool there = key < it.kv && scale_page < p.num_pages;
-            const long long at = there ? scale_page * g8.c.scale_page + head * g8.c.scale_head +
-                                             ((key & (ps - 1)) / kScaleBlock) * g8.c.scale_block
-                                       : 0;
-            copy4_async(smem_u32(&s.scales[stage][0][0]) + lane * 4, scale_base + at, there);
-          }
-          arrive_after_copies(&s.full[stage]);
-          if (lane < boxes) {
-            const int row = (kb + lane * box_rows) & (ps - 1);
-            const uint32_t dst = smem_u32(s.ring[stage]) + lane * box_bytes;
-            tma_page(dst, &kmap, &s.full[stage], 0, row, head, page);
-            tma_page(dst + S::kTile, &vmap, &s.full[stage], 0, row, head, page);
+            const int page = __shfl_sync(0xffffffffu, ids, i * ppb + grp_box);
+            if (lane < 2 * kGroups) {
+              const int key = kb + grp * kScaleBlock;
+              const bool there = key < it.kv && page < p.num_pages;
+              const long long at = there ? page * g8.c.scale_page + head * g8.c.scale_head +
+                                               ((key & (ps - 1)) / kScaleBlock) * g8.c.scale_block
+                                         : 0;
+              copy4_async(smem_u32(&s.scales[stage][0][0]) + lane * 4, scale_base + at, there);
+            }
+            arrive_after_copies(&s.full[stage]);
+          } else {
+            uint32_t dst = smem_u32(s.ring[stage]) + (warp == 1 ? S::kTile : 0);
+            if (one_thread()) mbar_arrive_expect_tx(&s.full[stage], boxes * box_bytes);
+            for (int j = 0; j < boxes; ++j, dst += box_bytes) {
+              const int page = __shfl_sync(0xffffffffu, ids, i * ppb + j);
+              if (one_thread())
+                tma_page(dst, map, &s.full[stage], 0, (kb + j * box_rows) & (ps - 1), head, page);
+            }
           }
           filled |= 1u << stage;
           last_ph = (last_ph & ~(1u << stage)) | (ph << stage);
@@ -203,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ------------------------------------------------------------------ consumers
-  const int cw = warp - 1, grp = cw >> 2;
+  const int cw = warp - kProducers, grp = cw >> 2;
   const int gid = lane >> 2, tig = lane & 3;
   const int krow = (cw & 3) * 16 * kSub;                // this warp's keys in a block
   // where its 16-key tiles lie in a stage, and the ldmatrix lane addresses in a
@@ -218,66 +248,77 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lv_row = (lane & 7) + (((lane >> 3) & 1) << 3), lv_c = lane >> 4;
   const int units = p.head_dim >> 4;
   const bool bf16 = g8.dtype == MOE_ATTN_BF16;
-  int parity = 0;                                       // blocks this CTA took so far, mod 2
+  int turn = 0;                                         // blocks this CTA took so far, mod groups
   bool ok = true;
-  while (next_piece<kBlk>(p, walk, g)) {
+  while (next_piece<Split<ND>>(p, walk, g)) {
     const Span& it = g.it;
     const int head = g.head, n0 = g.n0, end = g.end;
     const int rows = it.n * p.group;
     const int prefix = prefix_of(p.sc, g.seq, it.kv);
-    // Q fragments; rows gid and gid + 8 are (token r / group, head r % group)
-    uint32_t qf[kUnits][4];
-    int pos[2], kept[2];
-    float slope[2], unit[2] = {1.0f, 1.0f};
+    // Q fragments: row gid of each tile, (token r / group, head r % group)
+    uint32_t qf[NT][kUnits][2];
+    float down[NT];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = min(gid + 8 * i, rows - 1);
+    for (int t = 0; t < NT; ++t) {
+      const int r = min(gid + 8 * t, rows - 1);
       const int tok = r / p.group, h = head * p.group + (r - tok * p.group);
-      pos[i] = it.kv - it.n + tok;
-      kept[i] = kept_of(p.sc, prefix, pos[i]);
-      slope[i] = FORM != kPlain && p.sc.slopes ? p.sc.slopes[h] : 0.0f;
       const uint16_t* qp =
           p.q.p + (long long)(it.first + tok) * p.q.token + (long long)h * p.q.head + 4 * tig;
-      uint2 w[kUnits];
       float top = 0.0f;
 #pragma unroll
       for (int k = 0; k < kUnits; ++k) {
-        w[k] = k < units && gid + 8 * i < rows ? __ldg(reinterpret_cast<const uint2*>(qp + 16 * k))
-                                               : make_uint2(0, 0);
-        if (bf16)
-          top = fmaxf(fmaxf(top, fmaxf(fabsf(bf16_bits_to_f32((uint16_t)w[k].x)),
-                                       fabsf(bf16_bits_to_f32((uint16_t)(w[k].x >> 16))))),
-                      fmaxf(fabsf(bf16_bits_to_f32((uint16_t)w[k].y)),
-                            fabsf(bf16_bits_to_f32((uint16_t)(w[k].y >> 16)))));
+        const uint2 w = k < units && gid + 8 * t < rows
+                            ? __ldg(reinterpret_cast<const uint2*>(qp + 16 * k))
+                            : make_uint2(0, 0);
+        qf[t][k][0] = w.x;
+        qf[t][k][1] = w.y;
+        if (bf16) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            top = fmaxf(top, fmaxf(fabsf(bf16_bits_to_f32((uint16_t)qf[t][k][i])),
+                                   fabsf(bf16_bits_to_f32((uint16_t)(qf[t][k][i] >> 16)))));
+        }
       }
+      down[t] = 1.0f;
       if (bf16) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const RowUnit u(top);
-        unit[i] = u.down;
+        down[t] = u.down;
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-          w[k].x = Fp16::pack(bf16_bits_to_f32((uint16_t)w[k].x) * u.up,
-                              bf16_bits_to_f32((uint16_t)(w[k].x >> 16)) * u.up);
-          w[k].y = Fp16::pack(bf16_bits_to_f32((uint16_t)w[k].y) * u.up,
-                              bf16_bits_to_f32((uint16_t)(w[k].y >> 16)) * u.up);
-        }
-      }
+        for (int k = 0; k < kUnits; ++k)
 #pragma unroll
-      for (int k = 0; k < kUnits; ++k) {
-        qf[k][i] = w[k].x;
-        qf[k][2 + i] = w[k].y;
+          for (int i = 0; i < 2; ++i)
+            qf[t][k][i] = Fp16::pack(bf16_bits_to_f32((uint16_t)qf[t][k][i]) * u.up,
+                                     bf16_bits_to_f32((uint16_t)(qf[t][k][i] >> 16)) * u.up);
       }
     }
-    float o[ND * 8][4];
+    // the rows whose scores this thread gets, see State8
+    int pos[R], kept[R];
+    float slope[R], unit[R];
 #pragma unroll
-    for (int i = 0; i < ND * 8; ++i)
+    for (int i = 0; i < R; ++i) {
+      const int r = min(State::row(i, lane), rows - 1);
+      const int tok = r / p.group, h = head * p.group + (r - tok * p.group);
+      pos[i] = it.kv - it.n + tok;
+      kept[i] = kept_of(p.sc, prefix, pos[i]);
+      slope[i] = FORM != kPlain && p.sc.slopes ? p.sc.slopes[h] : 0.0f;
+      unit[i] = __shfl_sync(0xffffffffu, down[i >> 1], (2 * tig + (i & 1)) * 4);
+      if (FORM == kPlain) unit[i] *= p.sc.scale * kLog2e;
+    }
+    typename State::Values o;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[t][i][j] = 0.0f;
+    float m[R], l[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) m[r] = -INFINITY, l[r] = 0.0f;
 
     for (int n = n0; n < end; ++n) {
-      if (parity == grp) {
+      if (turn == grp) {
         if (ok) ok = warp_wait(&s.full[stage], ph, p.err);
         const int k0 = (n < it.near ? n : n + it.skip) * kBlk + krow;
         if (ok && k0 < it.kv) {
@@ -296,91 +337,92 @@ __global__ void __launch_bounds__(kThreads, 1)
           float sk[kSub], lv[kSub], back[kSub];  // scale of K, log2 of V's, its inverse
 #pragma unroll
           for (int i = 0; i < kSub; ++i) {
-            const int t = krow / 16 + i;
-            sk[i] = scale_in_range(s.scales[stage][0][t]);
-            lv[i] = log2_of_scale(scale_in_range(s.scales[stage][1][t]));
+            sk[i] = scale_in_range(s.scales[stage][0][krow / 16 + i]);
+            lv[i] = log2_of_scale(scale_in_range(s.scales[stage][1][krow / 16 + i]));
             back[i] = ex2(-lv[i]);
           }
-          float sacc[2 * kSub][4] = {};
+          float x[kSub][NT][4] = {};
 #pragma unroll
           for (int k = 0; k < kUnits / 2; ++k) {
             if (2 * k >= units) break;
 #pragma unroll
             for (int i = 0; i < kSub; ++i) {
-              uint32_t b[4];
+              uint32_t b[4], a[2][4];
               ldsm4(kt + tile_at[i] + lk_row * S::kRow + swizzled<ND>(lk_row, 2 * k + lk_c), b);
-              mma16<Fp16>(sacc[2 * i], qf[2 * k], f16_of_codes(b[0], false),
-                          f16_of_codes(b[0], true));
-              mma16<Fp16>(sacc[2 * i + 1], qf[2 * k], f16_of_codes(b[2], false),
-                          f16_of_codes(b[2], true));
-              mma16<Fp16>(sacc[2 * i], qf[2 * k + 1], f16_of_codes(b[1], false),
-                          f16_of_codes(b[1], true));
-              mma16<Fp16>(sacc[2 * i + 1], qf[2 * k + 1], f16_of_codes(b[3], false),
-                          f16_of_codes(b[3], true));
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                a[u][0] = f16_of_codes(b[u], false);
+                a[u][1] = f16_of_codes(b[2 + u], false);
+                a[u][2] = f16_of_codes(b[u], true);
+                a[u][3] = f16_of_codes(b[2 + u], true);
+              }
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                  mma16<Fp16>(x[i][t], a[u], qf[t][2 * k + u][0], qf[t][2 * k + u][1]);
             }
           }
-          if (FORM != kPlain || !(k0 + 16 * kSub <= it.kv - it.n + 1 && p.sc.window == 0)) {
+          // x[i][t][j]: key 16 i + gid + 8 (j >> 1), row 2 tig + (j & 1) of tile t
+          const bool whole = k0 + 16 * kSub <= it.kv - it.n + 1 && p.sc.window == 0;
 #pragma unroll
-            for (int t = 0; t < 2 * kSub; ++t)
+          for (int i = 0; i < kSub; ++i)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int key = k0 + t * 8 + 2 * tig + (i & 1), r = i >> 1;
-                const int away = pos[r] - key;
-                const bool seen =
-                    key < it.kv && (key < kept[r] || (away >= 0 && (p.sc.window == 0 ||
-                                                                    away < p.sc.window)));
-                sacc[t][i] = seen ? score<FORM>(p.sc, sacc[t][i] * (unit[r] * sk[t >> 1]),
-                                                slope[r], away)
-                                  : -INFINITY;
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int r = 2 * t + (j & 1);
+                const float dot = x[i][t][j] * (unit[r] * sk[i]);
+                if (FORM == kPlain && whole) {  // every row sees every key
+                  x[i][t][j] = dot;
+                } else {
+                  const int key = k0 + 16 * i + gid + 8 * (j >> 1), away = pos[r] - key;
+                  const bool seen =
+                      key < it.kv && (key < kept[r] || (away >= 0 && (p.sc.window == 0 ||
+                                                                      away < p.sc.window)));
+                  const float y = FORM == kPlain ? dot : score<FORM>(p.sc, dot, slope[r], away);
+                  x[i][t][j] = seen ? y : -INFINITY;
+                }
               }
-          } else {  // every row sees every key
+          float base[R], scale[R];
+          bool moved = false;
 #pragma unroll
-            for (int t = 0; t < 2 * kSub; ++t)
+          for (int r = 0; r < R; ++r) {
+            float mx = -INFINITY;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                sacc[t][i] *= (p.sc.scale * kLog2e) * unit[i >> 1] * sk[t >> 1];
-          }
-          float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int t = 0; t < kSub; ++t)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              mx[r] = fmaxf(mx[r], fmaxf(fmaxf(sacc[2 * t][2 * r], sacc[2 * t][2 * r + 1]),
-                                         fmaxf(sacc[2 * t + 1][2 * r], sacc[2 * t + 1][2 * r + 1])) +
-                                       lv[t]);
-          float base[2], scale[2];
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+            for (int i = 0; i < kSub; ++i)
+              mx = fmaxf(mx, fmaxf(x[i][r >> 1][r & 1], x[i][r >> 1][2 + (r & 1)]) + lv[i]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             // up: no numerator above 2^kUp
-            mx[r] = fmaxf(m[r], __fadd_ru(mx[r], -kUp));
-            base[r] = mx[r] == -INFINITY ? 0.0f : mx[r];
+            mx = fmaxf(m[r], __fadd_ru(mx, -kUp));
+            base[r] = mx == -INFINITY ? 0.0f : mx;
             scale[r] = ex2(m[r] - base[r]);
-            m[r] = mx[r];
+            m[r] = mx;
             l[r] *= scale[r];
+            moved |= scale[r] != 1.0f;
           }
-          uint32_t pf[kSub][4];
+          uint32_t pf[kSub][NT][2];
 #pragma unroll
-          for (int t = 0; t < kSub; ++t)
+          for (int i = 0; i < kSub; ++i)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float b = base[r] - lv[t];
+            for (int t = 0; t < NT; ++t) {
               float e[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) e[i] = ex2(sacc[2 * t + (i >> 1)][2 * r + (i & 1)] - b);
-              l[r] = fmaf((e[0] + e[1]) + (e[2] + e[3]), back[t], l[r]);
-              pf[t][r] = Fp16::pack(e[0], e[1]);
-              pf[t][2 + r] = Fp16::pack(e[2], e[3]);
+              for (int j = 0; j < 4; ++j) e[j] = ex2(x[i][t][j] - (base[2 * t + (j & 1)] - lv[i]));
+              l[2 * t] = fmaf(e[0] + e[2], back[i], l[2 * t]);
+              l[2 * t + 1] = fmaf(e[1] + e[3], back[i], l[2 * t + 1]);
+              pf[i][t][0] = transposed(Fp16::pack(e[0], e[1]));
+              pf[i][t][1] = transposed(Fp16::pack(e[2], e[3]));
             }
-          if (__any_sync(0xffffffffu, scale[0] != 1.0f || scale[1] != 1.0f)) {
+          if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-            for (int i = 0; i < ND * 8; ++i) {
-              o[i][0] *= scale[0];
-              o[i][1] *= scale[0];
-              o[i][2] *= scale[1];
-              o[i][3] *= scale[1];
-            }
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[t][i][j] *= scale[2 * t + (j & 1)];
           }
 #pragma unroll
           for (int d = 0; d < kUnits / 2; ++d) {
@@ -390,14 +432,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t b[4];
               ldsm4t(vt + tile_at[i] + lv_row * S::kRow + swizzled<ND>(lv_row, 2 * d + lv_c), b);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) b[k] = __byte_perm(b[k], 0, 0x3120);
+              for (int u = 0; u < 2; ++u) {
+                const uint32_t lo = __byte_perm(b[2 * u], 0, 0x3120);
+                const uint32_t hi = __byte_perm(b[2 * u + 1], 0, 0x3120);
+                const uint32_t a[4] = {f16_of_codes(lo, false), f16_of_codes(lo, true),
+                                       f16_of_codes(hi, false), f16_of_codes(hi, true)};
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float(*to)[4] = &o[4 * d + 2 * k];
-                mma16<Fp16>(to[0], pf[i], f16_of_codes(b[2 * k], false),
-                            f16_of_codes(b[2 * k + 1], false));
-                mma16<Fp16>(to[1], pf[i], f16_of_codes(b[2 * k], true),
-                            f16_of_codes(b[2 * k + 1], true));
+                for (int t = 0; t < NT; ++t)
+                  mma16<Fp16>(o[t][2 * d + u], a, pf[i][t][0], pf[i][t][1]);
               }
             }
           }
@@ -407,56 +449,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.empty[stage]);
       }
-      parity ^= 1;
+      if (++turn == S::kGroupsOfWarps) turn = 0;
       if (++stage == S::kStages) {
         stage = 0;
         ph ^= 1u;
       }
     }
-    finish_item<State8<ND>, S::kD>(p, ws, s, sh, g, cw, o, m, l, [bf16](float x, float y) {
-      return bf16 ? Bf16::pack(x, y) : Fp16::pack(x, y);
-    });
+    finish_item<Split<ND>, State, kProducers * 32, kConsumers<NT>, S::kD>(
+        p, ws, s, sh, g, cw, o, m, l,
+        [bf16](float x, float y) { return bf16 ? Bf16::pack(x, y) : Fp16::pack(x, y); });
   }
 }
 
-template <int ND>
+template <int ND, int NT>
 constexpr int smem_bytes() {
-  return (int)sizeof(Smem<ND>) + 1024;
+  return (int)sizeof(Smem<ND, NT>) + 1024;
 }
-static_assert(smem_bytes<1>() <= 227 * 1024 && smem_bytes<2>() <= 227 * 1024,
+static_assert(smem_bytes<1, 1>() <= 227 * 1024 && smem_bytes<2, 1>() <= 227 * 1024 &&
+                  smem_bytes<1, 2>() <= 227 * 1024 && smem_bytes<2, 2>() <= 227 * 1024,
               "shared memory of a CTA");
 
-template <int ND>
+template <int ND, int NT>
 cudaError_t setup_nd() {
   cudaError_t e = cudaSuccess;
-  for (auto f : {attn8_decode_kernel<ND, kPlain>, attn8_decode_kernel<ND, kGeneral>,
-                 attn8_decode_kernel<ND, kWide>})
+  for (auto f : {attn8_decode_kernel<ND, NT, kPlain>, attn8_decode_kernel<ND, NT, kGeneral>,
+                 attn8_decode_kernel<ND, NT, kWide>})
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<ND>());
+      e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               smem_bytes<ND, NT>());
   return e;
 }
 
-template <int ND>
+template <int ND, int NT>
 cudaError_t launch_nd(const Attn8Params& p, const Partials& w, const CUtensorMap& kmap,
                       const CUtensorMap& vmap, int grid, cudaStream_t s) {
   const Form form = form_of(p.a.sc);
-  return launch_after(form == kPlain     ? attn8_decode_kernel<ND, kPlain>
-                      : form == kGeneral ? attn8_decode_kernel<ND, kGeneral>
-                                         : attn8_decode_kernel<ND, kWide>,
-                      dim3(grid), dim3(kThreads), smem_bytes<ND>(), s, kmap, vmap, p, w);
+  return launch_after(form == kPlain     ? attn8_decode_kernel<ND, NT, kPlain>
+                      : form == kGeneral ? attn8_decode_kernel<ND, NT, kGeneral>
+                                         : attn8_decode_kernel<ND, NT, kWide>,
+                      dim3(grid), dim3(kThreads<NT>), smem_bytes<ND, NT>(), s, kmap, vmap, p, w);
 }
 
 }  // namespace
 
 cudaError_t attn8_decode_setup() {
-  const cudaError_t e = setup_nd<1>();
-  return e != cudaSuccess ? e : setup_nd<2>();
+  cudaError_t e = setup_nd<1, 1>();
+  if (e == cudaSuccess) e = setup_nd<1, 2>();
+  if (e == cudaSuccess) e = setup_nd<2, 1>();
+  return e != cudaSuccess ? e : setup_nd<2, 2>();
 }
 
 cudaError_t launch_attn8_decode(const Attn8Params& p, const Partials& w, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, int grid, cudaStream_t s) {
-  return p.a.head_dim > 64 ? launch_nd<2>(p, w, kmap, vmap, grid, s)
-                           : launch_nd<1>(p, w, kmap, vmap, grid, s);
+  const bool wide = p.a.head_dim > 64;
+  if ((long long)p.a.b.max_q * p.a.group <= 8)
+    return wide ? launch_nd<2, 1>(p, w, kmap, vmap, grid, s)
+                : launch_nd<1, 1>(p, w, kmap, vmap, grid, s);
+  return wide ? launch_nd<2, 2>(p, w, kmap, vmap, grid, s)
+              : launch_nd<1, 2>(p, w, kmap, vmap, grid, s);
 }
 
 }  // namespace attn

@@ -30,6 +30,16 @@ __device__ __forceinline__ float log2_of_scale(float s) {
   return (float)((bits >> 23) - 127) + m;
 }
 
+// One thread of the converged warp, the same one every time: the compiler then knows
+// that a single thread issues what follows.
+__device__ __forceinline__ bool one_thread() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // 4 bytes from global to shared memory, or zeros where `on` is false
 __device__ __forceinline__ void copy4_async(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),

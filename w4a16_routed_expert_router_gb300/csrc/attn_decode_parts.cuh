@@ -9,8 +9,6 @@ namespace attn {
 
 using namespace tc;
 
-constexpr int kConsumers = 8;
-constexpr int kThreads = (1 + kConsumers) * 32;
 constexpr int kRows = kDecodeRows;
 constexpr int kStateRows = 4 * kRows;
 constexpr int kAhead = 12;  // pieces whose loads are under way together in a join
@@ -44,23 +42,24 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t* r) {
                : "r"(addr)
                : "memory");
 }
+template <int CONSUMERS>
 __device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS * 32) : "memory");
 }
 
-// An item's fixed cost in blocks, counted when the work is divided (four tokens of
-// 33 sequences: without it 28.8 us, 28.1 at 3, 24.6 at 6, 26.7 at 9).
-constexpr int kItemUnits = 6;
+// How a kernel divides the work: kBlk keys a block, and kItem, an item's fixed cost in
+// blocks.
+template <class C>
 __device__ __forceinline__ int units_of(const Span& r) {
-  return r.blocks ? r.blocks + kItemUnits : 0;
+  return r.blocks ? r.blocks + C::kItem : 0;
 }
 
-template <int BLK>
+template <class C>
 __device__ __forceinline__ Span item_of(const AttnParams& p, int s) {
   Span r = read_sequence(p.b, p.page_shift, s, p.err);
   r.blocks = 0;
   if (r.n > 0)  // and at most max_q, which is kRows / group or less
-    span_blocks(r, r.kv - r.n, r.kv - 1, p.sc, prefix_of(p.sc, s, r.kv), BLK);
+    span_blocks(r, r.kv - r.n, r.kv - 1, p.sc, prefix_of(p.sc, s, r.kv), C::kBlk);
   return r;
 }
 
@@ -76,11 +75,11 @@ struct Piece {
   long long first;
   int seq, head, n0, end;
 };
-template <int BLK>
+template <class C>
 __device__ __forceinline__ bool next_piece(const AttnParams& p, Walk& k, Piece& g) {
   while (k.w < k.hi) {
-    g.it = item_of<BLK>(p, k.seq);
-    const int units = units_of(g.it);
+    g.it = item_of<C>(p, k.seq);
+    const int units = units_of<C>(g.it);
     if (units == 0) {
       ++k.seq;
       continue;
@@ -90,8 +89,8 @@ __device__ __forceinline__ bool next_piece(const AttnParams& p, Walk& k, Piece& 
     g.head = k.head;
     g.first = k.at + (long long)k.head * units;
     const int u0 = (int)(k.w - g.first), u1 = (int)min((long long)units, u0 + (k.hi - k.w));
-    g.n0 = max(0, u0 - kItemUnits);
-    g.end = max(0, u1 - kItemUnits);
+    g.n0 = max(0, u0 - C::kItem);
+    g.end = max(0, u1 - C::kItem);
     k.w = g.first + u1;
     if (++k.head == p.hk) {  // (a share's last item may end early; nothing follows it)
       k.head = 0;
@@ -105,7 +104,7 @@ __device__ __forceinline__ bool next_piece(const AttnParams& p, Walk& k, Piece& 
 
 // Units of all sequences, and where this CTA's share begins; false where it has none.
 // The CTA's barriers are set up behind it.
-template <int BLK, class S>
+template <class C, int THREADS, class S>
 __device__ __forceinline__ bool begin_share(const AttnParams& p, S& s, long long& total,
                                             Walk& walk) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -113,7 +112,7 @@ __device__ __forceinline__ bool begin_share(const AttnParams& p, S& s, long long
   long long lo = 0, at = 0;
   int seq = 0;
   if (p.b.num_seqs <= 32) {  // each warp for itself
-    const long long mine = lane < p.b.num_seqs ? (long long)units_of(item_of<BLK>(p, lane)) * p.hk : 0;
+    const long long mine = lane < p.b.num_seqs ? (long long)units_of<C>(item_of<C>(p, lane)) * p.hk : 0;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -128,11 +127,11 @@ __device__ __forceinline__ bool begin_share(const AttnParams& p, S& s, long long
     at = __shfl_sync(0xffffffffu, incl - mine, seq);
     __syncthreads();  // the barriers are set up
   } else {
-    const int per = (p.b.num_seqs + kThreads - 1) / kThreads;
+    const int per = (p.b.num_seqs + THREADS - 1) / THREADS;
     const int s0 = min(p.b.num_seqs, (int)threadIdx.x * per);
     const int s1 = min(p.b.num_seqs, s0 + per);
     long long mine = 0;
-    for (int q = s0; q < s1; ++q) mine += (long long)units_of(item_of<BLK>(p, q)) * p.hk;
+    for (int q = s0; q < s1; ++q) mine += (long long)units_of<C>(item_of<C>(p, q)) * p.hk;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -142,7 +141,7 @@ __device__ __forceinline__ bool begin_share(const AttnParams& p, S& s, long long
     if (lane == 31) s.scan[warp] = incl;
     __syncthreads();
     long long before = incl - mine;
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < THREADS / 32; ++i) {
       if (i < warp) before += s.scan[i];
       total += s.scan[i];
     }
@@ -152,7 +151,7 @@ __device__ __forceinline__ bool begin_share(const AttnParams& p, S& s, long long
     if (lo >= before && lo < before + mine) {
       long long first = before;
       for (int q = s0; q < s1; ++q) {
-        const long long c = (long long)units_of(item_of<BLK>(p, q)) * p.hk;
+        const long long c = (long long)units_of<C>(item_of<C>(p, q)) * p.hk;
         if (lo < first + c) {
           s.begin_seq = q;
           s.begin_at = first;
@@ -171,58 +170,62 @@ __device__ __forceinline__ bool begin_share(const AttnParams& p, S& s, long long
 }
 
 // The end of an item: the warps' states joined in shared memory, and its results
-// written, or left as a piece, which the last CTA of the item joins. L: where the
-// values of a state lie in its threads; D: row length of the pieces.
-template <class L, int D, class S, class Pack>
+// written, or left as a piece, which the last CTA of the item joins. L: which rows a
+// thread has and where the values of a state lie in it; FIRST: first consumer thread;
+// D: row length of the pieces.
+template <class C, class L, int FIRST, int CONSUMERS, int D, class S, class Pack>
 __device__ __forceinline__ void finish_item(const AttnParams& p, const Partials& ws, S& s,
-                                          const Shares& sh, const Piece& g, int cw,
-                                          typename L::Values& o, float (&m)[2], float (&l)[2],
-                                          const Pack& pack) {
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+                                            const Shares& sh, const Piece& g, int cw,
+                                            typename L::Values& o, float (&m)[L::kRows],
+                                            float (&l)[L::kRows], const Pack& pack) {
+  const int lane = threadIdx.x & 31;
   const Span& it = g.it;
   const int head = g.head, n0 = g.n0, end = g.end, rows = it.n * p.group;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+  for (int r = 0; r < L::kRows; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], L::kLanes);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2 * L::kLanes);
+    if (L::kLanes == 4) l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
   }
-  // Join the warps' states: with more than 8 rows warps 4-7 first hand theirs
-  // to warps 0-3, then all states lie in shared memory and every thread adds up
-  // its values of them.
+  // Join the warps' states: where they are more than there is room for, the upper half
+  // of the warps first hand theirs to the lower half; then all states lie in shared
+  // memory and every thread adds up its values of them.
   const auto put = [&](int state, int per_state) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = gid + 8 * r;
+    for (int r = 0; r < L::kRows; ++r) {
+      const int row = L::row(r, lane);
       if (row >= rows) continue;
       const int at_row = state * per_state + row;
-      if (tig == 0) s.ml[at_row] = make_float2(m[r], l[r]);
-      L::put(s.o[at_row], o, r, tig);
+      if (L::first(lane)) s.ml[at_row] = make_float2(m[r], l[r]);
+      L::put(s.o[at_row], o, r, lane);
     }
   };
-  const int states = rows > 8 ? 4 : 8, per_state = rows > 8 ? kRows : 8;
-  if (rows > 8) {
-    if (cw >= 4) put(cw - 4, kRows);
-    consumers_sync();
-    if (cw < 4) {
+  const bool many = rows > 8, fold = many || CONSUMERS > 8;
+  const int states = fold ? CONSUMERS / 2 : CONSUMERS, per_state = many ? kRows : 8;
+  static_assert(CONSUMERS <= 16, "eight states of 8 rows have room");
+  if (fold) {
+    if (cw >= CONSUMERS / 2) put(cw - CONSUMERS / 2, per_state);
+    consumers_sync<CONSUMERS>();
+    if (cw < CONSUMERS / 2) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = gid + 8 * r;
+      for (int r = 0; r < L::kRows; ++r) {
+        const int row = L::row(r, lane);
         if (row >= rows) continue;
-        const float2 x = s.ml[cw * kRows + row];
+        const float2 x = s.ml[cw * per_state + row];
         const float mm = fmaxf(m[r], x.x), base = mm == -INFINITY ? 0.0f : mm;
         const float a = ex2(m[r] - base), b = ex2(x.x - base);
         m[r] = mm;
         l[r] = l[r] * a + x.y * b;
-        L::add(s.o[cw * kRows + row], o, r, tig, a, b);
+        L::add(s.o[cw * per_state + row], o, r, lane, a, b);
       }
     }
-    consumers_sync();
+    consumers_sync<CONSUMERS>();
   }
   if (cw < states) put(cw, per_state);
-  consumers_sync();
+  consumers_sync<CONSUMERS>();
 
   const bool split = end - n0 < it.blocks;
-  const int c0 = split ? sh.of(g.first + kItemUnits) : 0;  // CTA of the item's first block
+  const int c0 = split ? sh.of(g.first + C::kItem) : 0;  // CTA of the item's first block
   const long long slot = 2LL * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0);
   const int half_d = p.head_dim >> 1;
   const auto write = [&](int row, int c, float x, float y, float mm, float sum) {
@@ -234,7 +237,7 @@ __device__ __forceinline__ void finish_item(const AttnParams& p, const Partials&
       p.lse[(long long)(it.first + tok) * p.hq + h] =
           sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
   };
-  for (int e = threadIdx.x - 32; e < rows * half_d; e += kConsumers * 32) {
+  for (int e = threadIdx.x - FIRST; e < rows * half_d; e += CONSUMERS * 32) {
     const int row = e / half_d, c = 2 * (e - row * half_d);
     float2 q[8], v[8];
     float mm = -INFINITY, sum = 0.0f, x = 0.0f, y = 0.0f;
@@ -266,20 +269,20 @@ __device__ __forceinline__ void finish_item(const AttnParams& p, const Partials&
     }
   }
   if (split) __threadfence();
-  consumers_sync();  // the states are read, and a piece is written
+  consumers_sync<CONSUMERS>();  // the states are read, and a piece is written
   if (split) {
     // the last CTA of the item joins the pieces, in their order
-    const int c1 = sh.of(g.first + units_of(it) - 1);
+    const int c1 = sh.of(g.first + units_of<C>(it) - 1);
     if (cw == 0 && lane == 0) {
       const unsigned got = atomicAdd(ws.count + c0, 1u);
       s.last = got == (unsigned)(c1 - c0);
       if (s.last) ws.count[c0] = 0;
       __threadfence();
     }
-    consumers_sync();
+    consumers_sync<CONSUMERS>();
     if (s.last) {
       const int pieces = c1 - c0 + 1;
-      for (int e = threadIdx.x - 32; e < rows * half_d; e += kConsumers * 32) {
+      for (int e = threadIdx.x - FIRST; e < rows * half_d; e += CONSUMERS * 32) {
         const int row = e / half_d, c = 2 * (e - row * half_d);
         float mm = -INFINITY, sum = 0.0f, x = 0.0f, y = 0.0f;
         for (int i0 = 0; i0 < pieces; i0 += kAhead) {
