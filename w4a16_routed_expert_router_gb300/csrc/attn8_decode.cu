@@ -31,7 +31,8 @@ namespace moe {
 namespace attn {
 namespace {
 
-// Row tiles of 8: warps that consume, in groups of four that take blocks in turn.
+// Warps that consume, in groups of four that take blocks in turn. (Twelve for two row
+// tiles of small heads, whose registers then spill: 45 -> 64 us for 48 drafts.)
 template <int NT>
 constexpr int kConsumers = NT == 1 ? 12 : 8;
 // Before them four that produce: K, V, scales; the last of them fills the warpgroup. (One
@@ -55,8 +56,8 @@ struct Smem {
   static constexpr int kSub = kBlk / 64;              // 16-key tiles of a warp in a block
   static constexpr int kTile = 16 * 1024;             // K or V of a block
   static constexpr int kGroupsOfWarps = kConsumers<NT> / 4;
-  static constexpr int kStages = NT == 1 ? 6 : 4;     // 192 or 128 KB in flight
-  static constexpr int kStateRows = NT == 1 ? kConsumers<1> / 2 * 8 : 4 * kRows;
+  static constexpr int kStages = ND * NT <= 2 ? 6 : 4;  // 192 or 128 KB in flight
+  static constexpr int kStateRows = kConsumers<NT> / 2 * 8 * NT;
   static_assert(kTile == kBlk * kRow, "a block's codes");
   // a warp has to wait for every phase of a barrier it uses
   static_assert(kStages % kGroupsOfWarps == 0, "stages belong to one consumer group each");
@@ -364,7 +365,9 @@ __global__ void __launch_bounds__(kThreads<NT>, 1)
             }
           }
           // x[i][t][j]: key 16 i + gid + 8 (j >> 1), row 2 tig + (j & 1) of tile t
-          const bool whole = k0 + 16 * kSub <= it.kv - it.n + 1 && p.sc.window == 0;
+          // every row of the sequence sees every key of the warp's, or not
+          const bool whole = k0 + 16 * kSub <= it.kv - it.n + 1 &&
+                             (p.sc.window == 0 || k0 > it.kv - 1 - p.sc.window);
 #pragma unroll
           for (int i = 0; i < kSub; ++i)
 #pragma unroll
@@ -372,18 +375,26 @@ __global__ void __launch_bounds__(kThreads<NT>, 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const int r = 2 * t + (j & 1);
-                const float dot = x[i][t][j] * (unit[r] * sk[i]);
-                if (FORM == kPlain && whole) {  // every row sees every key
-                  x[i][t][j] = dot;
-                } else {
+                x[i][t][j] *= unit[r] * sk[i];
+                if (FORM != kPlain)
+                  x[i][t][j] = score<FORM>(p.sc, x[i][t][j], slope[r],
+                                           pos[r] - (k0 + 16 * i + gid + 8 * (j >> 1)));
+              }
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < kSub; ++i)
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int r = 2 * t + (j & 1);
                   const int key = k0 + 16 * i + gid + 8 * (j >> 1), away = pos[r] - key;
                   const bool seen =
                       key < it.kv && (key < kept[r] || (away >= 0 && (p.sc.window == 0 ||
                                                                       away < p.sc.window)));
-                  const float y = FORM == kPlain ? dot : score<FORM>(p.sc, dot, slope[r], away);
-                  x[i][t][j] = seen ? y : -INFINITY;
+                  if (!seen) x[i][t][j] = -INFINITY;
                 }
-              }
+          }
           float base[R], scale[R];
           bool moved = false;
 #pragma unroll
