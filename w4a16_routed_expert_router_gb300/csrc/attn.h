@@ -294,13 +294,17 @@ struct Attn8Params {
   Cache8 c;
   int dtype;
 };
-cudaError_t launch_attn8_rows(const Attn8Params& p, cudaStream_t s);
-
 // keys per block of the few-token kernel, by 64-value chunks of a head: 32 KB of codes
 __host__ __device__ constexpr int decode8_block(int chunks) { return 256 / chunks; }
 cudaError_t attn8_decode_setup();
 cudaError_t launch_attn8_decode(const Attn8Params& p, const Partials& w, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, int grid, cudaStream_t s);
+
+// every other batch; *usable as above
+cudaError_t attn8_tc_setup(bool* usable);
+cudaError_t launch_attn8_tc(const Attn8Params& p, const TcPieces& w, const CUtensorMap& qmap,
+                            const CUtensorMap& kmap, const CUtensorMap& vmap, int grid,
+                            cudaStream_t s);
 
 }  // namespace attn
 }  // namespace moe

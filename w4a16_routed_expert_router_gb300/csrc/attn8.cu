@@ -114,7 +114,8 @@ int encode_codes(CUtensorMap* m, const moe_attn_config& c, const moe_attn_cache8
 // The kernels' attributes are set before a handle's first call over an 8-bit cache.
 int make_ready(moe_attn_handle* h) {
   if (h->ready8) return MOE_ATTN_OK;
-  const int st = cuda_status(attn8_decode_setup());
+  int st = cuda_status(attn8_decode_setup());
+  if (st == MOE_ATTN_OK) st = cuda_status(attn8_tc_setup(&h->tc8_usable));
   h->ready8 = st == MOE_ATTN_OK;
   return st;
 }
@@ -365,18 +366,25 @@ int moe_attn_forward8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn
   p.a = params_of(h, q, out, lse, cache->num_pages, b, sc, sinks);
   p.c = cache_of(cache);
   p.dtype = c.dtype;
+  if ((st = make_ready(h)) != MOE_ATTN_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  CUtensorMap kmap, vmap;
-  if ((long long)b->max_q * p.a.group <= kDecodeRows) {
-    if ((st = make_ready(h)) != MOE_ATTN_OK) return st;
-    const int chunks = c.head_dim > 64 ? 2 : 1, block = decode8_block(chunks);
-    const int box = c.page_size < block ? c.page_size : block;
-    if ((st = encode_codes(&kmap, c, cache, cache->k, box, 64 * chunks)) != MOE_ATTN_OK ||
-        (st = encode_codes(&vmap, c, cache, cache->v, box, 64 * chunks)) != MOE_ATTN_OK)
-      return st;
-    return cuda_status(launch_attn8_decode(p, h->decode, kmap, vmap, h->grid, s));
+  // as in moe_attn_forward: one kernel for the whole batch
+  CUtensorMap qmap, kmap, vmap;
+  const bool few = (long long)b->max_q * p.a.group <= kDecodeRows;
+  const int chunks = c.head_dim > 64 ? 2 : 1;
+  const int block = few ? decode8_block(chunks) : kTcBlock;
+  const int box = c.page_size < block ? c.page_size : block;
+  const int width = few ? 64 * chunks : 128;
+  if ((st = encode_codes(&kmap, c, cache, cache->k, box, width)) != MOE_ATTN_OK ||
+      (st = encode_codes(&vmap, c, cache, cache->v, box, width)) != MOE_ATTN_OK)
+    return st;
+  if (few) return cuda_status(launch_attn8_decode(p, h->decode, kmap, vmap, h->grid, s));
+  if (!h->tc8_usable) {  // another compiler: few-token batches go on
+    fprintf(stderr, "moe_attn: the tensor-core kernel was built with other registers than it needs\n");
+    return MOE_ATTN_ERR_CUDA;
   }
-  return cuda_status(launch_attn8_rows(p, s));
+  if ((st = encode_q(&qmap, c, q, b->num_tokens)) != MOE_ATTN_OK) return st;
+  return cuda_status(launch_attn8_tc(p, h->tc, qmap, kmap, vmap, h->grid, s));
 }
 
 int moe_attn_forward_sinks(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out,

@@ -29,6 +29,8 @@
 // winds down. The four warps of a softmax group meet at named barriers, which have
 // no limit, so they go on or leave as one (group_all): a warp whose wait gave up
 // takes part in the next vote before it leaves.
+// (attn8_tc.cu includes this file for what it shares with the kernel over an 8-bit
+// cache, all that comes before the kernel here.)
 #include "attn_common.cuh"
 
 namespace moe {
@@ -86,8 +88,9 @@ template <typename T>
 constexpr float kUp = T::kFp16 ? 12.0f : 0.0f;
 
 // one value per warp of a scan over the CTA
+template <int THREADS>
 struct Scan {
-  long long part[kThreads / 32];
+  long long part[THREADS / 32];
 };
 // What an entry needs of its sequence: n = 0 where its lengths leave their ranges.
 struct alignas(16) Seq {
@@ -115,7 +118,7 @@ struct Smem {
   uint8_t q[2][ND * kChunk];
   uint8_t piece[kPieces][kPieceBytes];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
-  Scan scan;
+  Scan<kThreads> scan;
   Share share;
   unsigned there[2];
   uint64_t kv_full[kSlots], kv_empty[kSlots];
@@ -304,9 +307,9 @@ struct alignas(16) Piece {
 static_assert(sizeof(Piece) == kPieceBytes, "shared memory of a piece");
 
 // One role's way through the pieces; `whole` warps or single threads.
-template <int ND, bool kWarp>
+template <class S, bool kWarp>
 struct Pieces {
-  Smem<ND>& s;
+  S& s;
   unsigned* err;
   int i = 0;
   uint32_t ph = 0;
@@ -378,7 +381,9 @@ __device__ __forceinline__ Entry entry_of(const AttnParams& p, const Seq& q, int
 }
 
 // Exclusive scan of a value per thread over the CTA; the sum in `whole`.
-__device__ __forceinline__ long long cta_scan(Scan& sc, long long mine, long long& whole) {
+template <int THREADS>
+__device__ __forceinline__ long long cta_scan(Scan<THREADS>& sc, long long mine,
+                                              long long& whole) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long v = mine;
 #pragma unroll
@@ -392,7 +397,7 @@ __device__ __forceinline__ long long cta_scan(Scan& sc, long long mine, long lon
   long long before = v - mine;
   whole = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
+  for (int i = 0; i < THREADS / 32; ++i) {
     if (i < warp) before += sc.part[i];
     whole += sc.part[i];
   }
@@ -407,13 +412,13 @@ __device__ __forceinline__ int rest_of(int units) { return units ? units + kRest
 // run of entries a thread. `room` is shared memory for a number per sequence and
 // one more, and for the sequences themselves while they are few.
 constexpr int kSeqsKept = 4096;
-template <bool CUT>
-__device__ __forceinline__ void divide(const AttnParams& p, Scan& sc, uint8_t* room, Share& share,
-                                       int tpt) {
+template <bool CUT, int THREADS>
+__device__ __forceinline__ void divide(const AttnParams& p, Scan<THREADS>& sc, uint8_t* room,
+                                       Share& share, int tpt) {
   const int tid = threadIdx.x, seqs = p.b.num_seqs;
   Seq* kept = reinterpret_cast<Seq*>(room);
   int* first = reinterpret_cast<int*>(room + (seqs <= kSeqsKept ? seqs * sizeof(Seq) : 0));
-  const int per = (seqs + kThreads - 1) / kThreads;
+  const int per = (seqs + THREADS - 1) / THREADS;
   const int s0 = min(seqs, tid * per), s1 = min(seqs, s0 + per);
   const auto get = [&](int q) { return seqs <= kSeqsKept ? kept[q] : sequence_of(p, q); };
   long long mine = 0, n = 0;
@@ -429,7 +434,7 @@ __device__ __forceinline__ void divide(const AttnParams& p, Scan& sc, uint8_t* r
   }
   if (tid == 0) first[seqs] = (int)n;
   __syncthreads();
-  const int run = ((int)n + kThreads - 1) / kThreads;
+  const int run = ((int)n + THREADS - 1) / THREADS;
   const int e0 = min((int)n, tid * run), e1 = min((int)n, e0 + run);
   int seq = 0;
   if (e0 < e1) {  // last sequence with first <= e0
@@ -493,8 +498,8 @@ __device__ __forceinline__ void divide(const AttnParams& p, Scan& sc, uint8_t* r
 // O in TMEM (cnt > 0). Its loops are not unrolled: the code runs once a piece, and
 // what it takes is mostly the fetching of its instructions (unrolled, a whole
 // item's results took 6500 cycles to store, 3300 so).
-template <typename T, int ND, bool CUT>
-__device__ __forceinline__ void finish_piece(const AttnParams& p, const TcPieces& ws, Smem<ND>& s,
+template <typename T, int ND, bool CUT, class S>
+__device__ __forceinline__ void finish_piece(const AttnParams& p, const TcPieces& ws, S& s,
                                           const Piece* piece, int t, uint32_t o_tm, int cnt,
                                           float m, float l) {
   const Piece& g = *piece;
@@ -657,6 +662,197 @@ __device__ __forceinline__ void finish_piece(const AttnParams& p, const TcPieces
   }
 }
 
+// One thread walks the CTA's share and hands its pieces to the others.
+template <bool CUT, class S>
+__device__ __forceinline__ void walk_share(const AttnParams& p, S& s, int tpt) {
+  const Share& sh = s.share;
+  const int cta = blockIdx.x;
+  const bool chunk = CUT && cta < sh.cuts;  // a chunk of an item, and nothing else
+  long long at = sh.at, entry_at = sh.entry_at;
+  const long long hi = sh.hi;
+  int seq = sh.seq, index = sh.index, cut_at = sh.cut_at;
+  Entry e;
+  Seq r = sh.s;
+  // an item of the entry: its chunks; the units it has on the list, the first
+  // of which read nothing, and the block that the others begin with
+  int chunks = 0, listed = 0, fixed = 0, behind = 0;
+  int head = -1, i = 0;   // head -2: the sequence is to be read, -1: the entry made
+  uint32_t ph = 0;
+  bool ok = true;
+  while (ok) {
+    Piece o = {};
+    while (at < hi) {
+      if (head < 0) {
+        if (head == -2) r = sequence_of(p, seq);
+        if (index == entries_of(r, tpt)) {
+          ++seq;
+          index = 0;
+          head = -2;
+          continue;
+        }
+        e = entry_of(p, r, seq, index, tpt);
+        listed = units_of(e);
+        if (CUT && sh.cut) {
+          chunks = listed / (int)sh.per;
+          listed = rest_of(listed - chunks * (int)sh.per);
+          behind = max(0, chunks * (int)sh.per - kItemUnits);
+        }
+        fixed = listed - (e.blocks - behind);
+        head = chunk ? (cta - cut_at) / chunks
+                     : listed ? (int)quotient(at - entry_at, listed) : p.hk;
+      }
+      const long long item = entry_at + (long long)head * listed;
+      if (chunk) {
+        o.number = cta - cut_at - head * chunks;
+        o.n0 = max(0, o.number * (int)sh.per - kItemUnits);
+        o.end = (o.number + 1) * (int)sh.per - kItemUnits;
+        at = hi;
+      } else if (listed) {
+        const int u0 = (int)(at - item), u1 = (int)min((long long)listed, u0 + (hi - at));
+        at = item + u1;
+        o.n0 = behind + max(0, u0 - fixed);
+        o.end = behind + max(0, u1 - fixed);
+      }
+      if (o.end <= o.n0) o.end = 0;  // nothing to read: no piece
+      if (o.end) {
+        o.head = head;
+        o.first = e.first, o.ntok = e.ntok, o.p0 = e.p0, o.kv = e.kv;
+        o.near = e.near, o.skip = e.skip, o.blocks = e.blocks, o.prefix = e.prefix;
+        o.seq = e.seq;
+        o.cnt[0] = min(o.end, blocks_of_tile0(e, tpt)) - o.n0;
+        o.cnt[1] = e.ntok > tpt ? o.end - o.n0 : 0;
+        if (o.end - o.n0 < e.blocks) {
+          o.cta0 = sh.cuts + (int)quotient(item + fixed, sh.per);
+          const int last = sh.cuts + (int)quotient(item + listed - 1, sh.per);
+          o.pieces = chunks + (listed ? last - o.cta0 + 1 : 0);
+          o.chunks = chunks;
+          o.chunk0 = chunks ? cut_at + head * chunks : o.cta0;
+          if (!chunk) o.number = chunks + cta - o.cta0;
+        }
+      }
+      if (listed == 0 || at == item + listed) ++head;
+      if (head >= p.hk) {
+        head = -1;
+        ++index;
+        entry_at += (long long)listed * p.hk;
+        cut_at += chunks * p.hk;
+      }
+      if (o.end) break;
+    }
+    ok = bwait_piece(&s.piece_empty[i], ph ^ 1u, p.err);
+    if (!ok) break;
+    *reinterpret_cast<Piece*>(s.piece[i]) = o;
+    mbar_arrive(&s.piece_full[i]);
+    if (++i == kPieces) {
+      i = 0;
+      ph ^= 1u;
+    }
+    if (o.end == 0) break;  // the end of the share, told to all
+  }
+}
+
+// Dot products of a row as scores in log2 units: cap and distance bias. `mine`: the row
+// exists.
+template <int FORM>
+__device__ __forceinline__ void general_scores(const AttnParams& p, float (&x)[kBlk],
+                                               float scale2, int kb, int kv, bool mine, int pos,
+                                               int p_first, float slope) {
+  const float cap_in = p.sc.cap_in;
+  const float cap_out = p.sc.softcap * kLog2e;
+  if (p.sc.softcap > 0.0f) {
+    // cap tanh(y) in log2 units, y = x scale / cap. While every |y| of the
+    // warp's rows is below kTanhMax, it is y times a polynomial in y^2, two
+    // keys to an instruction; else as FORM has it. Rows and keys that do
+    // not exist have no part in the choice: the block with the last key takes
+    // the second form. (The powers of scale / cap do not go into the
+    // coefficients, which saves a product but lets the highest ones vanish
+    // where scale / cap is small: scores were 0.3 off at a cap of 2000.)
+    float top = fabsf(x[0]);
+#pragma unroll
+    for (int i = 1; i < kBlk - 1; i += 2) top = max3(top, fabsf(x[i]), fabsf(x[i + 1]));
+    top = fmaxf(top, fabsf(x[kBlk - 1]));
+    if (kb + kBlk <= kv &&
+        __all_sync(0xffffffffu, !mine || top * fabsf(cap_in) < kTanhMax)) {
+      const uint64_t in2 = pack2(cap_in, cap_in);
+      float f[kTanhTerms];
+#pragma unroll
+      for (int k = 0; k < kTanhTerms; ++k) f[k] = kTanh[k] * cap_out;
+#pragma unroll
+      for (int i = 0; i < kBlk / 2; ++i) {
+        const uint64_t y = mul2(pack2(x[2 * i], x[2 * i + 1]), in2);
+        const uint64_t t = mul2(y, y);
+        uint64_t r = pack2(f[kTanhTerms - 1], f[kTanhTerms - 1]);
+#pragma unroll
+        for (int k = kTanhTerms - 2; k >= 0; --k) r = fma2(r, t, pack2(f[k], f[k]));
+        unpack2(mul2(r, y), x[2 * i], x[2 * i + 1]);
+      }
+    } else if (FORM == kWide) {
+#pragma unroll
+      for (int i = 0; i < kBlk / 2; ++i) {
+        const uint64_t y = pack2(tanh_range(x[2 * i] * cap_in),
+                                 tanh_range(x[2 * i + 1] * cap_in));
+        const uint64_t t = mul2(y, y);
+        uint64_t a = pack2(kTanhP[4], kTanhP[4]), b = pack2(kTanhQ[4], kTanhQ[4]);
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          a = fma2(a, t, pack2(kTanhP[k], kTanhP[k]));
+          b = fma2(b, t, pack2(kTanhQ[k], kTanhQ[k]));
+        }
+        float b0, b1;
+        unpack2(b, b0, b1);
+        a = mul2(mul2(a, y), pack2(rcp(b0), rcp(b1)));
+        unpack2(mul2(a, pack2(cap_out, cap_out)), x[2 * i], x[2 * i + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBlk; ++i) {
+        const float e = ex2(x[i] * (2.0f * kLog2e * cap_in));
+        x[i] = fmaf(-2.0f * cap_out, rcp(1.0f + e), cap_out);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kBlk / 2; ++i) {
+      const uint64_t r = mul2(pack2(x[2 * i], x[2 * i + 1]), pack2(scale2, scale2));
+      unpack2(r, x[2 * i], x[2 * i + 1]);
+    }
+  }
+  if (p.sc.slopes) {
+    // distances are whole numbers: exact steps of -1 from key to key, where
+    // fp32 holds them all and no key lies ahead of its query
+    const float far = (float)(pos - kb);
+    if (kb + kBlk - 1 <= p_first && p_first - kb < (1 << 24) - 128) {
+      uint64_t away = pack2(far, far - 1.0f);
+#pragma unroll
+      for (int i = 0; i < kBlk / 2; ++i) {
+        const uint64_t r =
+            fma2(away, pack2(-slope, -slope), pack2(x[2 * i], x[2 * i + 1]));
+        unpack2(r, x[2 * i], x[2 * i + 1]);
+        away = add2(away, pack2(-2.0f, -2.0f));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBlk; ++i) x[i] = fmaf(-slope, fabsf(far - (float)i), x[i]);
+    }
+  }
+}
+
+// Scores of a row's keys that it does not see, of the block from key kb on.
+__device__ __forceinline__ void mask_row(const AttnParams& p, float (&x)[kBlk], int kb, int prefix,
+                                         int pos) {
+  // bit i of word w: this row sees key kb + 32 w + i
+  const int a = pos - kb + 1, b = p.sc.window ? pos - p.sc.window - kb + 1 : 0;
+  const int pre = kept_of(p.sc, prefix, pos) - kb;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t bits = (below(a - 32 * w) & ~below(b - 32 * w)) | below(pre - 32 * w);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!(bits & (1u << i))) x[32 * w + i] = -INFINITY;
+  }
+}
+
+#ifndef MOE_ATTN8_TC
 // ------------------------------------------------------------------ attention
 template <typename T, int ND, int FORM, bool BOTH>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -724,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int per_batch = 32 / ppb;
       uint32_t slot = 0, ph = 0, filled = 0, last_ph = 0, qph = 0;
       bool ok = true, q_used = false;
-      Pieces<ND, true> pieces{s, p.err};
+      Pieces<S, true> pieces{s, p.err};
       while (ok && pieces.next(g)) {
         const int* table = p.b.page_table + (long long)g.seq * p.b.table_stride;
         const int bi = lane / ppb, pi = lane - bi * ppb;
@@ -817,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t slot = 0, ph = 0, qph = 0, cph = 0;
         uint32_t pph[2] = {0, 0}, oph[2] = {0, 0};
         bool ok = true;
-        Pieces<ND, false> pieces{s, p.err};
+        Pieces<S, false> pieces{s, p.err};
         const auto wait_slot = [&]() { return bwait(&s.kv_full[slot], ph, p.err); };
         const auto advance = [&]() {
           if (++slot == S::kSlots) {
@@ -905,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the issuer has seen it arrive.
       uint32_t slot = 0, cph = 0;
       bool ok = true;
-      Pieces<ND, true> pieces{s, p.err};
+      Pieces<S, true> pieces{s, p.err};
       while (ok && pieces.next(g)) {
         for (int n = g.n0; n < g.end; ++n) {
           const uint32_t vslot = (slot + 1) % S::kSlots;
@@ -927,91 +1123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (lane == 0) {
-      // ---------------------------------------------------------------- the share, piece by piece
-      const Share& sh = s.share;
-      const int cta = blockIdx.x;
-      const bool chunk = kCut && cta < sh.cuts;  // a chunk of an item, and nothing else
-      long long at = sh.at, entry_at = sh.entry_at;
-      const long long hi = sh.hi;
-      int seq = sh.seq, index = sh.index, cut_at = sh.cut_at;
-      Entry e;
-      Seq r = sh.s;
-      // an item of the entry: its chunks; the units it has on the list, the first
-      // of which read nothing, and the block that the others begin with
-      int chunks = 0, listed = 0, fixed = 0, behind = 0;
-      int head = -1, i = 0;   // head -2: the sequence is to be read, -1: the entry made
-      uint32_t ph = 0;
-      bool ok = true;
-      while (ok) {
-        Piece o = {};
-        while (at < hi) {
-          if (head < 0) {
-            if (head == -2) r = sequence_of(p, seq);
-            if (index == entries_of(r, tpt)) {
-              ++seq;
-              index = 0;
-              head = -2;
-              continue;
-            }
-            e = entry_of(p, r, seq, index, tpt);
-            listed = units_of(e);
-            if (kCut && sh.cut) {
-              chunks = listed / (int)sh.per;
-              listed = rest_of(listed - chunks * (int)sh.per);
-              behind = max(0, chunks * (int)sh.per - kItemUnits);
-            }
-            fixed = listed - (e.blocks - behind);
-            head = chunk ? (cta - cut_at) / chunks
-                         : listed ? (int)quotient(at - entry_at, listed) : p.hk;
-          }
-          const long long item = entry_at + (long long)head * listed;
-          if (chunk) {
-            o.number = cta - cut_at - head * chunks;
-            o.n0 = max(0, o.number * (int)sh.per - kItemUnits);
-            o.end = (o.number + 1) * (int)sh.per - kItemUnits;
-            at = hi;
-          } else if (listed) {
-            const int u0 = (int)(at - item), u1 = (int)min((long long)listed, u0 + (hi - at));
-            at = item + u1;
-            o.n0 = behind + max(0, u0 - fixed);
-            o.end = behind + max(0, u1 - fixed);
-          }
-          if (o.end <= o.n0) o.end = 0;  // nothing to read: no piece
-          if (o.end) {
-            o.head = head;
-            o.first = e.first, o.ntok = e.ntok, o.p0 = e.p0, o.kv = e.kv;
-            o.near = e.near, o.skip = e.skip, o.blocks = e.blocks, o.prefix = e.prefix;
-            o.seq = e.seq;
-            o.cnt[0] = min(o.end, blocks_of_tile0(e, tpt)) - o.n0;
-            o.cnt[1] = e.ntok > tpt ? o.end - o.n0 : 0;
-            if (o.end - o.n0 < e.blocks) {
-              o.cta0 = sh.cuts + (int)quotient(item + fixed, sh.per);
-              const int last = sh.cuts + (int)quotient(item + listed - 1, sh.per);
-              o.pieces = chunks + (listed ? last - o.cta0 + 1 : 0);
-              o.chunks = chunks;
-              o.chunk0 = chunks ? cut_at + head * chunks : o.cta0;
-              if (!chunk) o.number = chunks + cta - o.cta0;
-            }
-          }
-          if (listed == 0 || at == item + listed) ++head;
-          if (head >= p.hk) {
-            head = -1;
-            ++index;
-            entry_at += (long long)listed * p.hk;
-            cut_at += chunks * p.hk;
-          }
-          if (o.end) break;
-        }
-        ok = bwait_piece(&s.piece_empty[i], ph ^ 1u, p.err);
-        if (!ok) break;
-        *reinterpret_cast<Piece*>(s.piece[i]) = o;
-        mbar_arrive(&s.piece_full[i]);
-        if (++i == kPieces) {
-          i = 0;
-          ph ^= 1u;
-        }
-        if (o.end == 0) break;  // the end of the share, told to all
-      }
+      walk_share<kCut>(p, s, tpt);
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -1025,10 +1137,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale2 = p.sc.scale * kLog2e;
     // scores are dot products until the exponent (plain), or log2 units (GEN)
     const float c = GEN ? 1.0f : scale2, raise = GEN ? kRaise<T> : kRaise<T> / c;
-    const float cap_in = p.sc.cap_in;
-    const float cap_out = p.sc.softcap * kLog2e;
     uint32_t sph = 0, oph = 0;
-    Pieces<ND, true> pieces{s, p.err};
+    Pieces<S, true> pieces{s, p.err};
     for (;;) {
       const Piece* held = pieces.hold();
       if (!group_all(t, held != nullptr)) break;  // the end of the share, or a timeout
@@ -1062,96 +1172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 8; ++i) loaded16(reinterpret_cast<uint32_t*>(x) + i * 16);
         // every row of the tile sees every key of the block, or not
         const bool whole = (kb + kBlk - 1 <= p_first && kb > lo_last) || kb + kBlk <= prefix;
-        if (GEN) {
-          if (p.sc.softcap > 0.0f) {
-            // cap tanh(y) in log2 units, y = x scale / cap. While every |y| of the
-            // warp's rows is below kTanhMax, it is y times a polynomial in y^2, two
-            // keys to an instruction; else as FORM has it. Rows and keys that do
-            // not exist have no part in the choice: the block with the last key takes
-            // the second form. (The powers of scale / cap do not go into the
-            // coefficients, which saves a product but lets the highest ones vanish
-            // where scale / cap is small: scores were 0.3 off at a cap of 2000.)
-            float top = fabsf(x[0]);
-#pragma unroll
-            for (int i = 1; i < kBlk - 1; i += 2) top = max3(top, fabsf(x[i]), fabsf(x[i + 1]));
-            top = fmaxf(top, fabsf(x[kBlk - 1]));
-            if (kb + kBlk <= kv &&
-                __all_sync(0xffffffffu, !mine || top * fabsf(cap_in) < kTanhMax)) {
-              const uint64_t in2 = pack2(cap_in, cap_in);
-              float f[kTanhTerms];
-#pragma unroll
-              for (int k = 0; k < kTanhTerms; ++k) f[k] = kTanh[k] * cap_out;
-#pragma unroll
-              for (int i = 0; i < kBlk / 2; ++i) {
-                const uint64_t y = mul2(pack2(x[2 * i], x[2 * i + 1]), in2);
-                const uint64_t t = mul2(y, y);
-                uint64_t r = pack2(f[kTanhTerms - 1], f[kTanhTerms - 1]);
-#pragma unroll
-                for (int k = kTanhTerms - 2; k >= 0; --k) r = fma2(r, t, pack2(f[k], f[k]));
-                unpack2(mul2(r, y), x[2 * i], x[2 * i + 1]);
-              }
-            } else if (FORM == kWide) {
-#pragma unroll
-              for (int i = 0; i < kBlk / 2; ++i) {
-                const uint64_t y = pack2(tanh_range(x[2 * i] * cap_in),
-                                         tanh_range(x[2 * i + 1] * cap_in));
-                const uint64_t t = mul2(y, y);
-                uint64_t a = pack2(kTanhP[4], kTanhP[4]), b = pack2(kTanhQ[4], kTanhQ[4]);
-#pragma unroll
-                for (int k = 3; k >= 0; --k) {
-                  a = fma2(a, t, pack2(kTanhP[k], kTanhP[k]));
-                  b = fma2(b, t, pack2(kTanhQ[k], kTanhQ[k]));
-                }
-                float b0, b1;
-                unpack2(b, b0, b1);
-                a = mul2(mul2(a, y), pack2(rcp(b0), rcp(b1)));
-                unpack2(mul2(a, pack2(cap_out, cap_out)), x[2 * i], x[2 * i + 1]);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < kBlk; ++i) {
-                const float e = ex2(x[i] * (2.0f * kLog2e * cap_in));
-                x[i] = fmaf(-2.0f * cap_out, rcp(1.0f + e), cap_out);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < kBlk / 2; ++i) {
-              const uint64_t r = mul2(pack2(x[2 * i], x[2 * i + 1]), pack2(scale2, scale2));
-              unpack2(r, x[2 * i], x[2 * i + 1]);
-            }
-          }
-          if (p.sc.slopes) {
-            // distances are whole numbers: exact steps of -1 from key to key, where
-            // fp32 holds them all and no key lies ahead of its query
-            const float far = (float)(pos - kb);
-            if (kb + kBlk - 1 <= p_first && p_first - kb < (1 << 24) - 128) {
-              uint64_t away = pack2(far, far - 1.0f);
-#pragma unroll
-              for (int i = 0; i < kBlk / 2; ++i) {
-                const uint64_t r =
-                    fma2(away, pack2(-slope, -slope), pack2(x[2 * i], x[2 * i + 1]));
-                unpack2(r, x[2 * i], x[2 * i + 1]);
-                away = add2(away, pack2(-2.0f, -2.0f));
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < kBlk; ++i) x[i] = fmaf(-slope, fabsf(far - (float)i), x[i]);
-            }
-          }
-        }
-        if (!whole) {
-          // bit i of word w: this row sees key kb + 32 w + i
-          const int a = pos - kb + 1, b = p.sc.window ? pos - p.sc.window - kb + 1 : 0;
-          const int pre = kept_of(p.sc, prefix, pos) - kb;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t bits = (below(a - 32 * w) & ~below(b - 32 * w)) | below(pre - 32 * w);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(bits & (1u << i))) x[32 * w + i] = -INFINITY;
-          }
-        }
+        if (GEN) general_scores<FORM>(p, x, scale2, kb, kv, mine, pos, p_first, slope);
+        if (!whole) mask_row(p, x, kb, prefix, pos);
         float mt[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
         for (int i = 4; i < kBlk - 4; i += 8)
@@ -1316,6 +1338,10 @@ cudaError_t launch_attn_tc(const AttnParams& p, const TcPieces& w, const CUtenso
   return dtype == MOE_ATTN_BF16 ? launch_t<Bf16>(p, w, qmap, kmap, vmap, grid, s)
                                 : launch_t<Fp16>(p, w, qmap, kmap, vmap, grid, s);
 }
+
+#else
+}  // namespace
+#endif  // MOE_ATTN8_TC
 
 }  // namespace attn
 }  // namespace moe
