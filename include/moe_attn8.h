@@ -142,10 +142,20 @@ int moe_attn_append8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
 int moe_attn_read8(moe_attn_handle* h, const moe_attn_cache8* cache, const moe_attn_extent* extent,
                    const moe_attn_rows* k_out, const moe_attn_rows* v_out, void* stream);
 
-/* moe_attn_forward over an 8-bit cache; sinks: see above (0: none). */
+/* Device bytes that moe_attn_forward8 works faster with: room for the batch's keys and
+ * values in 16 bits, as far as its page table goes, where its sequences have many new
+ * tokens (else, and where that were more than 8 GiB, 0). */
+int moe_attn_forward8_scratch_bytes(const moe_attn_handle* h, const moe_attn_batch* batch,
+                                    size_t* bytes);
+
+/* moe_attn_forward over an 8-bit cache; sinks: see above (0: none). scratch: as many
+ * bytes as above, 256-byte aligned, or NULL; it keeps nothing between calls. With it, the
+ * keys and values that queries see are brought to the handle's type first (exactly, where
+ * scales are powers of two and values in the type's range; fp16 has none above 65504). */
 int moe_attn_forward8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out,
                       float* lse, const moe_attn_cache8* cache, const moe_attn_batch* batch,
-                      const moe_attn_scores* scores, int32_t sinks, void* stream);
+                      const moe_attn_scores* scores, int32_t sinks, void* scratch,
+                      size_t scratch_bytes, void* stream);
 
 /* moe_attn_forward with sinks. */
 int moe_attn_forward_sinks(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out,

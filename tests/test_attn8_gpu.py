@@ -434,8 +434,10 @@ def test_forward8_blocks_of_different_scales(lens, dtype, gains):
     err = (out.cpu().double() - b.want).abs()
     # scores of sizes up to 2^3 of the plain ones': their fp32 error with them. A result
     # below fp16's normal range is rounded to 2^-25; one above its range is infinite
+    # numerators are fp16, or of the type where the keys are brought to 16 bits (560 rows)
     u = ac.ROUND[dtype]
-    bound = u * b.want.abs() + (2.0 ** -11 + 8e-4) * b.bound + 2.0 ** -24
+    numerator = u if lens[0][0] > 100 else 2.0 ** -11
+    bound = u * b.want.abs() + (numerator + 8e-4) * b.bound + 2.0 ** -24
     fits = b.want.abs() < 60000
     assert bool((err <= bound)[fits].all()), float((err / bound)[fits].max())
     assert bool(((lse.cpu().double() - b.want_lse).abs() <= 8e-4).all())

@@ -145,7 +145,8 @@ def test_null_handles_are_refused(L):
     assert L.moe_attn_append_norm(*[None] * 7, 0, None, None, None, None) == -1
     assert L.moe_attn_append8(*[None] * 7, 0, None, None, None, None) == -1
     assert L.moe_attn_read8(*[None] * 6) == -1
-    assert L.moe_attn_forward8(*[None] * 7, 0, None) == -1
+    assert L.moe_attn_forward8(*[None] * 7, 0, None, 0, None) == -1
+    assert L.moe_attn_forward8_scratch_bytes(None, None, None) == -1
     assert L.moe_attn_forward_sinks(*[None] * 7, 0, None) == -1
 
 

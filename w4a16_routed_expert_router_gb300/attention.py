@@ -44,6 +44,7 @@ EXPORTS_ATTN8 = (
     "moe_attn_append_norm",
     "moe_attn_append8",
     "moe_attn_read8",
+    "moe_attn_forward8_scratch_bytes",
     "moe_attn_forward8",
     "moe_attn_forward_sinks",
 )
@@ -148,7 +149,9 @@ def _signatures8():
         "moe_attn_append_norm": [*appended, p(moe_attn_cache), _vp],
         "moe_attn_append8": [*appended, cache, _vp],
         "moe_attn_read8": [_vp, cache, p(moe_attn_extent), rows, rows, _vp],
-        "moe_attn_forward8": [_vp, rows, rows, _vp, cache, batch, scores, _i32, _vp],
+        "moe_attn_forward8_scratch_bytes": [_vp, batch, p(ctypes.c_size_t)],
+        "moe_attn_forward8": [_vp, rows, rows, _vp, cache, batch, scores, _i32, _vp,
+                              ctypes.c_size_t, _vp],
         "moe_attn_forward_sinks": [_vp, rows, rows, _vp, p(moe_attn_cache), batch, scores, _i32,
                                    _vp],
     }
@@ -194,7 +197,8 @@ def _lib() -> ctypes.CDLL:
 
         functions = tuple(address(f"moe_attn_{name}") for name in (
             "rope", "append", "forward", "norm_rope", "norm_rope_backward_bytes",
-            "norm_rope_backward", "append_norm", "append8", "read8", "forward8", "forward_sinks"))
+            "norm_rope_backward", "append_norm", "append8", "read8", "forward8", "forward_sinks",
+            "forward8_scratch_bytes"))
         _attn_binding.setup(functions, _check, torch.empty, _raw_stream, _current_device,
                             torch.is_grad_enabled, torch.is_inference_mode_enabled,
                             _increment_version, torch.bfloat16, torch.float16, torch.float32,
@@ -488,7 +492,9 @@ class PagedAttention:
         cu_q int32 [seqs + 1]: first row of each sequence; kv_len int32 [seqs]:
         its keys, the new ones included; page_table int32 [seqs, columns]; max_q:
         no sequence has more new tokens. scale defaults to 1 / sqrt(head_dim).
-        sinks: first tokens of a sequence that a window does not hide.
+        sinks: first tokens of a sequence that a window does not hide. Over an 8-bit
+        cache, batches of many tokens bring the keys to 16 bits first, in memory that
+        torch hands out for the call (up to 8 GiB; not where `stream` is given).
         Returns out, or (out, lse) with lse fp32 [tokens, q_heads].
         """
         given = stream

@@ -5,8 +5,6 @@
 
 namespace {
 
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
-
 // Workspace carve-up; the order is the order of the fields filled in create().
 struct Layout {
   size_t off[7], sizes[7];
@@ -102,6 +100,23 @@ int encode_tc_cache(CUtensorMap* m, const moe_attn_config& c, const moe_attn_cac
 
 }  // namespace
 
+int moe::attn::forward_many(moe_attn_handle* h, AttnParams p, const moe_attn_rows* q,
+                            const moe_attn_cache* cache, cudaStream_t s) {
+  const moe_attn_config& c = h->cfg;
+  CUtensorMap qmap, kmap, vmap;
+  int st;
+  if (!h->tc_usable) {  // another compiler: few-token batches go on
+    fprintf(stderr, "moe_attn: the tensor-core kernel was built with other registers than it needs\n");
+    return MOE_ATTN_ERR_CUDA;
+  }
+  p.boxes = tc_boxes(c, cache);
+  if ((st = encode_tc_cache(&kmap, c, cache, cache->k, p.boxes)) != MOE_ATTN_OK ||
+      (st = encode_tc_cache(&vmap, c, cache, cache->v, p.boxes)) != MOE_ATTN_OK ||
+      (st = encode_q(&qmap, c, q, p.b.num_tokens)) != MOE_ATTN_OK)
+    return st;
+  return cuda_status(launch_attn_tc(p, h->tc, qmap, kmap, vmap, c.dtype, h->grid, s));
+}
+
 int moe::attn::forward_sinks(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out,
                              float* lse, const moe_attn_cache* cache, const moe_attn_batch* b,
                              const moe_attn_scores* sc, int sinks, void* stream) {
@@ -119,8 +134,8 @@ int moe::attn::forward_sinks(moe_attn_handle* h, const moe_attn_rows* q, const m
   // has few rows, else the tensor-core kernel, whose single tokens run beside the
   // chunks (16 sequences, 4 of them chunks, 104 us in two launches, 90 us so).
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  CUtensorMap qmap, kmap, vmap;
   if ((long long)b->max_q * p.group <= kDecodeRows) {
+    CUtensorMap kmap, vmap;
     const int block = decode_block(c.head_dim > 64 ? 2 : 1);
     const int box = c.page_size < block ? c.page_size : block;
     if ((st = encode_cache_chunks(&kmap, c, cache, cache->k, box)) != MOE_ATTN_OK ||
@@ -128,16 +143,7 @@ int moe::attn::forward_sinks(moe_attn_handle* h, const moe_attn_rows* q, const m
       return st;
     return cuda_status(launch_attn_decode(p, h->decode, kmap, vmap, c.dtype, h->grid, s));
   }
-  if (!h->tc_usable) {  // another compiler: few-token batches go on
-    fprintf(stderr, "moe_attn: the tensor-core kernel was built with other registers than it needs\n");
-    return MOE_ATTN_ERR_CUDA;
-  }
-  p.boxes = tc_boxes(c, cache);
-  if ((st = encode_tc_cache(&kmap, c, cache, cache->k, p.boxes)) != MOE_ATTN_OK ||
-      (st = encode_tc_cache(&vmap, c, cache, cache->v, p.boxes)) != MOE_ATTN_OK ||
-      (st = encode_q(&qmap, c, q, b->num_tokens)) != MOE_ATTN_OK)
-    return st;
-  return cuda_status(launch_attn_tc(p, h->tc, qmap, kmap, vmap, c.dtype, h->grid, s));
+  return forward_many(h, p, q, cache, s);
 }
 
 extern "C" {

@@ -289,6 +289,19 @@ cudaError_t launch_attn_tc(const AttnParams& p, const TcPieces& w, const CUtenso
                            cudaStream_t s);
 
 // ------------------------------------------------------------------ 8-bit attention
+// The keys of a batch out of an 8-bit cache as 16-bit pages [pages, heads, page, dim], the
+// pages of one sequence behind those of the one before, and the batch's table of them.
+struct Expand8Params {
+  Cache8 c;
+  Batch b;
+  Scores sc;
+  uint16_t *k, *v;
+  int* table;                 // [num_seqs, columns]
+  int hk, head_dim, page_shift;
+  unsigned* err;
+};
+cudaError_t launch_expand8(const Expand8Params& p, int dtype, int grid, cudaStream_t s);
+
 struct Attn8Params {
   AttnParams a;
   Cache8 c;

@@ -120,6 +120,31 @@ int make_ready(moe_attn_handle* h) {
   return st;
 }
 
+// Keys and values of a batch in 16 bits, and the page table of them: K, V, table.
+struct Scratch {
+  size_t half, table, total;
+};
+Scratch scratch_of(const moe_attn_config& c, const moe_attn_batch* b) {
+  const size_t pages = (size_t)b->num_seqs * b->columns;
+  Scratch s;
+  s.half = align256(pages * c.kv_heads * c.page_size * c.head_dim * 2);
+  s.table = 2 * s.half;
+  s.total = s.table + align256(pages * 4);
+  return s;
+}
+// Batches of many tokens are worth it: the kernel over 16 bits takes 1.5 us for 256 query
+// rows by 128 keys on an SM, the one over codes 2.8, and 128 keys of a head take 16 ns
+// (all SMs) to bring to 16 bits, so about 500 rows a sequence and kv head pay for it.
+// (400 rows over 32768 keys 108 us over codes, 104 so; 4000 over 65536 1189 and 700.)
+constexpr long long kExpandRows = 512;
+constexpr size_t kScratchMost = size_t(8) << 30;
+bool expands(const moe_attn_config& c, const moe_attn_batch* b) {
+  const long long group = c.q_heads / c.kv_heads;
+  return (long long)b->max_q * group > kDecodeRows &&
+         b->num_tokens * group >= kExpandRows * b->num_seqs &&
+         (long long)b->num_seqs * b->columns <= 0x7ffffffeLL && scratch_of(c, b).total <= kScratchMost;
+}
+
 // What moe_attn_append_norm and moe_attn_append8 have in common.
 int check_append(const moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* q_out,
                  int32_t T, const moe_attn_rotation* r, const moe_attn_norm* norm) {
@@ -351,9 +376,19 @@ int moe_attn_read8(moe_attn_handle* h, const moe_attn_cache8* cache, const moe_a
   return cuda_status(launch_read8(p, c.dtype, static_cast<cudaStream_t>(stream)));
 }
 
+int moe_attn_forward8_scratch_bytes(const moe_attn_handle* h, const moe_attn_batch* b,
+                                    size_t* bytes) {
+  if (!h || !b || !bytes) return MOE_ATTN_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (b->num_tokens > 0 && b->num_seqs > 0 && b->columns > 0 && expands(h->cfg, b))
+    *bytes = scratch_of(h->cfg, b).total;
+  return MOE_ATTN_OK;
+}
+
 int moe_attn_forward8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out,
                       float* lse, const moe_attn_cache8* cache, const moe_attn_batch* b,
-                      const moe_attn_scores* sc, int32_t sinks, void* stream) {
+                      const moe_attn_scores* sc, int32_t sinks, void* scratch,
+                      size_t scratch_bytes, void* stream) {
   int st = check_call(h, b, sc, sinks);
   if (st != MOE_ATTN_OK) return st;
   const moe_attn_config& c = h->cfg;
@@ -366,8 +401,33 @@ int moe_attn_forward8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn
   p.a = params_of(h, q, out, lse, cache->num_pages, b, sc, sinks);
   p.c = cache_of(cache);
   p.dtype = c.dtype;
-  if ((st = make_ready(h)) != MOE_ATTN_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (scratch && expands(c, b) && h->tc_usable) {
+    const Scratch room = scratch_of(c, b);
+    if (scratch_bytes < room.total) return MOE_ATTN_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(scratch) & 255u) return MOE_ATTN_ERR_MISALIGNED;
+    uint8_t* at = static_cast<uint8_t*>(scratch);
+    Expand8Params e{};
+    e.c = p.c;
+    e.b = p.a.b;
+    e.sc = p.a.sc;
+    e.k = reinterpret_cast<uint16_t*>(at);
+    e.v = reinterpret_cast<uint16_t*>(at + room.half);
+    e.table = reinterpret_cast<int*>(at + room.table);
+    e.hk = c.kv_heads;
+    e.head_dim = c.head_dim;
+    e.page_shift = p.a.page_shift;
+    e.err = h->err;
+    if ((st = cuda_status(launch_expand8(e, c.dtype, h->grid, s))) != MOE_ATTN_OK) return st;
+    const int64_t row = c.head_dim, head = row * c.page_size;
+    const moe_attn_cache wide = {e.k, e.v, (int64_t)b->num_seqs * b->columns, head * c.kv_heads,
+                                 row, head};
+    p.a.num_pages = wide.num_pages;
+    p.a.b.page_table = e.table;
+    p.a.b.table_stride = b->columns;
+    return forward_many(h, p.a, q, &wide, s);
+  }
+  if ((st = make_ready(h)) != MOE_ATTN_OK) return st;
   // as in moe_attn_forward: one kernel for the whole batch
   CUtensorMap qmap, kmap, vmap;
   const bool few = (long long)b->max_q * p.a.group <= kDecodeRows;

@@ -196,6 +196,8 @@ inline int log2i(int v) {
   return n;
 }
 
+inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
 inline int encode(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims,
            const cuuint64_t* strides, const cuuint32_t* box,
            CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT16,
@@ -291,6 +293,10 @@ inline AttnParams params_of(const moe_attn_handle* h, const moe_attn_rows* q,
   p.err = h->err;
   return p;
 }
+
+// the tensor-core kernel over a 16-bit cache
+int forward_many(moe_attn_handle* h, AttnParams p, const moe_attn_rows* q,
+                 const moe_attn_cache* cache, cudaStream_t s);
 
 // moe_attn_forward with first tokens that stay visible behind a window
 int forward_sinks(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out, float* lse,

@@ -41,7 +41,8 @@ typedef int (*read8_fn)(moe_attn_handle*, const moe_attn_cache8*, const moe_attn
                         const moe_attn_rows*, const moe_attn_rows*, void*);
 typedef int (*forward8_fn)(moe_attn_handle*, const moe_attn_rows*, const moe_attn_rows*, float*,
                            const moe_attn_cache8*, const moe_attn_batch*, const moe_attn_scores*,
-                           int32_t, void*);
+                           int32_t, void*, size_t, void*);
+typedef int (*scratch_fn)(const moe_attn_handle*, const moe_attn_batch*, size_t*);
 typedef int (*forward_sinks_fn)(moe_attn_handle*, const moe_attn_rows*, const moe_attn_rows*,
                                 float*, const moe_attn_cache*, const moe_attn_batch*,
                                 const moe_attn_scores*, int32_t, void*);
@@ -58,6 +59,7 @@ static struct {
   read8_fn read8;
   forward8_fn forward8;
   forward_sinks_fn forward_sinks;
+  scratch_fn scratch;
   PyObject *check;                       /* (status, what): raises */
   PyObject *empty, *raw_stream, *current_device;
   PyObject *grad_enabled, *inference_enabled; /* of the thread */
@@ -708,15 +710,31 @@ static PyObject* forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     Py_DECREF(lse);
     return NULL;
   }
+  /* room for keys in 16 bits: torch's memory of the current stream */
+  size_t bytes = 0;
+  void* room = NULL;
+  PyObject* scratch = NULL;
+  if (bits8 && a[19] == Py_None) {
+    if (checked(G.scratch(l->handle, &b, &bytes), "moe_attn_forward8_scratch_bytes") ||
+        (bytes && (!(scratch = new_tensor(Py_BuildValue("(L)", (long long)(bytes / 4)), G.f32,
+                                          l->device)) ||
+                   pointer_of(scratch, &room)))) {
+      Py_XDECREF(scratch);
+      Py_DECREF(out);
+      Py_DECREF(lse);
+      return NULL;
+    }
+  }
   int status;
   Py_BEGIN_ALLOW_THREADS;
   if (bits8)
-    status = G.forward8(l->handle, &q, &o, lse_at, &c8, &b, &s, sinks, stream);
+    status = G.forward8(l->handle, &q, &o, lse_at, &c8, &b, &s, sinks, room, bytes, stream);
   else if (sinks)
     status = G.forward_sinks(l->handle, &q, &o, lse_at, &c, &b, &s, sinks, stream);
   else
     status = G.forward(l->handle, &q, &o, lse_at, &c, &b, &s, stream);
   Py_END_ALLOW_THREADS;
+  Py_XDECREF(scratch);
   PyObject* result = NULL;
   if (!checked(status, bits8 ? "moe_attn_forward8" : "moe_attn_forward") && !wrote(tracked + 4, 2))
     result = with_lse ? PyTuple_Pack(2, out, lse) : Py_NewRef(out);
@@ -950,9 +968,9 @@ done:
 static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   if (arity(n, 14, "setup")) return NULL;
-  void* f[11];
-  if (!PyTuple_Check(a[0]) || arity(PyTuple_GET_SIZE(a[0]), 11, "addresses")) return NULL;
-  for (int i = 0; i < 11; ++i) f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[0], i));
+  void* f[12];
+  if (!PyTuple_Check(a[0]) || arity(PyTuple_GET_SIZE(a[0]), 12, "addresses")) return NULL;
+  for (int i = 0; i < 12; ++i) f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[0], i));
   if (PyErr_Occurred()) return NULL;
   G.rope = (rope_fn)f[0];
   G.append = (append_fn)f[1];
@@ -965,6 +983,7 @@ static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   G.read8 = (read8_fn)f[8];
   G.forward8 = (forward8_fn)f[9];
   G.forward_sinks = (forward_sinks_fn)f[10];
+  G.scratch = (scratch_fn)f[11];
   PyObject** to[] = {&G.check,        &G.empty,             &G.raw_stream,
                      &G.current_device, &G.grad_enabled,    &G.inference_enabled,
                      &G.increment_version, &G.bf16,         &G.fp16,

@@ -634,6 +634,104 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const Read8Params p, in
   }
 }
 
+// ------------------------------------------------------------------ a batch's keys in 16 bits
+// Persistent CTAs over the pages of all sequences, dealt out in turn: every CTA adds up
+// the sequences' pages for itself, keeps the first page of each while they are few, and
+// finds a page's sequence by bisection. Blocks of kTcBlock keys that no query sees are
+// passed over. Bound by memory.
+constexpr int kFirstKept = 2048;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) expand8_kernel(const Expand8Params p) {
+  __shared__ int first[kFirstKept + 1];
+  __shared__ int sums[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, seqs = p.b.num_seqs;
+  const int page_rows = 1 << p.page_shift, chunks = p.head_dim >> 4;
+  wait_prior_launch();
+  let_next_launch();
+  // Pages of sequence s. (A sequence whose lengths leave their ranges has none.)
+  const auto pages_of = [&](int s) {
+    const Span r = read_sequence(p.b, p.page_shift, s, p.err);
+    return r.n > 0 ? (r.kv + page_rows - 1) >> p.page_shift : 0;
+  };
+  int base = 0;                                        // pages before sequence s0
+  for (int s0 = 0; s0 < seqs; s0 += kFirstKept) {
+    const int n = min(kFirstKept, seqs - s0);
+    const int per = (n + kThreads - 1) / kThreads;
+    const int a = min(n, tid * per), b = min(n, a + per);
+    int mine = 0;
+    for (int i = a; i < b; ++i) mine += pages_of(s0 + i);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int at = base + incl - mine, total = base;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) at += sums[i];
+      total += sums[i];
+    }
+    for (int i = a; i < b; ++i) {
+      first[i] = at;
+      at += pages_of(s0 + i);
+    }
+    if (tid == 0) first[n] = total;
+    __syncthreads();
+    // this CTA's pages of [base, total)
+    int i = base + (int)((blockIdx.x + gridDim.x - base % gridDim.x) % gridDim.x);
+    int lo = 0;
+    for (; i < total; i += gridDim.x) {
+      int hi = n - 1;                                  // last sequence with first <= i
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= i)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int seq = s0 + lo, column = i - first[lo], key0 = column << p.page_shift;
+      if (tid == 0) p.table[(long long)seq * p.b.columns + column] = i;
+      const int kv = p.b.kv_len[seq], n_new = p.b.cu_q[seq + 1] - p.b.cu_q[seq];
+      const int kept = kept_of(p.sc, prefix_of(p.sc, seq, kv), kv - 1);
+      const int from = p.sc.window ? max(0, kv - n_new - p.sc.window + 1) : 0;
+      if (key0 + page_rows <= from / kTcBlock * kTcBlock &&
+          key0 >= (kept + kTcBlock - 1) / kTcBlock * kTcBlock)
+        continue;
+      const int page = p.b.page_table[seq * p.b.table_stride + column];
+      const bool bad = page < 0 || page >= p.c.num_pages;
+      if (bad && tid == 0) atomicOr(p.err, kErrRange);
+      const int rows = min(page_rows, kv - key0), row_chunks = page_rows * chunks;
+      const long long out = (long long)i * p.hk * page_rows * p.head_dim;
+#pragma unroll 2
+      for (int e = tid; e < p.hk * row_chunks; e += kThreads) {
+        const int h = e / row_chunks, rest = e - h * row_chunks;
+        const int r = rest / chunks, c = rest - r * chunks;
+        if (r >= rows) continue;
+        uint16_t* k = p.k + out + (long long)e * 16;
+        uint16_t* v = p.v + out + (long long)e * 16;
+        if (bad) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            reinterpret_cast<uint4*>(k)[q] = reinterpret_cast<uint4*>(v)[q] = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        const long long from_code = page * p.c.page + h * p.c.head + r * p.c.token + c * 16;
+        const long long from_scale =
+            page * p.c.scale_page + h * p.c.scale_head + r / kScaleBlock * p.c.scale_block;
+        const float ks = __ldg(p.c.k_scales + from_scale), vs = __ldg(p.c.v_scales + from_scale);
+        read16<T>(p.c.k + from_code, ks, k, true);
+        read16<T>(p.c.v + from_code, vs, v, true);
+      }
+    }
+    base = total;
+    __syncthreads();
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_append8(const Append8Params& g, int dtype, cudaStream_t s) {
@@ -651,6 +749,12 @@ cudaError_t launch_read8(const Read8Params& p, int dtype, cudaStream_t s) {
   const int wide = rows_aligned(p.k_out) && rows_aligned(p.v_out);
   return dtype == MOE_ATTN_BF16 ? launch_after(read8_kernel<Bf16>, grid, block, 0, s, p, wide)
                                 : launch_after(read8_kernel<Fp16>, grid, block, 0, s, p, wide);
+}
+
+cudaError_t launch_expand8(const Expand8Params& p, int dtype, int grid, cudaStream_t s) {
+  const dim3 ctas(4 * grid), block(kThreads);
+  return dtype == MOE_ATTN_BF16 ? launch_after(expand8_kernel<Bf16>, ctas, block, 0, s, p)
+                                : launch_after(expand8_kernel<Fp16>, ctas, block, 0, s, p);
 }
 
 }  // namespace attn
