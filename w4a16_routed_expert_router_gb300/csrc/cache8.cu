@@ -1,14 +1,14 @@
 // Writing keys and values to the 8-bit cache, and reading them back.
 //
 // Append. Tokens of one block (16 rows of a page) follow each other in a call, so a
-// block's new tokens are a run of at most 16 consecutive tokens. A warp has one run
-// and one kv head, of K or of V: it reads the run's rows, raises the block's scale to
-// the power of two that their largest value needs, writes their codes, and where the
-// scale has grown re-expresses the codes of the block's other rows. A CTA looks at a
+// block's new tokens are a run of at most 16 consecutive tokens. Two warps have one run
+// and one kv head, of K or of V, 8 rows each: they read the rows, raise the block's scale
+// to the power of two that their largest value needs, write their codes, and where the
+// scale has grown re-express the codes of the block's other rows. A CTA looks at a
 // window of 16 tokens for the runs that begin there (one, in a prompt; up to 16, in a
 // decode step, which `split` CTAs share), so nothing is planned on the host. Keys are
-// normed and turned on the way, twice (for the largest value and for the codes)
-// rather than kept. Queries are normed and turned by CTAs of the same launch.
+// normed and turned on the way, and kept in registers between the largest value and the
+// codes. Queries are normed and turned by CTAs of the same launch.
 // Bound by memory.
 #include "norm_parts.cuh"
 
@@ -64,187 +64,183 @@ struct Divide {
 
 // ------------------------------------------------------------------ append
 struct Dims {  // of a launch
-  int q_ctas, token_groups;           // CTAs of the queries; along the tokens
+  int kv_ctas, token_groups;          // CTAs of keys and values; of queries along the tokens
   int q_heads, q_z, q_tokens;         // heads of one, tokens side by side, tokens of a thread
   int q_rows;                         // groups of heads
-  int split, combos;                  // CTAs that share a window's runs; of 8 (half, head)s
+  int split, combos;                  // CTAs that share a window's runs; of 4 (half, head)s
   int units, turned, lanes;
 };
 
-// A row's values in a lane, in either form: `a` and `b` chunks, or up to 4 single
-// values (head sizes up to 128).
-// (STEPS: how often a warp goes on until it has 16 rows; 0: a row at a time, any form.)
-template <typename T, bool IL, int STEPS>
-struct RowOf {
-  static constexpr int kSteps = STEPS;
+// A warp's rows of a run, in either form: in a lane, of each of its kSteps rows kValues
+// values (chunks `a` and `b`, or single values).
+constexpr int kWarpRows = kRun / 2;
+
+template <typename T, bool IL, bool FAST>
+struct RowsOf;
+
+template <typename T, bool IL>
+struct RowsOf<T, IL, true> {
+  // 16 lanes a row with interleaved pairs (8 or fewer otherwise): 2 rows (4) at a time
+  static constexpr int kSteps = IL ? 4 : 2, kValues = IL ? 8 : 16;
   Lane<IL> lane;
   int lanes, group, rows;
   bool active;
-  struct Raw {
-    Chunk8 a, b;
-  };
-  __device__ __forceinline__ RowOf(const Dims& d, int rot)
+  float w[kValues];
+  float v[kSteps][kValues];
+  __device__ __forceinline__ RowsOf(const Dims& d, const RopeParams& r, float*)
       : lane((threadIdx.x & (d.lanes - 1)) < d.units ? threadIdx.x & (d.lanes - 1) : 0, d.turned,
-             rot),
+             r.r.rot, r.head_dim),
         lanes(d.lanes),
         group((threadIdx.x & 31) / d.lanes),
         rows(32 / d.lanes),
         active((int)(threadIdx.x & (d.lanes - 1)) < d.units) {}
-  __device__ __forceinline__ int steps() const { return (kRun + rows - 1) / rows; }
-  __device__ __forceinline__ void load(const uint16_t* row, bool on, Raw& raw) const {
-    raw.a.v = raw.b.v = make_uint4(0, 0, 0, 0);
-    if (on && active) {
-      raw.a.v = *reinterpret_cast<const uint4*>(row + lane.at);
-      if (lane.two) raw.b.v = *reinterpret_cast<const uint4*>(row + lane.at + lane.gap);
-    }
-  }
-  struct Weights {
-    float a[8], b[8];
-  };
-  __device__ __forceinline__ void weights(const Norm& n, int h, Weights& w) const {
-    lane.template weights<T>(n.k_weight, h * n.k_head, n.wide, n.offset, w.a, w.b);
-  }
-  __device__ __forceinline__ float squares(const Raw& raw) const {
-    float fa[8], fb[8], s = 0.0f;
-    unpack8<T>(raw.a, fa);
-    unpack8<T>(raw.b, fb);
+  // rows [0, n) from `first` on, `stride` apart, without norm and rotation
+  __device__ __forceinline__ void load(const uint16_t* first, long long stride, int n) {
+    Chunk8 a[kSteps], b[kSteps];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s = fmaf(fa[k], fa[k], fmaf(fb[k], fb[k], s));
-    return s;
-  }
-  // f: the norm's factor; weights null: neither norm nor weight
-  template <bool KEY>
-  __device__ __forceinline__ void values(const Raw& raw, float f, const Weights* w,
-                                         const float* cosines, const float* sines, float* fa,
-                                         float* fb) const {
-    unpack8<T>(raw.a, fa);
-    unpack8<T>(raw.b, fb);
-    if (!KEY) return;
-    if (w) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        fa[k] = fa[k] * f * w->a[k];
-        if (lane.two) fb[k] = fb[k] * f * w->b[k];
+    for (int i = 0; i < kSteps; ++i) {
+      const int k = i * rows + group;
+      a[i].v = b[i].v = make_uint4(0, 0, 0, 0);
+      if (active && k < n) {
+        a[i].v = *reinterpret_cast<const uint4*>(first + k * stride + lane.at);
+        if (lane.two) b[i].v = *reinterpret_cast<const uint4*>(first + k * stride + lane.at + lane.gap);
       }
     }
-    if (lane.turns) lane.turn(fa, fb, cosines, sines);
-  }
-  template <bool KEY>
-  __device__ __forceinline__ float top(const Raw& raw, float f, const Weights* w,
-                                       const float* cosines, const float* sines) const {
-    float fa[8], fb[8], m = 0.0f;
-    values<KEY>(raw, f, w, cosines, sines, fa, fb);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = fmaxf(m, size_of(fa[k]));
-    if (lane.two) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) m = fmaxf(m, size_of(fb[k]));
+    for (int i = 0; i < kSteps; ++i) {
+      unpack8<T>(a[i], v[i]);
+      if (!IL) unpack8<T>(b[i], v[i] + (IL ? 0 : 8));
     }
-    return active ? m : 0.0f;
+  }
+  __device__ __forceinline__ void norm(const Norm& n, int h, float mean) {
+    float sum[kSteps];
+    lane.template weights<T>(n.k_weight, h * n.k_head, n.wide, n.offset, w, w + (IL ? 0 : 8));
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      sum[i] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kValues; ++k) sum[i] = fmaf(v[i][k], v[i][k], sum[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) sum[i] = group_sum(sum[i], lanes);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const float f = rsqrtf(fmaf(sum[i], mean, n.eps));
+#pragma unroll
+      for (int k = 0; k < kValues; ++k)
+        if (k < 8 || lane.two) v[i][k] = v[i][k] * f * w[k];
+    }
+  }
+  __device__ __forceinline__ void turn(const RopeParams& r, const float* cosines,
+                                       const float* sines, int, int n) {
+    const int pairs = r.r.rot >> 1;
+    if (!lane.turns) return;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int k = min(i * rows + group, n - 1);
+      lane.turn(v[i], v[i] + (IL ? 0 : 8), cosines + k * pairs, sines + k * pairs);
+    }
+  }
+  __device__ __forceinline__ float top() const {
+    float m = 0.0f;
+    if (active) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int k = 0; k < kValues; ++k)
+          if (k < 8 || lane.two) m = fmaxf(m, size_of(v[i][k]));
+    }
+    return m;
   }
   static __device__ __forceinline__ uint2 codes(const float* f, const Divide& by) {
-    uint32_t w[2];
+    uint32_t c[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      w[i] = to_codes(by(f[4 * i]), by(f[4 * i + 1])) |
+      c[i] = to_codes(by(f[4 * i]), by(f[4 * i + 1])) |
              (uint32_t)to_codes(by(f[4 * i + 2]), by(f[4 * i + 3])) << 16;
-    return make_uint2(w[0], w[1]);
+    return make_uint2(c[0], c[1]);
   }
-  template <bool KEY>
-  __device__ __forceinline__ void store(const Raw& raw, float f, const Weights* w,
-                                        const float* cosines, const float* sines, const Divide& by,
-                                        uint8_t* row) const {
-    float fa[8], fb[8];
-    values<KEY>(raw, f, w, cosines, sines, fa, fb);
-    if (!active) return;
-    *reinterpret_cast<uint2*>(row + lane.at) = codes(fa, by);
-    if (lane.two) *reinterpret_cast<uint2*>(row + lane.at + lane.gap) = codes(fb, by);
+  // at(k): where row k goes
+  template <class At>
+  __device__ __forceinline__ void store(const Divide& by, int n, const At& at) const {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int k = i * rows + group;
+      if (!active || k >= n) continue;
+      uint8_t* row = at(k) + lane.at;
+      *reinterpret_cast<uint2*>(row) = codes(v[i], by);
+      if (lane.two) *reinterpret_cast<uint2*>(row + lane.gap) = codes(v[i] + (IL ? 0 : 8), by);
+    }
   }
 };
 
 template <typename T>
-struct RowOf<T, false, 0> {
-  static constexpr int kSteps = kRun, kLane = 4;
-  const Append8Params& g;
-  float* row_smem;
-  int lanes = 32, group = 0, rows = 1;
-  bool active = true;
+struct RowsOf<T, false, false> {
+  static constexpr int kLane = 4;
   int dim;
-  struct Raw {
-    uint16_t x[kLane];
-  };
-  struct Weights {
-    float w[kLane];
-  };
-  __device__ __forceinline__ RowOf(const Append8Params& p, float* smem)
-      : g(p), row_smem(smem + (threadIdx.x >> 5) * 128), dim(p.p.r.head_dim) {}
-  __device__ __forceinline__ int steps() const { return kRun; }
-  __device__ __forceinline__ void load(const uint16_t* row, bool on, Raw& raw) const {
+  float* row;
+  float v[kWarpRows][kLane];
+  __device__ __forceinline__ RowsOf(const Dims&, const RopeParams& r, float* smem)
+      : dim(r.head_dim), row(smem + (threadIdx.x >> 5) * 128) {}
+  __device__ __forceinline__ int index(int k) const { return (threadIdx.x & 31) + 32 * k; }
+  __device__ __forceinline__ void load(const uint16_t* first, long long stride, int n) {
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) {
-      const int i = (threadIdx.x & 31) + 32 * k;
-      raw.x[k] = on && i < dim ? row[i] : (uint16_t)0;
+    for (int i = 0; i < kWarpRows; ++i)
+#pragma unroll
+      for (int k = 0; k < kLane; ++k)
+        v[i][k] = i < n && index(k) < dim ? T::to_f32(first[i * stride + index(k)]) : 0.0f;
+  }
+  __device__ __forceinline__ void norm(const Norm& n, int h, float mean) {
+#pragma unroll
+    for (int i = 0; i < kWarpRows; ++i) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kLane; ++k) sum = fmaf(v[i][k], v[i][k], sum);
+      const float f = rsqrtf(fmaf(group_sum(sum, 32), mean, n.eps));
+#pragma unroll
+      for (int k = 0; k < kLane; ++k)
+        if (index(k) < dim)
+          v[i][k] *= f * weight_any<T>(n.k_weight, h * n.k_head + index(k), n.wide, n.offset);
     }
   }
-  __device__ __forceinline__ void weights(const Norm& n, int h, Weights& w) const {
+  __device__ __forceinline__ void turn(const RopeParams& r, const float*, const float*, int t0,
+                                       int n) {
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) {
-      const int i = (threadIdx.x & 31) + 32 * k;
-      w.w[k] = i < dim ? weight_any<T>(n.k_weight, h * n.k_head + i, n.wide, n.offset) : 0.0f;
+    for (int i = 0; i < kWarpRows; ++i) {
+      if (i >= n) break;
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kLane; ++k) row[index(k)] = v[i][k];
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kLane; ++k)
+        if (index(k) < dim) v[i][k] = turned_any(r.r, r.positions[t0 + i], row, index(k));
     }
   }
-  __device__ __forceinline__ float squares(const Raw& raw) const {
-    float s = 0.0f;
+  __device__ __forceinline__ float top() const {
+    float m = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) s = fmaf(T::to_f32(raw.x[k]), T::to_f32(raw.x[k]), s);
-    return s;
-  }
-  template <bool KEY>
-  __device__ __forceinline__ void values(const Raw& raw, float f, const Weights* w, int position,
-                                         float* v) const {
-    if (KEY) __syncwarp();
+    for (int i = 0; i < kWarpRows; ++i)
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) {
-      const int i = (threadIdx.x & 31) + 32 * k;
-      v[k] = T::to_f32(raw.x[k]);
-      if (KEY && w) v[k] = v[k] * f * w->w[k];
-      if (KEY) row_smem[i] = v[k];
-    }
-    if (!KEY) return;
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < kLane; ++k) {
-      const int i = (threadIdx.x & 31) + 32 * k;
-      v[k] = i < dim ? turned_any(g.p.r.r, position, row_smem, i) : 0.0f;
-    }
-  }
-  template <bool KEY>
-  __device__ __forceinline__ float top(const Raw& raw, float f, const Weights* w,
-                                       int position) const {
-    float v[kLane], m = 0.0f;
-    values<KEY>(raw, f, w, position, v);
-#pragma unroll
-    for (int k = 0; k < kLane; ++k) m = fmaxf(m, size_of(v[k]));
+      for (int k = 0; k < kLane; ++k) m = fmaxf(m, size_of(v[i][k]));
     return m;
   }
-  template <bool KEY>
-  __device__ __forceinline__ void store(const Raw& raw, float f, const Weights* w, int position,
-                                        const Divide& by, uint8_t* row) const {
-    float v[kLane];
-    values<KEY>(raw, f, w, position, v);
+  template <class At>
+  __device__ __forceinline__ void store(const Divide& by, int n, const At& at) const {
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) {
-      const int i = (threadIdx.x & 31) + 32 * k;
-      if (i < dim) row[i] = (uint8_t)to_codes(by(v[k]), 0.0f);
-    }
+    for (int i = 0; i < kWarpRows; ++i)
+#pragma unroll
+      for (int k = 0; k < kLane; ++k)
+        if (i < n && index(k) < dim) at(i)[index(k)] = (uint8_t)to_codes(by(v[i][k]), 0.0f);
   }
 };
 
-// Codes of a block's rows that are not in `written` (a bit a row), by a new scale.
+// Codes of a block's rows that are not in `written` (a bit a row), by a new scale; two
+// warps, `sub` of them.
 __device__ __forceinline__ void reexpress(uint8_t* block, long long token, int dim,
-                                          unsigned written, float ratio) {
-  const int lane = threadIdx.x & 31, chunks = dim >> 4;
-  for (int i = lane; i < kScaleBlock * chunks; i += 32) {
+                                          unsigned written, float ratio, int sub) {
+  const int chunks = dim >> 4;
+  for (int i = (threadIdx.x & 31) + 32 * sub; i < kScaleBlock * chunks; i += 64) {
     const int r = i / chunks, c = i - r * chunks;
     if (written >> r & 1) continue;
     uint4* at = reinterpret_cast<uint4*>(block + r * token + c * 16);
@@ -260,95 +256,20 @@ __device__ __forceinline__ void reexpress(uint8_t* block, long long token, int d
   }
 }
 
-// One warp: the run [t0, t0 + n) into its block, of K (KEY) or V, kv head h.
-template <typename T, bool IL, int STEPS, bool KEY>
-__device__ __forceinline__ void append_run(const Append8Params& g, const RowOf<T, IL, STEPS>& of,
-                                           int t0, int n, int h, const float* cosines,
-                                           const float* sines) {
-  typedef RowOf<T, IL, STEPS> R;
-  const RopeParams& r = g.p.r;
-  const Rows& in = KEY ? r.k : r.v;
-  const long long slot = r.slots[t0], page = slot >> r.page_shift;
-  const int in_page = (int)(slot - (page << r.page_shift));
-  const int first = in_page & (kScaleBlock - 1), block = in_page / kScaleBlock;
-  uint8_t* codes = (KEY ? g.c.k : g.c.v) + page * g.c.page + (long long)h * g.c.head +
-                   (long long)(in_page - first) * g.c.token;
-  float* scale_at = (KEY ? g.c.k_scales : g.c.v_scales) + page * g.c.scale_page +
-                    h * g.c.scale_head + block * g.c.scale_block;
-  const float before = first ? *scale_at : 0.0f;
-  typename R::Raw raw[R::kSteps];
-  const int steps = min(of.steps(), (n + of.rows - 1) / of.rows);
-#pragma unroll
-  for (int i = 0; i < R::kSteps; ++i)
-    if (i < steps) {
-      const int k = i * of.rows + of.group;
-      of.load(in.p + (long long)(t0 + min(k, n - 1)) * in.token + (long long)h * in.head, k < n,
-              raw[i]);
-    }
-  typename R::Weights w;
-  const typename R::Weights* wp = nullptr;
-  float f[R::kSteps], top = 0.0f;
-  if (KEY && g.p.n.on) {
-    of.weights(g.p.n, h, w);
-    wp = &w;
-  }
-  const int pairs = r.r.rot >> 1;
-#pragma unroll
-  for (int i = 0; i < R::kSteps; ++i)
-    if (i < steps) {
-      const int k = min(i * of.rows + of.group, n - 1);
-      f[i] = 1.0f;
-      if (wp)
-        f[i] = rsqrtf(fmaf(group_sum(of.squares(raw[i]), of.lanes), 1.0f / (float)r.head_dim,
-                           g.p.n.eps));
-      float m;
-      if constexpr (STEPS > 0)
-        m = of.template top<KEY>(raw[i], f[i], wp, cosines + k * pairs, sines + k * pairs);
-      else
-        m = of.template top<KEY>(raw[i], f[i], wp, KEY ? r.positions[t0 + k] : 0);
-      top = fmaxf(top, m);
-    }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float scale = scale_for(top);
-  unsigned written = 0;  // rows of the block that the run has
-  for (int k = 0; k < n; ++k) written |= 1u << ((int)(r.slots[t0 + k] - slot) + first);
-  if (first && before > 0.0f && before < INFINITY) {
-    if (before >= scale)
-      scale = before;
-    else
-      reexpress(codes, g.c.token, r.head_dim, written, before / scale);
-  }
-  if ((threadIdx.x & 31) == 0) *scale_at = scale;
-  const Divide by(scale);
-#pragma unroll
-  for (int i = 0; i < R::kSteps; ++i)
-    if (i < steps) {
-      const int k = i * of.rows + of.group, kk = min(k, n - 1);
-      uint8_t* row = codes + (first + (r.slots[t0 + kk] - slot)) * g.c.token;
-      if constexpr (STEPS > 0) {
-        if (k < n)
-          of.template store<KEY>(raw[i], f[i], wp, cosines + kk * pairs, sines + kk * pairs, by,
-                                 row);
-      } else {
-        of.template store<KEY>(raw[i], f[i], wp, KEY ? r.positions[t0 + kk] : 0, by, row);
-      }
-    }
-}
-
 // Queries: norm and rotation, a lane group a head, as in norm_rope.cu.
 template <typename T, bool IL>
-__device__ __forceinline__ void queries(const Append8Params& g, const Dims& d, float* table) {
+__device__ __forceinline__ void queries(const Append8Params& g, const Dims& d, int cta,
+                                        float* table) {
   const RopeParams& r = g.p.r;
   const int pairs = r.r.rot >> 1;
-  const int tg = blockIdx.x % d.token_groups, hg = blockIdx.x / d.token_groups;
+  const int tg = cta % d.token_groups, hg = cta / d.token_groups;
   const int u = threadIdx.x & (d.lanes - 1), y = threadIdx.x / d.lanes;
   const int z = y / d.q_heads, hd = hg * d.q_heads + (y - z * d.q_heads);
   const int per_cta = d.q_tokens * d.q_z, cta0 = tg * per_cta;
   const int cta_tokens = min(per_cta, r.tokens - cta0);
   const int first = z * d.q_tokens;
   const bool active = z < d.q_z && hd < r.hq && u < d.units;
-  const Lane<IL> lane(u < d.units ? u : 0, d.turned, r.r.rot);
+  const Lane<IL> lane(u < d.units ? u : 0, d.turned, r.r.rot, r.head_dim);
   float* cosines = table;
   float* sines = table + per_cta * pairs;
   constexpr int kTokens = IL ? 4 : 2;
@@ -398,11 +319,12 @@ __device__ __forceinline__ void queries(const Append8Params& g, const Dims& d, f
 
 // Queries in the form for any rows: a warp a head.
 template <typename T>
-__device__ __forceinline__ void queries_any(const Append8Params& g, const Dims& d, float* smem) {
+__device__ __forceinline__ void queries_any(const Append8Params& g, const Dims& d, int cta,
+                                            float* smem) {
   const RopeParams& r = g.p.r;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x % d.token_groups;
-  const int hd = blockIdx.x / d.token_groups * kWarps + warp;
+  const int t = cta % d.token_groups;
+  const int hd = cta / d.token_groups * kWarps + warp;
   if (hd >= r.hq) return;
   float* row = smem + warp * 128;
   const uint16_t* src = r.q.p + (long long)t * r.q.token + (long long)hd * r.q.head;
@@ -434,28 +356,31 @@ __device__ __forceinline__ void queries_any(const Append8Params& g, const Dims& 
   }
 }
 
-template <typename T, bool IL, int STEPS>
+template <typename T, bool IL, bool FAST>
 __global__ void __launch_bounds__(kThreads, 2)
     append8_kernel(const __grid_constant__ Append8Params g, const Dims d) {
   extern __shared__ float4 smem4[];
+  __shared__ float tops[kWarps];
   float* smem = reinterpret_cast<float*>(smem4);
   const RopeParams& r = g.p.r;
   wait_prior_launch();
   let_next_launch();
-  if ((int)blockIdx.x < d.q_ctas) {
-    if constexpr (STEPS > 0)
-      queries<T, IL>(g, d, smem);
+  int cta = blockIdx.x;                 // keys and values, which take longest, come first
+  if (cta >= d.kv_ctas) {
+    if constexpr (FAST)
+      queries<T, IL>(g, d, cta - d.kv_ctas, smem);
     else
-      queries_any<T>(g, d, smem);
+      queries_any<T>(g, d, cta - d.kv_ctas, smem);
     return;
   }
-  int cta = blockIdx.x - d.q_ctas;
-  const int combo = cta % d.combos * kWarps + (threadIdx.x >> 5);  // K heads, then V heads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp & 1;
+  const int first_combo = cta % d.combos * (kWarps / 2);
+  const int combo = first_combo + (warp >> 1);         // K heads, then V heads
   cta /= d.combos;
   const int part = cta % d.split, w0 = cta / d.split * kRun;
   // lane l has token w0 - 1 + l: the one before the window, the window, and what runs
   // that begin there may go on with
-  const int lane = threadIdx.x & 31, t = w0 - 1 + lane;
+  const int t = w0 - 1 + lane;
   long long slot = -1;
   if (t >= 0 && t < r.tokens) {
     slot = r.slots[t];
@@ -470,46 +395,86 @@ __global__ void __launch_bounds__(kThreads, 2)
   const unsigned go_on = __ballot_sync(0xffffffffu, follows);
   unsigned begin = __ballot_sync(0xffffffffu, slot >= 0 && !follows && lane > 0 && lane <= kRun);
   const bool key = combo < r.hk, on = combo < 2 * r.hk;
-  const bool any_keys = combo - (int)(threadIdx.x >> 5) < r.hk;  // in the CTA
+  const bool any_keys = first_combo < r.hk;            // in the CTA
   const int h = key ? combo : combo - r.hk;
+  const Rows& in = key ? r.k : r.v;
   const int pairs = r.r.rot >> 1;
   float *cosines = smem, *sines = smem + kRun * pairs;
   for (int i = 0; begin; ++i) {
     const int at = __ffs(begin) - 1;
     begin &= begin - 1;
     if (i % d.split != part) continue;
-    // the run goes on while the bits behind its first token are set
+    // the run [t0, t0 + n) goes on while the bits behind its first token are set; this
+    // warp has `mine` rows from k0 on
     const int n = at == 31 ? 1 : __ffs(~(go_on >> (at + 1)));
-    const int t0 = w0 - 1 + at;
-    if constexpr (STEPS > 0) {
-      const RowOf<T, IL, STEPS> of(d, r.r.rot);
-      if (any_keys) {
-        __syncthreads();
-        fill_table(r.r, r.positions + t0, n, cosines, sines, threadIdx.x, kThreads);
-        __syncthreads();
-      }
-      if (!on) continue;
-      if (key)
-        append_run<T, IL, STEPS, true>(g, of, t0, n, h, cosines, sines);
-      else
-        append_run<T, IL, STEPS, false>(g, of, t0, n, h, cosines, sines);
-    } else {
-      const RowOf<T, false, 0> of(g, smem);
-      if (!on) continue;
-      if (key)
-        append_run<T, false, 0, true>(g, of, t0, n, h, nullptr, nullptr);
-      else
-        append_run<T, false, 0, false>(g, of, t0, n, h, nullptr, nullptr);
+    const int t0 = w0 - 1 + at, k0 = sub * kWarpRows, mine = min(kWarpRows, n - k0);
+    const long long slot0 = __shfl_sync(0xffffffffu, slot, at);
+    // rows of the block that the run has, and the row of each of its tokens
+    const int row_of = (int)(slot - slot0) + (int)(slot0 & (kScaleBlock - 1));
+    const unsigned written =
+        __reduce_or_sync(0xffffffffu, lane >= at && lane < at + n ? 1u << (row_of & 31) : 0u);
+    const long long page = slot0 >> r.page_shift;
+    const int in_page = (int)(slot0 - (page << r.page_shift));
+    const int first = in_page & (kScaleBlock - 1), block = in_page / kScaleBlock;
+    uint8_t* codes = (key ? g.c.k : g.c.v) + page * g.c.page + (long long)h * g.c.head +
+                     (long long)(in_page - first) * g.c.token;
+    float* scale_at = (key ? g.c.k_scales : g.c.v_scales) + page * g.c.scale_page +
+                      h * g.c.scale_head + block * g.c.scale_block;
+    RowsOf<T, IL, FAST> of(d, r, smem);
+    float top = 0.0f, before = 0.0f;
+    if (on) {
+      if (first) before = *scale_at;
+      if (mine > 0)
+        of.load(in.p + (long long)(t0 + k0) * in.token + (long long)h * in.head, in.token, mine);
     }
+    if (FAST && any_keys) {
+      fill_table(r.r, r.positions + t0, n, cosines, sines, threadIdx.x, kThreads);
+      __syncthreads();
+    }
+    if (on && mine > 0) {
+      if (key) {
+        if (g.p.n.on) of.norm(g.p.n, h, 1.0f / (float)r.head_dim);
+        of.turn(r, cosines + k0 * pairs, sines + k0 * pairs, t0 + k0, mine);
+      }
+      top = of.top();
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();  // (and the old scale is read, and the table done with)
+    float scale = scale_for(fmaxf(top, tops[warp ^ 1]));
+    if (on) {
+      if (first && before > 0.0f && before < INFINITY) {
+        if (before >= scale)
+          scale = before;
+        else
+          reexpress(codes, g.c.token, r.head_dim, written, before / scale, sub);
+      }
+      if (lane == 0 && sub == 0) *scale_at = scale;
+    }
+    // (by all lanes: they hand out the rows)
+    const Divide by(scale);
+    int rows[kWarpRows];
+#pragma unroll
+    for (int k = 0; k < kWarpRows; ++k)
+      rows[k] = __shfl_sync(0xffffffffu, row_of, (at + k0 + k) & 31);
+    if (on && mine > 0)
+      of.store(by, mine, [&](int k) {
+        int row = rows[0];
+#pragma unroll
+        for (int q = 1; q < kWarpRows; ++q) row = k == q ? rows[q] : row;
+        return codes + (long long)row * g.c.token;
+      });
+    __syncthreads();  // tops is free again
   }
 }
 
-template <typename T, bool IL, int STEPS>
+template <typename T, bool IL, bool FAST>
 cudaError_t launch_append(const Append8Params& g, cudaStream_t s) {
   const RopeParams& r = g.p.r;
   Dims d{};
   int smem;
-  if (STEPS > 0) {
+  if (FAST) {
     const Units u = units_of_head<IL>(r.head_dim, r.r.rot);
     d.units = u.count;
     d.turned = u.turned;
@@ -532,35 +497,25 @@ cudaError_t launch_append(const Append8Params& g, cudaStream_t s) {
     d.token_groups = r.tokens;
     smem = kWarps * 128 * (int)sizeof(float);
   }
-  d.q_ctas = d.token_groups * d.q_rows;
-  d.combos = (2 * r.hk + kWarps - 1) / kWarps;
+  d.combos = (2 * r.hk + kWarps / 2 - 1) / (kWarps / 2);
   const int windows = (r.tokens + kRun - 1) / kRun;
   // a window's runs to as many CTAs as the GPU takes at once: decode steps have a run
   // for each token, prompts one for each window
   d.split = kRun;
   while (d.split > 1 && (long long)windows * d.combos * d.split > 4 * kSms) d.split /= 2;
-  const long long ctas = d.q_ctas + (long long)windows * d.combos * d.split;
-  return launch_after(append8_kernel<T, IL, STEPS>, dim3((unsigned)ctas), dim3(kThreads), smem, s, g,
+  d.kv_ctas = windows * d.combos * d.split;
+  const long long ctas = d.kv_ctas + (long long)d.token_groups * d.q_rows;
+  return launch_after(append8_kernel<T, IL, FAST>, dim3((unsigned)ctas), dim3(kThreads), smem, s, g,
                       d);
 }
 
-// four rows at a time, or two
-template <typename T>
-cudaError_t launch_units(const Append8Params& g, cudaStream_t s) {
-  const RopeParams& r = g.p.r;
-  if (r.r.interleaved)
-    return units_of_head<true>(r.head_dim, r.r.rot).lanes <= 8 ? launch_append<T, true, 4>(g, s)
-                                                               : launch_append<T, true, 8>(g, s);
-  return units_of_head<false>(r.head_dim, r.r.rot).lanes <= 8 ? launch_append<T, false, 4>(g, s)
-                                                              : launch_append<T, false, 8>(g, s);
-}
-
 // ------------------------------------------------------------------ read back
-// A CTA has 32 rows of the outputs, all heads: it finds their sequence (every thread
-// counts some of the sequences that begin at or before its first row), 32 lanes look
-// up their pages, then all threads bring 16 codes at a time to 32 bytes of the
+// A CTA has up to 32 rows of the outputs, all heads: it brings the sequences' first rows
+// to shared memory (as many as there is room for; every thread then counts some of those
+// that begin at or before its first row), a lane a row finds its sequence by bisection and
+// looks up its page, then all threads bring 16 codes at a time to 32 bytes of the
 // outputs. Bound by memory.
-constexpr int kReadRows = 32;
+constexpr int kReadRows = 32, kReadSeqs = 1024;
 
 template <typename T>
 __device__ __forceinline__ void read16(const uint8_t* codes, float scale, uint16_t* to, bool wide) {
@@ -583,26 +538,45 @@ __device__ __forceinline__ void read16(const uint8_t* codes, float scale, uint16
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) read8_kernel(const Read8Params p, int wide) {
+__global__ void __launch_bounds__(kThreads) read8_kernel(const Read8Params p, int rows_shift,
+                                                         int wide) {
   __shared__ long long code_at[kReadRows], scale_at[kReadRows];
+  __shared__ int cu[kReadSeqs + 1];
   __shared__ int counts[kWarps];
-  const int row0 = blockIdx.x * kReadRows;
+  const int cta_rows = 1 << rows_shift, row0 = blockIdx.x << rows_shift;
   wait_prior_launch();
   let_next_launch();
-  int mine = 0;
-  for (int s = 1 + threadIdx.x; s <= p.num_seqs; s += kThreads) mine += p.cu[s] <= row0;
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = mine;
-  __syncthreads();
-  if (threadIdx.x < kReadRows) {
-    int s = 0;
+  // the sequences from s0 on, the first of them the one that row0 may be in
+  int s0 = 0;
+  if (p.num_seqs > kReadSeqs) {
+    int mine = 0;
+    for (int s = 1 + threadIdx.x; s <= p.num_seqs; s += kThreads) mine += p.cu[s] <= row0;
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = mine;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) s += counts[i];
+    for (int i = 0; i < kWarps; ++i) s0 += counts[i];
+  }
+  const int kept = min(p.num_seqs - s0, kReadSeqs);
+  for (int i = threadIdx.x; i <= kept; i += kThreads) cu[i] = p.cu[s0 + i];
+  __syncthreads();
+  if (threadIdx.x < cta_rows) {
     const int row = row0 + threadIdx.x;
+    int lo = 0, hi = kept;                             // last sequence with cu <= row
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cu[mid] <= row)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    // (behind what is kept, where thousands of sequences have no rows)
+    int s = s0 + lo;
     while (s < p.num_seqs && p.cu[s + 1] <= row) ++s;
     long long at = -1, sc = 0;
-    if (row < p.rows && s < p.num_seqs && p.cu[s] >= 0 && row >= p.cu[s]) {
-      const long long pos = (long long)p.first[s] + (row - p.cu[s]);
+    const int begin = s < p.num_seqs ? p.cu[s] : 0;
+    if (row < p.rows && s < p.num_seqs && begin >= 0 && row >= begin) {
+      const long long pos = (long long)p.first[s] + (row - begin);
       const long long limit = (long long)p.columns << p.page_shift;
       int page = -1;
       if (p.first[s] >= 0 && pos < limit)
@@ -619,11 +593,11 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const Read8Params p, in
     scale_at[threadIdx.x] = sc;
   }
   __syncthreads();
-  const int chunks = p.head_dim >> 4, heads = p.hk, items = kReadRows * heads * chunks;
+  const int chunks = p.head_dim >> 4, items = (p.hk * chunks) << rows_shift;
 #pragma unroll 4
   for (int i = threadIdx.x; i < items; i += kThreads) {
     const int rest = i / chunks, c = i - rest * chunks;
-    const int r = rest & (kReadRows - 1), h = rest / kReadRows;
+    const int r = rest & (cta_rows - 1), h = rest >> rows_shift;
     if (code_at[r] < 0) continue;
     const long long at = code_at[r] + h * p.c.head + c * 16, sc = scale_at[r] + h * p.c.scale_head;
     const float ks = __ldg(p.c.k_scales + sc), vs = __ldg(p.c.v_scales + sc);
@@ -738,17 +712,24 @@ cudaError_t launch_append8(const Append8Params& g, int dtype, cudaStream_t s) {
   const RopeParams& r = g.p.r;
   const bool fast = units_fit(r.r, r.head_dim) && weights_aligned(g.p.n) && rows_aligned(r.q) &&
                     rows_aligned(r.q_out) && rows_aligned(r.k) && rows_aligned(r.v);
-  if (!fast)
-    return dtype == MOE_ATTN_BF16 ? launch_append<Bf16, false, 0>(g, s)
-                                  : launch_append<Fp16, false, 0>(g, s);
-  return dtype == MOE_ATTN_BF16 ? launch_units<Bf16>(g, s) : launch_units<Fp16>(g, s);
+  const bool il = r.r.interleaved;
+  if (dtype == MOE_ATTN_BF16)
+    return !fast ? launch_append<Bf16, false, false>(g, s)
+           : il  ? launch_append<Bf16, true, true>(g, s)
+                 : launch_append<Bf16, false, true>(g, s);
+  return !fast ? launch_append<Fp16, false, false>(g, s)
+         : il  ? launch_append<Fp16, true, true>(g, s)
+               : launch_append<Fp16, false, true>(g, s);
 }
 
 cudaError_t launch_read8(const Read8Params& p, int dtype, cudaStream_t s) {
-  const dim3 grid((p.rows + kReadRows - 1) / kReadRows), block(kThreads);
+  int shift = 5;  // fewer rows a CTA until every SM has some
+  while (shift > 1 && (p.rows >> shift) < 2 * kSms) --shift;
+  const dim3 grid((p.rows + (1 << shift) - 1) >> shift), block(kThreads);
   const int wide = rows_aligned(p.k_out) && rows_aligned(p.v_out);
-  return dtype == MOE_ATTN_BF16 ? launch_after(read8_kernel<Bf16>, grid, block, 0, s, p, wide)
-                                : launch_after(read8_kernel<Fp16>, grid, block, 0, s, p, wide);
+  return dtype == MOE_ATTN_BF16
+             ? launch_after(read8_kernel<Bf16>, grid, block, 0, s, p, shift, wide)
+             : launch_after(read8_kernel<Fp16>, grid, block, 0, s, p, shift, wide);
 }
 
 cudaError_t launch_expand8(const Expand8Params& p, int dtype, int grid, cudaStream_t s) {

@@ -2,9 +2,10 @@
 //
 // Fast form: a head's values are cut into units, one a lane of a group of `lanes`
 // (a power of two, 32 at most). In the half layout a unit of the turned part is a
-// chunk of 8 values of either half, so that both values of a pair are in one lane;
-// interleaved pairs lie in one chunk; the part that does not turn is in single
-// chunks. Every access is 16 bytes, and a sum over a head is a few shuffles.
+// chunk of 8 values of either half, so that both values of a pair are in one lane, and
+// of the part that does not turn two neighbouring chunks; interleaved pairs lie in one
+// chunk, and so units are single chunks there. Every access is 16 bytes, and a sum over
+// a head is a few shuffles.
 #pragma once
 
 #include "attn_common.cuh"
@@ -19,7 +20,7 @@ template <bool IL>
 __host__ __device__ __forceinline__ Units units_of_head(int head_dim, int rot) {
   Units u;
   u.turned = IL ? rot / 8 : rot / 16;
-  u.count = u.turned + (head_dim - rot) / 8;
+  u.count = u.turned + (IL ? (head_dim - rot) / 8 : (head_dim - rot + 8) / 16);
   u.lanes = 1;
   while (u.lanes < u.count) u.lanes *= 2;
   return u;
@@ -31,7 +32,9 @@ union Chunk8 {
 };
 
 __device__ __forceinline__ float group_sum(float x, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 
@@ -55,11 +58,11 @@ template <bool IL>
 struct Lane {
   int at, gap, pair;   // first value, pairs of a half, first pair
   bool turns, two;
-  __device__ __forceinline__ Lane(int u, int turned, int rot) {
+  __device__ __forceinline__ Lane(int u, int turned, int rot, int head_dim) {
     turns = u < turned;
-    two = turns && !IL;
-    at = turns ? u * 8 : rot + (u - turned) * 8;
-    gap = rot >> 1;
+    at = turns ? u * 8 : rot + (u - turned) * (IL ? 8 : 16);
+    gap = turns ? rot >> 1 : 8;
+    two = !IL && (turns || at + 8 < head_dim);
     pair = turns ? u * (IL ? 4 : 8) : 0;
   }
   // fp32 weights plus offset of the unit's values

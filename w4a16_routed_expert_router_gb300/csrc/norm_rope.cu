@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   const int u = threadIdx.x, hd = blockIdx.y * blockDim.y + threadIdx.y;
   const bool active = hd < r.hq + r.hk + r.hv && u < units;
   const Head hh(r, active ? hd : 0);
-  const Lane<IL> lane(active ? u : 0, turned, r.r.rot);
+  const Lane<IL> lane(active ? u : 0, turned, r.r.rot, r.head_dim);
   const Rows& in = hh.in(r);
   const uint16_t* src = in.p + (long long)t0 * in.token + (long long)hh.h * in.head + lane.at;
   Chunk8 a[kTokens], b[kTokens];
@@ -95,23 +95,33 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
              blockDim.x * blockDim.y * blockDim.z);
   __syncthreads();
   const float mean = 1.0f / (float)r.head_dim;
+  float sum[kTokens];
 #pragma unroll
   for (int t = 0; t < kTokens; ++t) {
-    float fa[8], fb[8], sum = 0.0f;
+    float fa[8], fb[8];
     unpack8<T>(a[t], fa);
     unpack8<T>(b[t], fb);
+    sum[t] = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      sum = fmaf(fa[k], fa[k], sum);
-      sum = fmaf(fb[k], fb[k], sum);
+    for (int k = 0; k < 8; ++k) sum[t] = fmaf(fa[k], fa[k], sum[t]);
+    if (!IL) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[t] = fmaf(fb[k], fb[k], sum[t]);
     }
-    sum = group_sum(sum, blockDim.x);
+  }
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t) sum[t] = group_sum(sum[t], blockDim.x);
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t) {
     if (!active || t >= nt) continue;
+    float fa[8], fb[8];
+    unpack8<T>(a[t], fa);
+    unpack8<T>(b[t], fb);
     uint16_t* dst = hh.out(p, t0 + t);
     if (!dst) continue;
     dst += lane.at;
     if (!hh.value) {
-      const float f = rsqrtf(fmaf(sum, mean, p.n.eps));
+      const float f = rsqrtf(fmaf(sum[t], mean, p.n.eps));
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         fa[k] = fa[k] * f * wa[k];
@@ -220,10 +230,10 @@ cudaError_t launch_t(const NormParams& p, cudaStream_t s) {
 
 // ------------------------------------------------------------------ gradient
 
-constexpr int kGradThreads = 256;  // and registers for three CTAs an SM
+constexpr int kGradThreads = 256;
 
 template <typename T, bool IL>
-__global__ void __launch_bounds__(kGradThreads, 3)
+__global__ void __launch_bounds__(kGradThreads, 2)
     norm_grad_kernel(const NormGradParams g, int units, int turned, int shared) {
   extern __shared__ float4 smem4[];
   float* smem = reinterpret_cast<float*>(smem4);
@@ -236,7 +246,7 @@ __global__ void __launch_bounds__(kGradThreads, 3)
   const int u = threadIdx.x, hd = blockIdx.y * blockDim.y + threadIdx.y;
   const bool active = hd < heads && u < units;
   const Head hh(r, active ? hd : 0);
-  const Lane<IL> lane(active ? u : 0, turned, r.r.rot);
+  const Lane<IL> lane(active ? u : 0, turned, r.r.rot, r.head_dim);
   const Rows &in = hh.in(r), &dy = hh.key ? g.dk : g.dq, &dx = hh.key ? p.k_out : r.q_out;
   const long long hi = hh.h * in.head + lane.at, hy = hh.h * dy.head + lane.at,
                   ho = hh.h * dx.head + lane.at;
@@ -250,26 +260,42 @@ __global__ void __launch_bounds__(kGradThreads, 3)
   const int tid = (threadIdx.z * blockDim.y + threadIdx.y) * blockDim.x + threadIdx.x;
   const int threads = blockDim.x * blockDim.y * blockDim.z;
   const float mean = 1.0f / (float)r.head_dim;
-  int turn = 0;
-  for (int c0 = blockIdx.x * z; c0 < r.tokens; c0 += gridDim.x * z, turn ^= 1) {
+  // a token's chunks, and the table of its CTA's tokens, one iteration ahead
+  Chunk8 next[4];
+  const auto load = [&](int c0) {
     const int t = c0 + threadIdx.z;
-    const bool on = active && t < r.tokens;
-    Chunk8 xa, xb, ya, yb;
-    xa.v = xb.v = ya.v = yb.v = make_uint4(0, 0, 0, 0);
-    if (on) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) next[k].v = make_uint4(0, 0, 0, 0);
+    if (active && t < r.tokens) {
       const uint16_t* x = in.p + (long long)t * in.token + hi;
       const uint16_t* y = dy.p + (long long)t * dy.token + hy;
-      xa.v = *reinterpret_cast<const uint4*>(x);
-      ya.v = *reinterpret_cast<const uint4*>(y);
+      next[0].v = *reinterpret_cast<const uint4*>(x);
+      next[1].v = *reinterpret_cast<const uint4*>(y);
       if (lane.two) {
-        xb.v = *reinterpret_cast<const uint4*>(x + lane.gap);
-        yb.v = *reinterpret_cast<const uint4*>(y + lane.gap);
+        next[2].v = *reinterpret_cast<const uint4*>(x + lane.gap);
+        next[3].v = *reinterpret_cast<const uint4*>(y + lane.gap);
       }
     }
+  };
+  const auto table = [&](int c0, int turn) {
     float* cosines = smem + turn * 2 * z * pairs;
-    float* sines = cosines + z * pairs;
-    fill_table(r.r, r.positions + c0, min(z, r.tokens - c0), cosines, sines, tid, threads);
-    __syncthreads();
+    if (c0 < r.tokens)
+      fill_table(r.r, r.positions + c0, min(z, r.tokens - c0), cosines, cosines + z * pairs, tid,
+                 threads);
+  };
+  const int step = gridDim.x * z;
+  int turn = 0;
+  load(blockIdx.x * z);
+  table(blockIdx.x * z, 0);
+  for (int c0 = blockIdx.x * z; c0 < r.tokens; c0 += step, turn ^= 1) {
+    const int t = c0 + threadIdx.z;
+    const bool on = active && t < r.tokens;
+    const Chunk8 xa = next[0], ya = next[1], xb = next[2], yb = next[3];
+    __syncthreads();  // this iteration's table is there, the last one's is free
+    load(c0 + step);
+    table(c0 + step, turn ^ 1);
+    const float* cosines = smem + turn * 2 * z * pairs;
+    const float* sines = cosines + z * pairs;
     float fx[8], gx[8], ua[8], ub[8];
     unpack8<T>(xa, fx);
     unpack8<T>(xb, gx);
@@ -413,16 +439,15 @@ __global__ void __launch_bounds__(32 * kAddRows) norm_grad_add_kernel(const AddP
   float sum = 0.0f;
   if (on) {
     const int j = key ? i - n_q : i, w = j / a.d, v = j - w * a.d;
-    // first of the weight's rows among all rows of one CTA along the tokens
-    const long long row0 = a.per ? (key ? a.heads_q : 0) + w : (key ? 1 : 0);
+    // the weight's rows, one behind the other; CTAs dealt out over threadIdx.y
+    const int h0 = a.per ? (key ? a.heads_q : 0) + w : (key ? 1 : 0);
     const int inner = key ? a.inner_k : a.inner_q;
-    // (CTA, row) pairs in order, dealt out over threadIdx.y
-    const long long n = (long long)a.outer * inner;
-    for (long long k = threadIdx.y; k < n; k += kAddRows) {
-      const long long o = k / inner, h = row0 + (k - o * inner);
-      const long long at = a.per ? (o * a.groups + h / a.per) * a.rows + h % a.per
-                                 : o * a.rows + h;
-      sum += a.parts[at * a.d + v];
+    const long long stride = (long long)a.rows * (a.per ? a.groups : 1) * a.d;
+    for (int h = h0; h < h0 + inner; ++h) {
+      const int at = a.per ? h / a.per * a.rows + h % a.per : h;
+      const float* from = a.parts + (long long)at * a.d + v;
+#pragma unroll 4
+      for (int o = threadIdx.y; o < a.outer; o += kAddRows) sum += from[o * stride];
     }
   }
   part[threadIdx.y][threadIdx.x] = sum;
