@@ -46,8 +46,9 @@ __device__ __forceinline__ void fill_table(const Rotation& r, const int* positio
     const int t = i / pairs, c = i - t * pairs;
     const long long phase = (long long)((unsigned long long)(long long)positions[t] *
                                         (unsigned long long)r.freq[c]);
+    // (the upper half says it to 2^-32 turns; all of it takes a conversion of 64 bits)
     float sn, cn;
-    sincospif(__ll2float_rn(phase) * 0x1p-63f, &sn, &cn);
+    sincospif((float)(int)(phase >> 32) * 0x1p-31f, &sn, &cn);
     cosines[i] = cn * r.magnitude;
     sines[i] = sn * r.magnitude * r.sign;
   }

@@ -43,19 +43,23 @@ struct Head {
     value = hd >= r.hq + r.hk;
     h = hd - (value ? r.hq + r.hk : key ? r.hq : 0);
   }
-  __device__ __forceinline__ const Rows& in(const RopeParams& r) const {
-    return value ? r.v : key ? r.k : r.q;
+  // (by value: a reference makes every use a load from an address among the parameters)
+  static __device__ __forceinline__ Rows pick(bool first, const Rows& a, const Rows& b) {
+    return Rows{first ? a.p : b.p, first ? a.token : b.token, first ? a.head : b.head};
+  }
+  __device__ __forceinline__ Rows in(const RopeParams& r) const {
+    return pick(value, r.v, pick(key, r.k, r.q));
   }
   __device__ __forceinline__ uint16_t* out(const NormParams& p, int t) const {
     if ((key || value) && p.r.slots) return page_row(p.r, key, t, h);
-    const Rows& o = key ? p.k_out : p.r.q_out;
+    const Rows o = pick(key, p.k_out, p.r.q_out);
     return o.p + (long long)t * o.token + (long long)h * o.head;
   }
 };
 
 template <typename T, bool IL>
 __global__ void __launch_bounds__(kMaxThreads, 2)
-    norm_rope_kernel(const NormParams p, int tokens_per_thread, int units, int turned) {
+    norm_rope_kernel(const __grid_constant__ NormParams p, int tokens_per_thread, int units, int turned) {
   extern __shared__ float4 table4[];  // cosines, then sines: [tokens of the CTA][rot / 2]
   float* cosines = reinterpret_cast<float*>(table4);
   constexpr int kTokens = tokens_of(!IL);
@@ -74,7 +78,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   const bool active = hd < r.hq + r.hk + r.hv && u < units;
   const Head hh(r, active ? hd : 0);
   const Lane<IL> lane(active ? u : 0, turned, r.r.rot, r.head_dim);
-  const Rows& in = hh.in(r);
+  const Rows in = hh.in(r);
   const uint16_t* src = in.p + (long long)t0 * in.token + (long long)hh.h * in.head + lane.at;
   Chunk8 a[kTokens], b[kTokens];
 #pragma unroll
@@ -94,6 +98,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   fill_table(r.r, r.positions + cta0, cta_tokens, cosines, sines, tid,
              blockDim.x * blockDim.y * blockDim.z);
   __syncthreads();
+  const bool paged = r.slots && (hh.key || hh.value);
+  const Rows o = Head::pick(hh.key, p.k_out, r.q_out);
+  uint16_t* out = o.p + (long long)t0 * o.token + (long long)hh.h * o.head + lane.at;
   const float mean = 1.0f / (float)r.head_dim;
   float sum[kTokens];
 #pragma unroll
@@ -117,9 +124,12 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     float fa[8], fb[8];
     unpack8<T>(a[t], fa);
     unpack8<T>(b[t], fb);
-    uint16_t* dst = hh.out(p, t0 + t);
-    if (!dst) continue;
-    dst += lane.at;
+    uint16_t* dst = out + t * o.token;
+    if (paged) {
+      dst = page_row(r, hh.key, t0 + t, hh.h);
+      if (!dst) continue;
+      dst += lane.at;
+    }
     if (!hh.value) {
       const float f = rsqrtf(fmaf(sum[t], mean, p.n.eps));
 #pragma unroll
@@ -141,7 +151,7 @@ constexpr int kAnyWarps = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(kAnyWarps * 32)
-    norm_rope_any_kernel(const NormParams p, int tokens_per_warp) {
+    norm_rope_any_kernel(const __grid_constant__ NormParams p, int tokens_per_warp) {
   __shared__ float row[kAnyWarps][32 * kAnyValues];
   const RopeParams& r = p.r;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -150,7 +160,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32)
   let_next_launch();
   if (hd >= r.hq + r.hk + r.hv) return;
   const Head hh(r, hd);
-  const Rows& in = hh.in(r);
+  const Rows in = hh.in(r);
   const void* w = hh.key ? p.n.k_weight : p.n.q_weight;
   const long long wh = hh.h * (hh.key ? p.n.k_head : p.n.q_head);
   const int t1 = min(r.tokens, (int)(blockIdx.x + 1) * tokens_per_warp);
@@ -230,11 +240,11 @@ cudaError_t launch_t(const NormParams& p, cudaStream_t s) {
 
 // ------------------------------------------------------------------ gradient
 
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 256, kTables = 4;
 
 template <typename T, bool IL>
 __global__ void __launch_bounds__(kGradThreads, 2)
-    norm_grad_kernel(const NormGradParams g, int units, int turned, int shared) {
+    norm_grad_kernel(const __grid_constant__ NormGradParams g, int units, int turned, int shared) {
   extern __shared__ float4 smem4[];
   float* smem = reinterpret_cast<float*>(smem4);
   const NormParams& p = g.p;
@@ -247,7 +257,8 @@ __global__ void __launch_bounds__(kGradThreads, 2)
   const bool active = hd < heads && u < units;
   const Head hh(r, active ? hd : 0);
   const Lane<IL> lane(active ? u : 0, turned, r.r.rot, r.head_dim);
-  const Rows &in = hh.in(r), &dy = hh.key ? g.dk : g.dq, &dx = hh.key ? p.k_out : r.q_out;
+  const Rows in = hh.in(r), dy = Head::pick(hh.key, g.dk, g.dq),
+             dx = Head::pick(hh.key, p.k_out, r.q_out);
   const long long hi = hh.h * in.head + lane.at, hy = hh.h * dy.head + lane.at,
                   ho = hh.h * dx.head + lane.at;
   float wa[8], wb[8], da[8], db[8];
@@ -277,25 +288,36 @@ __global__ void __launch_bounds__(kGradThreads, 2)
       }
     }
   };
-  const auto table = [&](int c0, int turn) {
-    float* cosines = smem + turn * 2 * z * pairs;
-    if (c0 < r.tokens)
-      fill_table(r.r, r.positions + c0, min(z, r.tokens - c0), cosines, cosines + z * pairs, tid,
-                 threads);
+  // of kTables iterations at once, which takes most threads
+  const auto table = [&](int c0) {
+    const int step = gridDim.x * z;
+    for (int i = tid; i < kTables * z * pairs; i += threads) {
+      const int row = i / pairs, c = i - row * pairs;
+      const int t = c0 + row / z * step + row % z;
+      if (t >= r.tokens) continue;
+      const long long phase = (long long)((unsigned long long)(long long)r.positions[t] *
+                                          (unsigned long long)r.r.freq[c]);
+      float sn, cn;
+      sincospif((float)(int)(phase >> 32) * 0x1p-31f, &sn, &cn);
+      smem[i] = cn * r.r.magnitude;
+      smem[kTables * z * pairs + i] = sn * r.r.magnitude * r.r.sign;
+    }
   };
   const int step = gridDim.x * z;
   int turn = 0;
   load(blockIdx.x * z);
-  table(blockIdx.x * z, 0);
-  for (int c0 = blockIdx.x * z; c0 < r.tokens; c0 += step, turn ^= 1) {
+  for (int c0 = blockIdx.x * z; c0 < r.tokens; c0 += step, turn = (turn + 1) % kTables) {
     const int t = c0 + threadIdx.z;
     const bool on = active && t < r.tokens;
     const Chunk8 xa = next[0], ya = next[1], xb = next[2], yb = next[3];
-    __syncthreads();  // this iteration's table is there, the last one's is free
     load(c0 + step);
-    table(c0 + step, turn ^ 1);
-    const float* cosines = smem + turn * 2 * z * pairs;
-    const float* sines = cosines + z * pairs;
+    if (turn == 0) {
+      __syncthreads();
+      table(c0);
+      __syncthreads();
+    }
+    const float* cosines = smem + turn * z * pairs;
+    const float* sines = cosines + kTables * z * pairs;
     float fx[8], gx[8], ua[8], ub[8];
     unpack8<T>(xa, fx);
     unpack8<T>(xb, gx);
@@ -362,7 +384,7 @@ __global__ void __launch_bounds__(kGradThreads, 2)
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kAnyWarps * 32) norm_grad_any_kernel(const NormGradParams g) {
+__global__ void __launch_bounds__(kAnyWarps * 32) norm_grad_any_kernel(const __grid_constant__ NormGradParams g) {
   __shared__ float row[kAnyWarps][32 * kAnyValues];
   const NormParams& p = g.p;
   const RopeParams& r = p.r;
@@ -372,7 +394,8 @@ __global__ void __launch_bounds__(kAnyWarps * 32) norm_grad_any_kernel(const Nor
   let_next_launch();
   if (hd >= heads) return;
   const Head hh(r, hd);
-  const Rows &in = hh.in(r), &dy = hh.key ? g.dk : g.dq, &dx = hh.key ? p.k_out : r.q_out;
+  const Rows in = hh.in(r), dy = Head::pick(hh.key, g.dk, g.dq),
+             dx = Head::pick(hh.key, p.k_out, r.q_out);
   const void* w = hh.key ? p.n.k_weight : p.n.q_weight;
   const long long wh = hh.h * (hh.key ? p.n.k_head : p.n.q_head);
   const float mean = 1.0f / (float)r.head_dim;
@@ -465,7 +488,7 @@ cudaError_t launch_grad_fast(const NormGradParams& g, const NormGradPlan& n, cud
   const RopeParams& r = g.p.r;
   const Units u = units_of_head<IL>(r.head_dim, r.r.rot);
   const int shared = (!r.hq || g.p.n.q_head == 0) && (!r.hk || g.p.n.k_head == 0);
-  const int table = 4 * n.z * (r.r.rot / 2), sums = n.rows * n.z * r.head_dim;
+  const int table = 2 * kTables * n.z * (r.r.rot / 2), sums = n.rows * n.z * r.head_dim;
   cudaError_t e = launch_after(norm_grad_kernel<T, IL>, dim3(n.parts, n.groups),
                                dim3(u.lanes, n.rows, n.z),
                                (table > sums ? table : sums) * (int)sizeof(float), s, g, u.count,
