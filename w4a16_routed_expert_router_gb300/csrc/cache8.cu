@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(kThreads) expand8_kernel(const Expand8Params p
       if (bad && tid == 0) atomicOr(p.err, kErrRange);
       const int rows = min(page_rows, kv - key0), row_chunks = page_rows * chunks;
       const long long out = (long long)i * p.hk * page_rows * p.head_dim;
-#pragma unroll 2
+#pragma unroll 4
       for (int e = tid; e < p.hk * row_chunks; e += kThreads) {
         const int h = e / row_chunks, rest = e - h * row_chunks;
         const int r = rest / chunks, c = rest - r * chunks;
@@ -733,7 +733,7 @@ cudaError_t launch_read8(const Read8Params& p, int dtype, cudaStream_t s) {
 }
 
 cudaError_t launch_expand8(const Expand8Params& p, int dtype, int grid, cudaStream_t s) {
-  const dim3 ctas(4 * grid), block(kThreads);
+  const dim3 ctas(6 * grid), block(kThreads);
   return dtype == MOE_ATTN_BF16 ? launch_after(expand8_kernel<Bf16>, ctas, block, 0, s, p)
                                 : launch_after(expand8_kernel<Fp16>, ctas, block, 0, s, p);
 }
