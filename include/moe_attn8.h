@@ -87,7 +87,7 @@ typedef struct moe_attn_extent {
   int64_t table_stride;
   int32_t columns;           /* first[s] + rows of s <= columns * page_size <= 2^29    */
   int32_t num_seqs;
-  int32_t num_rows;          /* of the outputs                                         */
+  int32_t num_rows;          /* of the outputs, up to 2^30                             */
 } moe_attn_extent;
 
 /* q_out = norm and rotary positions of q [num_tokens, q_heads, head_dim], k_out of k

@@ -162,6 +162,10 @@ def test_python_refusals(L):
         moe.moe_attn_norm_rope_backward(x, None, x, None, pos, freq, None)
     with pytest.raises(ValueError, match="torch stream"):
         moe.moe_attn_norm_rope_backward(x, None, x, None, pos, freq, moe.HeadNorm(w, w), stream=64)
+    with pytest.raises(ValueError, match="needed"):
+        moe.moe_attn_norm_rope(None, None, pos, freq, moe.HeadNorm(w, w))
+    with pytest.raises(ValueError, match="needed"):
+        moe.moe_attn_norm_rope_backward(None, None, None, None, pos, freq, moe.HeadNorm(w, w))
 
 
 def test_cache_of_8_bits():

@@ -266,3 +266,45 @@ def test_masks_that_leave_nothing():
     assert not out[0].any() and bool((lse[0] == -math.inf).all())
     assert layer.check_device_errors() == 0
     ac.check_attention(out[1:], lse[1:], b.want[1:], b.bound[1:], b.want_lse[1:], BF)
+
+
+def test_expanded_weights_are_refused():
+    # a gradient of their shape would have rows that no head has
+    x = torch.zeros(2, 3, 64, dtype=BF, device=DEV)
+    pos, freq = torch.zeros(2, dtype=torch.int32, device=DEV), ac.frequencies(64).to(DEV)
+    w = torch.ones(64, dtype=BF, device=DEV)
+    for call in (lambda n: moe.moe_attn_norm_rope(x, None, pos, freq, n),
+                 lambda n: moe.moe_attn_norm_rope_backward(x, None, x, None, pos, freq, n)):
+        with pytest.raises(ValueError, match="q_weight"):
+            call(moe.HeadNorm(w.expand(3, 64), None))
+    shapes = [t.shape for t in moe.moe_attn_norm_rope_backward(
+        x[:, :1], None, x[:, :1], None, pos, freq, moe.HeadNorm(w[None], None)) if t is not None]
+    assert shapes == [(2, 1, 64), (1, 64)]
+
+
+def test_read8_of_too_many_rows_is_refused():
+    layer = moe.PagedAttention(1, 1, 16, 16, 8, 2)
+    c = moe.attention
+    byte = torch.zeros(1024, device=DEV)
+    at = byte.data_ptr()
+    rows = c.moe_attn_rows(at, 16, 16)
+    cache = c.moe_attn_cache8(at, at, at, at, 1, 256, 16, 256, 0, 0, 0)
+    for n, status in ((2**30 + 1, -3), (2**31 - 1, -3), (-1, -1)):  # too many, invalid
+        extent = c.moe_attn_extent(at, at, at, 1, 1, 1, n)
+        assert layer._library.moe_attn_read8(layer.handle, cache, extent, rows, rows, None) == status
+
+
+def test_no_room_to_bring_keys_to_16_bits():
+    # torch has no memory for it: the call goes on without
+    b = a8.Batch8([(300, 4000)] * 3, 8, 2, 128, 64, BF)
+    layer = moe.PagedAttention(8, 2, 128, 64, b.tokens, 3)
+    out, lse = torch.empty_like(b.q), torch.empty(b.tokens, 8, device=DEV)
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 20)) / total)
+    try:
+        b.run(layer, out=out, lse=lse)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert layer.check_device_errors() == 0
+    b.check(out, lse)

@@ -344,7 +344,7 @@ int moe_attn_read8(moe_attn_handle* h, const moe_attn_cache8* cache, const moe_a
                    const moe_attn_rows* k_out, const moe_attn_rows* v_out, void* stream) {
   if (!h || !e || e->num_seqs < 0 || e->num_rows < 0) return MOE_ATTN_ERR_INVALID_ARG;
   const moe_attn_config& c = h->cfg;
-  if (e->num_seqs > c.max_seqs) return MOE_ATTN_ERR_TOO_MANY_TOKENS;
+  if (e->num_seqs > c.max_seqs || e->num_rows > (1 << 30)) return MOE_ATTN_ERR_TOO_MANY_TOKENS;
   int st = validate_cache8(c, cache);
   if (st != MOE_ATTN_OK || e->num_seqs == 0 || e->num_rows == 0) return st;
   if ((st = validate_rows(k_out)) != MOE_ATTN_OK || (st = validate_rows(v_out)) != MOE_ATTN_OK)

@@ -339,7 +339,8 @@ static int weight_of(PyObject* t, long long heads, long long dim, PyObject* dtyp
   long long d[MAX_DIMS], s[MAX_DIMS];
   const int n = shape_of(t, d);
   if (n < 0 || strides_of(t, s) < 0) return -1;
-  const int each = n == 2 && d[0] == heads;
+  /* (an expanded weight is one of all heads: its gradient has no row for each) */
+  const int each = n == 2 && d[0] == heads && (heads == 1 || s[0] > 0);
   if (!(n == 1 || each) || d[n - 1] != dim || (s[n - 1] != 1 && dim > 1)) {
     PyErr_Format(PyExc_ValueError, "%s must be [%lld] or [%lld, %lld], contiguous along head_dim",
                  what, dim, heads, dim);
@@ -710,15 +711,23 @@ static PyObject* forward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     Py_DECREF(lse);
     return NULL;
   }
-  /* room for keys in 16 bits: torch's memory of the current stream */
+  /* room for keys in 16 bits: torch's memory of the current stream; where it has no
+   * more (a RuntimeError), the call goes on without */
   size_t bytes = 0;
   void* room = NULL;
   PyObject* scratch = NULL;
   if (bits8 && a[19] == Py_None) {
-    if (checked(G.scratch(l->handle, &b, &bytes), "moe_attn_forward8_scratch_bytes") ||
-        (bytes && (!(scratch = new_tensor(Py_BuildValue("(L)", (long long)(bytes / 4)), G.f32,
-                                          l->device)) ||
-                   pointer_of(scratch, &room)))) {
+    int bad = checked(G.scratch(l->handle, &b, &bytes), "moe_attn_forward8_scratch_bytes");
+    if (!bad && bytes) {
+      scratch = new_tensor(Py_BuildValue("(L)", (long long)(bytes / 4)), G.f32, l->device);
+      if (scratch)
+        bad = pointer_of(scratch, &room);
+      else if (PyErr_ExceptionMatches(PyExc_RuntimeError))
+        PyErr_Clear();
+      else
+        bad = -1;
+    }
+    if (bad) {
       Py_XDECREF(scratch);
       Py_DECREF(out);
       Py_DECREF(lse);
@@ -817,6 +826,10 @@ static int heads_of(PyObject* q, PyObject* k, PyObject* positions, PyObject* fre
                     PyObject* layout, PyObject* magnitude, PyObject* stream, heads_t* t) {
   PyObject* x = q != Py_None ? q : k;
   t->device = NULL;
+  if (x == Py_None) {
+    PyErr_SetString(PyExc_ValueError, "q or k is needed");
+    return -1;
+  }
   t->dtype = PyObject_GetAttr(x, G.dtype);
   if (!t->dtype) return -1;
   Py_DECREF(t->dtype); /* torch keeps its types for good */
