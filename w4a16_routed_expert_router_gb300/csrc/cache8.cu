@@ -51,15 +51,16 @@ __device__ __forceinline__ float size_of(float x) {
 __device__ __forceinline__ bool power_of_two(float s) {
   return (__float_as_int(s) & 0x807fffff) == 0;
 }
-// what x / scale is: exactly the product where the scale is a power of two
+// what x / scale is: exactly the product where the scale is a power of two (all scales
+// that append wrote; chosen once for a run: a choice for each value made the kernel 1.5
+// times as long)
+struct Times {
+  float inverse;
+  __device__ __forceinline__ float operator()(float x) const { return x * inverse; }
+};
 struct Divide {
-  float scale, inverse;
-  bool exact;
-  __device__ __forceinline__ explicit Divide(float s)
-      : scale(s), inverse(1.0f / s), exact(power_of_two(s)) {}
-  __device__ __forceinline__ float operator()(float x) const {
-    return exact ? x * inverse : __fdiv_rn(x, scale);
-  }
+  float scale;
+  __device__ __forceinline__ float operator()(float x) const { return __fdiv_rn(x, scale); }
 };
 
 // ------------------------------------------------------------------ append
@@ -80,8 +81,8 @@ struct RowsOf;
 
 template <typename T, bool IL>
 struct RowsOf<T, IL, true> {
-  // 16 lanes a row with interleaved pairs (8 or fewer otherwise): 2 rows (4) at a time
-  static constexpr int kSteps = IL ? 4 : 2, kValues = IL ? 8 : 16;
+  // 8 lanes a row or fewer: 4 rows at a time
+  static constexpr int kSteps = 2, kValues = 16;
   Lane<IL> lane;
   int lanes, group, rows;
   bool active;
@@ -109,12 +110,12 @@ struct RowsOf<T, IL, true> {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       unpack8<T>(a[i], v[i]);
-      if (!IL) unpack8<T>(b[i], v[i] + (IL ? 0 : 8));
+      unpack8<T>(b[i], v[i] + 8);
     }
   }
   __device__ __forceinline__ void norm(const Norm& n, int h, float mean) {
     float sum[kSteps];
-    lane.template weights<T>(n.k_weight, h * n.k_head, n.wide, n.offset, w, w + (IL ? 0 : 8));
+    lane.template weights<T>(n.k_weight, h * n.k_head, n.wide, n.offset, w, w + 8);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       sum[i] = 0.0f;
@@ -138,7 +139,7 @@ struct RowsOf<T, IL, true> {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int k = min(i * rows + group, n - 1);
-      lane.turn(v[i], v[i] + (IL ? 0 : 8), cosines + k * pairs, sines + k * pairs);
+      lane.turn(v[i], v[i] + 8, cosines + k * pairs, sines + k * pairs);
     }
   }
   __device__ __forceinline__ float top() const {
@@ -152,7 +153,8 @@ struct RowsOf<T, IL, true> {
     }
     return m;
   }
-  static __device__ __forceinline__ uint2 codes(const float* f, const Divide& by) {
+  template <class By>
+  static __device__ __forceinline__ uint2 codes(const float* f, const By& by) {
     uint32_t c[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -160,16 +162,17 @@ struct RowsOf<T, IL, true> {
              (uint32_t)to_codes(by(f[4 * i + 2]), by(f[4 * i + 3])) << 16;
     return make_uint2(c[0], c[1]);
   }
-  // at(k): where row k goes
-  template <class At>
-  __device__ __forceinline__ void store(const Divide& by, int n, const At& at) const {
+  // row_of(k): the block's row that row k goes to, asked for by all lanes at once
+  template <class By, class RowOf>
+  __device__ __forceinline__ void store(const By& by, int n, uint8_t* block, long long token,
+                                        const RowOf& row_of) const {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int k = i * rows + group;
+      const int k = i * rows + group, to = row_of(k);
       if (!active || k >= n) continue;
-      uint8_t* row = at(k) + lane.at;
+      uint8_t* row = block + to * token + lane.at;
       *reinterpret_cast<uint2*>(row) = codes(v[i], by);
-      if (lane.two) *reinterpret_cast<uint2*>(row + lane.gap) = codes(v[i] + (IL ? 0 : 8), by);
+      if (lane.two) *reinterpret_cast<uint2*>(row + lane.gap) = codes(v[i] + 8, by);
     }
   }
 };
@@ -225,13 +228,16 @@ struct RowsOf<T, false, false> {
       for (int k = 0; k < kLane; ++k) m = fmaxf(m, size_of(v[i][k]));
     return m;
   }
-  template <class At>
-  __device__ __forceinline__ void store(const Divide& by, int n, const At& at) const {
+  template <class By, class RowOf>
+  __device__ __forceinline__ void store(const By& by, int n, uint8_t* block, long long token,
+                                        const RowOf& row_of) const {
 #pragma unroll
-    for (int i = 0; i < kWarpRows; ++i)
+    for (int i = 0; i < kWarpRows; ++i) {
+      uint8_t* row = block + row_of(i) * token;
 #pragma unroll
       for (int k = 0; k < kLane; ++k)
-        if (i < n && index(k) < dim) at(i)[index(k)] = (uint8_t)to_codes(by(v[i][k]), 0.0f);
+        if (i < n && index(k) < dim) row[index(k)] = (uint8_t)to_codes(by(v[i][k]), 0.0f);
+    }
   }
 };
 
@@ -272,7 +278,7 @@ __device__ __forceinline__ void queries(const Append8Params& g, const Dims& d, i
   const Lane<IL> lane(u < d.units ? u : 0, d.turned, r.r.rot, r.head_dim);
   float* cosines = table;
   float* sines = table + per_cta * pairs;
-  constexpr int kTokens = IL ? 4 : 2;
+  constexpr int kTokens = 2;
   Chunk8 a[kTokens], b[kTokens];
 #pragma unroll
   for (int t = 0; t < kTokens; ++t) {
@@ -296,7 +302,10 @@ __device__ __forceinline__ void queries(const Append8Params& g, const Dims& d, i
     unpack8<T>(b[t], fb);
     if (g.p.n.on) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum = fmaf(fa[k], fa[k], fmaf(fb[k], fb[k], sum));
+      for (int k = 0; k < 8; ++k) {
+        sum = fmaf(fa[k], fa[k], sum);
+        sum = fmaf(fb[k], fb[k], sum);
+      }
       sum = group_sum(sum, d.lanes);
     }
     if (!active || t >= d.q_tokens || first + t >= cta_tokens) continue;
@@ -357,7 +366,7 @@ __device__ __forceinline__ void queries_any(const Append8Params& g, const Dims& 
 }
 
 template <typename T, bool IL, bool FAST>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
     append8_kernel(const __grid_constant__ Append8Params g, const Dims d) {
   extern __shared__ float4 smem4[];
   __shared__ float tops[kWarps];
@@ -452,19 +461,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (lane == 0 && sub == 0) *scale_at = scale;
     }
-    // (by all lanes: they hand out the rows)
-    const Divide by(scale);
-    int rows[kWarpRows];
-#pragma unroll
-    for (int k = 0; k < kWarpRows; ++k)
-      rows[k] = __shfl_sync(0xffffffffu, row_of, (at + k0 + k) & 31);
-    if (on && mine > 0)
-      of.store(by, mine, [&](int k) {
-        int row = rows[0];
-#pragma unroll
-        for (int q = 1; q < kWarpRows; ++q) row = k == q ? rows[q] : row;
-        return codes + (long long)row * g.c.token;
-      });
+    // (all lanes: they hand out the rows)
+    const auto row = [&](int k) { return __shfl_sync(0xffffffffu, row_of, (at + k0 + k) & 31); };
+    if (on && mine > 0) {
+      if (power_of_two(scale))
+        of.store(Times{1.0f / scale}, mine, codes, g.c.token, row);
+      else
+        of.store(Divide{scale}, mine, codes, g.c.token, row);
+    }
     __syncthreads();  // tops is free again
   }
 }
@@ -475,7 +479,7 @@ cudaError_t launch_append(const Append8Params& g, cudaStream_t s) {
   Dims d{};
   int smem;
   if (FAST) {
-    const Units u = units_of_head<IL>(r.head_dim, r.r.rot);
+    const Units u = units_of_head(r.head_dim, r.r.rot);
     d.units = u.count;
     d.turned = u.turned;
     d.lanes = u.lanes;
@@ -486,7 +490,7 @@ cudaError_t launch_append(const Append8Params& g, cudaStream_t s) {
     const long long all = (long long)r.tokens * d.q_rows;
     while (d.q_z > 1 && (all < 4LL * kSms * d.q_z || d.q_z * r.r.rot > 4096)) d.q_z /= 2;
     d.q_tokens = 1;
-    while (d.q_tokens < (IL ? 4 : 2) && all >= 8LL * kSms * d.q_z * d.q_tokens &&
+    while (d.q_tokens < 2 && all >= 8LL * kSms * d.q_z * d.q_tokens &&
            2 * d.q_tokens * d.q_z * r.r.rot <= 4096)
       d.q_tokens *= 2;
     const int table = d.q_tokens * d.q_z > kRun ? d.q_tokens * d.q_z : kRun;

@@ -11,15 +11,15 @@
 // mean(h n) = r mean(h x), so both sums over a head, of x^2 and of h x, are taken
 // together. Each thread keeps one unit of one head for many tokens and adds up that
 // unit's dw; a CTA adds its rows in order, and a second launch the CTAs.
+#include <algorithm>
+
 #include "norm_parts.cuh"
 
 namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kMaxThreads = 512;
 constexpr int kSms = 152;
-constexpr int tokens_of(bool two_chunks) { return two_chunks ? 2 : 4; }
 
 // where a key or value of token t goes in the pages, or null
 __device__ __forceinline__ uint16_t* page_row(const RopeParams& r, bool key, int t, int h) {
@@ -57,94 +57,52 @@ struct Head {
   }
 };
 
-template <typename T, bool IL>
-__global__ void __launch_bounds__(kMaxThreads, 2)
-    norm_rope_kernel(const __grid_constant__ NormParams p, int tokens_per_thread, int units, int turned) {
-  extern __shared__ float4 table4[];  // cosines, then sines: [tokens of the CTA][rot / 2]
-  float* cosines = reinterpret_cast<float*>(table4);
-  constexpr int kTokens = tokens_of(!IL);
-  const RopeParams& r = p.r;
-  const int pairs = r.r.rot >> 1;
-  const int tokens_per_cta = tokens_per_thread * blockDim.z;
-  const int cta0 = blockIdx.x * tokens_per_cta;
-  const int cta_tokens = min(tokens_per_cta, r.tokens - cta0);
-  const int first = threadIdx.z * tokens_per_thread, t0 = cta0 + first;
-  const int nt = min(tokens_per_thread, cta_tokens - first);
-  float* sines = cosines + tokens_per_cta * pairs;
+// Where rows go in a launch that writes keys and values to pages.
+struct PagedRun {
+  const RopeParams& r;
+  RowRun run;
+  bool key, paged;
+  int h, at;
+  __device__ __forceinline__ uint16_t* next(int t) {
+    if (!paged) return run.next(t);
+    uint16_t* row = page_row(r, key, t, h);
+    return row ? row + at : nullptr;
+  }
+};
 
+template <typename T, bool IL, bool PAGES>
+__global__ void __launch_bounds__(kWalkThreads, 3)
+    norm_rope_kernel(const __grid_constant__ NormParams p, int units, int turned) {
+  extern __shared__ float4 smem4[];
+  const RopeParams& r = p.r;
   wait_prior_launch();
   let_next_launch();
   const int u = threadIdx.x, hd = blockIdx.y * blockDim.y + threadIdx.y;
   const bool active = hd < r.hq + r.hk + r.hv && u < units;
   const Head hh(r, active ? hd : 0);
   const Lane<IL> lane(active ? u : 0, turned, r.r.rot, r.head_dim);
-  const Rows in = hh.in(r);
-  const uint16_t* src = in.p + (long long)t0 * in.token + (long long)hh.h * in.head + lane.at;
-  Chunk8 a[kTokens], b[kTokens];
-#pragma unroll
-  for (int t = 0; t < kTokens; ++t) {
-    a[t].v = b[t].v = make_uint4(0, 0, 0, 0);
-    if (active && t < nt) {
-      a[t].v = *reinterpret_cast<const uint4*>(src + t * in.token);
-      if (lane.two) b[t].v = *reinterpret_cast<const uint4*>(src + t * in.token + lane.gap);
-    }
-  }
-  float wa[8], wb[8];
-  if (active && !hh.value)
-    lane.template weights<T>(hh.key ? p.n.k_weight : p.n.q_weight,
-                             hh.h * (hh.key ? p.n.k_head : p.n.q_head), p.n.wide, p.n.offset, wa,
-                             wb);
-  const int tid = (threadIdx.z * blockDim.y + threadIdx.y) * blockDim.x + threadIdx.x;
-  fill_table(r.r, r.positions + cta0, cta_tokens, cosines, sines, tid,
-             blockDim.x * blockDim.y * blockDim.z);
-  __syncthreads();
-  const bool paged = r.slots && (hh.key || hh.value);
-  const Rows o = Head::pick(hh.key, p.k_out, r.q_out);
-  uint16_t* out = o.p + (long long)t0 * o.token + (long long)hh.h * o.head + lane.at;
-  const float mean = 1.0f / (float)r.head_dim;
-  float sum[kTokens];
-#pragma unroll
-  for (int t = 0; t < kTokens; ++t) {
-    float fa[8], fb[8];
-    unpack8<T>(a[t], fa);
-    unpack8<T>(b[t], fb);
-    sum[t] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sum[t] = fmaf(fa[k], fa[k], sum[t]);
-    if (!IL) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum[t] = fmaf(fb[k], fb[k], sum[t]);
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < kTokens; ++t) sum[t] = group_sum(sum[t], blockDim.x);
-#pragma unroll
-  for (int t = 0; t < kTokens; ++t) {
-    if (!active || t >= nt) continue;
-    float fa[8], fb[8];
-    unpack8<T>(a[t], fa);
-    unpack8<T>(b[t], fb);
-    uint16_t* dst = out + t * o.token;
-    if (paged) {
-      dst = page_row(r, hh.key, t0 + t, hh.h);
-      if (!dst) continue;
-      dst += lane.at;
-    }
-    if (!hh.value) {
-      const float f = rsqrtf(fmaf(sum[t], mean, p.n.eps));
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        fa[k] = fa[k] * f * wa[k];
-        if (lane.two) fb[k] = fb[k] * f * wb[k];
-      }
-      if (lane.turns)
-        lane.turn(fa, fb, cosines + (first + t) * pairs, sines + (first + t) * pairs);
-      a[t].v = pack8<T>(fa);
-      b[t].v = pack8<T>(fb);
-    }
-    *reinterpret_cast<uint4*>(dst) = a[t].v;
-    if (lane.two) *reinterpret_cast<uint4*>(dst + lane.gap) = b[t].v;
-  }
+  Walk k;
+  k.tid = (threadIdx.z * blockDim.y + threadIdx.y) * blockDim.x + threadIdx.x;
+  k.threads = blockDim.x * blockDim.y * blockDim.z;
+  k.lanes = blockDim.x;
+  k.z = threadIdx.z;
+  k.zs = blockDim.z;
+  k.c0 = blockIdx.x * k.zs;
+  k.step = gridDim.x * k.zs;
+  const Rows in = hh.in(r), o = Head::pick(hh.key, p.k_out, r.q_out);
+  const long long first = k.c0 + k.z;
+  const RowRun run = {o.p + first * o.token + (long long)hh.h * o.head + lane.at, o.token * k.step};
+  const auto walk = [&](auto out) {
+    norm_walk<T, IL>(k, r.r, r.positions, r.tokens, r.head_dim, p.n, lane, active, hh.value,
+                     in.p + first * in.token + (long long)hh.h * in.head + lane.at, in.token,
+                     hh.key ? p.n.k_weight : p.n.q_weight,
+                     hh.h * (hh.key ? p.n.k_head : p.n.q_head), reinterpret_cast<float*>(smem4),
+                     out);
+  };
+  if constexpr (PAGES)
+    walk(PagedRun{r, run, hh.key, hh.key || hh.value, hh.h, lane.at});
+  else
+    walk(run);
 }
 
 constexpr int kAnyWarps = 8;
@@ -200,25 +158,23 @@ __global__ void __launch_bounds__(kAnyWarps * 32)
 template <typename T, bool IL>
 cudaError_t launch_fast(const NormParams& p, cudaStream_t s) {
   const RopeParams& r = p.r;
-  const Units u = units_of_head<IL>(r.head_dim, r.r.rot);
+  const Units u = units_of_head(r.head_dim, r.r.rot);
   const int heads = r.hq + r.hk + r.hv;
-  // as in launch_il of the rotation alone: groups of heads of at most kMaxThreads
-  // threads, tokens side by side where heads are few, several tokens to a thread
-  // where every SM has enough
-  const int most = kMaxThreads / u.lanes;
+  // groups of heads of at most kWalkThreads threads, tokens side by side where heads are
+  // few, and as many CTAs along the tokens as the GPU takes at once
+  const int most = kWalkThreads / u.lanes;
   const int groups = (heads + most - 1) / most;
   dim3 block(u.lanes, (heads + groups - 1) / groups, 1);
-  const long long all = (long long)r.tokens * groups;
-  while (block.x * block.y * block.z <= 128 && block.z < 64 && all >= 4LL * kSms * block.z &&
-         2 * block.z * r.r.rot <= 4096)
+  while (2 * block.x * block.y * block.z <= kWalkThreads && block.z < 64 &&
+         2 * block.z * r.r.rot <= 1024 &&
+         (long long)r.tokens * groups >= 8LL * kSms * block.z)
     block.z *= 2;
-  int tokens = 1;
-  while (tokens < tokens_of(!IL) && all >= 8LL * kSms * block.z * tokens &&
-         2 * tokens * block.z * r.r.rot <= 4096)
-    tokens *= 2;
-  const int cta = tokens * block.z;
-  return launch_after(norm_rope_kernel<T, IL>, dim3((r.tokens + cta - 1) / cta, groups), block,
-                      cta * r.r.rot * (int)sizeof(float), s, p, tokens, u.count, u.turned);
+  const int threads = block.x * block.y * block.z;
+  const int want = std::max(1, kSms * (3 * kWalkThreads / threads) / groups);
+  const int all = (r.tokens + block.z - 1) / block.z;
+  return launch_after(r.slots ? norm_rope_kernel<T, IL, true> : norm_rope_kernel<T, IL, false>,
+                      dim3(std::min(want, all), groups), block,
+                      (int)Walk::bytes(block.z, r.r.rot), s, p, u.count, u.turned);
 }
 
 bool fits(const NormParams& p) {
@@ -295,12 +251,7 @@ __global__ void __launch_bounds__(kGradThreads, 2)
       const int row = i / pairs, c = i - row * pairs;
       const int t = c0 + row / z * step + row % z;
       if (t >= r.tokens) continue;
-      const long long phase = (long long)((unsigned long long)(long long)r.positions[t] *
-                                          (unsigned long long)r.r.freq[c]);
-      float sn, cn;
-      sincospif((float)(int)(phase >> 32) * 0x1p-31f, &sn, &cn);
-      smem[i] = cn * r.r.magnitude;
-      smem[kTables * z * pairs + i] = sn * r.r.magnitude * r.r.sign;
+      cos_sin(r.r, r.positions[t], c, smem[i], smem[kTables * z * pairs + i]);
     }
   };
   const int step = gridDim.x * z;
@@ -486,7 +437,7 @@ __global__ void __launch_bounds__(32 * kAddRows) norm_grad_add_kernel(const AddP
 template <typename T, bool IL>
 cudaError_t launch_grad_fast(const NormGradParams& g, const NormGradPlan& n, cudaStream_t s) {
   const RopeParams& r = g.p.r;
-  const Units u = units_of_head<IL>(r.head_dim, r.r.rot);
+  const Units u = units_of_head(r.head_dim, r.r.rot);
   const int shared = (!r.hq || g.p.n.q_head == 0) && (!r.hk || g.p.n.k_head == 0);
   const int table = 2 * kTables * n.z * (r.r.rot / 2), sums = n.rows * n.z * r.head_dim;
   cudaError_t e = launch_after(norm_grad_kernel<T, IL>, dim3(n.parts, n.groups),
@@ -546,8 +497,7 @@ cudaError_t launch_norm_rope_grad(const NormGradParams& g, int dtype, cudaStream
   a.heads_q = r.hq;
   cudaError_t e;
   if (fast) {
-    const int lanes = r.r.interleaved ? units_of_head<true>(r.head_dim, r.r.rot).lanes
-                                      : units_of_head<false>(r.head_dim, r.r.rot).lanes;
+    const int lanes = units_of_head(r.head_dim, r.r.rot).lanes;
     const NormGradPlan n = norm_grad_plan(r.tokens, heads, lanes);
     if (shared) {  // two rows a CTA, of the queries and of the keys
       a.outer = n.parts * n.groups;
