@@ -10,13 +10,15 @@
 // normed and turned on the way, and kept in registers between the largest value and the
 // codes. Queries are normed and turned by CTAs of the same launch.
 // Bound by memory.
+#include <algorithm>
+
 #include "norm_parts.cuh"
 
 namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = kWalkThreads, kWarps = kThreads / 32;
 constexpr int kSms = 152;
 constexpr int kRun = kScaleBlock;
 
@@ -66,9 +68,10 @@ struct Divide {
 // ------------------------------------------------------------------ append
 struct Dims {  // of a launch
   int kv_ctas, token_groups;          // CTAs of keys and values; of queries along the tokens
-  int q_heads, q_z, q_tokens;         // heads of one, tokens side by side, tokens of a thread
+  int q_heads, q_z;                   // heads of one, tokens side by side
   int q_rows;                         // groups of heads
-  int split, combos;                  // CTAs that share a window's runs; of 4 (half, head)s
+  int split, combos, loops;           // CTAs that share a window's runs; of `loops` times
+                                      // 4 (half, head)s
   int units, turned, lanes;
 };
 
@@ -265,65 +268,28 @@ __device__ __forceinline__ void reexpress(uint8_t* block, long long token, int d
 // Queries: norm and rotation, a lane group a head, as in norm_rope.cu.
 template <typename T, bool IL>
 __device__ __forceinline__ void queries(const Append8Params& g, const Dims& d, int cta,
-                                        float* table) {
+                                        float* smem) {
   const RopeParams& r = g.p.r;
-  const int pairs = r.r.rot >> 1;
   const int tg = cta % d.token_groups, hg = cta / d.token_groups;
   const int u = threadIdx.x & (d.lanes - 1), y = threadIdx.x / d.lanes;
-  const int z = y / d.q_heads, hd = hg * d.q_heads + (y - z * d.q_heads);
-  const int per_cta = d.q_tokens * d.q_z, cta0 = tg * per_cta;
-  const int cta_tokens = min(per_cta, r.tokens - cta0);
-  const int first = z * d.q_tokens;
-  const bool active = z < d.q_z && hd < r.hq && u < d.units;
+  Walk k;
+  k.tid = threadIdx.x;
+  k.threads = kThreads;
+  k.lanes = d.lanes;
+  k.z = y / d.q_heads;
+  k.zs = d.q_z;
+  k.c0 = tg * d.q_z;
+  k.step = d.token_groups * d.q_z;
+  const int hd = hg * d.q_heads + (y - k.z * d.q_heads);
+  const bool active = k.z < d.q_z && hd < r.hq && u < d.units;
+  if (!active) k.z = 0;
   const Lane<IL> lane(u < d.units ? u : 0, d.turned, r.r.rot, r.head_dim);
-  float* cosines = table;
-  float* sines = table + per_cta * pairs;
-  constexpr int kTokens = 2;
-  Chunk8 a[kTokens], b[kTokens];
-#pragma unroll
-  for (int t = 0; t < kTokens; ++t) {
-    a[t].v = b[t].v = make_uint4(0, 0, 0, 0);
-    if (active && t < d.q_tokens && first + t < cta_tokens) {
-      const uint16_t* src = r.q.p + (long long)(cta0 + first + t) * r.q.token +
-                            (long long)hd * r.q.head + lane.at;
-      a[t].v = *reinterpret_cast<const uint4*>(src);
-      if (lane.two) b[t].v = *reinterpret_cast<const uint4*>(src + lane.gap);
-    }
-  }
-  float wa[8], wb[8];
-  if (active && g.p.n.on)
-    lane.template weights<T>(g.p.n.q_weight, hd * g.p.n.q_head, g.p.n.wide, g.p.n.offset, wa, wb);
-  fill_table(r.r, r.positions + cta0, cta_tokens, cosines, sines, threadIdx.x, kThreads);
-  __syncthreads();
-#pragma unroll
-  for (int t = 0; t < kTokens; ++t) {
-    float fa[8], fb[8], sum = 0.0f;
-    unpack8<T>(a[t], fa);
-    unpack8<T>(b[t], fb);
-    if (g.p.n.on) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        sum = fmaf(fa[k], fa[k], sum);
-        sum = fmaf(fb[k], fb[k], sum);
-      }
-      sum = group_sum(sum, d.lanes);
-    }
-    if (!active || t >= d.q_tokens || first + t >= cta_tokens) continue;
-    if (g.p.n.on) {
-      const float f = rsqrtf(fmaf(sum, 1.0f / (float)r.head_dim, g.p.n.eps));
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        fa[k] = fa[k] * f * wa[k];
-        if (lane.two) fb[k] = fb[k] * f * wb[k];
-      }
-    }
-    if (lane.turns)
-      lane.turn(fa, fb, cosines + (first + t) * pairs, sines + (first + t) * pairs);
-    uint16_t* dst = r.q_out.p + (long long)(cta0 + first + t) * r.q_out.token +
-                    (long long)hd * r.q_out.head + lane.at;
-    *reinterpret_cast<uint4*>(dst) = pack8<T>(fa);
-    if (lane.two) *reinterpret_cast<uint4*>(dst + lane.gap) = pack8<T>(fb);
-  }
+  const long long first = k.c0 + k.z, h = active ? hd : 0;
+  norm_walk<T, IL>(
+      k, r.r, r.positions, r.tokens, r.head_dim, g.p.n, lane, active, false,
+      r.q.p + first * r.q.token + h * r.q.head + lane.at, r.q.token, g.p.n.q_weight,
+      h * g.p.n.q_head, smem,
+      RowRun{r.q_out.p + first * r.q_out.token + h * r.q_out.head + lane.at, r.q_out.token * k.step});
 }
 
 // Queries in the form for any rows: a warp a head.
@@ -366,7 +332,7 @@ __device__ __forceinline__ void queries_any(const Append8Params& g, const Dims& 
 }
 
 template <typename T, bool IL, bool FAST>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     append8_kernel(const __grid_constant__ Append8Params g, const Dims d) {
   extern __shared__ float4 smem4[];
   __shared__ float tops[kWarps];
@@ -383,8 +349,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     return;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp & 1;
-  const int first_combo = cta % d.combos * (kWarps / 2);
-  const int combo = first_combo + (warp >> 1);         // K heads, then V heads
+  const int first_combo = cta % d.combos * d.loops * (kWarps / 2);  // K heads, then V heads
   cta /= d.combos;
   const int part = cta % d.split, w0 = cta / d.split * kRun;
   // lane l has token w0 - 1 + l: the one before the window, the window, and what runs
@@ -403,10 +368,7 @@ __global__ void __launch_bounds__(kThreads, 3)
                        prev / kScaleBlock == slot / kScaleBlock;
   const unsigned go_on = __ballot_sync(0xffffffffu, follows);
   unsigned begin = __ballot_sync(0xffffffffu, slot >= 0 && !follows && lane > 0 && lane <= kRun);
-  const bool key = combo < r.hk, on = combo < 2 * r.hk;
   const bool any_keys = first_combo < r.hk;            // in the CTA
-  const int h = key ? combo : combo - r.hk;
-  const Rows& in = key ? r.k : r.v;
   const int pairs = r.r.rot >> 1;
   float *cosines = smem, *sines = smem + kRun * pairs;
   for (int i = 0; begin; ++i) {
@@ -425,51 +387,56 @@ __global__ void __launch_bounds__(kThreads, 3)
     const long long page = slot0 >> r.page_shift;
     const int in_page = (int)(slot0 - (page << r.page_shift));
     const int first = in_page & (kScaleBlock - 1), block = in_page / kScaleBlock;
-    uint8_t* codes = (key ? g.c.k : g.c.v) + page * g.c.page + (long long)h * g.c.head +
-                     (long long)(in_page - first) * g.c.token;
-    float* scale_at = (key ? g.c.k_scales : g.c.v_scales) + page * g.c.scale_page +
-                      h * g.c.scale_head + block * g.c.scale_block;
-    RowsOf<T, IL, FAST> of(d, r, smem);
-    float top = 0.0f, before = 0.0f;
-    if (on) {
-      if (first) before = *scale_at;
-      if (mine > 0)
-        of.load(in.p + (long long)(t0 + k0) * in.token + (long long)h * in.head, in.token, mine);
-    }
-    if (FAST && any_keys) {
+    if (FAST && any_keys)
       fill_table(r.r, r.positions + t0, n, cosines, sines, threadIdx.x, kThreads);
-      __syncthreads();
-    }
-    if (on && mine > 0) {
-      if (key) {
-        if (g.p.n.on) of.norm(g.p.n, h, 1.0f / (float)r.head_dim);
-        of.turn(r, cosines + k0 * pairs, sines + k0 * pairs, t0 + k0, mine);
+    for (int loop = 0; loop < d.loops; ++loop) {
+      const int combo = first_combo + loop * (kWarps / 2) + (warp >> 1);
+      const bool key = combo < r.hk, on = combo < 2 * r.hk;
+      const int h = key ? combo : combo - r.hk;
+      const Rows& in = key ? r.k : r.v;
+      uint8_t* codes = (key ? g.c.k : g.c.v) + page * g.c.page + (long long)h * g.c.head +
+                       (long long)(in_page - first) * g.c.token;
+      float* scale_at = (key ? g.c.k_scales : g.c.v_scales) + page * g.c.scale_page +
+                        h * g.c.scale_head + block * g.c.scale_block;
+      RowsOf<T, IL, FAST> of(d, r, smem);
+      float top = 0.0f, before = 0.0f;
+      if (on) {
+        if (first) before = *scale_at;
+        if (mine > 0)
+          of.load(in.p + (long long)(t0 + k0) * in.token + (long long)h * in.head, in.token, mine);
       }
-      top = of.top();
-    }
+      if (FAST && any_keys && loop == 0) __syncthreads();  // the table is there
+      if (on && mine > 0) {
+        if (key) {
+          if (g.p.n.on) of.norm(g.p.n, h, 1.0f / (float)r.head_dim);
+          of.turn(r, cosines + k0 * pairs, sines + k0 * pairs, t0 + k0, mine);
+        }
+        top = of.top();
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();  // (and the old scale is read, and the table done with)
-    float scale = scale_for(fmaxf(top, tops[warp ^ 1]));
-    if (on) {
-      if (first && before > 0.0f && before < INFINITY) {
-        if (before >= scale)
-          scale = before;
-        else
-          reexpress(codes, g.c.token, r.head_dim, written, before / scale, sub);
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (lane == 0) tops[warp] = top;
+      __syncthreads();  // (and the old scale is read)
+      float scale = scale_for(fmaxf(top, tops[warp ^ 1]));
+      if (on) {
+        if (first && before > 0.0f && before < INFINITY) {
+          if (before >= scale)
+            scale = before;
+          else
+            reexpress(codes, g.c.token, r.head_dim, written, before / scale, sub);
+        }
+        if (lane == 0 && sub == 0) *scale_at = scale;
       }
-      if (lane == 0 && sub == 0) *scale_at = scale;
+      // (all lanes: they hand out the rows)
+      const auto row = [&](int k) { return __shfl_sync(0xffffffffu, row_of, (at + k0 + k) & 31); };
+      if (on && mine > 0) {
+        if (power_of_two(scale))
+          of.store(Times{1.0f / scale}, mine, codes, g.c.token, row);
+        else
+          of.store(Divide{scale}, mine, codes, g.c.token, row);
+      }
+      __syncthreads();  // tops is free again, and at the end the table
     }
-    // (all lanes: they hand out the rows)
-    const auto row = [&](int k) { return __shfl_sync(0xffffffffu, row_of, (at + k0 + k) & 31); };
-    if (on && mine > 0) {
-      if (power_of_two(scale))
-        of.store(Times{1.0f / scale}, mine, codes, g.c.token, row);
-      else
-        of.store(Divide{scale}, mine, codes, g.c.token, row);
-    }
-    __syncthreads();  // tops is free again
   }
 }
 
@@ -486,16 +453,16 @@ cudaError_t launch_append(const Append8Params& g, cudaStream_t s) {
     const int most = kThreads / u.lanes;
     d.q_rows = (r.hq + most - 1) / most;
     d.q_heads = d.q_rows ? (r.hq + d.q_rows - 1) / d.q_rows : 1;
-    d.q_z = most / d.q_heads;
-    const long long all = (long long)r.tokens * d.q_rows;
-    while (d.q_z > 1 && (all < 4LL * kSms * d.q_z || d.q_z * r.r.rot > 4096)) d.q_z /= 2;
-    d.q_tokens = 1;
-    while (d.q_tokens < 2 && all >= 8LL * kSms * d.q_z * d.q_tokens &&
-           2 * d.q_tokens * d.q_z * r.r.rot <= 4096)
-      d.q_tokens *= 2;
-    const int table = d.q_tokens * d.q_z > kRun ? d.q_tokens * d.q_z : kRun;
-    smem = table * r.r.rot * (int)sizeof(float);
-    d.token_groups = (r.tokens + d.q_tokens * d.q_z - 1) / (d.q_tokens * d.q_z);
+    d.q_z = 1;
+    while (2 * d.q_z * d.q_heads <= most && 2 * d.q_z * r.r.rot <= 1024 &&
+           (long long)r.tokens * d.q_rows >= 8LL * kSms * d.q_z)
+      d.q_z *= 2;
+    // up to 8 tokens to a thread, where every SM has CTAs enough
+    const int all = (r.tokens + d.q_z - 1) / d.q_z;
+    const int few = d.q_rows ? (4 * kSms + d.q_rows - 1) / d.q_rows : 1;
+    d.token_groups = std::min(all, std::max(few, (all + 7) / 8));
+    smem = std::max(kRun * r.r.rot * (int)sizeof(float),
+                    r.hq ? (int)Walk::bytes(d.q_z, r.r.rot) : 0);
   } else {
     d.q_rows = (r.hq + kWarps - 1) / kWarps;
     d.token_groups = r.tokens;
@@ -503,6 +470,12 @@ cudaError_t launch_append(const Append8Params& g, cudaStream_t s) {
   }
   d.combos = (2 * r.hk + kWarps / 2 - 1) / (kWarps / 2);
   const int windows = (r.tokens + kRun - 1) / kRun;
+  // in long calls up to four times four, which share a window's plan and its table
+  d.loops = 1;
+  while (d.loops < 4 && d.combos > 1 && (long long)windows * d.combos > 4 * kSms) {
+    d.loops *= 2;
+    d.combos = (d.combos + 1) / 2;
+  }
   // a window's runs to as many CTAs as the GPU takes at once: decode steps have a run
   // for each token, prompts one for each window
   d.split = kRun;
