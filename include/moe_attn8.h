@@ -32,9 +32,10 @@
  * scale: scores and sums in fp32, codes times queries exact (bf16 queries are
  * brought to fp16 by a power of two for each row, which loses what is below 2^-39 of
  * the row's largest value), and the softmax's numerators, times the scales of V,
- * rounded to fp16 with all bits down to 2^-26 of the largest. What lies behind
- * kv_len is never used; a NaN in a code or scale before it may reach other rows of
- * its sequence.
+ * rounded to fp16 with all bits down to 2^-26 of the largest. Where a call has scratch
+ * and brings the keys to 16 bits, it is moe_attn_forward over those, whose numerators
+ * are rounded to the handle's type. What lies behind kv_len is never used; a NaN in a
+ * code or scale before it may reach other rows of its sequence.
  *
  * Sinks. With a window and sinks > 0, query i at p also sees key j where j <= p and
  * j < sinks. Without a window they change nothing.
@@ -93,8 +94,9 @@ typedef struct moe_attn_extent {
 /* q_out = norm and rotary positions of q [num_tokens, q_heads, head_dim], k_out of k
  * [num_tokens, kv_heads, head_dim], in one launch; q and q_out, or k and k_out, may
  * both be NULL. num_tokens up to 2^30, head_dim 1..256, heads 0..65536, any element
- * strides (16-byte multiples are fastest); an output may be its input, other overlaps are refused, as are
- * outputs whose rows lie on each other. */
+ * strides (16-byte multiples, and rotations of a multiple of 16 values, are fastest); an
+ * output may be its input, other overlaps are refused, as are outputs whose rows lie on
+ * each other. */
 int moe_attn_norm_rope(const moe_attn_rows* q, const moe_attn_rows* q_out, const moe_attn_rows* k,
                        const moe_attn_rows* k_out, const int32_t* positions, int32_t num_tokens,
                        int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t dtype,
@@ -144,7 +146,8 @@ int moe_attn_read8(moe_attn_handle* h, const moe_attn_cache8* cache, const moe_a
 
 /* Device bytes that moe_attn_forward8 works faster with: room for the batch's keys and
  * values in 16 bits, as far as its page table goes, where its sequences have many new
- * tokens (else, and where that were more than 8 GiB, 0). */
+ * tokens (more than 512 query rows to a kv head on average; else, and where that were
+ * more than 8 GiB, 0). */
 int moe_attn_forward8_scratch_bytes(const moe_attn_handle* h, const moe_attn_batch* batch,
                                     size_t* bytes);
 

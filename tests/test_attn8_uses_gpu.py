@@ -166,13 +166,13 @@ def test_many_sequences(seqs, new):
 
 
 def test_many_sequences_brought_to_16_bits():
-    # more sequences than one pass over their pages keeps: 260 rows each
-    lens = [(260, 260)] * 3 + [(0, 50)] * 2100 + [(300, 411)] * 2
-    b = a8.Batch8(lens, 2, 1, 16, 16, BF)
-    b.max_q = 300
-    layer = moe.PagedAttention(2, 1, 16, 16, b.tokens, len(lens))
+    # more sequences than one pass over their pages keeps, 576 rows each, some empty
+    lens = [(9, 9 + i % 40) for i in range(2150)] + [(0, 50)] * 3 + [(90, 411)] * 2
+    b = a8.Batch8(lens, 64, 1, 16, 16, BF)
+    layer = moe.PagedAttention(64, 1, 16, 16, b.tokens, len(lens))
     n = moe.attention.ctypes.c_size_t()
-    batch = moe.attention.moe_attn_batch(None, None, None, 64, b.table.shape[1], 5, b.tokens, 300)
+    batch = moe.attention.moe_attn_batch(None, None, None, b.table.shape[1], b.table.shape[1],
+                                         len(lens), b.tokens, b.max_q)
     assert layer._library.moe_attn_forward8_scratch_bytes(layer.handle, batch, n) == 0 and n.value
     out, lse = b.run(layer)
     assert layer.check_device_errors() == 0

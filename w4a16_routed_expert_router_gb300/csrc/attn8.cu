@@ -132,16 +132,17 @@ Scratch scratch_of(const moe_attn_config& c, const moe_attn_batch* b) {
   s.total = s.table + align256(pages * 4);
   return s;
 }
-// Batches of many tokens are worth it: the kernel over 16 bits takes 1.5 us for 256 query
-// rows by 128 keys on an SM, the one over codes 2.8, and 128 keys of a head take 16 ns
-// (all SMs) to bring to 16 bits, so about 500 rows a sequence and kv head pay for it.
-// (400 rows over 32768 keys 108 us over codes, 104 so; 4000 over 65536 1189 and 700.)
+// Batches of many rows a sequence and kv head are worth it: bringing the keys to 16 bits
+// takes the same for any number of rows, and the kernel over 16 bits is faster for each.
+// Rows over 32768 keys of 8 kv heads, over codes and so: 400 108 and 120 us, 512 109 and
+// 121, 1024 176 and 153, 4000 (over 65536) 1189 and 714; 8 sequences of 8192 keys: 256
+// 104 and 159, 512 180 and 202, 1024 330 and 288.
 constexpr long long kExpandRows = 512;
 constexpr size_t kScratchMost = size_t(8) << 30;
 bool expands(const moe_attn_config& c, const moe_attn_batch* b) {
   const long long group = c.q_heads / c.kv_heads;
   return (long long)b->max_q * group > kDecodeRows &&
-         b->num_tokens * group >= kExpandRows * b->num_seqs &&
+         b->num_tokens * group > kExpandRows * b->num_seqs &&
          (long long)b->num_seqs * b->columns <= 0x7ffffffeLL && scratch_of(c, b).total <= kScratchMost;
 }
 

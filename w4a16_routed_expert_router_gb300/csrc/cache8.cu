@@ -8,8 +8,13 @@
 // window of 16 tokens for the runs that begin there (one, in a prompt; up to 16, in a
 // decode step, which `split` CTAs share), so nothing is planned on the host. Keys are
 // normed and turned on the way, and kept in registers between the largest value and the
-// codes. Queries are normed and turned by CTAs of the same launch.
-// Bound by memory.
+// codes. Queries are normed and turned by CTAs of the same launch, as in norm_rope.cu.
+//
+// Bound by instructions at 72 % of the issue slots: 8191 tokens of 32 + 8 heads of 128,
+// with norms, take 45 us (185 MB, 4.1 TB/s; 27 us at the copy rate). A choice between
+// product and division for each value cost 15 us of 94, four CTAs of 64 registers with
+// some spills save 2 us over three of 80, heads that share a window's plan and its table
+// of cosines 6 us. A decode step of 64 tokens is bound by latency, 6 us.
 #include <algorithm>
 
 #include "norm_parts.cuh"
@@ -54,8 +59,7 @@ __device__ __forceinline__ bool power_of_two(float s) {
   return (__float_as_int(s) & 0x807fffff) == 0;
 }
 // what x / scale is: exactly the product where the scale is a power of two (all scales
-// that append wrote; chosen once for a run: a choice for each value made the kernel 1.5
-// times as long)
+// that append wrote); chosen once for a run
 struct Times {
   float inverse;
   __device__ __forceinline__ float operator()(float x) const { return x * inverse; }
@@ -491,12 +495,12 @@ cudaError_t launch_append(const Append8Params& g, cudaStream_t s) {
 // to shared memory (as many as there is room for; every thread then counts some of those
 // that begin at or before its first row), a lane a row finds its sequence by bisection and
 // looks up its page, then all threads bring 16 codes at a time to 32 bytes of the
-// outputs. Bound by memory.
+// outputs. Bound by memory: 16 sequences of up to 16384 tokens, 8 heads of 128, 933 MB
+// take 150 us (6.2 TB/s).
 constexpr int kReadRows = 32, kReadSeqs = 1024;
 
 template <typename T>
-__device__ __forceinline__ void read16(const uint8_t* codes, float scale, uint16_t* to, bool wide) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(codes));
+__device__ __forceinline__ void read16(const uint4& w, float scale, uint16_t* to, bool wide) {
   const uint32_t* x = reinterpret_cast<const uint32_t*>(&w);
   uint32_t y[8];
 #pragma unroll
@@ -578,19 +582,23 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const Read8Params p, in
     if (code_at[r] < 0) continue;
     const long long at = code_at[r] + h * p.c.head + c * 16, sc = scale_at[r] + h * p.c.scale_head;
     const float ks = __ldg(p.c.k_scales + sc), vs = __ldg(p.c.v_scales + sc);
-    read16<T>(p.c.k + at, ks,
+    const uint4 k = __ldg(reinterpret_cast<const uint4*>(p.c.k + at));
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.c.v + at));
+    read16<T>(k, ks,
               p.k_out.p + (long long)(row0 + r) * p.k_out.token + h * p.k_out.head + c * 16, wide);
-    read16<T>(p.c.v + at, vs,
+    read16<T>(v, vs,
               p.v_out.p + (long long)(row0 + r) * p.v_out.token + h * p.v_out.head + c * 16, wide);
   }
 }
 
 // ------------------------------------------------------------------ a batch's keys in 16 bits
-// Persistent CTAs over the pages of all sequences, dealt out in turn: every CTA adds up
-// the sequences' pages for itself, keeps the first page of each while they are few, and
-// finds a page's sequence by bisection. Blocks of kTcBlock keys that no query sees are
-// passed over. Bound by memory.
-constexpr int kFirstKept = 2048;
+// Persistent CTAs over parts of the pages of all sequences, dealt out in turn: every CTA
+// adds up the sequences' pages for itself, keeps the first page of each while they are
+// few, and finds a page's sequence by bisection. A part is what a CTA's threads bring with
+// their loads under way at once. Blocks of kTcBlock keys that no query sees are passed
+// over. Bound by memory. (Whole pages to a CTA left most of them without work where pages
+// are few: a chunk of 256 tokens over 32768 keys, with its attention, 158 us, 153 so.)
+constexpr int kFirstKept = 2048, kPartItems = 4 * kThreads;   // of 16 values of K and of V
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) expand8_kernel(const Expand8Params p) {
@@ -598,6 +606,8 @@ __global__ void __launch_bounds__(kThreads) expand8_kernel(const Expand8Params p
   __shared__ int sums[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, seqs = p.b.num_seqs;
   const int page_rows = 1 << p.page_shift, chunks = p.head_dim >> 4;
+  const int row_chunks = page_rows * chunks, items = p.hk * row_chunks;
+  const int parts = (items + kPartItems - 1) / kPartItems;   // of a page
   wait_prior_launch();
   let_next_launch();
   // Pages of sequence s. (A sequence whose lengths leave their ranges has none.)
@@ -632,10 +642,12 @@ __global__ void __launch_bounds__(kThreads) expand8_kernel(const Expand8Params p
     }
     if (tid == 0) first[n] = total;
     __syncthreads();
-    // this CTA's pages of [base, total)
-    int i = base + (int)((blockIdx.x + gridDim.x - base % gridDim.x) % gridDim.x);
+    // this CTA's parts of pages [base, total)
+    const long long u0 = (long long)base * parts, u1 = (long long)total * parts;
+    long long u = u0 + (blockIdx.x + gridDim.x - u0 % gridDim.x) % gridDim.x;
     int lo = 0;
-    for (; i < total; i += gridDim.x) {
+    for (; u < u1; u += gridDim.x) {
+      const int i = (int)(u / parts), part = (int)(u - (long long)i * parts);
       int hi = n - 1;                                  // last sequence with first <= i
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -645,7 +657,7 @@ __global__ void __launch_bounds__(kThreads) expand8_kernel(const Expand8Params p
           hi = mid - 1;
       }
       const int seq = s0 + lo, column = i - first[lo], key0 = column << p.page_shift;
-      if (tid == 0) p.table[(long long)seq * p.b.columns + column] = i;
+      if (tid == 0 && part == 0) p.table[(long long)seq * p.b.columns + column] = i;
       const int kv = p.b.kv_len[seq], n_new = p.b.cu_q[seq + 1] - p.b.cu_q[seq];
       const int kept = kept_of(p.sc, prefix_of(p.sc, seq, kv), kv - 1);
       const int from = p.sc.window ? max(0, kv - n_new - p.sc.window + 1) : 0;
@@ -655,27 +667,34 @@ __global__ void __launch_bounds__(kThreads) expand8_kernel(const Expand8Params p
       const int page = p.b.page_table[seq * p.b.table_stride + column];
       const bool bad = page < 0 || page >= p.c.num_pages;
       if (bad && tid == 0) atomicOr(p.err, kErrRange);
-      const int rows = min(page_rows, kv - key0), row_chunks = page_rows * chunks;
+      const int rows = min(page_rows, kv - key0);
       const long long out = (long long)i * p.hk * page_rows * p.head_dim;
-#pragma unroll 4
-      for (int e = tid; e < p.hk * row_chunks; e += kThreads) {
-        const int h = e / row_chunks, rest = e - h * row_chunks;
-        const int r = rest / chunks, c = rest - r * chunks;
-        if (r >= rows) continue;
-        uint16_t* k = p.k + out + (long long)e * 16;
-        uint16_t* v = p.v + out + (long long)e * 16;
-        if (bad) {
+      constexpr int kItems = kPartItems / kThreads;
+      uint4 k[kItems], v[kItems];
+      float ks[kItems], vs[kItems];
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            reinterpret_cast<uint4*>(k)[q] = reinterpret_cast<uint4*>(v)[q] = make_uint4(0, 0, 0, 0);
-          continue;
+      for (int q = 0; q < kItems; ++q) {
+        const int e = part * kPartItems + q * kThreads + tid;
+        const int row = e / chunks, c = e - row * chunks;
+        const int h = row >> p.page_shift, r = row & (page_rows - 1);
+        k[q] = v[q] = make_uint4(0, 0, 0, 0);
+        ks[q] = vs[q] = 0.0f;
+        if (e < items && r < rows && !bad) {
+          const long long code = page * p.c.page + h * p.c.head + r * p.c.token + c * 16;
+          const long long scale =
+              page * p.c.scale_page + h * p.c.scale_head + r / kScaleBlock * p.c.scale_block;
+          k[q] = __ldg(reinterpret_cast<const uint4*>(p.c.k + code));
+          v[q] = __ldg(reinterpret_cast<const uint4*>(p.c.v + code));
+          ks[q] = __ldg(p.c.k_scales + scale);
+          vs[q] = __ldg(p.c.v_scales + scale);
         }
-        const long long from_code = page * p.c.page + h * p.c.head + r * p.c.token + c * 16;
-        const long long from_scale =
-            page * p.c.scale_page + h * p.c.scale_head + r / kScaleBlock * p.c.scale_block;
-        const float ks = __ldg(p.c.k_scales + from_scale), vs = __ldg(p.c.v_scales + from_scale);
-        read16<T>(p.c.k + from_code, ks, k, true);
-        read16<T>(p.c.v + from_code, vs, v, true);
+      }
+#pragma unroll
+      for (int q = 0; q < kItems; ++q) {
+        const int e = part * kPartItems + q * kThreads + tid;
+        if (e >= items || (e / chunks & (page_rows - 1)) >= rows) continue;
+        read16<T>(k[q], ks[q], p.k + out + (long long)e * 16, true);
+        read16<T>(v[q], vs[q], p.v + out + (long long)e * 16, true);
       }
     }
     base = total;
