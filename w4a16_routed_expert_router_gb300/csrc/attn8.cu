@@ -134,9 +134,9 @@ Scratch scratch_of(const moe_attn_config& c, const moe_attn_batch* b) {
 }
 // Batches of many rows a sequence and kv head are worth it: bringing the keys to 16 bits
 // takes the same for any number of rows, and the kernel over 16 bits is faster for each.
-// Rows over 32768 keys of 8 kv heads, over codes and so: 400 108 and 120 us, 512 109 and
-// 121, 1024 176 and 153, 4000 (over 65536) 1189 and 714; 8 sequences of 8192 keys: 256
-// 104 and 159, 512 180 and 202, 1024 330 and 288.
+// Rows over 32768 keys of 8 kv heads, over codes and so: 400 108 and 113 us, 512 109 and
+// 113, 1024 176 and 145, 4000 (over 65536) 1189 and 702; 8 sequences of 8192 keys: 256
+// 104 and 146, 512 180 and 189, 1024 330 and 275.
 constexpr long long kExpandRows = 512;
 constexpr size_t kScratchMost = size_t(8) << 30;
 bool expands(const moe_attn_config& c, const moe_attn_batch* b) {

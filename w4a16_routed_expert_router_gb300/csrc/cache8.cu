@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const Read8Params p, in
 // few, and finds a page's sequence by bisection. A part is what a CTA's threads bring with
 // their loads under way at once. Blocks of kTcBlock keys that no query sees are passed
 // over. Bound by memory. (Whole pages to a CTA left most of them without work where pages
-// are few: a chunk of 256 tokens over 32768 keys, with its attention, 158 us, 153 so.)
-constexpr int kFirstKept = 2048, kPartItems = 4 * kThreads;   // of 16 values of K and of V
+// are few: a chunk of 256 tokens over 32768 keys, with its attention, 158 us, 146 so.)
+constexpr int kFirstKept = 2048, kPartItems = 2 * kThreads;   // of 16 values of K and of V
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) expand8_kernel(const Expand8Params p) {
@@ -729,7 +729,12 @@ cudaError_t launch_read8(const Read8Params& p, int dtype, cudaStream_t s) {
 }
 
 cudaError_t launch_expand8(const Expand8Params& p, int dtype, int grid, cudaStream_t s) {
-  const dim3 ctas(6 * grid), block(kThreads);
+  // 16 CTAs for each SM, as far as the table's pages have parts for them (prompts of 8192
+  // tokens, with their attention: 378 us with the 4 or 6 that run at once, 372 with 16,
+  // 376 with 32)
+  const long long items = (long long)p.hk * p.head_dim / 16 << p.page_shift;
+  const long long parts = (items + kPartItems - 1) / kPartItems * p.b.num_seqs * p.b.columns;
+  const dim3 ctas((unsigned)std::min(16LL * grid, parts)), block(kThreads);
   return dtype == MOE_ATTN_BF16 ? launch_after(expand8_kernel<Bf16>, ctas, block, 0, s, p)
                                 : launch_after(expand8_kernel<Fp16>, ctas, block, 0, s, p);
 }
