@@ -2,9 +2,13 @@
 then the routed-expert layer.
 
     python examples/decoder_layer.py [--config tiny16|decode64] [--steps 8]
+        [--norm] [--cache8] [--window N --sinks M]
 
 Prompts of different lengths are prefilled in chunks, single tokens of some
 sequences beside chunks of others in one batch, then every sequence decodes.
+--norm puts norms of the heads in front of their rotation, --cache8 holds keys and
+values in 8 bits, --window and --sinks hide what lies between a sequence's first
+tokens and its last ones.
 Weights are random, projections are plain matrix products; the cache, the
 rotary positions, the attention and the experts are the framework's kernels.
 """
@@ -35,7 +39,8 @@ class DecoderLayer:
     """x + attention(norm(x)), then x + experts(norm(x))."""
 
     def __init__(self, shape: ms.MoeShape, q_heads, kv_heads, head_dim, page_size=16,
-                 num_pages=1024, max_tokens=2048, max_seqs=64, device="cuda:0", seed=0):
+                 num_pages=1024, max_tokens=2048, max_seqs=64, device="cuda:0", seed=0,
+                 norm=False, cache8=False, window=0, sinks=0):
         gen = torch.Generator(device=device).manual_seed(seed)
         hidden, self.q_heads, self.kv_heads, self.dim = shape.hidden, q_heads, kv_heads, head_dim
         self.device = torch.device(device)
@@ -46,8 +51,15 @@ class DecoderLayer:
 
         self.w_qkv = weight((q_heads + 2 * kv_heads) * head_dim, hidden)
         self.w_out = weight(hidden, q_heads * head_dim)
+        self.norm = None
+        if norm:
+            self.norm = moe.HeadNorm(*(1 + 0.1 * torch.randn(head_dim, generator=gen, device=device)
+                                       for _ in range(2)))
+        self.window, self.sinks = window, sinks
         self.freq, self.magnitude = moe.moe_attn_rope_frequencies(head_dim, device=device)
-        self.cache = moe.PagedKvCache(num_pages, kv_heads, page_size, head_dim, device=device)
+        dtype = torch.float8_e4m3fn if cache8 else torch.bfloat16
+        self.cache = moe.PagedKvCache(num_pages, kv_heads, page_size, head_dim, dtype=dtype,
+                                      device=device)
         self.attention_op = moe.PagedAttention(q_heads, kv_heads, head_dim, page_size, max_tokens,
                                                max_seqs, device=device)
         layer = ms.make_layer(shape)
@@ -74,9 +86,11 @@ class DecoderLayer:
         k_pages, v_pages = self.cache.k_pages, self.cache.v_pages
         q = self.attention_op.append(q, k, v, torch.tensor(positions, dtype=torch.int32, **to),
                                      torch.tensor(slots, dtype=torch.int64, **to), k_pages,
-                                     v_pages, self.freq, magnitude=self.magnitude)
+                                     v_pages, self.freq, magnitude=self.magnitude,
+                                     norm=self.norm, **self.cache.scales)
         out = self.attention_op.forward(q, k_pages, v_pages, table, cu_q.to(self.device), kv_len,
-                                        max(counts))
+                                        max(counts), window=self.window, sinks=self.sinks,
+                                        **self.cache.scales)
         return x + out.view(len(x), -1) @ self.w_out.T
 
     def forward(self, x, seqs, counts):
@@ -94,10 +108,15 @@ def main(argv=None):
     p = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     p.add_argument("--config", default="tiny16", choices=["tiny16", "decode64"])
     p.add_argument("--steps", type=int, default=8)
+    p.add_argument("--norm", action="store_true", help="norms of the heads of q and k")
+    p.add_argument("--cache8", action="store_true", help="keys and values in 8 bits")
+    p.add_argument("--window", type=int, default=0, help="last keys that a token sees (0: all)")
+    p.add_argument("--sinks", type=int, default=0, help="first keys that it sees all the same")
     args = p.parse_args(argv)
     shape = ms.CONFIGS[args.config]
     heads = (32, 8, 128) if shape.hidden == 4096 else (4, 2, 64)
-    layer = DecoderLayer(shape, *heads)
+    layer = DecoderLayer(shape, *heads, norm=args.norm, cache8=args.cache8, window=args.window,
+                         sinks=args.sinks)
     gen = torch.Generator(device="cuda:0").manual_seed(1)
 
     def tokens(n):
