@@ -51,12 +51,22 @@ __device__ __forceinline__ void cos_sin(const Rotation& r, int position, int pai
   cosine = cn * r.magnitude;
   sine = sn * r.magnitude * r.sign;
 }
+// The pairs of a head, and which token's an entry of a table is: entries are below 4096
+// and pairs 8 to 128 of them, so the quotient is exact in 32 bits (a division takes about
+// as long as the rest of an entry).
+struct Pairs {
+  int count;
+  unsigned inverse;
+  __device__ __forceinline__ explicit Pairs(int rot)
+      : count(rot >> 1), inverse(count ? ((1u << 22) + count - 1) / count : 0) {}
+  __device__ __forceinline__ int token(int entry) const { return entry * inverse >> 22; }
+};
 // cosines and sines of the pairs of positions[0 .. tokens), by all threads of the CTA
 __device__ __forceinline__ void fill_table(const Rotation& r, const int* positions, int tokens,
                                            float* cosines, float* sines, int tid, int threads) {
-  const int pairs = r.rot >> 1;
-  for (int i = tid; i < tokens * pairs; i += threads) {
-    const int t = i / pairs, c = i - t * pairs;
+  const Pairs pairs(r.rot);
+  for (int i = tid; i < tokens * pairs.count; i += threads) {
+    const int t = pairs.token(i), c = i - t * pairs.count;
     cos_sin(r, positions[t], c, cosines[i], sines[i]);
   }
 }
@@ -159,7 +169,7 @@ __device__ __forceinline__ void copies_wait() {
 
 struct Walk {
   int tid, threads, lanes;   // of the CTA, up to kWalkThreads; lanes of a head
-  int z, zs;                 // token side by side, and how many
+  int z, zs;                 // token side by side, and how many (a power of two)
   int c0, step;
   __host__ __device__ static int table_floats(int zs, int rot) { return kAhead * zs * rot; }
   static size_t bytes(int zs, int rot) {
@@ -187,7 +197,8 @@ __device__ __forceinline__ void norm_walk(const Walk& k, const Rotation& rot,
                                           const Norm& n, const Lane<IL>& lane, bool active,
                                           bool plain, const uint16_t* src, long long src_token,
                                           const void* w, long long w_head, float* smem, Out out) {
-  const int pairs = rot.rot >> 1;
+  const Pairs table(rot.rot);
+  const int pairs = table.count, z_shift = __ffs(k.zs) - 1;
   constexpr int kHalf = kWalkThreads, kSlot = 2 * kHalf;   // of the ring, chunks
   const uint4* ring = reinterpret_cast<uint4*>(smem + Walk::table_floats(k.zs, rot.rot)) + k.tid;
   const uint32_t ring_at = smem_u32(ring);
@@ -214,8 +225,8 @@ __device__ __forceinline__ void norm_walk(const Walk& k, const Rotation& rot,
   for (int c0 = k.c0; c0 < tokens;) {
     __syncthreads();
     for (int e = k.tid; e < kAhead * k.zs * pairs; e += k.threads) {
-      const int row = e / pairs, c = e - row * pairs;
-      const int of = c0 + row / k.zs * k.step + row % k.zs;
+      const int row = table.token(e), c = e - row * pairs;
+      const int of = c0 + (row >> z_shift) * k.step + (row & (k.zs - 1));
       if (of < tokens) cos_sin(rot, positions[of], c, smem[e], smem[kAhead * k.zs * pairs + e]);
     }
     __syncthreads();

@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(kGradThreads, 2)
   float* smem = reinterpret_cast<float*>(smem4);
   const NormParams& p = g.p;
   const RopeParams& r = p.r;
-  const int pairs = r.r.rot >> 1, z = blockDim.z, heads = r.hq + r.hk;
+  const Pairs head(r.r.rot);
+  const int pairs = head.count, z = blockDim.z, z_shift = __ffs(z) - 1, heads = r.hq + r.hk;
   wait_prior_launch();
   let_next_launch();
   const int u = threadIdx.x, hd = blockIdx.y * blockDim.y + threadIdx.y;
@@ -234,54 +235,59 @@ __global__ void __launch_bounds__(kGradThreads, 2)
   const int threads = blockDim.x * blockDim.y * blockDim.z;
   const float mean = 1.0f / (float)r.head_dim;
   // a token's chunks, one iteration ahead
+  const int step = gridDim.x * z;
+  int t = blockIdx.x * z + threadIdx.z, coming = active ? t : r.tokens;
+  const uint16_t* x = in.p + (long long)t * in.token + hi;
+  const uint16_t* y = dy.p + (long long)t * dy.token + hy;
+  uint16_t* out = dx.p + (long long)t * dx.token + ho;
+  const long long x_step = in.token * step, y_step = dy.token * step, out_step = dx.token * step;
   Chunk8 next[4];
-  const auto load = [&](int c0) {
-    const int t = c0 + threadIdx.z;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) next[k].v = make_uint4(0, 0, 0, 0);
-    if (active && t < r.tokens) {
-      const uint16_t* x = in.p + (long long)t * in.token + hi;
-      const uint16_t* y = dy.p + (long long)t * dy.token + hy;
+  for (int k = 0; k < 4; ++k) next[k].v = make_uint4(0, 0, 0, 0);
+  const auto load = [&]() {
+    if (coming < r.tokens) {
       next[0].v = *reinterpret_cast<const uint4*>(x);
       next[1].v = *reinterpret_cast<const uint4*>(y);
       if (lane.two) {
         next[2].v = *reinterpret_cast<const uint4*>(x + lane.gap);
         next[3].v = *reinterpret_cast<const uint4*>(y + lane.gap);
       }
+      x += x_step;
+      y += y_step;
+      coming += step;
     }
   };
   // of kTables iterations at once, which takes most threads
   const auto table = [&](int c0) {
-    const int step = gridDim.x * z;
     for (int i = tid; i < kTables * z * pairs; i += threads) {
-      const int row = i / pairs, c = i - row * pairs;
-      const int t = c0 + row / z * step + row % z;
+      const int row = head.token(i), c = i - row * pairs;
+      const int t = c0 + (row >> z_shift) * step + (row & (z - 1));
       if (t >= r.tokens) continue;
       cos_sin(r.r, r.positions[t], c, smem[i], smem[kTables * z * pairs + i]);
     }
   };
-  const int step = gridDim.x * z;
-  int turn = 0;
-  load(blockIdx.x * z);
-  for (int c0 = blockIdx.x * z; c0 < r.tokens; c0 += step, turn = (turn + 1) % kTables) {
-    const int t = c0 + threadIdx.z;
+  const float* cosines = smem;
+  load();
+  for (int c0 = blockIdx.x * z, turn = 0; c0 < r.tokens; c0 += step, t += step) {
     const bool on = active && t < r.tokens;
     const Chunk8 xa = next[0], ya = next[1], xb = next[2], yb = next[3];
-    load(c0 + step);
+    load();
     if (turn == 0) {
       __syncthreads();
       table(c0);
       __syncthreads();
+      turn = kTables;
+      cosines = smem + threadIdx.z * pairs;
     }
-    const float* cosines = smem + turn * z * pairs;
-    const float* sines = cosines + kTables * z * pairs;
     float fx[8], gx[8], ua[8], ub[8];
     unpack8<T>(xa, fx);
     unpack8<T>(xb, gx);
     unpack8<T>(ya, ua);
     unpack8<T>(yb, ub);
     if (on && lane.turns)
-      lane.turn(ua, ub, cosines + threadIdx.z * pairs, sines + threadIdx.z * pairs);
+      lane.turn(ua, ub, cosines, cosines + kTables * z * pairs);
+    --turn;
+    cosines += z * pairs;
     float sq = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -294,19 +300,21 @@ __global__ void __launch_bounds__(kGradThreads, 2)
     dot = group_sum(dot, blockDim.x);
     if (!on) continue;
     const float f = rsqrtf(fmaf(sq, mean, p.n.eps));
-    const float c = dot * mean * f * f;
+    const float c = -(dot * mean * f * f) * f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      da[k] = fmaf(ua[k], fx[k] * f, da[k]);
-      ua[k] = f * fmaf(-c, fx[k], ua[k] * wa[k]);
+      ua[k] *= f;
+      da[k] = fmaf(ua[k], fx[k], da[k]);
+      ua[k] = fmaf(c, fx[k], ua[k] * wa[k]);
       if (lane.two) {
-        db[k] = fmaf(ub[k], gx[k] * f, db[k]);
-        ub[k] = f * fmaf(-c, gx[k], ub[k] * wb[k]);
+        ub[k] *= f;
+        db[k] = fmaf(ub[k], gx[k], db[k]);
+        ub[k] = fmaf(c, gx[k], ub[k] * wb[k]);
       }
     }
-    uint16_t* out = dx.p + (long long)t * dx.token + ho;
     *reinterpret_cast<uint4*>(out) = pack8<T>(ua);
     if (lane.two) *reinterpret_cast<uint4*>(out + lane.gap) = pack8<T>(ub);
+    out += out_step;
   }
   // the CTA's rows in order: tokens side by side, then the heads that share a weight
   __syncthreads();
