@@ -5,8 +5,8 @@
 // group of lanes has a head and walks along the tokens (norm_walk in norm_parts.cuh). The
 // CTA makes the tables of cosines and sines, one evaluation for its heads. 8192 tokens of
 // 40 heads of 128 take 36 us (168 MB, 4.6 TB/s; the same kernel without sums, rotation
-// and weights takes 28, the copy rate 25): instructions, 270 for 16 values of a lane, at
-// 55 % of the issue slots. (A few tokens a thread, loaded to registers first, took 44 us:
+// and weights takes 28, the copy rate 25): latency and instructions, 260 for 16 values of a
+// lane, at 55 % of the issue slots. (A few tokens a thread, loaded to registers first, took 44 us:
 // a third of its instructions prepared a thread for them. Rows in units of one chunk for
 // interleaved pairs cost as many sums and addresses again.)
 //
@@ -15,9 +15,9 @@
 // mean(h n) = r mean(h x), so both sums over a head, of x^2 and of h x, are taken
 // together. Each thread keeps one unit of one head for many tokens and adds up that
 // unit's dw; a CTA adds its rows in order, and a second launch the CTAs. 16384 tokens of
-// 40 heads of 128 take 114 us (503 MB, 4.4 TB/s; 75 at the copy rate): latency, with 15
-// warps an SM at 104 registers and more. (The forward's ring of copies in place of
-// registers: 134 us, for its instructions and spills.)
+// 40 heads of 128 take 107 us (503 MB, 4.7 TB/s; 75 at the copy rate): latency, with 15
+// warps an SM at 122 registers; two values to an instruction change nothing. (The
+// forward's ring of copies in place of registers: 134 us, for its instructions and spills.)
 #include <algorithm>
 
 #include "norm_parts.cuh"
