@@ -148,7 +148,7 @@ class Batch8:
 
     def __init__(self, lens, hq, hk, d, page, dtype, seed=0, device="cuda:0", softcap=0.0,
                  window=0, slopes=False, prefix=None, sinks=0, heads_inner=True, scale=None,
-                 gains=None, cover=None):
+                 gains=None):
         g = torch.Generator().manual_seed(seed)
         self.lens, self.dtype, self.device, self.page = lens, dtype, device, page
         self.softcap, self.window, self.sinks = softcap, window, sinks
