@@ -474,11 +474,15 @@ __global__ void __launch_bounds__(kThreads8, 1)
       float ref = -INFINITY, l = 0.0f;                    // 2^ref is the sums' unit
       bool ok = true;
       for (int j = 0; j < cnt; ++j) {
-        const uint32_t at = (block0 + j) % S::kScales;
-        if (!(ok = warp_wait(&s.sc_ready[at], (block0 + j) / S::kScales & 1u, p.err))) break;
+        // The products first: K of this block has then been spread by every converter, and
+        // the scales of all blocks before it are ready, so that the parity below can only
+        // mean this block's. (A tile without tokens passes its pieces over and may be
+        // whole phases ahead of the converters, where the parity says nothing.)
         if (!(ok = warp_wait(&s.s_full[t], sph, p.err))) break;
         sph ^= 1u;
         tc_fence_after();
+        const uint32_t at = (block0 + j) % S::kScales;
+        if (!(ok = warp_wait(&s.sc_ready[at], (block0 + j) / S::kScales & 1u, p.err))) break;
         if (!T::kFp16 && j == 0)
           unit = __int_as_float((127 - (int)s.q_exp[odd ^ 1u][t][row]) << 23);
         const int n = n0 + j, kb = (n < near ? n : n + skip) * kBlk;
