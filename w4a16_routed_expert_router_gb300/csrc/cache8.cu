@@ -338,8 +338,8 @@ __device__ __forceinline__ void queries_any(const Append8Params& g, const Dims& 
 template <typename T, bool IL, bool FAST>
 __global__ void __launch_bounds__(kThreads, 4)
     append8_kernel(const __grid_constant__ Append8Params g, const Dims d) {
+  // (nothing static beside it: the queries' ring and tables may take all there is)
   extern __shared__ float4 smem4[];
-  __shared__ float tops[kWarps];
   float* smem = reinterpret_cast<float*>(smem4);
   const RopeParams& r = g.p.r;
   wait_prior_launch();
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   unsigned begin = __ballot_sync(0xffffffffu, slot >= 0 && !follows && lane > 0 && lane <= kRun);
   const bool any_keys = first_combo < r.hk;            // in the CTA
   const int pairs = r.r.rot >> 1;
-  float *cosines = smem, *sines = smem + kRun * pairs;
+  float *tops = smem, *cosines = smem + kWarps, *sines = cosines + kRun * pairs;
   for (int i = 0; begin; ++i) {
     const int at = __ffs(begin) - 1;
     begin &= begin - 1;
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                        (long long)(in_page - first) * g.c.token;
       float* scale_at = (key ? g.c.k_scales : g.c.v_scales) + page * g.c.scale_page +
                         h * g.c.scale_head + block * g.c.scale_block;
-      RowsOf<T, IL, FAST> of(d, r, smem);
+      RowsOf<T, IL, FAST> of(d, r, smem + kWarps);
       float top = 0.0f, before = 0.0f;
       if (on) {
         if (first) before = *scale_at;
@@ -458,19 +458,19 @@ cudaError_t launch_append(const Append8Params& g, cudaStream_t s) {
     d.q_rows = (r.hq + most - 1) / most;
     d.q_heads = d.q_rows ? (r.hq + d.q_rows - 1) / d.q_rows : 1;
     d.q_z = 1;
-    while (2 * d.q_z * d.q_heads <= most && 2 * d.q_z * r.r.rot <= 1024 &&
+    while (2 * d.q_z * d.q_heads <= most && 2 * d.q_z * r.r.rot <= kWalkTurned &&
            (long long)r.tokens * d.q_rows >= 8LL * kSms * d.q_z)
       d.q_z *= 2;
     // up to 8 tokens to a thread, where every SM has CTAs enough
     const int all = (r.tokens + d.q_z - 1) / d.q_z;
     const int few = d.q_rows ? (4 * kSms + d.q_rows - 1) / d.q_rows : 1;
     d.token_groups = std::min(all, std::max(few, (all + 7) / 8));
-    smem = std::max(kRun * r.r.rot * (int)sizeof(float),
+    smem = std::max((kWarps + kRun * r.r.rot) * (int)sizeof(float),
                     r.hq ? (int)Walk::bytes(d.q_z, r.r.rot) : 0);
   } else {
     d.q_rows = (r.hq + kWarps - 1) / kWarps;
     d.token_groups = r.tokens;
-    smem = kWarps * 128 * (int)sizeof(float);
+    smem = kWarps * (1 + 128) * (int)sizeof(float);
   }
   d.combos = (2 * r.hk + kWarps / 2 - 1) / (kWarps / 2);
   const int windows = (r.tokens + kRun - 1) / kRun;

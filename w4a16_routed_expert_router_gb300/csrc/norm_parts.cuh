@@ -155,6 +155,11 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 // once. What bounds it is instructions, so addresses go on by additions and slots are
 // told apart at compile time.
 constexpr int kAhead = 4, kWalkThreads = 256;
+// Turned values of the tokens side by side, where they are more than one: ring and
+// tables then take the 48 KB that a kernel has without asking, to the byte.
+constexpr int kWalkTurned = 1024;
+static_assert(kAhead * (kWalkTurned * 4 + kWalkThreads * 32) <= 48 * 1024,
+              "shared memory of a walk");
 
 __device__ __forceinline__ void copy_async16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");

@@ -173,7 +173,7 @@ cudaError_t launch_fast(const NormParams& p, cudaStream_t s) {
   const int groups = (heads + most - 1) / most;
   dim3 block(u.lanes, (heads + groups - 1) / groups, 1);
   while (2 * block.x * block.y * block.z <= kWalkThreads && block.z < 64 &&
-         2 * block.z * r.r.rot <= 1024 &&
+         2 * block.z * r.r.rot <= kWalkTurned &&
          (long long)r.tokens * groups >= 8LL * kSms * block.z)
     block.z *= 2;
   const int threads = block.x * block.y * block.z;
