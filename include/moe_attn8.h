@@ -139,8 +139,9 @@ int moe_attn_append8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
                      void* stream);
 
 /* k_out and v_out [num_rows, kv_heads, head_dim] of the handle's type = the cache's
- * values, code * scale rounded once. Rows of no sequence, and rows whose position or
- * page leaves its range (MOE_ATTN_DEVERR_RANGE), are not written. */
+ * values, code * scale rounded once; fp16 takes what is above 65504 as that. Rows of no
+ * sequence, and rows whose position or page leaves its range (MOE_ATTN_DEVERR_RANGE), are
+ * not written. */
 int moe_attn_read8(moe_attn_handle* h, const moe_attn_cache8* cache, const moe_attn_extent* extent,
                    const moe_attn_rows* k_out, const moe_attn_rows* v_out, void* stream);
 
@@ -153,8 +154,10 @@ int moe_attn_forward8_scratch_bytes(const moe_attn_handle* h, const moe_attn_bat
 
 /* moe_attn_forward over an 8-bit cache; sinks: see above (0: none). scratch: as many
  * bytes as above, 256-byte aligned, or NULL; it keeps nothing between calls. With it, the
- * keys and values that queries see are brought to the handle's type first (exactly, where
- * scales are powers of two and values in the type's range; fp16 has none above 65504). */
+ * keys and values that queries see are brought to the handle's type first, as
+ * moe_attn_read8 gives them: exactly, where scales are powers of two and values in the
+ * type's range. (Keys above 65504, which norms in an fp16 layer can make, count in full
+ * only without it.) */
 int moe_attn_forward8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* out,
                       float* lse, const moe_attn_cache8* cache, const moe_attn_batch* batch,
                       const moe_attn_scores* scores, int32_t sinks, void* scratch,

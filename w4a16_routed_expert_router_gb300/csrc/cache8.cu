@@ -499,6 +499,17 @@ cudaError_t launch_append(const Append8Params& g, cudaStream_t s) {
 // take 150 us (6.2 TB/s).
 constexpr int kReadRows = 32, kReadSeqs = 1024;
 
+// Two values of the cache in 16 bits. A finite value stays finite: fp16 takes what is
+// above 65504 as that (append holds 65000 as 256 * 256, half a step of the codes above
+// it). bf16 has room for every code by every scale.
+template <typename T>
+__device__ __forceinline__ uint32_t pack_held(float lo, float hi) {
+  if (!T::kFp16) return T::pack(lo, hi);
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ void read16(const uint4& w, float scale, uint16_t* to, bool wide) {
   const uint32_t* x = reinterpret_cast<const uint32_t*>(&w);
@@ -506,8 +517,8 @@ __device__ __forceinline__ void read16(const uint4& w, float scale, uint16_t* to
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float2 lo = codes_to_f32((uint16_t)x[k]), hi = codes_to_f32((uint16_t)(x[k] >> 16));
-    y[2 * k] = T::pack(lo.x * scale, lo.y * scale);
-    y[2 * k + 1] = T::pack(hi.x * scale, hi.y * scale);
+    y[2 * k] = pack_held<T>(lo.x * scale, lo.y * scale);
+    y[2 * k + 1] = pack_held<T>(hi.x * scale, hi.y * scale);
   }
   if (wide) {
     reinterpret_cast<uint4*>(to)[0] = make_uint4(y[0], y[1], y[2], y[3]);
