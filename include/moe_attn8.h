@@ -109,10 +109,10 @@ int moe_attn_norm_rope_backward_bytes(int32_t num_tokens, int32_t q_heads, int32
 /* The gradient of moe_attn_norm_rope: dq and dk are the gradients of its results,
  * q and k its inputs; dx_q and dx_k get the gradients of q and k, dw_q and dw_k
  * (fp32, contiguous, of the weights' shape: [head_dim] where the head stride is 0)
- * those of the weights, which are overwritten. The q or the k arguments may all be
- * NULL. dx may be dq or q in place. workspace: as many bytes as above, 16-byte
- * aligned; it keeps nothing between calls. Sums are in an order that depends on the
- * sizes alone: repeats are equal bit by bit. */
+ * those of the weights, which are overwritten (zeros without tokens, or heads). The q or
+ * the k arguments may all be NULL. dx may be dq or q in place. workspace: as many bytes
+ * as above, 16-byte aligned; it keeps nothing between calls. Sums are in an order that
+ * depends on the sizes alone: repeats are equal bit by bit. */
 int moe_attn_norm_rope_backward(const moe_attn_rows* dq, const moe_attn_rows* q,
                                 const moe_attn_rows* dx_q, float* dw_q, const moe_attn_rows* dk,
                                 const moe_attn_rows* k, const moe_attn_rows* dx_k, float* dw_k,

@@ -254,18 +254,23 @@ int moe_attn_norm_rope_backward(const moe_attn_rows* dq, const moe_attn_rows* q,
   const bool with_q = q || dq || dx_q || dw_q, with_k = k || dk || dx_k || dw_k;
   const int hq = with_q ? q_heads : 0, hk = with_k ? kv_heads : 0;
   if ((st = validate_norm(norm, head_dim, hq, hk)) != MOE_ATTN_OK) return st;
-  if (hq + hk == 0) return MOE_ATTN_OK;
   if ((hq && !dw_q) || (hk && !dw_k)) return MOE_ATTN_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(dw_q) | reinterpret_cast<uintptr_t>(dw_k)) & 3u)
     return MOE_ATTN_ERR_MISALIGNED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T == 0) {  // no token: no gradient of the weights
-    const size_t row = (size_t)head_dim * sizeof(float);
-    if (hq && (st = cuda_status(cudaMemsetAsync(dw_q, 0, row * (norm->q_head_stride ? hq : 1), s))))
+  // no token, or no head that has the weight: no gradient of it
+  const struct {
+    float* dw;
+    int64_t stride;
+    int heads;
+  } weights[2] = {{dw_q, norm->q_head_stride, hq}, {dw_k, norm->k_head_stride, hk}};
+  for (const auto& w : weights) {
+    const size_t bytes = (size_t)(w.stride ? w.heads : 1) * head_dim * sizeof(float);
+    if (w.dw && (T == 0 || w.heads == 0) && bytes &&
+        (st = cuda_status(cudaMemsetAsync(w.dw, 0, bytes, s))) != MOE_ATTN_OK)
       return st;
-    return hk ? cuda_status(cudaMemsetAsync(dw_k, 0, row * (norm->k_head_stride ? hk : 1), s))
-              : MOE_ATTN_OK;
   }
+  if (T == 0 || hq + hk == 0) return MOE_ATTN_OK;
   const struct {
     const moe_attn_rows *dy, *x, *dx;
     int heads;

@@ -947,7 +947,14 @@ static PyObject* norm_back(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       goto done;
     }
     out[i] = output(Py_None, t.tokens, heads, t.dim, t.dtype, t.device, t.index, &dx[i], "");
-    const int each = (i ? t.norm.k_head_stride : t.norm.q_head_stride) != 0;
+    int64_t* const stride = i ? &t.norm.k_head_stride : &t.norm.q_head_stride;
+    if (!heads) { /* of no heads, the weight has not been looked at */
+      long long d[MAX_DIMS];
+      const int dims = shape_of(PyTuple_GET_ITEM(a[6], i), d);
+      if (dims < 0) goto done;
+      *stride = dims == 2 ? t.dim : 0;
+    }
+    const int each = *stride != 0;
     out[2 + i] = new_tensor(each ? Py_BuildValue("(LL)", heads, t.dim) : Py_BuildValue("(L)", t.dim),
                             G.f32, t.device);
     if (!out[i] || !out[2 + i] || pointer_of(out[2 + i], &dw[i])) goto done;
