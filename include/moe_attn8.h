@@ -64,7 +64,7 @@ typedef struct moe_attn_norm {
 } moe_attn_norm;
 
 /* Codes and scales share their strides between K and V (codes: bytes, scales:
- * elements, not negative). Code pointers are 16-byte aligned. */
+ * elements, not negative; 0, one scale for all, where the cache is only read). Code pointers are 16-byte aligned. */
 typedef struct moe_attn_cache8 {
   void* k;
   void* v;
@@ -128,9 +128,10 @@ int moe_attn_append_norm(moe_attn_handle* h, const moe_attn_rows* q, const moe_a
                          const moe_attn_rotation* rotation, const moe_attn_cache* cache,
                          void* stream);
 
-/* The same into an 8-bit cache; norm NULL: none. New tokens of one block follow each
- * other in the call, in the order of their slots; a block that the call comes to
- * twice (or a slot given twice) is left with parts of both. Slots that are negative or
+/* The same into an 8-bit cache, whose scales and codes do not lie on each other (each
+ * stride reaches past what lies within it); norm NULL: none. New tokens of one block
+ * follow each other in the call, in the order of their slots; a block that the call comes
+ * to twice (or a slot given twice) is left with parts of both. Slots that are negative or
  * past the cache as in moe_attn_append. */
 int moe_attn_append8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_rows* q_out,
                      const moe_attn_rows* k, const moe_attn_rows* v, const int32_t* positions,

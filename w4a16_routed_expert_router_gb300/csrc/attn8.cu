@@ -87,6 +87,37 @@ int validate_cache8(const moe_attn_config& cfg, const moe_attn_cache8* c) {
   return MOE_ATTN_OK;
 }
 
+// Whether each stride reaches past what lies within it, from `reach` elements on: no two
+// places of such a view are one.
+struct Dim {
+  int64_t n, stride;
+};
+bool nested(std::initializer_list<Dim> dims, int64_t reach) {
+  Dim d[3];
+  int n = 0;
+  for (const Dim& x : dims)
+    if (x.n > 1) d[n++] = x;
+  std::sort(d, d + n, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  __int128 within = reach;
+  for (int i = 0; i < n; ++i) {
+    if (d[i].stride < within) return false;
+    within += (__int128)(d[i].n - 1) * d[i].stride;
+  }
+  return true;
+}
+
+// A cache that is written to: blocks whose scales or codes lie on each other would raise
+// one another's scales, each by its own values.
+int validate_written(const moe_attn_config& cfg, const moe_attn_cache8* c) {
+  const int64_t blocks = cfg.page_size / MOE_ATTN8_BLOCK;
+  const bool ok = nested({{c->num_pages, c->scale_page_stride},
+                          {cfg.kv_heads, c->scale_head_stride},
+                          {blocks, c->scale_block_stride}}, 1) &&
+                  nested({{c->num_pages, c->page_stride}, {cfg.kv_heads, c->head_stride},
+                          {cfg.page_size, c->token_stride}}, cfg.head_dim);
+  return ok ? MOE_ATTN_OK : MOE_ATTN_ERR_INVALID_ARG;
+}
+
 Cache8 cache_of(const moe_attn_cache8* c) {
   return Cache8{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_scales, c->v_scales,
                 c->num_pages, c->page_stride, c->token_stride, c->head_stride,
@@ -335,7 +366,9 @@ int moe_attn_append8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn_
                      const int64_t* slots, int32_t T, const moe_attn_norm* norm,
                      const moe_attn_rotation* r, const moe_attn_cache8* cache, void* stream) {
   int st = check_append(h, q, q_out, T, r, norm);
-  if (st != MOE_ATTN_OK || (st = validate_cache8(h->cfg, cache)) != MOE_ATTN_OK || T == 0) return st;
+  if (st != MOE_ATTN_OK || (st = validate_cache8(h->cfg, cache)) != MOE_ATTN_OK ||
+      (st = validate_written(h->cfg, cache)) != MOE_ATTN_OK || T == 0)
+    return st;
   if ((st = check_append_rows(h->cfg, q, q_out, k, v, positions, slots, T)) != MOE_ATTN_OK)
     return st;
   const OnDevice on(h->device);
