@@ -111,3 +111,28 @@ def test_a_cache_that_lies_on_itself_is_not_appended_to(F):
               (2 * HEADS * PAGE * DIM, 2 * DIM, 2 * PAGE * DIM)):
         assert h.append(h.cache(9, codes=c)) == 0, c
     assert F.moe_attn_destroy(h.h) == 0
+
+
+def test_kernels_are_set_up_once_for_a_handle(F):
+    h = Handle(F)
+    setup = ["decode8 setup", "tc8 usable", "tc8 setup"]
+    assert h.forward(1) == 0 and h.calls() == setup + ["decode8 on 1"]
+    assert h.forward(40) == 0 and h.forward(1) == 0 and h.calls() == ["tc8 on 1", "decode8 on 1"]
+    assert F.moe_attn_destroy(h.h) == 0
+
+
+@pytest.mark.parametrize("what", ["decode8 setup", "tc8 setup"])
+def test_a_set_up_that_failed_is_made_again(F, what):
+    h = Handle(F)
+    F.fake_fail(what.encode())
+    assert h.forward(1) == -5 and "decode8 on 1" not in h.calls()
+    assert h.forward(1) == 0 and h.calls()[-1] == "decode8 on 1"
+    assert F.moe_attn_destroy(h.h) == 0
+
+
+def test_single_tokens_run_where_the_tensor_core_kernel_does_not(F):
+    h = Handle(F)
+    F.fake_fail(b"tc8 usable")
+    assert h.forward(1) == 0 and h.calls()[-1] == "decode8 on 1"
+    assert h.forward(40) == -5 and h.calls() == [] and h.forward(1) == 0
+    assert F.moe_attn_destroy(h.h) == 0

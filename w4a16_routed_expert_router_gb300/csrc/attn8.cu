@@ -142,13 +142,20 @@ int encode_codes(CUtensorMap* m, const moe_attn_config& c, const moe_attn_cache8
                 width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// The kernels' attributes are set before a handle's first call over an 8-bit cache.
-int make_ready(moe_attn_handle* h) {
-  if (h->ready8) return MOE_ATTN_OK;
-  int st = cuda_status(attn8_decode_setup());
-  if (st == MOE_ATTN_OK) st = cuda_status(attn8_tc_setup(&h->tc8_usable));
-  h->ready8 = st == MOE_ATTN_OK;
-  return st;
+// The kernels' attributes are set in a handle's first call over an 8-bit cache (handles
+// over 16 bits do without). `all`: the tensor-core kernel among them.
+int make_ready(moe_attn_handle* h, bool* all) {
+  int ready = h->ready8.load(std::memory_order_acquire);
+  if (!ready) {
+    bool usable = false;
+    int st = cuda_status(attn8_decode_setup());
+    if (st == MOE_ATTN_OK) st = cuda_status(attn8_tc_setup(&usable));
+    if (st != MOE_ATTN_OK) return st;
+    ready = usable ? 2 : 1;
+    h->ready8.store(ready, std::memory_order_release);
+  }
+  *all = ready == 2;
+  return MOE_ATTN_OK;
 }
 
 // Keys and values of a batch in 16 bits, and the page table of them: K, V, table.
@@ -466,7 +473,8 @@ int moe_attn_forward8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn
     p.a.b.table_stride = b->columns;
     return forward_many(h, p.a, q, &wide, s);
   }
-  if ((st = make_ready(h)) != MOE_ATTN_OK) return st;
+  bool all;
+  if ((st = make_ready(h, &all)) != MOE_ATTN_OK) return st;
   // as in moe_attn_forward: one kernel for the whole batch
   CUtensorMap qmap, kmap, vmap;
   const bool few = (long long)b->max_q * p.a.group <= kDecodeRows;
@@ -478,7 +486,7 @@ int moe_attn_forward8(moe_attn_handle* h, const moe_attn_rows* q, const moe_attn
       (st = encode_codes(&vmap, c, cache, cache->v, box, width)) != MOE_ATTN_OK)
     return st;
   if (few) return cuda_status(launch_attn8_decode(p, h->decode, kmap, vmap, h->grid, s));
-  if (!h->tc8_usable) {  // another compiler: few-token batches go on
+  if (!all) {  // another compiler: few-token batches go on
     fprintf(stderr, "moe_attn: the tensor-core kernel was built with other registers than it needs\n");
     return MOE_ATTN_ERR_CUDA;
   }

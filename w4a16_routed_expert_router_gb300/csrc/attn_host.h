@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <cstdio>
@@ -26,8 +27,9 @@ struct moe_attn_handle {
   Partials decode{};
   TcPieces tc{};
   bool tc_usable = false;
-  bool ready8 = false;          // the kernels over an 8-bit cache are set up
-  bool tc8_usable = false;
+  // The kernels over an 8-bit cache: 0 until they are set up, 1 those of few tokens, 2
+  // all. Threads may make a handle's first calls at once.
+  std::atomic<int> ready8{0};
 };
 // The error word is the workspace's first; tests set its bits through here.
 static_assert(offsetof(moe_attn_handle, ws) == sizeof(moe_attn_config) + 8, "place of ws");
