@@ -1,5 +1,7 @@
 """Attention over the 8-bit cache of batches that mix single tokens, parts of a tile and
 chunks, against the definition in fp64 (attn8_cases.py)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -40,3 +42,26 @@ def test_single_tiles_in_front_of_pairs_of_tiles(d, dtype, opt):
         again, lse2 = b.run(layer)
         assert torch.equal(again, out) and torch.equal(lse2, lse)
     assert layer.check_device_errors() == 0
+
+
+def scratch_bytes(layer, b):
+    n = ctypes.c_size_t()
+    batch = moe.attention.moe_attn_batch(None, None, None, b.table.shape[1], b.table.shape[1],
+                                         len(b.lens), b.tokens, b.max_q)
+    assert layer._library.moe_attn_forward8_scratch_bytes(layer.handle, batch, n) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("lens,brought", [
+    ([(1, 1000), (380, 900), (1, 77), (2, 130)], False), ([(1, 1000), (382, 900), (1, 77)], False),
+    ([(1, 1000), (383, 900), (1, 77)], True), ([(1, 1000), (700, 900), (1, 77)], True)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_chunks_beside_single_tokens_on_both_sides_of_the_rule(lens, brought, dtype):
+    # more than 512 rows to a sequence and kv head, on average, bring the keys to 16 bits
+    b = a8.Batch8(lens, 8, 2, 128, 32, dtype)
+    layer = moe.PagedAttention(8, 2, 128, 32, b.tokens, len(lens), dtype=dtype)
+    assert (b.tokens * 4 > 512 * len(lens)) == (scratch_bytes(layer, b) > 0) == brought
+    for kw in ({}, dict(stream=torch.cuda.current_stream())):   # on a given one: over codes
+        out, lse = b.run(layer, **kw)
+        assert layer.check_device_errors() == 0
+        b.check(out, lse)
