@@ -32,10 +32,13 @@
  * scale: scores and sums in fp32, codes times queries exact (bf16 queries are
  * brought to fp16 by a power of two for each row, which loses what is below 2^-39 of
  * the row's largest value), and the softmax's numerators, times the scales of V,
- * rounded to fp16 with all bits down to 2^-26 of the largest. Where a call has scratch
- * and brings the keys to 16 bits, it is moe_attn_forward over those, whose numerators
- * are rounded to the handle's type. What lies behind kv_len is never used; a NaN in a
- * code or scale before it may reach other rows of its sequence.
+ * rounded to fp16 with all bits down to 2^-26 of the largest. (A weight may be lost to
+ * the softmax's sum where it is below 2^(d - 126) of that of a key whose scale of V is
+ * 2^d times its own: nothing that counts while a row's scales are within 2^80.) Where a
+ * call has scratch and brings the keys to 16 bits, it is moe_attn_forward over those,
+ * whose numerators are rounded to the handle's type: in bf16 the same batch then has other
+ * last bits than without. What lies behind kv_len is never used; a NaN in a code or scale
+ * before it may reach other rows of its sequence.
  *
  * Sinks. With a window and sinks > 0, query i at p also sees key j where j <= p and
  * j < sinks. Without a window they change nothing.
