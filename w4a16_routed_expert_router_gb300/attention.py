@@ -494,8 +494,9 @@ class PagedAttention:
         no sequence has more new tokens. scale defaults to 1 / sqrt(head_dim).
         sinks: first tokens of a sequence that a window does not hide. Over an 8-bit
         cache, batches of many tokens bring the keys to 16 bits first, in memory that
-        torch hands out for the call (up to 8 GiB; not where `stream` is given or torch has
-        no more).
+        torch hands out for the call (for all columns of the page table, up to 8 GiB; not
+        where `stream` is given or torch has no more). With bf16, results have other last
+        bits then than over the codes.
         Returns out, or (out, lse) with lse fp32 [tokens, q_heads].
         """
         given = stream

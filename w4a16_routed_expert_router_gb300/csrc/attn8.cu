@@ -174,7 +174,12 @@ Scratch scratch_of(const moe_attn_config& c, const moe_attn_batch* b) {
 // takes the same for any number of rows, and the kernel over 16 bits is faster for each.
 // Rows over 32768 keys of 8 kv heads, over codes and so: 400 108 and 113 us, 512 109 and
 // 113, 1024 176 and 145, 4000 (over 65536) 1189 and 702; 8 sequences of 8192 keys: 256
-// 104 and 146, 512 180 and 189, 1024 330 and 275.
+// 104 and 146, 512 180 and 189, 1024 330 and 275. Those were sequences of one length; a
+// batch goes one way as a whole, by its mean: a chunk beside many single tokens goes over
+// codes, and beside few of them their keys are brought along.
+// What it rounds: keys and values are exact in either type, but the softmax's numerators
+// become bf16 in a bf16 layer (the products there take one type), 2^-8 where fp16 ones
+// over codes are 2^-11: results of one batch differ in their last bits between the two.
 constexpr long long kExpandRows = 512;
 constexpr size_t kScratchMost = size_t(8) << 30;
 bool expands(const moe_attn_config& c, const moe_attn_batch* b) {

@@ -25,10 +25,13 @@
 // the sum of weights takes 1 / sv back, once for 16 keys. bf16 queries become fp16 by a
 // power of two of their own for each row.
 //
-// 64 sequences of up to 16384 keys, 8 kv heads of 128, take 184 us (1.1 GB, 5.9 TB/s of
+// 64 sequences of up to 16384 keys, 8 kv heads of 128, take 185 us (1.1 GB, 5.9 TB/s of
 // codes and scales; 16-bit keys take 331). Four drafted tokens of 48 sequences under a
 // window of 4096, heads of 64, take 45 us for 100 MB: a block of 32 KB takes 0.9 us an SM,
 // 23 of them 20 us, and the ends and joins of two to three pieces an SM most of the rest.
+// 9 to 16 rows of heads of 128 (64 sequences of up to 16384 keys, 4 tokens each, 1.4 GB)
+// take 354 us, 225 with one token: twice the products and sums on eight warps of 168
+// registers, of which 80 to 130 bytes a thread go to memory and back.
 // One token over 4096 keys is a chain of latencies as in attn_decode.cu, 11 us.
 #include "attn8_parts.cuh"
 #include "attn_decode_parts.cuh"

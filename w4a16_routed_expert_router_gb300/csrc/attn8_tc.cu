@@ -21,12 +21,14 @@
 // weights takes 1 / sv back, once for 16 keys.
 //
 // For batches of up to 512 rows a sequence and kv head, or where there is no room for the
-// keys in 16 bits: 64 tokens over 32768 keys take 78 us, 100 108, 8 sequences of 64 over
-// 8192 keys 104. Bound by shared memory: a block's codes are read and written as fp16
-// there, 2560 cycles of its bandwidth a block of two tiles where the 16-bit kernel takes
-// 2048, and by the way from the copy over the converters to the products. (Slots of codes
-// beside those of 16 bits, converters in pairs, the ratio of scales applied by the
-// converters, and V's slots given back early: none was faster.)
+// keys in 16 bits, heads of 128, 4 to a kv head: 64 tokens over 32768 keys take 75 us (18
+// at the matrix products' rate), 100 102 (28), 8 sequences of 64 over 8192 keys 98 (36).
+// No unit bounds it: in the last, 6700 cycles a block of two tiles with the matrix unit
+// at 30 % of them, issue slots at 35, shared memory at 24 (of the threads' accesses) and
+// DRAM at 18. It is the way of a block from the copy over the converters, products and
+// softmax, one behind the other. (Slots of codes beside those of 16 bits, converters in
+// pairs, the ratio of scales applied by the converters, and V's slots given back early:
+// none was faster.)
 #define MOE_ATTN8_TC
 #include "attn_tc.cu"
 #include "attn8_parts.cuh"

@@ -11,10 +11,12 @@
 // codes. Queries are normed and turned by CTAs of the same launch, as in norm_rope.cu.
 //
 // Bound by instructions at 72 % of the issue slots: 8191 tokens of 32 + 8 heads of 128,
-// with norms, take 45 us (185 MB, 4.1 TB/s; 27 us at the copy rate). A choice between
+// with norms, take 41 us (185 MB, 4.5 TB/s; 27 us at the copy rate). A choice between
 // product and division for each value cost 15 us of 94, four CTAs of 64 registers with
 // some spills save 2 us over three of 80, heads that share a window's plan and its table
-// of cosines 6 us. A decode step of 64 tokens is bound by latency, 6 us.
+// of cosines 6 us. A decode step of 64 tokens is bound by latency, 6 us. The form for any
+// rows (see norm_rope.cu): heads of 80 with 40 turned 139 us for 8192 tokens, of 96 with 24
+// turned 123 (17 and 20 at the copy rate).
 #include <algorithm>
 
 #include "norm_parts.cuh"
@@ -495,8 +497,8 @@ cudaError_t launch_append(const Append8Params& g, cudaStream_t s) {
 // to shared memory (as many as there is room for; every thread then counts some of those
 // that begin at or before its first row), a lane a row finds its sequence by bisection and
 // looks up its page, then all threads bring 16 codes at a time to 32 bytes of the
-// outputs. Bound by memory: 16 sequences of up to 16384 tokens, 8 heads of 128, 933 MB
-// take 150 us (6.2 TB/s).
+// outputs. Bound by memory: 16 sequences of up to 16384 tokens, 8 heads of 128, 931 MB
+// take 148 us (6.3 TB/s).
 constexpr int kReadRows = 32, kReadSeqs = 1024;
 
 // Two values of the cache in 16 bits. A finite value stays finite: fp16 takes what is

@@ -4,17 +4,24 @@
 // Forward: y = R_p(x rsqrt(mean x^2 + eps) (w + offset)), read once, written once. A
 // group of lanes has a head and walks along the tokens (norm_walk in norm_parts.cuh). The
 // CTA makes the tables of cosines and sines, one evaluation for its heads. 8192 tokens of
-// 40 heads of 128 take 36 us (168 MB, 4.6 TB/s; the same kernel without sums, rotation
+// 40 heads of 128 take 35 us (168 MB, 4.8 TB/s; the same kernel without sums, rotation
 // and weights takes 28, the copy rate 25): latency and instructions, 260 for 16 values of a
 // lane, at 55 % of the issue slots. (A few tokens a thread, loaded to registers first, took 44 us:
 // a third of its instructions prepared a thread for them. Rows in units of one chunk for
-// interleaved pairs cost as many sums and addresses again.)
+// interleaved pairs cost as many sums and addresses again.) Into 16-bit pages, with 8
+// heads of values beside them, 42 us (201 MB; 30 at the copy rate).
+//
+// Rotations that are not a multiple of 16 values, and rows that are not aligned, go a warp
+// a head, which evaluates an angle for each value of each head: 8192 tokens of 40 heads of
+// 80 with 40 turned 147 us (15.5 at the copy rate; all 80 turned, in the fast form, 30), of
+// 96 with 24 turned 129 (18.6); their gradient 390 (23) and 364 (28).
 //
 // Gradient: with u = R_p^T dy, n = x r and h = u (w + offset),
 //   dx = r (h - n mean(h n)),  dw = sum u n.
 // mean(h n) = r mean(h x), so both sums over a head, of x^2 and of h x, are taken
 // together. Each thread keeps one unit of one head for many tokens and adds up that
-// unit's dw; a CTA adds its rows in order, and a second launch the CTAs. 16384 tokens of
+// unit's dw; a CTA adds its rows in order, and a second launch the CTAs (8 of 16 us for
+// 2047 tokens of 20 heads of 64: 456 rows). 16384 tokens of
 // 40 heads of 128 take 107 us (503 MB, 4.7 TB/s; 75 at the copy rate): latency, with 15
 // warps an SM at 122 registers; two values to an instruction change nothing. (The
 // forward's ring of copies in place of registers: 134 us, for its instructions and spills.)
