@@ -67,7 +67,8 @@ typedef struct moe_attn_norm {
 } moe_attn_norm;
 
 /* Codes and scales share their strides between K and V (codes: bytes, scales:
- * elements, not negative; 0, one scale for all, where the cache is only read). Code pointers are 16-byte aligned. */
+ * elements, not negative; 0, one scale for all, where the cache is only read). Code
+ * pointers are 16-byte aligned. */
 typedef struct moe_attn_cache8 {
   void* k;
   void* v;

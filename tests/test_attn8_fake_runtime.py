@@ -113,6 +113,16 @@ def test_a_cache_that_lies_on_itself_is_not_appended_to(F):
     assert F.moe_attn_destroy(h.h) == 0
 
 
+def test_keys_and_values_in_one_place_are_not_appended(F):
+    h = Handle(F)
+    for twin in (("k", "v"), ("k_scales", "v_scales")):
+        cache = h.cache()
+        setattr(cache, twin[1], getattr(cache, twin[0]))
+        assert h.append(cache) == -1 and h.read(cache) == 0
+    assert h.append(h.cache()) == 0
+    assert F.moe_attn_destroy(h.h) == 0
+
+
 def test_kernels_are_set_up_once_for_a_handle(F):
     h = Handle(F)
     setup = ["decode8 setup", "tc8 usable", "tc8 setup"]

@@ -106,9 +106,10 @@ bool nested(std::initializer_list<Dim> dims, int64_t reach) {
   return true;
 }
 
-// A cache that is written to: blocks whose scales or codes lie on each other would raise
-// one another's scales, each by its own values.
+// A cache that is written to: blocks whose scales or codes lie on each other, or K's on
+// V's, would raise one another's scales, each by its own values.
 int validate_written(const moe_attn_config& cfg, const moe_attn_cache8* c) {
+  if (c->k == c->v || c->k_scales == c->v_scales) return MOE_ATTN_ERR_INVALID_ARG;
   const int64_t blocks = cfg.page_size / MOE_ATTN8_BLOCK;
   const bool ok = nested({{c->num_pages, c->scale_page_stride},
                           {cfg.kv_heads, c->scale_head_stride},
